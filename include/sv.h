@@ -347,6 +347,128 @@ sv_status sv_map_pool_static(const void* x, void* out, int batch, int gemm_dtype
 /* y[i] = e4m3 code of 16 * x[i] (saturating, round to nearest even); x f16, n % 16 == 0. */
 sv_status sv_quantize_e4m3(const void* x, void* y, size_t n, void* stream);
 
+/* ---------------------------------------------------------------- rotary positions */
+
+/* How the two values of a rotated pair lie in a head. */
+typedef enum {
+  SV_ROPE_HALF = 0,       /* pair i of n: values i and i + n of the axis' section */
+  SV_ROPE_INTERLEAVED = 1 /* pair i: values 2 i and 2 i + 1 */
+} sv_rope_layout;
+
+/* How the frequencies f_i = base^(-i / n) of the n pairs of an axis are scaled for positions beyond the
+ * length a model was trained at (factor >= 1). */
+typedef enum {
+  SV_ROPE_SCALE_NONE = 0,
+  SV_ROPE_SCALE_LINEAR = 1,  /* f_i / factor */
+  SV_ROPE_SCALE_BASE = 2,    /* base * factor^(n / (n - 1)): the fastest pair stays, the slowest is divided by factor */
+  SV_ROPE_SCALE_BY_PARTS = 3 /* by the turns r_i = original_len f_i / 2 pi that a pair makes over the trained length
+                                (YaRN, Peng et al. 2023): f_i (w + (1 - w) / factor) with w = (r_i - 1) / 31 held to
+                                [0, 1], cosines and sines multiplied by 0.1 ln(factor) + 1 */
+} sv_rope_scaling;
+
+#define SV_ROPE_MAX_PAIRS 128
+
+/* A rotation, made by sv_rope_plan_init and kept by the caller in host memory; it holds no device memory and may be
+ * used by any number of calls, threads and streams, and freed or changed as soon as a call has returned. */
+typedef struct {
+  int rot_dim, axes, layout;
+  int pairs;  /* per axis */
+  float gain; /* factor on cosines and sines */
+  unsigned long long turns[SV_ROPE_MAX_PAIRS]; /* frequency of each pair of an axis: turns per position times 2^64 */
+} sv_rope_plan;
+
+/*
+ * Fills *plan: the first rot_dim values of a head are rotated, in `axes` (1 or 2) equal sections, each by its own
+ * position (2: patch row and column of an image), the rest of the head is left as it is.
+ * Requirements: rot_dim even (a multiple of 4 with two axes), 2 <= rot_dim <= 256, base >= 1; with a scaling,
+ * factor >= 1; SV_ROPE_SCALE_BASE: at least two pairs per axis; SV_ROPE_SCALE_BY_PARTS: original_len >= 1.
+ * Host only. Errors: SV_ERR_INVALID_ARG.
+ */
+sv_status sv_rope_plan_init(sv_rope_plan* plan, int rot_dim, int axes, int layout, double base, int scaling,
+                            double factor, int original_len);
+
+/*
+ * y = x with every head rotated: the pair (a, b) of frequency f becomes
+ * gain * (a cos(p f) - b sin(p f), b cos(p f) + a sin(p f)), in F32, rounded to F16 once.
+ * x, y: f16 [rows, heads * head_dim] with row strides x_stride, y_stride in values (0: contiguous rows; else at least
+ * heads * head_dim and a multiple of 8). y may be x (with the same stride); other overlaps are not allowed.
+ * positions: int32 [axes, rows], any values (negative ones too); the angle of a far position loses nothing to its
+ * size (whole turns are dropped in 64-bit fixed point).
+ * Requirements: head_dim a multiple of 8, 8 <= head_dim <= 256, plan->rot_dim <= head_dim; rows 0 is no work.
+ * Errors: SV_ERR_INVALID_ARG, SV_ERR_CUDA.
+ */
+sv_status sv_rope(const void* x, void* y, const int* positions, const sv_rope_plan* plan, int rows, int heads,
+                  int head_dim, long long x_stride, long long y_stride, void* stream);
+
+/* Norms of sv_qk_norm_rope, over the head_dim values of each head. */
+typedef enum {
+  SV_NORM_RMS = 0,  /* x / sqrt(mean(x^2) + eps) * gamma */
+  SV_NORM_LAYER = 1 /* (x - mean) / sqrt(mean((x - mean)^2) + eps) * gamma */
+} sv_norm;
+
+/*
+ * Every query and every key head normalised and then rotated as by sv_rope, in one pass: statistics and arithmetic in
+ * F32, rounded to F16 once. What stands between a fused QKV projection (sv_gemm_bias_act) and sv_attention_packed: q
+ * and k may be columns of its output, with its row stride.
+ * q: f16 [rows, q_heads * head_dim]; k: f16 [rows, kv_heads * head_dim]; strides as in sv_rope. q_out may be q, k_out
+ * may be k (with the same strides); other overlaps are not allowed. q_gamma, k_gamma: f16 [head_dim], or NULL (ones).
+ * plan: NULL for the norm alone (positions is then not used).
+ * Requirements and errors: as sv_rope; eps >= 0.
+ */
+sv_status sv_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out, const void* q_gamma,
+                          const void* k_gamma, int norm, float eps, const int* positions, const sv_rope_plan* plan,
+                          int rows, int q_heads, int kv_heads, int head_dim, long long q_stride, long long k_stride,
+                          long long q_out_stride, long long k_out_stride, void* stream);
+
+/* ---------------------------------------------------------------- packed attention */
+
+/* Which keys of its document a query sees. Query i of a document with Lq queries and Lk keys stands at key position
+ * p_i = i + Lk - Lq (the last query at the last key). */
+typedef enum {
+  SV_MASK_DOCUMENT = 0, /* every key of the document */
+  SV_MASK_PREFIX = 1    /* keys j <= p_i, and the keys j < prefix of the document's visible prefix */
+} sv_mask;
+
+/* Options of sv_attention_packed (NULL there: every field 0). The pointers are device pointers, read during the call. */
+typedef struct {
+  float scale;         /* factor on q . k; <= 0 selects 1 / sqrt(head_dim) */
+  float softcap;       /* > 0: scores become softcap * tanh(score / softcap); 0: they stay */
+  int mask;            /* sv_mask */
+  const int* prefix;   /* int32 [docs]: visible prefix of each document (SV_MASK_PREFIX); NULL: none */
+  const float* slopes; /* f32 [q_heads]: scores of head h lose slopes[h] * |p_i - j|, after the cap; NULL: none */
+} sv_attention_options;
+
+/* Bytes of workspace with which sv_attention_packed may divide long key ranges among the SMs. Host only. */
+size_t sv_attention_packed_workspace(int docs, int total_q, int total_k, int q_heads, int kv_heads, int head_dim);
+
+/*
+ * Attention over documents packed one behind another: images of different sizes in one sequence, prompts, or one new
+ * query for each of many long key sequences. o = softmax(scores) v over the keys that a query sees (sv_mask), scores
+ * as in sv_attention_options; a query that sees no key gets zeros. Keys that a query does not see have no part in its
+ * result, whatever their values (NaN and infinities too).
+ * q: f16 [total_q, q_heads * head_dim], k, v: f16 [total_k, kv_heads * head_dim]; q_heads is a multiple of kv_heads,
+ * and query head h reads key head h / (q_heads / kv_heads). Row strides in values, as in sv_rope (multiples of 8; 0:
+ * contiguous): q, k and v may be columns of one projection's output.
+ * o: [total_q, q_heads * head_dim] f16 or e4m3 (out_dtype), row stride o_stride (0: contiguous); it must not overlap
+ * the inputs. Scores, softmax and accumulation in F32; the probabilities are rounded to F16 for their product with v.
+ * q_offsets, k_offsets: device int32 [docs + 1], non-decreasing: document d has queries q_offsets[d] ..
+ * q_offsets[d + 1] - 1 and keys likewise (either may be none). NULL: documents of equal size, total_q / docs or
+ * total_k / docs. Rows of o outside every document are left as they were. Offsets that decrease or leave [0, total]
+ * are held to that range, and the next sv_sync reports SV_ERR_INVALID_ARG; outputs are then undefined.
+ * workspace: NULL, or sv_attention_packed_workspace() bytes of device memory, 16-byte aligned, that were zero before
+ * their first use by this function; every call leaves what the next one needs, of the same sizes or others. Without
+ * it, results are the same up to rounding, but few queries over many keys use few SMs. Calls that may run at the same
+ * time (other streams, or graphs that replay side by side) need workspaces of their own.
+ * The same call gives the same bits every time.
+ * Requirements: head_dim a multiple of 8 in [8, 128]; q_heads / kv_heads <= 64; docs >= 1; total_q, total_k >= 0.
+ * Errors: SV_ERR_INVALID_ARG; SV_ERR_UNSUPPORTED (head_dim, heads), SV_ERR_CUDA.
+ */
+sv_status sv_attention_packed(const void* q, const void* k, const void* v, void* o, const int* q_offsets,
+                              const int* k_offsets, int docs, int total_q, int total_k, int q_heads, int kv_heads,
+                              int head_dim, long long q_stride, long long k_stride, long long v_stride,
+                              long long o_stride, const sv_attention_options* options, int out_dtype, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
 /* ---------------------------------------------------------------- utilities */
 
 /* Pixels [batch, tokens, patch_dim] f16 uniform in [-1, 1] from `seed` (synth/synth.h), written to dev_dst. */
@@ -356,7 +478,8 @@ sv_status sv_make_pixels(uint64_t seed, int batch, void* dev_dst, void* stream);
  * Waits for `stream`, then reports any asynchronous CUDA error and the
  * library's device error word: SV_ERR_TIMEOUT if a kernel gave up a bounded
  * wait (the kernel then returned without finishing; its outputs are
- * undefined). Clears the error word.
+ * undefined), SV_ERR_INVALID_ARG if sv_attention_packed was given bad document
+ * offsets. Clears the error word.
  */
 sv_status sv_sync(void* stream);
 

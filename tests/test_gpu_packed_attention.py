@@ -1,0 +1,386 @@
+"""sv_attention_packed against the formulas in 64 bits (packed_ref: the tolerances' derivation stands at bound())."""
+import math
+
+import pytest
+import torch
+
+import packed_ref
+from gpu_util import decode_e4m3
+
+pytestmark = pytest.mark.gpu
+
+
+def _randn(seed, *shape):
+    return torch.randn(*shape, generator=torch.Generator("cuda").manual_seed(seed), device="cuda")
+
+
+def _offsets(lens, start=0):
+    return torch.tensor([start] + lens, dtype=torch.int64).cumsum(0).to(torch.int32).cuda()
+
+
+class Case:
+    """Inputs of one call: documents with lq queries and lk keys, optionally as columns of one projection's output,
+    with rows before the first and behind the last document that belong to nobody."""
+
+    def __init__(self, lq, lk, hq, hk, d, seed=0, fused=False, lead=0, tail=0, scale_q=1.0):
+        self.lq, self.lk, self.hq, self.hk, self.d = lq, lk, hq, hk, d
+        self.lead = lead
+        self.tq, self.tk = lead + sum(lq) + tail, lead + sum(lk) + tail
+        if fused:
+            assert lq == lk
+            width = (hq + 2 * hk) * d + 16
+            qkv = _randn(seed, self.tq, width).half()
+            self.q, self.k, self.v = (qkv[:, a * d:(a + h) * d] for a, h in ((0, hq), (hq, hk), (hq + hk, hk)))
+        else:
+            self.q = _randn(seed, self.tq, hq * d).half()
+            self.k, self.v = _randn(seed + 1, self.tk, hk * d).half(), _randn(seed + 2, self.tk, hk * d).half()
+        self.q.mul_(scale_q)
+        self.q_off, self.k_off = _offsets(lq, lead), _offsets(lk, lead)
+
+    def run(self, sv, out="f16", workspace=True, uniform=False, o=None, stream=None, **opt):
+        prefix = opt.pop("prefix", None)
+        if prefix is not None:
+            prefix = torch.tensor(prefix, dtype=torch.int32).cuda()
+        self.options = sv.sv_attention_options(prefix=prefix, **opt)
+        if o is None:
+            o = torch.full((self.tq, self.hq * self.d), 0x7F if out == "e4m3" else math.nan, device="cuda",
+                           dtype=torch.uint8 if out == "e4m3" else torch.float16)
+        ws = None
+        if workspace is True:
+            n = sv.sv_attention_packed_workspace(len(self.lq), self.tq, self.tk, self.hq, self.hk, self.d)
+            ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+        elif workspace is not False:
+            ws = workspace
+        self.ws = ws
+        sv.sv_attention_packed(self.q, self.k, self.v, o, None if uniform else self.q_off,
+                               None if uniform else self.k_off, len(self.lq), self.tq, self.tk, self.hq, self.hk,
+                               self.d, q_stride=self.q.stride(0), k_stride=self.k.stride(0), v_stride=self.v.stride(0),
+                               options=self.options, out_dtype=1 if out == "e4m3" else 0, workspace=ws, stream=stream)
+        return o
+
+    def docs(self):
+        a = b = self.lead
+        for n, (lq, lk) in enumerate(zip(self.lq, self.lk)):
+            yield (n, a, lq, self.q[a:a + lq].reshape(lq, self.hq, self.d), self.k[b:b + lk].reshape(lk, self.hk, self.d),
+                   self.v[b:b + lk].reshape(lk, self.hk, self.d))
+            a, b = a + lq, b + lk
+
+    def check(self, o, out="f16", mask=0, prefix=None, scale=None, softcap=0.0, slopes=None):
+        got = decode_e4m3(o) if out == "e4m3" else o.double().cpu().numpy()
+        got = torch.from_numpy(got)
+        for n, a, lq, q, k, v in self.docs():
+            if lq == 0:
+                continue
+            ref, av, terms = packed_ref.document(q, k, v, mask, prefix[n] if prefix is not None else 0, scale, softcap,
+                                                 slopes)
+            vmax = float(v.abs().max()) if v.numel() else 0.0
+            tol = packed_ref.bound(ref, av, terms, k.shape[0], vmax, self.d, softcap, out == "e4m3")
+            x = got[a:a + lq].reshape(ref.shape).cuda()
+            assert torch.isfinite(x).all(), (n, "not finite")
+            err = (x - ref).abs()
+            assert (err <= tol).all(), (n, float((err - tol).max()), float(err.max()))
+        # rows of no document
+        rest = torch.cat([got[:self.lead], got[self.lead + sum(self.lq):]])
+        assert torch.isnan(rest).all()
+
+
+LENGTHS = [
+    [1], [2, 1], [127], [128], [129], [64, 65, 63], [0, 5, 0, 0, 300, 1, 0], [255, 256, 257], [729, 730], [383, 1, 640],
+    [17] * 40,
+]
+
+
+@pytest.mark.parametrize("lens", LENGTHS)
+@pytest.mark.parametrize("hq,hk,d", [(3, 3, 72), (4, 2, 64), (2, 1, 128)])
+def test_documents(sv, lens, hq, hk, d):
+    c = Case(lens, lens, hq, hk, d, seed=sum(lens) + d, fused=True)
+    c.check(c.run(sv))
+    sv.sv_sync()
+
+
+@pytest.mark.parametrize("lens", LENGTHS)
+@pytest.mark.parametrize("hq,hk,d", [(3, 3, 72), (6, 2, 64), (4, 1, 128)])
+def test_prefix_mask(sv, lens, hq, hk, d):
+    c = Case(lens, lens, hq, hk, d, seed=sum(lens) + d)
+    c.check(c.run(sv, mask=1), mask=1)
+    prefix = [(7 * i + n) % (n + 3) for i, n in enumerate(lens)]
+    c.check(c.run(sv, mask=1, prefix=prefix), mask=1, prefix=prefix)
+    sv.sv_sync()
+
+
+@pytest.mark.parametrize("d", [8, 16, 24, 40, 56, 64, 72, 80, 96, 104, 120, 128])
+def test_head_widths(sv, d):
+    c = Case([150, 33], [150, 290], 2, 2, d, seed=d)
+    c.check(c.run(sv))
+    c.check(c.run(sv, out="e4m3", mask=1), out="e4m3", mask=1)
+    sv.sv_sync()
+
+
+@pytest.mark.parametrize("hq,hk", [(1, 1), (6, 2), (5, 1), (7, 1), (12, 4), (16, 1), (64, 1), (33, 1), (40, 8)])
+def test_shared_key_heads(sv, hq, hk):
+    c = Case([70, 1, 19], [70, 140, 300], hq, hk, 64, seed=hq)
+    slopes = torch.linspace(0.0, 0.3, hq, device="cuda")
+    c.check(c.run(sv, mask=1, slopes=slopes), mask=1, slopes=slopes)
+    sv.sv_sync()
+
+
+# unequal numbers of queries and keys: more keys (a cache), more queries (rows that see nothing), none of either
+UNEQUAL = [([1], [1000]), ([1] * 7, [1, 64, 65, 129, 700, 2, 1023]), ([5, 3], [300, 4]), ([200], [50]),
+           ([4, 9, 0], [0, 9, 30]), ([130, 20], [1, 513]), ([16] * 3, [2048, 100, 16]), ([1, 1], [0, 0]),
+           ([1], [9000]), ([2, 1, 1], [4500, 33, 129])]
+
+
+@pytest.mark.parametrize("lq,lk", UNEQUAL)
+@pytest.mark.parametrize("mask", [0, 1])
+@pytest.mark.parametrize("hq,hk,d", [(2, 2, 72), (8, 2, 128)])
+def test_unequal_lengths(sv, lq, lk, mask, hq, hk, d):
+    c = Case(lq, lk, hq, hk, d, seed=sum(lk))
+    c.check(c.run(sv, mask=mask), mask=mask)
+    c.check(c.run(sv, mask=mask, workspace=False), mask=mask)
+    prefix = [3] * len(lq)
+    c.check(c.run(sv, mask=1, prefix=prefix), mask=1, prefix=prefix)
+    sv.sv_sync()
+
+
+@pytest.mark.parametrize("cap,scale_q", [(30.0, 1.0), (30.0, 20.0), (5.0, 30.0), (0.25, 4.0), (500.0, 3.0)])
+@pytest.mark.parametrize("lq,lk", [([300, 70], [300, 70]), ([1, 2], [700, 200])])
+def test_softcap(sv, cap, scale_q, lq, lk):
+    c = Case(lq, lk, 4, 2, 64, seed=int(cap), scale_q=scale_q)
+    slopes = torch.tensor([0.5, 0.0, 0.01, 2.0], device="cuda")
+    c.check(c.run(sv, softcap=cap), softcap=cap)
+    c.check(c.run(sv, softcap=cap, mask=1, slopes=slopes), softcap=cap, mask=1, slopes=slopes)
+    sv.sv_sync()
+
+
+@pytest.mark.parametrize("lens", [[700], [130, 260, 9]])
+def test_distance_bias(sv, lens):
+    """Slopes of either sign, with and without the prefix mask."""
+    c = Case(lens, lens, 4, 4, 72, seed=3, fused=True)
+    slopes = torch.tensor([1.0, 0.125, 0.0, -0.05], device="cuda")
+    c.check(c.run(sv, slopes=slopes), slopes=slopes)
+    c.check(c.run(sv, slopes=slopes, mask=1, scale=0.3), slopes=slopes, mask=1, scale=0.3)
+    sv.sv_sync()
+
+
+@pytest.mark.parametrize("scale_q", [0.0, 40.0, 400.0])
+def test_flat_and_steep_scores(sv, scale_q):
+    """All scores equal, and scores in the hundreds (one key takes all)."""
+    c = Case([200, 1], [200, 600], 2, 1, 64, seed=8, scale_q=scale_q)
+    c.check(c.run(sv))
+    sv.sv_sync()
+
+
+def test_equal_documents_without_offsets(sv):
+    c = Case([90] * 5, [90] * 5, 3, 3, 72, seed=2, fused=True)
+    a, b = c.run(sv, uniform=True), c.run(sv)
+    c.check(a)
+    assert torch.equal(a, b)
+    c = Case([1] * 6, [400] * 6, 4, 2, 64, seed=2)
+    a, b = c.run(sv, uniform=True), c.run(sv)
+    c.check(a)
+    assert torch.equal(a, b)
+    sv.sv_sync()
+
+
+@pytest.mark.parametrize("out", ["f16", "e4m3"])
+@pytest.mark.parametrize("lq,lk", [([140, 3], [140, 3]), ([1, 1], [300, 40])])
+def test_rows_of_no_document_stay(sv, out, lq, lk):
+    c = Case(lq, lk, 2, 2, 72, seed=4, lead=5, tail=9)
+    c.check(c.run(sv, out=out), out=out)
+    sv.sv_sync()
+
+
+def test_large_values_saturate_in_e4m3(sv):
+    c = Case([40], [40], 1, 1, 64, seed=4)
+    c.v.mul_(100.0)
+    o = c.run(sv, out="e4m3")
+    sv.sv_sync()
+    ref = packed_ref.document(*next(c.docs())[3:])[0].reshape(40, 64) * 16
+    got = torch.from_numpy(decode_e4m3(o)).cuda() * 16
+    assert (got[ref.abs() > 500].abs() == 448).all() and torch.isfinite(got).all()
+
+
+def _by_rows(c, mask, prefix=0):
+    """Row by row over the visible keys alone, so that hidden values cannot enter."""
+    out = []
+    for n, a, lq, q, k, v in c.docs():
+        lim = packed_ref.limits(mask, lq, k.shape[0], prefix)
+        for i in range(lq):
+            out.append(packed_ref.document(q[i:i + 1], k[:lim[i]], v[:lim[i]])[0][0].reshape(-1) if lim[i]
+                       else torch.zeros(c.hq * c.d, dtype=torch.float64, device="cuda"))
+    return torch.stack(out)
+
+
+@pytest.mark.parametrize("poison", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("lq,lk,hidden", [
+    ([60, 70], [60, 70], [45]),            # a later key of the first document
+    ([150, 140], [150, 140], [149, 150]),  # the first document's last key, the second one's first
+    ([3, 1], [200, 90], [198, 199]),       # few queries
+    ([1, 1], [64, 300], [63, 64]),         # a neighbour's keys
+])
+def test_hidden_values_have_no_part(sv, poison, lq, lk, hidden):
+    """NaN and infinities in keys and values reach the queries that see them, and no other."""
+    mask = 1
+    c = Case(lq, lk, 2, 1, 64, seed=21, lead=2, tail=3)
+    clean = _by_rows(c, mask)
+    rows = sum(lq)
+    for what in (c.k, c.v):
+        what[:2] = poison
+        what[-3:] = poison
+    for h in hidden:
+        c.v[2 + h] = poison
+        c.k[2 + h] = poison
+    o = c.run(sv, mask=mask)
+    sv.sv_sync()
+    got = o[2:2 + rows].double()
+    b = row = 0
+    for a, n in zip(lq, lk):
+        lim = packed_ref.limits(mask, a, n, 0)
+        for i in range(a):
+            sees = any(b <= h < b + lim[i] for h in hidden)
+            if sees:
+                # a score of NaN or +inf makes the row NaN; -inf times a query of either sign does as well
+                assert not torch.isfinite(got[row]).all(), row
+            else:
+                assert torch.isfinite(got[row]).all(), row
+                assert (got[row] - clean[row]).abs().max() <= 2.0 ** -9 * max(1.0, float(clean[row].abs().max())), row
+            row += 1
+        b += n
+
+
+def test_same_bits_every_time_and_other_sizes_between(sv):
+    """Repeated calls give the same bits, whatever ran on the workspace in between."""
+    big = Case([1, 1, 1], [5000, 33, 9000], 8, 2, 128, seed=1)
+    mid = Case([300, 200], [300, 200], 8, 2, 128, seed=2)
+    n = sv.sv_attention_packed_workspace(3, big.tq, big.tk, 8, 2, 128)
+    n = max(n, sv.sv_attention_packed_workspace(2, mid.tq, mid.tk, 8, 2, 128))
+    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    a, b = big.run(sv, workspace=ws, mask=1), mid.run(sv, workspace=ws, mask=1)
+    for _ in range(3):
+        assert torch.equal(big.run(sv, workspace=ws, mask=1), a)
+        assert torch.equal(mid.run(sv, workspace=ws, mask=1), b)
+    sv.sv_sync()
+    big.check(a, mask=1)
+    mid.check(b, mask=1)
+
+
+@pytest.mark.parametrize("lq,lk", [([200, 90], [200, 90]), ([1, 1, 1], [3000, 700, 40])])
+def test_in_a_graph_and_on_two_streams(sv, lq, lk):
+    """A captured call, replayed beside an eager one on another stream, each with a workspace of its own."""
+    c = Case(lq, lk, 4, 2, 72, seed=6)
+    want = c.run(sv, mask=1)
+    o1, o2 = torch.zeros_like(want), torch.zeros_like(want)
+    ws1, ws2 = torch.zeros_like(c.ws), torch.zeros_like(c.ws)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.run(sv, mask=1, o=o1, workspace=ws1)
+    keep = c.options
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        g.replay()
+        c.run(sv, mask=1, o=o2, workspace=ws2, stream=side)
+    torch.cuda.synchronize()
+    sv.sv_sync()
+    assert torch.equal(o1, want) and torch.equal(o2, want)
+    # offsets are read on the device: a replay follows them
+    c.q_off.copy_(_offsets(lq[::-1]))
+    c.k_off.copy_(_offsets(lk[::-1]))
+    g.replay()
+    eager = c.run(sv, mask=1)
+    torch.cuda.synchronize()
+    assert torch.equal(o1[:sum(lq)], eager[:sum(lq)])
+    del keep
+
+
+@pytest.mark.parametrize("which", ["q", "k"])
+@pytest.mark.parametrize("bad", [[0, 50, 40], [-7, 30, 40], [0, 30, 1000]])
+def test_bad_offsets_are_reported(sv, which, bad):
+    """Held inside the buffers on the device and reported by the next sv_sync; the context stays usable."""
+    c = Case([30, 30], [30, 30], 2, 2, 64, seed=1)
+    good = c.run(sv)
+    sv.sv_sync()
+    keep = getattr(c, which + "_off").clone()
+    getattr(c, which + "_off").copy_(torch.tensor(bad, dtype=torch.int32))
+    c.run(sv)
+    with pytest.raises(sv.SvError) as e:
+        sv.sv_sync()
+    assert e.value.status == sv.SV_ERR_INVALID_ARG and "offsets" in str(e.value)
+    getattr(c, which + "_off").copy_(keep)
+    assert torch.equal(c.run(sv), good)
+    sv.sv_sync()
+
+
+def test_many_documents(sv):
+    g = torch.Generator().manual_seed(5)
+    lens = torch.randint(0, 40, (700,), generator=g).tolist()
+    c = Case(lens, lens, 2, 2, 40, seed=7, fused=True)
+    c.check(c.run(sv, mask=1), mask=1)
+    keys = torch.randint(0, 200, (700,), generator=g).tolist()
+    c = Case([1] * 700, keys, 2, 1, 64, seed=7)
+    c.check(c.run(sv, mask=1), mask=1)
+    sv.sv_sync()
+
+
+def test_far_into_a_long_cache(sv):
+    """Keys behind 2^31 values: row offsets pass 32 bits."""
+    stride, n = 65536, 36000
+    k = torch.empty(n * stride, dtype=torch.float16, device="cuda")[:n * stride].view(n, stride)
+    d, lk = 64, [n - 700, 700]
+    kv = _randn(3, n, 2 * d).half()
+    k[:, 512:512 + 2 * d] = kv
+    c = Case([1, 40], lk, 1, 1, d, seed=5)
+    c.k, c.v = k[:, 512:512 + d], k[:, 512 + d:512 + 2 * d]
+    c.tk = n
+    c.check(c.run(sv, mask=1), mask=1)
+    sv.sv_sync()
+
+
+def test_projection_norm_rotation_attention_projection(sv):
+    """The operators as they run together: fused projection, norm and rotation in place, packed attention, output
+    projection with its residual, against the same chain in 64 bits rounded where the library stores F16."""
+    lens, heads, d, width = [196, 729, 64], 16, 72, 1152
+    rows = sum(lens)
+    x = _randn(1, rows, width).half()
+    w1, b1 = (_randn(2, 3 * width, width) / 34).half(), (_randn(3, 3 * width) * 0.1).half()
+    w2, b2 = (_randn(4, width, width) / 34).half(), (_randn(5, width) * 0.1).half()
+    gq, gk = (_randn(6, d) * 0.1 + 1).half(), (_randn(7, d) * 0.1 + 1).half()
+    side = [14, 27, 8]
+    pos = torch.cat([torch.stack([torch.arange(n * n) // n, torch.arange(n * n) % n]) for n in side], 1).int().cuda()
+    plan = sv.sv_rope_plan_init(d, 2, sv.SV_ROPE_HALF, 100.0)
+    qkv = torch.empty(rows, 3 * width, dtype=torch.float16, device="cuda")
+    sv.sv_gemm_bias_act(x, w1, b1, None, 1, None, qkv, rows, 3 * width, width)
+    raw = qkv.clone()
+    q, k, v = qkv[:, :width], qkv[:, width:2 * width], qkv[:, 2 * width:]
+    s = 3 * width
+    sv.sv_qk_norm_rope(q, k, q, k, gq, gk, pos, plan, rows, heads, heads, d, q_stride=s, k_stride=s, q_out_stride=s,
+                       k_out_stride=s)
+    o = torch.empty(rows, width, dtype=torch.float16, device="cuda")
+    off = _offsets(lens)
+    ws = torch.zeros(sv.sv_attention_packed_workspace(3, rows, rows, heads, heads, d), dtype=torch.uint8, device="cuda")
+    sv.sv_attention_packed(q, k, v, o, off, off, 3, rows, rows, heads, heads, d, q_stride=s, k_stride=s, v_stride=s,
+                           workspace=ws)
+    y = torch.empty(rows, width, dtype=torch.float16, device="cuda")
+    sv.sv_gemm_bias_act(o, w2, b2, None, 1, x, y, rows, width, width)
+    sv.sv_sync()
+
+    import numpy as np
+    import rope_ref
+    ref = (x.double() @ w1.double().t() + b1.double())
+    assert (raw.double() - ref).abs().max() <= 2.0 ** -10 * ref.abs().max()
+    full = raw.double().cpu().numpy().reshape(rows, 3 * heads, d)
+    parts = []
+    for j, g in ((0, gq), (1, gk)):
+        z = rope_ref.head_norm(full[:, j * heads:(j + 1) * heads], g.double().cpu().numpy(), 0, 1e-6)
+        parts.append(torch.from_numpy(np.ascontiguousarray(rope_ref.rotate(z, pos.cpu().numpy(), d, 2, 0, 100.0)[0])))
+    qr, kr = (p.half().cuda() for p in parts)
+    vr = raw[:, 2 * width:].reshape(rows, heads, d)
+    outs, a = [], 0
+    for n in lens:
+        outs.append(packed_ref.document(qr[a:a + n], kr[a:a + n], vr[a:a + n])[0].reshape(n, width))
+        a += n
+    oref = torch.cat(outs)
+    # F16 operands one rounding apart move a score by up to 2^-11 of its terms (here below 1 in sum)
+    assert (o.double() - oref).abs().max() <= 2.0 ** -8 * oref.abs().max()
+    yref = oref @ w2.double().t() + b2.double() + x.double()
+    assert (y.double() - yref).abs().max() <= 2.0 ** -8 * yref.abs().max()

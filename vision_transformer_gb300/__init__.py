@@ -26,7 +26,23 @@ STATUS_NAMES = ("SV_OK", "SV_ERR_INVALID_ARG", "SV_ERR_UNSUPPORTED", "SV_ERR_NOT
 
 # (name, restype, argtypes) of every exported function, in header order.
 _VP, _I, _U64, _F, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_uint64, ctypes.c_float, ctypes.c_size_t
+_LL = ctypes.c_longlong
 _IP, _DP, _LLP = ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_longlong)
+
+
+class SvRopePlan(ctypes.Structure):
+    """sv_rope_plan: a rotation, filled by :func:`sv_rope_plan_init`."""
+    _fields_ = [("rot_dim", ctypes.c_int), ("axes", ctypes.c_int), ("layout", ctypes.c_int), ("pairs", ctypes.c_int),
+                ("gain", ctypes.c_float), ("turns", ctypes.c_ulonglong * 128)]
+
+
+class SvAttentionOptions(ctypes.Structure):
+    """sv_attention_options, see :func:`sv_attention_options`."""
+    _fields_ = [("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("mask", ctypes.c_int),
+                ("prefix", ctypes.c_void_p), ("slopes", ctypes.c_void_p)]
+
+
+_PP, _OP = ctypes.POINTER(SvRopePlan), ctypes.POINTER(SvAttentionOptions)
 SIGNATURES = [
     ("sv_init_weights", _I, [_U64]),
     ("sv_init_weights_dims", _I, [_U64, _I, _I, _I, _I, _I, _I]),
@@ -48,6 +64,12 @@ SIGNATURES = [
     ("sv_map_pool_static", _I, [_VP, _VP, _I, _I, _VP]),
     ("sv_quantize_e4m3", _I, [_VP, _VP, _SZ, _VP]),
     ("sv_make_pixels", _I, [_U64, _I, _VP, _VP]),
+    ("sv_rope_plan_init", _I, [_PP, _I, _I, _I, ctypes.c_double, _I, ctypes.c_double, _I]),
+    ("sv_rope", _I, [_VP, _VP, _VP, _PP, _I, _I, _I, _LL, _LL, _VP]),
+    ("sv_qk_norm_rope", _I, [_VP, _VP, _VP, _VP, _VP, _VP, _I, _F, _VP, _PP, _I, _I, _I, _I, _LL, _LL, _LL, _LL, _VP]),
+    ("sv_attention_packed_workspace", _SZ, [_I, _I, _I, _I, _I, _I]),
+    ("sv_attention_packed", _I, [_VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _I, _I, _LL, _LL, _LL, _LL, _OP, _I,
+                                 _VP, _SZ, _VP]),
     ("sv_sync", _I, [_VP]),
     ("sv_last_error", ctypes.c_char_p, []),
     ("sv_launch_count", ctypes.c_longlong, []),
@@ -137,6 +159,10 @@ SV_ENCODE_EAGER = 4
 SV_ATTENTION_QK_E4M3 = 1
 (SV_STAGE_PATCH, SV_STAGE_QKV, SV_STAGE_ATTENTION, SV_STAGE_OUT_PROJ, SV_STAGE_MLP_UP, SV_STAGE_MLP_DOWN,
  SV_STAGE_FINAL_LN) = range(7)
+SV_ROPE_HALF, SV_ROPE_INTERLEAVED = 0, 1
+SV_ROPE_SCALE_NONE, SV_ROPE_SCALE_LINEAR, SV_ROPE_SCALE_BASE, SV_ROPE_SCALE_BY_PARTS = range(4)
+SV_NORM_RMS, SV_NORM_LAYER = 0, 1
+SV_MASK_DOCUMENT, SV_MASK_PREFIX = 0, 1
 
 
 def sv_encode_ex(pixels, out, batch: int, layers: int, gemm_dtype: int = SV_GEMM_F16, flags: int = 0, stream=None):
@@ -223,6 +249,57 @@ def sv_quantize_e4m3(x, y, n: int, stream=None):
 
 def sv_make_pixels(seed: int, batch: int, dst, stream=None):
     _check("sv_make_pixels", load().sv_make_pixels(seed, batch, _ptr(dst), _stream(stream)))
+
+
+def sv_rope_plan_init(rot_dim: int, axes: int = 1, layout: int = SV_ROPE_HALF, base: float = 10000.0,
+                      scaling: int = SV_ROPE_SCALE_NONE, factor: float = 1.0, original_len: int = 0) -> SvRopePlan:
+    """A rotation for sv_rope and sv_qk_norm_rope; computed on the host, needs no GPU."""
+    plan = SvRopePlan()
+    _check("sv_rope_plan_init", load().sv_rope_plan_init(plan, rot_dim, axes, layout, base, scaling, factor,
+                                                         original_len))
+    return plan
+
+
+def sv_rope(x, y, positions, plan: SvRopePlan, rows: int, heads: int, head_dim: int, x_stride: int = 0,
+            y_stride: int = 0, stream=None):
+    _check("sv_rope", load().sv_rope(_ptr(x), _ptr(y), _ptr(positions), plan, rows, heads, head_dim, x_stride,
+                                     y_stride, _stream(stream)))
+
+
+def sv_qk_norm_rope(q, k, q_out, k_out, q_gamma, k_gamma, positions, plan, rows: int, q_heads: int, kv_heads: int,
+                    head_dim: int, norm: int = SV_NORM_RMS, eps: float = 1e-6, q_stride: int = 0, k_stride: int = 0,
+                    q_out_stride: int = 0, k_out_stride: int = 0, stream=None):
+    """plan None (and positions None): the norm alone."""
+    _check("sv_qk_norm_rope", load().sv_qk_norm_rope(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), _ptr(q_gamma),
+                                                     _ptr(k_gamma), norm, eps, _ptr(positions), plan, rows, q_heads,
+                                                     kv_heads, head_dim, q_stride, k_stride, q_out_stride,
+                                                     k_out_stride, _stream(stream)))
+
+
+def sv_attention_options(scale: float = 0.0, softcap: float = 0.0, mask: int = SV_MASK_DOCUMENT, prefix=None,
+                         slopes=None) -> SvAttentionOptions:
+    """Options of sv_attention_packed; keeps prefix and slopes (tensors or device pointers) alive."""
+    opt = SvAttentionOptions(scale, softcap, mask, _ptr(prefix), _ptr(slopes))
+    opt.tensors = (prefix, slopes)
+    return opt
+
+
+def sv_attention_packed_workspace(docs: int, total_q: int, total_k: int, q_heads: int, kv_heads: int,
+                                  head_dim: int) -> int:
+    return int(load().sv_attention_packed_workspace(docs, total_q, total_k, q_heads, kv_heads, head_dim))
+
+
+def sv_attention_packed(q, k, v, o, q_offsets, k_offsets, docs: int, total_q: int, total_k: int, q_heads: int,
+                        kv_heads: int, head_dim: int, q_stride: int = 0, k_stride: int = 0, v_stride: int = 0,
+                        o_stride: int = 0, options: SvAttentionOptions | None = None, out_dtype: int = SV_DT_F16,
+                        workspace=None, workspace_bytes: int | None = None, stream=None):
+    """workspace: a zeroed tensor of sv_attention_packed_workspace() bytes (or a device pointer and workspace_bytes)."""
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check("sv_attention_packed", load().sv_attention_packed(
+        _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(q_offsets), _ptr(k_offsets), docs, total_q, total_k, q_heads,
+        kv_heads, head_dim, q_stride, k_stride, v_stride, o_stride, options, out_dtype, _ptr(workspace),
+        workspace_bytes, _stream(stream)))
 
 
 def sv_sync(stream=None):

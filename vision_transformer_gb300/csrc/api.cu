@@ -14,6 +14,7 @@
 #include <vector>
 
 #include "../../synth/synth.h"
+#include "ptx.cuh"
 #include "sv_internal.h"
 
 namespace sv {
@@ -1281,6 +1282,10 @@ sv_status sv_sync(void* stream) {
   if (e != cudaSuccess) return cuda_fail(e, "sv_sync (error word)");
   if (flag) {
     cudaMemset(g_rt.dev_err, 0, sizeof(int));
+    if (!(flag & kDevErrTimeout)) {
+      set_error("sv_attention_packed: document offsets decrease or leave [0, total]; its outputs are undefined");
+      return SV_ERR_INVALID_ARG;
+    }
     set_error("a kernel gave up a bounded wait (device error word 0x%x); its outputs are undefined", flag);
     return SV_ERR_TIMEOUT;
   }

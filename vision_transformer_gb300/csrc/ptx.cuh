@@ -6,7 +6,7 @@
 namespace sv {
 
 // Device error word codes (set by kernels, read by sv_sync).
-enum : int { kDevErrTimeout = 1 };
+enum : int { kDevErrTimeout = 1, kDevErrOffsets = 2 };
 
 // A bounded wait gives up after this many nanoseconds of %globaltimer.
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;
