@@ -453,8 +453,8 @@ size_t sv_attention_packed_workspace(int docs, int total_q, int total_k, int q_h
  * the inputs. Scores, softmax and accumulation in F32; the probabilities are rounded to F16 for their product with v.
  * q_offsets, k_offsets: device int32 [docs + 1], non-decreasing: document d has queries q_offsets[d] ..
  * q_offsets[d + 1] - 1 and keys likewise (either may be none). NULL: documents of equal size, total_q / docs or
- * total_k / docs. Rows of o outside every document are left as they were. Offsets that decrease or leave [0, total]
- * are held to that range, and the next sv_sync reports SV_ERR_INVALID_ARG; outputs are then undefined.
+ * total_k / docs. Rows of o outside every document are left as they were. With offsets that
+ * decrease or leave [0, total] the call computes nothing, and the next sv_sync reports SV_ERR_INVALID_ARG.
  * workspace: NULL, or sv_attention_packed_workspace() bytes of device memory, 16-byte aligned, that were zero before
  * their first use by this function; every call leaves what the next one needs, of the same sizes or others. Without
  * it, results are the same up to rounding, but few queries over many keys use few SMs. Calls that may run at the same

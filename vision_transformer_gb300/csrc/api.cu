@@ -1283,7 +1283,7 @@ sv_status sv_sync(void* stream) {
   if (flag) {
     cudaMemset(g_rt.dev_err, 0, sizeof(int));
     if (!(flag & kDevErrTimeout)) {
-      set_error("sv_attention_packed: document offsets decrease or leave [0, total]; its outputs are undefined");
+      set_error("sv_attention_packed: document offsets decrease or leave [0, total]; nothing was computed");
       return SV_ERR_INVALID_ARG;
     }
     set_error("a kernel gave up a bounded wait (device error word 0x%x); its outputs are undefined", flag);

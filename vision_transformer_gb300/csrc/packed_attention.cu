@@ -6,6 +6,24 @@
 //   s_j = scale q . k_j;  s_j = cap tanh(s_j / cap);  s_j -= slope |p_i - j|,
 //   o = sum_j 2^(s_j log2 e - m) v_j / sum_j 2^(s_j log2 e - m),
 // m following the running maximum. lim = 0 gives zeros.
+//
+// One pass over the keys on the tensor cores, scores never leaving the SM. A tile of 128
+// rows holds 128 / group queries with the `group` query heads of one key head (row r =
+// query r / group, head r % group), so shared key heads are read once for all of them, and
+// a single query of many heads fills rows. Persistent CTAs (one per SM) walk work items of
+// two such tiles against the document's key tiles of 128; 320 threads:
+//   warp 0      works out the items from the documents' lengths on the device (the lengths
+//               never visit the host) and copies: Q of an item, key and value tiles in turn
+//               into a ring, all by TMA from the caller's strided rows (values past a head's
+//               width arrive as zeros: no copy into a padded layout);
+//   warp 1      the MMA issuer: S_w = Q_w K^T (both in shared memory, 128-byte swizzle),
+//               O_w += P_w V (P from tensor memory);
+//   warps 2..5  softmax of tile 0, warps 6..9 of tile 1: a thread per row turns its S row into
+//               P (F16, over S in tensor memory), keeps the exponent and the sum in F32, and
+//               rescales O in tensor memory when the exponent rises by more than 2^15.
+// Key ranges are divided among CTAs when there are few items (Schedule); the parts' O, m and
+// l go to the caller's workspace and the last of them to arrive joins them in order.
+// Tensor memory: S_0, S_1, O_0, O_1 of 128 columns each.
 #include <cuda_fp8.h>
 
 #include <cmath>
@@ -17,6 +35,21 @@ namespace sv {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kTile = 128;                  // rows of a query tile, keys of a key tile
+constexpr int kBoxBytes = kTile * 128;      // 128 rows of 64 values: one box of an operand tile
+constexpr int kThreads = 320;
+constexpr int kBarBytes = 768;              // barriers, TMEM address slot, abort flag, items
+constexpr int kItems = 4;                   // work items between the copy warp and the others
+constexpr uint32_t kTmemCols = 512;
+constexpr int kMaxGrid = 152;               // CTAs of a launch at most (the workspace is sized by it)
+constexpr int kMaxSlots = 2 * kMaxGrid;     // partial results of a launch at most (see Schedule)
+constexpr int kMinSplit = 2;                // key tiles of a divided range at least
+constexpr size_t kCounterBytes = size_t(kMaxSlots) * 8 * sizeof(unsigned);
+
+// The reference exponent of a row is set kHead below a tile's maximum when that maximum is
+// more than kSlack above it: P <= 2^15 stays finite in F16, small probabilities stay above
+// its subnormal range for longer, and O is rescaled rarely.
+constexpr float kSlack = 15.0f, kHead = 8.0f;
 
 struct PackedParams {
   const __half *q, *k, *v;
@@ -27,100 +60,745 @@ struct PackedParams {
   long long qs, ks, vs, os;
   float scale, cap;
   int causal, out_e4m3;
+  int qt;              // queries of a tile: 128 / group
+  unsigned* counters;  // workspace: arrivals of each divided tile and warp; null: nothing is divided
+  float* partial;      // workspace: partial results
   int* err;
 };
 
-// Offset d of `docs` documents: the caller's, held to [0, total], or equal lengths.
+template <int NB>
+struct Smem {
+  static constexpr int kQBufs = NB == 1 ? 2 : 1;
+  static constexpr int kStages = NB == 1 ? 8 : 5;  // key and value tiles in turn
+  static constexpr int kOp = NB * kBoxBytes;       // one operand tile
+  static constexpr int kOffKV = 2 * kQBufs * kOp;
+  static constexpr int kOffBar = kOffKV + kStages * kOp;
+  static constexpr int kBytes = 1024 + kOffBar + kBarBytes;
+  static_assert(kBytes <= 232448, "shared memory budget");
+};
+
+enum {
+  kBarQFull = 0,    // +buffer
+  kBarQEmpty = 2,   // +buffer: the item's last S products have read Q
+  kBarFull = 4,     // +stage
+  kBarEmpty = 12,   // +stage
+  kBarSFull = 20,   // +group: S_w has finished (and with it the P V products before it)
+  kBarPFull = 22,   // +group: the group has written P_w (and any O rescale) to TMEM
+  kBarDrain = 24,
+  kBarItem = 25,       // +item slot: the copy warp has written the item
+  kBarItemDone = 29,   // +item slot: the issuer and the eight softmax warps are through with it
+  kBarOFull = 33,      // +group: the item's last P V product of the group has finished
+  kNumBars = 35
+};
+
+// Offset d of `docs` documents: the caller's, or equal lengths.
 __device__ __forceinline__ int offset_of(const int* off, int d, int docs, int total) {
-  if (!off) return int(static_cast<long long>(total / docs) * d);
-  return min(max(off[d], 0), total);
+  return off ? __ldg(off + d) : (total / docs) * d;
 }
 
 // Visible keys of a query at position `at` (p_i) of a document with lk keys.
-__device__ __forceinline__ int limit_of(bool causal, int at, int lk, int prefix) {
+__device__ __forceinline__ int limit_of(int causal, int at, int lk, int prefix) {
   return causal ? min(lk, max(max(at + 1, prefix), 0)) : lk;
 }
 
-__device__ __forceinline__ float score_of(float s, float cap) { return cap > 0.0f ? cap * tanhf(s / cap) : s; }
+// One work item: up to 2 qt queries of a document with the query heads of one key head
+// (two tiles of rows, row r = query r / group, head r % group), over key tiles jb .. je - 1.
+struct Item {
+  int q0, nq;           // first query (row of q), queries of the item
+  int k0, lk;           // the document's keys
+  int at, prefix, kvh;  // position of the first query among the keys
+  int jb, je;           // key tiles
+  int slot, splits, split;  // partial result; splits 1: none
+  int live;             // 0: no more items
+};
+constexpr int kOffItems = 8 * kNumBars + 8;  // in the barrier area
+static_assert(kOffItems + kItems * sizeof(Item) <= kBarBytes, "barrier area");
 
-// One warp per (query, head): 32 keys at a time, a lane's key dotted with q from shared
-// memory, then a lane's output columns summed over the 32 keys.
-__global__ void __launch_bounds__(128) packed_rows_kernel(const PackedParams p) {
-  __shared__ float qs[4][128];
-  __shared__ float ps[4][32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (blockIdx.x == 0 && warp == 0)  // the documents' offsets, once
-    for (int d = lane; d < p.docs; d += 32) {
-      bool bad = false;
-      if (p.q_off) bad |= p.q_off[d] < 0 || p.q_off[d + 1] < p.q_off[d] || p.q_off[d + 1] > p.total_q;
-      if (p.k_off) bad |= p.k_off[d] < 0 || p.k_off[d + 1] < p.k_off[d] || p.k_off[d + 1] > p.total_k;
-      if (bad) atomicOr(p.err, kDevErrOffsets);
+// The items in order, worked out by the copy warp from the documents' lengths: a
+// chunk of 32 documents at a time, one per lane, with their item counts summed by shuffles.
+// Within a document: key heads, then pairs of tiles from the last (longest) on, then parts
+// of the key range. Where the launch has less work than its CTAs could share evenly, a
+// document's key range is divided into parts of at most `chunk` tiles, chunk = the launch's
+// key tiles per CTA: then a launch has at most 2 x grid parts in divided ranges, since a
+// range of n > chunk tiles has ceil(n / chunk) <= 2 n / chunk parts.
+class Schedule {
+ public:
+  __device__ __forceinline__ Schedule(const PackedParams& p, int lane) : p_(p), lane_(lane), docs_(p.docs) {
+    long long work = 0;
+    bool bad = false;
+    for (int d0 = 0; d0 < p.docs; d0 += 32) {
+      load(d0);
+      bad |= bad_;
+      work += static_cast<long long>(pairs_) * tiles_;
     }
-  const long long job = static_cast<long long>(blockIdx.x) * 4 + warp;
-  const int row = int(job / p.hq), h = int(job % p.hq);
-  if (row >= p.total_q) return;
-  int doc = -1;
-  for (int d0 = 0; d0 < p.docs && doc < 0; d0 += 32) {
-    const int d = d0 + lane;
-    const bool in = d < p.docs && offset_of(p.q_off, d, p.docs, p.total_q) <= row &&
-                    row < offset_of(p.q_off, d + 1, p.docs, p.total_q);
-    const unsigned hit = __ballot_sync(0xffffffffu, in);
-    if (hit) doc = d0 + __ffs(hit) - 1;
+    for (int o = 16; o; o >>= 1) work += __shfl_xor_sync(0xffffffffu, work, o);
+    const long long share = (work * p.hk + int(gridDim.x) - 1) / int(gridDim.x);
+    chunk_ = p.counters ? int(min(max(share, static_cast<long long>(kMinSplit)), 0x7fffffffll)) : 0x7fffffff;
+    // offsets that decrease or leave [0, total]: reported, and nothing is computed, since
+    // the bounds on items and parts hold for documents that do not overlap
+    if (__any_sync(0xffffffffu, bad)) {
+      if (lane == 0) atomicOr(p.err, kDevErrOffsets);
+      docs_ = 0;
+    }
+    if (p.docs > 32 || docs_ == 0) load(0);
+    open(0);
   }
-  if (doc < 0) return;
-  const int q0 = offset_of(p.q_off, doc, p.docs, p.total_q), q1 = offset_of(p.q_off, doc + 1, p.docs, p.total_q);
-  const int k0 = offset_of(p.k_off, doc, p.docs, p.total_k);
-  const int lk = max(0, offset_of(p.k_off, doc + 1, p.docs, p.total_k) - k0);
-  const int at = row - q0 + lk - (q1 - q0);
-  const int lim = limit_of(p.causal, at, lk, p.prefix ? p.prefix[doc] : 0);
-  const float slope = p.slopes ? p.slopes[h] : 0.0f;
-  const __half* q = p.q + row * p.qs + h * p.D;
-  for (int c = lane; c < p.D; c += 32) qs[warp][c] = __half2float(q[c]);
-  __syncwarp();
-  const __half* kb = p.k + k0 * p.ks + (h / p.group) * p.D;
-  const __half* vb = p.v + k0 * p.vs + (h / p.group) * p.D;
-  float m = -INFINITY, l = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int j0 = 0; j0 < lim; j0 += 32) {
-    const int j = j0 + lane, n = min(32, lim - j0);
-    float s = -INFINITY;
-    if (j < lim) {
-      const __half* kr = kb + j * p.ks;
-      float dot = 0.0f;
-      for (int c = 0; c < p.D; ++c) dot = fmaf(qs[warp][c], __half2float(kr[c]), dot);
-      s = score_of(dot * p.scale, p.cap) - slope * fabsf(float(at - j));
-      s *= kLog2e;
+  // Item number `it` (increasing from call to call); false behind the last.
+  __device__ __forceinline__ bool get(int it, Item& r) {
+    while (it >= base_ + total_) {
+      if (d0_ + 32 >= docs_) return false;
+      base_ += total_;
+      slot_base_ += slot_total_;
+      load(d0_ + 32);
+      open(d0_ + 32);
     }
-    float mx = s;
-    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    const float mn = fmaxf(m, mx), ref = mn == -INFINITY ? 0.0f : mn;
-    const float f = exp2f(m - ref);
-    const float e = j < lim ? exp2f(s - ref) : 0.0f;
-    float es = e;
-    for (int o = 16; o; o >>= 1) es += __shfl_xor_sync(0xffffffffu, es, o);
-    l = l * f + es;
+    const int at = it - base_;
+    const int src = __ffs(__ballot_sync(0xffffffffu, incl_ > at)) - 1;
+    auto of = [&](int v) { return __shfl_sync(0xffffffffu, v, src); };
+    const int pairs = of(pairs_), splits = of(splits_), tiles = of(tiles_);
+    int k = at - of(incl_ - count_);
+    r.slot = slot_base_ + of(slot_incl_ - (splits_ > 1 ? count_ : 0)) + k;
+    r.splits = splits;
+    r.split = k % splits;
+    k /= splits;
+    r.kvh = k / pairs;
+    const int pair = pairs - 1 - (k - r.kvh * pairs);
+    const int lq = of(lq_);
+    r.lk = of(lk_);
+    r.k0 = of(k0_);
+    r.prefix = of(prefix_);
+    const int i0 = pair * 2 * p_.qt;
+    r.q0 = of(q0_) + i0;
+    r.nq = min(lq - i0, 2 * p_.qt);
+    r.at = i0 + r.lk - lq;
+    const int n = (limit_of(p_.causal, r.at + r.nq - 1, r.lk, r.prefix) + kTile - 1) / kTile;
+    const int part = (tiles + splits - 1) / splits;
+    r.jb = min(r.split * part, n);
+    r.je = min(r.jb + part, n);
+    return true;
+  }
+
+ private:
+  __device__ __forceinline__ void load(int d0) {
+    const int d = d0 + lane_;
+    lq_ = lk_ = q0_ = k0_ = prefix_ = 0;
+    bad_ = false;
+    if (d < docs_) {
+      q0_ = offset_of(p_.q_off, d, p_.docs, p_.total_q);
+      k0_ = offset_of(p_.k_off, d, p_.docs, p_.total_k);
+      lq_ = offset_of(p_.q_off, d + 1, p_.docs, p_.total_q) - q0_;
+      lk_ = offset_of(p_.k_off, d + 1, p_.docs, p_.total_k) - k0_;
+      bad_ = q0_ < 0 || lq_ < 0 || q0_ + static_cast<long long>(lq_) > p_.total_q || k0_ < 0 || lk_ < 0 ||
+             k0_ + static_cast<long long>(lk_) > p_.total_k;
+      prefix_ = p_.prefix ? __ldg(p_.prefix + d) : 0;
+    }
+    pairs_ = (lq_ + 2 * p_.qt - 1) / (2 * p_.qt);
+    tiles_ = (limit_of(p_.causal, lk_ - 1, lk_, prefix_) + kTile - 1) / kTile;  // of the last query
+  }
+  __device__ __forceinline__ void open(int d0) {
+    d0_ = d0;
+    splits_ = tiles_ > chunk_ ? (tiles_ + chunk_ - 1) / chunk_ : 1;
+    count_ = pairs_ * p_.hk * splits_;
+    incl_ = count_;
+    slot_incl_ = splits_ > 1 ? count_ : 0;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int a = __shfl_up_sync(0xffffffffu, incl_, o), b = __shfl_up_sync(0xffffffffu, slot_incl_, o);
+      if (lane_ >= o) incl_ += a, slot_incl_ += b;
+    }
+    total_ = __shfl_sync(0xffffffffu, incl_, 31);
+    slot_total_ = __shfl_sync(0xffffffffu, slot_incl_, 31);
+  }
+  const PackedParams& p_;
+  int lane_, docs_, chunk_;
+  bool bad_;
+  int d0_ = 0, base_ = 0, total_ = 0, slot_base_ = 0, slot_total_ = 0;
+  int lq_, lk_, q0_, k0_, prefix_, pairs_, tiles_, splits_, count_, incl_, slot_incl_;  // this lane's document
+};
+
+__device__ __forceinline__ void store8(const PackedParams& p, size_t at, const float* y) {
+  if (p.out_e4m3) {
+    uint2 w;
+    __nv_fp8x2_storage_t* h = reinterpret_cast<__nv_fp8x2_storage_t*>(&w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      h[i] = __nv_cvt_float2_to_fp8x2(make_float2(16.0f * y[2 * i], 16.0f * y[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.o) + at) = w;
+  } else {
+    uint4 w;
+    __half2* h = reinterpret_cast<__half2*>(&w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(y[2 * i], y[2 * i + 1]);
+    *reinterpret_cast<uint4*>(static_cast<__half*>(p.o) + at) = w;
+  }
+}
+
+// A row whose tensor-core result is not finite, again from the visible keys alone: a tile's
+// product multiplies the probability 0 of a hidden key with its value, which is NaN for an
+// infinite or NaN value. Keys kb .. ke - 1 of the document; the row's sums go to `out`
+// (head_dim columns apart by `step` floats), its exponent and denominator to m and l.
+__device__ __noinline__ void row_again(const PackedParams& p, const __half* q, const __half* k, const __half* v, int kb,
+                                       int ke, int at, float slope, float* acc, float& m_out, float& l_out) {
+  float m = -INFINITY, l = 0.0f;
+  for (int c = 0; c < p.D; ++c) acc[c] = 0.0f;
+  for (int j = kb; j < ke; ++j) {
+    const __half *kr = k + j * p.ks, *vr = v + j * p.vs;
+    float s = 0.0f;
+    for (int c = 0; c < p.D; ++c) s = fmaf(__half2float(q[c]), __half2float(kr[c]), s);
+    s *= p.scale;
+    if (p.cap > 0.0f) s = p.cap * tanhf(s / p.cap);
+    s = (s - slope * fabsf(float(at - j))) * kLog2e;
+    const float mn = (s > m || s != s) ? s : m;  // NaN stays
+    const float ref = mn == -INFINITY ? 0.0f : mn;
+    const float f = m == mn ? 1.0f : exp2f(m - ref), e = exp2f(s - ref);
+    l = l * f + e;
+    for (int c = 0; c < p.D; ++c) acc[c] = fmaf(e, __half2float(vr[c]), acc[c] * f);
     m = mn;
-    ps[warp][lane] = e;
-    __syncwarp();
-    for (int i = 0; i < 4; ++i) {
-      const int c = lane + 32 * i;
-      if (c >= p.D) break;
-      float a = acc[i] * f;
-      for (int jj = 0; jj < n; ++jj) a = fmaf(ps[warp][jj], __half2float(vb[(j0 + jj) * p.vs + c]), a);
-      acc[i] = a;
+  }
+  m_out = m;
+  l_out = l;
+}
+
+template <int NB, bool CAP, bool BIAS>
+// 10 warps: three share each of two SM sub-partitions, so a thread may hold at most
+// 16384 / (3 x 32) registers, rounded down to the allocation granule.
+__global__ void __maxnreg__(168)
+    packed_tile_kernel(const __grid_constant__ PackedParams p, const __grid_constant__ CUtensorMap tq,
+                       const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv) {
+  using L = Smem<NB>;
+  constexpr int kOp = L::kOp, kStages = L::kStages, kQBufs = L::kQBufs;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bar0 = sbase + L::kOffBar;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffBar + 8 * kNumBars);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  auto bar = [&](int i) { return bar0 + 8u * uint32_t(i); };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kQBufs; ++s) {
+      mbar_init(bar(kBarQFull + s), 1);
+      mbar_init(bar(kBarQEmpty + s), 1);
     }
-    __syncwarp();
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(bar(kBarFull + s), 1);
+      mbar_init(bar(kBarEmpty + s), 1);
+    }
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(bar(kBarSFull + w), 1);
+      mbar_init(bar(kBarPFull + w), 128);  // every softmax thread of the group arrives
+      mbar_init(bar(kBarOFull + w), 1);
+    }
+    for (int s = 0; s < kItems; ++s) {
+      mbar_init(bar(kBarItem + s), 1);
+      mbar_init(bar(kBarItemDone + s), 9);
+    }
+    mbar_init(bar(kBarDrain), 1);
+    *abort_flag = 0;
+    fence_barrier_init();
   }
-  const float inv = lim > 0 ? 1.0f / l : 0.0f;
-  for (int i = 0; i < 4; ++i) {
-    const int c = lane + 32 * i;
-    if (c >= p.D) break;
-    const size_t at_o = size_t(row) * size_t(p.os) + size_t(h) * size_t(p.D) + size_t(c);
-    const float y = lim > 0 ? acc[i] * inv : 0.0f;
-    if (p.out_e4m3)
-      static_cast<uint8_t*>(p.o)[at_o] = __nv_cvt_float_to_fp8(16.0f * y, __NV_SATFINITE, __NV_E4M3);
-    else
-      static_cast<__half*>(p.o)[at_o] = __float2half_rn(y);
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish();
   }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_launch_dependents();
+  pdl_wait();  // q, k, v, offsets, prefix and slopes may be written by the previous kernel
+  Item* items = reinterpret_cast<Item*>(smem + L::kOffBar + kOffItems);
+  auto item_wait = [&](int n) {
+    return mbar_wait(bar(kBarItem + n % kItems), (n / kItems) & 1, abort_flag, p.err);
+  };
+
+  if (warp == 0) {
+    Schedule sched(p, lane);
+    if (lane == 0) {
+      prefetch_tmap(&tq);
+      prefetch_tmap(&tk);
+      prefetch_tmap(&tv);
+    }
+    // copies in flight per full barrier (bit b: Q buffer b, 4 + stage) and their phase bits
+    uint32_t issued = 0, issued_phase = 0;
+    auto note = [&](int bit, uint32_t ph) {
+      issued |= 1u << bit;
+      issued_phase = (issued_phase & ~(1u << bit)) | (ph << bit);
+    };
+    const uint32_t q_bytes = uint32_t(2 * NB * 128 * p.group * p.qt);
+    int t = 0, n = 0;  // operand tiles and non-empty items so far
+    int told = 0;      // items written for the other warps
+    // The next item, written for the other warps. (It waits for the item four before to be
+    // written out, so it must not come before copies that this depends on.)
+    auto tell = [&](Item& r) -> int {
+      r.live = sched.get(int(blockIdx.x) + told * int(gridDim.x), r);
+      const int slot = told % kItems;
+      int ok = mbar_wait(bar(kBarItemDone + slot), ((told / kItems) & 1) ^ 1, abort_flag, p.err);
+      ok = __all_sync(0xffffffffu, ok);
+      if (ok && lane == 0) {
+        items[slot] = r;
+        mbar_arrive(bar(kBarItem + slot));
+      }
+      ++told;
+      return ok;
+    };
+    Item it;
+    int ok = 1;
+    while (ok && tell(it) && it.live) {
+      if (it.jb >= it.je) continue;
+      if (lane == 0) {
+        auto kv = [&](const CUtensorMap& map, int j) -> bool {
+          const int st = t % kStages;
+          const uint32_t ph = (t / kStages) & 1;
+          if (!mbar_wait(bar(kBarEmpty + st), ph ^ 1, abort_flag, p.err)) return false;
+          mbar_arrive_expect_tx(bar(kBarFull + st), kOp);
+          for (int b = 0; b < NB; ++b)
+            tma_load_3d(sbase + L::kOffKV + st * kOp + b * kBoxBytes, &map, bar(kBarFull + st), 64 * b, it.kvh,
+                        it.k0 + j * kTile);
+          note(4 + st, ph);
+          ++t;
+          return true;
+        };
+        ok = kv(tk, it.jb);
+        if (ok) {
+          const int qb = n % kQBufs;
+          const uint32_t ph = (n / kQBufs) & 1;
+          if ((ok = mbar_wait(bar(kBarQEmpty + qb), ph ^ 1, abort_flag, p.err))) {
+            mbar_arrive_expect_tx(bar(kBarQFull + qb), q_bytes);
+            for (int w = 0; w < 2; ++w)
+              for (int b = 0; b < NB; ++b)
+                tma_load_3d(sbase + (2 * qb + w) * kOp + b * kBoxBytes, &tq, bar(kBarQFull + qb), 64 * b,
+                            it.kvh * p.group, it.q0 + w * p.qt);
+            note(qb, ph);
+          }
+        }
+        for (int j = it.jb; ok && j < it.je; ++j) {
+          ok = kv(tv, j);
+          if (ok && j + 1 < it.je) ok = kv(tk, j + 1);
+        }
+      }
+      ++n;
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+    }
+    if (lane == 0)  // every copy this thread issued lands before the CTA can exit
+      for (int i = 0; i < 4 + kStages; ++i)
+        if (issued & (1u << i))
+          mbar_wait_bounded(bar(i < 4 ? kBarQFull + i : kBarFull + i - 4), (issued_phase >> i) & 1, p.err);
+  } else if (warp == 1) {
+    // The MMA issuer: S_0(0), S_1(0), then per key tile t of all items: O_0 += P_0(t) V_t,
+    // S_0(t+1), O_1 += P_1(t) V_t, S_1(t+1). MMAs run in issue order, so S_w(t+1)
+    // overwrites P_w(t) only after the product has read it, and the completion of
+    // S_w(t+1) also means that O_w holds the sum up to tile t.
+    constexpr uint32_t idesc_s = make_idesc(128, 128, 0, false);
+    const uint32_t idesc_o = make_idesc(128, (p.D + 15) / 16 * 16, 0, true);
+    const int steps = (p.D + 15) / 16;
+    auto stage = [&](int x) { return sbase + L::kOffKV + uint32_t(x % kStages) * kOp; };
+    auto issue_s = [&](int w, int qb, int x) {  // x: the key tile's place in the ring
+      const uint32_t qa = sbase + uint32_t(2 * qb + w) * kOp, ka = stage(x);
+      for (int kk = 0; kk < steps; ++kk) {
+        const uint32_t off = uint32_t(kk >> 2) * kBoxBytes + uint32_t(kk & 3) * 32;
+        mma_f16(tmem + uint32_t(128 * w), make_sdesc(qa + off, 16, 1024, 2), make_sdesc(ka + off, 16, 1024, 2),
+                idesc_s, kk > 0);
+      }
+      tc_commit(bar(kBarSFull + w));
+    };
+    auto issue_pv = [&](int w, int x, bool first) {
+      const uint32_t va = stage(x);
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk)  // 16 keys a step: 8 TMEM columns of P, 16 rows of V
+        mma_f16_ts(tmem + uint32_t(256 + 128 * w), tmem + uint32_t(128 * w + 8 * kk),
+                   make_sdesc(va + kk * 2048, kBoxBytes, 1024, 2), idesc_o, !first || kk > 0);
+    };
+    auto wait_full = [&](int x) { return mbar_wait(bar(kBarFull + x % kStages), (x / kStages) & 1, abort_flag, p.err); };
+    if (lane == 0) {
+      int read = 0;  // items so far
+      // key tiles of the next item that has any (0: there is none); -1 after a time-out, or
+      // where it is not there yet and `wait` is false
+      auto next = [&](bool wait) -> int {
+        for (;;) {
+          if (wait ? !item_wait(read) : !mbar_test(bar(kBarItem + read % kItems), (read / kItems) & 1)) return -1;
+          const Item& r = items[read % kItems];
+          const int live = r.live, tiles = r.je - r.jb;
+          mbar_arrive(bar(kBarItemDone + read % kItems));
+          if (!live) return 0;
+          ++read;
+          if (tiles > 0) return tiles;
+        }
+      };
+      int tiles = next(true);
+      bool ok = tiles > 0 && wait_full(0) && mbar_wait(bar(kBarQFull), 0, abort_flag, p.err);
+      if (ok) {
+        tc_fence_after();
+        issue_s(0, 0, 0);
+        issue_s(1, 0, 0);
+        tc_commit(bar(kBarEmpty));
+        if (tiles == 1) tc_commit(bar(kBarQEmpty));
+      }
+      int x = 0, tt = 0;  // ring place of the current key tile, tiles so far
+      for (int n = 0; ok && tiles > 0; ++n) {
+        int more = 0;  // key tiles of the next item
+        for (int j = 0; ok && j < tiles; ++j, ++tt, x += 2) {
+          // ring: key tile at x, its values at x + 1, the next key tile at x + 2
+          const bool last = j + 1 == tiles;
+          const int qb = (last ? n + 1 : n) % kQBufs;
+          auto next_s = [&](int w) {
+            if (w == 0) {
+              ok = wait_full(x + 2) &&
+                   (!last || mbar_wait(bar(kBarQFull + qb), ((n + 1) / kQBufs) & 1, abort_flag, p.err));
+              if (!ok) return;
+              tc_fence_after();
+            }
+            issue_s(w, qb, x + 2);
+            if (w == 1) {
+              tc_commit(bar(kBarEmpty + (x + 2) % kStages));
+              // the last S product of its item has read Q
+              if (last ? more == 1 : j + 2 == tiles) tc_commit(bar(kBarQEmpty + qb));
+            }
+          };
+          bool late = false;  // the next item was not there for S_0
+          for (int w = 0; w < 2 && ok; ++w) {
+            ok = mbar_wait(bar(kBarPFull + w), tt & 1, abort_flag, p.err) && (w == 1 || wait_full(x + 1));
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv(w, x + 1, j == 0);
+            if (w == 1) tc_commit(bar(kBarEmpty + (x + 1) % kStages));
+            if (last) {
+              tc_commit(bar(kBarOFull + w));
+              // The copy warp may need this item's slot for the next one (behind items without
+              // keys): both groups' O must be on their way before the issuer waits for it.
+              if (w == 0) late = (more = next(false)) < 0;
+              else if (late && (more = next(true)) < 0) ok = false;
+              if (!ok || more == 0 || (w == 0 && late)) continue;
+              if (late) next_s(0);
+            }
+            if (ok) next_s(w);
+          }
+        }
+        tiles = more;
+      }
+    }
+    if (lane == 0) {
+      tc_commit(bar(kBarDrain));
+      mbar_wait_bounded(bar(kBarDrain), 0, p.err);
+    }
+  } else {
+    const int w = (warp - 2) >> 2;  // softmax group
+    const int sub = warp & 3;       // TMEM lane quarter
+    const int r = sub * 32 + lane;  // row of the group's tile == TMEM lane
+    const uint32_t lane_off = uint32_t(sub * 32) << 16;
+    const uint32_t s_tm = tmem + uint32_t(w * 128) + lane_off;
+    const uint32_t o_tm = tmem + uint32_t(256 + w * 128) + lane_off;
+    const int qi = r / p.group, head = r - qi * p.group;  // this row's query in the tile, head in the group
+    const int Dn = (p.D + 15) / 16 * 16;
+    const float sl2 = CAP ? 2.0f * kLog2e * p.scale / p.cap : kLog2e * p.scale;
+    const float cap2 = p.cap * kLog2e;
+    // query of this row in an item: index, -1 if the row holds none
+    auto query = [&](const Item& it) {
+      const int i = w * p.qt + qi;
+      return (qi < p.qt && i < it.nq) ? i : -1;
+    };
+    auto out_at = [&](const Item& it, int i) {
+      return size_t(it.q0 + i) * size_t(p.os) + size_t(it.kvh * p.group + head) * size_t(p.D);
+    };
+    float m = -INFINITY, l = 0.0f;
+
+    // Adds the parts of a divided range, once this warp is the last of the range's CTAs to
+    // arrive: in the order of the parts, so that the result does not depend on who is last.
+    auto join = [&](const Item& it) {
+      __threadfence();
+      __syncwarp();
+      unsigned seen = 0;
+      const int first = it.slot - it.split;
+      if (lane == 0)  // counts 0 .. splits - 1 and starts again at 0
+        seen = atomicInc(p.counters + size_t(first) * 8 + (w * 4 + sub), unsigned(it.splits - 1));
+      seen = __shfl_sync(0xffffffffu, seen, 0);
+      if (seen != unsigned(it.splits - 1)) return;
+      __threadfence();
+      const int i = query(it);
+      const float* base = p.partial + (size_t(first) * 2 + w) * size_t(Dn + 2) * kTile + r;
+      const size_t stride = size_t(2) * size_t(Dn + 2) * kTile;  // to the next part
+      float mx = -INFINITY, sum = 0.0f;
+      for (int s = 0; s < it.splits; ++s) mx = fmaxf(mx, __ldcg(base + s * stride));
+      const float ref = mx == -INFINITY ? 0.0f : mx;
+      for (int s = 0; s < it.splits; ++s) sum += ex2(__ldcg(base + s * stride) - ref) * __ldcg(base + s * stride + kTile);
+      if (i < 0) return;
+      const bool none = limit_of(p.causal, it.at + i, it.lk, it.prefix) == 0;
+      const float inv = 1.0f / sum;
+      const size_t at = out_at(it, i);
+      for (int c = 0; c < p.D; c += 8) {
+        float y[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+        for (int s = 0; s < it.splits; ++s) {
+          const float* b = base + s * stride;
+          const float pm = __ldcg(b);
+          if (pm == -INFINITY) continue;  // no key of this part is visible
+          const float f = ex2(pm - ref);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] = fmaf(f, __ldcg(b + size_t(2 + c + e) * kTile), y[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = none ? 0.0f : y[e] * inv;
+        store8(p, at + c, y);
+      }
+    };
+
+    // The item's rows once its last P V has finished: O / l as the output, or O, m and l as
+    // a part of a divided range.
+    auto write_item = [&](const Item& it) {
+      const int i = query(it);
+      const bool part = it.splits > 1;
+      float* pb = p.partial + (size_t(it.slot) * 2 + w) * size_t(Dn + 2) * kTile + r;
+      const int lim = i < 0 ? 0 : limit_of(p.causal, it.at + i, it.lk, it.prefix);
+      const float inv = part ? 1.0f : 1.0f / l;
+      const size_t at = i < 0 ? 0 : out_at(it, i);
+      float bad = 0.0f;  // NaN once a value of the row is not finite
+      for (int c = 0; c < p.D; c += 8) {
+        uint32_t o[8];
+        tmem_ld8(o_tm + uint32_t(c), o);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) asm volatile("" : "+r"(o[e]));  // no use before the wait
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          y[e] = __uint_as_float(o[e]) * inv;
+          if (lim == 0) y[e] = 0.0f;
+          bad = fmaf(y[e], 0.0f, bad);
+        }
+        if (i < 0) continue;
+        if (part) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) __stcg(pb + size_t(2 + c + e) * kTile, y[e]);
+        } else {
+          store8(p, at + c, y);
+        }
+      }
+      if (i >= 0 && bad != 0.0f) {
+        float acc[128];
+        const __half* q = p.q + static_cast<long long>(it.q0 + i) * p.qs + (it.kvh * p.group + head) * p.D;
+        row_again(p, q, p.k + it.k0 * p.ks + it.kvh * p.D, p.v + it.k0 * p.vs + it.kvh * p.D, it.jb * kTile,
+                  min(lim, it.je * kTile), it.at + i, p.slopes ? __ldg(p.slopes + it.kvh * p.group + head) : 0.0f, acc,
+                  m, l);
+        for (int c = 0; c < p.D; c += 8) {
+          float y[8];
+          for (int e = 0; e < 8; ++e) y[e] = part ? acc[c + e] : acc[c + e] / l;
+          if (part)
+            for (int e = 0; e < 8; ++e) __stcg(pb + size_t(2 + c + e) * kTile, y[e]);
+          else
+            store8(p, at + c, y);
+        }
+      }
+      if (part) {
+        __stcg(pb, lim > it.jb * kTile ? m : -INFINITY);
+        __stcg(pb + kTile, lim > it.jb * kTile ? l : 0.0f);
+        join(it);
+      }
+    };
+    // An item without keys: zeros, or an empty part.
+    auto write_none = [&](const Item& it) {
+      const int i = query(it);
+      if (it.splits > 1) {
+        float* pb = p.partial + (size_t(it.slot) * 2 + w) * size_t(Dn + 2) * kTile + r;
+        __stcg(pb, -INFINITY);
+        __stcg(pb + kTile, 0.0f);
+        join(it);
+      } else if (i >= 0) {
+        const float y[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+        for (int c = 0; c < p.D; c += 8) store8(p, out_at(it, i) + c, y);
+      }
+    };
+
+    // through with item n
+    auto done = [&](int n) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarItemDone + n % kItems));
+    };
+    int pending = -1;  // the item whose rows are not written yet
+    int full = 0;      // items with keys so far
+    // O of the pending item is final: its rows are written
+    auto flush = [&]() -> bool {
+      if (pending < 0) return true;
+      if (!__all_sync(0xffffffffu, mbar_wait(bar(kBarOFull + w), (full - 1) & 1, abort_flag, p.err))) return false;
+      tc_fence_after();
+      write_item(items[pending % kItems]);
+      done(pending);
+      pending = -1;
+      return true;
+    };
+    bool ok = true;
+    int t = 0;  // S tiles so far
+    for (int n = 0;; ++n) {
+      if (!__all_sync(0xffffffffu, item_wait(n))) {
+        ok = false;
+        break;
+      }
+      const Item& it = items[n % kItems];
+      if (!it.live) break;
+      const int jb = it.jb, je = it.je;
+      if (jb >= je) {  // (the pending item's slot may be the one that the copy warp waits for)
+        if (!(ok = flush())) break;
+        write_none(it);
+        done(n);
+        continue;
+      }
+      const int i = query(it);
+      const int at = it.at + i;
+      // rows without a query are computed like the others and never stored
+      const int lim = i < 0 ? 0x7fffffff : limit_of(p.causal, at, it.lk, it.prefix);
+      const float slope2 = BIAS && i >= 0 ? __ldg(p.slopes + it.kvh * p.group + head) * kLog2e : 0.0f;
+      for (int j = jb; j < je; ++j, ++t) {
+        // S(t) has finished, and with it every P V product of the group before it
+        if (!__all_sync(0xffffffffu, mbar_wait(bar(kBarSFull + w), t & 1, abort_flag, p.err))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (j == jb) {
+          if (!(ok = flush())) break;
+          m = -INFINITY;
+          l = 0.0f;
+        }
+        float sv[4][32];
+        uint32_t(&su)[4][32] = reinterpret_cast<uint32_t(&)[4][32]>(sv);
+        tmem_ld32(s_tm, su[0]);
+        tmem_ld32(s_tm + 32, su[1]);
+        tmem_ld32(s_tm + 64, su[2]);
+        tmem_ld32(s_tm + 96, su[3]);
+        tmem_ld_wait(su[0]);
+        reg_fence(su[1]);
+        reg_fence(su[2]);
+        reg_fence(su[3]);
+        if constexpr (CAP || BIAS) {  // scores in units of log 2
+          const float d0 = float(at - j * kTile);
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              float x = sv[c][e] * sl2;
+              if constexpr (CAP) {  // cap tanh(y) = cap - 2 cap / (2^(2 y log2 e) + 1)
+                const float u = ex2(x) + 1.0f;
+                float rc;
+                asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rc) : "f"(u));
+                x = fmaf(-2.0f * cap2, rc, cap2);
+              }
+              if constexpr (BIAS) x = fmaf(-slope2, fabsf(d0 - float(32 * c + e)), x);
+              sv[c][e] = x;
+            }
+        }
+        const int valid = lim - j * kTile;  // visible keys of this tile
+        if (valid < kTile) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (32 * c + e >= valid) sv[c][e] = -INFINITY;
+        }
+        float mq[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mq[k] = fmaxf(sv[k >> 1][(k & 1) * 16], sv[k >> 1][(k & 1) * 16 + 1]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+#pragma unroll
+          for (int e = 2; e < 16; e += 2)
+            mq[k] = fmax3(mq[k], sv[k >> 1][(k & 1) * 16 + e], sv[k >> 1][(k & 1) * 16 + e + 1]);
+        const float mx = fmaxf(fmaxf(fmax3(mq[0], mq[1], mq[2]), fmax3(mq[3], mq[4], mq[5])), fmaxf(mq[6], mq[7]));
+        constexpr bool kUnits = CAP || BIAS;
+        const float m_tile = kUnits ? mx : mx * sl2;
+        const bool raise = m_tile > m + kSlack;
+        const float m_new = raise ? m_tile - kHead : m;
+        if (j > jb && __any_sync(0xffffffffu, raise)) {
+          const float f = raise ? ex2(m - m_new) : 1.0f;
+          l *= f;
+#pragma unroll 1
+          for (int c = 0; c < Dn; c += 8) {
+            uint32_t e[8];
+            tmem_ld8(o_tm + uint32_t(c), e);
+            tmem_ld_wait();
+            asm volatile("" : "+r"(e[0]), "+r"(e[1]), "+r"(e[2]), "+r"(e[3]), "+r"(e[4]), "+r"(e[5]), "+r"(e[6]),
+                         "+r"(e[7]));
+#pragma unroll
+            for (int k = 0; k < 8; ++k) e[k] = __float_as_uint(__uint_as_float(e[k]) * f);
+            tmem_st8(o_tm + uint32_t(c), e);
+          }
+        }
+        m = m_new;
+        const float ref = m == -INFINITY ? 0.0f : m;
+        float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float* s = &sv[2 * c + (e >> 4)][2 * (e & 15)];
+            float x0, x1;
+            if constexpr (kUnits) add_x2(x0, x1, s[0], s[1], -ref, -ref);
+            else fma_x2(x0, x1, s[0], s[1], sl2, sl2, -ref, -ref);
+            x0 = ex2(x0);
+            x1 = ex2(x1);
+            if (e & 1) add_x2(s2, s3, s2, s3, x0, x1);
+            else add_x2(s0, s1, s0, s1, x0, x1);
+            const __half2 h = __floats2half2_rn(x0, x1);
+            pk[e] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+          tmem_st32(s_tm + 32 * c, pk);
+        }
+        l += (s0 + s1) + (s2 + s3);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(bar(kBarPFull + w));
+      }
+      if (!ok) break;
+      pending = n;
+      ++full;
+    }
+    if (ok) flush();
+    tmem_ld_wait();
+    tmem_st_wait();
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Tensor map of [rows, heads * D] with a row stride: boxes of 64 values x `box_heads` heads x
+// `box_rows` rows, 128-byte swizzle; values past a head's width and rows past the last read as 0.
+sv_status packed_map(CUtensorMap* m, const void* ptr, int D, int heads, int rows, long long stride, int box_heads,
+                     int box_rows) {
+  const uint64_t dims[3] = {uint64_t(D), uint64_t(heads), uint64_t(rows)};
+  const uint64_t strides[2] = {uint64_t(D) * 2u, uint64_t(stride) * 2u};
+  const uint32_t box[3] = {64u, uint32_t(box_heads), uint32_t(box_rows)};
+  return make_tmap(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, ptr, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <int NB, bool CAP, bool BIAS>
+sv_status packed_launch_as(const PackedParams& p, int grid, cudaStream_t s) {
+  auto kern = packed_tile_kernel<NB, CAP, BIAS>;
+  static unsigned long long attr_set = 0;  // the attribute is per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice(packed attention)");
+  const unsigned long long bit = (dev >= 0 && dev < kMaxAttrDevices) ? 1ull << dev : 0ull;
+  if (!(attr_set & bit) || !bit) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<NB>::kBytes);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(packed attention)");
+    attr_set |= bit;
+  }
+  CUtensorMap tq, tk, tv;
+  sv_status st = packed_map(&tq, p.q, p.D, p.hq, p.total_q, p.qs, p.group, p.qt);
+  // (without keys no item copies any; the maps then only need to be valid)
+  const bool keys = p.total_k > 0;
+  if (st == SV_OK) st = packed_map(&tk, keys ? p.k : p.q, p.D, p.hk, keys ? p.total_k : 1, p.ks, 1, kTile);
+  if (st == SV_OK) st = packed_map(&tv, keys ? p.v : p.q, p.D, p.hk, keys ? p.total_k : 1, p.vs, 1, kTile);
+  if (st != SV_OK) return st;
+  e = launch_pdl(kern, dim3(unsigned(grid)), dim3(kThreads), size_t(Smem<NB>::kBytes), s, p, tq, tk, tv);
+  return e == cudaSuccess ? SV_OK : cuda_fail(e, "packed attention launch");
+}
+
+template <int NB>
+sv_status packed_launch(const PackedParams& p, int grid, cudaStream_t s) {
+  if (p.cap > 0.0f) return p.slopes ? packed_launch_as<NB, true, true>(p, grid, s) : packed_launch_as<NB, true, false>(p, grid, s);
+  return p.slopes ? packed_launch_as<NB, false, true>(p, grid, s) : packed_launch_as<NB, false, false>(p, grid, s);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -131,8 +809,9 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 
 extern "C" {
 
 size_t sv_attention_packed_workspace(int docs, int total_q, int total_k, int q_heads, int kv_heads, int head_dim) {
-  (void)docs, (void)total_q, (void)total_k, (void)q_heads, (void)kv_heads, (void)head_dim;
-  return 16;
+  (void)docs, (void)total_q, (void)total_k, (void)q_heads, (void)kv_heads;  // bounded by the grid alone
+  const size_t d = size_t(head_dim < 8 ? 8 : (head_dim > 128 ? 128 : head_dim));
+  return sv::kCounterBytes + size_t(sv::kMaxSlots) * 2 * ((d + 15) / 16 * 16 + 2) * sv::kTile * sizeof(float);
 }
 
 sv_status sv_attention_packed(const void* q, const void* k, const void* v, void* o, const int* q_offsets,
@@ -216,15 +895,22 @@ sv_status sv_attention_packed(const void* q, const void* k, const void* v, void*
   p.out_e4m3 = out_dtype == SV_DT_E4M3;
   p.err = dev_err();
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const long long blocks = (static_cast<long long>(total_q) * q_heads + 3) / 4;
-  if (blocks > 0x7fffffffll) {
+  p.qt = kTile / p.group;
+  if (workspace) {
+    p.counters = static_cast<unsigned*>(workspace);
+    p.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + kCounterBytes);
+  }
+  // items at most: every document rounds its pairs of tiles up, and ranges are only divided
+  // while there are fewer items than two rounds of the grid
+  const long long pairs = total_q / (2 * p.qt) + docs;
+  if (pairs * kv_heads > (1ll << 30)) {
     set_error("%s: %d queries of %d heads are too many for one call", fn, total_q, q_heads);
     return SV_ERR_UNSUPPORTED;
   }
+  int grid = num_sms() < kMaxGrid ? num_sms() : kMaxGrid;
+  if (!workspace && pairs * kv_heads < grid) grid = int(pairs * kv_heads);
   LaunchScope L(kKindAttn, 0.0, 0.0, s);
-  packed_rows_kernel<<<unsigned(blocks), 128, 0, s>>>(p);
-  cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? SV_OK : cuda_fail(e, "packed attention launch");
+  return head_dim > 64 ? packed_launch<2>(p, grid, s) : packed_launch<1>(p, grid, s);
 }
 
 }  // extern "C"
