@@ -17,8 +17,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libsv.so")
 SOURCES = ["api.cu", "gemm_tc.cu", "attention.cu", "elementwise.cu", "map_static.cu", "rope.cu",
-           "packed_attention.cu"]
-HEADERS = ["ptx.cuh", "sv_internal.h"]
+           "packed_attention.cu", "packed_few.cu"]
+HEADERS = ["ptx.cuh", "sv_internal.h", "packed_attention.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -24,47 +24,23 @@
 // Key ranges are divided among CTAs when there are few items (Schedule); the parts' O, m and
 // l go to the caller's workspace and the last of them to arrive joins them in order.
 // Tensor memory: S_0, S_1, O_0, O_1 of 128 columns each.
-#include <cuda_fp8.h>
-
 #include <cmath>
 
-#include "ptx.cuh"
-#include "sv_internal.h"
+#include "packed_attention.h"
 
 namespace sv {
+namespace packed {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kTile = 128;                  // rows of a query tile, keys of a key tile
 constexpr int kBoxBytes = kTile * 128;      // 128 rows of 64 values: one box of an operand tile
 constexpr int kThreads = 320;
 constexpr int kBarBytes = 768;              // barriers, TMEM address slot, abort flag, items
 constexpr int kItems = 4;                   // work items between the copy warp and the others
 constexpr uint32_t kTmemCols = 512;
-constexpr int kMaxGrid = 152;               // CTAs of a launch at most (the workspace is sized by it)
-constexpr int kMaxSlots = 2 * kMaxGrid;     // partial results of a launch at most (see Schedule)
+constexpr int kMaxSlots = 2 * kMaxSms;      // partial results of a launch at most (see Schedule)
 constexpr int kMinSplit = 2;                // key tiles of a divided range at least
-constexpr size_t kCounterBytes = size_t(kMaxSlots) * 8 * sizeof(unsigned);
-
-// The reference exponent of a row is set kHead below a tile's maximum when that maximum is
-// more than kSlack above it: P <= 2^15 stays finite in F16, small probabilities stay above
-// its subnormal range for longer, and O is rescaled rarely.
-constexpr float kSlack = 15.0f, kHead = 8.0f;
-
-struct PackedParams {
-  const __half *q, *k, *v;
-  void* o;
-  const int *q_off, *k_off, *prefix;
-  const float* slopes;
-  int docs, total_q, total_k, hq, hk, group, D;
-  long long qs, ks, vs, os;
-  float scale, cap;
-  int causal, out_e4m3;
-  int qt;              // queries of a tile: 128 / group
-  unsigned* counters;  // workspace: arrivals of each divided tile and warp; null: nothing is divided
-  float* partial;      // workspace: partial results
-  int* err;
-};
+static_assert(kCounterBytes >= size_t(kMaxSlots) * 8 * sizeof(unsigned), "counters");
 
 template <int NB>
 struct Smem {
@@ -91,16 +67,6 @@ enum {
   kNumBars = 35
 };
 
-// Offset d of `docs` documents: the caller's, or equal lengths.
-__device__ __forceinline__ int offset_of(const int* off, int d, int docs, int total) {
-  return off ? __ldg(off + d) : (total / docs) * d;
-}
-
-// Visible keys of a query at position `at` (p_i) of a document with lk keys.
-__device__ __forceinline__ int limit_of(int causal, int at, int lk, int prefix) {
-  return causal ? min(lk, max(max(at + 1, prefix), 0)) : lk;
-}
-
 // One work item: up to 2 qt queries of a document with the query heads of one key head
 // (two tiles of rows, row r = query r / group, head r % group), over key tiles jb .. je - 1.
 struct Item {
@@ -123,7 +89,7 @@ static_assert(kOffItems + kItems * sizeof(Item) <= kBarBytes, "barrier area");
 // range of n > chunk tiles has ceil(n / chunk) <= 2 n / chunk parts.
 class Schedule {
  public:
-  __device__ __forceinline__ Schedule(const PackedParams& p, int lane) : p_(p), lane_(lane), docs_(p.docs) {
+  __device__ __forceinline__ Schedule(const Params& p, int lane) : p_(p), lane_(lane), docs_(p.docs) {
     long long work = 0;
     bool bad = false;
     for (int d0 = 0; d0 < p.docs; d0 += 32) {
@@ -163,12 +129,12 @@ class Schedule {
     k /= splits;
     r.kvh = k / pairs;
     const int pair = pairs - 1 - (k - r.kvh * pairs);
-    const int lq = of(lq_);
-    r.lk = of(lk_);
-    r.k0 = of(k0_);
-    r.prefix = of(prefix_);
+    const int lq = of(doc_.lq);
+    r.lk = of(doc_.lk);
+    r.k0 = of(doc_.k0);
+    r.prefix = of(doc_.prefix);
     const int i0 = pair * 2 * p_.qt;
-    r.q0 = of(q0_) + i0;
+    r.q0 = of(doc_.q0) + i0;
     r.nq = min(lq - i0, 2 * p_.qt);
     r.at = i0 + r.lk - lq;
     const int n = (limit_of(p_.causal, r.at + r.nq - 1, r.lk, r.prefix) + kTile - 1) / kTile;
@@ -180,20 +146,9 @@ class Schedule {
 
  private:
   __device__ __forceinline__ void load(int d0) {
-    const int d = d0 + lane_;
-    lq_ = lk_ = q0_ = k0_ = prefix_ = 0;
-    bad_ = false;
-    if (d < docs_) {
-      q0_ = offset_of(p_.q_off, d, p_.docs, p_.total_q);
-      k0_ = offset_of(p_.k_off, d, p_.docs, p_.total_k);
-      lq_ = offset_of(p_.q_off, d + 1, p_.docs, p_.total_q) - q0_;
-      lk_ = offset_of(p_.k_off, d + 1, p_.docs, p_.total_k) - k0_;
-      bad_ = q0_ < 0 || lq_ < 0 || q0_ + static_cast<long long>(lq_) > p_.total_q || k0_ < 0 || lk_ < 0 ||
-             k0_ + static_cast<long long>(lk_) > p_.total_k;
-      prefix_ = p_.prefix ? __ldg(p_.prefix + d) : 0;
-    }
-    pairs_ = (lq_ + 2 * p_.qt - 1) / (2 * p_.qt);
-    tiles_ = (limit_of(p_.causal, lk_ - 1, lk_, prefix_) + kTile - 1) / kTile;  // of the last query
+    bad_ = !document(p_, d0 + lane_, docs_, doc_);
+    pairs_ = (doc_.lq + 2 * p_.qt - 1) / (2 * p_.qt);
+    tiles_ = (limit_of(p_.causal, doc_.lk - 1, doc_.lk, doc_.prefix) + kTile - 1) / kTile;  // of the last query
   }
   __device__ __forceinline__ void open(int d0) {
     d0_ = d0;
@@ -208,61 +163,19 @@ class Schedule {
     total_ = __shfl_sync(0xffffffffu, incl_, 31);
     slot_total_ = __shfl_sync(0xffffffffu, slot_incl_, 31);
   }
-  const PackedParams& p_;
+  const Params& p_;
   int lane_, docs_, chunk_;
   bool bad_;
   int d0_ = 0, base_ = 0, total_ = 0, slot_base_ = 0, slot_total_ = 0;
-  int lq_, lk_, q0_, k0_, prefix_, pairs_, tiles_, splits_, count_, incl_, slot_incl_;  // this lane's document
+  Document doc_;  // this lane's
+  int pairs_, tiles_, splits_, count_, incl_, slot_incl_;
 };
-
-__device__ __forceinline__ void store8(const PackedParams& p, size_t at, const float* y) {
-  if (p.out_e4m3) {
-    uint2 w;
-    __nv_fp8x2_storage_t* h = reinterpret_cast<__nv_fp8x2_storage_t*>(&w);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      h[i] = __nv_cvt_float2_to_fp8x2(make_float2(16.0f * y[2 * i], 16.0f * y[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
-    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.o) + at) = w;
-  } else {
-    uint4 w;
-    __half2* h = reinterpret_cast<__half2*>(&w);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(y[2 * i], y[2 * i + 1]);
-    *reinterpret_cast<uint4*>(static_cast<__half*>(p.o) + at) = w;
-  }
-}
-
-// A row whose tensor-core result is not finite, again from the visible keys alone: a tile's
-// product multiplies the probability 0 of a hidden key with its value, which is NaN for an
-// infinite or NaN value. Keys kb .. ke - 1 of the document; the row's sums go to `out`
-// (head_dim columns apart by `step` floats), its exponent and denominator to m and l.
-__device__ __noinline__ void row_again(const PackedParams& p, const __half* q, const __half* k, const __half* v, int kb,
-                                       int ke, int at, float slope, float* acc, float& m_out, float& l_out) {
-  float m = -INFINITY, l = 0.0f;
-  for (int c = 0; c < p.D; ++c) acc[c] = 0.0f;
-  for (int j = kb; j < ke; ++j) {
-    const __half *kr = k + j * p.ks, *vr = v + j * p.vs;
-    float s = 0.0f;
-    for (int c = 0; c < p.D; ++c) s = fmaf(__half2float(q[c]), __half2float(kr[c]), s);
-    s *= p.scale;
-    if (p.cap > 0.0f) s = p.cap * tanhf(s / p.cap);
-    s = (s - slope * fabsf(float(at - j))) * kLog2e;
-    const float mn = (s > m || s != s) ? s : m;  // NaN stays
-    const float ref = mn == -INFINITY ? 0.0f : mn;
-    const float f = m == mn ? 1.0f : exp2f(m - ref), e = exp2f(s - ref);
-    l = l * f + e;
-    for (int c = 0; c < p.D; ++c) acc[c] = fmaf(e, __half2float(vr[c]), acc[c] * f);
-    m = mn;
-  }
-  m_out = m;
-  l_out = l;
-}
 
 template <int NB, bool CAP, bool BIAS>
 // 10 warps: three share each of two SM sub-partitions, so a thread may hold at most
 // 16384 / (3 x 32) registers, rounded down to the allocation granule.
 __global__ void __maxnreg__(168)
-    packed_tile_kernel(const __grid_constant__ PackedParams p, const __grid_constant__ CUtensorMap tq,
+    packed_tile_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap tq,
                        const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv) {
   using L = Smem<NB>;
   constexpr int kOp = L::kOp, kStages = L::kStages, kQBufs = L::kQBufs;
@@ -674,12 +587,7 @@ __global__ void __maxnreg__(168)
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
               float x = sv[c][e] * sl2;
-              if constexpr (CAP) {  // cap tanh(y) = cap - 2 cap / (2^(2 y log2 e) + 1)
-                const float u = ex2(x) + 1.0f;
-                float rc;
-                asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rc) : "f"(u));
-                x = fmaf(-2.0f * cap2, rc, cap2);
-              }
+              if constexpr (CAP) x = capped(x, cap2);
               if constexpr (BIAS) x = fmaf(-slope2, fabsf(d0 - float(32 * c + e)), x);
               sv[c][e] = x;
             }
@@ -772,7 +680,7 @@ sv_status packed_map(CUtensorMap* m, const void* ptr, int D, int heads, int rows
 }
 
 template <int NB, bool CAP, bool BIAS>
-sv_status packed_launch_as(const PackedParams& p, int grid, cudaStream_t s) {
+sv_status packed_launch_as(const Params& p, int grid, cudaStream_t s) {
   auto kern = packed_tile_kernel<NB, CAP, BIAS>;
   static unsigned long long attr_set = 0;  // the attribute is per device
   int dev = 0;
@@ -796,7 +704,7 @@ sv_status packed_launch_as(const PackedParams& p, int grid, cudaStream_t s) {
 }
 
 template <int NB>
-sv_status packed_launch(const PackedParams& p, int grid, cudaStream_t s) {
+sv_status packed_launch(const Params& p, int grid, cudaStream_t s) {
   if (p.cap > 0.0f) return p.slopes ? packed_launch_as<NB, true, true>(p, grid, s) : packed_launch_as<NB, true, false>(p, grid, s);
   return p.slopes ? packed_launch_as<NB, false, true>(p, grid, s) : packed_launch_as<NB, false, false>(p, grid, s);
 }
@@ -804,6 +712,16 @@ sv_status packed_launch(const PackedParams& p, int grid, cudaStream_t s) {
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 }  // namespace
+
+sv_status tile_launch(const Params& p, cudaStream_t s) {
+  // items at most: every document rounds its pairs of tiles up
+  const long long items = (p.total_q / (2 * p.qt) + p.docs) * static_cast<long long>(p.hk);
+  int grid = num_sms() < kMaxSms ? num_sms() : kMaxSms;
+  if (!p.counters && items < grid) grid = int(items);
+  return p.D > 64 ? packed_launch<2>(p, grid, s) : packed_launch<1>(p, grid, s);
+}
+
+}  // namespace packed
 }  // namespace sv
 
 extern "C" {
@@ -811,7 +729,10 @@ extern "C" {
 size_t sv_attention_packed_workspace(int docs, int total_q, int total_k, int q_heads, int kv_heads, int head_dim) {
   (void)docs, (void)total_q, (void)total_k, (void)q_heads, (void)kv_heads;  // bounded by the grid alone
   const size_t d = size_t(head_dim < 8 ? 8 : (head_dim > 128 ? 128 : head_dim));
-  return sv::kCounterBytes + size_t(sv::kMaxSlots) * 2 * ((d + 15) / 16 * 16 + 2) * sv::kTile * sizeof(float);
+  const size_t tiles = sv::packed::kCounterBytes +
+                       size_t(sv::packed::kMaxSlots) * 2 * ((d + 15) / 16 * 16 + 2) * sv::packed::kTile * sizeof(float);
+  const size_t few = sv::packed::few_workspace(int(d));
+  return tiles > few ? tiles : few;
 }
 
 sv_status sv_attention_packed(const void* q, const void* k, const void* v, void* o, const int* q_offsets,
@@ -820,6 +741,7 @@ sv_status sv_attention_packed(const void* q, const void* k, const void* v, void*
                               long long o_stride, const sv_attention_options* options, int out_dtype, void* workspace,
                               size_t workspace_bytes, void* stream) {
   using namespace sv;
+  using namespace sv::packed;
   const char* fn = "sv_attention_packed";
   if (docs < 1 || total_q < 0 || total_k < 0 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads ||
       (out_dtype != SV_DT_F16 && out_dtype != SV_DT_E4M3)) {
@@ -869,7 +791,7 @@ sv_status sv_attention_packed(const void* q, const void* k, const void* v, void*
   if (total_q == 0) return SV_OK;
   sv_status st = ensure_runtime();
   if (st != SV_OK) return st;
-  PackedParams p = {};
+  Params p = {};
   p.q = static_cast<const __half*>(q);
   p.k = static_cast<const __half*>(k);
   p.v = static_cast<const __half*>(v);
@@ -900,17 +822,13 @@ sv_status sv_attention_packed(const void* q, const void* k, const void* v, void*
     p.counters = static_cast<unsigned*>(workspace);
     p.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + kCounterBytes);
   }
-  // items at most: every document rounds its pairs of tiles up, and ranges are only divided
-  // while there are fewer items than two rounds of the grid
-  const long long pairs = total_q / (2 * p.qt) + docs;
-  if (pairs * kv_heads > (1ll << 30)) {
-    set_error("%s: %d queries of %d heads are too many for one call", fn, total_q, q_heads);
+  if (docs > (1 << 24) || (total_q / (2 * p.qt) + static_cast<long long>(docs)) * kv_heads > (1ll << 30)) {
+    set_error("%s: %d documents of %d queries with %d heads are too many for one call", fn, docs, total_q, q_heads);
     return SV_ERR_UNSUPPORTED;
   }
-  int grid = num_sms() < kMaxGrid ? num_sms() : kMaxGrid;
-  if (!workspace && pairs * kv_heads < grid) grid = int(pairs * kv_heads);
   LaunchScope L(kKindAttn, 0.0, 0.0, s);
-  return head_dim > 64 ? packed_launch<2>(p, grid, s) : packed_launch<1>(p, grid, s);
+  // few rows per document on average: bound by reading the keys and values, not by products
+  return static_cast<long long>(total_q) * p.group <= 16ll * docs ? few_launch(p, s) : tile_launch(p, s);
 }
 
 }  // extern "C"

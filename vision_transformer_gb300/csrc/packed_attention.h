@@ -1,0 +1,125 @@
+// What the two kernels of sv_attention_packed share (packed_attention.cu: tiles of 128 rows
+// on the tensor cores; packed_few.cu: a few rows per document).
+#pragma once
+#include <cuda_fp8.h>
+
+#include "ptx.cuh"
+#include "sv_internal.h"
+
+namespace sv {
+namespace packed {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kMaxSms = 152;  // SMs that a launch uses at most (the workspace is sized by it)
+// Workspace: counters of arrivals first (zero before and after every call), then partial results.
+constexpr size_t kCounterBytes = size_t(2 * kMaxSms) * 8 * sizeof(unsigned);
+
+// The reference exponent of a row is set kHead below a tile's maximum when that maximum is
+// more than kSlack above it: P <= 2^15 stays finite in F16, small probabilities stay above
+// its subnormal range for longer, and O is rescaled rarely.
+constexpr float kSlack = 15.0f, kHead = 8.0f;
+
+struct Params {
+  const __half *q, *k, *v;
+  void* o;
+  const int *q_off, *k_off, *prefix;
+  const float* slopes;
+  int docs, total_q, total_k, hq, hk, group, D;
+  long long qs, ks, vs, os;
+  float scale, cap;
+  int causal, out_e4m3;
+  int qt;              // queries of a 128-row tile: 128 / group
+  unsigned* counters;  // workspace: arrivals; null: no key range is divided
+  float* partial;      // workspace: partial results
+  int* err;
+};
+
+// packed_few.cu
+sv_status few_launch(const Params& p, cudaStream_t s);
+size_t few_workspace(int head_dim);
+
+// Offset d of `docs` documents: the caller's, or equal lengths.
+__device__ __forceinline__ int offset_of(const int* off, int d, int docs, int total) {
+  return off ? __ldg(off + d) : (total / docs) * d;
+}
+
+// Visible keys of a query at position `at` (p_i) of a document with lk keys.
+__device__ __forceinline__ int limit_of(int causal, int at, int lk, int prefix) {
+  return causal ? min(lk, max(max(at + 1, prefix), 0)) : lk;
+}
+
+// Queries q0 .. q0 + lq - 1 and keys k0 .. k0 + lk - 1 of a document.
+struct Document {
+  int q0, lq, k0, lk, prefix;
+};
+// Document d (no queries and keys from `docs` on); false if its offsets decrease or leave [0, total].
+__device__ __forceinline__ bool document(const Params& p, int d, int docs, Document& r) {
+  r = {0, 0, 0, 0, 0};
+  if (d >= docs) return true;
+  r.q0 = offset_of(p.q_off, d, p.docs, p.total_q);
+  r.k0 = offset_of(p.k_off, d, p.docs, p.total_k);
+  const int q1 = offset_of(p.q_off, d + 1, p.docs, p.total_q), k1 = offset_of(p.k_off, d + 1, p.docs, p.total_k);
+  r.prefix = p.prefix ? __ldg(p.prefix + d) : 0;
+  if (r.q0 < 0 || q1 < r.q0 || q1 > p.total_q || r.k0 < 0 || k1 < r.k0 || k1 > p.total_k) return false;
+  r.lq = q1 - r.q0;
+  r.lk = k1 - r.k0;
+  return true;
+}
+
+// cap tanh(s / cap) = cap - 2 cap / (2^(2 s log2 e / cap) + 1): x = 2 s log2 e / cap, c = cap
+// (in any unit); exact limits for infinite s. The error, about 2^-22 cap, is that of the
+// reciprocal of a number >= 1.
+__device__ __forceinline__ float capped(float x, float c) {
+  const float u = ex2(x) + 1.0f;
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(u));
+  return fmaf(-2.0f * c, r, c);
+}
+
+// Eight values of an output row.
+__device__ __forceinline__ void store8(const Params& p, size_t at, const float* y) {
+  if (p.out_e4m3) {
+    uint2 w;
+    __nv_fp8x2_storage_t* h = reinterpret_cast<__nv_fp8x2_storage_t*>(&w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      h[i] = __nv_cvt_float2_to_fp8x2(make_float2(16.0f * y[2 * i], 16.0f * y[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.o) + at) = w;
+  } else {
+    uint4 w;
+    __half2* h = reinterpret_cast<__half2*>(&w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(y[2 * i], y[2 * i + 1]);
+    *reinterpret_cast<uint4*>(static_cast<__half*>(p.o) + at) = w;
+  }
+}
+
+// A row whose tensor-core result is not finite, again from the visible keys alone: a tile's
+// product multiplies the probability 0 of a hidden key with its value, which is NaN for an
+// infinite or NaN value. Keys kb .. ke - 1 of the document, query position `at`; unscaled
+// sums to acc[D], their exponent and denominator to m and l.
+static __device__ __noinline__ void row_again(const Params& p, const __half* q, const __half* k, const __half* v,
+                                              int kb, int ke, int at, float slope, float* acc, float& m_out,
+                                              float& l_out) {
+  float m = -INFINITY, l = 0.0f;
+  for (int c = 0; c < p.D; ++c) acc[c] = 0.0f;
+  for (int j = kb; j < ke; ++j) {
+    const __half *kr = k + j * p.ks, *vr = v + j * p.vs;
+    float s = 0.0f;
+    for (int c = 0; c < p.D; ++c) s = fmaf(__half2float(q[c]), __half2float(kr[c]), s);
+    s *= p.scale;
+    if (p.cap > 0.0f) s = p.cap * tanhf(s / p.cap);
+    s = (s - slope * fabsf(float(at - j))) * kLog2e;
+    const float mn = (s > m || s != s) ? s : m;  // NaN stays
+    const float ref = mn == -INFINITY ? 0.0f : mn;
+    const float f = m == mn ? 1.0f : exp2f(m - ref), e = exp2f(s - ref);
+    l = l * f + e;
+    for (int c = 0; c < p.D; ++c) acc[c] = fmaf(e, __half2float(vr[c]), acc[c] * f);
+    m = mn;
+  }
+  m_out = m;
+  l_out = l;
+}
+
+}  // namespace packed
+}  // namespace sv

@@ -1,0 +1,480 @@
+// sv_attention_packed for a few rows (queries x heads of a key head) per document: one new
+// token of many requests over long caches, pooling probes over many images.
+//
+// Bound: DRAM, every key and value read once for (up to) 8 or 16 rows. The arithmetic runs on
+// warp-level matrix instructions (mma.sync m16n8k16, F32 accumulation) because the rows fill
+// no tcgen05 tile and keys and values can then go from global memory straight to the
+// registers of the instruction, with nothing to wait for but the loads themselves:
+//   S^T = K Q^T: 16 keys x 8 rows. The order of the summed dimensions is free as long as K
+//     and Q agree, so a lane's 16 contiguous bytes of a key row (8 dimensions) serve as its
+//     operand values of two instructions; four lanes read 64 contiguous bytes of a key.
+//   O^T += V^T P^T: 16 dimensions x 8 rows. The order of O's dimensions is free as well: eight
+//     lanes read 128 contiguous bytes of a value row, a lane holds the same 8 dimensions of the
+//     keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9, and byte permutes pair the keys. P^T goes from the
+//     accumulator's layout to the operand's by a transposing 8 x 8 move.
+// A warp takes 16 keys at a time (its registers of K are reloaded as soon as S^T is done, those
+// of V as soon as O^T is), the four warps of a CTA take turns, three CTAs run per SM.
+//
+// Work: the (document, key head, block of rows) items are laid out one behind another in steps
+// of 64 keys, and every CTA takes an equal, contiguous share of the steps, so that any
+// distribution of lengths fills the GPU. An item inside one share is finished there; one that
+// is cut goes in parts to the workspace, and the last CTA of its parts joins them in order. A
+// CTA has at most two such parts, at the start and at the end of its share.
+#include "packed_attention.h"
+
+namespace sv {
+namespace packed {
+namespace {
+
+constexpr int kFewThreads = 128;
+constexpr int kStepKeys = 64;       // keys of a step: 16 for each of 4 warps
+constexpr int kCtasPerSm = 3;
+constexpr int kMaxFewGrid = kMaxSms * kCtasPerSm;
+
+__device__ __forceinline__ uint4 load16(const __half* p) {
+  uint4 r;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p));
+  return r;
+}
+
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+// A run of steps of one item that falls into this CTA's share.
+struct Segment {
+  Document doc;
+  int kvh, row0;          // key head, first of the item's rows (query x group + head) in the document
+  int s0, s1, steps;      // steps of the item: this segment's, all
+  long long base;         // place of the item's first step among all steps
+};
+
+// The items in order: documents, key heads, blocks of rows. 32 documents at a time, one per
+// lane, with their steps summed by shuffles; every warp works it out for itself.
+template <int ROWS>
+class Share {
+ public:
+  __device__ __forceinline__ Share(const Params& p, int lane) : p_(p), lane_(lane), docs_(p.docs) {
+    long long work = 0;
+    bool bad = false;
+    for (int d0 = 0; d0 < p.docs; d0 += 32) {
+      bad |= !load(d0);
+      work += mine();
+    }
+    for (int o = 16; o; o >>= 1) work += __shfl_xor_sync(0xffffffffu, work, o);
+    // offsets that decrease or leave [0, total]: reported, and nothing is computed
+    if (__any_sync(0xffffffffu, bad)) {
+      if (lane == 0) atomicOr(p.err, kDevErrOffsets);
+      docs_ = 0;
+      work = 0;
+    }
+    chunk_ = (work + gridDim.x - 1) / gridDim.x;
+    if (chunk_ < 1) chunk_ = 1;
+    at_ = chunk_ * blockIdx.x;
+    end_ = min(at_ + chunk_, work);
+    if (p.docs > 32 || docs_ == 0) load(0);
+    open(0);
+  }
+  // The next segment of this CTA's share. Without a workspace nothing is cut: a CTA takes the
+  // items that begin in its share, whole.
+  __device__ __forceinline__ bool get(Segment& r) {
+    while (at_ < end_) {
+      while (at_ >= base_ + total_) {
+        base_ += total_;
+        load(d0_ + 32);
+        open(d0_ + 32);
+      }
+      const int src = __ffs(__ballot_sync(0xffffffffu, base_ + incl_ > at_)) - 1;
+      r.doc.q0 = of(doc_.q0, src);
+      r.doc.lq = of(doc_.lq, src);
+      r.doc.k0 = of(doc_.k0, src);
+      r.doc.lk = of(doc_.lk, src);
+      r.doc.prefix = of(doc_.prefix, src);
+      r.steps = of(steps_, src);
+      const int blocks = of(blocks_, src);
+      const long long first = base_ + __shfl_sync(0xffffffffu, incl_ - mine(), src);
+      const long long item = (at_ - first) / r.steps;
+      r.base = first + item * r.steps;
+      r.kvh = int(item / blocks);
+      r.row0 = int(item - static_cast<long long>(r.kvh) * blocks) * ROWS;
+      r.s0 = int(at_ - r.base);
+      r.s1 = int(min(end_ - r.base, static_cast<long long>(r.steps)));
+      if (!p_.counters) {
+        r.s1 = r.steps;
+        if (r.s0 > 0) {  // begun by the CTA before
+          at_ = r.base + r.steps;
+          continue;
+        }
+      }
+      at_ = r.base + r.s1;
+      return true;
+    }
+    return false;
+  }
+  __device__ __forceinline__ int cta_of(long long step) const { return int(step / chunk_); }
+
+ private:
+  __device__ __forceinline__ static int of(int v, int src) { return __shfl_sync(0xffffffffu, v, src); }
+  __device__ __forceinline__ long long mine() const {
+    return static_cast<long long>(blocks_) * p_.hk * steps_;
+  }
+  __device__ __forceinline__ bool load(int d0) {
+    d0_ = d0;
+    const bool good = document(p_, d0 + lane_, docs_, doc_);
+    blocks_ = int((static_cast<long long>(doc_.lq) * p_.group + ROWS - 1) / ROWS);
+    steps_ = max(1, (doc_.lk + kStepKeys - 1) / kStepKeys);  // (a step without keys writes the zeros)
+    return good;
+  }
+  __device__ __forceinline__ void open(int d0) {
+    incl_ = mine();
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long a = __shfl_up_sync(0xffffffffu, incl_, o);
+      if (lane_ >= o) incl_ += a;
+    }
+    total_ = __shfl_sync(0xffffffffu, incl_, 31);
+  }
+  const Params& p_;
+  int lane_, docs_, d0_ = 0, blocks_, steps_;
+  Document doc_;
+  long long chunk_, at_, end_, base_ = 0, total_ = 0, incl_;
+};
+
+// KI: 32-dimension groups of a key row, VI: 64-dimension groups of a value row, NT: 8-row
+// tiles of an item.
+template <int KI, int VI, int NT>
+__global__ void __launch_bounds__(kFewThreads, NT == 1 ? kCtasPerSm : 2) few_kernel(const __grid_constant__ Params p) {
+  constexpr int kRows = 8 * NT;
+  constexpr int kOut = 64 * VI + 4;  // row pitch of the merge buffer (floats)
+  __shared__ float red[4][kRows][kOut];
+  __shared__ float red_m[4][kRows], red_l[4][kRows];
+  __shared__ int row_bad[kRows];
+  __shared__ unsigned seen;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  pdl_launch_dependents();
+  pdl_wait();
+  Share<kRows> share(p, lane);
+  const int chunks = p.D / 8;  // 16-byte chunks of a row
+  const float sl2 = p.cap > 0.0f ? 2.0f * kLog2e * p.scale / p.cap : kLog2e * p.scale;
+
+  Segment sg;
+  while (share.get(sg)) {
+    const int rows_all = sg.doc.lq * p.group;  // of the document (for this key head)
+    const int lk = sg.doc.lk;
+    const __half* kb = p.k + sg.doc.k0 * p.ks + sg.kvh * p.D;
+    const __half* vb = p.v + sg.doc.k0 * p.vs + sg.kvh * p.D;
+    const int last = min(lk, sg.s1 * kStepKeys);  // keys of this segment end here
+
+    // this lane's two rows of each tile as columns of S^T: visible keys, position, slope
+    int lim[NT][2];
+    float at[NT][2], slope[NT][2];
+    uint32_t q[NT][KI][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = sg.row0 + 8 * n + 2 * t + e;
+        const int i = r / p.group, pos = i + lk - sg.doc.lq;
+        lim[n][e] = r < rows_all ? limit_of(p.causal, pos, lk, sg.doc.prefix) : lk;
+        at[n][e] = float(pos);
+        slope[n][e] = p.slopes && r < rows_all ? __ldg(p.slopes + sg.kvh * p.group + (r - i * p.group)) * kLog2e : 0.0f;
+      }
+      const int r = sg.row0 + 8 * n + g;  // Q^T: this lane's column
+      const int i = r / p.group;
+      const __half* qr = p.q + static_cast<long long>(sg.doc.q0 + i) * p.qs + (sg.kvh * p.group + r - i * p.group) * p.D;
+#pragma unroll
+      for (int c = 0; c < KI; ++c) {
+        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+        if (r < rows_all && 4 * c + t < chunks) x = load16(qr + 8 * (4 * c + t));
+        q[n][c][0] = x.x, q[n][c][1] = x.y, q[n][c][2] = x.z, q[n][c][3] = x.w;
+      }
+    }
+
+    uint4 kx[2][KI], vx[4][VI];
+    auto load_k = [&](int key0) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int key = key0 + g + 8 * h;
+        const __half* row = kb + key * p.ks;
+#pragma unroll
+        for (int c = 0; c < KI; ++c)
+          kx[h][c] = key < last && 4 * c + t < chunks ? load16(row + 8 * (4 * c + t)) : make_uint4(0u, 0u, 0u, 0u);
+      }
+    };
+    auto load_v = [&](int key0) {
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        const int key = key0 + 2 * t + (h & 1) + 8 * (h >> 1);
+        const __half* row = vb + key * p.vs;
+#pragma unroll
+        for (int c = 0; c < VI; ++c)
+          vx[h][c] = key < last && 8 * c + g < chunks ? load16(row + 8 * (8 * c + g)) : make_uint4(0u, 0u, 0u, 0u);
+      }
+    };
+    float o[NT][4 * VI][4];
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int j = 0; j < 4 * VI; ++j) o[n][j][0] = o[n][j][1] = o[n][j][2] = o[n][j][3] = 0.0f;
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.0f;
+    }
+
+    int key0 = sg.s0 * kStepKeys + 16 * warp;
+    load_k(key0);
+    load_v(key0);
+    for (; key0 < last; key0 += kStepKeys) {
+      uint32_t b[NT][2];
+      float s[NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
+#pragma unroll
+        for (int c = 0; c < KI; ++c) {
+          mma16816(s[n], kx[0][c].x, kx[1][c].x, kx[0][c].y, kx[1][c].y, q[n][c][0], q[n][c][1]);
+          mma16816(s[n], kx[0][c].z, kx[1][c].z, kx[0][c].w, kx[1][c].w, q[n][c][2], q[n][c][3]);
+        }
+      }
+      load_k(key0 + kStepKeys);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float x[4];
+        float f[2];
+        bool raise = false;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {  // e & 1: the row, e >> 1: keys g, g + 8
+          const int key = key0 + g + 8 * (e >> 1);
+          float y = s[n][e] * sl2;
+          if (p.cap > 0.0f) y = capped(y, p.cap * kLog2e);
+          if (p.slopes) y = fmaf(-slope[n][e & 1], fabsf(at[n][e & 1] - float(key)), y);
+          x[e] = key < min(lim[n][e & 1], last) ? y : -INFINITY;
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float mx = fmaxf(x[e], x[e + 2]);
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+          const bool up = mx > m[n][e] + kSlack;
+          const float mn = up ? mx - kHead : m[n][e];
+          f[e] = up ? ex2(m[n][e] - mn) : 1.0f;
+          m[n][e] = mn;
+          raise |= up;
+        }
+        if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+          for (int j = 0; j < 4 * VI; ++j) {
+            o[n][j][0] *= f[0];
+            o[n][j][1] *= f[1];
+            o[n][j][2] *= f[0];
+            o[n][j][3] *= f[1];
+          }
+          l[n][0] *= f[0];
+          l[n][1] *= f[1];
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float ref = m[n][e] == -INFINITY ? 0.0f : m[n][e];
+          x[e] = ex2(x[e] - ref);
+          x[e + 2] = ex2(x[e + 2] - ref);
+          l[n][e] += x[e] + x[e + 2];
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const __half2 w = __floats2half2_rn(x[2 * h], x[2 * h + 1]);
+          b[n][h] = transpose8x8(*reinterpret_cast<const uint32_t*>(&w));
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < VI; ++c) {
+        const uint32_t* v0 = reinterpret_cast<const uint32_t*>(&vx[0][c]);
+        const uint32_t* v1 = reinterpret_cast<const uint32_t*>(&vx[1][c]);
+        const uint32_t* v2 = reinterpret_cast<const uint32_t*>(&vx[2][c]);
+        const uint32_t* v3 = reinterpret_cast<const uint32_t*>(&vx[3][c]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {  // dimensions 2 j and 2 j + 1 of this lane's eight
+          const uint32_t a0 = __byte_perm(v0[j], v1[j], 0x5410), a1 = __byte_perm(v0[j], v1[j], 0x7632);
+          const uint32_t a2 = __byte_perm(v2[j], v3[j], 0x5410), a3 = __byte_perm(v2[j], v3[j], 0x7632);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma16816(o[n][4 * c + j], a0, a1, a2, a3, b[n][0], b[n][1]);
+        }
+      }
+      load_v(key0 + kStepKeys);
+    }
+
+    // the four warps' sums, brought to one exponent
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float x = l[n][e];
+        x += __shfl_xor_sync(0xffffffffu, x, 4);
+        x += __shfl_xor_sync(0xffffffffu, x, 8);
+        x += __shfl_xor_sync(0xffffffffu, x, 16);
+        if (g == 0) {
+          red_m[warp][8 * n + 2 * t + e] = m[n][e];
+          red_l[warp][8 * n + 2 * t + e] = x;
+        }
+      }
+    if (threadIdx.x < kRows) row_bad[threadIdx.x] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float f[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = 8 * n + 2 * t + e;
+        const float mx = fmaxf(fmaxf(red_m[0][r], red_m[1][r]), fmaxf(red_m[2][r], red_m[3][r]));
+        f[e] = ex2(m[n][e] - (mx == -INFINITY ? 0.0f : mx));
+      }
+#pragma unroll
+      for (int j = 0; j < 4 * VI; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)  // e & 1: the row, e >> 1: the dimension
+          red[warp][8 * n + 2 * t + (e & 1)][64 * (j >> 2) + 8 * g + 2 * (j & 3) + (e >> 1)] = o[n][j][e] * f[e & 1];
+    }
+    __syncthreads();
+    const bool whole = sg.s0 == 0 && sg.s1 == sg.steps;
+    const int rows = min(kRows, rows_all - sg.row0);
+    // a part's place: at the start of this CTA's share (0) or at its end (1)
+    auto part = [&](int cta, int end) {
+      return p.partial + (size_t(cta) * 2 + end) * size_t(kRows) * size_t(p.D + 2);
+    };
+    float* mine = whole ? nullptr : part(int(blockIdx.x), sg.s0 == 0 ? 1 : 0);
+    auto row_of = [&](int r, int& i, int& head) {
+      i = (sg.row0 + r) / p.group;
+      head = sg.kvh * p.group + (sg.row0 + r - i * p.group);
+    };
+    auto sums = [&](int r, float& mx, float& sum) {
+      mx = fmaxf(fmaxf(red_m[0][r], red_m[1][r]), fmaxf(red_m[2][r], red_m[3][r]));
+      const float ref = mx == -INFINITY ? 0.0f : mx;
+      sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) sum += ex2(red_m[w][r] - ref) * red_l[w][r];
+    };
+    for (int x = int(threadIdx.x); x < rows * chunks; x += kFewThreads) {
+      const int r = x / chunks, c = 8 * (x - r * chunks);
+      int i, head;
+      row_of(r, i, head);
+      float mx, sum;
+      sums(r, mx, sum);
+      const bool none = limit_of(p.causal, i + lk - sg.doc.lq, lk, sg.doc.prefix) == 0;
+      const float inv = whole ? 1.0f / sum : 1.0f;
+      float y[8], bad = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        y[e] = ((red[0][r][c + e] + red[1][r][c + e]) + (red[2][r][c + e] + red[3][r][c + e])) * inv;
+        if (none) y[e] = 0.0f;
+        bad = fmaf(y[e], 0.0f, bad);
+      }
+      if (bad != 0.0f) row_bad[r] = 1;
+      if (whole) {
+        store8(p, size_t(sg.doc.q0 + i) * size_t(p.os) + size_t(head) * size_t(p.D) + size_t(c), y);
+      } else {
+        float* at_p = mine + size_t(r) * size_t(p.D + 2);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) __stcg(at_p + c + e, y[e]);
+        if (c == 0) {
+          __stcg(at_p + p.D, mx);
+          __stcg(at_p + p.D + 1, sum);
+        }
+      }
+    }
+    __syncthreads();
+    if (int(threadIdx.x) < rows && row_bad[threadIdx.x]) {
+      const int r = int(threadIdx.x);
+      int i, head;
+      row_of(r, i, head);
+      const int pos = i + lk - sg.doc.lq;
+      float acc[128], mx, sum;
+      row_again(p, p.q + static_cast<long long>(sg.doc.q0 + i) * p.qs + head * p.D, kb, vb, sg.s0 * kStepKeys,
+                min(last, limit_of(p.causal, pos, lk, sg.doc.prefix)), pos, p.slopes ? __ldg(p.slopes + head) : 0.0f, acc,
+                mx, sum);
+      for (int c = 0; c < p.D; c += 8) {
+        float y[8];
+        for (int e = 0; e < 8; ++e) y[e] = whole ? acc[c + e] / sum : acc[c + e];
+        if (whole) store8(p, size_t(sg.doc.q0 + i) * size_t(p.os) + size_t(head) * size_t(p.D) + size_t(c), y);
+        else
+          for (int e = 0; e < 8; ++e) __stcg(mine + size_t(r) * size_t(p.D + 2) + c + e, y[e]);
+      }
+      if (!whole) {
+        __stcg(mine + size_t(r) * size_t(p.D + 2) + p.D, mx);
+        __stcg(mine + size_t(r) * size_t(p.D + 2) + p.D + 1, sum);
+      }
+    }
+    if (whole) continue;
+
+    // the last CTA of the item's parts joins them, in order
+    const int c0 = share.cta_of(sg.base), c1 = share.cta_of(sg.base + sg.steps - 1);
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) seen = atomicInc(p.counters + c0, unsigned(c1 - c0));  // counts 0 .. c1 - c0, then 0 again
+    __syncthreads();
+    if (seen == unsigned(c1 - c0)) {
+      __threadfence();
+      for (int x = int(threadIdx.x); x < rows * chunks; x += kFewThreads) {
+        const int r = x / chunks, c = 8 * (x - r * chunks);
+        int i, head;
+        row_of(r, i, head);
+        float mx = -INFINITY, sum = 0.0f, y[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+        for (int w = c0; w <= c1; ++w) mx = fmaxf(mx, __ldcg(part(w, w == c0) + size_t(r) * size_t(p.D + 2) + p.D));
+        const float ref = mx == -INFINITY ? 0.0f : mx;
+        for (int w = c0; w <= c1; ++w) {
+          const float* a = part(w, w == c0) + size_t(r) * size_t(p.D + 2);
+          const float f = ex2(__ldcg(a + p.D) - ref);
+          sum = fmaf(f, __ldcg(a + p.D + 1), sum);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] = fmaf(f, __ldcg(a + c + e), y[e]);
+        }
+        const bool none = limit_of(p.causal, i + lk - sg.doc.lq, lk, sg.doc.prefix) == 0;
+        const float inv = 1.0f / sum;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = none ? 0.0f : y[e] * inv;
+        store8(p, size_t(sg.doc.q0 + i) * size_t(p.os) + size_t(head) * size_t(p.D) + size_t(c), y);
+      }
+    }
+    __syncthreads();  // `seen` and the merge buffers are free again
+  }
+}
+
+template <int KI, int VI, int NT>
+cudaError_t few_launch_as(const Params& p, cudaStream_t s) {
+  const int sms = num_sms() < kMaxSms ? num_sms() : kMaxSms;
+  return launch_pdl(few_kernel<KI, VI, NT>, dim3(unsigned(sms * (NT == 1 ? kCtasPerSm : 2))), dim3(kFewThreads), 0, s, p);
+}
+
+template <int NT>
+cudaError_t few_launch_rows(const Params& p, cudaStream_t s) {
+  if (p.D <= 64) return few_launch_as<2, 1, NT>(p, s);
+  if (p.D <= 96) return few_launch_as<3, 2, NT>(p, s);
+  return few_launch_as<4, 2, NT>(p, s);
+}
+
+}  // namespace
+
+size_t few_workspace(int head_dim) {
+  return kCounterBytes + size_t(kMaxFewGrid) * 2 * 16 * size_t(head_dim + 2) * sizeof(float);
+}
+
+sv_status few_launch(const Params& p, cudaStream_t s) {
+  static_assert(kMaxFewGrid * sizeof(unsigned) <= kCounterBytes, "counters");
+  // rows of the documents on average decide between one and two 8-row tiles
+  const bool small = static_cast<long long>(p.total_q) * p.group <= 8ll * p.docs;
+  const cudaError_t e = small ? few_launch_rows<1>(p, s) : few_launch_rows<2>(p, s);
+  return e == cudaSuccess ? SV_OK : cuda_fail(e, "packed attention launch (few rows)");
+}
+
+}  // namespace packed
+}  // namespace sv
