@@ -15,12 +15,16 @@
 // exactly (error below 2^-22 turns at 2^31 positions, 2^-33 at a million); its upper 32
 // bits, as a signed fraction of half a turn, go to sincospif.
 //
-// Bound: DRAM, every value read and written once (4 bytes a value). The cosines of a row
-// are the same for all of its heads: a warp computes them once and walks heads with them.
-// A head is spread over L lanes (a power of two >= head_dim / 16), each holding eight
-// pairs in runs of V values whose partners lie n values on (V = 8, 4, 2 or 1 by what
-// divides n, so that every run is one aligned load); neighbouring lanes hold neighbouring
-// runs. Statistics are xor-shuffle sums over the L lanes.
+// Bound: DRAM, every value read and written once (4 bytes a value). A lane holds eight
+// values, four pairs, so that few registers keep many warps and their loads in flight: a run of
+// V values and the run n values on with their partners (V = 4, 2 or 1 by what divides n, so
+// that every run is one aligned load), or one run of eight for neighbouring pairs. A head takes
+// head_dim / 8 lanes, a warp as many whole heads as fit (72 values: 3 heads on 27 lanes), and
+// neighbouring lanes hold neighbouring runs. The cosines of a row are the same for all of its
+// heads: a block computes those of its rows once into shared memory, one to eight warps walk a
+// row's heads with their share of them in registers, the next heads' loads ahead of the
+// arithmetic. (Sixteen values a lane, a power of two of lanes a head, cosines in every warp:
+// 23,328 rows of 32 heads of 72, 97 us, 337 instructions per warp and step.)
 #include <cmath>
 
 #include "ptx.cuh"
@@ -30,6 +34,7 @@ namespace sv {
 namespace {
 
 constexpr int kRopeThreads = 256;
+constexpr int kRopeWarps = kRopeThreads / 32;
 enum { kNormNone = 0, kNormRms = 1, kNormLayer = 2 };
 
 struct RopeParams {
@@ -39,208 +44,192 @@ struct RopeParams {
   long long xs[2], ys[2];  // row strides in values
   int heads0, heads;       // heads of x[0], of both
   const int* pos;          // [axes, rows]
-  int rows, head_dim, lanes, per_warp;  // heads a warp walks: per_warp x (32 / lanes)
-  int chunks;              // warps per row
+  int rows, head_dim;
+  int lanes, fold;         // lanes of a head, the largest power of two of them
+  int slots, trips;        // heads of a warp at a time, times for all heads
+  int warps_row;           // warps that share a row (1, 2, 4 or 8)
   float eps, inv_dim, gain;
   int pairs, n;            // rotated pairs, pairs per axis
   unsigned long long turns[SV_ROPE_MAX_PAIRS];
 };
 
-// One lane's runs: V values at `a`, V more at `b`; V = 0 (neighbouring pairs): eight
-// values at `a`, four pairs. Run g of a head; returns its first pair.
-template <int V>
-__device__ __forceinline__ int run_at(int g, int pairs, int n, int& a, int& b) {
-  if constexpr (V == 0) {
-    a = 8 * g;
-    b = a;
-    return 4 * g;
-  } else {
-    const int p = g * V;
-    if (p < pairs) {
-      const int axis = p / n;
-      a = p + axis * n;  // 2 n axis + (p - n axis)
-      b = a + n;
-    } else {
-      a = 2 * p;
-      b = a + V;
-    }
-    return p;
-  }
-}
-
+// Runs of a lane: V > 0: kRuns runs of V values at a[] with their partners at b[]; V = 0
+// (neighbouring pairs): eight values at a[0].
 template <int V>
 struct Runs {
   static constexpr int kPer = V == 0 ? 4 : V;  // pairs per run
-  static constexpr int kRuns = 8 / kPer;
+  static constexpr int kRuns = 4 / kPer;
 };
 
+// A lane's eight values, as loaded: pairs of halves, for V = 1 (first, second) of each pair.
 template <int V>
-__device__ __forceinline__ void load_half(const __half* p, __half2* h) {
-  if constexpr (V == 8) *reinterpret_cast<uint4*>(h) = *reinterpret_cast<const uint4*>(p);
-  else if constexpr (V == 4) *reinterpret_cast<uint2*>(h) = *reinterpret_cast<const uint2*>(p);
-  else *reinterpret_cast<unsigned*>(h) = *reinterpret_cast<const unsigned*>(p);
-}
-template <int V>
-__device__ __forceinline__ void store_half(__half* p, const __half2* h) {
-  if constexpr (V == 8) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(h);
-  else if constexpr (V == 4) *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(h);
-  else *reinterpret_cast<unsigned*>(p) = *reinterpret_cast<const unsigned*>(h);
-}
-
-// The kPer pairs of a run at p + a, p + b.
-template <int V>
-__device__ __forceinline__ void load_run(const __half* p, int a, int b, float* fa, float* fb) {
+__device__ __forceinline__ void load_runs(const __half* p, const int* a, const int* b, __half2 (&h)[4]) {
   if constexpr (V == 0) {
-    __half2 h[4];
-    load_half<8>(p + a, h);
+    *reinterpret_cast<uint4*>(h) = *reinterpret_cast<const uint4*>(p + a[0]);
+  } else if constexpr (V == 4) {
+    *reinterpret_cast<uint2*>(h) = *reinterpret_cast<const uint2*>(p + a[0]);
+    *reinterpret_cast<uint2*>(h + 2) = *reinterpret_cast<const uint2*>(p + b[0]);
+  } else if constexpr (V == 2) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = __half22float2(h[i]);
-      fa[i] = f.x;
-      fb[i] = f.y;
+    for (int s = 0; s < 2; ++s) {
+      h[s] = *reinterpret_cast<const __half2*>(p + a[s]);
+      h[2 + s] = *reinterpret_cast<const __half2*>(p + b[s]);
     }
-  } else if constexpr (V == 1) {
-    fa[0] = __half2float(p[a]);
-    fb[0] = __half2float(p[b]);
   } else {
-    __half2 h[V / 2], k[V / 2];
-    load_half<V>(p + a, h);
-    load_half<V>(p + b, k);
 #pragma unroll
-    for (int i = 0; i < V / 2; ++i) {
-      const float2 f = __half22float2(h[i]), g = __half22float2(k[i]);
-      fa[2 * i] = f.x;
-      fa[2 * i + 1] = f.y;
-      fb[2 * i] = g.x;
-      fb[2 * i + 1] = g.y;
-    }
+    for (int s = 0; s < 4; ++s) h[s] = __halves2half2(p[a[s]], p[b[s]]);
   }
 }
 template <int V>
-__device__ __forceinline__ void store_run(__half* p, int a, int b, const float* fa, const float* fb) {
+__device__ __forceinline__ void store_runs(__half* p, const int* a, const int* b, const __half2 (&h)[4]) {
   if constexpr (V == 0) {
-    __half2 h[4];
+    *reinterpret_cast<uint4*>(p + a[0]) = *reinterpret_cast<const uint4*>(h);
+  } else if constexpr (V == 4) {
+    *reinterpret_cast<uint2*>(p + a[0]) = *reinterpret_cast<const uint2*>(h);
+    *reinterpret_cast<uint2*>(p + b[0]) = *reinterpret_cast<const uint2*>(h + 2);
+  } else if constexpr (V == 2) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(fa[i], fb[i]);
-    store_half<8>(p + a, h);
-  } else if constexpr (V == 1) {
-    p[a] = __float2half_rn(fa[0]);
-    p[b] = __float2half_rn(fb[0]);
-  } else {
-    __half2 h[V / 2], k[V / 2];
-#pragma unroll
-    for (int i = 0; i < V / 2; ++i) {
-      h[i] = __floats2half2_rn(fa[2 * i], fa[2 * i + 1]);
-      k[i] = __floats2half2_rn(fb[2 * i], fb[2 * i + 1]);
+    for (int s = 0; s < 2; ++s) {
+      *reinterpret_cast<__half2*>(p + a[s]) = h[s];
+      *reinterpret_cast<__half2*>(p + b[s]) = h[2 + s];
     }
-    store_half<V>(p + a, h);
-    store_half<V>(p + b, k);
+  } else {
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      p[a[s]] = __low2half(h[s]);
+      p[b[s]] = __high2half(h[s]);
+    }
+  }
+}
+// Between the loaded form and the four pairs (fa, fb).
+template <int V>
+__device__ __forceinline__ void unpack(const __half2 (&h)[4], float (&fa)[4], float (&fb)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(h[i]);
+    if constexpr (V <= 1) fa[i] = f.x, fb[i] = f.y;
+    else if (i < 2) fa[2 * i] = f.x, fa[2 * i + 1] = f.y;
+    else fb[2 * i - 4] = f.x, fb[2 * i - 3] = f.y;
+  }
+}
+template <int V>
+__device__ __forceinline__ void pack(const float (&fa)[4], const float (&fb)[4], __half2 (&h)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (V <= 1) h[i] = __floats2half2_rn(fa[i], fb[i]);
+    else h[i] = i < 2 ? __floats2half2_rn(fa[2 * i], fa[2 * i + 1]) : __floats2half2_rn(fb[2 * i - 4], fb[2 * i - 3]);
   }
 }
 
-__device__ __forceinline__ float lanes_sum(float v, int lanes) {
-  for (int o = 1; o < lanes; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+// Sum over a head's lanes first .. first + lanes - 1, the same bits in each: the lanes behind
+// the largest power of two are folded onto the first ones, which then sum by exchange.
+__device__ __forceinline__ float head_sum(float v, int first, int l, const RopeParams& p) {
+  if (p.fold < p.lanes) {
+    const float t = __shfl_sync(0xffffffffu, v, first + l + p.fold);
+    if (l + p.fold < p.lanes) v += t;
+  }
+  for (int o = p.fold >> 1; o; o >>= 1) v += __shfl_sync(0xffffffffu, v, first + ((l & (p.fold - 1)) ^ o));
+  return p.fold < p.lanes ? __shfl_sync(0xffffffffu, v, first + (l & (p.fold - 1))) : v;
 }
 
 template <int V, int NORM>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kPer = Runs<V>::kPer, kRuns = Runs<V>::kRuns;
-  __shared__ unsigned long long turns[SV_ROPE_MAX_PAIRS];
-  for (int i = threadIdx.x; i < p.n; i += kRopeThreads) turns[i] = p.turns[i];
+  __shared__ float2 table[kRopeWarps * SV_ROPE_MAX_PAIRS];  // [row of the block][rotated pair]
   pdl_launch_dependents();
-  __syncthreads();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long job = static_cast<long long>(blockIdx.x) * (kRopeThreads / 32) + warp;
-  const long long row_ll = job / p.chunks;
-  if (row_ll >= p.rows) return;
-  const int row = int(row_ll), chunk = int(job - row_ll * p.chunks);
-  const int slots = 32 / p.lanes, slot = lane / p.lanes, l = lane - slot * p.lanes;
-  const int runs = p.head_dim / (2 * kPer);  // of one head
+  const int rows_block = kRopeWarps / p.warps_row;
+  const int row0 = int(blockIdx.x) * rows_block;
+  for (int i = threadIdx.x; i < rows_block * p.pairs; i += kRopeThreads) {
+    const int r = i / p.pairs, pair = i - r * p.pairs, axis = pair >= p.n ? 1 : 0;
+    if (row0 + r >= p.rows) break;
+    const long long pos = p.pos[static_cast<long long>(axis) * p.rows + row0 + r];
+    const unsigned long long phase = p.turns[pair - axis * p.n] * static_cast<unsigned long long>(pos);
+    float sn, cs;
+    sincospif(static_cast<float>(static_cast<int>(phase >> 32)) * 0x1p-31f, &sn, &cs);
+    table[i] = make_float2(cs * p.gain, sn * p.gain);
+  }
+  __syncthreads();
+  const int r = warp / p.warps_row;
+  const int row = row0 + r;
+  if (row >= p.rows) return;
+  const int slot = lane / p.lanes, first = slot * p.lanes, l = lane - first;
+  const bool in = slot < p.slots;
 
-  float cs[8], sn[8];
+  // this lane's runs and their cosines: run g = s lanes + l of the head
   int at_a[kRuns], at_b[kRuns];
+  float cs[4], sn[4];
 #pragma unroll
   for (int s = 0; s < kRuns; ++s) {
-    const int pair = run_at<V>(s * p.lanes + l, p.pairs, p.n, at_a[s], at_b[s]);
+    const int g = s * p.lanes + l, pair = g * kPer;
+    const int axis = pair >= p.n ? 1 : 0;
+    if (V == 0) at_a[s] = 8 * g, at_b[s] = 8 * g;
+    else if (pair < p.pairs) at_a[s] = pair + axis * p.n, at_b[s] = at_a[s] + p.n;
+    else at_a[s] = 2 * pair, at_b[s] = 2 * pair + V;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      cs[s * kPer + i] = 1.0f;
-      sn[s * kPer + i] = 0.0f;
-      if (pair + i < p.pairs) {
-        const int axis = (pair + i) / p.n;
-        const long long pos = p.pos[static_cast<long long>(axis) * p.rows + row];
-        const unsigned long long phase = turns[pair + i - axis * p.n] * static_cast<unsigned long long>(pos);
-        float a, b;
-        sincospif(static_cast<float>(static_cast<int>(phase >> 32)) * 0x1p-31f, &a, &b);
-        sn[s * kPer + i] = a * p.gain;
-        cs[s * kPer + i] = b * p.gain;
-      }
+      const float2 t = pair + i < p.pairs ? table[r * p.pairs + pair + i] : make_float2(1.0f, 0.0f);
+      cs[s * kPer + i] = t.x;
+      sn[s * kPer + i] = t.y;
     }
   }
-
-  float ga[8], gb[8];
-  int gamma_of = -1;
-  for (int it = 0; it < p.per_warp; ++it) {
-    const int h = (chunk * p.per_warp + it) * slots + slot;
-    if ((chunk * p.per_warp + it) * slots >= p.heads) break;
-    const bool live = h < p.heads;
-    const int which = live && h >= p.heads0 ? 1 : 0;
-    const int head = which ? h - p.heads0 : h;
-    const __half* x = p.x[which] + row * p.xs[which] + static_cast<long long>(head) * p.head_dim;
-    float a[8], b[8];
+  __half2 gamma[2][4];
+  if constexpr (NORM != kNormNone) {
 #pragma unroll
-    for (int s = 0; s < kRuns; ++s) {
-      if (live && s * p.lanes + l < runs) load_run<V>(x, at_a[s], at_b[s], a + s * kPer, b + s * kPer);
-      else
+    for (int w = 0; w < 2; ++w) {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) a[s * kPer + i] = b[s * kPer + i] = 0.0f;
+      for (int i = 0; i < 4; ++i) gamma[w][i] = __float2half2_rn(1.0f);
+      if (p.gamma[w] && in) load_runs<V>(p.gamma[w], at_a, at_b, gamma[w]);
     }
+  }
+  const __half *x0 = p.x[0] + row * p.xs[0], *x1 = p.x[1] + row * p.xs[1];
+  __half *y0 = p.y[0] + row * p.ys[0], *y1 = p.y[1] + row * p.ys[1];
+  const int sub = warp & (p.warps_row - 1);
+  auto head_of = [&](int trip) { return in && trip < p.trips && trip * p.slots + slot < p.heads ? trip * p.slots + slot : -1; };
+  auto fetch = [&](int h, __half2 (&raw)[4]) {
+    if (h < 0) return;
+    load_runs<V>(h < p.heads0 ? x0 + h * p.head_dim : x1 + (h - p.heads0) * p.head_dim, at_a, at_b, raw);
+  };
+  __half2 next[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) next[i] = __float2half2_rn(0.0f);
+  int h = head_of(sub);
+  fetch(h, next);
+  for (int trip = sub; trip < p.trips; trip += p.warps_row) {
+    float a[4], b[4];
+    unpack<V>(next, a, b);
+    const int now = h;
+    h = head_of(trip + p.warps_row);
+    fetch(h, next);
     if constexpr (NORM != kNormNone) {
-      if (gamma_of != which) {
-        gamma_of = which;
-        const __half* g = p.gamma[which];
-#pragma unroll
-        for (int s = 0; s < kRuns; ++s) {
-          if (g && s * p.lanes + l < runs) load_run<V>(g, at_a[s], at_b[s], ga + s * kPer, gb + s * kPer);
-          else
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) ga[s * kPer + i] = gb[s * kPer + i] = 1.0f;
-        }
-      }
       if constexpr (NORM == kNormLayer) {
-        float sum = 0.0f;
+        const float mean = head_sum(((a[0] + b[0]) + (a[1] + b[1])) + ((a[2] + b[2]) + (a[3] + b[3])), first, l, p) * p.inv_dim;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum += a[i] + b[i];
-        const float mean = lanes_sum(sum, p.lanes) * p.inv_dim;
-#pragma unroll
-        for (int s = 0; s < kRuns; ++s)
-          if (s * p.lanes + l < runs)
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) a[s * kPer + i] -= mean, b[s * kPer + i] -= mean;
+        for (int i = 0; i < 4; ++i) a[i] -= mean, b[i] -= mean;
       }
       float sq = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sq = fmaf(a[i], a[i], fmaf(b[i], b[i], sq));
-      const float r = rsqrtf(lanes_sum(sq, p.lanes) * p.inv_dim + p.eps);
+      for (int i = 0; i < 4; ++i) sq = fmaf(a[i], a[i], fmaf(b[i], b[i], sq));
+      const float rs = rsqrtf(head_sum(sq, first, l, p) * p.inv_dim + p.eps);
+      float ga[4], gb[4];
+      __half2 gm[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) a[i] *= r * ga[i], b[i] *= r * gb[i];
+      for (int i = 0; i < 4; ++i) gm[i] = now >= p.heads0 ? gamma[1][i] : gamma[0][i];
+      unpack<V>(gm, ga, gb);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a[i] *= rs * ga[i], b[i] *= rs * gb[i];
     }
-    if (!live) continue;
-    __half* y = p.y[which] + row * p.ys[which] + static_cast<long long>(head) * p.head_dim;
+    if (now < 0) continue;
+    float ya[4], yb[4];
 #pragma unroll
-    for (int s = 0; s < kRuns; ++s) {
-      if (s * p.lanes + l >= runs) continue;
-      float ya[kPer], yb[kPer];
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int k = s * kPer + i;
-        ya[i] = a[k] * cs[k] - b[k] * sn[k];
-        yb[i] = b[k] * cs[k] + a[k] * sn[k];
-      }
-      store_run<V>(y, at_a[s], at_b[s], ya, yb);
+    for (int i = 0; i < 4; ++i) {
+      ya[i] = a[i] * cs[i] - b[i] * sn[i];
+      yb[i] = b[i] * cs[i] + a[i] * sn[i];
     }
+    __half2 out[4];
+    pack<V>(ya, yb, out);
+    store_runs<V>(now < p.heads0 ? y0 + now * p.head_dim : y1 + (now - p.heads0) * p.head_dim, at_a, at_b, out);
   }
 }
 
@@ -254,33 +243,27 @@ cudaError_t rope_launch_v(const RopeParams& p, int norm, unsigned grid, cudaStre
 sv_status rope_launch(RopeParams& p, const sv_rope_plan* plan, int norm, cudaStream_t s) {
   const int D = p.head_dim;
   p.pairs = plan ? plan->rot_dim / 2 : 0;
-  p.n = plan ? plan->pairs : 8;  // (no plan: no rotated pair, runs as wide as the head allows)
+  p.n = plan ? plan->pairs : 4;  // (no plan: no rotated pair, runs as wide as they get)
   p.gain = plan ? plan->gain : 1.0f;
   p.inv_dim = 1.0f / float(D);
   for (int i = 0; i < (plan ? plan->pairs : 0); ++i) p.turns[i] = plan->turns[i];
-  p.lanes = 1;
-  while (p.lanes * 16 < D) p.lanes *= 2;
-  const int slots = 32 / p.lanes;
-  const int trips = (p.heads + slots - 1) / slots;
-  // heads per warp: enough to spread the row's cosines over, while the warps still fill
-  // the GPU (about 32 warps on each SM)
-  const long long want = 32ll * num_sms();
-  p.per_warp = 1;
-  while (p.per_warp < trips && p.per_warp < 8 &&
-         static_cast<long long>(p.rows) * ((trips + p.per_warp) / (p.per_warp + 1)) >= want)
-    ++p.per_warp;
-  p.chunks = (trips + p.per_warp - 1) / p.per_warp;
-  const long long warps = static_cast<long long>(p.rows) * p.chunks;
-  const long long blocks = (warps + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
-  if (blocks > 0x7fffffffll) {
-    set_error("rope: %d rows of %d heads are too many for one call", p.rows, p.heads);
-    return SV_ERR_UNSUPPORTED;
-  }
+  p.lanes = D / 8;
+  p.fold = 1;
+  while (2 * p.fold <= p.lanes) p.fold *= 2;
+  p.slots = 32 / p.lanes;
+  p.trips = (p.heads + p.slots - 1) / p.slots;
+  // warps per row: one (a row's cosines and gammas are then loaded into registers once) where
+  // that fills the GPU with 32 warps an SM, more where rows are few
+  p.warps_row = 1;
+  while (p.warps_row < kRopeWarps && p.warps_row < p.trips &&
+         static_cast<long long>(p.rows) * p.warps_row < 32ll * num_sms())
+    p.warps_row *= 2;
+  const int rows_block = kRopeWarps / p.warps_row;
+  const long long blocks = (static_cast<long long>(p.rows) + rows_block - 1) / rows_block;
   const unsigned grid = unsigned(blocks);
   LaunchScope L(kKindOther, 0.0, 4.0 * p.rows * double(p.heads) * D, s);
   cudaError_t e;
   if (plan && plan->layout == SV_ROPE_INTERLEAVED) e = rope_launch_v<0>(p, norm, grid, s);
-  else if (p.n % 8 == 0 && D % 16 == 0) e = rope_launch_v<8>(p, norm, grid, s);
   else if (p.n % 4 == 0) e = rope_launch_v<4>(p, norm, grid, s);
   else if (p.n % 2 == 0) e = rope_launch_v<2>(p, norm, grid, s);
   else e = rope_launch_v<1>(p, norm, grid, s);
