@@ -46,7 +46,7 @@ struct RopeParams {
   const int* pos;          // [axes, rows]
   int rows, head_dim;
   int lanes, fold;         // lanes of a head, the largest power of two of them
-  int slots, trips;        // heads of a warp at a time, times for all heads
+  int slots;               // heads of a warp at a time
   int warps_row;           // warps that share a row (1, 2, 4 or 8)
   float eps, inv_dim, gain;
   int pairs, n;            // rotated pairs, pairs per axis
@@ -121,16 +121,33 @@ __device__ __forceinline__ void pack(const float (&fa)[4], const float (&fb)[4],
   }
 }
 
-// Sum over a head's lanes first .. first + lanes - 1, the same bits in each: the lanes behind
-// the largest power of two are folded onto the first ones, which then sum by exchange.
-__device__ __forceinline__ float head_sum(float v, int first, int l, const RopeParams& p) {
-  if (p.fold < p.lanes) {
-    const float t = __shfl_sync(0xffffffffu, v, first + l + p.fold);
-    if (l + p.fold < p.lanes) v += t;
+// Sum over a head's lanes, the same bits in each. Where the lanes are no power of two, those
+// behind the largest one (`fold`) are folded onto the first ones, which then sum by exchange.
+struct HeadSum {
+  int fold, from_fold, from[4], from_low;  // source lanes
+  bool folds, has_fold;
+  __device__ __forceinline__ HeadSum(const RopeParams& p, int first, int l) {
+    fold = p.fold;
+    folds = p.fold < p.lanes;
+    has_fold = l + p.fold < p.lanes;
+    from_fold = (first + l + p.fold) & 31;
+    from_low = first + (l & (p.fold - 1));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) from[i] = first + ((l & (p.fold - 1)) ^ (8 >> i));
   }
-  for (int o = p.fold >> 1; o; o >>= 1) v += __shfl_sync(0xffffffffu, v, first + ((l & (p.fold - 1)) ^ o));
-  return p.fold < p.lanes ? __shfl_sync(0xffffffffu, v, first + (l & (p.fold - 1))) : v;
-}
+  __device__ __forceinline__ float operator()(float v) const {
+    if (folds) {
+      const float t = __shfl_sync(0xffffffffu, v, from_fold);
+      if (has_fold) v += t;
+    }
+    if (fold == 32) v += __shfl_xor_sync(0xffffffffu, v, 16);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (fold > (8 >> i)) v += __shfl_sync(0xffffffffu, v, from[i]);
+    if (folds) v = __shfl_sync(0xffffffffu, v, from_low);
+    return v;
+  }
+};
 
 template <int V, int NORM>
 __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_constant__ RopeParams p) {
@@ -155,7 +172,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_cons
   const int row = row0 + r;
   if (row >= p.rows) return;
   const int slot = lane / p.lanes, first = slot * p.lanes, l = lane - first;
-  const bool in = slot < p.slots;
+  const HeadSum head_sum(p, first, l);
 
   // this lane's runs and their cosines: run g = s lanes + l of the head
   int at_a[kRuns], at_b[kRuns];
@@ -174,62 +191,75 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_cons
       sn[s * kPer + i] = t.y;
     }
   }
-  __half2 gamma[2][4];
-  if constexpr (NORM != kNormNone) {
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) gamma[w][i] = __float2half2_rn(1.0f);
-      if (p.gamma[w] && in) load_runs<V>(p.gamma[w], at_a, at_b, gamma[w]);
-    }
-  }
-  const __half *x0 = p.x[0] + row * p.xs[0], *x1 = p.x[1] + row * p.xs[1];
-  __half *y0 = p.y[0] + row * p.ys[0], *y1 = p.y[1] + row * p.ys[1];
   const int sub = warp & (p.warps_row - 1);
-  auto head_of = [&](int trip) { return in && trip < p.trips && trip * p.slots + slot < p.heads ? trip * p.slots + slot : -1; };
-  auto fetch = [&](int h, __half2 (&raw)[4]) {
-    if (h < 0) return;
-    load_runs<V>(h < p.heads0 ? x0 + h * p.head_dim : x1 + (h - p.heads0) * p.head_dim, at_a, at_b, raw);
-  };
-  __half2 next[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) next[i] = __float2half2_rn(0.0f);
-  int h = head_of(sub);
-  fetch(h, next);
-  for (int trip = sub; trip < p.trips; trip += p.warps_row) {
-    float a[4], b[4];
-    unpack<V>(next, a, b);
-    const int now = h;
-    h = head_of(trip + p.warps_row);
-    fetch(h, next);
+#pragma unroll 1
+  for (int part = 0; part < (NORM == kNormNone ? 1 : 2); ++part) {  // queries, keys
+    const int heads = part ? p.heads - p.heads0 : p.heads0;
+    // with a norm the weights go into the rotation: (a, b) -> rs (a ga cs - b gb sn, b gb cs + a ga sn)
+    float aa[4], ab[4], bb[4], ba[4];
     if constexpr (NORM != kNormNone) {
-      if constexpr (NORM == kNormLayer) {
-        const float mean = head_sum(((a[0] + b[0]) + (a[1] + b[1])) + ((a[2] + b[2]) + (a[3] + b[3])), first, l, p) * p.inv_dim;
+      __half2 g[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) a[i] -= mean, b[i] -= mean;
-      }
-      float sq = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) sq = fmaf(a[i], a[i], fmaf(b[i], b[i], sq));
-      const float rs = rsqrtf(head_sum(sq, first, l, p) * p.inv_dim + p.eps);
+      for (int i = 0; i < 4; ++i) g[i] = __float2half2_rn(1.0f);
+      if (p.gamma[part] && slot < p.slots) load_runs<V>(p.gamma[part], at_a, at_b, g);
       float ga[4], gb[4];
-      __half2 gm[4];
+      unpack<V>(g, ga, gb);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) gm[i] = now >= p.heads0 ? gamma[1][i] : gamma[0][i];
-      unpack<V>(gm, ga, gb);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) a[i] *= rs * ga[i], b[i] *= rs * gb[i];
+      for (int i = 0; i < 4; ++i) {
+        aa[i] = ga[i] * cs[i];
+        ab[i] = gb[i] * sn[i];
+        bb[i] = gb[i] * cs[i];
+        ba[i] = ga[i] * sn[i];
+      }
     }
-    if (now < 0) continue;
-    float ya[4], yb[4];
+    int h = sub * p.slots + slot;
+    const int head_step = p.warps_row * p.slots;
+    const __half* x = p.x[part] + row * p.xs[part] + h * p.head_dim;
+    __half* y = p.y[part] + row * p.ys[part] + h * p.head_dim;
+    const int step = head_step * p.head_dim;
+    if (slot >= p.slots) h = heads;  // (a lane of no head: never below `heads`)
+    __half2 next[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      ya[i] = a[i] * cs[i] - b[i] * sn[i];
-      yb[i] = b[i] * cs[i] + a[i] * sn[i];
+    for (int i = 0; i < 4; ++i) next[i] = __float2half2_rn(0.0f);
+    if (h < heads) load_runs<V>(x, at_a, at_b, next);
+    for (int h0 = sub * p.slots; h0 < heads; h0 += head_step) {
+      float a[4], b[4];
+      unpack<V>(next, a, b);
+      const bool live = h < heads;
+      h += head_step;
+      x += step;
+      if (h < heads) load_runs<V>(x, at_a, at_b, next);
+      float ya[4], yb[4];
+      if constexpr (NORM == kNormNone) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          ya[i] = a[i] * cs[i] - b[i] * sn[i];
+          yb[i] = b[i] * cs[i] + a[i] * sn[i];
+        }
+      } else {
+        if constexpr (NORM == kNormLayer) {
+          const float mean =
+              head_sum(((a[0] + b[0]) + (a[1] + b[1])) + ((a[2] + b[2]) + (a[3] + b[3]))) * p.inv_dim;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) a[i] -= mean, b[i] -= mean;
+        }
+        float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) fma_x2(s0, s1, a[i], b[i], a[i], b[i], s0, s1);
+        const float rs = rsqrtf(head_sum(s0 + s1) * p.inv_dim + p.eps);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          ya[i] = rs * (a[i] * aa[i] - b[i] * ab[i]);
+          yb[i] = rs * (b[i] * bb[i] + a[i] * ba[i]);
+        }
+      }
+      if (live) {
+        __half2 out[4];
+        pack<V>(ya, yb, out);
+        store_runs<V>(y, at_a, at_b, out);
+      }
+      y += step;
     }
-    __half2 out[4];
-    pack<V>(ya, yb, out);
-    store_runs<V>(now < p.heads0 ? y0 + now * p.head_dim : y1 + (now - p.heads0) * p.head_dim, at_a, at_b, out);
   }
 }
 
@@ -251,11 +281,11 @@ sv_status rope_launch(RopeParams& p, const sv_rope_plan* plan, int norm, cudaStr
   p.fold = 1;
   while (2 * p.fold <= p.lanes) p.fold *= 2;
   p.slots = 32 / p.lanes;
-  p.trips = (p.heads + p.slots - 1) / p.slots;
+  const int trips = (p.heads + p.slots - 1) / p.slots;
   // warps per row: one (a row's cosines and gammas are then loaded into registers once) where
   // that fills the GPU with 32 warps an SM, more where rows are few
   p.warps_row = 1;
-  while (p.warps_row < kRopeWarps && p.warps_row < p.trips &&
+  while (p.warps_row < kRopeWarps && p.warps_row < trips &&
          static_cast<long long>(p.rows) * p.warps_row < 32ll * num_sms())
     p.warps_row *= 2;
   const int rows_block = kRopeWarps / p.warps_row;
