@@ -158,25 +158,12 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_cons
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rows_block = kRopeWarps / p.warps_row;
   const int row0 = int(blockIdx.x) * rows_block;
-  for (int i = threadIdx.x; i < rows_block * p.pairs; i += kRopeThreads) {
-    const int r = i / p.pairs, pair = i - r * p.pairs, axis = pair >= p.n ? 1 : 0;
-    if (row0 + r >= p.rows) break;
-    const long long pos = p.pos[static_cast<long long>(axis) * p.rows + row0 + r];
-    const unsigned long long phase = p.turns[pair - axis * p.n] * static_cast<unsigned long long>(pos);
-    float sn, cs;
-    sincospif(static_cast<float>(static_cast<int>(phase >> 32)) * 0x1p-31f, &sn, &cs);
-    table[i] = make_float2(cs * p.gain, sn * p.gain);
-  }
-  __syncthreads();
-  const int r = warp / p.warps_row;
-  const int row = row0 + r;
-  if (row >= p.rows) return;
+  const int r = warp / p.warps_row, sub = warp & (p.warps_row - 1);
+  const int row = min(row0 + r, p.rows - 1);
   const int slot = lane / p.lanes, first = slot * p.lanes, l = lane - first;
-  const HeadSum head_sum(p, first, l);
 
-  // this lane's runs and their cosines: run g = s lanes + l of the head
+  // this lane's runs: run g = s lanes + l of the head
   int at_a[kRuns], at_b[kRuns];
-  float cs[4], sn[4];
 #pragma unroll
   for (int s = 0; s < kRuns; ++s) {
     const int g = s * p.lanes + l, pair = g * kPer;
@@ -184,14 +171,38 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_cons
     if (V == 0) at_a[s] = 8 * g, at_b[s] = 8 * g;
     else if (pair < p.pairs) at_a[s] = pair + axis * p.n, at_b[s] = at_a[s] + p.n;
     else at_a[s] = 2 * pair, at_b[s] = 2 * pair + V;
+  }
+  const int head_step = p.warps_row * p.slots, step = head_step * p.head_dim;
+  const int h_first = slot < p.slots ? sub * p.slots + slot : 0x40000000;  // (a lane of no head)
+  __half2 next[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) next[i] = __float2half2_rn(0.0f);
+  // the first heads are on their way while the cosines are worked out
+  if (h_first < p.heads0) load_runs<V>(p.x[0] + row * p.xs[0] + h_first * p.head_dim, at_a, at_b, next);
+
+  for (int i = threadIdx.x; i < rows_block * p.pairs; i += kRopeThreads) {
+    const int tr = i / p.pairs, pair = i - tr * p.pairs, axis = pair >= p.n ? 1 : 0;
+    if (row0 + tr >= p.rows) break;
+    const long long pos = p.pos[static_cast<long long>(axis) * p.rows + row0 + tr];
+    const unsigned long long phase = p.turns[pair - axis * p.n] * static_cast<unsigned long long>(pos);
+    float sn, cs;
+    sincospif(static_cast<float>(static_cast<int>(phase >> 32)) * 0x1p-31f, &sn, &cs);
+    table[i] = make_float2(cs * p.gain, sn * p.gain);
+  }
+  __syncthreads();
+  if (row0 + r >= p.rows) return;
+  const HeadSum head_sum(p, first, l);
+  float cs[4], sn[4];
+#pragma unroll
+  for (int s = 0; s < kRuns; ++s)
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const float2 t = pair + i < p.pairs ? table[r * p.pairs + pair + i] : make_float2(1.0f, 0.0f);
+      const int pair = (s * p.lanes + l) * kPer + i;
+      const float2 t = pair < p.pairs ? table[r * p.pairs + pair] : make_float2(1.0f, 0.0f);
       cs[s * kPer + i] = t.x;
       sn[s * kPer + i] = t.y;
     }
-  }
-  const int sub = warp & (p.warps_row - 1);
+
 #pragma unroll 1
   for (int part = 0; part < (NORM == kNormNone ? 1 : 2); ++part) {  // queries, keys
     const int heads = part ? p.heads - p.heads0 : p.heads0;
@@ -212,16 +223,12 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_cons
         ba[i] = ga[i] * sn[i];
       }
     }
-    int h = sub * p.slots + slot;
-    const int head_step = p.warps_row * p.slots;
-    const __half* x = p.x[part] + row * p.xs[part] + h * p.head_dim;
-    __half* y = p.y[part] + row * p.ys[part] + h * p.head_dim;
-    const int step = head_step * p.head_dim;
-    if (slot >= p.slots) h = heads;  // (a lane of no head: never below `heads`)
-    __half2 next[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) next[i] = __float2half2_rn(0.0f);
-    if (h < heads) load_runs<V>(x, at_a, at_b, next);
+    int h = h_first;
+    const int h_at = slot < p.slots ? h : 0;
+    const __half* x = p.x[part] + row * p.xs[part] + h_at * p.head_dim;
+    __half* y = p.y[part] + row * p.ys[part] + h_at * p.head_dim;
+    if (part && h < heads) load_runs<V>(x, at_a, at_b, next);
+#pragma unroll 1
     for (int h0 = sub * p.slots; h0 < heads; h0 += head_step) {
       float a[4], b[4];
       unpack<V>(next, a, b);
