@@ -15,16 +15,18 @@
 // exactly (error below 2^-22 turns at 2^31 positions, 2^-33 at a million); its upper 32
 // bits, as a signed fraction of half a turn, go to sincospif.
 //
-// Bound: DRAM, every value read and written once (4 bytes a value). A lane holds eight
-// values, four pairs, so that few registers keep many warps and their loads in flight: a run of
-// V values and the run n values on with their partners (V = 4, 2 or 1 by what divides n, so
-// that every run is one aligned load), or one run of eight for neighbouring pairs. A head takes
-// head_dim / 8 lanes, a warp as many whole heads as fit (72 values: 3 heads on 27 lanes), and
-// neighbouring lanes hold neighbouring runs. The cosines of a row are the same for all of its
-// heads: a block computes those of its rows once into shared memory, one to eight warps walk a
-// row's heads with their share of them in registers, the next heads' loads ahead of the
-// arithmetic. (Sixteen values a lane, a power of two of lanes a head, cosines in every warp:
-// 23,328 rows of 32 heads of 72, 97 us, 337 instructions per warp and step.)
+// Bound: DRAM, every value read and written once (4 bytes a value). What it takes to get there
+// is bytes in flight and few instructions: the heads of a row lie one behind another, so a warp
+// copies up to 3 KB of them at a time to shared memory and back with one bulk copy each way, two
+// ahead of the arithmetic, and works on them in place. (Loads and stores by the lanes, any
+// layout and prefetch tried: 64 us at best for 23,328 rows of 32 heads of 72, at 170
+// instructions per 216 values and 13 KB in flight per SM.)
+// A lane holds eight pairs: runs of V values and the runs n values on with their partners
+// (V = 4, 2 or 1 by what divides n, so that every run is one aligned access), or runs of eight
+// for neighbouring pairs. A head takes head_dim / 16 lanes, a warp as many whole heads as fit
+// (72 values: 6 heads on 30 lanes), and neighbouring lanes hold neighbouring runs.
+// The cosines of a row are the same for all of its heads: a warp works them out once per row,
+// the norm's weights multiplied in.
 #include <cmath>
 
 #include "ptx.cuh"
@@ -37,94 +39,95 @@ constexpr int kRopeThreads = 256;
 constexpr int kRopeWarps = kRopeThreads / 32;
 enum { kNormNone = 0, kNormRms = 1, kNormLayer = 2 };
 
+constexpr int kBufBytes = 4096, kBufs = 3;  // of a warp
+
 struct RopeParams {
   const __half* x[2];      // queries, keys (or the one tensor of sv_rope)
   __half* y[2];
   const __half* gamma[2];  // [head_dim] or null (ones)
   long long xs[2], ys[2];  // row strides in values
-  int heads0, heads;       // heads of x[0], of both
+  int heads[2];            // keys: 0 for the one tensor of sv_rope
   const int* pos;          // [axes, rows]
   int rows, head_dim;
   int lanes, fold;         // lanes of a head, the largest power of two of them
   int slots;               // heads of a warp at a time
-  int warps_row;           // warps that share a row (1, 2, 4 or 8)
+  int chunk, chunks0, chunks;  // heads of a job, jobs of a row's queries, of a row
   float eps, inv_dim, gain;
   int pairs, n;            // rotated pairs, pairs per axis
+  int* err;
   unsigned long long turns[SV_ROPE_MAX_PAIRS];
 };
 
-// Runs of a lane: V > 0: kRuns runs of V values at a[] with their partners at b[]; V = 0
-// (neighbouring pairs): eight values at a[0].
+// Runs of a lane: V > 0: kRuns runs of V values at a with their partners at b; V = 0
+// (neighbouring pairs): runs of eight values at a.
 template <int V>
 struct Runs {
   static constexpr int kPer = V == 0 ? 4 : V;  // pairs per run
-  static constexpr int kRuns = 4 / kPer;
+  static constexpr int kRuns = 8 / kPer;
 };
 
-// A lane's eight values, as loaded: pairs of halves, for V = 1 (first, second) of each pair.
+// The pairs (fa, fb) of a run.
 template <int V>
-__device__ __forceinline__ void load_runs(const __half* p, const int* a, const int* b, __half2 (&h)[4]) {
+__device__ __forceinline__ void load_run(const __half* p, int a, int b, float* fa, float* fb) {
   if constexpr (V == 0) {
-    *reinterpret_cast<uint4*>(h) = *reinterpret_cast<const uint4*>(p + a[0]);
-  } else if constexpr (V == 4) {
-    *reinterpret_cast<uint2*>(h) = *reinterpret_cast<const uint2*>(p + a[0]);
-    *reinterpret_cast<uint2*>(h + 2) = *reinterpret_cast<const uint2*>(p + b[0]);
-  } else if constexpr (V == 2) {
+    __half2 h[4];
+    *reinterpret_cast<uint4*>(h) = *reinterpret_cast<const uint4*>(p + a);
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      h[s] = *reinterpret_cast<const __half2*>(p + a[s]);
-      h[2 + s] = *reinterpret_cast<const __half2*>(p + b[s]);
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(h[i]);
+      fa[i] = f.x, fb[i] = f.y;
     }
+  } else if constexpr (V == 1) {
+    fa[0] = __half2float(p[a]);
+    fb[0] = __half2float(p[b]);
   } else {
+    __half2 h[V / 2], k[V / 2];
+    if constexpr (V == 4) {
+      *reinterpret_cast<uint2*>(h) = *reinterpret_cast<const uint2*>(p + a);
+      *reinterpret_cast<uint2*>(k) = *reinterpret_cast<const uint2*>(p + b);
+    } else {
+      h[0] = *reinterpret_cast<const __half2*>(p + a);
+      k[0] = *reinterpret_cast<const __half2*>(p + b);
+    }
 #pragma unroll
-    for (int s = 0; s < 4; ++s) h[s] = __halves2half2(p[a[s]], p[b[s]]);
+    for (int i = 0; i < V / 2; ++i) {
+      const float2 f = __half22float2(h[i]), g = __half22float2(k[i]);
+      fa[2 * i] = f.x, fa[2 * i + 1] = f.y;
+      fb[2 * i] = g.x, fb[2 * i + 1] = g.y;
+    }
   }
 }
 template <int V>
-__device__ __forceinline__ void store_runs(__half* p, const int* a, const int* b, const __half2 (&h)[4]) {
+__device__ __forceinline__ void store_run(__half* p, int a, int b, const float* fa, const float* fb) {
   if constexpr (V == 0) {
-    *reinterpret_cast<uint4*>(p + a[0]) = *reinterpret_cast<const uint4*>(h);
-  } else if constexpr (V == 4) {
-    *reinterpret_cast<uint2*>(p + a[0]) = *reinterpret_cast<const uint2*>(h);
-    *reinterpret_cast<uint2*>(p + b[0]) = *reinterpret_cast<const uint2*>(h + 2);
-  } else if constexpr (V == 2) {
+    __half2 h[4];
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      *reinterpret_cast<__half2*>(p + a[s]) = h[s];
-      *reinterpret_cast<__half2*>(p + b[s]) = h[2 + s];
-    }
+    for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(fa[i], fb[i]);
+    *reinterpret_cast<uint4*>(p + a) = *reinterpret_cast<const uint4*>(h);
+  } else if constexpr (V == 1) {
+    p[a] = __float2half_rn(fa[0]);
+    p[b] = __float2half_rn(fb[0]);
   } else {
+    __half2 h[V / 2], k[V / 2];
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      p[a[s]] = __low2half(h[s]);
-      p[b[s]] = __high2half(h[s]);
+    for (int i = 0; i < V / 2; ++i) {
+      h[i] = __floats2half2_rn(fa[2 * i], fa[2 * i + 1]);
+      k[i] = __floats2half2_rn(fb[2 * i], fb[2 * i + 1]);
     }
-  }
-}
-// Between the loaded form and the four pairs (fa, fb).
-template <int V>
-__device__ __forceinline__ void unpack(const __half2 (&h)[4], float (&fa)[4], float (&fb)[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = __half22float2(h[i]);
-    if constexpr (V <= 1) fa[i] = f.x, fb[i] = f.y;
-    else if (i < 2) fa[2 * i] = f.x, fa[2 * i + 1] = f.y;
-    else fb[2 * i - 4] = f.x, fb[2 * i - 3] = f.y;
-  }
-}
-template <int V>
-__device__ __forceinline__ void pack(const float (&fa)[4], const float (&fb)[4], __half2 (&h)[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (V <= 1) h[i] = __floats2half2_rn(fa[i], fb[i]);
-    else h[i] = i < 2 ? __floats2half2_rn(fa[2 * i], fa[2 * i + 1]) : __floats2half2_rn(fb[2 * i - 4], fb[2 * i - 3]);
+    if constexpr (V == 4) {
+      *reinterpret_cast<uint2*>(p + a) = *reinterpret_cast<const uint2*>(h);
+      *reinterpret_cast<uint2*>(p + b) = *reinterpret_cast<const uint2*>(k);
+    } else {
+      *reinterpret_cast<__half2*>(p + a) = h[0];
+      *reinterpret_cast<__half2*>(p + b) = k[0];
+    }
   }
 }
 
 // Sum over a head's lanes, the same bits in each. Where the lanes are no power of two, those
 // behind the largest one (`fold`) are folded onto the first ones, which then sum by exchange.
 struct HeadSum {
-  int fold, from_fold, from[4], from_low;  // source lanes
+  int fold, from_fold, from[4], from_low;  // source lanes (a head has at most 16)
   bool folds, has_fold;
   __device__ __forceinline__ HeadSum(const RopeParams& p, int first, int l) {
     fold = p.fold;
@@ -140,7 +143,6 @@ struct HeadSum {
       const float t = __shfl_sync(0xffffffffu, v, from_fold);
       if (has_fold) v += t;
     }
-    if (fold == 32) v += __shfl_xor_sync(0xffffffffu, v, 16);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (fold > (8 >> i)) v += __shfl_sync(0xffffffffu, v, from[i]);
@@ -149,132 +151,241 @@ struct HeadSum {
   }
 };
 
-template <int V, int NORM>
-__global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_constant__ RopeParams p) {
-  constexpr int kPer = Runs<V>::kPer, kRuns = Runs<V>::kRuns;
-  __shared__ float2 table[kRopeWarps * SV_ROPE_MAX_PAIRS];  // [row of the block][rotated pair]
-  pdl_launch_dependents();
-  pdl_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rows_block = kRopeWarps / p.warps_row;
-  const int row0 = int(blockIdx.x) * rows_block;
-  const int r = warp / p.warps_row, sub = warp & (p.warps_row - 1);
-  const int row = min(row0 + r, p.rows - 1);
-  const int slot = lane / p.lanes, first = slot * p.lanes, l = lane - first;
+__host__ __device__ constexpr size_t rope_smem(int head_dim, int parts) {
+  return size_t(kRopeWarps) * kBufs * kBufBytes + size_t(kRopeWarps + parts) * (head_dim / 2) * sizeof(float2);
+}
 
+template <int V, int NORM>
+__global__ void __launch_bounds__(kRopeThreads, 2) rope_kernel(const __grid_constant__ RopeParams p) {
+  constexpr int kPer = Runs<V>::kPer, kRuns = Runs<V>::kRuns;
+  constexpr int kParts = NORM == kNormNone ? 1 : 2;  // queries, keys
+  extern __shared__ __align__(128) uint8_t rope_shared[];
+  __shared__ unsigned long long turns[SV_ROPE_MAX_PAIRS];
+  __shared__ __align__(8) unsigned long long full[kRopeWarps][kBufs];
+  __shared__ int abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int all = p.head_dim / 2;  // pairs, with those behind the rotated part
+  uint8_t* bufs = rope_shared + warp * kBufs * kBufBytes;
+  // the row's (cosine, sine) of every pair; the norm's weights of its two values
+  float2* tables = reinterpret_cast<float2*>(rope_shared + kRopeWarps * kBufs * kBufBytes);
+  float2* weights = tables + kRopeWarps * all;
+  float2* table = tables + warp * all;
+  // the values of pair i of a head
+  auto first_of = [&](int i) {
+    if (V == 0) return 2 * i;
+    if (i < p.pairs) return i + (i >= p.n ? p.n : 0);
+    return 2 * i - i % kPer;
+  };
+  auto second_of = [&](int i) { return V == 0 ? 2 * i + 1 : first_of(i) + (i < p.pairs ? p.n : kPer); };
+  for (int i = threadIdx.x; i < p.n && p.pairs; i += kRopeThreads) turns[i] = p.turns[i];
+  if (lane == 0) {
+    for (int b = 0; b < kBufs; ++b) mbar_init(smem_u32(&full[warp][b]), 1);
+    if (warp == 0) abort_flag = 0;
+    fence_barrier_init();
+  }
+  const int slot = lane / p.lanes, first = slot * p.lanes, l = lane - first;
+  const HeadSum head_sum(p, first, l);
+  const bool in = slot < p.slots;  // (a lane of no head otherwise)
   // this lane's runs: run g = s lanes + l of the head
-  int at_a[kRuns], at_b[kRuns];
+  int at_a[kRuns], at_b[kRuns], pair_of[kRuns];
+  bool has[kRuns];
 #pragma unroll
   for (int s = 0; s < kRuns; ++s) {
-    const int g = s * p.lanes + l, pair = g * kPer;
-    const int axis = pair >= p.n ? 1 : 0;
-    if (V == 0) at_a[s] = 8 * g, at_b[s] = 8 * g;
-    else if (pair < p.pairs) at_a[s] = pair + axis * p.n, at_b[s] = at_a[s] + p.n;
-    else at_a[s] = 2 * pair, at_b[s] = 2 * pair + V;
+    has[s] = in && (s * p.lanes + l) * kPer < all;
+    pair_of[s] = min((s * p.lanes + l) * kPer, all - kPer);
+    at_a[s] = first_of(pair_of[s]) + slot * p.head_dim;
+    at_b[s] = V == 0 ? at_a[s] : second_of(pair_of[s]) + slot * p.head_dim;
   }
-  const int head_step = p.warps_row * p.slots, step = head_step * p.head_dim;
-  const int h_first = slot < p.slots ? sub * p.slots + slot : 0x40000000;  // (a lane of no head)
-  __half2 next[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) next[i] = __float2half2_rn(0.0f);
-  // the first heads are on their way while the cosines are worked out
-  if (h_first < p.heads0) load_runs<V>(p.x[0] + row * p.xs[0] + h_first * p.head_dim, at_a, at_b, next);
-
-  for (int i = threadIdx.x; i < rows_block * p.pairs; i += kRopeThreads) {
-    const int tr = i / p.pairs, pair = i - tr * p.pairs, axis = pair >= p.n ? 1 : 0;
-    if (row0 + tr >= p.rows) break;
-    const long long pos = p.pos[static_cast<long long>(axis) * p.rows + row0 + tr];
-    const unsigned long long phase = p.turns[pair - axis * p.n] * static_cast<unsigned long long>(pos);
-    float sn, cs;
-    sincospif(static_cast<float>(static_cast<int>(phase >> 32)) * 0x1p-31f, &sn, &cs);
-    table[i] = make_float2(cs * p.gain, sn * p.gain);
-  }
-  __syncthreads();
-  if (row0 + r >= p.rows) return;
-  const HeadSum head_sum(p, first, l);
-  float cs[4], sn[4];
-#pragma unroll
-  for (int s = 0; s < kRuns; ++s)
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int pair = (s * p.lanes + l) * kPer + i;
-      const float2 t = pair < p.pairs ? table[r * p.pairs + pair] : make_float2(1.0f, 0.0f);
-      cs[s * kPer + i] = t.x;
-      sn[s * kPer + i] = t.y;
+  pdl_launch_dependents();
+  pdl_wait();
+  if constexpr (NORM != kNormNone)
+    for (int i = threadIdx.x; i < 2 * all; i += kRopeThreads) {
+      const int part = i >= all, pair = part ? i - all : i;
+      const __half* g = p.gamma[part];
+      weights[i] =
+          g ? make_float2(__half2float(g[first_of(pair)]), __half2float(g[second_of(pair)])) : make_float2(1.0f, 1.0f);
     }
+  __syncthreads();
 
-#pragma unroll 1
-  for (int part = 0; part < (NORM == kNormNone ? 1 : 2); ++part) {  // queries, keys
-    const int heads = part ? p.heads - p.heads0 : p.heads0;
-    // with a norm the weights go into the rotation: (a, b) -> rs (a ga cs - b gb sn, b gb cs + a ga sn)
-    float aa[4], ab[4], bb[4], ba[4];
-    if constexpr (NORM != kNormNone) {
-      __half2 g[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) g[i] = __float2half2_rn(1.0f);
-      if (p.gamma[part] && slot < p.slots) load_runs<V>(p.gamma[part], at_a, at_b, g);
-      float ga[4], gb[4];
-      unpack<V>(g, ga, gb);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        aa[i] = ga[i] * cs[i];
-        ab[i] = gb[i] * sn[i];
-        bb[i] = gb[i] * cs[i];
-        ba[i] = ga[i] * sn[i];
+  // Jobs: chunk c of row r is job r x chunks + c; a warp takes a contiguous share of them.
+  const long long jobs = static_cast<long long>(p.rows) * p.chunks, warps = static_cast<long long>(gridDim.x) * kRopeWarps;
+  const long long me = static_cast<long long>(blockIdx.x) * kRopeWarps + warp;
+  const long long begin = jobs * me / warps;
+  const int count = int(jobs * (me + 1) / warps - begin);
+  struct Job {
+    int row, chunk, part, h0, heads;
+  };
+  auto fill = [&](Job& j) {
+    j.part = j.chunk >= p.chunks0 ? 1 : 0;
+    j.h0 = (j.part ? j.chunk - p.chunks0 : j.chunk) * p.chunk;
+    j.heads = min(p.chunk, (j.part ? p.heads[1] : p.heads[0]) - j.h0);
+  };
+  auto advance = [&](Job& j) {
+    if (++j.chunk == p.chunks) j.chunk = 0, ++j.row;
+    fill(j);
+  };
+  Job now, load;
+  now.row = int(begin / p.chunks);
+  now.chunk = int(begin - static_cast<long long>(now.row) * p.chunks);
+  fill(now);
+  load = now;
+  auto copy_in = [&](int n) {  // job `load`, the warp's n-th, into its buffer (lane 0)
+    const uint32_t bar = smem_u32(&full[warp][n % kBufs]), bytes = uint32_t(load.heads * p.head_dim * 2);
+    const __half* src = (load.part ? p.x[1] + load.row * p.xs[1] : p.x[0] + load.row * p.xs[0]) + load.h0 * p.head_dim;
+    mbar_arrive_expect_tx(bar, bytes);
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(bufs + (n % kBufs) * kBufBytes)),
+                 "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+                 : "memory");
+  };
+  for (int n = 0; n < kBufs - 1 && n < count; ++n) {
+    if (lane == 0) copy_in(n);
+    advance(load);
+  }
+  int table_row = -1, pos_row = now.row;
+  auto position = [&](int axis, int row) {
+    return p.pairs > axis * p.n ? p.pos[static_cast<long long>(axis) * p.rows + row] : 0;
+  };
+  int pos0 = count ? position(0, now.row) : 0, pos1 = count ? position(1, now.row) : 0;
+
+  for (int n = 0; n < count; ++n, advance(now)) {
+    if (now.row != table_row) {  // the row's cosines, each once for all heads
+      table_row = now.row;
+      if (pos_row != now.row) {
+        pos_row = now.row;
+        pos0 = position(0, pos_row);
+        pos1 = position(1, pos_row);
+      }
+      __syncwarp();
+      for (int i = lane; i < all; i += 32) {
+        float sn = 0.0f, cs = 1.0f;
+        if (i < p.pairs) {
+          const bool second = i >= p.n;
+          const unsigned long long phase =
+              turns[second ? i - p.n : i] * static_cast<unsigned long long>(static_cast<long long>(second ? pos1 : pos0));
+          sincospif(static_cast<float>(static_cast<int>(phase >> 32)) * 0x1p-31f, &sn, &cs);
+          sn *= p.gain;
+          cs *= p.gain;
+        }
+        table[i] = make_float2(cs, sn);
+      }
+      __syncwarp();
+      if (table_row + 1 < p.rows) {  // the next row's positions are on their way
+        pos_row = table_row + 1;
+        pos0 = position(0, pos_row);
+        pos1 = position(1, pos_row);
       }
     }
-    int h = h_first;
-    const int h_at = slot < p.slots ? h : 0;
-    const __half* x = p.x[part] + row * p.xs[part] + h_at * p.head_dim;
-    __half* y = p.y[part] + row * p.ys[part] + h_at * p.head_dim;
-    if (part && h < heads) load_runs<V>(x, at_a, at_b, next);
-#pragma unroll 1
-    for (int h0 = sub * p.slots; h0 < heads; h0 += head_step) {
-      float a[4], b[4];
-      unpack<V>(next, a, b);
-      const bool live = h < heads;
-      h += head_step;
-      x += step;
-      if (h < heads) load_runs<V>(x, at_a, at_b, next);
-      float ya[4], yb[4];
-      if constexpr (NORM == kNormNone) {
+    // a' = a aa + b ab, b' = b bb + a ba, the norm's weights in them
+    float aa[8], ab[8], bb[8], ba[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          ya[i] = a[i] * cs[i] - b[i] * sn[i];
-          yb[i] = b[i] * cs[i] + a[i] * sn[i];
-        }
-      } else {
+    for (int s = 0; s < kRuns; ++s)
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const float2 t = table[pair_of[s] + i];
+        const float2 g = NORM == kNormNone ? make_float2(1.0f, 1.0f) : weights[(now.part ? all : 0) + pair_of[s] + i];
+        const int k = s * kPer + i;
+        aa[k] = g.x * t.x, ab[k] = -g.y * t.y, bb[k] = g.y * t.x, ba[k] = g.x * t.y;
+      }
+    uint8_t* buf = bufs + (n % kBufs) * kBufBytes;
+    if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&full[warp][n % kBufs]), (n / kBufs) & 1, &abort_flag, p.err))) {
+      // (the copies behind this one land before the block can exit)
+      for (int i = n; lane == 0 && i < count && i < n + kBufs - 1; ++i)
+        mbar_wait_bounded(smem_u32(&full[warp][i % kBufs]), (i / kBufs) & 1, p.err);
+      break;
+    }
+    __half* xb = reinterpret_cast<__half*>(buf);
+    for (int h = 0; h < now.heads; h += p.slots, xb += p.slots * p.head_dim) {
+      const bool live = h + slot < now.heads;
+      float a[8], b[8];
+#pragma unroll
+      for (int s = 0; s < kRuns; ++s) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) a[s * kPer + i] = b[s * kPer + i] = 0.0f;
+        if (live && has[s]) load_run<V>(xb, at_a[s], at_b[s], a + s * kPer, b + s * kPer);
+      }
+      float rs = 1.0f;
+      if constexpr (NORM != kNormNone) {
         if constexpr (NORM == kNormLayer) {
-          const float mean =
-              head_sum(((a[0] + b[0]) + (a[1] + b[1])) + ((a[2] + b[2]) + (a[3] + b[3]))) * p.inv_dim;
+          float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) a[i] -= mean, b[i] -= mean;
+          for (int i = 0; i < 8; i += 2) {
+            add_x2(s0, s1, s0, s1, a[i], a[i + 1]);
+            add_x2(s0, s1, s0, s1, b[i], b[i + 1]);
+          }
+          const float mean = head_sum(s0 + s1) * p.inv_dim;
+#pragma unroll
+          for (int s = 0; s < kRuns; ++s)
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+              if (has[s]) a[s * kPer + i] -= mean, b[s * kPer + i] -= mean;
         }
         float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) fma_x2(s0, s1, a[i], b[i], a[i], b[i], s0, s1);
-        const float rs = rsqrtf(head_sum(s0 + s1) * p.inv_dim + p.eps);
+        for (int i = 0; i < 8; i += 2) {
+          fma_x2(s0, s1, a[i], a[i + 1], a[i], a[i + 1], s0, s1);
+          fma_x2(s0, s1, b[i], b[i + 1], b[i], b[i + 1], s0, s1);
+        }
+        const float var = fmaf(head_sum(s0 + s1), p.inv_dim, p.eps);
+        asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(rs) : "f"(var));
+      }
+      float ya[8], yb[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          ya[i] = rs * (a[i] * aa[i] - b[i] * ab[i]);
-          yb[i] = rs * (b[i] * bb[i] + a[i] * ba[i]);
+      for (int i = 0; i < 8; i += 2) {
+        mul_x2(ya[i], ya[i + 1], a[i], a[i + 1], aa[i], aa[i + 1]);
+        mul_x2(yb[i], yb[i + 1], b[i], b[i + 1], bb[i], bb[i + 1]);
+        fma_x2(ya[i], ya[i + 1], b[i], b[i + 1], ab[i], ab[i + 1], ya[i], ya[i + 1]);
+        fma_x2(yb[i], yb[i + 1], a[i], a[i + 1], ba[i], ba[i + 1], yb[i], yb[i + 1]);
+        if constexpr (NORM != kNormNone) {
+          mul_x2(ya[i], ya[i + 1], ya[i], ya[i + 1], rs, rs);
+          mul_x2(yb[i], yb[i + 1], yb[i], yb[i + 1], rs, rs);
         }
       }
-      if (live) {
-        __half2 out[4];
-        pack<V>(ya, yb, out);
-        store_runs<V>(y, at_a, at_b, out);
-      }
-      y += step;
+#pragma unroll
+      for (int s = 0; s < kRuns; ++s)
+        if (live && has[s]) store_run<V>(xb, at_a[s], at_b[s], ya + s * kPer, yb + s * kPer);
     }
+    fence_proxy_async_smem();  // the lanes' writes, before the copy out reads them
+    __syncwarp();
+    if (lane == 0) {
+      __half* dst = (now.part ? p.y[1] + now.row * p.ys[1] : p.y[0] + now.row * p.ys[0]) + now.h0 * p.head_dim;
+      asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(reinterpret_cast<uint64_t>(dst)),
+                   "r"(smem_u32(buf)), "r"(uint32_t(now.heads * p.head_dim * 2))
+                   : "memory");
+      bulk_commit();
+      if (n + kBufs - 1 < count) {
+        bulk_wait_read<1>();  // the buffer of the job before has been read out
+        copy_in(n + kBufs - 1);
+      }
+    }
+    if (n + kBufs - 1 < count) advance(load);
   }
+  if (lane == 0) bulk_wait_all();
+}
+
+template <int V, int NORM>
+cudaError_t rope_launch_as(const RopeParams& p, cudaStream_t s) {
+  const size_t smem = rope_smem(p.head_dim, NORM == kNormNone ? 1 : 2);
+  static unsigned long long attr_set = 0;  // the attribute is per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = (dev >= 0 && dev < kMaxAttrDevices) ? 1ull << dev : 0ull;
+  if (!(attr_set & bit) || !bit) {
+    e = cudaFuncSetAttribute(rope_kernel<V, NORM>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(rope_smem(256, 2)));
+    if (e != cudaSuccess) return e;
+    attr_set |= bit;
+  }
+  const long long jobs = static_cast<long long>(p.rows) * p.chunks, most = 2ll * num_sms();
+  const long long blocks = (jobs + kRopeWarps - 1) / kRopeWarps;
+  return launch_pdl(rope_kernel<V, NORM>, dim3(unsigned(blocks < most ? blocks : most)), dim3(kRopeThreads), smem, s, p);
 }
 
 template <int V>
-cudaError_t rope_launch_v(const RopeParams& p, int norm, unsigned grid, cudaStream_t s) {
-  if (norm == kNormRms) return launch_pdl(rope_kernel<V, kNormRms>, dim3(grid), dim3(kRopeThreads), 0, s, p);
-  if (norm == kNormLayer) return launch_pdl(rope_kernel<V, kNormLayer>, dim3(grid), dim3(kRopeThreads), 0, s, p);
-  return launch_pdl(rope_kernel<V, kNormNone>, dim3(grid), dim3(kRopeThreads), 0, s, p);
+cudaError_t rope_launch_v(const RopeParams& p, int norm, cudaStream_t s) {
+  if (norm == kNormRms) return rope_launch_as<V, kNormRms>(p, s);
+  if (norm == kNormLayer) return rope_launch_as<V, kNormLayer>(p, s);
+  return rope_launch_as<V, kNormNone>(p, s);
 }
 
 sv_status rope_launch(RopeParams& p, const sv_rope_plan* plan, int norm, cudaStream_t s) {
@@ -283,27 +394,30 @@ sv_status rope_launch(RopeParams& p, const sv_rope_plan* plan, int norm, cudaStr
   p.n = plan ? plan->pairs : 4;  // (no plan: no rotated pair, runs as wide as they get)
   p.gain = plan ? plan->gain : 1.0f;
   p.inv_dim = 1.0f / float(D);
+  p.err = dev_err();
   for (int i = 0; i < (plan ? plan->pairs : 0); ++i) p.turns[i] = plan->turns[i];
-  p.lanes = D / 8;
+  p.lanes = (D + 15) / 16;
   p.fold = 1;
   while (2 * p.fold <= p.lanes) p.fold *= 2;
   p.slots = 32 / p.lanes;
-  const int trips = (p.heads + p.slots - 1) / p.slots;
-  // warps per row: one (a row's cosines and gammas are then loaded into registers once) where
-  // that fills the GPU with 32 warps an SM, more where rows are few
-  p.warps_row = 1;
-  while (p.warps_row < kRopeWarps && p.warps_row < trips &&
-         static_cast<long long>(p.rows) * p.warps_row < 32ll * num_sms())
-    p.warps_row *= 2;
-  const int rows_block = kRopeWarps / p.warps_row;
-  const long long blocks = (static_cast<long long>(p.rows) + rows_block - 1) / rows_block;
-  const unsigned grid = unsigned(blocks);
-  LaunchScope L(kKindOther, 0.0, 4.0 * p.rows * double(p.heads) * D, s);
+  // heads of a job: what a buffer holds, less where the GPU's warps would not all get one,
+  // down to the heads that a warp takes at a time
+  p.chunk = kBufBytes / (2 * D);
+  auto split = [&]() {
+    p.chunks0 = (p.heads[0] + p.chunk - 1) / p.chunk;
+    p.chunks = p.chunks0 + (p.heads[1] + p.chunk - 1) / p.chunk;
+  };
+  split();
+  while (p.chunk > p.slots && static_cast<long long>(p.rows) * p.chunks < 2ll * kRopeWarps * num_sms()) {
+    p.chunk = p.chunk / 2 > p.slots ? p.chunk / 2 : p.slots;
+    split();
+  }
+  LaunchScope L(kKindOther, 0.0, 4.0 * p.rows * (double(p.heads[0]) + p.heads[1]) * D, s);
   cudaError_t e;
-  if (plan && plan->layout == SV_ROPE_INTERLEAVED) e = rope_launch_v<0>(p, norm, grid, s);
-  else if (p.n % 4 == 0) e = rope_launch_v<4>(p, norm, grid, s);
-  else if (p.n % 2 == 0) e = rope_launch_v<2>(p, norm, grid, s);
-  else e = rope_launch_v<1>(p, norm, grid, s);
+  if (plan && plan->layout == SV_ROPE_INTERLEAVED) e = rope_launch_v<0>(p, norm, s);
+  else if (p.n % 4 == 0) e = rope_launch_v<4>(p, norm, s);
+  else if (p.n % 2 == 0) e = rope_launch_v<2>(p, norm, s);
+  else e = rope_launch_v<1>(p, norm, s);
   return e == cudaSuccess ? SV_OK : cuda_fail(e, "rope launch");
 }
 
@@ -404,7 +518,7 @@ sv_status sv_rope(const void* x, void* y, const int* positions, const sv_rope_pl
   p.y[0] = p.y[1] = static_cast<__half*>(y);
   p.xs[0] = p.xs[1] = x_stride;
   p.ys[0] = p.ys[1] = y_stride;
-  p.heads0 = p.heads = heads;
+  p.heads[0] = heads;
   p.pos = positions;
   p.rows = rows;
   p.head_dim = head_dim;
@@ -449,8 +563,8 @@ sv_status sv_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out
   p.xs[1] = k_stride;
   p.ys[0] = q_out_stride;
   p.ys[1] = k_out_stride;
-  p.heads0 = q_heads;
-  p.heads = q_heads + kv_heads;
+  p.heads[0] = q_heads;
+  p.heads[1] = kv_heads;
   p.pos = positions;
   p.rows = rows;
   p.head_dim = head_dim;
