@@ -301,99 +301,139 @@ __global__ void __maxnreg__(168)
     // The MMA issuer: S_0(0), S_1(0), then per key tile t of all items: O_0 += P_0(t) V_t,
     // S_0(t+1), O_1 += P_1(t) V_t, S_1(t+1). MMAs run in issue order, so S_w(t+1)
     // overwrites P_w(t) only after the product has read it, and the completion of
-    // S_w(t+1) also means that O_w holds the sum up to tile t.
+    // S_w(t+1) also means that O_w holds the sum up to tile t. One issuer for both tiles keeps
+    // them half a period apart, one's products under the other's softmax. The whole warp runs
+    // this, in step (every condition is a vote), and one elected lane issues: descriptors
+    // and addresses then stay in uniform registers, and an MMA takes few cycles to issue.
     constexpr uint32_t idesc_s = make_idesc(128, 128, 0, false);
     const uint32_t idesc_o = make_idesc(128, (p.D + 15) / 16 * 16, 0, true);
     const int steps = (p.D + 15) / 16;
-    auto stage = [&](int x) { return sbase + L::kOffKV + uint32_t(x % kStages) * kOp; };
-    auto issue_s = [&](int w, int qb, int x) {  // x: the key tile's place in the ring
-      const uint32_t qa = sbase + uint32_t(2 * qb + w) * kOp, ka = stage(x);
-      for (int kk = 0; kk < steps; ++kk) {
-        const uint32_t off = uint32_t(kk >> 2) * kBoxBytes + uint32_t(kk & 3) * 32;
-        mma_f16(tmem + uint32_t(128 * w), make_sdesc(qa + off, 16, 1024, 2), make_sdesc(ka + off, 16, 1024, 2),
-                idesc_s, kk > 0);
-      }
-      tc_commit(bar(kBarSFull + w));
+    const uint32_t lead = elect_one();
+    auto all = [](bool x) { return __all_sync(0xffffffffu, x) != 0; };
+    auto commit = [&](int b) { tc_commit_if(lead, bar(b)); };
+    auto wait = [&](int b, uint32_t parity) { return all(mbar_wait(bar(b), parity, abort_flag, p.err)); };
+    uint32_t kv = 0, kv_phase = 0;  // ring place and phase of the current key tile
+    auto place = [&](uint32_t ahead, uint32_t& st, uint32_t& ph) {
+      st = kv + ahead;
+      ph = kv_phase;
+      if (st >= kStages) st -= kStages, ph ^= 1;
     };
-    auto issue_pv = [&](int w, int x, bool first) {
-      const uint32_t va = stage(x);
+    auto wait_full = [&](uint32_t ahead) {
+      uint32_t st, ph;
+      place(ahead, st, ph);
+      return wait(kBarFull + int(st), ph);
+    };
+    auto issue_s = [&](int w, int qb, uint32_t st) {
+      uint64_t qd = make_sdesc(sbase + uint32_t(2 * qb + w) * kOp, 16, 1024, 2);
+      uint64_t kd = make_sdesc(sbase + L::kOffKV + st * kOp, 16, 1024, 2);
+      const uint32_t d = tmem + uint32_t(128 * w);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)  // 32 bytes of each row a step
+          if (4 * b + kk < steps)
+            mma_f16_if(lead, d, qd + uint64_t(b * (kBoxBytes >> 4) + 2 * kk), kd + uint64_t(b * (kBoxBytes >> 4) + 2 * kk),
+                       idesc_s, b + kk > 0);
+      }
+      commit(kBarSFull + w);
+    };
+    auto issue_pv = [&](int w, uint32_t st, uint32_t keep) {
+      const uint64_t vd = make_sdesc(sbase + L::kOffKV + st * kOp, kBoxBytes, 1024, 2);
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk)  // 16 keys a step: 8 TMEM columns of P, 16 rows of V
-        mma_f16_ts(tmem + uint32_t(256 + 128 * w), tmem + uint32_t(128 * w + 8 * kk),
-                   make_sdesc(va + kk * 2048, kBoxBytes, 1024, 2), idesc_o, !first || kk > 0);
+        mma_f16_ts_if(lead, tmem + uint32_t(256 + 128 * w), tmem + uint32_t(128 * w + 8 * kk), vd + uint64_t(kk * (2048 >> 4)),
+                      idesc_o, kk > 0 ? 1u : keep);
     };
-    auto wait_full = [&](int x) { return mbar_wait(bar(kBarFull + x % kStages), (x / kStages) & 1, abort_flag, p.err); };
-    if (lane == 0) {
-      int read = 0;  // items so far
-      // key tiles of the next item that has any (0: there is none); -1 after a time-out, or
-      // where it is not there yet and `wait` is false
-      auto next = [&](bool wait) -> int {
-        for (;;) {
-          if (wait ? !item_wait(read) : !mbar_test(bar(kBarItem + read % kItems), (read / kItems) & 1)) return -1;
-          const Item& r = items[read % kItems];
-          const int live = r.live, tiles = r.je - r.jb;
-          mbar_arrive(bar(kBarItemDone + read % kItems));
-          if (!live) return 0;
-          ++read;
-          if (tiles > 0) return tiles;
-        }
-      };
-      int tiles = next(true);
-      bool ok = tiles > 0 && wait_full(0) && mbar_wait(bar(kBarQFull), 0, abort_flag, p.err);
-      if (ok) {
-        tc_fence_after();
-        issue_s(0, 0, 0);
-        issue_s(1, 0, 0);
-        tc_commit(bar(kBarEmpty));
-        if (tiles == 1) tc_commit(bar(kBarQEmpty));
+    int read = 0;  // items so far
+    // key tiles of the next item that has any (0: there is none); -1 after a time-out, or
+    // where it is not there yet and `block` is false
+    auto next = [&](bool block) -> int {
+      for (;;) {
+        const int b = kBarItem + read % kItems, ph = (read / kItems) & 1;
+        if (block ? !wait(b, uint32_t(ph)) : !all(mbar_test(bar(b), uint32_t(ph)))) return -1;
+        const Item& r = items[read % kItems];
+        const int live = r.live, tiles = r.je - r.jb;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarItemDone + read % kItems));
+        __syncwarp();
+        if (!all(live)) return 0;
+        ++read;
+        if (all(tiles > 0)) return tiles;
       }
-      int x = 0, tt = 0;  // ring place of the current key tile, tiles so far
-      for (int n = 0; ok && tiles > 0; ++n) {
-        int more = 0;  // key tiles of the next item
-        for (int j = 0; ok && j < tiles; ++j, ++tt, x += 2) {
-          // ring: key tile at x, its values at x + 1, the next key tile at x + 2
-          const bool last = j + 1 == tiles;
-          const int qb = (last ? n + 1 : n) % kQBufs;
-          auto next_s = [&](int w) {
+    };
+    int tiles = next(true);
+    bool ok = all(tiles > 0) && wait_full(0) && wait(kBarQFull, 0);
+    if (ok) {
+      tc_fence_after();
+      issue_s(0, 0, 0);
+      issue_s(1, 0, 0);
+      commit(kBarEmpty);
+      if (all(tiles == 1)) commit(kBarQEmpty);
+    }
+    uint32_t tt = 0;  // parity of the tiles so far
+    int qb = 0, qph = 0;  // Q buffer and phase of the current item
+    while (ok && all(tiles > 0)) {
+      int more = 0;  // key tiles of the next item
+      const int qb_next = qb + 1 == kQBufs ? 0 : qb + 1, qph_next = qb + 1 == kQBufs ? qph ^ 1 : qph;
+      for (int j = 0; ok && all(j < tiles); ++j, tt ^= 1) {
+        // ring: key tile at 0, its values at 1, the next key tile at 2
+        const bool last = all(j + 1 == tiles);
+        uint32_t st_v, st_k, ph;
+        place(1, st_v, ph);
+        place(2, st_k, ph);
+        // S_w of the next key tile
+        auto next_s = [&](int w) {
+          if (last) {
             if (w == 0) {
-              ok = wait_full(x + 2) &&
-                   (!last || mbar_wait(bar(kBarQFull + qb), ((n + 1) / kQBufs) & 1, abort_flag, p.err));
+              ok = wait_full(2) && wait(kBarQFull + qb_next, uint32_t(qph_next));
               if (!ok) return;
               tc_fence_after();
             }
-            issue_s(w, qb, x + 2);
-            if (w == 1) {
-              tc_commit(bar(kBarEmpty + (x + 2) % kStages));
-              // the last S product of its item has read Q
-              if (last ? more == 1 : j + 2 == tiles) tc_commit(bar(kBarQEmpty + qb));
-            }
-          };
-          bool late = false;  // the next item was not there for S_0
-          for (int w = 0; w < 2 && ok; ++w) {
-            ok = mbar_wait(bar(kBarPFull + w), tt & 1, abort_flag, p.err) && (w == 1 || wait_full(x + 1));
-            if (!ok) break;
-            tc_fence_after();
-            issue_pv(w, x + 1, j == 0);
-            if (w == 1) tc_commit(bar(kBarEmpty + (x + 1) % kStages));
-            if (last) {
-              tc_commit(bar(kBarOFull + w));
-              // The copy warp may need this item's slot for the next one (behind items without
-              // keys): both groups' O must be on their way before the issuer waits for it.
-              if (w == 0) late = (more = next(false)) < 0;
-              else if (late && (more = next(true)) < 0) ok = false;
-              if (!ok || more == 0 || (w == 0 && late)) continue;
-              if (late) next_s(0);
-            }
-            if (ok) next_s(w);
+            issue_s(w, qb_next, st_k);
+          } else {
+            issue_s(w, qb, st_k);
           }
+          if (w == 1) {
+            commit(kBarEmpty + int(st_k));
+            // the last S product of its item has read Q
+            if (last ? all(more == 1) : all(j + 2 == tiles)) commit(kBarQEmpty + (last ? qb_next : qb));
+          }
+        };
+        // (the copies are waited for before P, which is what the products really wait for)
+        ok = wait_full(1) && (last || wait_full(2));
+        bool late = false;  // the next item was not there for S_0
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          ok = ok && wait(kBarPFull + w, tt);
+          if (!ok) break;
+          tc_fence_after();
+          issue_pv(w, st_v, j > 0);
+          if (last) {
+            commit(kBarOFull + w);
+            // The copy warp may need this item's slot for the next one (behind items without
+            // keys): both tiles' O must be on their way before the issuer waits for it.
+            if (w == 0) late = all((more = next(false)) < 0);
+            else if (late) ok = !all((more = next(true)) < 0);
+            if (!ok) break;
+            if (all(more != 0) && !(w == 0 && late)) {
+              if (late) next_s(0);
+              if (ok) next_s(w);
+            }
+          } else {
+            next_s(w);
+          }
+          if (w == 1) commit(kBarEmpty + int(st_v));
         }
-        tiles = more;
+        kv += 2;
+        if (kv >= kStages) kv -= kStages, kv_phase ^= 1;
       }
+      tiles = more;
+      qb = qb_next;
+      qph = qph_next;
     }
-    if (lane == 0) {
-      tc_commit(bar(kBarDrain));
-      mbar_wait_bounded(bar(kBarDrain), 0, p.err);
-    }
+    commit(kBarDrain);
+    __syncwarp();
+    mbar_wait_bounded(bar(kBarDrain), 0, p.err);
   } else {
     const int w = (warp - 2) >> 2;  // softmax group
     const int sub = warp & 3;       // TMEM lane quarter
