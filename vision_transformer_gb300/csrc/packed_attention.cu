@@ -82,41 +82,72 @@ static_assert(kOffItems + kItems * sizeof(Item) <= kBarBytes, "barrier area");
 
 // The items in order, worked out by the copy warp from the documents' lengths: a
 // chunk of 32 documents at a time, one per lane, with their item counts summed by shuffles.
-// Within a document: key heads, then pairs of tiles from the last (longest) on, then parts
-// of the key range. Where the launch has less work than its CTAs could share evenly, a
+// Within a document: pairs of tiles from the last (longest) on, then key heads, then parts of
+// the key range. Where the launch has less work than its CTAs could share evenly, a
 // document's key range is divided into parts of at most `chunk` tiles, chunk = the launch's
 // key tiles per CTA: then a launch has at most 2 x grid parts in divided ranges, since a
 // range of n > chunk tiles has ceil(n / chunk) <= 2 n / chunk parts.
 class Schedule {
  public:
   __device__ __forceinline__ Schedule(const Params& p, int lane) : p_(p), lane_(lane), docs_(p.docs) {
+    chunk_ = 0x7fffffff;
     long long work = 0;
     bool bad = false;
-    for (int d0 = 0; d0 < p.docs; d0 += 32) {
-      load(d0);
-      bad |= bad_;
-      work += static_cast<long long>(pairs_) * tiles_;
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {  // the work, then the items that it makes
+      int items = 0;
+#pragma unroll 1
+      for (int d0 = 0; d0 < docs_; d0 += 32) {
+        load(d0);
+        bad |= bad_;
+        work += static_cast<long long>(pairs_) * tiles_;
+        items += count_;
+      }
+#pragma unroll 1
+      for (int o = 16; o; o >>= 1) {
+        work += __shfl_xor_sync(0xffffffffu, work, o);
+        items += __shfl_xor_sync(0xffffffffu, items, o);
+      }
+      items_ = items;
+      if (pass == 0) {
+        // offsets that decrease or leave [0, total]: reported, and nothing is computed, since
+        // the bounds on items and parts hold for documents that do not overlap
+        if (__any_sync(0xffffffffu, bad)) {
+          if (lane == 0) atomicOr(p.err, kDevErrOffsets);
+          docs_ = 0;
+        }
+        if (!p.counters) break;  // nothing is divided, and no tickets are drawn
+        const long long share = (work * p.hk + int(gridDim.x) - 1) / int(gridDim.x);
+        chunk_ = int(min(max(share, static_cast<long long>(kMinSplit)), 0x7fffffffll));
+      }
     }
-    for (int o = 16; o; o >>= 1) work += __shfl_xor_sync(0xffffffffu, work, o);
-    const long long share = (work * p.hk + int(gridDim.x) - 1) / int(gridDim.x);
-    chunk_ = p.counters ? int(min(max(share, static_cast<long long>(kMinSplit)), 0x7fffffffll)) : 0x7fffffff;
-    // offsets that decrease or leave [0, total]: reported, and nothing is computed, since
-    // the bounds on items and parts hold for documents that do not overlap
-    if (__any_sync(0xffffffffu, bad)) {
-      if (lane == 0) atomicOr(p.err, kDevErrOffsets);
-      docs_ = 0;
-    }
-    if (p.docs > 32 || docs_ == 0) load(0);
-    open(0);
+  }
+  // The CTA's first item is its own number, the others go to whoever is free, by a ticket from
+  // the workspace: CTAs draw until they are refused, `items` tickets in all, and the counter
+  // is back at 0. Without a workspace every CTA takes every gridDim-th item.
+  __device__ __forceinline__ int after(int it) const {
+    if (!p_.counters) return it + int(gridDim.x);
+    unsigned t = 0;
+    if (lane_ == 0) t = atomicInc(p_.counters + kTicket, unsigned(items_ - 1));
+    return int(gridDim.x) + int(__shfl_sync(0xffffffffu, t, 0));
   }
   // Item number `it` (increasing from call to call); false behind the last.
   __device__ __forceinline__ bool get(int it, Item& r) {
     while (it >= base_ + total_) {
-      if (d0_ + 32 >= docs_) return false;
+      d0_ += 32;
+      if (d0_ >= docs_) return false;
       base_ += total_;
       slot_base_ += slot_total_;
-      load(d0_ + 32);
-      open(d0_ + 32);
+      load(d0_);
+      incl_ = count_;
+      slot_incl_ = splits_ > 1 ? count_ : 0;
+#pragma unroll 1
+      for (int o = 1; o < 32; o <<= 1) {
+        const int a = __shfl_up_sync(0xffffffffu, incl_, o), b = __shfl_up_sync(0xffffffffu, slot_incl_, o);
+        if (lane_ >= o) incl_ += a, slot_incl_ += b;
+      }
+      total_ = __shfl_sync(0xffffffffu, incl_, 31);
+      slot_total_ = __shfl_sync(0xffffffffu, slot_incl_, 31);
     }
     const int at = it - base_;
     const int src = __ffs(__ballot_sync(0xffffffffu, incl_ > at)) - 1;
@@ -127,8 +158,9 @@ class Schedule {
     r.splits = splits;
     r.split = k % splits;
     k /= splits;
-    r.kvh = k / pairs;
-    const int pair = pairs - 1 - (k - r.kvh * pairs);
+    const int back = k / p_.hk;
+    r.kvh = k - back * p_.hk;
+    const int pair = pairs - 1 - back;
     const int lq = of(doc_.lq);
     r.lk = of(doc_.lk);
     r.k0 = of(doc_.k0);
@@ -148,28 +180,138 @@ class Schedule {
   __device__ __forceinline__ void load(int d0) {
     bad_ = !document(p_, d0 + lane_, docs_, doc_);
     pairs_ = (doc_.lq + 2 * p_.qt - 1) / (2 * p_.qt);
-    tiles_ = (limit_of(p_.causal, doc_.lk - 1, doc_.lk, doc_.prefix) + kTile - 1) / kTile;  // of the last query
-  }
-  __device__ __forceinline__ void open(int d0) {
-    d0_ = d0;
+    tiles_ = (doc_.lk + kTile - 1) / kTile;  // of the last query
     splits_ = tiles_ > chunk_ ? (tiles_ + chunk_ - 1) / chunk_ : 1;
     count_ = pairs_ * p_.hk * splits_;
-    incl_ = count_;
-    slot_incl_ = splits_ > 1 ? count_ : 0;
-    for (int o = 1; o < 32; o <<= 1) {
-      const int a = __shfl_up_sync(0xffffffffu, incl_, o), b = __shfl_up_sync(0xffffffffu, slot_incl_, o);
-      if (lane_ >= o) incl_ += a, slot_incl_ += b;
-    }
-    total_ = __shfl_sync(0xffffffffu, incl_, 31);
-    slot_total_ = __shfl_sync(0xffffffffu, slot_incl_, 31);
   }
   const Params& p_;
   int lane_, docs_, chunk_;
   bool bad_;
-  int d0_ = 0, base_ = 0, total_ = 0, slot_base_ = 0, slot_total_ = 0;
+  int items_ = 0;
+  int d0_ = -32, base_ = 0, total_ = 0, slot_base_ = 0, slot_total_ = 0;
   Document doc_;  // this lane's
   int pairs_, tiles_, splits_, count_, incl_, slot_incl_;
 };
+
+// Adds the parts of a divided range to row r of tile w (query index i of the item, -1 none),
+// once this warp is the last of the range's CTAs to arrive: in the order of the parts, so that
+// the result does not depend on who is last.
+// A wait whose long form is one function for all of the kernel's waits: inlined, the waits alone
+// were a sixth of the code, and code that runs once an item then came from beyond the
+// instruction caches.
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int* abort, int* err) {
+  return mbar_wait(bar, parity, abort, err);
+}
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort, int* err) {
+  return mbar_try_wait(bar, parity) || wait_long(bar, parity, abort, err);
+}
+
+__device__ __noinline__ void join_parts(const Params& p, const Item& it, long long out_to, int w, int r) {
+  const int Dn = (p.D + 15) / 16 * 16;
+  __threadfence();
+  __syncwarp();
+  unsigned seen = 0;
+  const int first = it.slot - it.split;
+  if ((r & 31) == 0)  // counts 0 .. splits - 1 and starts again at 0
+    seen = atomicInc(p.counters + size_t(first) * 8 + (w * 4 + (r >> 5)), unsigned(it.splits - 1));
+  seen = __shfl_sync(0xffffffffu, seen, 0);
+  if (seen != unsigned(it.splits - 1)) return;
+  __threadfence();
+  if (out_to < 0) return;
+  const float* base = p.partial + (size_t(first) * 2 + w) * size_t(Dn + 2) * kTile + r;
+  const size_t stride = size_t(2) * size_t(Dn + 2) * kTile;  // to the next part
+  float mx = -INFINITY, sum = 0.0f;
+  for (int s = 0; s < it.splits; ++s) mx = fmaxf(mx, __ldcg(base + s * stride));
+  const float ref = mx == -INFINITY ? 0.0f : mx;
+  for (int s = 0; s < it.splits; ++s) sum += ex2(__ldcg(base + s * stride) - ref) * __ldcg(base + s * stride + kTile);
+  const int i = w * p.qt + r / p.group;
+  const bool none = limit_of(p.causal, it.at + i, it.lk, it.prefix) == 0;
+  const float inv = 1.0f / sum;
+  for (int c = 0; c < p.D; c += 8) {
+    float y[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    for (int s = 0; s < it.splits; ++s) {
+      const float* b = base + s * stride;
+      const float pm = __ldcg(b);
+      if (pm == -INFINITY) continue;  // no key of this part is visible
+      const float f = ex2(pm - ref);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = fmaf(f, __ldcg(b + size_t(2 + c + e) * kTile), y[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = none ? 0.0f : y[e] * inv;
+    store8(p, size_t(out_to) + c, y);
+  }
+}
+
+// Row r of tile w of a divided range's part: O, m and l to the workspace (or, not finite, again
+// from the visible keys), then the join.
+enum { kNothing = 1, kPart = 2, kAgain = 4 };  // the row sees no key; its item is a part; O is not finite
+__device__ __noinline__ void write_special(const Params& p, const Item& it, float m, float l, long long out_to, int how,
+                                           int w, int r) {
+  const int Dn = (p.D + 15) / 16 * 16;
+  const int i = w * p.qt + r / p.group, head = it.kvh * p.group + r % p.group;
+  const int lim = out_to < 0 ? 0 : limit_of(p.causal, it.at + i, it.lk, it.prefix);
+  float* pb = p.partial + (size_t(it.slot) * 2 + w) * size_t(Dn + 2) * kTile + r;
+  if (how & kAgain) {
+    float acc[128];
+    row_again(p, p.q + static_cast<long long>(it.q0 + i) * p.qs + head * p.D, p.k + it.k0 * p.ks + it.kvh * p.D,
+              p.v + it.k0 * p.vs + it.kvh * p.D, it.jb * kTile, min(lim, it.je * kTile), it.at + i,
+              p.slopes ? __ldg(p.slopes + head) : 0.0f, acc, m, l);
+    for (int c = 0; c < p.D; c += 8) {
+      float y[8];
+      for (int e = 0; e < 8; ++e) y[e] = how & kPart ? acc[c + e] : acc[c + e] / l;
+      if (how & kPart)
+        for (int e = 0; e < 8; ++e) __stcg(pb + size_t(2 + c + e) * kTile, y[e]);
+      else
+        store8(p, size_t(out_to) + c, y);
+    }
+  }
+  __syncwarp();
+  if (how & kPart) {
+    const bool some = lim > it.jb * kTile;
+    __stcg(pb, some ? m : -INFINITY);
+    __stcg(pb + kTile, some ? l : 0.0f);
+    join_parts(p, it, out_to, w, r);
+  }
+}
+
+// Row r of tile w of an item, once its last P V has finished: O / l to o, or O, m and l as a part
+// of a divided range.
+__device__ __forceinline__ void write_rows(const Params& p, const Item& it, uint32_t o_tm, float m, float l,
+                                           long long out_to, int how, int w, int r) {
+  const int Dn = (p.D + 15) / 16 * 16;
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(l));
+  if (how & kPart) inv = 1.0f;
+  float bad = 0.0f;  // NaN once a value of the row is not finite
+  float* pb = p.partial + (size_t(it.slot) * 2 + w) * size_t(Dn + 2) * kTile + r;
+#pragma unroll 1
+  for (int c = 0; c < p.D; c += 32) {
+    uint32_t o[32];
+    tmem_ld32(o_tm + uint32_t(c), o);
+    tmem_ld_wait(o);
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {  // eight columns at a time
+      if (c + 8 * g < p.D && out_to >= 0) {
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          y[e] = __uint_as_float(o[8 * g + e]) * inv;
+          bad = fmaf(y[e], 0.0f, bad);
+          if (how & kNothing) y[e] = 0.0f;
+        }
+        if (!(how & kPart)) {
+          store8(p, size_t(out_to) + c + 8 * g, y);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) __stcg(pb + size_t(2 + c + 8 * g + e) * kTile, y[e]);
+        }
+      }
+    }
+  }
+  if (out_to >= 0 && !(how & kNothing) && bad != 0.0f) how |= kAgain;
+  if (__any_sync(0xffffffffu, how & (kPart | kAgain))) write_special(p, it, m, l, out_to, how, w, r);
+}
 
 template <int NB, bool CAP, bool BIAS>
 // 10 warps: three share each of two SM sub-partitions, so a thread may hold at most
@@ -222,7 +364,7 @@ __global__ void __maxnreg__(168)
   pdl_wait();  // q, k, v, offsets, prefix and slopes may be written by the previous kernel
   Item* items = reinterpret_cast<Item*>(smem + L::kOffBar + kOffItems);
   auto item_wait = [&](int n) {
-    return mbar_wait(bar(kBarItem + n % kItems), (n / kItems) & 1, abort_flag, p.err);
+    return wait_bar(bar(kBarItem + n % kItems), (n / kItems) & 1, abort_flag, p.err);
   };
 
   if (warp == 0) {
@@ -243,10 +385,12 @@ __global__ void __maxnreg__(168)
     int told = 0;      // items written for the other warps
     // The next item, written for the other warps. (It waits for the item four before to be
     // written out, so it must not come before copies that this depends on.)
+    int number = int(blockIdx.x);  // of the next item
     auto tell = [&](Item& r) -> int {
-      r.live = sched.get(int(blockIdx.x) + told * int(gridDim.x), r);
+      if (told > 0) number = sched.after(number);
+      r.live = sched.get(number, r);
       const int slot = told % kItems;
-      int ok = mbar_wait(bar(kBarItemDone + slot), ((told / kItems) & 1) ^ 1, abort_flag, p.err);
+      int ok = wait_bar(bar(kBarItemDone + slot), ((told / kItems) & 1) ^ 1, abort_flag, p.err);
       ok = __all_sync(0xffffffffu, ok);
       if (ok && lane == 0) {
         items[slot] = r;
@@ -263,7 +407,7 @@ __global__ void __maxnreg__(168)
         auto kv = [&](const CUtensorMap& map, int j) -> bool {
           const int st = t % kStages;
           const uint32_t ph = (t / kStages) & 1;
-          if (!mbar_wait(bar(kBarEmpty + st), ph ^ 1, abort_flag, p.err)) return false;
+          if (!wait_bar(bar(kBarEmpty + st), ph ^ 1, abort_flag, p.err)) return false;
           mbar_arrive_expect_tx(bar(kBarFull + st), kOp);
           for (int b = 0; b < NB; ++b)
             tma_load_3d(sbase + L::kOffKV + st * kOp + b * kBoxBytes, &map, bar(kBarFull + st), 64 * b, it.kvh,
@@ -272,22 +416,22 @@ __global__ void __maxnreg__(168)
           ++t;
           return true;
         };
-        ok = kv(tk, it.jb);
-        if (ok) {
-          const int qb = n % kQBufs;
-          const uint32_t ph = (n / kQBufs) & 1;
-          if ((ok = mbar_wait(bar(kBarQEmpty + qb), ph ^ 1, abort_flag, p.err))) {
-            mbar_arrive_expect_tx(bar(kBarQFull + qb), q_bytes);
-            for (int w = 0; w < 2; ++w)
-              for (int b = 0; b < NB; ++b)
-                tma_load_3d(sbase + (2 * qb + w) * kOp + b * kBoxBytes, &tq, bar(kBarQFull + qb), 64 * b,
-                            it.kvh * p.group, it.q0 + w * p.qt);
-            note(qb, ph);
+#pragma unroll 1
+        for (int x = 0; ok && x < 2 * (it.je - it.jb); ++x) {  // a key tile, its values, the next key tile, ...
+          ok = kv(x & 1 ? tv : tk, it.jb + (x >> 1));
+          if (ok && x == 0) {
+            const int qb = n % kQBufs;
+            const uint32_t ph = (n / kQBufs) & 1;
+            if ((ok = wait_bar(bar(kBarQEmpty + qb), ph ^ 1, abort_flag, p.err))) {
+              mbar_arrive_expect_tx(bar(kBarQFull + qb), q_bytes);
+#pragma unroll 1
+              for (int w = 0; w < 2; ++w)
+                for (int b = 0; b < NB; ++b)
+                  tma_load_3d(sbase + (2 * qb + w) * kOp + b * kBoxBytes, &tq, bar(kBarQFull + qb), 64 * b,
+                              it.kvh * p.group, it.q0 + w * p.qt);
+              note(qb, ph);
+            }
           }
-        }
-        for (int j = it.jb; ok && j < it.je; ++j) {
-          ok = kv(tv, j);
-          if (ok && j + 1 < it.je) ok = kv(tk, j + 1);
         }
       }
       ++n;
@@ -311,7 +455,7 @@ __global__ void __maxnreg__(168)
     const uint32_t lead = elect_one();
     auto all = [](bool x) { return __all_sync(0xffffffffu, x) != 0; };
     auto commit = [&](int b) { tc_commit_if(lead, bar(b)); };
-    auto wait = [&](int b, uint32_t parity) { return all(mbar_wait(bar(b), parity, abort_flag, p.err)); };
+    auto wait = [&](int b, uint32_t parity) { return all(wait_bar(bar(b), parity, abort_flag, p.err)); };
     uint32_t kv = 0, kv_phase = 0;  // ring place and phase of the current key tile
     auto place = [&](uint32_t ahead, uint32_t& st, uint32_t& ph) {
       st = kv + ahead;
@@ -365,8 +509,8 @@ __global__ void __maxnreg__(168)
     bool ok = all(tiles > 0) && wait_full(0) && wait(kBarQFull, 0);
     if (ok) {
       tc_fence_after();
-      issue_s(0, 0, 0);
-      issue_s(1, 0, 0);
+#pragma unroll 1
+      for (int w = 0; w < 2; ++w) issue_s(w, 0, 0);
       commit(kBarEmpty);
       if (all(tiles == 1)) commit(kBarQEmpty);
     }
@@ -381,46 +525,40 @@ __global__ void __maxnreg__(168)
         uint32_t st_v, st_k, ph;
         place(1, st_v, ph);
         place(2, st_k, ph);
-        // S_w of the next key tile
-        auto next_s = [&](int w) {
-          if (last) {
-            if (w == 0) {
-              ok = wait_full(2) && wait(kBarQFull + qb_next, uint32_t(qph_next));
-              if (!ok) return;
-              tc_fence_after();
-            }
-            issue_s(w, qb_next, st_k);
-          } else {
-            issue_s(w, qb, st_k);
-          }
-          if (w == 1) {
-            commit(kBarEmpty + int(st_k));
-            // the last S product of its item has read Q
-            if (last ? all(more == 1) : all(j + 2 == tiles)) commit(kBarQEmpty + (last ? qb_next : qb));
-          }
-        };
         // (the copies are waited for before P, which is what the products really wait for)
         ok = wait_full(1) && (last || wait_full(2));
         bool late = false;  // the next item was not there for S_0
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          ok = ok && wait(kBarPFull + w, tt);
-          if (!ok) break;
+#pragma unroll 1
+        for (int w = 0; w < 2 && ok; ++w) {
+          if (!(ok = wait(kBarPFull + w, tt))) break;
           tc_fence_after();
           issue_pv(w, st_v, j > 0);
+          int first = w;  // S products to issue: tiles first .. w
           if (last) {
             commit(kBarOFull + w);
             // The copy warp may need this item's slot for the next one (behind items without
             // keys): both tiles' O must be on their way before the issuer waits for it.
-            if (w == 0) late = all((more = next(false)) < 0);
-            else if (late) ok = !all((more = next(true)) < 0);
-            if (!ok) break;
-            if (all(more != 0) && !(w == 0 && late)) {
-              if (late) next_s(0);
-              if (ok) next_s(w);
+            if (w == 0 || late) {
+              more = next(w == 1);
+              if (w == 1) first = 0;
+              late = all(more < 0);
+              if (late && w == 1) ok = false;
             }
-          } else {
-            next_s(w);
+            if (late || all(more == 0)) first = 2;
+            if (first == 0) {
+              ok = wait_full(2) && wait(kBarQFull + qb_next, uint32_t(qph_next));
+              tc_fence_after();
+            }
+          }
+          const int q = last ? qb_next : qb;
+#pragma unroll 1
+          for (int s = first; s <= w && ok; ++s) {
+            issue_s(s, q, st_k);
+            if (s == 1) {
+              commit(kBarEmpty + int(st_k));
+              // the last S product of its item has read Q
+              if (last ? all(more == 1) : all(j + 2 == tiles)) commit(kBarQEmpty + q);
+            }
           }
           if (w == 1) commit(kBarEmpty + int(st_v));
         }
@@ -455,97 +593,9 @@ __global__ void __maxnreg__(168)
     };
     float m = -INFINITY, l = 0.0f;
 
-    // Adds the parts of a divided range, once this warp is the last of the range's CTAs to
-    // arrive: in the order of the parts, so that the result does not depend on who is last.
-    auto join = [&](const Item& it) {
-      __threadfence();
-      __syncwarp();
-      unsigned seen = 0;
-      const int first = it.slot - it.split;
-      if (lane == 0)  // counts 0 .. splits - 1 and starts again at 0
-        seen = atomicInc(p.counters + size_t(first) * 8 + (w * 4 + sub), unsigned(it.splits - 1));
-      seen = __shfl_sync(0xffffffffu, seen, 0);
-      if (seen != unsigned(it.splits - 1)) return;
-      __threadfence();
-      const int i = query(it);
-      const float* base = p.partial + (size_t(first) * 2 + w) * size_t(Dn + 2) * kTile + r;
-      const size_t stride = size_t(2) * size_t(Dn + 2) * kTile;  // to the next part
-      float mx = -INFINITY, sum = 0.0f;
-      for (int s = 0; s < it.splits; ++s) mx = fmaxf(mx, __ldcg(base + s * stride));
-      const float ref = mx == -INFINITY ? 0.0f : mx;
-      for (int s = 0; s < it.splits; ++s) sum += ex2(__ldcg(base + s * stride) - ref) * __ldcg(base + s * stride + kTile);
-      if (i < 0) return;
-      const bool none = limit_of(p.causal, it.at + i, it.lk, it.prefix) == 0;
-      const float inv = 1.0f / sum;
-      const size_t at = out_at(it, i);
-      for (int c = 0; c < p.D; c += 8) {
-        float y[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-        for (int s = 0; s < it.splits; ++s) {
-          const float* b = base + s * stride;
-          const float pm = __ldcg(b);
-          if (pm == -INFINITY) continue;  // no key of this part is visible
-          const float f = ex2(pm - ref);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = fmaf(f, __ldcg(b + size_t(2 + c + e) * kTile), y[e]);
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = none ? 0.0f : y[e] * inv;
-        store8(p, at + c, y);
-      }
-    };
-
-    // The item's rows once its last P V has finished: O / l as the output, or O, m and l as
-    // a part of a divided range.
-    auto write_item = [&](const Item& it) {
-      const int i = query(it);
-      const bool part = it.splits > 1;
-      float* pb = p.partial + (size_t(it.slot) * 2 + w) * size_t(Dn + 2) * kTile + r;
-      const int lim = i < 0 ? 0 : limit_of(p.causal, it.at + i, it.lk, it.prefix);
-      const float inv = part ? 1.0f : 1.0f / l;
-      const size_t at = i < 0 ? 0 : out_at(it, i);
-      float bad = 0.0f;  // NaN once a value of the row is not finite
-      for (int c = 0; c < p.D; c += 8) {
-        uint32_t o[8];
-        tmem_ld8(o_tm + uint32_t(c), o);
-        tmem_ld_wait();
-#pragma unroll
-        for (int e = 0; e < 8; ++e) asm volatile("" : "+r"(o[e]));  // no use before the wait
-        float y[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          y[e] = __uint_as_float(o[e]) * inv;
-          if (lim == 0) y[e] = 0.0f;
-          bad = fmaf(y[e], 0.0f, bad);
-        }
-        if (i < 0) continue;
-        if (part) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) __stcg(pb + size_t(2 + c + e) * kTile, y[e]);
-        } else {
-          store8(p, at + c, y);
-        }
-      }
-      if (i >= 0 && bad != 0.0f) {
-        float acc[128];
-        const __half* q = p.q + static_cast<long long>(it.q0 + i) * p.qs + (it.kvh * p.group + head) * p.D;
-        row_again(p, q, p.k + it.k0 * p.ks + it.kvh * p.D, p.v + it.k0 * p.vs + it.kvh * p.D, it.jb * kTile,
-                  min(lim, it.je * kTile), it.at + i, p.slopes ? __ldg(p.slopes + it.kvh * p.group + head) : 0.0f, acc,
-                  m, l);
-        for (int c = 0; c < p.D; c += 8) {
-          float y[8];
-          for (int e = 0; e < 8; ++e) y[e] = part ? acc[c + e] : acc[c + e] / l;
-          if (part)
-            for (int e = 0; e < 8; ++e) __stcg(pb + size_t(2 + c + e) * kTile, y[e]);
-          else
-            store8(p, at + c, y);
-        }
-      }
-      if (part) {
-        __stcg(pb, lim > it.jb * kTile ? m : -INFINITY);
-        __stcg(pb + kTile, lim > it.jb * kTile ? l : 0.0f);
-        join(it);
-      }
-    };
+    // The pending item's row: where it goes in o (-1: the row holds no query), and what to do.
+    long long out_to = -1;
+    int out_how = 0;
     // An item without keys: zeros, or an empty part.
     auto write_none = [&](const Item& it) {
       const int i = query(it);
@@ -553,7 +603,7 @@ __global__ void __maxnreg__(168)
         float* pb = p.partial + (size_t(it.slot) * 2 + w) * size_t(Dn + 2) * kTile + r;
         __stcg(pb, -INFINITY);
         __stcg(pb + kTile, 0.0f);
-        join(it);
+        join_parts(p, it, i < 0 ? -1 : static_cast<long long>(out_at(it, i)), w, r);
       } else if (i >= 0) {
         const float y[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
         for (int c = 0; c < p.D; c += 8) store8(p, out_at(it, i) + c, y);
@@ -567,16 +617,6 @@ __global__ void __maxnreg__(168)
     };
     int pending = -1;  // the item whose rows are not written yet
     int full = 0;      // items with keys so far
-    // O of the pending item is final: its rows are written
-    auto flush = [&]() -> bool {
-      if (pending < 0) return true;
-      if (!__all_sync(0xffffffffu, mbar_wait(bar(kBarOFull + w), (full - 1) & 1, abort_flag, p.err))) return false;
-      tc_fence_after();
-      write_item(items[pending % kItems]);
-      done(pending);
-      pending = -1;
-      return true;
-    };
     bool ok = true;
     int t = 0;  // S tiles so far
     for (int n = 0;; ++n) {
@@ -585,10 +625,16 @@ __global__ void __maxnreg__(168)
         break;
       }
       const Item& it = items[n % kItems];
+      if (pending >= 0) {  // the item before: its rows go out as soon as O is final
+        if (!__all_sync(0xffffffffu, wait_bar(bar(kBarOFull + w), (full - 1) & 1, abort_flag, p.err))) break;
+        tc_fence_after();
+        write_rows(p, items[pending % kItems], o_tm, m, l, out_to, out_how, w, r);
+        done(pending);
+        pending = -1;
+      }
       if (!it.live) break;
       const int jb = it.jb, je = it.je;
-      if (jb >= je) {  // (the pending item's slot may be the one that the copy warp waits for)
-        if (!(ok = flush())) break;
+      if (jb >= je) {
         write_none(it);
         done(n);
         continue;
@@ -597,19 +643,18 @@ __global__ void __maxnreg__(168)
       const int at = it.at + i;
       // rows without a query are computed like the others and never stored
       const int lim = i < 0 ? 0x7fffffff : limit_of(p.causal, at, it.lk, it.prefix);
+      out_to = i < 0 ? -1 : static_cast<long long>(out_at(it, i));
+      out_how = (lim == 0 ? kNothing : 0) | (it.splits > 1 ? kPart : 0);
       const float slope2 = BIAS && i >= 0 ? __ldg(p.slopes + it.kvh * p.group + head) * kLog2e : 0.0f;
+      m = -INFINITY;
+      l = 0.0f;
       for (int j = jb; j < je; ++j, ++t) {
         // S(t) has finished, and with it every P V product of the group before it
-        if (!__all_sync(0xffffffffu, mbar_wait(bar(kBarSFull + w), t & 1, abort_flag, p.err))) {
+        if (!__all_sync(0xffffffffu, wait_bar(bar(kBarSFull + w), t & 1, abort_flag, p.err))) {
           ok = false;
           break;
         }
         tc_fence_after();
-        if (j == jb) {
-          if (!(ok = flush())) break;
-          m = -INFINITY;
-          l = 0.0f;
-        }
         float sv[4][32];
         uint32_t(&su)[4][32] = reinterpret_cast<uint32_t(&)[4][32]>(sv);
         tmem_ld32(s_tm, su[0]);
@@ -698,7 +743,6 @@ __global__ void __maxnreg__(168)
       pending = n;
       ++full;
     }
-    if (ok) flush();
     tmem_ld_wait();
     tmem_st_wait();
   }

@@ -12,7 +12,8 @@ namespace packed {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMaxSms = 152;  // SMs that a launch uses at most (the workspace is sized by it)
 // Workspace: counters of arrivals first (zero before and after every call), then partial results.
-constexpr size_t kCounterBytes = size_t(2 * kMaxSms) * 8 * sizeof(unsigned);
+constexpr int kTicket = 2 * kMaxSms * 8;  // the next item to hand out, behind the arrivals
+constexpr size_t kCounterBytes = (size_t(kTicket) + 16) * sizeof(unsigned);
 
 // The reference exponent of a row is set kHead below a tile's maximum when that maximum is
 // more than kSlack above it: P <= 2^15 stays finite in F16, small probabilities stay above
@@ -76,22 +77,26 @@ __device__ __forceinline__ float capped(float x, float c) {
   return fmaf(-2.0f * c, r, c);
 }
 
-// Eight values of an output row.
-__device__ __forceinline__ void store8(const Params& p, size_t at, const float* y) {
-  if (p.out_e4m3) {
+// Eight values in the output's type at `to`.
+__device__ __forceinline__ void put8(int e4m3, uint8_t* to, const float* y) {
+  if (e4m3) {
     uint2 w;
     __nv_fp8x2_storage_t* h = reinterpret_cast<__nv_fp8x2_storage_t*>(&w);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       h[i] = __nv_cvt_float2_to_fp8x2(make_float2(16.0f * y[2 * i], 16.0f * y[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
-    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.o) + at) = w;
+    *reinterpret_cast<uint2*>(to) = w;
   } else {
     uint4 w;
     __half2* h = reinterpret_cast<__half2*>(&w);
 #pragma unroll
     for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(y[2 * i], y[2 * i + 1]);
-    *reinterpret_cast<uint4*>(static_cast<__half*>(p.o) + at) = w;
+    *reinterpret_cast<uint4*>(to) = w;
   }
+}
+// Eight values of an output row, `at` values into o.
+__device__ __forceinline__ void store8(const Params& p, size_t at, const float* y) {
+  put8(p.out_e4m3, static_cast<uint8_t*>(p.o) + (p.out_e4m3 ? at : 2 * at), y);
 }
 
 // A row whose tensor-core result is not finite, again from the visible keys alone: a tile's
