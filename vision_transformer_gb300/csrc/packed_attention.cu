@@ -117,8 +117,9 @@ class Schedule {
           docs_ = 0;
         }
         if (!p.counters) break;  // nothing is divided, and no tickets are drawn
-        const long long share = (work * p.hk + int(gridDim.x) - 1) / int(gridDim.x);
-        chunk_ = int(min(max(share, static_cast<long long>(kMinSplit)), 0x7fffffffll));
+        // work x heads / grid, rounded up (F32: a little more does no harm)
+        const float share = float(work) * float(p.hk) * (1.000001f / float(gridDim.x));
+        chunk_ = max(kMinSplit, int(fminf(share, 1e9f)) + 1);
       }
     }
   }
@@ -243,16 +244,39 @@ __device__ __noinline__ void join_parts(const Params& p, const Item& it, long lo
   }
 }
 
-// Row r of tile w of a divided range's part: O, m and l to the workspace (or, not finite, again
-// from the visible keys), then the join.
-enum { kNothing = 1, kPart = 2, kAgain = 4 };  // the row sees no key; its item is a part; O is not finite
-__device__ __noinline__ void write_special(const Params& p, const Item& it, float m, float l, long long out_to, int how,
-                                           int w, int r) {
+// What a row of an item needs beside O / l: it sees no key; its item is a part of a
+// divided range; its O is not finite; its item has no keys at all.
+enum { kNothing = 1, kPart = 2, kAgain = 4, kEmpty = 8 };
+// Row r of tile w where `how` is not 0 for its warp. Out of the way of the common case, whose code
+// must stay in the instruction caches.
+__device__ __noinline__ void write_special(const Params& p, const Item& it, uint32_t o_tm, float m, float l,
+                                           long long out_to, int how, int w, int r) {
   const int Dn = (p.D + 15) / 16 * 16;
   const int i = w * p.qt + r / p.group, head = it.kvh * p.group + r % p.group;
   const int lim = out_to < 0 ? 0 : limit_of(p.causal, it.at + i, it.lk, it.prefix);
+  const float inv = 1.0f / l;
   float* pb = p.partial + (size_t(it.slot) * 2 + w) * size_t(Dn + 2) * kTile + r;
-  if (how & kAgain) {
+  float bad = 0.0f;
+  for (int c = 0; c < p.D; c += 8) {
+    uint32_t o[8];
+    tmem_ld8(o_tm + uint32_t(c), o);
+    tmem_ld_wait();
+    float y[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      asm volatile("" : "+r"(o[e]));  // no use before the wait
+      y[e] = how & (kNothing | kEmpty) ? 0.0f : __uint_as_float(o[e]) * (how & kPart ? 1.0f : inv);
+      bad = fmaf(y[e], 0.0f, bad);
+    }
+    if (out_to < 0) continue;
+    if (how & kPart) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) __stcg(pb + size_t(2 + c + e) * kTile, y[e]);
+    } else {
+      store8(p, size_t(out_to) + c, y);
+    }
+  }
+  if (out_to >= 0 && bad != 0.0f) {  // again, from the visible keys alone
     float acc[128];
     row_again(p, p.q + static_cast<long long>(it.q0 + i) * p.qs + head * p.D, p.k + it.k0 * p.ks + it.kvh * p.D,
               p.v + it.k0 * p.vs + it.kvh * p.D, it.jb * kTile, min(lim, it.je * kTile), it.at + i,
@@ -268,49 +292,73 @@ __device__ __noinline__ void write_special(const Params& p, const Item& it, floa
   }
   __syncwarp();
   if (how & kPart) {
-    const bool some = lim > it.jb * kTile;
+    const bool some = lim > it.jb * kTile && !(how & kEmpty);
     __stcg(pb, some ? m : -INFINITY);
     __stcg(pb + kTile, some ? l : 0.0f);
     join_parts(p, it, out_to, w, r);
   }
 }
 
-// Row r of tile w of an item, once its last P V has finished: O / l to o, or O, m and l as a part
-// of a divided range.
+// Row r of tile w of an item, once its last P V has finished (o_tm: the row's O). Four lanes, which
+// hold four rows of 32 columns, exchange their quarters, so that they store 64 contiguous bytes of
+// one row at a time: 16 bytes of 32 rows an instruction took 22 of 134 us (32 images of 729 tokens).
 __device__ __forceinline__ void write_rows(const Params& p, const Item& it, uint32_t o_tm, float m, float l,
                                            long long out_to, int how, int w, int r) {
-  const int Dn = (p.D + 15) / 16 * 16;
-  float inv;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(l));
-  if (how & kPart) inv = 1.0f;
-  float bad = 0.0f;  // NaN once a value of the row is not finite
-  float* pb = p.partial + (size_t(it.slot) * 2 + w) * size_t(Dn + 2) * kTile + r;
+  if (!__any_sync(0xffffffffu, how)) {  // O / l
+    const int lane = r & 31, quarter = lane & 3;
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(l));
+    if (p.out_e4m3) inv *= 16.0f;
+    long long to[4];  // the four rows' places
+#pragma unroll
+    for (int k = 0; k < 4; ++k) to[k] = __shfl_sync(0xffffffffu, out_to, (lane & 28) + k);
+    float bad0 = 0.0f, bad1 = 0.0f;  // NaN once a value of the row is not finite
 #pragma unroll 1
-  for (int c = 0; c < p.D; c += 32) {
-    uint32_t o[32];
-    tmem_ld32(o_tm + uint32_t(c), o);
-    tmem_ld_wait(o);
+    for (int c = 0; c < p.D; c += 32) {
+      uint32_t o[32];
+      tmem_ld32(o_tm + uint32_t(c), o);
+      tmem_ld_wait(o);
+      uint32_t v[4][4];  // [eight columns][four registers of F16 pairs, or two of E4M3]
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {  // eight columns at a time
-      if (c + 8 * g < p.D && out_to >= 0) {
-        float y[8];
+      for (int g = 0; g < 4; ++g) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          y[e] = __uint_as_float(o[8 * g + e]) * inv;
-          bad = fmaf(y[e], 0.0f, bad);
-          if (how & kNothing) y[e] = 0.0f;
-        }
-        if (!(how & kPart)) {
-          store8(p, size_t(out_to) + c + 8 * g, y);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) __stcg(pb + size_t(2 + c + 8 * g + e) * kTile, y[e]);
+        for (int e = 0; e < 4; ++e) {
+          float a, b;
+          mul_x2(a, b, __uint_as_float(o[8 * g + 2 * e]), __uint_as_float(o[8 * g + 2 * e + 1]), inv, inv);
+          if (c + 8 * g < p.D) fma_x2(bad0, bad1, a, b, 0.0f, 0.0f, bad0, bad1);
+          if (p.out_e4m3) {
+            const uint32_t h = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+            v[g][e >> 1] = e & 1 ? v[g][e >> 1] | h << 16 : h;
+          } else {
+            const __half2 h = __floats2half2_rn(a, b);
+            v[g][e] = *reinterpret_cast<const uint32_t*>(&h);
+          }
         }
       }
+#pragma unroll
+      for (int x = 1; x < 4; x <<= 1)  // transpose the quarters among the four lanes
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          if (!(g & x))
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const bool high = lane & x;
+              const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? v[g][e] : v[g ^ x][e], x);
+              if (high) v[g][e] = got;
+              else v[g ^ x][e] = got;
+            }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (to[k] < 0 || c + 8 * quarter >= p.D) continue;
+        const long long at = to[k] + c + 8 * quarter;
+        if (p.out_e4m3) *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.o) + at) = make_uint2(v[k][0], v[k][1]);
+        else *reinterpret_cast<uint4*>(static_cast<__half*>(p.o) + at) = make_uint4(v[k][0], v[k][1], v[k][2], v[k][3]);
+      }
     }
+    if (out_to >= 0 && bad0 + bad1 != 0.0f) how = kAgain;
   }
-  if (out_to >= 0 && !(how & kNothing) && bad != 0.0f) how |= kAgain;
-  if (__any_sync(0xffffffffu, how & (kPart | kAgain))) write_special(p, it, m, l, out_to, how, w, r);
+  __syncwarp();  // (a row written again comes after the other lanes' stores to it)
+  if (__any_sync(0xffffffffu, how)) write_special(p, it, o_tm, m, l, out_to, how, w, r);
 }
 
 template <int NB, bool CAP, bool BIAS>
@@ -596,26 +644,13 @@ __global__ void __maxnreg__(168)
     // The pending item's row: where it goes in o (-1: the row holds no query), and what to do.
     long long out_to = -1;
     int out_how = 0;
-    // An item without keys: zeros, or an empty part.
-    auto write_none = [&](const Item& it) {
-      const int i = query(it);
-      if (it.splits > 1) {
-        float* pb = p.partial + (size_t(it.slot) * 2 + w) * size_t(Dn + 2) * kTile + r;
-        __stcg(pb, -INFINITY);
-        __stcg(pb + kTile, 0.0f);
-        join_parts(p, it, i < 0 ? -1 : static_cast<long long>(out_at(it, i)), w, r);
-      } else if (i >= 0) {
-        const float y[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-        for (int c = 0; c < p.D; c += 8) store8(p, out_at(it, i) + c, y);
-      }
-    };
-
     // through with item n
     auto done = [&](int n) {
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBarItemDone + n % kItems));
     };
     int pending = -1;  // the item whose rows are not written yet
+    bool pending_keys = false;
     int full = 0;      // items with keys so far
     bool ok = true;
     int t = 0;  // S tiles so far
@@ -626,7 +661,8 @@ __global__ void __maxnreg__(168)
       }
       const Item& it = items[n % kItems];
       if (pending >= 0) {  // the item before: its rows go out as soon as O is final
-        if (!__all_sync(0xffffffffu, wait_bar(bar(kBarOFull + w), (full - 1) & 1, abort_flag, p.err))) break;
+        if (pending_keys && !__all_sync(0xffffffffu, wait_bar(bar(kBarOFull + w), (full - 1) & 1, abort_flag, p.err)))
+          break;
         tc_fence_after();
         write_rows(p, items[pending % kItems], o_tm, m, l, out_to, out_how, w, r);
         done(pending);
@@ -634,17 +670,12 @@ __global__ void __maxnreg__(168)
       }
       if (!it.live) break;
       const int jb = it.jb, je = it.je;
-      if (jb >= je) {
-        write_none(it);
-        done(n);
-        continue;
-      }
       const int i = query(it);
       const int at = it.at + i;
       // rows without a query are computed like the others and never stored
       const int lim = i < 0 ? 0x7fffffff : limit_of(p.causal, at, it.lk, it.prefix);
       out_to = i < 0 ? -1 : static_cast<long long>(out_at(it, i));
-      out_how = (lim == 0 ? kNothing : 0) | (it.splits > 1 ? kPart : 0);
+      out_how = (lim == 0 ? kNothing : 0) | (it.splits > 1 ? kPart : 0) | (jb >= je ? kEmpty : 0);
       const float slope2 = BIAS && i >= 0 ? __ldg(p.slopes + it.kvh * p.group + head) * kLog2e : 0.0f;
       m = -INFINITY;
       l = 0.0f;
@@ -681,9 +712,10 @@ __global__ void __maxnreg__(168)
         if (valid < kTile) {
 #pragma unroll
           for (int c = 0; c < 4; ++c)
+            if (valid < 32 * c + 32)
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (32 * c + e >= valid) sv[c][e] = -INFINITY;
+              for (int e = 0; e < 32; ++e)
+                if (32 * c + e >= valid) sv[c][e] = -INFINITY;
         }
         float mq[8];
 #pragma unroll
@@ -741,7 +773,8 @@ __global__ void __maxnreg__(168)
       }
       if (!ok) break;
       pending = n;
-      ++full;
+      pending_keys = jb < je;
+      full += pending_keys;
     }
     tmem_ld_wait();
     tmem_st_wait();
