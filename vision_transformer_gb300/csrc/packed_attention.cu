@@ -36,6 +36,7 @@ constexpr int kTile = 128;                  // rows of a query tile, keys of a k
 constexpr int kBoxBytes = kTile * 128;      // 128 rows of 64 values: one box of an operand tile
 constexpr int kThreads = 320;
 constexpr int kBarBytes = 768;              // barriers, TMEM address slot, abort flag, items
+constexpr int kOutBytes = 32 * 64;          // 32 rows of 32 output columns
 constexpr int kItems = 4;                   // work items between the copy warp and the others
 constexpr uint32_t kTmemCols = 512;
 constexpr int kMaxSlots = 2 * kMaxSms;      // partial results of a launch at most (see Schedule)
@@ -45,10 +46,11 @@ static_assert(kCounterBytes >= size_t(kMaxSlots) * 8 * sizeof(unsigned), "counte
 template <int NB>
 struct Smem {
   static constexpr int kQBufs = NB == 1 ? 2 : 1;
-  static constexpr int kStages = NB == 1 ? 8 : 5;  // key and value tiles in turn
+  static constexpr int kStages = NB == 1 ? 8 : 4;  // key and value tiles in turn
   static constexpr int kOp = NB * kBoxBytes;       // one operand tile
   static constexpr int kOffKV = 2 * kQBufs * kOp;
-  static constexpr int kOffBar = kOffKV + kStages * kOp;
+  static constexpr int kOffOut = kOffKV + kStages * kOp;  // output rows on their way out: two buffers a softmax warp
+  static constexpr int kOffBar = kOffOut + 8 * 2 * kOutBytes;
   static constexpr int kBytes = 1024 + kOffBar + kBarBytes;
   static_assert(kBytes <= 232448, "shared memory budget");
 };
@@ -244,18 +246,49 @@ __device__ __noinline__ void join_parts(const Params& p, const Item& it, long lo
   }
 }
 
-// What a row of an item needs beside O / l: it sees no key; its item is a part of a
-// divided range; its O is not finite; its item has no keys at all.
-enum { kNothing = 1, kPart = 2, kAgain = 4, kEmpty = 8 };
-// Row r of tile w where `how` is not 0 for its warp. Out of the way of the common case, whose code
-// must stay in the instruction caches.
+// What a row of an item needs beside O / l: it sees no key; its item is a part of a divided range;
+// its item has no keys at all.
+enum { kNothing = 1, kPart = 2, kEmpty = 4 };
+
+// Row r of tile w whose O is not finite, again from the visible keys alone; of a part, its sums,
+// exponent and denominator.
+__device__ __noinline__ void write_again(const Params& p, const Item& it, long long out_to, int how, int w, int r) {
+  const int Dn = (p.D + 15) / 16 * 16;
+  const int i = w * p.qt + r / p.group, head = it.kvh * p.group + r % p.group;
+  float* pb = p.partial + (size_t(it.slot) * 2 + w) * size_t(Dn + 2) * kTile + r;
+  float acc[128], m, l;
+  row_again(p, p.q + static_cast<long long>(it.q0 + i) * p.qs + head * p.D, p.k + it.k0 * p.ks + it.kvh * p.D,
+            p.v + it.k0 * p.vs + it.kvh * p.D, it.jb * kTile,
+            min(limit_of(p.causal, it.at + i, it.lk, it.prefix), it.je * kTile), it.at + i,
+            p.slopes ? __ldg(p.slopes + head) : 0.0f, acc, m, l);
+  for (int c = 0; c < p.D; c += 8) {
+    float y[8];
+    for (int e = 0; e < 8; ++e) y[e] = how & kPart ? acc[c + e] : acc[c + e] / l;
+    if (how & kPart)
+      for (int e = 0; e < 8; ++e) __stcg(pb + size_t(2 + c + e) * kTile, y[e]);
+    else
+      store8(p, size_t(out_to) + c, y);
+  }
+  if (how & kPart) {
+    __stcg(pb, m);
+    __stcg(pb + kTile, l);
+  }
+}
+
+// Row r of tile w where `how` is not 0 for its whole warp. Out of the way of the common case,
+// whose code must stay in the instruction caches.
 __device__ __noinline__ void write_special(const Params& p, const Item& it, uint32_t o_tm, float m, float l,
                                            long long out_to, int how, int w, int r) {
   const int Dn = (p.D + 15) / 16 * 16;
-  const int i = w * p.qt + r / p.group, head = it.kvh * p.group + r % p.group;
+  const int i = w * p.qt + r / p.group;
   const int lim = out_to < 0 ? 0 : limit_of(p.causal, it.at + i, it.lk, it.prefix);
   const float inv = 1.0f / l;
   float* pb = p.partial + (size_t(it.slot) * 2 + w) * size_t(Dn + 2) * kTile + r;
+  if (how & kPart) {
+    const bool some = lim > it.jb * kTile && !(how & kEmpty);
+    __stcg(pb, some ? m : -INFINITY);
+    __stcg(pb + kTile, some ? l : 0.0f);
+  }
   float bad = 0.0f;
   for (int c = 0; c < p.D; c += 8) {
     uint32_t o[8];
@@ -276,89 +309,122 @@ __device__ __noinline__ void write_special(const Params& p, const Item& it, uint
       store8(p, size_t(out_to) + c, y);
     }
   }
-  if (out_to >= 0 && bad != 0.0f) {  // again, from the visible keys alone
-    float acc[128];
-    row_again(p, p.q + static_cast<long long>(it.q0 + i) * p.qs + head * p.D, p.k + it.k0 * p.ks + it.kvh * p.D,
-              p.v + it.k0 * p.vs + it.kvh * p.D, it.jb * kTile, min(lim, it.je * kTile), it.at + i,
-              p.slopes ? __ldg(p.slopes + head) : 0.0f, acc, m, l);
-    for (int c = 0; c < p.D; c += 8) {
-      float y[8];
-      for (int e = 0; e < 8; ++e) y[e] = how & kPart ? acc[c + e] : acc[c + e] / l;
-      if (how & kPart)
-        for (int e = 0; e < 8; ++e) __stcg(pb + size_t(2 + c + e) * kTile, y[e]);
-      else
-        store8(p, size_t(out_to) + c, y);
-    }
-  }
+  if (out_to >= 0 && bad != 0.0f) write_again(p, it, out_to, how, w, r);
   __syncwarp();
-  if (how & kPart) {
-    const bool some = lim > it.jb * kTile && !(how & kEmpty);
-    __stcg(pb, some ? m : -INFINITY);
-    __stcg(pb + kTile, some ? l : 0.0f);
-    join_parts(p, it, out_to, w, r);
-  }
+  if (how & kPart) join_parts(p, it, out_to, w, r);
 }
 
-// Row r of tile w of an item, once its last P V has finished (o_tm: the row's O). Four lanes, which
-// hold four rows of 32 columns, exchange their quarters, so that they store 64 contiguous bytes of
-// one row at a time: 16 bytes of 32 rows an instruction took 22 of 134 us (32 images of 729 tokens).
-__device__ __forceinline__ void write_rows(const Params& p, const Item& it, uint32_t o_tm, float m, float l,
-                                           long long out_to, int how, int w, int r) {
-  if (!__any_sync(0xffffffffu, how)) {  // O / l
-    const int lane = r & 31, quarter = lane & 3;
-    float inv;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(l));
-    if (p.out_e4m3) inv *= 16.0f;
-    long long to[4];  // the four rows' places
+// Row r of tile w of an item, once its last P V has finished (o_tm: the row's O). `loaded` is called
+// when O has left tensor memory. Where a warp's 32 rows are all the item's and whole queries (the
+// rule of p.out_tma), they go out by TMA from shared memory (`stage`: two buffers), 32 columns at a
+// time; otherwise four lanes, which hold four rows, exchange quarters of 32 columns and store
+// runs of one row. (16 bytes of 32 rows an instruction: 24 us for 23,328 rows of 16 heads of 72 by
+// itself, and the load-store unit held up for everything else meanwhile; 64-byte runs: 14 us.)
+template <int NB, typename F>
+__device__ __forceinline__ void write_rows(const Params& p, const Item& it, const CUtensorMap& to_map, uint8_t* stage,
+                                           uint32_t o_tm, float m, float l, long long out_to, int how, int w, int r,
+                                           F loaded) {
+  if (__any_sync(0xffffffffu, how)) {
+    write_special(p, it, o_tm, m, l, out_to, how, w, r);
+    loaded();
+    return;
+  }
+  uint32_t o[NB * 2][32];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) to[k] = __shfl_sync(0xffffffffu, out_to, (lane & 28) + k);
-    float bad0 = 0.0f, bad1 = 0.0f;  // NaN once a value of the row is not finite
-#pragma unroll 1
-    for (int c = 0; c < p.D; c += 32) {
-      uint32_t o[32];
-      tmem_ld32(o_tm + uint32_t(c), o);
-      tmem_ld_wait(o);
-      uint32_t v[4][4];  // [eight columns][four registers of F16 pairs, or two of E4M3]
+  for (int c = 0; c < NB * 2; ++c) tmem_ld32(o_tm + uint32_t(32 * c), o[c]);
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
+  for (int c = 0; c < NB * 2; ++c) tmem_ld_wait(o[c]);
+  loaded();
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(l));
+  if (p.out_e4m3) inv *= 16.0f;
+  const int lane = r & 31;
+  float bad0 = 0.0f, bad1 = 0.0f;  // NaN once a value of the row is not finite
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float a, b;
-          mul_x2(a, b, __uint_as_float(o[8 * g + 2 * e]), __uint_as_float(o[8 * g + 2 * e + 1]), inv, inv);
-          if (c + 8 * g < p.D) fma_x2(bad0, bad1, a, b, 0.0f, 0.0f, bad0, bad1);
-          if (p.out_e4m3) {
-            const uint32_t h = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-            v[g][e >> 1] = e & 1 ? v[g][e >> 1] | h << 16 : h;
-          } else {
-            const __half2 h = __floats2half2_rn(a, b);
-            v[g][e] = *reinterpret_cast<const uint32_t*>(&h);
-          }
+  for (int c = 0; c < NB * 2; ++c) {  // in the output's type, over the first half of o[c]
+    if (32 * c < p.D) {
+#pragma unroll
+      for (int e = 0; e < 32; e += 2) {
+        float a, b;
+        mul_x2(a, b, __uint_as_float(o[c][e]), __uint_as_float(o[c][e + 1]), inv, inv);
+        fma_x2(bad0, bad1, a, b, 0.0f, 0.0f, bad0, bad1);
+        if (p.out_e4m3) {
+          const uint32_t h = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+          o[c][e >> 2] = e & 2 ? o[c][e >> 2] | h << 16 : h;
+        } else {
+          const __half2 h = __floats2half2_rn(a, b);
+          o[c][e >> 1] = *reinterpret_cast<const uint32_t*>(&h);
         }
       }
+    }
+  }
+  const bool bad = out_to >= 0 && bad0 + bad1 != 0.0f;
+  if (p.out_tma && __all_sync(0xffffffffu, out_to >= 0 && !bad)) {
+    if (lane == 0) bulk_wait_read<0>();
+#pragma unroll
+    for (int c = 0; c < NB * 2; ++c) {
+      if (32 * c < p.D) {
+        if (c >= 2 && lane == 0) bulk_wait_read<1>();  // the buffer's columns before have been read out
+        __syncwarp();
+        uint8_t* buf = stage + (c & 1) * kOutBytes;
+        if (p.out_e4m3) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u)  // 32-byte swizzle
+            *reinterpret_cast<uint4*>(buf + lane * 32 + ((u ^ ((lane >> 2) & 1)) << 4)) =
+                make_uint4(o[c][4 * u], o[c][4 * u + 1], o[c][4 * u + 2], o[c][4 * u + 3]);
+        } else {
+#pragma unroll
+          for (int u = 0; u < 4; ++u)  // 64-byte swizzle
+            *reinterpret_cast<uint4*>(buf + lane * 64 + ((u ^ ((lane >> 1) & 3)) << 4)) =
+                make_uint4(o[c][4 * u], o[c][4 * u + 1], o[c][4 * u + 2], o[c][4 * u + 3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_3d(&to_map, smem_u32(buf), 32 * c, it.kvh * p.group, it.q0 + (w * kTile + r) / p.group);
+          bulk_commit();
+        }
+      }
+    }
+    return;
+  }
+  const int quarter = lane & 3;
+  long long to[4];  // the four rows' places
+#pragma unroll
+  for (int k = 0; k < 4; ++k) to[k] = __shfl_sync(0xffffffffu, out_to, (lane & 28) + k);
+  const int regs = p.out_e4m3 ? 2 : 4;  // of eight columns
+#pragma unroll
+  for (int c = 0; c < NB * 2; ++c) {
+    if (32 * c < p.D) {
+      uint32_t v[4][4];
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[g][e] = p.out_e4m3 ? o[c][2 * g + (e & 1)] : o[c][4 * g + e];
 #pragma unroll
       for (int x = 1; x < 4; x <<= 1)  // transpose the quarters among the four lanes
 #pragma unroll
         for (int g = 0; g < 4; ++g)
           if (!(g & x))
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const bool high = lane & x;
-              const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? v[g][e] : v[g ^ x][e], x);
-              if (high) v[g][e] = got;
-              else v[g ^ x][e] = got;
-            }
+            for (int e = 0; e < 4; ++e)
+              if (e < regs) {
+                const bool high = lane & x;
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? v[g][e] : v[g ^ x][e], x);
+                if (high) v[g][e] = got;
+                else v[g ^ x][e] = got;
+              }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        if (to[k] < 0 || c + 8 * quarter >= p.D) continue;
-        const long long at = to[k] + c + 8 * quarter;
+        if (to[k] < 0 || 32 * c + 8 * quarter >= p.D) continue;
+        const long long at = to[k] + 32 * c + 8 * quarter;
         if (p.out_e4m3) *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.o) + at) = make_uint2(v[k][0], v[k][1]);
         else *reinterpret_cast<uint4*>(static_cast<__half*>(p.o) + at) = make_uint4(v[k][0], v[k][1], v[k][2], v[k][3]);
       }
     }
-    if (out_to >= 0 && bad0 + bad1 != 0.0f) how = kAgain;
   }
   __syncwarp();  // (a row written again comes after the other lanes' stores to it)
-  if (__any_sync(0xffffffffu, how)) write_special(p, it, o_tm, m, l, out_to, how, w, r);
+  if (bad) write_again(p, it, out_to, how, w, r);
 }
 
 template <int NB, bool CAP, bool BIAS>
@@ -366,7 +432,8 @@ template <int NB, bool CAP, bool BIAS>
 // 16384 / (3 x 32) registers, rounded down to the allocation granule.
 __global__ void __maxnreg__(168)
     packed_tile_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap tq,
-                       const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv) {
+                       const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                       const __grid_constant__ CUtensorMap to) {
   using L = Smem<NB>;
   constexpr int kOp = L::kOp, kStages = L::kStages, kQBufs = L::kQBufs;
   extern __shared__ uint8_t smem_raw[];
@@ -640,6 +707,7 @@ __global__ void __maxnreg__(168)
       return size_t(it.q0 + i) * size_t(p.os) + size_t(it.kvh * p.group + head) * size_t(p.D);
     };
     float m = -INFINITY, l = 0.0f;
+    uint8_t* stage = smem + L::kOffOut + (w * 4 + sub) * 2 * kOutBytes;
 
     // The pending item's row: where it goes in o (-1: the row holds no query), and what to do.
     long long out_to = -1;
@@ -660,11 +728,12 @@ __global__ void __maxnreg__(168)
         break;
       }
       const Item& it = items[n % kItems];
-      if (pending >= 0) {  // the item before: its rows go out as soon as O is final
+      const bool keys = it.live && it.jb < it.je;
+      if (pending >= 0 && !keys) {  // nothing to hide the item before's rows under
         if (pending_keys && !__all_sync(0xffffffffu, wait_bar(bar(kBarOFull + w), (full - 1) & 1, abort_flag, p.err)))
           break;
         tc_fence_after();
-        write_rows(p, items[pending % kItems], o_tm, m, l, out_to, out_how, w, r);
+        write_rows<NB>(p, items[pending % kItems], to, stage, o_tm, m, l, out_to, out_how, w, r, [] {});
         done(pending);
         pending = -1;
       }
@@ -674,6 +743,10 @@ __global__ void __maxnreg__(168)
       const int at = it.at + i;
       // rows without a query are computed like the others and never stored
       const int lim = i < 0 ? 0x7fffffff : limit_of(p.causal, at, it.lk, it.prefix);
+      // the item before, whose rows go out behind this one's first tile
+      const float m_before = m, l_before = l;
+      const long long to_before = out_to;
+      const int how_before = out_how;
       out_to = i < 0 ? -1 : static_cast<long long>(out_at(it, i));
       out_how = (lim == 0 ? kNothing : 0) | (it.splits > 1 ? kPart : 0) | (jb >= je ? kEmpty : 0);
       const float slope2 = BIAS && i >= 0 ? __ldg(p.slopes + it.kvh * p.group + head) * kLog2e : 0.0f;
@@ -767,9 +840,22 @@ __global__ void __maxnreg__(168)
           tmem_st32(s_tm + 32 * c, pk);
         }
         l += (s0 + s1) + (s2 + s3);
-        tmem_st_wait();
-        tc_fence_before();
-        mbar_arrive(bar(kBarPFull + w));
+        auto arrive = [&]() {
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(bar(kBarPFull + w));
+        };
+        if (j == jb && pending >= 0) {
+          // The item before: this S followed its last P V, so its O is final, and the first P V
+          // of this item, which overwrites O, waits for the arrival. Between the two O is only
+          // loaded; its rows are written while the products run. (Written before the item's
+          // first tile they took 4,000 to 6,000 cycles that nothing else ran in.)
+          write_rows<NB>(p, items[pending % kItems], to, stage, o_tm, m_before, l_before, to_before, how_before, w, r, arrive);
+          done(pending);
+          pending = -1;
+        } else {
+          arrive();
+        }
       }
       if (!ok) break;
       pending = n;
@@ -778,6 +864,7 @@ __global__ void __maxnreg__(168)
     }
     tmem_ld_wait();
     tmem_st_wait();
+    if (lane == 0) bulk_wait_all();
   }
   __syncthreads();
   if (warp == 1) {
@@ -815,8 +902,18 @@ sv_status packed_launch_as(const Params& p, int grid, cudaStream_t s) {
   const bool keys = p.total_k > 0;
   if (st == SV_OK) st = packed_map(&tk, keys ? p.k : p.q, p.D, p.hk, keys ? p.total_k : 1, p.ks, 1, kTile);
   if (st == SV_OK) st = packed_map(&tv, keys ? p.v : p.q, p.D, p.hk, keys ? p.total_k : 1, p.vs, 1, kTile);
+  // the output: 32 columns of the rows of a softmax warp
+  CUtensorMap to = tq;
+  if (st == SV_OK && p.out_tma) {
+    const uint64_t es = p.out_e4m3 ? 1 : 2;
+    const uint64_t dims[3] = {uint64_t(p.D), uint64_t(p.hq), uint64_t(p.total_q)};
+    const uint64_t strides[2] = {uint64_t(p.D) * es, uint64_t(p.os) * es};
+    const uint32_t box[3] = {32u, uint32_t(p.group), uint32_t(32 / p.group)};
+    st = make_tmap(&to, p.out_e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, p.o, dims,
+                   strides, box, p.out_e4m3 ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_64B);
+  }
   if (st != SV_OK) return st;
-  e = launch_pdl(kern, dim3(unsigned(grid)), dim3(kThreads), size_t(Smem<NB>::kBytes), s, p, tq, tk, tv);
+  e = launch_pdl(kern, dim3(unsigned(grid)), dim3(kThreads), size_t(Smem<NB>::kBytes), s, p, tq, tk, tv, to);
   return e == cudaSuccess ? SV_OK : cuda_fail(e, "packed attention launch");
 }
 
@@ -935,6 +1032,8 @@ sv_status sv_attention_packed(const void* q, const void* k, const void* v, void*
   p.err = dev_err();
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   p.qt = kTile / p.group;
+  // rows of a warp that are whole queries, and 16-byte strides of the output
+  p.out_tma = 32 % p.group == 0 && (!p.out_e4m3 || (head_dim % 16 == 0 && o_stride % 16 == 0));
   if (workspace) {
     p.counters = static_cast<unsigned*>(workspace);
     p.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + kCounterBytes);

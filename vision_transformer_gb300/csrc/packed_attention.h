@@ -30,6 +30,7 @@ struct Params {
   float scale, cap;
   int causal, out_e4m3;
   int qt;              // queries of a 128-row tile: 128 / group
+  int out_tma;         // whole warps' output rows go out by TMA
   unsigned* counters;  // workspace: arrivals; null: no key range is divided
   float* partial;      // workspace: partial results
   int* err;
