@@ -769,17 +769,30 @@ __global__ void __maxnreg__(168)
         reg_fence(su[1]);
         reg_fence(su[2]);
         reg_fence(su[3]);
-        if constexpr (CAP || BIAS) {  // scores in units of log 2
-          const float d0 = float(at - j * kTile);
+        if constexpr (CAP)  // scores in units of log 2 from here on
 #pragma unroll
           for (int c = 0; c < 4; ++c)
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              float x = sv[c][e] * sl2;
-              if constexpr (CAP) x = capped(x, cap2);
-              if constexpr (BIAS) x = fmaf(-slope2, fabsf(d0 - float(32 * c + e)), x);
-              sv[c][e] = x;
-            }
+            for (int e = 0; e < 32; e += 4) capped4(&sv[c][e], sl2, cap2);
+        if constexpr (BIAS) {
+          const float d0 = float(at - j * kTile);
+          const float on = CAP ? 1.0f : sl2;
+          if (__all_sync(0xffffffffu, at >= j * kTile + kTile - 1)) {
+            // no key of the tile behind the query: |d0 - e| = d0 - e, one line of slope `slope2`
+            const float first = -slope2 * d0;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int e = 0; e < 32; e += 2)
+                fma_x2(sv[c][e], sv[c][e + 1], sv[c][e], sv[c][e + 1], on, on, fmaf(slope2, float(32 * c + e), first),
+                       fmaf(slope2, float(32 * c + e + 1), first));
+          } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                sv[c][e] = fmaf(-slope2, fabsf(d0 - float(32 * c + e)), CAP ? sv[c][e] : sv[c][e] * sl2);
+          }
         }
         const int valid = lim - j * kTile;  // visible keys of this tile
         if (valid < kTile) {

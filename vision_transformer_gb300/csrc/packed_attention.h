@@ -68,14 +68,36 @@ __device__ __forceinline__ bool document(const Params& p, int d, int docs, Docum
   return true;
 }
 
-// cap tanh(s / cap) = cap - 2 cap / (2^(2 s log2 e / cap) + 1): x = 2 s log2 e / cap, c = cap
-// (in any unit); exact limits for infinite s. The error, about 2^-22 cap, is that of the
-// reciprocal of a number >= 1.
+// cap tanh(s / cap) = cap - 2 cap / (2^x + 1), x = 2 s log2 e / cap, c = cap in any unit; exact
+// limits for infinite s. The error, about 2^-22 cap, is that of the reciprocal of a number >= 1.
 __device__ __forceinline__ float capped(float x, float c) {
   const float u = ex2(x) + 1.0f;
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(u));
   return fmaf(-2.0f * c, r, c);
+}
+// The same for four values x y[i], with one reciprocal: 1 / u_0 = (u_1 (u_2 u_3)) / (u_0 u_1 u_2 u_3)
+// and so on. Reciprocals run at a quarter of the exponentials' rate here, and the products on
+// another pipe. x is held to 30, where 2 / (2^x + 1) is below the last bit of 1, so that the product
+// of four stays finite; NaN passes through (into its neighbours too).
+__device__ __forceinline__ void capped4(float* y, float x, float c) {
+  float u[4];
+#pragma unroll
+  for (int i = 0; i < 4; i += 2) {
+    mul_x2(u[i], u[i + 1], y[i], y[i + 1], x, x);
+    asm("min.NaN.f32 %0, %0, 0f41F00000;" : "+f"(u[i]));
+    asm("min.NaN.f32 %0, %0, 0f41F00000;" : "+f"(u[i + 1]));
+    u[i] = ex2(u[i]);
+    u[i + 1] = ex2(u[i + 1]);
+    add_x2(u[i], u[i + 1], u[i], u[i + 1], 1.0f, 1.0f);
+  }
+  const float a = u[0] * u[1], b = u[2] * u[3];
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a * b));
+  r *= -2.0f * c;
+  const float ra = r * b, rb = r * a;
+  fma_x2(y[0], y[1], ra, ra, u[1], u[0], c, c);
+  fma_x2(y[2], y[3], rb, rb, u[3], u[2], c, c);
 }
 
 // Eight values in the output's type at `to`.
