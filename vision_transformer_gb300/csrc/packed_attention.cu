@@ -142,6 +142,7 @@ class Schedule {
       base_ += total_;
       slot_base_ += slot_total_;
       load(d0_);
+      longest_first();
       incl_ = count_;
       slot_incl_ = splits_ > 1 ? count_ : 0;
 #pragma unroll 1
@@ -186,6 +187,29 @@ class Schedule {
     tiles_ = (doc_.lk + kTile - 1) / kTile;  // of the last query
     splits_ = tiles_ > chunk_ ? (tiles_ + chunk_ - 1) / chunk_ : 1;
     count_ = pairs_ * p_.hk * splits_;
+  }
+  // Lane i takes the document with the i-th most key tiles of the 32 (equal ones in order): long
+  // items come early, and the last ones to be handed out are short.
+  __device__ __forceinline__ void longest_first() {
+    int rank = 0, from = 0;
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i) {
+      const int t = __shfl_sync(0xffffffffu, tiles_, i);
+      rank += t > tiles_ || (t == tiles_ && i < lane_);
+    }
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+      if (__shfl_sync(0xffffffffu, rank, i) == lane_) from = i;
+    auto take = [&](int& v) { v = __shfl_sync(0xffffffffu, v, from); };
+    take(doc_.q0);
+    take(doc_.lq);
+    take(doc_.k0);
+    take(doc_.lk);
+    take(doc_.prefix);
+    take(pairs_);
+    take(tiles_);
+    take(splits_);
+    take(count_);
   }
   const Params& p_;
   int lane_, docs_, chunk_;
