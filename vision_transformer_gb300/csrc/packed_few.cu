@@ -13,13 +13,17 @@
 //     keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9, and byte permutes pair the keys. P^T goes from the
 //     accumulator's layout to the operand's by a transposing 8 x 8 move.
 // A warp takes 16 keys at a time (its registers of K are reloaded as soon as S^T is done, those
-// of V as soon as O^T is), the four warps of a CTA take turns, three CTAs run per SM.
+// of V as soon as O^T is). The four warps of a CTA take four neighbouring key heads where their
+// number allows (or two heads and alternate keys, or one head): the rows of a key lie side by
+// side, a row of a narrow head is no whole number of DRAM's 64 bytes, and so the parts of a sector
+// are asked for at the same time (64 probes, 16 heads of 72: 252 MB read for 163 MB of keys and
+// values with a head per CTA). Three CTAs run per SM.
 //
-// Work: the (document, key head, block of rows) items are laid out one behind another in steps
-// of 64 keys, and every CTA takes an equal, contiguous share of the steps, so that any
-// distribution of lengths fills the GPU. An item inside one share is finished there; one that
-// is cut goes in parts to the workspace, and the last CTA of its parts joins them in order. A
-// CTA has at most two such parts, at the start and at the end of its share.
+// Work: the (document, group of key heads, block of rows) items are laid out one behind another
+// in steps of 64 keys of one head or 16 of four, and every CTA takes an equal, contiguous share of
+// the steps, so that any distribution of lengths fills the GPU. An item inside one share is
+// finished there; one that is cut goes in parts to the workspace, and the last CTA of its parts
+// joins them in order. A CTA has at most two such parts, at the start and at the end of its share.
 #include "packed_attention.h"
 
 namespace sv {
@@ -27,7 +31,7 @@ namespace packed {
 namespace {
 
 constexpr int kFewThreads = 128;
-constexpr int kStepKeys = 64;       // keys of a step: 16 for each of 4 warps
+constexpr int kMinShare = 64;       // keys of a CTA's share at least
 constexpr int kCtasPerSm = 3;
 constexpr int kMaxFewGrid = kMaxSms * kCtasPerSm;
 
@@ -55,15 +59,16 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 // A run of steps of one item that falls into this CTA's share.
 struct Segment {
   Document doc;
-  int kvh, row0;          // key head, first of the item's rows (query x group + head) in the document
+  int kvh, row0;          // first key head, first of the item's rows (query x group + head) in the document
   int s0, s1, steps;      // steps of the item: this segment's, all
   long long base;         // place of the item's first step among all steps
 };
 
 // The items in order: documents, key heads, blocks of rows. 32 documents at a time, one per
 // lane, with their steps summed by shuffles; every warp works it out for itself.
-template <int ROWS>
+template <int ROWS, int HEADS>
 class Share {
+  static constexpr int kStep = 64 / HEADS;  // keys of a step
  public:
   __device__ __forceinline__ Share(const Params& p, int lane) : p_(p), lane_(lane), docs_(p.docs) {
     long long work = 0;
@@ -80,9 +85,9 @@ class Share {
       work = 0;
     }
     chunk_ = (work + gridDim.x - 1) / gridDim.x;
-    if (chunk_ < 1) chunk_ = 1;
+    if (chunk_ < kMinShare / kStep) chunk_ = kMinShare / kStep;
     at_ = chunk_ * blockIdx.x;
-    end_ = min(at_ + chunk_, work);
+    end_ = min(at_ + chunk_, work);  // (a share may begin behind the last step)
     if (p.docs > 32 || docs_ == 0) load(0);
     open(0);
   }
@@ -108,6 +113,7 @@ class Share {
       r.base = first + item * r.steps;
       r.kvh = int(item / blocks);
       r.row0 = int(item - static_cast<long long>(r.kvh) * blocks) * ROWS;
+      r.kvh *= HEADS;
       r.s0 = int(at_ - r.base);
       r.s1 = int(min(end_ - r.base, static_cast<long long>(r.steps)));
       if (!p_.counters) {
@@ -127,13 +133,13 @@ class Share {
  private:
   __device__ __forceinline__ static int of(int v, int src) { return __shfl_sync(0xffffffffu, v, src); }
   __device__ __forceinline__ long long mine() const {
-    return static_cast<long long>(blocks_) * p_.hk * steps_;
+    return static_cast<long long>(blocks_) * (p_.hk / HEADS) * steps_;
   }
   __device__ __forceinline__ bool load(int d0) {
     d0_ = d0;
     const bool good = document(p_, d0 + lane_, docs_, doc_);
     blocks_ = int((static_cast<long long>(doc_.lq) * p_.group + ROWS - 1) / ROWS);
-    steps_ = max(1, (doc_.lk + kStepKeys - 1) / kStepKeys);  // (a step without keys writes the zeros)
+    steps_ = max(1, (doc_.lk + kStep - 1) / kStep);  // (a step without keys writes the zeros)
     return good;
   }
   __device__ __forceinline__ void open(int d0) {
@@ -150,21 +156,47 @@ class Share {
   long long chunk_, at_, end_, base_ = 0, total_ = 0, incl_;
 };
 
+// Columns c .. c + 7 of row r of the item's head hw (key head kvh), from its parts c0 .. c1 in order.
+template <typename F>
+__device__ __forceinline__ void join(const Params& p, const Document& doc, int row0, int rows, int r, int c, int hw,
+                                     int kvh, int c0, int c1, F part) {
+  const size_t at = size_t(hw * rows + r) * size_t(p.D + 2);
+  float mx = -INFINITY, sum = 0.0f, y[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+  for (int w = c0; w <= c1; ++w) mx = fmaxf(mx, __ldcg(part(w, w == c0) + at + p.D));
+  const float ref = mx == -INFINITY ? 0.0f : mx;
+#pragma unroll 2
+  for (int w = c0; w <= c1; ++w) {
+    const float* a = part(w, w == c0) + at;
+    const float f = ex2(__ldcg(a + p.D) - ref);
+    sum = fmaf(f, __ldcg(a + p.D + 1), sum);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = fmaf(f, __ldcg(a + c + e), y[e]);
+  }
+  const int i = (row0 + r) / p.group, head = kvh * p.group + (row0 + r - i * p.group);
+  const bool none = limit_of(p.causal, i + doc.lk - doc.lq, doc.lk, doc.prefix) == 0;
+  const float inv = 1.0f / sum;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) y[e] = none ? 0.0f : y[e] * inv;
+  store8(p, size_t(doc.q0 + i) * size_t(p.os) + size_t(head) * size_t(p.D) + size_t(c), y);
+}
+
 // KI: 32-dimension groups of a key row, VI: 64-dimension groups of a value row, NT: 8-row
-// tiles of an item.
-template <int KI, int VI, int NT>
+// tiles of an item, HEADS: key heads of an item (4 / HEADS warps share a head's keys).
+template <int KI, int VI, int NT, int HEADS>
 __global__ void __launch_bounds__(kFewThreads, NT == 1 ? kCtasPerSm : 2) few_kernel(const __grid_constant__ Params p) {
-  constexpr int kRows = 8 * NT;
+  constexpr int kRows = 8 * NT, kSplit = 4 / HEADS, kStep = 16 * kSplit;
   constexpr int kOut = 64 * VI + 4;  // row pitch of the merge buffer (floats)
-  __shared__ float red[4][kRows][kOut];
+  __shared__ __align__(16) float red[4][kRows][kOut];
   __shared__ float red_m[4][kRows], red_l[4][kRows];
-  __shared__ int row_bad[kRows];
+  __shared__ int row_bad[HEADS * kRows];
   __shared__ unsigned seen;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   pdl_launch_dependents();
   pdl_wait();
-  Share<kRows> share(p, lane);
+  const int my_head = warp % HEADS, my_keys = warp / HEADS;
+  Share<kRows, HEADS> share(p, lane);
   const int chunks = p.D / 8;  // 16-byte chunks of a row
   const float sl2 = p.cap > 0.0f ? 2.0f * kLog2e * p.scale / p.cap : kLog2e * p.scale;
 
@@ -172,9 +204,10 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? kCtasPerSm : 2) few_ker
   while (share.get(sg)) {
     const int rows_all = sg.doc.lq * p.group;  // of the document (for this key head)
     const int lk = sg.doc.lk;
-    const __half* kb = p.k + sg.doc.k0 * p.ks + sg.kvh * p.D;
-    const __half* vb = p.v + sg.doc.k0 * p.vs + sg.kvh * p.D;
-    const int last = min(lk, sg.s1 * kStepKeys);  // keys of this segment end here
+    const int kvh = sg.kvh + my_head;
+    const __half* kb = p.k + sg.doc.k0 * p.ks + kvh * p.D;
+    const __half* vb = p.v + sg.doc.k0 * p.vs + kvh * p.D;
+    const int last = min(lk, sg.s1 * kStep);  // keys of this segment end here
 
     // this lane's two rows of each tile as columns of S^T: visible keys, position, slope
     int lim[NT][2];
@@ -188,11 +221,11 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? kCtasPerSm : 2) few_ker
         const int i = r / p.group, pos = i + lk - sg.doc.lq;
         lim[n][e] = r < rows_all ? limit_of(p.causal, pos, lk, sg.doc.prefix) : lk;
         at[n][e] = float(pos);
-        slope[n][e] = p.slopes && r < rows_all ? __ldg(p.slopes + sg.kvh * p.group + (r - i * p.group)) * kLog2e : 0.0f;
+        slope[n][e] = p.slopes && r < rows_all ? __ldg(p.slopes + kvh * p.group + (r - i * p.group)) * kLog2e : 0.0f;
       }
       const int r = sg.row0 + 8 * n + g;  // Q^T: this lane's column
       const int i = r / p.group;
-      const __half* qr = p.q + static_cast<long long>(sg.doc.q0 + i) * p.qs + (sg.kvh * p.group + r - i * p.group) * p.D;
+      const __half* qr = p.q + static_cast<long long>(sg.doc.q0 + i) * p.qs + (kvh * p.group + r - i * p.group) * p.D;
 #pragma unroll
       for (int c = 0; c < KI; ++c) {
         uint4 x = make_uint4(0u, 0u, 0u, 0u);
@@ -232,10 +265,10 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? kCtasPerSm : 2) few_ker
       l[n][0] = l[n][1] = 0.0f;
     }
 
-    int key0 = sg.s0 * kStepKeys + 16 * warp;
+    int key0 = sg.s0 * kStep + 16 * my_keys;
     load_k(key0);
     load_v(key0);
-    for (; key0 < last; key0 += kStepKeys) {
+    for (; key0 < last; key0 += kStep) {
       uint32_t b[NT][2];
       float s[NT][4];
 #pragma unroll
@@ -247,7 +280,7 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? kCtasPerSm : 2) few_ker
           mma16816(s[n], kx[0][c].z, kx[1][c].z, kx[0][c].w, kx[1][c].w, q[n][c][2], q[n][c][3]);
         }
       }
-      load_k(key0 + kStepKeys);
+      load_k(key0 + kStep);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         float x[4];
@@ -311,7 +344,91 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? kCtasPerSm : 2) few_ker
           for (int n = 0; n < NT; ++n) mma16816(o[n][4 * c + j], a0, a1, a2, a3, b[n][0], b[n][1]);
         }
       }
-      load_v(key0 + kStepKeys);
+      load_v(key0 + kStep);
+    }
+
+    const bool whole = sg.s0 == 0 && sg.s1 == sg.steps;
+    const int rows = min(kRows, rows_all - sg.row0);
+    // a part's place: at the start of this CTA's share (0) or at its end (1)
+    auto part = [&](int cta, int end) {
+      return p.partial + (size_t(cta) * 2 + end) * size_t(HEADS * kRows) * size_t(p.D + 2);
+    };
+    float* mine = whole ? nullptr : part(int(blockIdx.x), sg.s0 == 0 ? 1 : 0);
+    const int c0 = share.cta_of(sg.base), c1 = share.cta_of(sg.base + sg.steps - 1);  // the item's parts
+
+    if constexpr (kSplit == 1) {
+      // A warp has its head's rows to itself: they go out from its registers, and the warps of the
+      // CTA need not wait for one another. A lane holds eight neighbouring columns of two rows.
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = 8 * n + 2 * t + e, i = (sg.row0 + r) / p.group;
+          const int head = kvh * p.group + (sg.row0 + r - i * p.group);
+          const bool live = r < rows;
+          const size_t to = size_t(sg.doc.q0 + i) * size_t(p.os) + size_t(head) * size_t(p.D);
+          float* at_p = whole ? nullptr : mine + size_t(my_head * rows + r) * size_t(p.D + 2);
+          float sum = l[n][e];
+          sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+          const bool none = lim[n][e] == 0;
+          const float inv = whole ? 1.0f / sum : 1.0f;
+          float bad = 0.0f;
+#pragma unroll
+          for (int v = 0; v < VI; ++v) {
+            float y[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              y[2 * j] = none ? 0.0f : o[n][4 * v + j][e] * inv;
+              y[2 * j + 1] = none ? 0.0f : o[n][4 * v + j][e + 2] * inv;
+              bad = fmaf(y[2 * j], 0.0f, fmaf(y[2 * j + 1], 0.0f, bad));
+            }
+            if (!live || 8 * v + g >= chunks) continue;
+            if (whole) {
+              store8(p, to + 8 * (8 * v + g), y);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) __stcg(at_p + 8 * (8 * v + g) + j, y[j]);
+            }
+          }
+          if (live && !whole && g == 0) {
+            __stcg(at_p + p.D, m[n][e]);
+            __stcg(at_p + p.D + 1, sum);
+          }
+          const unsigned rows_bad = __ballot_sync(0xffffffffu, live && bad != 0.0f);
+          if (rows_bad) {  // again from the visible keys alone, a lane a row
+            __syncwarp();
+            if (g == 0 && (rows_bad & (0x11111111u << t))) {
+              const int pos = i + lk - sg.doc.lq;
+              float acc[128], mx;
+              row_again(p, p.q + static_cast<long long>(sg.doc.q0 + i) * p.qs + head * p.D, kb, vb, sg.s0 * kStep,
+                        min(last, lim[n][e]), pos, p.slopes ? __ldg(p.slopes + head) : 0.0f, acc, mx, sum);
+              for (int c = 0; c < p.D; c += 8) {
+                float y[8];
+                for (int j = 0; j < 8; ++j) y[j] = whole ? acc[c + j] / sum : acc[c + j];
+                if (whole) store8(p, to + c, y);
+                else
+                  for (int j = 0; j < 8; ++j) __stcg(at_p + c + j, y[j]);
+              }
+              if (!whole) {
+                __stcg(at_p + p.D, mx);
+                __stcg(at_p + p.D + 1, sum);
+              }
+            }
+            __syncwarp();
+          }
+        }
+      if (whole) continue;
+      __threadfence();
+      __syncwarp();
+      unsigned arrived = 0;
+      if (lane == 0) arrived = atomicInc(p.counters + c0 * 4 + warp, unsigned(c1 - c0));  // 0 .. c1 - c0, then 0 again
+      if (__shfl_sync(0xffffffffu, arrived, 0) != unsigned(c1 - c0)) continue;
+      __threadfence();
+      for (int x = lane; x < rows * chunks; x += 32)
+        join(p, sg.doc, sg.row0, rows, x / chunks, 8 * (x % chunks), my_head, kvh, c0, c1, part);
+      continue;
     }
 
     // the four warps' sums, brought to one exponent
@@ -328,7 +445,7 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? kCtasPerSm : 2) few_ker
           red_l[warp][8 * n + 2 * t + e] = x;
         }
       }
-    if (threadIdx.x < kRows) row_bad[threadIdx.x] = 0;
+    if (threadIdx.x < HEADS * kRows) row_bad[threadIdx.x] = 0;
     __syncthreads();
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -336,54 +453,52 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? kCtasPerSm : 2) few_ker
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int r = 8 * n + 2 * t + e;
-        const float mx = fmaxf(fmaxf(red_m[0][r], red_m[1][r]), fmaxf(red_m[2][r], red_m[3][r]));
+        float mx = red_m[my_head][r];
+#pragma unroll
+        for (int k = 1; k < kSplit; ++k) mx = fmaxf(mx, red_m[my_head + k * HEADS][r]);
         f[e] = ex2(m[n][e] - (mx == -INFINITY ? 0.0f : mx));
       }
 #pragma unroll
-      for (int j = 0; j < 4 * VI; ++j)
+      for (int j = 0; j < 4 * VI; j += 2)  // four neighbouring dimensions of a row
 #pragma unroll
-        for (int e = 0; e < 4; ++e)  // e & 1: the row, e >> 1: the dimension
-          red[warp][8 * n + 2 * t + (e & 1)][64 * (j >> 2) + 8 * g + 2 * (j & 3) + (e >> 1)] = o[n][j][e] * f[e & 1];
+        for (int e = 0; e < 2; ++e)
+          *reinterpret_cast<float4*>(&red[warp][8 * n + 2 * t + e][64 * (j >> 2) + 8 * g + 2 * (j & 3)]) =
+              make_float4(o[n][j][e] * f[e], o[n][j][e + 2] * f[e], o[n][j + 1][e] * f[e], o[n][j + 1][e + 2] * f[e]);
     }
     __syncthreads();
-    const bool whole = sg.s0 == 0 && sg.s1 == sg.steps;
-    const int rows = min(kRows, rows_all - sg.row0);
-    // a part's place: at the start of this CTA's share (0) or at its end (1)
-    auto part = [&](int cta, int end) {
-      return p.partial + (size_t(cta) * 2 + end) * size_t(kRows) * size_t(p.D + 2);
-    };
-    float* mine = whole ? nullptr : part(int(blockIdx.x), sg.s0 == 0 ? 1 : 0);
-    auto row_of = [&](int r, int& i, int& head) {
+    // row x of the item's HEADS x rows: which head and row, query and query head
+    auto row_of = [&](int x, int& hw, int& r, int& i, int& head) {
+      hw = x / rows;
+      r = x - hw * rows;
       i = (sg.row0 + r) / p.group;
-      head = sg.kvh * p.group + (sg.row0 + r - i * p.group);
+      head = (sg.kvh + hw) * p.group + (sg.row0 + r - i * p.group);
     };
-    auto sums = [&](int r, float& mx, float& sum) {
-      mx = fmaxf(fmaxf(red_m[0][r], red_m[1][r]), fmaxf(red_m[2][r], red_m[3][r]));
-      const float ref = mx == -INFINITY ? 0.0f : mx;
-      sum = 0.0f;
+    for (int x = int(threadIdx.x); x < HEADS * rows * chunks; x += kFewThreads) {
+      const int row = x / chunks, c = 8 * (x - row * chunks);
+      int hw, r, i, head;
+      row_of(row, hw, r, i, head);
+      float mx = red_m[hw][r], sum = 0.0f;
 #pragma unroll
-      for (int w = 0; w < 4; ++w) sum += ex2(red_m[w][r] - ref) * red_l[w][r];
-    };
-    for (int x = int(threadIdx.x); x < rows * chunks; x += kFewThreads) {
-      const int r = x / chunks, c = 8 * (x - r * chunks);
-      int i, head;
-      row_of(r, i, head);
-      float mx, sum;
-      sums(r, mx, sum);
+      for (int k = 1; k < kSplit; ++k) mx = fmaxf(mx, red_m[hw + k * HEADS][r]);
+      const float ref = mx == -INFINITY ? 0.0f : mx;
+#pragma unroll
+      for (int k = 0; k < kSplit; ++k) sum += ex2(red_m[hw + k * HEADS][r] - ref) * red_l[hw + k * HEADS][r];
       const bool none = limit_of(p.causal, i + lk - sg.doc.lq, lk, sg.doc.prefix) == 0;
       const float inv = whole ? 1.0f / sum : 1.0f;
       float y[8], bad = 0.0f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        y[e] = ((red[0][r][c + e] + red[1][r][c + e]) + (red[2][r][c + e] + red[3][r][c + e])) * inv;
-        if (none) y[e] = 0.0f;
+        y[e] = red[hw][r][c + e];
+#pragma unroll
+        for (int k = 1; k < kSplit; ++k) y[e] += red[hw + k * HEADS][r][c + e];
+        y[e] = none ? 0.0f : y[e] * inv;
         bad = fmaf(y[e], 0.0f, bad);
       }
-      if (bad != 0.0f) row_bad[r] = 1;
+      if (bad != 0.0f) row_bad[row] = 1;
       if (whole) {
         store8(p, size_t(sg.doc.q0 + i) * size_t(p.os) + size_t(head) * size_t(p.D) + size_t(c), y);
       } else {
-        float* at_p = mine + size_t(r) * size_t(p.D + 2);
+        float* at_p = mine + size_t(row) * size_t(p.D + 2);
 #pragma unroll
         for (int e = 0; e < 8; ++e) __stcg(at_p + c + e, y[e]);
         if (c == 0) {
@@ -393,13 +508,14 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? kCtasPerSm : 2) few_ker
       }
     }
     __syncthreads();
-    if (int(threadIdx.x) < rows && row_bad[threadIdx.x]) {
-      const int r = int(threadIdx.x);
-      int i, head;
-      row_of(r, i, head);
+    if (int(threadIdx.x) < HEADS * rows && row_bad[threadIdx.x]) {
+      const int row = int(threadIdx.x);
+      int hw, r, i, head;
+      row_of(row, hw, r, i, head);
       const int pos = i + lk - sg.doc.lq;
       float acc[128], mx, sum;
-      row_again(p, p.q + static_cast<long long>(sg.doc.q0 + i) * p.qs + head * p.D, kb, vb, sg.s0 * kStepKeys,
+      row_again(p, p.q + static_cast<long long>(sg.doc.q0 + i) * p.qs + head * p.D,
+                p.k + sg.doc.k0 * p.ks + (sg.kvh + hw) * p.D, p.v + sg.doc.k0 * p.vs + (sg.kvh + hw) * p.D, sg.s0 * kStep,
                 min(last, limit_of(p.causal, pos, lk, sg.doc.prefix)), pos, p.slopes ? __ldg(p.slopes + head) : 0.0f, acc,
                 mx, sum);
       for (int c = 0; c < p.D; c += 8) {
@@ -407,72 +523,69 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? kCtasPerSm : 2) few_ker
         for (int e = 0; e < 8; ++e) y[e] = whole ? acc[c + e] / sum : acc[c + e];
         if (whole) store8(p, size_t(sg.doc.q0 + i) * size_t(p.os) + size_t(head) * size_t(p.D) + size_t(c), y);
         else
-          for (int e = 0; e < 8; ++e) __stcg(mine + size_t(r) * size_t(p.D + 2) + c + e, y[e]);
+          for (int e = 0; e < 8; ++e) __stcg(mine + size_t(row) * size_t(p.D + 2) + c + e, y[e]);
       }
       if (!whole) {
-        __stcg(mine + size_t(r) * size_t(p.D + 2) + p.D, mx);
-        __stcg(mine + size_t(r) * size_t(p.D + 2) + p.D + 1, sum);
+        __stcg(mine + size_t(row) * size_t(p.D + 2) + p.D, mx);
+        __stcg(mine + size_t(row) * size_t(p.D + 2) + p.D + 1, sum);
       }
     }
     if (whole) continue;
 
     // the last CTA of the item's parts joins them, in order
-    const int c0 = share.cta_of(sg.base), c1 = share.cta_of(sg.base + sg.steps - 1);
     __threadfence();
     __syncthreads();
-    if (threadIdx.x == 0) seen = atomicInc(p.counters + c0, unsigned(c1 - c0));  // counts 0 .. c1 - c0, then 0 again
+    if (threadIdx.x == 0) seen = atomicInc(p.counters + c0 * 4, unsigned(c1 - c0));  // 0 .. c1 - c0, then 0 again
     __syncthreads();
     if (seen == unsigned(c1 - c0)) {
       __threadfence();
-      for (int x = int(threadIdx.x); x < rows * chunks; x += kFewThreads) {
-        const int r = x / chunks, c = 8 * (x - r * chunks);
-        int i, head;
-        row_of(r, i, head);
-        float mx = -INFINITY, sum = 0.0f, y[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-        for (int w = c0; w <= c1; ++w) mx = fmaxf(mx, __ldcg(part(w, w == c0) + size_t(r) * size_t(p.D + 2) + p.D));
-        const float ref = mx == -INFINITY ? 0.0f : mx;
-        for (int w = c0; w <= c1; ++w) {
-          const float* a = part(w, w == c0) + size_t(r) * size_t(p.D + 2);
-          const float f = ex2(__ldcg(a + p.D) - ref);
-          sum = fmaf(f, __ldcg(a + p.D + 1), sum);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = fmaf(f, __ldcg(a + c + e), y[e]);
-        }
-        const bool none = limit_of(p.causal, i + lk - sg.doc.lq, lk, sg.doc.prefix) == 0;
-        const float inv = 1.0f / sum;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = none ? 0.0f : y[e] * inv;
-        store8(p, size_t(sg.doc.q0 + i) * size_t(p.os) + size_t(head) * size_t(p.D) + size_t(c), y);
+      for (int x = int(threadIdx.x); x < HEADS * rows * chunks; x += kFewThreads) {
+        const int row = x / chunks, hw = row / rows;
+        join(p, sg.doc, sg.row0, rows, row - hw * rows, 8 * (x - row * chunks), hw, sg.kvh + hw, c0, c1, part);
       }
     }
     __syncthreads();  // `seen` and the merge buffers are free again
   }
 }
 
-template <int KI, int VI, int NT>
+template <int KI, int VI, int NT, int HEADS>
 cudaError_t few_launch_as(const Params& p, cudaStream_t s) {
   const int sms = num_sms() < kMaxSms ? num_sms() : kMaxSms;
-  return launch_pdl(few_kernel<KI, VI, NT>, dim3(unsigned(sms * (NT == 1 ? kCtasPerSm : 2))), dim3(kFewThreads), 0, s, p);
+  return launch_pdl(few_kernel<KI, VI, NT, HEADS>, dim3(unsigned(sms * (NT == 1 ? kCtasPerSm : 2))), dim3(kFewThreads), 0,
+                    s, p);
+}
+
+template <int NT, int HEADS>
+cudaError_t few_launch_rows(const Params& p, cudaStream_t s) {
+  if (p.D <= 64) return few_launch_as<2, 1, NT, HEADS>(p, s);
+  if (p.D <= 96) return few_launch_as<3, 2, NT, HEADS>(p, s);
+  return few_launch_as<4, 2, NT, HEADS>(p, s);
 }
 
 template <int NT>
-cudaError_t few_launch_rows(const Params& p, cudaStream_t s) {
-  if (p.D <= 64) return few_launch_as<2, 1, NT>(p, s);
-  if (p.D <= 96) return few_launch_as<3, 2, NT>(p, s);
-  return few_launch_as<4, 2, NT>(p, s);
+cudaError_t few_launch_heads(const Params& p, cudaStream_t s) {
+  // Neighbouring heads in a CTA where a head's row is no whole number of 64 bytes (64 probes over
+  // images, 16 heads of 72: 52 us against 70 with a head per CTA); else a head per CTA, whose
+  // warps then share its long run of keys (one token of 16 requests, 8 key heads of 128: 162 us
+  // against 178).
+  if (p.D % 32 && p.hk % 4 == 0) return few_launch_rows<NT, 4>(p, s);
+  if (p.D % 32 && p.hk % 2 == 0) return few_launch_rows<NT, 2>(p, s);
+  return few_launch_rows<NT, 1>(p, s);
 }
 
 }  // namespace
 
 size_t few_workspace(int head_dim) {
-  return kCounterBytes + size_t(kMaxFewGrid) * 2 * 16 * size_t(head_dim + 2) * sizeof(float);
+  // two parts a CTA of up to four heads of 8 rows (three CTAs an SM) or 16 (two CTAs)
+  const size_t rows = size_t(kMaxSms) * (kCtasPerSm * 8 > 2 * 16 ? kCtasPerSm * 8 : 2 * 16);
+  return kCounterBytes + rows * 2 * 4 * size_t(head_dim + 2) * sizeof(float);
 }
 
 sv_status few_launch(const Params& p, cudaStream_t s) {
-  static_assert(kMaxFewGrid * sizeof(unsigned) <= kCounterBytes, "counters");
+  static_assert(kMaxFewGrid * 4 * sizeof(unsigned) <= kTicket * sizeof(unsigned), "counters");
   // rows of the documents on average decide between one and two 8-row tiles
   const bool small = static_cast<long long>(p.total_q) * p.group <= 8ll * p.docs;
-  const cudaError_t e = small ? few_launch_rows<1>(p, s) : few_launch_rows<2>(p, s);
+  const cudaError_t e = small ? few_launch_heads<1>(p, s) : few_launch_heads<2>(p, s);
   return e == cudaSuccess ? SV_OK : cuda_fail(e, "packed attention launch (few rows)");
 }
 
