@@ -567,9 +567,11 @@ cudaError_t few_launch_heads(const Params& p, cudaStream_t s) {
   // Neighbouring heads in a CTA where a head's row is no whole number of 64 bytes (64 probes over
   // images, 16 heads of 72: 52 us against 70 with a head per CTA); else a head per CTA, whose
   // warps then share its long run of keys (one token of 16 requests, 8 key heads of 128: 162 us
-  // against 178).
-  if (p.D % 32 && p.hk % 4 == 0) return few_launch_rows<NT, 4>(p, s);
-  if (p.D % 32 && p.hk % 2 == 0) return few_launch_rows<NT, 2>(p, s);
+  // against 178). Also where there is so little to read that a head's keys had better be spread
+  // over as many warps as there are.
+  const bool little = static_cast<long long>(p.total_k) * p.hk <= 64ll * 2 * kMaxFewGrid;
+  if (p.D % 32 && !little && p.hk % 4 == 0) return few_launch_rows<NT, 4>(p, s);
+  if (p.D % 32 && !little && p.hk % 2 == 0) return few_launch_rows<NT, 2>(p, s);
   return few_launch_rows<NT, 1>(p, s);
 }
 
