@@ -341,12 +341,14 @@ __device__ __noinline__ void write_special(const Params& p, const Item& it, uint
 }
 
 // Row r of tile w of an item, once its last P V has finished (o_tm: the row's O). `loaded` is called
-// when O has left tensor memory. Where a warp's 32 rows are all the item's and whole queries (the
-// rule of p.out_tma), they go out by TMA from shared memory (`stage`: two buffers), 32 columns at a
-// time; otherwise four lanes, which hold four rows, exchange quarters of 32 columns and store
-// runs of one row. (16 bytes of 32 rows an instruction: 24 us for 23,328 rows of 16 heads of 72 by
-// itself, and the load-store unit held up for everything else meanwhile; 64-byte runs: 14 us.)
-template <int NB, typename F>
+// when O has left tensor memory. Where a warp's 32 rows are all the item's and make whole queries
+// (p.out_tma) they go out by TMA from shared memory (`stage`: two buffers), 32 columns at a time;
+// the rows of a part-filled warp are stored by their lanes (a bulk copy a row instead: 134 against
+// 128 us for 32 images of 729 tokens). E4M3 rows that do not start on 16 bytes are stored in runs,
+// after four lanes, which hold four rows, have exchanged quarters of 32 columns. (All rows by their
+// lanes: 24 us for 23,328 rows of 16 heads of 72 by itself, and the load-store unit held up for
+// everything else meanwhile.)
+template <int NB, bool E4M3, typename F>
 __device__ __forceinline__ void write_rows(const Params& p, const Item& it, const CUtensorMap& to_map, uint8_t* stage,
                                            uint32_t o_tm, float m, float l, long long out_to, int how, int w, int r,
                                            F loaded) {
@@ -363,18 +365,18 @@ __device__ __forceinline__ void write_rows(const Params& p, const Item& it, cons
   loaded();
   float inv;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(l));
-  if (p.out_e4m3) inv *= 16.0f;
+  if (E4M3) inv *= 16.0f;
   const int lane = r & 31;
   float bad0 = 0.0f, bad1 = 0.0f;  // NaN once a value of the row is not finite
 #pragma unroll
-  for (int c = 0; c < NB * 2; ++c) {  // in the output's type, over the first half of o[c]
+  for (int c = 0; c < NB * 2; ++c) {  // in the output's type, over the first registers of o[c]
     if (32 * c < p.D) {
 #pragma unroll
       for (int e = 0; e < 32; e += 2) {
         float a, b;
         mul_x2(a, b, __uint_as_float(o[c][e]), __uint_as_float(o[c][e + 1]), inv, inv);
         fma_x2(bad0, bad1, a, b, 0.0f, 0.0f, bad0, bad1);
-        if (p.out_e4m3) {
+        if constexpr (E4M3) {
           const uint32_t h = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
           o[c][e >> 2] = e & 2 ? o[c][e >> 2] | h << 16 : h;
         } else {
@@ -385,7 +387,9 @@ __device__ __forceinline__ void write_rows(const Params& p, const Item& it, cons
     }
   }
   const bool bad = out_to >= 0 && bad0 + bad1 != 0.0f;
+  constexpr int kRow = E4M3 ? 32 : 64;  // bytes of a staged row, swizzled for a TMA store
   if (p.out_tma && __all_sync(0xffffffffu, out_to >= 0 && !bad)) {
+    const int turn = E4M3 ? (lane >> 2) & 1 : (lane >> 1) & 3;  // swizzle
     if (lane == 0) bulk_wait_read<0>();
 #pragma unroll
     for (int c = 0; c < NB * 2; ++c) {
@@ -393,17 +397,10 @@ __device__ __forceinline__ void write_rows(const Params& p, const Item& it, cons
         if (c >= 2 && lane == 0) bulk_wait_read<1>();  // the buffer's columns before have been read out
         __syncwarp();
         uint8_t* buf = stage + (c & 1) * kOutBytes;
-        if (p.out_e4m3) {
 #pragma unroll
-          for (int u = 0; u < 2; ++u)  // 32-byte swizzle
-            *reinterpret_cast<uint4*>(buf + lane * 32 + ((u ^ ((lane >> 2) & 1)) << 4)) =
-                make_uint4(o[c][4 * u], o[c][4 * u + 1], o[c][4 * u + 2], o[c][4 * u + 3]);
-        } else {
-#pragma unroll
-          for (int u = 0; u < 4; ++u)  // 64-byte swizzle
-            *reinterpret_cast<uint4*>(buf + lane * 64 + ((u ^ ((lane >> 1) & 3)) << 4)) =
-                make_uint4(o[c][4 * u], o[c][4 * u + 1], o[c][4 * u + 2], o[c][4 * u + 3]);
-        }
+        for (int u = 0; u < kRow / 16; ++u)
+          *reinterpret_cast<uint4*>(buf + lane * kRow + ((u ^ turn) << 4)) =
+              make_uint4(o[c][4 * u], o[c][4 * u + 1], o[c][4 * u + 2], o[c][4 * u + 3]);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -412,48 +409,49 @@ __device__ __forceinline__ void write_rows(const Params& p, const Item& it, cons
         }
       }
     }
-    return;
-  }
-  const int quarter = lane & 3;
-  long long to[4];  // the four rows' places
+  } else if constexpr (!E4M3) {
+    if (out_to >= 0)
 #pragma unroll
-  for (int k = 0; k < 4; ++k) to[k] = __shfl_sync(0xffffffffu, out_to, (lane & 28) + k);
-  const int regs = p.out_e4m3 ? 2 : 4;  // of eight columns
+      for (int g = 0; g < NB * 8; ++g)
+        if (8 * g < p.D)
+          *reinterpret_cast<uint4*>(static_cast<__half*>(p.o) + out_to + 8 * g) = make_uint4(
+              o[g >> 2][4 * (g & 3)], o[g >> 2][4 * (g & 3) + 1], o[g >> 2][4 * (g & 3) + 2], o[g >> 2][4 * (g & 3) + 3]);
+  } else if constexpr (E4M3) {
+    const int quarter = lane & 3;
+    long long to[4];  // the four rows' places
 #pragma unroll
-  for (int c = 0; c < NB * 2; ++c) {
-    if (32 * c < p.D) {
-      uint32_t v[4][4];
+    for (int k = 0; k < 4; ++k) to[k] = __shfl_sync(0xffffffffu, out_to, (lane & 28) + k);
 #pragma unroll
-      for (int g = 0; g < 4; ++g)
+    for (int c = 0; c < NB * 2; ++c) {
+      if (32 * c < p.D) {
+        uint32_t v[4][2];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[g][e] = p.out_e4m3 ? o[c][2 * g + (e & 1)] : o[c][4 * g + e];
+        for (int g = 0; g < 4; ++g) v[g][0] = o[c][2 * g], v[g][1] = o[c][2 * g + 1];
 #pragma unroll
-      for (int x = 1; x < 4; x <<= 1)  // transpose the quarters among the four lanes
+        for (int x = 1; x < 4; x <<= 1)  // transpose the quarters among the four lanes
 #pragma unroll
-        for (int g = 0; g < 4; ++g)
-          if (!(g & x))
+          for (int g = 0; g < 4; ++g)
+            if (!(g & x))
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (e < regs) {
+              for (int e = 0; e < 2; ++e) {
                 const bool high = lane & x;
                 const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? v[g][e] : v[g ^ x][e], x);
                 if (high) v[g][e] = got;
                 else v[g ^ x][e] = got;
               }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (to[k] < 0 || 32 * c + 8 * quarter >= p.D) continue;
-        const long long at = to[k] + 32 * c + 8 * quarter;
-        if (p.out_e4m3) *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.o) + at) = make_uint2(v[k][0], v[k][1]);
-        else *reinterpret_cast<uint4*>(static_cast<__half*>(p.o) + at) = make_uint4(v[k][0], v[k][1], v[k][2], v[k][3]);
+        for (int k = 0; k < 4; ++k)
+          if (to[k] >= 0 && 32 * c + 8 * quarter < p.D)
+            *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.o) + to[k] + 32 * c + 8 * quarter) =
+                make_uint2(v[k][0], v[k][1]);
       }
     }
+    __syncwarp();  // (a row written again comes after the other lanes' stores to it)
   }
-  __syncwarp();  // (a row written again comes after the other lanes' stores to it)
   if (bad) write_again(p, it, out_to, how, w, r);
 }
 
-template <int NB, bool CAP, bool BIAS>
+template <int NB, bool CAP, bool BIAS, bool E4M3>
 // 10 warps: three share each of two SM sub-partitions, so a thread may hold at most
 // 16384 / (3 x 32) registers, rounded down to the allocation granule.
 __global__ void __maxnreg__(168)
@@ -759,7 +757,7 @@ __global__ void __maxnreg__(168)
         if (pending_keys && !__all_sync(0xffffffffu, wait_bar(bar(kBarOFull + w), (full - 1) & 1, abort_flag, p.err)))
           break;
         tc_fence_after();
-        write_rows<NB>(p, items[pending % kItems], to, stage, o_tm, m, l, out_to, out_how, w, r, [] {});
+        write_rows<NB, E4M3>(p, items[pending % kItems], to, stage, o_tm, m, l, out_to, out_how, w, r, [] {});
         done(pending);
         pending = -1;
       }
@@ -889,7 +887,7 @@ __global__ void __maxnreg__(168)
           // of this item, which overwrites O, waits for the arrival. Between the two O is only
           // loaded; its rows are written while the products run. (Written before the item's
           // first tile they took 4,000 to 6,000 cycles that nothing else ran in.)
-          write_rows<NB>(p, items[pending % kItems], to, stage, o_tm, m_before, l_before, to_before, how_before, w, r, arrive);
+          write_rows<NB, E4M3>(p, items[pending % kItems], to, stage, o_tm, m_before, l_before, to_before, how_before, w, r, arrive);
           done(pending);
           pending = -1;
         } else {
@@ -922,9 +920,9 @@ sv_status packed_map(CUtensorMap* m, const void* ptr, int D, int heads, int rows
   return make_tmap(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, ptr, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <int NB, bool CAP, bool BIAS>
+template <int NB, bool CAP, bool BIAS, bool E4M3>
 sv_status packed_launch_as(const Params& p, int grid, cudaStream_t s) {
-  auto kern = packed_tile_kernel<NB, CAP, BIAS>;
+  auto kern = packed_tile_kernel<NB, CAP, BIAS, E4M3>;
   static unsigned long long attr_set = 0;  // the attribute is per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -956,10 +954,12 @@ sv_status packed_launch_as(const Params& p, int grid, cudaStream_t s) {
   return e == cudaSuccess ? SV_OK : cuda_fail(e, "packed attention launch");
 }
 
-template <int NB>
+template <int NB, bool E4M3>
 sv_status packed_launch(const Params& p, int grid, cudaStream_t s) {
-  if (p.cap > 0.0f) return p.slopes ? packed_launch_as<NB, true, true>(p, grid, s) : packed_launch_as<NB, true, false>(p, grid, s);
-  return p.slopes ? packed_launch_as<NB, false, true>(p, grid, s) : packed_launch_as<NB, false, false>(p, grid, s);
+  if (p.cap > 0.0f)
+    return p.slopes ? packed_launch_as<NB, true, true, E4M3>(p, grid, s) : packed_launch_as<NB, true, false, E4M3>(p, grid, s);
+  return p.slopes ? packed_launch_as<NB, false, true, E4M3>(p, grid, s)
+                  : packed_launch_as<NB, false, false, E4M3>(p, grid, s);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -971,7 +971,8 @@ sv_status tile_launch(const Params& p, cudaStream_t s) {
   const long long items = (p.total_q / (2 * p.qt) + p.docs) * static_cast<long long>(p.hk);
   int grid = num_sms() < kMaxSms ? num_sms() : kMaxSms;
   if (!p.counters && items < grid) grid = int(items);
-  return p.D > 64 ? packed_launch<2>(p, grid, s) : packed_launch<1>(p, grid, s);
+  if (p.out_e4m3) return p.D > 64 ? packed_launch<2, true>(p, grid, s) : packed_launch<1, true>(p, grid, s);
+  return p.D > 64 ? packed_launch<2, false>(p, grid, s) : packed_launch<1, false>(p, grid, s);
 }
 
 }  // namespace packed
@@ -1071,7 +1072,7 @@ sv_status sv_attention_packed(const void* q, const void* k, const void* v, void*
   p.err = dev_err();
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   p.qt = kTile / p.group;
-  // rows of a warp that are whole queries, and 16-byte strides of the output
+  // a warp's 32 output rows go by TMA where they are whole queries on 16 bytes
   p.out_tma = 32 % p.group == 0 && (!p.out_e4m3 || (head_dim % 16 == 0 && o_stride % 16 == 0));
   if (workspace) {
     p.counters = static_cast<unsigned*>(workspace);

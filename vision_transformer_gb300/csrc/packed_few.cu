@@ -428,123 +428,122 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? kCtasPerSm : 2) few_ker
       __threadfence();
       for (int x = lane; x < rows * chunks; x += 32)
         join(p, sg.doc, sg.row0, rows, x / chunks, 8 * (x % chunks), my_head, kvh, c0, c1, part);
-      continue;
-    }
-
-    // the four warps' sums, brought to one exponent
+    } else {
+      // the four warps' sums, brought to one exponent
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float x = l[n][e];
-        x += __shfl_xor_sync(0xffffffffu, x, 4);
-        x += __shfl_xor_sync(0xffffffffu, x, 8);
-        x += __shfl_xor_sync(0xffffffffu, x, 16);
-        if (g == 0) {
-          red_m[warp][8 * n + 2 * t + e] = m[n][e];
-          red_l[warp][8 * n + 2 * t + e] = x;
+        for (int e = 0; e < 2; ++e) {
+          float x = l[n][e];
+          x += __shfl_xor_sync(0xffffffffu, x, 4);
+          x += __shfl_xor_sync(0xffffffffu, x, 8);
+          x += __shfl_xor_sync(0xffffffffu, x, 16);
+          if (g == 0) {
+            red_m[warp][8 * n + 2 * t + e] = m[n][e];
+            red_l[warp][8 * n + 2 * t + e] = x;
+          }
         }
-      }
-    if (threadIdx.x < HEADS * kRows) row_bad[threadIdx.x] = 0;
-    __syncthreads();
+      if (threadIdx.x < HEADS * kRows) row_bad[threadIdx.x] = 0;
+      __syncthreads();
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      float f[2];
+      for (int n = 0; n < NT; ++n) {
+        float f[2];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = 8 * n + 2 * t + e;
-        float mx = red_m[my_head][r];
+        for (int e = 0; e < 2; ++e) {
+          const int r = 8 * n + 2 * t + e;
+          float mx = red_m[my_head][r];
 #pragma unroll
-        for (int k = 1; k < kSplit; ++k) mx = fmaxf(mx, red_m[my_head + k * HEADS][r]);
-        f[e] = ex2(m[n][e] - (mx == -INFINITY ? 0.0f : mx));
-      }
-#pragma unroll
-      for (int j = 0; j < 4 * VI; j += 2)  // four neighbouring dimensions of a row
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          *reinterpret_cast<float4*>(&red[warp][8 * n + 2 * t + e][64 * (j >> 2) + 8 * g + 2 * (j & 3)]) =
-              make_float4(o[n][j][e] * f[e], o[n][j][e + 2] * f[e], o[n][j + 1][e] * f[e], o[n][j + 1][e + 2] * f[e]);
-    }
-    __syncthreads();
-    // row x of the item's HEADS x rows: which head and row, query and query head
-    auto row_of = [&](int x, int& hw, int& r, int& i, int& head) {
-      hw = x / rows;
-      r = x - hw * rows;
-      i = (sg.row0 + r) / p.group;
-      head = (sg.kvh + hw) * p.group + (sg.row0 + r - i * p.group);
-    };
-    for (int x = int(threadIdx.x); x < HEADS * rows * chunks; x += kFewThreads) {
-      const int row = x / chunks, c = 8 * (x - row * chunks);
-      int hw, r, i, head;
-      row_of(row, hw, r, i, head);
-      float mx = red_m[hw][r], sum = 0.0f;
-#pragma unroll
-      for (int k = 1; k < kSplit; ++k) mx = fmaxf(mx, red_m[hw + k * HEADS][r]);
-      const float ref = mx == -INFINITY ? 0.0f : mx;
-#pragma unroll
-      for (int k = 0; k < kSplit; ++k) sum += ex2(red_m[hw + k * HEADS][r] - ref) * red_l[hw + k * HEADS][r];
-      const bool none = limit_of(p.causal, i + lk - sg.doc.lq, lk, sg.doc.prefix) == 0;
-      const float inv = whole ? 1.0f / sum : 1.0f;
-      float y[8], bad = 0.0f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        y[e] = red[hw][r][c + e];
-#pragma unroll
-        for (int k = 1; k < kSplit; ++k) y[e] += red[hw + k * HEADS][r][c + e];
-        y[e] = none ? 0.0f : y[e] * inv;
-        bad = fmaf(y[e], 0.0f, bad);
-      }
-      if (bad != 0.0f) row_bad[row] = 1;
-      if (whole) {
-        store8(p, size_t(sg.doc.q0 + i) * size_t(p.os) + size_t(head) * size_t(p.D) + size_t(c), y);
-      } else {
-        float* at_p = mine + size_t(row) * size_t(p.D + 2);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) __stcg(at_p + c + e, y[e]);
-        if (c == 0) {
-          __stcg(at_p + p.D, mx);
-          __stcg(at_p + p.D + 1, sum);
+          for (int k = 1; k < kSplit; ++k) mx = fmaxf(mx, red_m[my_head + k * HEADS][r]);
+          f[e] = ex2(m[n][e] - (mx == -INFINITY ? 0.0f : mx));
         }
+#pragma unroll
+        for (int j = 0; j < 4 * VI; j += 2)  // four neighbouring dimensions of a row
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            *reinterpret_cast<float4*>(&red[warp][8 * n + 2 * t + e][64 * (j >> 2) + 8 * g + 2 * (j & 3)]) =
+                make_float4(o[n][j][e] * f[e], o[n][j][e + 2] * f[e], o[n][j + 1][e] * f[e], o[n][j + 1][e + 2] * f[e]);
       }
-    }
-    __syncthreads();
-    if (int(threadIdx.x) < HEADS * rows && row_bad[threadIdx.x]) {
-      const int row = int(threadIdx.x);
-      int hw, r, i, head;
-      row_of(row, hw, r, i, head);
-      const int pos = i + lk - sg.doc.lq;
-      float acc[128], mx, sum;
-      row_again(p, p.q + static_cast<long long>(sg.doc.q0 + i) * p.qs + head * p.D,
-                p.k + sg.doc.k0 * p.ks + (sg.kvh + hw) * p.D, p.v + sg.doc.k0 * p.vs + (sg.kvh + hw) * p.D, sg.s0 * kStep,
-                min(last, limit_of(p.causal, pos, lk, sg.doc.prefix)), pos, p.slopes ? __ldg(p.slopes + head) : 0.0f, acc,
-                mx, sum);
-      for (int c = 0; c < p.D; c += 8) {
-        float y[8];
-        for (int e = 0; e < 8; ++e) y[e] = whole ? acc[c + e] / sum : acc[c + e];
-        if (whole) store8(p, size_t(sg.doc.q0 + i) * size_t(p.os) + size_t(head) * size_t(p.D) + size_t(c), y);
-        else
-          for (int e = 0; e < 8; ++e) __stcg(mine + size_t(row) * size_t(p.D + 2) + c + e, y[e]);
-      }
-      if (!whole) {
-        __stcg(mine + size_t(row) * size_t(p.D + 2) + p.D, mx);
-        __stcg(mine + size_t(row) * size_t(p.D + 2) + p.D + 1, sum);
-      }
-    }
-    if (whole) continue;
-
-    // the last CTA of the item's parts joins them, in order
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) seen = atomicInc(p.counters + c0 * 4, unsigned(c1 - c0));  // 0 .. c1 - c0, then 0 again
-    __syncthreads();
-    if (seen == unsigned(c1 - c0)) {
-      __threadfence();
+      __syncthreads();
+      // row x of the item's HEADS x rows: which head and row, query and query head
+      auto row_of = [&](int x, int& hw, int& r, int& i, int& head) {
+        hw = x / rows;
+        r = x - hw * rows;
+        i = (sg.row0 + r) / p.group;
+        head = (sg.kvh + hw) * p.group + (sg.row0 + r - i * p.group);
+      };
       for (int x = int(threadIdx.x); x < HEADS * rows * chunks; x += kFewThreads) {
-        const int row = x / chunks, hw = row / rows;
-        join(p, sg.doc, sg.row0, rows, row - hw * rows, 8 * (x - row * chunks), hw, sg.kvh + hw, c0, c1, part);
+        const int row = x / chunks, c = 8 * (x - row * chunks);
+        int hw, r, i, head;
+        row_of(row, hw, r, i, head);
+        float mx = red_m[hw][r], sum = 0.0f;
+#pragma unroll
+        for (int k = 1; k < kSplit; ++k) mx = fmaxf(mx, red_m[hw + k * HEADS][r]);
+        const float ref = mx == -INFINITY ? 0.0f : mx;
+#pragma unroll
+        for (int k = 0; k < kSplit; ++k) sum += ex2(red_m[hw + k * HEADS][r] - ref) * red_l[hw + k * HEADS][r];
+        const bool none = limit_of(p.causal, i + lk - sg.doc.lq, lk, sg.doc.prefix) == 0;
+        const float inv = whole ? 1.0f / sum : 1.0f;
+        float y[8], bad = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          y[e] = red[hw][r][c + e];
+#pragma unroll
+          for (int k = 1; k < kSplit; ++k) y[e] += red[hw + k * HEADS][r][c + e];
+          y[e] = none ? 0.0f : y[e] * inv;
+          bad = fmaf(y[e], 0.0f, bad);
+        }
+        if (bad != 0.0f) row_bad[row] = 1;
+        if (whole) {
+          store8(p, size_t(sg.doc.q0 + i) * size_t(p.os) + size_t(head) * size_t(p.D) + size_t(c), y);
+        } else {
+          float* at_p = mine + size_t(row) * size_t(p.D + 2);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) __stcg(at_p + c + e, y[e]);
+          if (c == 0) {
+            __stcg(at_p + p.D, mx);
+            __stcg(at_p + p.D + 1, sum);
+          }
+        }
       }
+      __syncthreads();
+      if (int(threadIdx.x) < HEADS * rows && row_bad[threadIdx.x]) {
+        const int row = int(threadIdx.x);
+        int hw, r, i, head;
+        row_of(row, hw, r, i, head);
+        const int pos = i + lk - sg.doc.lq;
+        float acc[128], mx, sum;
+        row_again(p, p.q + static_cast<long long>(sg.doc.q0 + i) * p.qs + head * p.D,
+                  p.k + sg.doc.k0 * p.ks + (sg.kvh + hw) * p.D, p.v + sg.doc.k0 * p.vs + (sg.kvh + hw) * p.D, sg.s0 * kStep,
+                  min(last, limit_of(p.causal, pos, lk, sg.doc.prefix)), pos, p.slopes ? __ldg(p.slopes + head) : 0.0f, acc,
+                  mx, sum);
+        for (int c = 0; c < p.D; c += 8) {
+          float y[8];
+          for (int e = 0; e < 8; ++e) y[e] = whole ? acc[c + e] / sum : acc[c + e];
+          if (whole) store8(p, size_t(sg.doc.q0 + i) * size_t(p.os) + size_t(head) * size_t(p.D) + size_t(c), y);
+          else
+            for (int e = 0; e < 8; ++e) __stcg(mine + size_t(row) * size_t(p.D + 2) + c + e, y[e]);
+        }
+        if (!whole) {
+          __stcg(mine + size_t(row) * size_t(p.D + 2) + p.D, mx);
+          __stcg(mine + size_t(row) * size_t(p.D + 2) + p.D + 1, sum);
+        }
+      }
+      if (whole) continue;
+
+      // the last CTA of the item's parts joins them, in order
+      __threadfence();
+      __syncthreads();
+      if (threadIdx.x == 0) seen = atomicInc(p.counters + c0 * 4, unsigned(c1 - c0));  // 0 .. c1 - c0, then 0 again
+      __syncthreads();
+      if (seen == unsigned(c1 - c0)) {
+        __threadfence();
+        for (int x = int(threadIdx.x); x < HEADS * rows * chunks; x += kFewThreads) {
+          const int row = x / chunks, hw = row / rows;
+          join(p, sg.doc, sg.row0, rows, row - hw * rows, 8 * (x - row * chunks), hw, sg.kvh + hw, c0, c1, part);
+        }
+      }
+      __syncthreads();  // `seen` and the merge buffers are free again
     }
-    __syncthreads();  // `seen` and the merge buffers are free again
   }
 }
 

@@ -158,7 +158,6 @@ __host__ __device__ constexpr size_t rope_smem(int head_dim, int parts) {
 template <int V, int NORM>
 __global__ void __launch_bounds__(kRopeThreads, 2) rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kPer = Runs<V>::kPer, kRuns = Runs<V>::kRuns;
-  constexpr int kParts = NORM == kNormNone ? 1 : 2;  // queries, keys
   extern __shared__ __align__(128) uint8_t rope_shared[];
   __shared__ unsigned long long turns[SV_ROPE_MAX_PAIRS];
   __shared__ __align__(8) unsigned long long full[kRopeWarps][kBufs];
@@ -349,9 +348,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_kernel(const __grid_cons
     __syncwarp();
     if (lane == 0) {
       __half* dst = (now.part ? p.y[1] + now.row * p.ys[1] : p.y[0] + now.row * p.ys[0]) + now.h0 * p.head_dim;
-      asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(reinterpret_cast<uint64_t>(dst)),
-                   "r"(smem_u32(buf)), "r"(uint32_t(now.heads * p.head_dim * 2))
-                   : "memory");
+      bulk_store(dst, smem_u32(buf), uint32_t(now.heads * p.head_dim * 2));
       bulk_commit();
       if (n + kBufs - 1 < count) {
         bulk_wait_read<1>();  // the buffer of the job before has been read out
