@@ -384,3 +384,148 @@ def test_projection_norm_rotation_attention_projection(sv):
     assert (o.double() - oref).abs().max() <= 2.0 ** -8 * oref.abs().max()
     yref = oref @ w2.double().t() + b2.double() + x.double()
     assert (y.double() - yref).abs().max() <= 2.0 ** -8 * yref.abs().max()
+
+
+# many rows over key ranges of more than 8 tiles of 128 keys, with few heads: the ranges are divided among the SMs
+DIVIDED = [([40], [9000]), ([200, 3, 0], [5000, 40, 1500]), ([64, 64, 1], [3100, 0, 2300]), ([2500], [2500]),
+           ([2300], [1500]), ([17] * 4, [1100, 1025, 2049, 4097])]
+
+
+@pytest.mark.parametrize("lq,lk", DIVIDED)
+@pytest.mark.parametrize("hq,hk,d,out", [(8, 2, 128, "f16"), (2, 1, 72, "e4m3"), (10, 1, 64, "f16")])
+def test_divided_key_ranges(sv, lq, lk, hq, hk, d, out):
+    c = Case(lq, lk, hq, hk, d, seed=sum(lk) + d, tail=3)
+    c.check(c.run(sv, out=out), out=out)
+    c.check(c.run(sv, out=out, mask=1), out=out, mask=1)
+    prefix = [lk[0] // 2] * len(lq)
+    slopes = torch.linspace(0.0, 0.01, hq, device="cuda")
+    opt = dict(mask=1, prefix=prefix, slopes=slopes, softcap=4.0)
+    c.check(c.run(sv, out=out, **opt), out=out, **opt)
+    sv.sv_sync()
+
+
+@pytest.mark.parametrize("poison", [math.nan, math.inf])
+def test_hidden_values_in_divided_ranges(sv, poison):
+    """A key hidden from some of the rows of a part, keys that no row sees, and a neighbour's keys."""
+    lq, lk = [90, 60], [2600, 1300]
+    c = Case(lq, lk, 2, 1, 64, seed=33, lead=2, tail=3)
+    clean = _by_rows(c, 1)
+    hidden = [2600 - 30, 2600 - 31, 2600 + 1299]
+    for what in (c.k, c.v):
+        what[:2] = poison
+        what[-3:] = poison
+        for h in hidden:
+            what[2 + h] = poison
+    got = c.run(sv, mask=1)[2:2 + sum(lq)].double()
+    sv.sv_sync()
+    sees = torch.tensor([i + 2600 - 90 >= 2600 - 31 for i in range(90)] + [i == 59 for i in range(60)], device="cuda")
+    finite = torch.isfinite(got).all(1)
+    assert torch.equal(finite, ~sees)
+    err = (got - clean).abs()[~sees].amax(1)
+    assert (err <= 2.0 ** -9 * clean[~sees].abs().amax(1).clamp(min=1.0)).all()
+
+
+def test_divided_ranges_share_a_workspace(sv):
+    """Calls of either kernel, divided and whole, one behind another on one workspace, eager and replayed: the same
+    bits as with a workspace of their own."""
+    cases = [Case([40], [9000], 8, 2, 128, seed=1), Case([1, 1], [7000, 300], 8, 2, 128, seed=2),
+             Case([200, 3], [5000, 40], 2, 1, 72, seed=3), Case([300, 200], [300, 200], 4, 4, 64, seed=4),
+             Case([1, 2], [6000, 9000], 4, 4, 72, seed=5)]
+    want = [c.run(sv, mask=1) for c in cases]
+    for c, o in zip(cases, want):
+        c.check(o, mask=1)
+    ws = torch.zeros(max(c.ws.numel() for c in cases), dtype=torch.uint8, device="cuda")
+    outs = [torch.zeros_like(o) for o in want]
+    for c, o in zip(cases, outs):
+        c.run(sv, mask=1, workspace=ws, o=o)
+    keep = []
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for c, o in zip(cases[::-1], outs[::-1]):
+            c.run(sv, mask=1, workspace=ws, o=o)
+            keep.append(c.options)
+    for _ in range(4):
+        for o in outs:
+            o.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        for o, w in zip(outs, want):
+            assert torch.equal(o, w)
+    sv.sv_sync()
+
+
+def test_runs_of_empty_documents(sv):
+    """Documents without queries, without keys and without either, many in a row."""
+    lq = [0] * 5 + [130] + [0] * 40 + [1] + [20, 30] + [0] * 33 + [260] + [0] * 3
+    lk = [0, 9, 0, 0, 0] + [130] + [0, 3] * 20 + [5] + [0, 0] + [0] * 33 + [300] + [7] * 3
+    for hq in (12, 3):  # many rows a document on average, few
+        c = Case(lq, lk, hq, 3, 64, seed=6)
+        for mask in (0, 1):
+            c.check(c.run(sv, mask=mask), mask=mask)
+            c.check(c.run(sv, mask=mask, workspace=False, out="e4m3"), mask=mask, out="e4m3")
+    # items without keys one behind another, more than SMs
+    c = Case([40] * 300, [0] * 299 + [200], 4, 4, 64, seed=6)
+    c.check(c.run(sv, mask=1), mask=1)
+    c = Case([1, 0, 0, 2] * 100, [0, 0, 70, 0] * 99 + [0, 0, 70, 9], 4, 4, 72, seed=6)
+    c.check(c.run(sv), mask=0)
+    # nothing but empty documents, and keys that nobody asks for
+    c = Case([0] * 7 + [400], [0] * 8, 2, 2, 64, seed=6, tail=2)
+    c.check(c.run(sv))
+    c = Case([400, 3], [0, 0], 2, 2, 64, seed=6)
+    c.check(c.run(sv, mask=1), mask=1)
+    sv.sv_sync()
+
+
+@pytest.mark.parametrize("group", [1, 3, 4, 5, 6, 12, 32, 33])
+@pytest.mark.parametrize("d", [24, 64, 72, 128])
+@pytest.mark.parametrize("out,pad", [("f16", 8), ("e4m3", 8), ("e4m3", 16)])
+def test_output_rows(sv, group, d, out, pad):
+    """Ways for a row to leave: whole warps of whole queries or not, on 16 bytes or not, with a row stride; the
+    columns between the rows stay."""
+    lq, lk = [70, 1, 150, 33], [70, 90, 150, 20]
+    c = Case(lq, lk, 2 * group, 2, d, seed=group)
+    width = 2 * group * d
+    wide = torch.full((c.tq, width + pad), 0x7F if out == "e4m3" else math.nan, device="cuda",
+                      dtype=torch.uint8 if out == "e4m3" else torch.float16)
+    opt = sv.sv_attention_options(mask=1)
+    sv.sv_attention_packed(c.q, c.k, c.v, wide, c.q_off, c.k_off, 4, c.tq, c.tk, 2 * group, 2, d, options=opt,
+                           o_stride=width + pad, out_dtype=1 if out == "e4m3" else 0)
+    sv.sv_sync()
+    assert torch.equal(wide[:, width:].contiguous().view(torch.uint8),
+                       torch.full_like(wide[:, width:].contiguous(), 0x7F if out == "e4m3" else math.nan).view(torch.uint8))
+    c.check(wide[:, :width].contiguous(), out=out, mask=1)
+
+
+@pytest.mark.parametrize("hk", [1, 2, 4, 6, 7])
+@pytest.mark.parametrize("group,lq", [(1, [1, 1, 1, 1, 1]), (4, [3, 4, 1, 2, 4]), (1, [9, 1, 0, 30, 20])])
+def test_few_rows_of_narrow_heads(sv, hk, group, lq):
+    """Heads side by side in a block where there is much to read (the keys of documents cut anywhere), either number
+    of row tiles, more rows in one document than a tile has."""
+    lk = [9000, 17, 20000, 4001, 30003]
+    c = Case(lq, lk, hk * group, hk, 72, seed=hk)
+    a = c.run(sv, mask=1)
+    c.check(a, mask=1)
+    assert torch.equal(a, c.run(sv, mask=1, workspace=c.ws))
+    slopes = torch.linspace(0.0, 0.002, hk * group, device="cuda")
+    c.check(c.run(sv, out="e4m3", softcap=3.0, slopes=slopes), out="e4m3", softcap=3.0, slopes=slopes)
+    c.check(c.run(sv, workspace=False))
+    # a NaN that the first document's queries but its last do not see; all others of other documents do not either
+    c.v[9000 - 1] = math.nan
+    o = c.run(sv, mask=1)
+    seen = lq[0] - 1
+    assert not torch.isfinite(o[seen]).any()
+    rest = torch.cat([o[:seen], o[seen + 1:]])
+    assert torch.isfinite(rest).all()
+    want = torch.cat([a[:seen], a[seen + 1:]])
+    assert (rest.double() - want.double()).abs().max() <= 2.0 ** -9 * max(1.0, float(want.abs().max()))
+    sv.sv_sync()
+
+
+@pytest.mark.parametrize("hq,hk,d", [(8, 8, 128), (1, 1, 8), (16, 1, 64), (6, 6, 72)])
+def test_one_row_over_a_very_long_range(sv, hq, hk, d):
+    """One document's keys shared out among all blocks and joined."""
+    c = Case([1], [70001], hq, hk, d, seed=9)
+    a = c.run(sv)
+    c.check(a)
+    assert torch.equal(a, c.run(sv, workspace=c.ws))
+    sv.sv_sync()

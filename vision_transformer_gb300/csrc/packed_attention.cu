@@ -981,12 +981,18 @@ sv_status tile_launch(const Params& p, cudaStream_t s) {
 extern "C" {
 
 size_t sv_attention_packed_workspace(int docs, int total_q, int total_k, int q_heads, int kv_heads, int head_dim) {
-  (void)docs, (void)total_q, (void)total_k, (void)q_heads, (void)kv_heads;  // bounded by the grid alone
-  const size_t d = size_t(head_dim < 8 ? 8 : (head_dim > 128 ? 128 : head_dim));
-  const size_t tiles = sv::packed::kCounterBytes +
-                       size_t(sv::packed::kMaxSlots) * 2 * ((d + 15) / 16 * 16 + 2) * sv::packed::kTile * sizeof(float);
-  const size_t few = sv::packed::few_workspace(int(d));
-  return tiles > few ? tiles : few;
+  using namespace sv::packed;
+  if (docs < 1 || total_q < 0 || total_k < 0 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads ||
+      q_heads / kv_heads > 64 || head_dim < 1)
+    return kCounterBytes;  // (the call refuses these)
+  const int group = q_heads / kv_heads, d = head_dim > 128 ? 128 : (head_dim + 15) / 16 * 16;
+  if (few_rows(docs, total_q, group)) return few_workspace(d);
+  // parts of divided ranges: twice the grid at most (see Schedule), and twice the key tiles over
+  // the shortest part
+  const double pairs = double(total_q / (2 * (kTile / group))) + docs, tiles = double(total_k / kTile) + 1.0;
+  const double most = 2.0 * pairs * kv_heads * tiles / kMinSplit + 1.0;
+  const size_t slots = total_k <= kMinSplit * kTile ? 0 : size_t(most < kMaxSlots ? most : kMaxSlots);
+  return kCounterBytes + slots * 2 * size_t(d + 2) * kTile * sizeof(float);
 }
 
 sv_status sv_attention_packed(const void* q, const void* k, const void* v, void* o, const int* q_offsets,
@@ -1083,8 +1089,7 @@ sv_status sv_attention_packed(const void* q, const void* k, const void* v, void*
     return SV_ERR_UNSUPPORTED;
   }
   LaunchScope L(kKindAttn, 0.0, 0.0, s);
-  // few rows per document on average: bound by reading the keys and values, not by products
-  return static_cast<long long>(total_q) * p.group <= 16ll * docs ? few_launch(p, s) : tile_launch(p, s);
+  return few_rows(docs, total_q, p.group) ? few_launch(p, s) : tile_launch(p, s);
 }
 
 }  // extern "C"

@@ -36,7 +36,11 @@ struct Params {
   int* err;
 };
 
-// packed_few.cu
+// packed_few.cu, for few rows per document on average: bound by reading the keys and values, not by
+// products
+inline bool few_rows(int docs, int total_q, int group) {
+  return static_cast<long long>(total_q) * group <= 16ll * docs;
+}
 sv_status few_launch(const Params& p, cudaStream_t s);
 size_t few_workspace(int head_dim);
 
