@@ -223,9 +223,6 @@ class Schedule {
   int pairs_, tiles_, splits_, count_, incl_, slot_incl_;
 };
 
-// Adds the parts of a divided range to row r of tile w (query index i of the item, -1 none),
-// once this warp is the last of the range's CTAs to arrive: in the order of the parts, so that
-// the result does not depend on who is last.
 // A wait whose long form is one function for all of the kernel's waits: inlined, the waits alone
 // were a sixth of the code, and code that runs once an item then came from beyond the
 // instruction caches.
@@ -236,6 +233,9 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
   return mbar_try_wait(bar, parity) || wait_long(bar, parity, abort, err);
 }
 
+// Adds the parts of a divided range to row r of tile w (out_to: its place, -1 none),
+// once this warp is the last of the range's CTAs to arrive: in the order of the parts, so that
+// the result does not depend on who is last.
 __device__ __noinline__ void join_parts(const Params& p, const Item& it, long long out_to, int w, int r) {
   const int Dn = (p.D + 15) / 16 * 16;
   __threadfence();

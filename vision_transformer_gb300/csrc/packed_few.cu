@@ -24,6 +24,9 @@
 // the steps, so that any distribution of lengths fills the GPU. An item inside one share is
 // finished there; one that is cut goes in parts to the workspace, and the last CTA of its parts
 // joins them in order. A CTA has at most two such parts, at the start and at the end of its share.
+// One long range makes many parts (one query, 8 key heads of 128, 32768 keys: 57 a head), and what
+// joins them is alone on the GPU by then, bound by the latency of L2: sixteen parts are on their
+// way at a time (two at a time: 48 us for that call, now 31, its 134 MB being 20 us).
 #include "packed_attention.h"
 
 namespace sv {
@@ -156,29 +159,57 @@ class Share {
   long long chunk_, at_, end_, base_ = 0, total_ = 0, incl_;
 };
 
-// Columns c .. c + 7 of row r of the item's head hw (key head kvh), from its parts c0 .. c1 in order.
-template <typename F>
-__device__ __forceinline__ void join(const Params& p, const Document& doc, int row0, int rows, int r, int c, int hw,
-                                     int kvh, int c0, int c1, F part) {
-  const size_t at = size_t(hw * rows + r) * size_t(p.D + 2);
-  float mx = -INFINITY, sum = 0.0f, y[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-  for (int w = c0; w <= c1; ++w) mx = fmaxf(mx, __ldcg(part(w, w == c0) + at + p.D));
-  const float ref = mx == -INFINITY ? 0.0f : mx;
-#pragma unroll 2
-  for (int w = c0; w <= c1; ++w) {
-    const float* a = part(w, w == c0) + at;
-    const float f = ex2(__ldcg(a + p.D) - ref);
-    sum = fmaf(f, __ldcg(a + p.D + 1), sum);
+// The parts c0, c0 + 1, ... of a cut item: `rows_all` rows of D sums, then exponent and denominator of each.
+struct Parts {
+  const float* base;
+  size_t slot;  // values of a part's place; a CTA has two, at the start of its share and at its end
+  int n, D, rows_all;
+  __device__ __forceinline__ const float* at(int w) const { return base + (w == 0 ? 1 : 2 * w) * slot; }
+  // A row over the parts first, first + step, ... in order, sixteen of them on their way at a time (they
+  // come from L2, and nothing else hides its latency): the lane's columns 4 lane .. 4 lane + 3, and the
+  // row's exponent and denominator.
+  __device__ __forceinline__ float4 sums(int row, int lane, int first, int step, float& mx, float& sum) const {
+    float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    mx = -INFINITY;
+    sum = 0.0f;
+    for (int w0 = first; w0 < n; w0 += 16 * step) {
+      float4 v[16];
+      float2 ml[16];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = fmaf(f, __ldcg(a + c + e), y[e]);
+      for (int b = 0; b < 16; ++b) {
+        const int w = w0 + b * step;
+        ml[b] = make_float2(-INFINITY, 0.0f);
+        v[b] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (w < n) {
+          ml[b] = __ldcg(reinterpret_cast<const float2*>(at(w) + rows_all * D) + row);
+          v[b] = __ldcg(reinterpret_cast<const float4*>(at(w) + row * D) + min(lane, D / 4 - 1));
+        }
+      }
+      float up = mx;
+#pragma unroll
+      for (int b = 0; b < 16; ++b) up = fmaxf(up, ml[b].x);
+      const float ref = up == -INFINITY ? 0.0f : up, back = ex2(mx - ref);
+      mx = up;
+      sum *= back;
+      y = make_float4(y.x * back, y.y * back, y.z * back, y.w * back);
+#pragma unroll
+      for (int b = 0; b < 16; ++b) {
+        const float e = ex2(ml[b].x - ref);
+        sum = fmaf(e, ml[b].y, sum);
+        y.x = fmaf(e, v[b].x, y.x);
+        y.y = fmaf(e, v[b].y, y.y);
+        y.z = fmaf(e, v[b].z, y.z);
+        y.w = fmaf(e, v[b].w, y.w);
+      }
+    }
+    return y;
   }
-  const int i = (row0 + r) / p.group, head = kvh * p.group + (row0 + r - i * p.group);
-  const bool none = limit_of(p.causal, i + doc.lk - doc.lq, doc.lk, doc.prefix) == 0;
-  const float inv = 1.0f / sum;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) y[e] = none ? 0.0f : y[e] * inv;
-  store8(p, size_t(doc.q0 + i) * size_t(p.os) + size_t(head) * size_t(p.D) + size_t(c), y);
+};
+
+// Eight sums of a part, as they are.
+__device__ __forceinline__ void put_part(float* to, const float* y) {
+  __stcg(reinterpret_cast<float4*>(to), make_float4(y[0], y[1], y[2], y[3]));
+  __stcg(reinterpret_cast<float4*>(to) + 1, make_float4(y[4], y[5], y[6], y[7]));
 }
 
 // KI: 32-dimension groups of a key row, VI: 64-dimension groups of a value row, NT: 8-row
@@ -353,8 +384,26 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? kCtasPerSm : 2) few_ker
     auto part = [&](int cta, int end) {
       return p.partial + (size_t(cta) * 2 + end) * size_t(HEADS * kRows) * size_t(p.D + 2);
     };
-    float* mine = whole ? nullptr : part(int(blockIdx.x), sg.s0 == 0 ? 1 : 0);
+    float* mine = whole ? nullptr : part(int(blockIdx.x), sg.s0 == 0 ? 1 : 0);  // [row][D], then [row] exponent, denominator
+    float* mine_ml = mine + HEADS * kRows * p.D;
     const int c0 = share.cta_of(sg.base), c1 = share.cta_of(sg.base + sg.steps - 1);  // the item's parts
+    const Parts parts{part(c0, 0), size_t(HEADS * kRows) * size_t(p.D + 2), c1 - c0 + 1, p.D, HEADS * kRows};
+
+    // Row r of head hw of the item from all its parts, by one warp.
+    auto join_row = [&](int hw, int r) {
+      float mx, sum;
+      const float4 a = parts.sums(hw * rows + r, lane, 0, 1, mx, sum);
+      const int i = (sg.row0 + r) / p.group, head = (sg.kvh + hw) * p.group + (sg.row0 + r - i * p.group);
+      const bool none = limit_of(p.causal, i + lk - sg.doc.lq, lk, sg.doc.prefix) == 0;
+      const float inv = 1.0f / sum;
+      float y[8] = {a.x, a.y, a.z, a.w};  // and the next lane's four
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y[4 + j] = __shfl_down_sync(0xffffffffu, y[j], 1);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] = none ? 0.0f : y[j] * inv;
+      if (!(lane & 1) && lane < p.D / 4)
+        store8(p, size_t(sg.doc.q0 + i) * size_t(p.os) + size_t(head) * size_t(p.D) + size_t(4 * lane), y);
+    };
 
     if constexpr (kSplit == 1) {
       // A warp has its head's rows to itself: they go out from its registers, and the warps of the
@@ -367,7 +416,8 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? kCtasPerSm : 2) few_ker
           const int head = kvh * p.group + (sg.row0 + r - i * p.group);
           const bool live = r < rows;
           const size_t to = size_t(sg.doc.q0 + i) * size_t(p.os) + size_t(head) * size_t(p.D);
-          float* at_p = whole ? nullptr : mine + size_t(my_head * rows + r) * size_t(p.D + 2);
+          float* at_p = mine + (my_head * rows + r) * p.D;
+          float* at_ml = mine_ml + 2 * (my_head * rows + r);
           float sum = l[n][e];
           sum += __shfl_xor_sync(0xffffffffu, sum, 4);
           sum += __shfl_xor_sync(0xffffffffu, sum, 8);
@@ -385,17 +435,10 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? kCtasPerSm : 2) few_ker
               bad = fmaf(y[2 * j], 0.0f, fmaf(y[2 * j + 1], 0.0f, bad));
             }
             if (!live || 8 * v + g >= chunks) continue;
-            if (whole) {
-              store8(p, to + 8 * (8 * v + g), y);
-            } else {
-#pragma unroll
-              for (int j = 0; j < 8; ++j) __stcg(at_p + 8 * (8 * v + g) + j, y[j]);
-            }
+            if (whole) store8(p, to + 8 * (8 * v + g), y);
+            else put_part(at_p + 8 * (8 * v + g), y);
           }
-          if (live && !whole && g == 0) {
-            __stcg(at_p + p.D, m[n][e]);
-            __stcg(at_p + p.D + 1, sum);
-          }
+          if (live && !whole && g == 0) __stcg(reinterpret_cast<float2*>(at_ml), make_float2(m[n][e], sum));
           const unsigned rows_bad = __ballot_sync(0xffffffffu, live && bad != 0.0f);
           if (rows_bad) {  // again from the visible keys alone, a lane a row
             __syncwarp();
@@ -408,13 +451,9 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? kCtasPerSm : 2) few_ker
                 float y[8];
                 for (int j = 0; j < 8; ++j) y[j] = whole ? acc[c + j] / sum : acc[c + j];
                 if (whole) store8(p, to + c, y);
-                else
-                  for (int j = 0; j < 8; ++j) __stcg(at_p + c + j, y[j]);
+                else put_part(at_p + c, y);
               }
-              if (!whole) {
-                __stcg(at_p + p.D, mx);
-                __stcg(at_p + p.D + 1, sum);
-              }
+              if (!whole) __stcg(reinterpret_cast<float2*>(at_ml), make_float2(mx, sum));
             }
             __syncwarp();
           }
@@ -426,8 +465,7 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? kCtasPerSm : 2) few_ker
       if (lane == 0) arrived = atomicInc(p.counters + c0 * 4 + warp, unsigned(c1 - c0));  // 0 .. c1 - c0, then 0 again
       if (__shfl_sync(0xffffffffu, arrived, 0) != unsigned(c1 - c0)) continue;
       __threadfence();
-      for (int x = lane; x < rows * chunks; x += 32)
-        join(p, sg.doc, sg.row0, rows, x / chunks, 8 * (x % chunks), my_head, kvh, c0, c1, part);
+      for (int r = 0; r < rows; ++r) join_row(my_head, r);
     } else {
       // the four warps' sums, brought to one exponent
 #pragma unroll
@@ -496,13 +534,8 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? kCtasPerSm : 2) few_ker
         if (whole) {
           store8(p, size_t(sg.doc.q0 + i) * size_t(p.os) + size_t(head) * size_t(p.D) + size_t(c), y);
         } else {
-          float* at_p = mine + size_t(row) * size_t(p.D + 2);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) __stcg(at_p + c + e, y[e]);
-          if (c == 0) {
-            __stcg(at_p + p.D, mx);
-            __stcg(at_p + p.D + 1, sum);
-          }
+          put_part(mine + row * p.D + c, y);
+          if (c == 0) __stcg(reinterpret_cast<float2*>(mine_ml) + row, make_float2(mx, sum));
         }
       }
       __syncthreads();
@@ -520,13 +553,9 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? kCtasPerSm : 2) few_ker
           float y[8];
           for (int e = 0; e < 8; ++e) y[e] = whole ? acc[c + e] / sum : acc[c + e];
           if (whole) store8(p, size_t(sg.doc.q0 + i) * size_t(p.os) + size_t(head) * size_t(p.D) + size_t(c), y);
-          else
-            for (int e = 0; e < 8; ++e) __stcg(mine + size_t(row) * size_t(p.D + 2) + c + e, y[e]);
+          else put_part(mine + row * p.D + c, y);
         }
-        if (!whole) {
-          __stcg(mine + size_t(row) * size_t(p.D + 2) + p.D, mx);
-          __stcg(mine + size_t(row) * size_t(p.D + 2) + p.D + 1, sum);
-        }
+        if (!whole) __stcg(reinterpret_cast<float2*>(mine_ml) + row, make_float2(mx, sum));
       }
       if (whole) continue;
 
@@ -537,9 +566,37 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? kCtasPerSm : 2) few_ker
       __syncthreads();
       if (seen == unsigned(c1 - c0)) {
         __threadfence();
-        for (int x = int(threadIdx.x); x < HEADS * rows * chunks; x += kFewThreads) {
-          const int row = x / chunks, hw = row / rows;
-          join(p, sg.doc, sg.row0, rows, row - hw * rows, 8 * (x - row * chunks), hw, sg.kvh + hw, c0, c1, part);
+        if (HEADS * rows >= 4) {  // a warp a row
+          for (int row = warp; row < HEADS * rows; row += 4) join_row(row / rows, row % rows);
+        } else {  // every fourth part a warp
+          for (int row = 0; row < HEADS * rows; ++row) {
+            float mx, sum;
+            const float4 a = parts.sums(row, lane, warp, 4, mx, sum);
+            if (lane == 0) red_m[warp][row] = mx, red_l[warp][row] = sum;
+            if (lane < p.D / 4) *reinterpret_cast<float4*>(&red[warp][row][4 * lane]) = a;
+          }
+          __syncthreads();
+          for (int x = int(threadIdx.x); x < HEADS * rows * chunks; x += kFewThreads) {
+            const int row = x / chunks, c = 8 * (x - row * chunks);
+            int hw, r, i, head;
+            row_of(row, hw, r, i, head);
+            float mx = red_m[0][row], sum = 0.0f, y[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int k = 1; k < 4; ++k) mx = fmaxf(mx, red_m[k][row]);
+            const float ref = mx == -INFINITY ? 0.0f : mx;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float f = ex2(red_m[k][row] - ref);
+              sum = fmaf(f, red_l[k][row], sum);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) y[e] = fmaf(f, red[k][row][c + e], y[e]);
+            }
+            const bool none = limit_of(p.causal, i + lk - sg.doc.lq, lk, sg.doc.prefix) == 0;
+            const float inv = 1.0f / sum;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = none ? 0.0f : y[e] * inv;
+            store8(p, size_t(sg.doc.q0 + i) * size_t(p.os) + size_t(head) * size_t(p.D) + size_t(c), y);
+          }
         }
       }
       __syncthreads();  // `seen` and the merge buffers are free again
