@@ -21,9 +21,22 @@
 //   warps 2..5  softmax of tile 0, warps 6..9 of tile 1: a thread per row turns its S row into
 //               P (F16, over S in tensor memory), keeps the exponent and the sum in F32, and
 //               rescales O in tensor memory when the exponent rises by more than 2^15.
-// Key ranges are divided among CTAs when there are few items (Schedule); the parts' O, m and
-// l go to the caller's workspace and the last of them to arrive joins them in order.
+// An item's rows go out behind the next item's first tile: O is loaded between that tile's
+// softmax and the arrival of its P, and scaled, rounded and stored while the products run.
+// Items are handed out by tickets, the longest documents of every 32 first. Key ranges are
+// divided among CTAs when there are few items (Schedule); the parts' O, m and l go to the
+// caller's workspace and are joined two and two.
 // Tensor memory: S_0, S_1, O_0, O_1 of 128 columns each.
+//
+// What bounds it: the chain of one tile of 128 rows, softmax (about 1,400 cycles), the way of P
+// to the issuer and of S back (500), the products P V and S (760 at 72 dimensions, 1,024 at 128);
+// two tiles a CTA run half a period apart, so that a pair of tiles takes 2,700 to 3,000 cycles, of
+// which the tensor cores work 1,331 (72) or 2,048 (128). Tried against it and slower: P handed over
+// in two halves, two warps for 32 rows, one arrival a warp, two issuers, warps of their own for
+// the output. The code of an item is as long as the instruction caches: what runs rarely is
+// out of line.
+// 32 images of 729 tokens, 16 heads of 72: 127 us (614 TFLOP/s of the products of visible keys);
+// one sequence of 8192 tokens behind the prefix mask, 32 heads of 128 over 8: 371 us, 1,480 TFLOP/s.
 #include <cmath>
 
 #include "packed_attention.h"
@@ -194,15 +207,19 @@ class Schedule {
   // Lane i takes the document with the i-th most key tiles of the 32 (equal ones in order): long
   // items come early, and the last ones to be handed out are short.
   __device__ __forceinline__ void longest_first() {
-    int rank = 0, from = 0;
+    // (equal ones, or one alone, are in order; a bitonic sort of tiles and lane in one word otherwise: every
+    // CTA of the launch waits for this)
+    const int before = __shfl_up_sync(0xffffffffu, tiles_, 1);
+    if (!__any_sync(0xffffffffu, lane_ > 0 && tiles_ > before)) return;
+    int key = tiles_ << 5 | (31 - lane_);  // (at most 2^24 tiles)
 #pragma unroll 1
-    for (int i = 0; i < 32; ++i) {
-      const int t = __shfl_sync(0xffffffffu, tiles_, i);
-      rank += t > tiles_ || (t == tiles_ && i < lane_);
-    }
+    for (int k = 2; k <= 32; k *= 2)
 #pragma unroll 1
-    for (int i = 0; i < 32; ++i)
-      if (__shfl_sync(0xffffffffu, rank, i) == lane_) from = i;
+      for (int j = k / 2; j; j /= 2) {
+        const int other = __shfl_xor_sync(0xffffffffu, key, j);
+        key = ((lane_ & j) == 0) == ((lane_ & k) == 0) ? max(key, other) : min(key, other);
+      }
+    const int from = 31 - (key & 31);
     auto take = [&](int& v) { v = __shfl_sync(0xffffffffu, v, from); };
     take(doc_.q0);
     take(doc_.lq);
@@ -233,42 +250,62 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
   return mbar_try_wait(bar, parity) || wait_long(bar, parity, abort, err);
 }
 
-// Adds the parts of a divided range to row r of tile w (out_to: its place, -1 none),
-// once this warp is the last of the range's CTAs to arrive: in the order of the parts, so that
-// the result does not depend on who is last.
+// Joins the parts of a divided range for row r of tile w (out_to: its place, -1 none), two at a time
+// along a binary tree over the parts: of two neighbours the warp that arrives second adds them, on
+// the left one's place, and goes on with the sum; the last one of all writes the row. So the joins
+// of a long range run on many SMs (by the last of all parts alone, in order: 40 queries of 8 heads
+// over 32768 keys of 2, 64 parts, 184 us; so 67), and the order of the sums is the tree's, whoever is
+// second.
 __device__ __noinline__ void join_parts(const Params& p, const Item& it, long long out_to, int w, int r) {
-  const int Dn = (p.D + 15) / 16 * 16;
-  __threadfence();
-  __syncwarp();
-  unsigned seen = 0;
-  const int first = it.slot - it.split;
-  if ((r & 31) == 0)  // counts 0 .. splits - 1 and starts again at 0
-    seen = atomicInc(p.counters + size_t(first) * 8 + (w * 4 + (r >> 5)), unsigned(it.splits - 1));
-  seen = __shfl_sync(0xffffffffu, seen, 0);
-  if (seen != unsigned(it.splits - 1)) return;
-  __threadfence();
-  if (out_to < 0) return;
-  const float* base = p.partial + (size_t(first) * 2 + w) * size_t(Dn + 2) * kTile + r;
-  const size_t stride = size_t(2) * size_t(Dn + 2) * kTile;  // to the next part
-  float mx = -INFINITY, sum = 0.0f;
-  for (int s = 0; s < it.splits; ++s) mx = fmaxf(mx, __ldcg(base + s * stride));
-  const float ref = mx == -INFINITY ? 0.0f : mx;
-  for (int s = 0; s < it.splits; ++s) sum += ex2(__ldcg(base + s * stride) - ref) * __ldcg(base + s * stride + kTile);
-  const int i = w * p.qt + r / p.group;
-  const bool none = limit_of(p.causal, it.at + i, it.lk, it.prefix) == 0;
-  const float inv = 1.0f / sum;
-  for (int c = 0; c < p.D; c += 8) {
-    float y[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-    for (int s = 0; s < it.splits; ++s) {
-      const float* b = base + s * stride;  // (the sums of a part without visible keys are 0)
-      const float f = ex2(__ldcg(b) - ref);
+  const int Dn = (p.D + 15) / 16 * 16, n = it.splits, first = it.slot - it.split;
+  auto place = [&](int part) {  // exponent, denominator, then the columns, kTile rows each
+    return p.partial + (size_t(first + part) * 2 + w) * size_t(Dn + 2) * kTile + r;
+  };
+  int left = it.split;  // the parts left .. left + step - 1 (below n) are summed at `left`
+#pragma unroll 1
+  for (int step = 1; step < n; step *= 2) {
+    int right = left + step;
+    if (left & step) right = left, left -= step;
+    if (right >= n) continue;  // (no neighbour on this level)
+    __threadfence();
+    __syncwarp();
+    unsigned seen = 0;
+    if ((r & 31) == 0)  // 0, then 1, and 0 again
+      seen = atomicInc(p.counters + size_t(first + right) * 8 + (w * 4 + (r >> 5)), 1u);
+    if (__shfl_sync(0xffffffffu, seen, 0) == 0) return;
+    __threadfence();
+    float* a = place(left);
+    const float* b = place(right);
+    const float ma = __ldcg(a), mb = __ldcg(b), la = __ldcg(a + kTile), lb = __ldcg(b + kTile);
+    const float mx = fmaxf(ma, mb), ref = mx == -INFINITY ? 0.0f : mx;
+    const float fa = ex2(ma - ref), fb = ex2(mb - ref), l = fmaf(fb, lb, fa * la);
+    const bool last = 2 * step >= n;
+    const int i = w * p.qt + r / p.group;
+    const bool none = limit_of(p.causal, it.at + i, it.lk, it.prefix) == 0;
+    const float inv = 1.0f / l;
+#pragma unroll 1
+    for (int c = 0; c < Dn; c += 16) {  // (what lies between D and Dn is read and of no use)
+      float y[16], yb[16];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = fmaf(f, __ldcg(b + size_t(2 + c + e) * kTile), y[e]);
+      for (int e = 0; e < 16; ++e) {
+        y[e] = __ldcg(a + (2 + c + e) * kTile);
+        yb[e] = __ldcg(b + (2 + c + e) * kTile);
+      }
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        y[e] = fmaf(fb, yb[e], fa * y[e]);
+        if (last) y[e] = none ? 0.0f : y[e] * inv;
+        else __stcg(a + (2 + c + e) * kTile, y[e]);
+      }
+      if (last && out_to >= 0) {
+        store8(p, size_t(out_to) + c, y);
+        if (c + 8 < p.D) store8(p, size_t(out_to) + c + 8, y + 8);
+      }
     }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = none ? 0.0f : y[e] * inv;
-    store8(p, size_t(out_to) + c, y);
+    if (!last) {
+      __stcg(a, mx);
+      __stcg(a + kTile, l);
+    }
   }
 }
 
