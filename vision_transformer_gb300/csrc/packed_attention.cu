@@ -109,7 +109,7 @@ class Schedule {
  public:
   __device__ __forceinline__ Schedule(const Params& p, int lane) : p_(p), lane_(lane), docs_(p.docs) {
     chunk_ = 0x7fffffff;
-    long long work = 0;
+    float work = 0.0f;
     bool bad = false;
 #pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {  // the work, then the items that it makes
@@ -118,16 +118,13 @@ class Schedule {
       for (int d0 = 0; d0 < docs_; d0 += 32) {
         load(d0);
         bad |= bad_;
-        work += static_cast<long long>(pairs_) * tiles_;
+        work += float(pairs_) * float(tiles_);
         items += count_;
       }
-#pragma unroll 1
-      for (int o = 16; o; o >>= 1) {
-        work += __shfl_xor_sync(0xffffffffu, work, o);
-        items += __shfl_xor_sync(0xffffffffu, items, o);
-      }
-      items_ = items;
+      items_ = int(__reduce_add_sync(0xffffffffu, unsigned(items)));
       if (pass == 0) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) work += __shfl_xor_sync(0xffffffffu, work, o);
         // offsets that decrease or leave [0, total]: reported, and nothing is computed, since
         // the bounds on items and parts hold for documents that do not overlap
         if (__any_sync(0xffffffffu, bad)) {
@@ -135,8 +132,9 @@ class Schedule {
           docs_ = 0;
         }
         if (!p.counters) break;  // nothing is divided, and no tickets are drawn
-        // work x heads / grid, rounded up (F32: a little more does no harm)
-        const float share = float(work) * float(p.hk) * (1.000001f / float(gridDim.x));
+        // work x heads / grid, rounded up (F32 sums of up to 2^24 documents, 32 lanes apart: a little more
+        // does no harm)
+        const float share = work * float(p.hk) * (1.1f / float(gridDim.x));
         chunk_ = max(kMinSplit, int(fminf(share, 1e9f)) + 1);
       }
     }
@@ -161,11 +159,17 @@ class Schedule {
       longest_first();
       incl_ = count_;
       slot_incl_ = splits_ > 1 ? count_ : 0;
-#pragma unroll 1
+#pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int a = __shfl_up_sync(0xffffffffu, incl_, o), b = __shfl_up_sync(0xffffffffu, slot_incl_, o);
-        if (lane_ >= o) incl_ += a, slot_incl_ += b;
+        const int a = __shfl_up_sync(0xffffffffu, incl_, o);
+        if (lane_ >= o) incl_ += a;
       }
+      if (__any_sync(0xffffffffu, splits_ > 1))
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int a = __shfl_up_sync(0xffffffffu, slot_incl_, o);
+          if (lane_ >= o) slot_incl_ += a;
+        }
       total_ = __shfl_sync(0xffffffffu, incl_, 31);
       slot_total_ = __shfl_sync(0xffffffffu, slot_incl_, 31);
     }
