@@ -394,7 +394,8 @@ sv_status sv_rope_plan_init(sv_rope_plan* plan, int rot_dim, int axes, int layou
  * heads * head_dim and a multiple of 8). y may be x (with the same stride); other overlaps are not allowed.
  * positions: int32 [axes, rows], any values (negative ones too); the angle of a far position loses nothing to its
  * size (whole turns are dropped in 64-bit fixed point).
- * Requirements: head_dim a multiple of 8, 8 <= head_dim <= 256, plan->rot_dim <= head_dim; rows 0 is no work.
+ * Requirements: head_dim a multiple of 8, 8 <= head_dim <= 256, plan->rot_dim <= head_dim, heads <= 2^20; rows 0 is
+ * no work.
  * Errors: SV_ERR_INVALID_ARG, SV_ERR_CUDA.
  */
 sv_status sv_rope(const void* x, void* y, const int* positions, const sv_rope_plan* plan, int rows, int heads,
@@ -438,7 +439,10 @@ typedef struct {
   const float* slopes; /* f32 [q_heads]: scores of head h lose slopes[h] * |p_i - j|, after the cap; NULL: none */
 } sv_attention_options;
 
-/* Bytes of workspace with which sv_attention_packed may divide long key ranges among the SMs. Host only. */
+/*
+ * Bytes of workspace with which sv_attention_packed hands out its work and divides long key ranges among the SMs, for
+ * these sizes and every smaller total_k: 10 KB where there is nothing to divide, 41 MB at most. Host only.
+ */
 size_t sv_attention_packed_workspace(int docs, int total_q, int total_k, int q_heads, int kv_heads, int head_dim);
 
 /*
@@ -456,12 +460,16 @@ size_t sv_attention_packed_workspace(int docs, int total_q, int total_k, int q_h
  * total_k / docs. Rows of o outside every document are left as they were. With offsets that
  * decrease or leave [0, total] the call computes nothing, and the next sv_sync reports SV_ERR_INVALID_ARG.
  * workspace: NULL, or sv_attention_packed_workspace() bytes of device memory, 16-byte aligned, that were zero before
- * their first use by this function; every call leaves what the next one needs, of the same sizes or others. Without
- * it, results are the same up to rounding, but few queries over many keys use few SMs. Calls that may run at the same
- * time (other streams, or graphs that replay side by side) need workspaces of their own.
+ * their first use by this function; every call leaves what the next one needs, of the same sizes or others (but zero
+ * it again after sv_sync has reported SV_ERR_TIMEOUT). Without it, results are the same up to rounding, but few
+ * queries over many keys use few SMs. Calls that may run at the same time (other streams, or graphs that replay side
+ * by side) need workspaces of their own.
  * The same call gives the same bits every time.
- * Requirements: head_dim a multiple of 8 in [8, 128]; q_heads / kv_heads <= 64; docs >= 1; total_q, total_k >= 0.
- * Errors: SV_ERR_INVALID_ARG; SV_ERR_UNSUPPORTED (head_dim, heads), SV_ERR_CUDA.
+ * Documents of up to 16 rows on average (queries x q_heads / kv_heads) are taken to be bound by reading their keys,
+ * others by their products: single queries over long caches and long prompts are faster in two calls than in one.
+ * Requirements: head_dim a multiple of 8 in [8, 128]; q_heads / kv_heads <= 64, q_heads <= 65536; 1 <= docs <= 2^24;
+ * total_q, total_k >= 0, below 2^31 - 4096; (total_q / (256 / (q_heads / kv_heads)) + docs) * kv_heads below 2^30.
+ * Errors: SV_ERR_INVALID_ARG; SV_ERR_UNSUPPORTED (head_dim, heads, sizes), SV_ERR_CUDA.
  */
 sv_status sv_attention_packed(const void* q, const void* k, const void* v, void* o, const int* q_offsets,
                               const int* k_offsets, int docs, int total_q, int total_k, int q_heads, int kv_heads,

@@ -46,3 +46,22 @@ def test_workspace_is_bounded(vt, docs, tq, tk, hq, hk, d):
     """The workspace does not grow with the sequences."""
     n = vt.sv_attention_packed_workspace(docs, tq, tk, hq, hk, d)
     assert 0 < n <= 64 << 20
+
+
+def test_sizes_too_large_for_one_call(vt):
+    """Turned down before any device work, whatever the pointers."""
+    buf = (ctypes.c_uint8 * 4096)()
+    p = (ctypes.addressof(buf) + 15) // 16 * 16
+    lib = vt.load()
+    most = 2 ** 31 - 1 - 4096
+    for docs, tq, tk, hq, hk in ((1, most + 1, 4, 1, 1), (1, 4, most + 1, 1, 1), (2 ** 24 + 1, 4, 4, 1, 1),
+                                 (1, most, 4, 1024, 1024), (2 ** 24, 4, 4, 128, 64)):
+        assert lib.sv_attention_packed(p, p, p, p, p, p, docs, tq, tk, hq, hk, 8, 0, 0, 0, 0, None, 0, None, 0,
+                                       None) == vt.SV_ERR_UNSUPPORTED, (docs, tq, tk, hq, hk)
+
+
+@pytest.mark.parametrize("tq,hq,hk", [(64, 16, 16), (4096, 32, 8)])
+def test_workspace_of_smaller_key_totals(vt, tq, hq, hk):
+    """The workspace does not shrink as total_k grows."""
+    sizes = [vt.sv_attention_packed_workspace(4, tq, tk, hq, hk, 72) for tk in (0, 1, 1024, 1025, 5000, 10 ** 5, 10 ** 9)]
+    assert sizes == sorted(sizes)

@@ -71,3 +71,14 @@ def test_call_refusals(vt):
     assert rope(plan=broken) == bad and b"sv_rope_plan_init" in lib.sv_last_error()
     # no rows is no work
     assert rope(rows=0) == vt.SV_OK and qk(rows=0) == vt.SV_OK
+
+
+def test_too_many_heads(vt):
+    buf = (ctypes.c_uint8 * 4096)()
+    p = (ctypes.addressof(buf) + 15) // 16 * 16
+    plan = vt.sv_rope_plan_init(8)
+    lib = vt.load()
+    assert lib.sv_rope(p, p, p, plan, 1, 2 ** 20 + 1, 8, 0, 0, None) == vt.SV_ERR_INVALID_ARG
+    for hq, hk in ((2 ** 20 + 1, 1), (1, 2 ** 20 + 1)):
+        assert lib.sv_qk_norm_rope(p, p, p, p, None, None, 0, 1e-6, p, plan, 1, hq, hk, 8, 0, 0, 0, 0,
+                                   None) == vt.SV_ERR_INVALID_ARG

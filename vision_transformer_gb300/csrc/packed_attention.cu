@@ -1055,6 +1055,13 @@ sv_status sv_attention_packed(const void* q, const void* k, const void* v, void*
               q_heads, kv_heads);
     return SV_ERR_UNSUPPORTED;
   }
+  constexpr int kMostRows = 0x7fffffff - 4096;  // (key and row numbers run past the last by less than that)
+  if (total_q > kMostRows || total_k > kMostRows || docs > (1 << 24) ||
+      (total_q / (2 * (kTile * kv_heads / q_heads)) + static_cast<long long>(docs)) * kv_heads >= (1ll << 30)) {
+    set_error("%s: %d documents of %d queries with %d heads and %d keys are too many for one call", fn, docs, total_q,
+              q_heads, total_k);
+    return SV_ERR_UNSUPPORTED;
+  }
   if ((!q_offsets && total_q % docs) || (!k_offsets && total_k % docs)) {
     set_error("%s: without offsets, %d queries and %d keys must divide by %d documents", fn, total_q, total_k, docs);
     return SV_ERR_INVALID_ARG;
@@ -1124,10 +1131,6 @@ sv_status sv_attention_packed(const void* q, const void* k, const void* v, void*
   if (workspace) {
     p.counters = static_cast<unsigned*>(workspace);
     p.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + kCounterBytes);
-  }
-  if (docs > (1 << 24) || (total_q / (2 * p.qt) + static_cast<long long>(docs)) * kv_heads > (1ll << 30)) {
-    set_error("%s: %d documents of %d queries with %d heads are too many for one call", fn, docs, total_q, q_heads);
-    return SV_ERR_UNSUPPORTED;
   }
   LaunchScope L(kKindAttn, 0.0, 0.0, s);
   return few_rows(docs, total_q, p.group) ? few_launch(p, s) : tile_launch(p, s);
