@@ -35,8 +35,8 @@
 // in two halves, two warps for 32 rows, one arrival a warp, two issuers, warps of their own for
 // the output. The code of an item is as long as the instruction caches: what runs rarely is
 // out of line.
-// 32 images of 729 tokens, 16 heads of 72: 127 us (614 TFLOP/s of the products of visible keys);
-// one sequence of 8192 tokens behind the prefix mask, 32 heads of 128 over 8: 371 us, 1,480 TFLOP/s.
+// 32 images of 729 tokens, 16 heads of 72: 120 us (650 TFLOP/s of the products of visible keys);
+// one sequence of 8192 tokens behind the prefix mask, 32 heads of 128 over 8: 370 us, 1,490 TFLOP/s.
 #include <cmath>
 
 #include "packed_attention.h"
@@ -54,8 +54,8 @@ constexpr int kItems = 4;                   // work items between the copy warp 
 constexpr uint32_t kTmemCols = 512;
 constexpr int kMaxSlots = 2 * kMaxSms;      // partial results of a launch at most (see Schedule)
 // Key tiles of a part of a divided range at least: below, the parts' way through the workspace
-// costs more than their length (one image of 729 tokens, 16 heads: 48 items of 6 tiles 18.4 us,
-// 144 parts of 2 tiles 37.8 us).
+// costs more than their length (40 queries over 2048 keys: two parts of 8 tiles 34 us, 16 tiles in a
+// row 32; one image of 729 tokens, 16 heads: 48 items of 6 tiles 16 us, 144 parts of 2 tiles 38 us).
 constexpr int kMinSplit = 8;
 static_assert(kCounterBytes >= size_t(kMaxSlots) * 8 * sizeof(unsigned), "counters");
 
@@ -142,11 +142,12 @@ class Schedule {
   // The CTA's first item is its own number, the others go to whoever is free, by a ticket from
   // the workspace: CTAs draw until they are refused, `items` tickets in all, and the counter
   // is back at 0. Without a workspace every CTA takes every gridDim-th item.
-  __device__ __forceinline__ int after(int it) const {
-    if (!p_.counters) return it + int(gridDim.x);
-    unsigned t = 0;
-    if (lane_ == 0) t = atomicInc(p_.counters + kTicket, unsigned(items_ - 1));
-    return int(gridDim.x) + int(__shfl_sync(0xffffffffu, t, 0));
+  __device__ __forceinline__ unsigned draw() const {  // (one lane; the answer takes a microsecond)
+    return p_.counters ? atomicInc(p_.counters + kTicket, unsigned(items_ - 1)) : 0u;
+  }
+  // The number of the item after `it`, with lane 0's ticket.
+  __device__ __forceinline__ int after(int it, unsigned ticket) const {
+    return int(gridDim.x) + (p_.counters ? int(__shfl_sync(0xffffffffu, ticket, 0)) : it);
   }
   // Item number `it` (increasing from call to call); false behind the last.
   __device__ __forceinline__ bool get(int it, Item& r) {
@@ -385,7 +386,7 @@ __device__ __noinline__ void write_special(const Params& p, const Item& it, uint
 // when O has left tensor memory. Where a warp's 32 rows are all the item's and make whole queries
 // (p.out_tma) they go out by TMA from shared memory (`stage`: two buffers), 32 columns at a time;
 // the rows of a part-filled warp are stored by their lanes (a bulk copy a row instead: 134 against
-// 128 us for 32 images of 729 tokens). E4M3 rows that do not start on 16 bytes are stored in runs,
+// 128 us then for 32 images of 729 tokens). E4M3 rows that do not start on 16 bytes are stored in runs,
 // after four lanes, which hold four rows, have exchanged quarters of 32 columns. (All rows by their
 // lanes: 24 us for 23,328 rows of 16 heads of 72 by itself, and the load-store unit held up for
 // everything else meanwhile.)
@@ -566,8 +567,9 @@ __global__ void __maxnreg__(168)
     // The next item, written for the other warps. (It waits for the item four before to be
     // written out, so it must not come before copies that this depends on.)
     int number = int(blockIdx.x);  // of the next item
+    unsigned ticket = 0;           // lane 0's, for the one after
     auto tell = [&](Item& r) -> int {
-      if (told > 0) number = sched.after(number);
+      if (told > 0) number = sched.after(number, ticket);
       r.live = sched.get(number, r);
       const int slot = told % kItems;
       int ok = wait_bar(bar(kBarItemDone + slot), ((told / kItems) & 1) ^ 1, abort_flag, p.err);
@@ -582,8 +584,15 @@ __global__ void __maxnreg__(168)
     Item it;
     int ok = 1;
     while (ok && tell(it) && it.live) {
-      if (it.jb >= it.je) continue;
+      if (it.jb >= it.je) {
+        if (lane == 0) ticket = sched.draw();
+        continue;
+      }
       if (lane == 0) {
+        // The next item is drawn late, so that the work stays balanced, but where the ring is short before
+        // the last copies, whose room has to be waited for anyway (32 images: 124.5 -> 121.5 us; where it holds
+        // four key tiles, earlier than behind the last copy costs 2%).
+        const int copies = 2 * (it.je - it.jb), draw_at = NB == 1 ? copies : copies - 2;
         auto kv = [&](const CUtensorMap& map, int j) -> bool {
           const int st = t % kStages;
           const uint32_t ph = (t / kStages) & 1;
@@ -597,7 +606,8 @@ __global__ void __maxnreg__(168)
           return true;
         };
 #pragma unroll 1
-        for (int x = 0; ok && x < 2 * (it.je - it.jb); ++x) {  // a key tile, its values, the next key tile, ...
+        for (int x = 0; ok && x < copies; ++x) {  // a key tile, its values, the next key tile, ...
+          if (x == draw_at) ticket = sched.draw();
           ok = kv(x & 1 ? tv : tk, it.jb + (x >> 1));
           if (ok && x == 0) {
             const int qb = n % kQBufs;
@@ -613,6 +623,7 @@ __global__ void __maxnreg__(168)
             }
           }
         }
+        if (draw_at == copies) ticket = sched.draw();
       }
       ++n;
       ok = __shfl_sync(0xffffffffu, ok, 0);
