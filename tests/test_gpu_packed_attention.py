@@ -529,3 +529,24 @@ def test_one_row_over_a_very_long_range(sv, hq, hk, d):
     c.check(a)
     assert torch.equal(a, c.run(sv, workspace=c.ws))
     sv.sv_sync()
+
+
+@pytest.mark.parametrize("hq,hk,d,out", [(2, 2, 64, "f16"), (4, 1, 72, "e4m3"), (2, 2, 72, "f16"), (3, 1, 128, "e4m3")])
+@pytest.mark.parametrize("steps", [1, 40, 64, 200])
+def test_rising_and_falling_scores(sv, hq, hk, d, out, steps):
+    """Scores that rise by hundreds along the keys, evenly or in steps, so that a row's exponent is raised again and
+    again, between tiles and inside them; and the same keys the other way round."""
+    lens = [300, 70, 129]
+    c = Case(lens, lens, hq, hk, d, seed=steps)
+    u = torch.sign(_randn(steps + 1, d)).half()
+    at = torch.cat([torch.arange(n) for n in lens]).cuda()
+    ramp = (at // steps * steps).float()[:, None] / 25.0
+    for flip in (False, True):
+        c.q.copy_((u.float() + 0.05 * _randn(2, c.tq, hq, d)).reshape(c.tq, hq * d))
+        c.k.copy_(((12.0 - ramp if flip else ramp)[:, None] * u.float() + 0.05 * _randn(3, c.tk, hk, d))
+                  .reshape(c.tk, hk * d))
+        c.check(c.run(sv, out=out), out=out)
+        c.check(c.run(sv, out=out, mask=1), out=out, mask=1)
+        slopes = torch.linspace(-0.1, 0.1, hq, device="cuda")
+        c.check(c.run(sv, out=out, softcap=100.0, slopes=slopes), out=out, softcap=100.0, slopes=slopes)
+    sv.sv_sync()

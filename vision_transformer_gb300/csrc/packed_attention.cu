@@ -782,6 +782,13 @@ __global__ void __maxnreg__(168)
     auto out_at = [&](const Item& it, int i) {
       return size_t(it.q0 + i) * size_t(p.os) + size_t(it.kvh * p.group + head) * size_t(p.D);
     };
+    constexpr bool kUnits = CAP || BIAS;       // scores in units of log 2 before the exponentials
+    // A tile of 128 keys in one step or in two of 64: then the second half of S is on its way while the first is
+    // worked on, and only the first half's maximum stands before the first exponentials, but a row's exponent is
+    // checked twice. 32 images of 729, 16 heads of 72, E4M3 out: 122 us in one step, 113 in two; 48 documents of up
+    // to 1024, 16 heads of 64: 127 and 122. Wide F16 heads lose what they gain (8192 causal, 32 heads of 128: 370
+    // and 377; 32 images, 72: 120.6 and 119.4), capped and biased scores more (106 and 124; 56 and 63).
+    constexpr int kSteps = kUnits || (NB == 2 && !E4M3) ? 1 : 2;
     float m = -INFINITY, l = 0.0f;
     uint8_t* stage = smem + L::kOffOut + (w * 4 + sub) * 2 * kOutBytes;
 
@@ -839,94 +846,132 @@ __global__ void __maxnreg__(168)
         uint32_t(&su)[4][32] = reinterpret_cast<uint32_t(&)[4][32]>(sv);
         tmem_ld32(s_tm, su[0]);
         tmem_ld32(s_tm + 32, su[1]);
+        if constexpr (kSteps == 2) {
+          tmem_ld_wait(su[0]);
+          reg_fence(su[1]);
+        }
         tmem_ld32(s_tm + 64, su[2]);
         tmem_ld32(s_tm + 96, su[3]);
-        tmem_ld_wait(su[0]);
-        reg_fence(su[1]);
-        reg_fence(su[2]);
-        reg_fence(su[3]);
-        if constexpr (CAP)  // scores in units of log 2 from here on
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) capped4(&sv[c][e], sl2, cap2);
-        if constexpr (BIAS) {
-          const float d0 = float(at - j * kTile);
-          const float on = CAP ? 1.0f : sl2;
-          if (__all_sync(0xffffffffu, at >= j * kTile + kTile - 1)) {
-            // no key of the tile behind the query: |d0 - e| = d0 - e, one line of slope `slope2`
-            const float first = -slope2 * d0;
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-#pragma unroll
-              for (int e = 0; e < 32; e += 2)
-                fma_x2(sv[c][e], sv[c][e + 1], sv[c][e], sv[c][e + 1], on, on, fmaf(slope2, float(32 * c + e), first),
-                       fmaf(slope2, float(32 * c + e + 1), first));
-          } else {
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                sv[c][e] = fmaf(-slope2, fabsf(d0 - float(32 * c + e)), CAP ? sv[c][e] : sv[c][e] * sl2);
-          }
+        if constexpr (kSteps == 1) {
+          tmem_ld_wait(su[0]);
+          reg_fence(su[1]);
+          reg_fence(su[2]);
+          reg_fence(su[3]);
         }
+        const float d0 = float(at - j * kTile);
+        // Where no visible key of the tile lies behind the query, or none before it, |d0 - e| is a line.
+        // (A row without a query has nothing to say.)
+        const bool none_behind = BIAS && __all_sync(0xffffffffu, i < 0 || at >= min(lim, j * kTile + kTile) - 1);
+        const bool line = BIAS && (none_behind || __all_sync(0xffffffffu, i < 0 || at <= j * kTile));
         const int valid = lim - j * kTile;  // visible keys of this tile
-        if (valid < kTile) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (valid < 32 * c + 32)
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (32 * c + e >= valid) sv[c][e] = -INFINITY;
-        }
-        float mq[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) mq[k] = fmaxf(sv[k >> 1][(k & 1) * 16], sv[k >> 1][(k & 1) * 16 + 1]);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-#pragma unroll
-          for (int e = 2; e < 16; e += 2)
-            mq[k] = fmax3(mq[k], sv[k >> 1][(k & 1) * 16 + e], sv[k >> 1][(k & 1) * 16 + e + 1]);
-        const float mx = fmaxf(fmaxf(fmax3(mq[0], mq[1], mq[2]), fmax3(mq[3], mq[4], mq[5])), fmaxf(mq[6], mq[7]));
-        constexpr bool kUnits = CAP || BIAS;
-        const float m_tile = kUnits ? mx : mx * sl2;
-        const bool raise = m_tile > m + kSlack;
-        const float m_new = raise ? m_tile - kHead : m;
-        if (j > jb && __any_sync(0xffffffffu, raise)) {
-          const float f = raise ? ex2(m - m_new) : 1.0f;
-          l *= f;
-#pragma unroll 1
-          for (int c = 0; c < Dn; c += 8) {
-            uint32_t e[8];
-            tmem_ld8(o_tm + uint32_t(c), e);
-            tmem_ld_wait();
-            asm volatile("" : "+r"(e[0]), "+r"(e[1]), "+r"(e[2]), "+r"(e[3]), "+r"(e[4]), "+r"(e[5]), "+r"(e[6]),
-                         "+r"(e[7]));
-#pragma unroll
-            for (int k = 0; k < 8; ++k) e[k] = __float_as_uint(__uint_as_float(e[k]) * f);
-            tmem_st8(o_tm + uint32_t(c), e);
-          }
-        }
-        m = m_new;
-        const float ref = m == -INFINITY ? 0.0f : m;
         float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t pk[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const float* s = &sv[2 * c + (e >> 4)][2 * (e & 15)];
-            float x0, x1;
-            if constexpr (kUnits) add_x2(x0, x1, s[0], s[1], -ref, -ref);
-            else fma_x2(x0, x1, s[0], s[1], sl2, sl2, -ref, -ref);
-            x0 = ex2(x0);
-            x1 = ex2(x1);
-            if (e & 1) add_x2(s2, s3, s2, s3, x0, x1);
-            else add_x2(s0, s1, s0, s1, x0, x1);
-            const __half2 h = __floats2half2_rn(x0, x1);
-            pk[e] = *reinterpret_cast<const uint32_t*>(&h);
+        for (int h = 0; h < kSteps; ++h) {
+          constexpr int kC = 4 / kSteps;  // 32-key groups of a step
+          if (h == 1) {
+            tmem_ld_wait(su[2]);
+            reg_fence(su[3]);
           }
-          tmem_st32(s_tm + 32 * c, pk);
+          if constexpr (CAP)
+#pragma unroll
+            for (int c = kC * h; c < kC * h + kC; ++c)
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) capped4(&sv[c][e], sl2, cap2);
+          if constexpr (BIAS) {
+            const float on = CAP ? 1.0f : sl2;
+            if (line) {
+              const float slope = none_behind ? slope2 : -slope2, first = -slope * d0;
+#pragma unroll
+              for (int c = kC * h; c < kC * h + kC; ++c)
+#pragma unroll
+                for (int e = 0; e < 32; e += 2)
+                  fma_x2(sv[c][e], sv[c][e + 1], sv[c][e], sv[c][e + 1], on, on, fmaf(slope, float(32 * c + e), first),
+                         fmaf(slope, float(32 * c + e + 1), first));
+            } else {
+#pragma unroll
+              for (int c = kC * h; c < kC * h + kC; ++c)
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  sv[c][e] = fmaf(-slope2, fabsf(d0 - float(32 * c + e)), CAP ? sv[c][e] : sv[c][e] * sl2);
+            }
+          }
+          if (valid < 32 * kC * (h + 1)) {
+#pragma unroll
+            for (int c = kC * h; c < kC * h + kC; ++c)
+              if (valid < 32 * c + 32)
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (32 * c + e >= valid) sv[c][e] = -INFINITY;
+          }
+          float mq[2 * kC];
+#pragma unroll
+          for (int k = 0; k < 2 * kC; ++k) {
+            const float* s = &sv[kC * h + (k >> 1)][(k & 1) * 16];
+            mq[k] = fmaxf(s[0], s[1]);
+          }
+#pragma unroll
+          for (int k = 0; k < 2 * kC; ++k)
+#pragma unroll
+            for (int e = 2; e < 16; e += 2) {
+              const float* s = &sv[kC * h + (k >> 1)][(k & 1) * 16];
+              mq[k] = fmax3(mq[k], s[e], s[e + 1]);
+            }
+          float mx = fmaxf(fmax3(mq[0], mq[1], mq[2]), mq[3]);
+          if constexpr (kC == 4) mx = fmaxf(fmax3(mq[4], mq[5], mq[6]), fmaxf(mq[7], mx));
+          const float m_half = kUnits ? mx : mx * sl2;
+          const bool raise = m_half > m + kSlack;
+          // (with two steps a whole number: the factor on the first one's P loses no bits)
+          const float m_new = raise ? (kSteps == 2 ? floorf(m_half) : m_half) - kHead : m;
+          if ((j > jb || h == 1) && __any_sync(0xffffffffu, raise)) {
+            const float f = raise ? ex2(m - m_new) : 1.0f;
+            l *= f;
+            if (h == 1) {  // what the first half has left
+              s0 *= f, s1 *= f, s2 *= f, s3 *= f;
+              tmem_st_wait();
+              uint32_t pk[32];
+              tmem_ld32(s_tm, pk);
+              tmem_ld_wait(pk);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&pk[e]));
+                const __half2 y = __floats2half2_rn(x.x * f, x.y * f);
+                pk[e] = *reinterpret_cast<const uint32_t*>(&y);
+              }
+              tmem_st32(s_tm, pk);
+            }
+            if (j > jb)
+#pragma unroll 1
+              for (int c = 0; c < Dn; c += 8) {
+                uint32_t e[8];
+                tmem_ld8(o_tm + uint32_t(c), e);
+                tmem_ld_wait();
+                asm volatile("" : "+r"(e[0]), "+r"(e[1]), "+r"(e[2]), "+r"(e[3]), "+r"(e[4]), "+r"(e[5]), "+r"(e[6]),
+                             "+r"(e[7]));
+#pragma unroll
+                for (int k = 0; k < 8; ++k) e[k] = __float_as_uint(__uint_as_float(e[k]) * f);
+                tmem_st8(o_tm + uint32_t(c), e);
+              }
+          }
+          m = m_new;
+          const float ref = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+          for (int c = kC * h; c < kC * h + kC; c += 2) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float* s = &sv[c + (e >> 4)][2 * (e & 15)];
+              float x0, x1;
+              if constexpr (kUnits) add_x2(x0, x1, s[0], s[1], -ref, -ref);
+              else fma_x2(x0, x1, s[0], s[1], sl2, sl2, -ref, -ref);
+              x0 = ex2(x0);
+              x1 = ex2(x1);
+              if (e & 1) add_x2(s2, s3, s2, s3, x0, x1);
+              else add_x2(s0, s1, s0, s1, x0, x1);
+              const __half2 y = __floats2half2_rn(x0, x1);
+              pk[e] = *reinterpret_cast<const uint32_t*>(&y);
+            }
+            tmem_st32(s_tm + 16 * c, pk);
+          }
         }
         l += (s0 + s1) + (s2 + s3);
         auto arrive = [&]() {
