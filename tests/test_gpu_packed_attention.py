@@ -550,3 +550,18 @@ def test_rising_and_falling_scores(sv, hq, hk, d, out, steps):
         slopes = torch.linspace(-0.1, 0.1, hq, device="cuda")
         c.check(c.run(sv, out=out, softcap=100.0, slopes=slopes), out=out, softcap=100.0, slopes=slopes)
     sv.sv_sync()
+
+
+@pytest.mark.parametrize("d", [8, 24, 64, 72, 80, 104])
+@pytest.mark.parametrize("out", ["f16", "e4m3"])
+def test_bits_do_not_depend_on_the_call_before(sv, d, out):
+    """What other calls leave on the SMs, NaN in every accumulator here, has no part in a result."""
+    c = Case([300, 270, 513], [300, 270, 513], 48, 48, d, seed=d)
+    clean = Case([300] * 4, [300] * 4, 48, 48, 128, seed=1)
+    clean.run(sv)
+    want = c.run(sv, out=out)
+    c.check(want, out=out)
+    clean.v.fill_(math.nan)
+    assert torch.isnan(clean.run(sv)).all()
+    assert torch.equal(c.run(sv, out=out).view(torch.uint8), want.view(torch.uint8))
+    sv.sv_sync()

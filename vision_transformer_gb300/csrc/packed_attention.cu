@@ -800,6 +800,13 @@ __global__ void __maxnreg__(168)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBarItemDone + n % kItems));
     };
+    // Rows are loaded 32 columns at a time. The columns that no product writes hold what an earlier kernel has left;
+    // a NaN among them would send every row the long way round (write_again).
+    for (int c = Dn; c < (p.D + 31) / 32 * 32; c += 8) {
+      const uint32_t zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+      tmem_st8(o_tm + uint32_t(c), zero);
+    }
+    tmem_st_wait();
     int pending = -1;  // the item whose rows are not written yet
     bool pending_keys = false;
     int full = 0;      // items with keys so far
