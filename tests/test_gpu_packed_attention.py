@@ -565,3 +565,59 @@ def test_bits_do_not_depend_on_the_call_before(sv, d, out):
     assert torch.isnan(clean.run(sv)).all()
     assert torch.equal(c.run(sv, out=out).view(torch.uint8), want.view(torch.uint8))
     sv.sv_sync()
+
+
+# Enough heads that items of two tiles fill the GPU (few heads: items of one tile, their keys shared out).
+@pytest.mark.parametrize("heads,group,d", [(48, 1, 72), (80, 2, 64), (64, 4, 128), (90, 3, 40)])
+@pytest.mark.parametrize("lens", [[300, 270, 513], [729], [129, 1, 0, 400], [640, 640]])
+@pytest.mark.parametrize("out", ["f16", "e4m3"])
+def test_many_heads(sv, heads, group, d, lens, out):
+    c = Case(lens, lens, heads, heads // group, d, seed=heads, tail=2)
+    c.check(c.run(sv, out=out), out=out)
+    prefix = [n // 3 for n in lens]
+    c.check(c.run(sv, out=out, mask=1, prefix=prefix), out=out, mask=1, prefix=prefix)
+    slopes = torch.linspace(-0.01, 0.1, heads, device="cuda")
+    for opt in (dict(slopes=slopes), dict(softcap=5.0, mask=1), dict(softcap=5.0, slopes=slopes, mask=1)):
+        o = c.run(sv, out=out, **opt)
+        c.check(o, out=out, **opt)
+        assert torch.equal(o.view(torch.uint8), c.run(sv, out=out, workspace=c.ws, **opt).view(torch.uint8))
+    sv.sv_sync()
+
+
+@pytest.mark.parametrize("hq,hk,d", [(1, 1, 64), (4, 4, 72), (8, 2, 128), (5, 1, 24)])
+@pytest.mark.parametrize("lq,lk", [([130], [1025]), ([1, 300], [1900, 300]), ([128], [1152]), ([700], [1024]),
+                                   ([64, 0, 200], [2900, 130, 640]), ([150, 20], [2049, 4000]), ([140], [257])])
+def test_few_items(sv, hq, hk, d, lq, lk):
+    """Items of one tile whose key tiles are shared out between two groups: odd and even numbers of them, masks that
+    leave one group's rows or both without keys, ranges that are divided among blocks as well."""
+    c = Case(lq, lk, hq, hk, d, seed=d + sum(lk), lead=1, tail=4)
+    slopes = torch.linspace(0.0, 0.05, hq, device="cuda")
+    for opt in (dict(), dict(mask=1), dict(mask=1, prefix=[5] * len(lq), softcap=6.0), dict(slopes=slopes),
+                dict(slopes=slopes, softcap=6.0, mask=1)):
+        for out in ("f16", "e4m3"):
+            o = c.run(sv, out=out, **opt)
+            c.check(o, out=out, **opt)
+            a = o.view(torch.uint8)
+            assert torch.equal(a, c.run(sv, out=out, workspace=c.ws, **opt).view(torch.uint8))
+    sv.sv_sync()
+
+
+@pytest.mark.parametrize("poison", [math.nan, math.inf])
+def test_hidden_values_among_few_items(sv, poison):
+    """Keys that some rows see and others do not, in either group's tiles, and a neighbour's behind the last tile."""
+    lq, lk = [200, 100], [1500, 900]
+    c = Case(lq, lk, 1, 1, 64, seed=5, lead=2, tail=3)
+    clean = _by_rows(c, 1)
+    hidden = [[1350, 1470], [870]]
+    for what in (c.k, c.v):
+        what[:2] = poison
+        what[-3:] = poison
+        for h in hidden[0]:
+            what[2 + h] = poison
+        what[2 + 1500 + hidden[1][0]] = poison
+    got = c.run(sv, mask=1)[2:2 + 300].double()
+    sv.sv_sync()
+    sees = torch.tensor([i + 1300 >= 1350 for i in range(200)] + [i + 800 >= 870 for i in range(100)], device="cuda")
+    assert torch.equal(torch.isfinite(got).all(1), ~sees)
+    err = (got - clean).abs()[~sees].amax(1)
+    assert (err <= 2.0 ** -9 * clean[~sees].abs().amax(1).clamp(min=1.0)).all()

@@ -23,7 +23,8 @@
 //               rescales O in tensor memory when the exponent rises by more than 2^15.
 // An item's rows go out behind the next item's first tile: O is loaded between that tile's
 // softmax and the arrival of its P, and scaled, rounded and stored while the products run.
-// Items are handed out by tickets, the longest documents of every 32 first. Key ranges are
+// Items are handed out by tickets, the longest documents of every 32 first. In launches of few
+// items (SOLO) an item is one tile, and the two groups share out its key tiles. Key ranges are
 // divided among CTAs when there are few items (Schedule); the parts' O, m and l go to the
 // caller's workspace and are joined two and two.
 // Tensor memory: S_0, S_1, O_0, O_1 of 128 columns each.
@@ -54,8 +55,8 @@ constexpr int kItems = 4;                   // work items between the copy warp 
 constexpr uint32_t kTmemCols = 512;
 constexpr int kMaxSlots = 2 * kMaxSms;      // partial results of a launch at most (see Schedule)
 // Key tiles of a part of a divided range at least: below, the parts' way through the workspace
-// costs more than their length (40 queries over 2048 keys: two parts of 8 tiles 34 us, 16 tiles in a
-// row 32; one image of 729 tokens, 16 heads: 48 items of 6 tiles 16 us, 144 parts of 2 tiles 38 us).
+// costs more than their length (40 queries over 2048 keys: two parts of 8 tiles 34 us, 16 tiles one
+// behind another 32; one image of 729 tokens, 16 heads: 48 items of 6 tiles 16 us, 144 parts of 2 tiles 38 us).
 constexpr int kMinSplit = 8;
 static_assert(kCounterBytes >= size_t(kMaxSlots) * 8 * sizeof(unsigned), "counters");
 
@@ -82,7 +83,9 @@ enum {
   kBarItem = 25,       // +item slot: the copy warp has written the item
   kBarItemDone = 29,   // +item slot: the issuer and the eight softmax warps are through with it
   kBarOFull = 33,      // +group: the item's last P V product of the group has finished
-  kNumBars = 35
+  kBarJoin = 35,       // one tile an item: the second group's exponents and sums are in shared memory
+  kBarRead = 36,       // and its O has been read
+  kNumBars = 37
 };
 
 // One work item: up to 2 qt queries of a document with the query heads of one key head
@@ -107,7 +110,9 @@ static_assert(kOffItems + kItems * sizeof(Item) <= kBarBytes, "barrier area");
 // range of n > chunk tiles has ceil(n / chunk) <= 2 n / chunk parts.
 class Schedule {
  public:
-  __device__ __forceinline__ Schedule(const Params& p, int lane) : p_(p), lane_(lane), docs_(p.docs) {
+  // span: queries of an item; min_split: key tiles of a part at least.
+  __device__ __forceinline__ Schedule(const Params& p, int lane, int span, int min_split)
+      : p_(p), lane_(lane), docs_(p.docs), span_(span) {
     chunk_ = 0x7fffffff;
     float work = 0.0f;
     bool bad = false;
@@ -135,7 +140,7 @@ class Schedule {
         // work x heads / grid, rounded up (F32 sums of up to 2^24 documents, 32 lanes apart: a little more
         // does no harm)
         const float share = work * float(p.hk) * (1.1f / float(gridDim.x));
-        chunk_ = max(kMinSplit, int(fminf(share, 1e9f)) + 1);
+        chunk_ = max(min_split, int(fminf(share, 1e9f)) + 1);
       }
     }
   }
@@ -190,9 +195,9 @@ class Schedule {
     r.lk = of(doc_.lk);
     r.k0 = of(doc_.k0);
     r.prefix = of(doc_.prefix);
-    const int i0 = pair * 2 * p_.qt;
+    const int i0 = pair * span_;
     r.q0 = of(doc_.q0) + i0;
-    r.nq = min(lq - i0, 2 * p_.qt);
+    r.nq = min(lq - i0, span_);
     r.at = i0 + r.lk - lq;
     const int n = (limit_of(p_.causal, r.at + r.nq - 1, r.lk, r.prefix) + kTile - 1) / kTile;
     const int part = (tiles + splits - 1) / splits;
@@ -204,7 +209,7 @@ class Schedule {
  private:
   __device__ __forceinline__ void load(int d0) {
     bad_ = !document(p_, d0 + lane_, docs_, doc_);
-    pairs_ = (doc_.lq + 2 * p_.qt - 1) / (2 * p_.qt);
+    pairs_ = (doc_.lq + span_ - 1) / span_;
     tiles_ = (doc_.lk + kTile - 1) / kTile;  // of the last query
     splits_ = tiles_ > chunk_ ? (tiles_ + chunk_ - 1) / chunk_ : 1;
     count_ = pairs_ * p_.hk * splits_;
@@ -237,7 +242,7 @@ class Schedule {
     take(count_);
   }
   const Params& p_;
-  int lane_, docs_, chunk_;
+  int lane_, docs_, span_, chunk_;
   bool bad_;
   int items_ = 0;
   int d0_ = -32, base_ = 0, total_ = 0, slot_base_ = 0, slot_total_ = 0;
@@ -259,7 +264,7 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
 // along a binary tree over the parts: of two neighbours the warp that arrives second adds them, on
 // the left one's place, and goes on with the sum; the last one of all writes the row. So the joins
 // of a long range run on many SMs (by the last of all parts alone, in order: 40 queries of 8 heads
-// over 32768 keys of 2, 64 parts, 184 us; so 67), and the order of the sums is the tree's, whoever is
+// over 32768 keys of 2, 64 parts, 184 us; so 67, 53 with the groups sharing tiles), and the order of the sums is the tree's, whoever is
 // second.
 __device__ __noinline__ void join_parts(const Params& p, const Item& it, long long out_to, int w, int r) {
   const int Dn = (p.D + 15) / 16 * 16, n = it.splits, first = it.slot - it.split;
@@ -382,6 +387,45 @@ __device__ __noinline__ void write_special(const Params& p, const Item& it, uint
   if (how & kPart) join_parts(p, it, out_to, w, r);
 }
 
+// Row r of an item of one tile whose key tiles the two groups have shared out: exponent, denominator and O of both.
+__device__ __noinline__ void write_shared(const Params& p, const Item& it, uint32_t o_tm, float m0, float l0, float m1,
+                                          float l1, long long out_to, int how, int r) {
+  const int Dn = (p.D + 15) / 16 * 16;
+  const float mx = fmaxf(m0, m1), ref = mx == -INFINITY ? 0.0f : mx;
+  const float f0 = ex2(m0 - ref), f1 = ex2(m1 - ref), l = fmaf(f1, l1, f0 * l0);
+  const float inv = how & kPart ? 1.0f : 1.0f / l;
+  float* pb = p.partial + size_t(it.slot) * 2 * size_t(Dn + 2) * kTile + r;
+  if (how & kPart) {
+    __stcg(pb, mx);
+    __stcg(pb + kTile, l);
+  }
+  float bad = 0.0f;
+#pragma unroll 1
+  for (int c = 0; c < p.D; c += 8) {
+    uint32_t a[8], b[8];
+    tmem_ld8(o_tm + uint32_t(c), a);
+    tmem_ld8(o_tm + uint32_t(128 + c), b);
+    tmem_ld_wait();
+    float y[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      asm volatile("" : "+r"(a[e]), "+r"(b[e]));  // no use before the wait
+      y[e] = how & kNothing ? 0.0f : fmaf(f1, __uint_as_float(b[e]), f0 * __uint_as_float(a[e])) * inv;
+      bad = fmaf(y[e], 0.0f, bad);
+    }
+    if (out_to < 0) continue;
+    if (how & kPart) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) __stcg(pb + size_t(2 + c + e) * kTile, y[e]);
+    } else {
+      store8(p, size_t(out_to) + c, y);
+    }
+  }
+  if (out_to >= 0 && bad != 0.0f) write_again(p, it, out_to, how, 0, r);
+  __syncwarp();
+  if (how & kPart) join_parts(p, it, out_to, 0, r);
+}
+
 // Row r of tile w of an item, once its last P V has finished (o_tm: the row's O). `loaded` is called
 // when O has left tensor memory. Where a warp's 32 rows are all the item's and make whole queries
 // (p.out_tma) they go out by TMA from shared memory (`stage`: two buffers), 32 columns at a time;
@@ -493,7 +537,9 @@ __device__ __forceinline__ void write_rows(const Params& p, const Item& it, cons
   if (bad) write_again(p, it, out_to, how, w, r);
 }
 
-template <int NB, bool CAP, bool BIAS, bool E4M3>
+// SOLO: items of one tile, whose key tiles the two groups take in turn (for launches of few items: half the chain, and
+// an end at which the groups' sums are joined). The output's type is then read from the parameters.
+template <int NB, bool CAP, bool BIAS, bool E4M3, bool SOLO>
 // 10 warps: three share each of two SM sub-partitions, so a thread may hold at most
 // 16384 / (3 x 32) registers, rounded down to the allocation granule.
 __global__ void __maxnreg__(168)
@@ -529,6 +575,8 @@ __global__ void __maxnreg__(168)
       mbar_init(bar(kBarItem + s), 1);
       mbar_init(bar(kBarItemDone + s), 9);
     }
+    mbar_init(bar(kBarJoin), 128);
+    mbar_init(bar(kBarRead), 128);
     mbar_init(bar(kBarDrain), 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -549,7 +597,7 @@ __global__ void __maxnreg__(168)
   };
 
   if (warp == 0) {
-    Schedule sched(p, lane);
+    Schedule sched(p, lane, (SOLO ? 1 : 2) * p.qt, (SOLO ? 2 : 1) * kMinSplit);
     if (lane == 0) {
       prefetch_tmap(&tq);
       prefetch_tmap(&tk);
@@ -592,7 +640,7 @@ __global__ void __maxnreg__(168)
         // The next item is drawn late, so that the work stays balanced, but where the ring is short before
         // the last copies, whose room has to be waited for anyway (32 images: 124.5 -> 121.5 us; where it holds
         // four key tiles, earlier than behind the last copy costs 2%).
-        const int copies = 2 * (it.je - it.jb), draw_at = NB == 1 ? copies : copies - 2;
+        const int copies = SOLO ? 4 * ((it.je - it.jb + 1) / 2) : 2 * (it.je - it.jb), draw_at = NB == 1 ? copies : copies - 2;
         auto kv = [&](const CUtensorMap& map, int j) -> bool {
           const int st = t % kStages;
           const uint32_t ph = (t / kStages) & 1;
@@ -608,7 +656,8 @@ __global__ void __maxnreg__(168)
 #pragma unroll 1
         for (int x = 0; ok && x < copies; ++x) {  // a key tile, its values, the next key tile, ...
           if (x == draw_at) ticket = sched.draw();
-          ok = kv(x & 1 ? tv : tk, it.jb + (x >> 1));
+          if constexpr (SOLO) ok = kv(x & 2 ? tv : tk, it.jb + 2 * (x >> 2) + (x & 1));  // two keys, their values, ...
+          else ok = kv(x & 1 ? tv : tk, it.jb + (x >> 1));
           if (ok && x == 0) {
             const int qb = n % kQBufs;
             const uint32_t ph = (n / kQBufs) & 1;
@@ -618,7 +667,7 @@ __global__ void __maxnreg__(168)
               for (int w = 0; w < 2; ++w)
                 for (int b = 0; b < NB; ++b)
                   tma_load_3d(sbase + (2 * qb + w) * kOp + b * kBoxBytes, &tq, bar(kBarQFull + qb), 64 * b,
-                              it.kvh * p.group, it.q0 + w * p.qt);
+                              it.kvh * p.group, it.q0 + (SOLO ? 0 : w * p.qt));
               note(qb, ph);
             }
           }
@@ -696,7 +745,47 @@ __global__ void __maxnreg__(168)
         if (all(tiles > 0)) return tiles;
       }
     };
-    int tiles = next(true);
+    if constexpr (SOLO) {
+      // S_0(0), S_1(1), then per two key tiles: O_0 += P_0 V, S_0 of the next two, O_1 += P_1 V, S_1
+      uint32_t copied = 0, tt = 0, item = 0;  // copies used up, parity of the P, items with keys
+      auto stage = [&](uint32_t k) { return (copied + k) % kStages; };
+      auto full = [&](uint32_t k) {
+        const bool got = wait(kBarFull + int(stage(k)), ((copied + k) / kStages) & 1);
+        tc_fence_after();
+        return got;
+      };
+      for (bool ok = true; ok; ++item) {
+        const int tiles = next(true), steps = (tiles + 1) / 2, qb = int(item % kQBufs);
+        if (!all(tiles > 0)) break;
+        ok = wait(kBarQFull + qb, (item / kQBufs) & 1);
+#pragma unroll 1
+        for (uint32_t w = 0; w < 2 && ok; ++w) {
+          if (!(ok = full(w))) break;
+          issue_s(int(w), qb, stage(w));
+          commit(kBarEmpty + int(stage(w)));
+        }
+        if (all(steps == 1)) commit(kBarQEmpty + qb);
+#pragma unroll 1
+        for (int s = 0; ok && all(s < steps); ++s, copied += 4, tt ^= 1) {
+#pragma unroll 1
+          for (uint32_t w = 0; w < 2 && ok; ++w) {
+            if (!(ok = full(2 + w) && wait(kBarPFull + int(w), tt))) break;
+            tc_fence_after();
+            issue_pv(int(w), stage(2 + w), s > 0);
+            commit(kBarEmpty + int(stage(2 + w)));
+            if (all(s + 1 == steps)) {
+              commit(kBarOFull + int(w));
+            } else {
+              if (!(ok = full(4 + w))) break;
+              issue_s(int(w), qb, stage(4 + w));
+              commit(kBarEmpty + int(stage(4 + w)));
+              if (w == 1 && all(s + 2 == steps)) commit(kBarQEmpty + qb);
+            }
+          }
+        }
+      }
+    }
+    int tiles = SOLO ? 0 : next(true);
     bool ok = all(tiles > 0) && wait_full(0) && wait(kBarQFull, 0);
     if (ok) {
       tc_fence_after();
@@ -776,7 +865,7 @@ __global__ void __maxnreg__(168)
     const float cap2 = p.cap * kLog2e;
     // query of this row in an item: index, -1 if the row holds none
     auto query = [&](const Item& it) {
-      const int i = w * p.qt + qi;
+      const int i = (SOLO ? 0 : w * p.qt) + qi;
       return (qi < p.qt && i < it.nq) ? i : -1;
     };
     auto out_at = [&](const Item& it, int i) {
@@ -842,7 +931,8 @@ __global__ void __maxnreg__(168)
       const float slope2 = BIAS && i >= 0 ? __ldg(p.slopes + it.kvh * p.group + head) * kLog2e : 0.0f;
       m = -INFINITY;
       l = 0.0f;
-      for (int j = jb; j < je; ++j, ++t) {
+      const int j0 = SOLO ? jb + w : jb, j_end = SOLO ? jb + (je - jb + 1) / 2 * 2 : je;
+      for (int j = j0; j < j_end; j += SOLO ? 2 : 1, ++t) {
         // S(t) has finished, and with it every P V product of the group before it
         if (!__all_sync(0xffffffffu, wait_bar(bar(kBarSFull + w), t & 1, abort_flag, p.err))) {
           ok = false;
@@ -870,7 +960,8 @@ __global__ void __maxnreg__(168)
         // (A row without a query has nothing to say.)
         const bool none_behind = BIAS && __all_sync(0xffffffffu, i < 0 || at >= min(lim, j * kTile + kTile) - 1);
         const bool line = BIAS && (none_behind || __all_sync(0xffffffffu, i < 0 || at <= j * kTile));
-        const int valid = lim - j * kTile;  // visible keys of this tile
+        // visible keys of this tile (shared out, the second group's last may lie behind the item's)
+        const int valid = (SOLO ? min(lim, je * kTile) : lim) - j * kTile;
         float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
 #pragma unroll
         for (int h = 0; h < kSteps; ++h) {
@@ -929,7 +1020,7 @@ __global__ void __maxnreg__(168)
           const bool raise = m_half > m + kSlack;
           // (with two steps a whole number: the factor on the first one's P loses no bits)
           const float m_new = raise ? (kSteps == 2 ? floorf(m_half) : m_half) - kHead : m;
-          if ((j > jb || h == 1) && __any_sync(0xffffffffu, raise)) {
+          if ((j > j0 || h == 1) && __any_sync(0xffffffffu, raise)) {
             const float f = raise ? ex2(m - m_new) : 1.0f;
             l *= f;
             if (h == 1) {  // what the first half has left
@@ -946,7 +1037,7 @@ __global__ void __maxnreg__(168)
               }
               tmem_st32(s_tm, pk);
             }
-            if (j > jb)
+            if (j > j0)
 #pragma unroll 1
               for (int c = 0; c < Dn; c += 8) {
                 uint32_t e[8];
@@ -986,7 +1077,7 @@ __global__ void __maxnreg__(168)
           tc_fence_before();
           mbar_arrive(bar(kBarPFull + w));
         };
-        if (j == jb && pending >= 0) {
+        if (!SOLO && j == j0 && pending >= 0) {
           // The item before: this S followed its last P V, so its O is final, and the first P V
           // of this item, which overwrites O, waits for the arrival. Between the two O is only
           // loaded; its rows are written while the products run. (Written before the item's
@@ -999,6 +1090,31 @@ __global__ void __maxnreg__(168)
         }
       }
       if (!ok) break;
+      if constexpr (SOLO) {
+        if (jb < je) {
+          float2* ml = reinterpret_cast<float2*>(smem + L::kOffOut) + r;
+          auto wait = [&](int b) {
+            const bool got = __all_sync(0xffffffffu, wait_bar(bar(b), full & 1, abort_flag, p.err));
+            tc_fence_after();
+            return got;
+          };
+          if (w == 1) {
+            *ml = make_float2(m, l);
+            mbar_arrive(bar(kBarJoin));
+            if (!wait(kBarRead)) break;  // (the next item's P V writes O again)
+          } else {
+            if (!wait(kBarOFull) || !wait(kBarOFull + 1) || !wait(kBarJoin)) break;
+            write_shared(p, it, o_tm, m, l, ml->x, ml->y, out_to, out_how, r);
+            tc_fence_before();
+            mbar_arrive(bar(kBarRead));
+          }
+          ++full;
+        } else if (w == 0) {
+          write_special(p, it, o_tm, m, l, out_to, out_how, 0, r);
+        }
+        done(n);
+        continue;
+      }
       pending = n;
       pending_keys = jb < je;
       full += pending_keys;
@@ -1024,9 +1140,9 @@ sv_status packed_map(CUtensorMap* m, const void* ptr, int D, int heads, int rows
   return make_tmap(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, ptr, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <int NB, bool CAP, bool BIAS, bool E4M3>
+template <int NB, bool CAP, bool BIAS, bool E4M3, bool SOLO>
 sv_status packed_launch_as(const Params& p, int grid, cudaStream_t s) {
-  auto kern = packed_tile_kernel<NB, CAP, BIAS, E4M3>;
+  auto kern = packed_tile_kernel<NB, CAP, BIAS, E4M3, SOLO>;
   static unsigned long long attr_set = 0;  // the attribute is per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1058,12 +1174,13 @@ sv_status packed_launch_as(const Params& p, int grid, cudaStream_t s) {
   return e == cudaSuccess ? SV_OK : cuda_fail(e, "packed attention launch");
 }
 
-template <int NB, bool E4M3>
+template <int NB, bool E4M3, bool SOLO>
 sv_status packed_launch(const Params& p, int grid, cudaStream_t s) {
   if (p.cap > 0.0f)
-    return p.slopes ? packed_launch_as<NB, true, true, E4M3>(p, grid, s) : packed_launch_as<NB, true, false, E4M3>(p, grid, s);
-  return p.slopes ? packed_launch_as<NB, false, true, E4M3>(p, grid, s)
-                  : packed_launch_as<NB, false, false, E4M3>(p, grid, s);
+    return p.slopes ? packed_launch_as<NB, true, true, E4M3, SOLO>(p, grid, s)
+                    : packed_launch_as<NB, true, false, E4M3, SOLO>(p, grid, s);
+  return p.slopes ? packed_launch_as<NB, false, true, E4M3, SOLO>(p, grid, s)
+                  : packed_launch_as<NB, false, false, E4M3, SOLO>(p, grid, s);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -1075,8 +1192,13 @@ sv_status tile_launch(const Params& p, cudaStream_t s) {
   const long long items = (p.total_q / (2 * p.qt) + p.docs) * static_cast<long long>(p.hk);
   int grid = num_sms() < kMaxSms ? num_sms() : kMaxSms;
   if (!p.counters && items < grid) grid = int(items);
-  if (p.out_e4m3) return p.D > 64 ? packed_launch<2, true>(p, grid, s) : packed_launch<1, true>(p, grid, s);
-  return p.D > 64 ? packed_launch<2, false>(p, grid, s) : packed_launch<1, false>(p, grid, s);
+  // Few items of 8 key tiles and more on average: a tile each, its keys shared out between the groups. (256 queries of
+  // 8 heads of 128 over 2: 1,024 keys 19.2 us in items of two tiles and 18.0 so, 2,048 keys 34 and 25, 9,000 keys
+  // 58 and 48; one image of 729 tokens, 16 heads of 72: 16.0 and 16.9, the end costs what the chain has saved.)
+  if (p.counters && 2 * items <= grid && p.total_k >= static_cast<long long>(kMinSplit) * kTile * p.docs)
+    return p.D > 64 ? packed_launch<2, false, true>(p, grid, s) : packed_launch<1, false, true>(p, grid, s);
+  if (p.out_e4m3) return p.D > 64 ? packed_launch<2, true, false>(p, grid, s) : packed_launch<1, true, false>(p, grid, s);
+  return p.D > 64 ? packed_launch<2, false, false>(p, grid, s) : packed_launch<1, false, false>(p, grid, s);
 }
 
 }  // namespace packed
