@@ -126,6 +126,12 @@ __device__ __forceinline__ void store8(const Params& p, size_t at, const float* 
   put8(p.out_e4m3, static_cast<uint8_t*>(p.o) + (p.out_e4m3 ? at : 2 * at), y);
 }
 
+// One value of an output row.
+__device__ __forceinline__ void store1(const Params& p, size_t at, float y) {
+  if (p.out_e4m3) static_cast<uint8_t*>(p.o)[at] = __nv_cvt_float_to_fp8(16.0f * y, __NV_SATFINITE, __NV_E4M3);
+  else static_cast<__half*>(p.o)[at] = __float2half_rn(y);
+}
+
 // A row whose tensor-core result is not finite, again from the visible keys alone: a tile's
 // product multiplies the probability 0 of a hidden key with its value, which is NaN for an
 // infinite or NaN value. Keys kb .. ke - 1 of the document, query position `at`; unscaled

@@ -35,8 +35,10 @@ namespace {
 
 constexpr int kFewThreads = 128;
 constexpr int kMinShare = 64;       // keys of a CTA's share at least
-constexpr int kCtasPerSm = 3;
-constexpr int kMaxFewGrid = kMaxSms * kCtasPerSm;
+constexpr int kMostPerSm = 4;
+constexpr int kMaxFewGrid = kMaxSms * kMostPerSm;
+// CTAs an SM, by what the registers of a warp allow.
+constexpr int per_sm(int nt, bool tail) { return nt > 1 ? 2 : (tail ? 4 : 3); }
 
 __device__ __forceinline__ uint4 load16(const __half* p) {
   uint4 r;
@@ -51,6 +53,23 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma1688(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5}, {%6}, {%0, %1, %2, %3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a0), "r"(a1), "r"(b0));
+}
+
+__device__ __forceinline__ uint32_t load4(const __half* p) {
+  uint32_t r;
+  asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(r) : "l"(p));
+  return r;
+}
+__device__ __forceinline__ uint32_t load2(const __half* p) {
+  uint16_t r;
+  asm volatile("ld.global.nc.L1::no_allocate.u16 %0, [%1];" : "=h"(r) : "l"(p));
+  return r;
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -213,11 +232,13 @@ __device__ __forceinline__ void put_part(float* to, const float* y) {
 }
 
 // KI: 32-dimension groups of a key row, VI: 64-dimension groups of a value row, NT: 8-row
-// tiles of an item, HEADS: key heads of an item (4 / HEADS warps share a head's keys).
-template <int KI, int VI, int NT, int HEADS>
-__global__ void __launch_bounds__(kFewThreads, NT == 1 ? kCtasPerSm : 2) few_kernel(const __grid_constant__ Params p) {
+// tiles of an item, HEADS: key heads of an item (4 / HEADS warps share a head's keys). TAIL: eight
+// more dimensions behind the groups (72), in instructions of their own: another group of each
+// would hold registers for 96 and 128 dimensions, and what is in flight is bound by registers.
+template <int KI, int VI, int NT, int HEADS, bool TAIL>
+__global__ void __launch_bounds__(kFewThreads, per_sm(NT, TAIL)) few_kernel(const __grid_constant__ Params p) {
   constexpr int kRows = 8 * NT, kSplit = 4 / HEADS, kStep = 16 * kSplit;
-  constexpr int kOut = 64 * VI + 4;  // row pitch of the merge buffer (floats)
+  constexpr int kOut = 64 * VI + (TAIL ? 12 : 4);  // row pitch of the merge buffer (floats)
   __shared__ __align__(16) float red[4][kRows][kOut];
   __shared__ float red_m[4][kRows], red_l[4][kRows];
   __shared__ int row_bad[HEADS * kRows];
@@ -243,7 +264,7 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? kCtasPerSm : 2) few_ker
     // this lane's two rows of each tile as columns of S^T: visible keys, position, slope
     int lim[NT][2];
     float at[NT][2], slope[NT][2];
-    uint32_t q[NT][KI][4];
+    uint32_t q[NT][KI][4], q_tail[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -263,9 +284,11 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? kCtasPerSm : 2) few_ker
         if (r < rows_all && 4 * c + t < chunks) x = load16(qr + 8 * (4 * c + t));
         q[n][c][0] = x.x, q[n][c][1] = x.y, q[n][c][2] = x.z, q[n][c][3] = x.w;
       }
+      q_tail[n] = TAIL && r < rows_all ? load4(qr + 32 * KI + 2 * t) : 0u;
     }
 
     uint4 kx[2][KI], vx[4][VI];
+    uint32_t k_tail[2], v_tail[4];
     auto load_k = [&](int key0) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -274,6 +297,7 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? kCtasPerSm : 2) few_ker
 #pragma unroll
         for (int c = 0; c < KI; ++c)
           kx[h][c] = key < last && 4 * c + t < chunks ? load16(row + 8 * (4 * c + t)) : make_uint4(0u, 0u, 0u, 0u);
+        if (TAIL) k_tail[h] = key < last ? load4(row + 32 * KI + 2 * t) : 0u;
       }
     };
     auto load_v = [&](int key0) {
@@ -284,14 +308,16 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? kCtasPerSm : 2) few_ker
 #pragma unroll
         for (int c = 0; c < VI; ++c)
           vx[h][c] = key < last && 8 * c + g < chunks ? load16(row + 8 * (8 * c + g)) : make_uint4(0u, 0u, 0u, 0u);
+        if (TAIL) v_tail[h] = key < last ? load2(row + 64 * VI + g) : 0u;
       }
     };
-    float o[NT][4 * VI][4];
+    float o[NT][4 * VI][4], o_tail[NT][4];  // the tail: dimension 64 VI + g of rows 2 t and 2 t + 1
     float m[NT][2], l[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
       for (int j = 0; j < 4 * VI; ++j) o[n][j][0] = o[n][j][1] = o[n][j][2] = o[n][j][3] = 0.0f;
+      o_tail[n][0] = o_tail[n][1] = o_tail[n][2] = o_tail[n][3] = 0.0f;
       m[n][0] = m[n][1] = -INFINITY;
       l[n][0] = l[n][1] = 0.0f;
     }
@@ -310,6 +336,7 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? kCtasPerSm : 2) few_ker
           mma16816(s[n], kx[0][c].x, kx[1][c].x, kx[0][c].y, kx[1][c].y, q[n][c][0], q[n][c][1]);
           mma16816(s[n], kx[0][c].z, kx[1][c].z, kx[0][c].w, kx[1][c].w, q[n][c][2], q[n][c][3]);
         }
+        if (TAIL) mma1688(s[n], k_tail[0], k_tail[1], q_tail[n]);
       }
       load_k(key0 + kStep);
 #pragma unroll
@@ -345,6 +372,8 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? kCtasPerSm : 2) few_ker
             o[n][j][2] *= f[0];
             o[n][j][3] *= f[1];
           }
+          o_tail[n][0] *= f[0];
+          o_tail[n][1] *= f[1];
           l[n][0] *= f[0];
           l[n][1] *= f[1];
         }
@@ -374,6 +403,11 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? kCtasPerSm : 2) few_ker
 #pragma unroll
           for (int n = 0; n < NT; ++n) mma16816(o[n][4 * c + j], a0, a1, a2, a3, b[n][0], b[n][1]);
         }
+      }
+      if constexpr (TAIL) {
+        const uint32_t a0 = __byte_perm(v_tail[0], v_tail[1], 0x5410), a2 = __byte_perm(v_tail[2], v_tail[3], 0x5410);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma16816(o_tail[n], a0, 0u, a2, 0u, b[n][0], b[n][1]);
       }
       load_v(key0 + kStep);
     }
@@ -438,6 +472,12 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? kCtasPerSm : 2) few_ker
             if (whole) store8(p, to + 8 * (8 * v + g), y);
             else put_part(at_p + 8 * (8 * v + g), y);
           }
+          if constexpr (TAIL) {
+            const float y = none ? 0.0f : o_tail[n][e] * inv;
+            bad = fmaf(y, 0.0f, bad);
+            if (live && whole) store1(p, to + 64 * VI + g, y);
+            else if (live) __stcg(at_p + 64 * VI + g, y);
+          }
           if (live && !whole && g == 0) __stcg(reinterpret_cast<float2*>(at_ml), make_float2(m[n][e], sum));
           const unsigned rows_bad = __ballot_sync(0xffffffffu, live && bad != 0.0f);
           if (rows_bad) {  // again from the visible keys alone, a lane a row
@@ -500,6 +540,18 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? kCtasPerSm : 2) few_ker
           for (int e = 0; e < 2; ++e)
             *reinterpret_cast<float4*>(&red[warp][8 * n + 2 * t + e][64 * (j >> 2) + 8 * g + 2 * (j & 3)]) =
                 make_float4(o[n][j][e] * f[e], o[n][j][e + 2] * f[e], o[n][j + 1][e] * f[e], o[n][j + 1][e + 2] * f[e]);
+      }
+      if constexpr (TAIL) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = 8 * n + 2 * t + e;
+            float mx = red_m[my_head][r];
+#pragma unroll
+            for (int k = 1; k < kSplit; ++k) mx = fmaxf(mx, red_m[my_head + k * HEADS][r]);
+            red[warp][r][64 * VI + g] = o_tail[n][e] * ex2(m[n][e] - (mx == -INFINITY ? 0.0f : mx));
+          }
       }
       __syncthreads();
       // row x of the item's HEADS x rows: which head and row, query and query head
@@ -604,16 +656,17 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? kCtasPerSm : 2) few_ker
   }
 }
 
-template <int KI, int VI, int NT, int HEADS>
+template <int KI, int VI, int NT, int HEADS, bool TAIL = false>
 cudaError_t few_launch_as(const Params& p, cudaStream_t s) {
   const int sms = num_sms() < kMaxSms ? num_sms() : kMaxSms;
-  return launch_pdl(few_kernel<KI, VI, NT, HEADS>, dim3(unsigned(sms * (NT == 1 ? kCtasPerSm : 2))), dim3(kFewThreads), 0,
-                    s, p);
+  return launch_pdl(few_kernel<KI, VI, NT, HEADS, TAIL>, dim3(unsigned(sms * per_sm(NT, TAIL))), dim3(kFewThreads), 0, s,
+                    p);
 }
 
 template <int NT, int HEADS>
 cudaError_t few_launch_rows(const Params& p, cudaStream_t s) {
   if (p.D <= 64) return few_launch_as<2, 1, NT, HEADS>(p, s);
+  if (p.D == 72) return few_launch_as<2, 1, NT, HEADS, true>(p, s);
   if (p.D <= 96) return few_launch_as<3, 2, NT, HEADS>(p, s);
   return few_launch_as<4, 2, NT, HEADS>(p, s);
 }
@@ -635,7 +688,7 @@ cudaError_t few_launch_heads(const Params& p, cudaStream_t s) {
 
 size_t few_workspace(int head_dim) {
   // two parts a CTA of up to four heads of 8 rows (three CTAs an SM) or 16 (two CTAs)
-  const size_t rows = size_t(kMaxSms) * (kCtasPerSm * 8 > 2 * 16 ? kCtasPerSm * 8 : 2 * 16);
+  const size_t rows = size_t(kMaxSms) * (kMostPerSm * 8 > 2 * 16 ? kMostPerSm * 8 : 2 * 16);
   return kCounterBytes + rows * 2 * 4 * size_t(head_dim + 2) * sizeof(float);
 }
 
