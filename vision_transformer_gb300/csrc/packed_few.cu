@@ -17,7 +17,8 @@
 // number allows (or two heads and alternate keys, or one head): the rows of a key lie side by
 // side, a row of a narrow head is no whole number of DRAM's 64 bytes, and so the parts of a sector
 // are asked for at the same time (64 probes, 16 heads of 72: 252 MB read for 163 MB of keys and
-// values with a head per CTA). Three CTAs run per SM.
+// values with a head per CTA). Two to four CTAs run per SM, by their registers: these hold what is in
+// flight.
 //
 // Work: the (document, group of key heads, block of rows) items are laid out one behind another
 // in steps of 64 keys of one head or 16 of four, and every CTA takes an equal, contiguous share of
@@ -234,7 +235,8 @@ __device__ __forceinline__ void put_part(float* to, const float* y) {
 // KI: 32-dimension groups of a key row, VI: 64-dimension groups of a value row, NT: 8-row
 // tiles of an item, HEADS: key heads of an item (4 / HEADS warps share a head's keys). TAIL: eight
 // more dimensions behind the groups (72), in instructions of their own: another group of each
-// would hold registers for 96 and 128 dimensions, and what is in flight is bound by registers.
+// would hold registers for 96 and 128 dimensions (64 probes, 16 heads of 72: 47.3 us with three CTAs
+// an SM; 42.4 so, and 41.2 with the four that then fit, though they spill some).
 template <int KI, int VI, int NT, int HEADS, bool TAIL>
 __global__ void __launch_bounds__(kFewThreads, per_sm(NT, TAIL)) few_kernel(const __grid_constant__ Params p) {
   constexpr int kRows = 8 * NT, kSplit = 4 / HEADS, kStep = 16 * kSplit;
@@ -674,7 +676,7 @@ cudaError_t few_launch_rows(const Params& p, cudaStream_t s) {
 template <int NT>
 cudaError_t few_launch_heads(const Params& p, cudaStream_t s) {
   // Neighbouring heads in a CTA where a head's row is no whole number of 64 bytes (64 probes over
-  // images, 16 heads of 72: 52 us against 70 with a head per CTA); else a head per CTA, whose
+  // images, 16 heads of 72: 52 us then against 70 with a head per CTA, and 47 against 58 with two); else a head per CTA, whose
   // warps then share its long run of keys (one token of 16 requests, 8 key heads of 128: 162 us
   // against 178). Also where there is so little to read that a head's keys had better be spread
   // over as many warps as there are.
