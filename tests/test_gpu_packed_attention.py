@@ -621,3 +621,28 @@ def test_hidden_values_among_few_items(sv, poison):
     assert torch.equal(torch.isfinite(got).all(1), ~sees)
     err = (got - clean).abs()[~sees].amax(1)
     assert (err <= 2.0 ** -9 * clean[~sees].abs().amax(1).clamp(min=1.0)).all()
+
+
+@pytest.mark.parametrize("rest", [100, 1100])
+def test_long_ranges_among_many_documents(sv, rest):
+    """Divided ranges in different groups of 32 documents, beside short ones."""
+    lk = [rest] * 40
+    lk[3], lk[35], lk[36], lk[20] = 9000, 7001, 0, 1025
+    for hq, hk, d in ((1, 1, 72), (4, 2, 64)):
+        c = Case([17] * 40, lk, hq, hk, d, seed=rest)
+        for mask in (0, 1):
+            o = c.run(sv, mask=mask)
+            c.check(o, mask=mask)
+            assert torch.equal(o, c.run(sv, mask=mask, workspace=c.ws))
+    sv.sv_sync()
+
+
+def test_more_parts_than_blocks(sv):
+    """Items of one tile, divided into more parts than there are SMs."""
+    for hq, hk, d in ((8, 2, 128), (6, 3, 64)):
+        c = Case([1000], [9000], hq, hk, d, seed=d)
+        for opt in (dict(), dict(mask=1), dict(mask=1, prefix=[4000], softcap=8.0)):
+            o = c.run(sv, **opt)
+            c.check(o, **opt)
+            assert torch.equal(o, c.run(sv, workspace=c.ws, **opt))
+    sv.sv_sync()
