@@ -646,3 +646,31 @@ def test_more_parts_than_blocks(sv):
             c.check(o, **opt)
             assert torch.equal(o, c.run(sv, workspace=c.ws, **opt))
     sv.sv_sync()
+
+
+@pytest.mark.parametrize("few", [False, True])
+def test_rows_far_behind_the_first(sv, few):
+    """Queries, keys and output rows behind 2^31 values, for either kernel."""
+    stride, n, d = 65536, 36000, 64
+    wide = torch.empty(n * stride, dtype=torch.float16, device="cuda").view(n, stride)
+    qkv = _randn(3, n, 3 * d).half()
+    wide[:, 1024:1024 + 3 * d] = qkv
+    lens = [1] * 17000 + [2] * 8000 + [3] * 1000 if few else [n - 500, 500]
+    q_off = _offsets(lens)
+    opt = sv.sv_attention_options(mask=1)
+    sv.sv_attention_packed(wide[:, 1024:1024 + d], wide[:, 1024 + d:1024 + 2 * d], wide[:, 1024 + 2 * d:1024 + 3 * d],
+                           wide[:, 2048:2048 + d], q_off, q_off, len(lens), n, n, 1, 1, d, q_stride=stride,
+                           k_stride=stride, v_stride=stride, o_stride=stride, options=opt)
+    sv.sv_sync()
+    got = wide[:, 2048:2048 + d].double()
+    a = 0
+    for m in lens[:3] + lens[-40:] if few else lens:
+        if few and a == 3:
+            a = n - sum(lens[-40:])
+        # (the last rows of a long document stand for all)
+        rows = slice(max(0, m - 300), m)
+        q, k, v = (qkv[a:a + m, i * d:(i + 1) * d].reshape(m, 1, d) for i in range(3))
+        ref, av, terms = packed_ref.document(q[rows], k, v, 1)
+        tol = packed_ref.bound(ref, av, terms, m, float(v.abs().max()), d)
+        assert ((got[a:a + m][rows].reshape(ref.shape) - ref).abs() <= tol).all(), (a, m)
+        a += m
