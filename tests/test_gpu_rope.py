@@ -145,3 +145,53 @@ def test_rope_on_another_stream_and_in_a_graph(sv):
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(y2, want)
+
+
+def test_rows_far_behind_the_first(sv):
+    """In place behind 2^31 values, the bits of a compact copy."""
+    stride, n, heads, D = 65536, 36000, 3, 72
+    wide = torch.empty(n * stride, dtype=torch.float16, device="cuda").view(n, stride)
+    gen = torch.Generator("cuda").manual_seed(7)
+    x = torch.randn(n, heads * D, generator=gen, device="cuda").half()
+    pos = torch.stack([torch.arange(n) % 191, torch.arange(n) // 191]).int().cuda()
+    plan = sv.sv_rope_plan_init(D, 2, 0, 100.0)
+    part = wide[:, 512:512 + heads * D]
+    for norm in (False, True):
+        part.copy_(x)
+        y = torch.empty_like(x)
+        if norm:
+            z, zk = x[:, :D].contiguous(), torch.empty(n, D, dtype=torch.float16, device="cuda")
+            sv.sv_qk_norm_rope(x, z, y, zk, None, None, pos, plan, n, heads, 1, D)
+            sv.sv_qk_norm_rope(part, z, part, zk, None, None, pos, plan, n, heads, 1, D, q_stride=stride,
+                               q_out_stride=stride)
+        else:
+            sv.sv_rope(x, y, pos, plan, n, heads, D)
+            sv.sv_rope(part, part, pos, plan, n, heads, D, x_stride=stride, y_stride=stride)
+        sv.sv_sync()
+        assert torch.equal(part, y)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("D,rot,layout", [(72, 72, 0), (128, 64, 1), (24, 20, 0)])
+def test_a_head_of_nan_stays_alone(sv, bad, D, rot, layout):
+    """Heads beside a head of NaN or infinities keep their bits, with and without the norm."""
+    rows, heads = 40, 9
+    x = _x(3, rows, heads * D).cuda()
+    pos = torch.arange(rows, dtype=torch.int32, device="cuda")[None].contiguous()
+    plan = sv.sv_rope_plan_init(rot, 1, layout)
+    runs = []
+    for spoiled in (False, True):
+        q = x.clone()
+        if spoiled:
+            q.view(rows, heads, D)[5, 4] = bad
+            q.view(rows, heads, D)[39, 0, 1] = bad
+        y, a, b = torch.empty_like(q), torch.empty_like(q), torch.empty_like(q)
+        sv.sv_rope(q, y, pos, plan, rows, heads, D)
+        sv.sv_qk_norm_rope(q, x, a, b, None, None, pos, plan, rows, heads, heads, D, norm=1)
+        sv.sv_sync()
+        runs.append([t.view(rows, heads, D).clone() for t in (y, a, b)])
+    keep = torch.ones(rows, heads, dtype=torch.bool, device="cuda")
+    keep[5, 4] = keep[39, 0] = False
+    for clean, got in zip(*runs):
+        assert torch.equal(clean[keep], got[keep])
+    assert torch.equal(runs[0][2], runs[1][2]) and not torch.isfinite(runs[1][1][5, 4]).any()
