@@ -38,8 +38,9 @@ constexpr int kFewThreads = 128;
 constexpr int kMinShare = 64;       // keys of a CTA's share at least
 constexpr int kMostPerSm = 4;
 constexpr int kMaxFewGrid = kMaxSms * kMostPerSm;
-// CTAs an SM, by what the registers of a warp allow.
-constexpr int per_sm(int nt, bool tail) { return nt > 1 ? 2 : (tail ? 4 : 3); }
+// CTAs an SM, by what the registers of a warp allow. (Four of heads of 72 side by side spill outside their loop
+// only; four of one such head, or of one of 64, inside it: 16 ranges of 8192 keys, 7 heads of 72, 115 against 47 us.)
+constexpr int per_sm(int nt, bool tail, int heads) { return nt > 1 ? 2 : (tail && heads == 4 ? 4 : 3); }
 
 __device__ __forceinline__ uint4 load16(const __half* p) {
   uint4 r;
@@ -236,9 +237,9 @@ __device__ __forceinline__ void put_part(float* to, const float* y) {
 // tiles of an item, HEADS: key heads of an item (4 / HEADS warps share a head's keys). TAIL: eight
 // more dimensions behind the groups (72), in instructions of their own: another group of each
 // would hold registers for 96 and 128 dimensions (64 probes, 16 heads of 72: 47.3 us with three CTAs
-// an SM; 42.4 so, and 41.2 with the four that then fit, though they spill some).
+// an SM; 42.4 so, and 41.2 with the four that then fit).
 template <int KI, int VI, int NT, int HEADS, bool TAIL>
-__global__ void __launch_bounds__(kFewThreads, per_sm(NT, TAIL)) few_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kFewThreads, per_sm(NT, TAIL, HEADS)) few_kernel(const __grid_constant__ Params p) {
   constexpr int kRows = 8 * NT, kSplit = 4 / HEADS, kStep = 16 * kSplit;
   constexpr int kOut = 64 * VI + (TAIL ? 12 : 4);  // row pitch of the merge buffer (floats)
   __shared__ __align__(16) float red[4][kRows][kOut];
@@ -661,7 +662,7 @@ __global__ void __launch_bounds__(kFewThreads, per_sm(NT, TAIL)) few_kernel(cons
 template <int KI, int VI, int NT, int HEADS, bool TAIL = false>
 cudaError_t few_launch_as(const Params& p, cudaStream_t s) {
   const int sms = num_sms() < kMaxSms ? num_sms() : kMaxSms;
-  return launch_pdl(few_kernel<KI, VI, NT, HEADS, TAIL>, dim3(unsigned(sms * per_sm(NT, TAIL))), dim3(kFewThreads), 0, s,
+  return launch_pdl(few_kernel<KI, VI, NT, HEADS, TAIL>, dim3(unsigned(sms * per_sm(NT, TAIL, HEADS))), dim3(kFewThreads), 0, s,
                     p);
 }
 
@@ -676,7 +677,7 @@ cudaError_t few_launch_rows(const Params& p, cudaStream_t s) {
 template <int NT>
 cudaError_t few_launch_heads(const Params& p, cudaStream_t s) {
   // Neighbouring heads in a CTA where a head's row is no whole number of 64 bytes (64 probes over
-  // images, 16 heads of 72: 52 us then against 70 with a head per CTA, and 47 against 58 with two); else a head per CTA, whose
+  // images, 16 heads of 72: 41 us against 58 with a head per CTA and 46 with two); else a head per CTA, whose
   // warps then share its long run of keys (one token of 16 requests, 8 key heads of 128: 162 us
   // against 178). Also where there is so little to read that a head's keys had better be spread
   // over as many warps as there are.
