@@ -970,11 +970,23 @@ __global__ void __maxnreg__(168)
             tmem_ld_wait(su[2]);
             reg_fence(su[3]);
           }
-          if constexpr (CAP)
+          auto hide = [&]() {
+            if (valid < 32 * kC * (h + 1)) {
+#pragma unroll
+              for (int c = kC * h; c < kC * h + kC; ++c)
+                if (valid < 32 * c + 32)
+#pragma unroll
+                  for (int e = 0; e < 32; ++e)
+                    if (32 * c + e >= valid) sv[c][e] = -INFINITY;
+            }
+          };
+          if constexpr (CAP) {
+            hide();  // (a hidden score has no part in its neighbours' reciprocal)
 #pragma unroll
             for (int c = kC * h; c < kC * h + kC; ++c)
 #pragma unroll
               for (int e = 0; e < 32; e += 4) capped4(&sv[c][e], sl2, cap2);
+          }
           if constexpr (BIAS) {
             const float on = CAP ? 1.0f : sl2;
             if (line) {
@@ -993,14 +1005,7 @@ __global__ void __maxnreg__(168)
                   sv[c][e] = fmaf(-slope2, fabsf(d0 - float(32 * c + e)), CAP ? sv[c][e] : sv[c][e] * sl2);
             }
           }
-          if (valid < 32 * kC * (h + 1)) {
-#pragma unroll
-            for (int c = kC * h; c < kC * h + kC; ++c)
-              if (valid < 32 * c + 32)
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  if (32 * c + e >= valid) sv[c][e] = -INFINITY;
-          }
+          hide();
           float mq[2 * kC];
 #pragma unroll
           for (int k = 0; k < 2 * kC; ++k) {
