@@ -95,6 +95,7 @@ struct Item {
   int k0, lk;           // the document's keys
   int at, prefix, kvh;  // position of the first query among the keys
   int jb, je;           // key tiles
+  int ke;               // keys that some row of the item sees end here
   int slot, splits, split;  // partial result; splits 1: none
   int live;             // 0: no more items
 };
@@ -199,7 +200,8 @@ class Schedule {
     r.q0 = of(doc_.q0) + i0;
     r.nq = min(lq - i0, span_);
     r.at = i0 + r.lk - lq;
-    const int n = (limit_of(p_.causal, r.at + r.nq - 1, r.lk, r.prefix) + kTile - 1) / kTile;
+    r.ke = limit_of(p_.causal, r.at + r.nq - 1, r.lk, r.prefix);  // (the last query sees the most)
+    const int n = (r.ke + kTile - 1) / kTile;
     const int part = (tiles + splits - 1) / splits;
     r.jb = min(r.split * part, n);
     r.je = min(r.jb + part, n);
@@ -721,14 +723,27 @@ __global__ void __maxnreg__(168)
       }
       commit(kBarSFull + w);
     };
-    auto issue_pv = [&](int w, uint32_t st, uint32_t keep) {
+    // `keys` of the tile are an item's (kTile and more: all): the steps behind them are left out.
+    auto issue_pv = [&](int w, uint32_t st, uint32_t keep, int keys) {
       const uint64_t vd = make_sdesc(sbase + L::kOffKV + st * kOp, kBoxBytes, 1024, 2);
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk)  // 16 keys a step: 8 TMEM columns of P, 16 rows of V
-        mma_f16_ts_if(lead, tmem + uint32_t(256 + 128 * w), tmem + uint32_t(128 * w + 8 * kk), vd + uint64_t(kk * (2048 >> 4)),
-                      idesc_o, kk > 0 ? 1u : keep);
+        mma_f16_ts_if(kk == 0 || 16 * kk < keys ? lead : 0u, tmem + uint32_t(256 + 128 * w),
+                      tmem + uint32_t(128 * w + 8 * kk), vd + uint64_t(kk * (2048 >> 4)), idesc_o, kk > 0 ? 1u : keep);
+    };
+    // Value rows of a tile's last step that no row of the item sees (the next document's, say) become zeros: their
+    // probabilities are 0, but 0 times an infinity or NaN would spoil every row. The values must have arrived.
+    auto clear_rest = [&](uint32_t st, int keys) {
+      const int rows = keys > 0 ? -keys & 15 : 16;
+      if (keys >= kTile || !rows) return;
+      uint8_t* to = smem + L::kOffKV + st * kOp + max(keys, 0) * 128;
+      for (int b = 0; b < NB; ++b)
+        for (int x = lane; x < rows * 8; x += 32) *reinterpret_cast<uint4*>(to + b * kBoxBytes + 16 * x) = make_uint4(0, 0, 0, 0);
+      fence_proxy_async_smem();
+      __syncwarp();
     };
     int read = 0;  // items so far
+    int rest = 0;  // keys of the last tile of the item that next() has returned
     // key tiles of the next item that has any (0: there is none); -1 after a time-out, or
     // where it is not there yet and `block` is false
     auto next = [&](bool block) -> int {
@@ -736,12 +751,13 @@ __global__ void __maxnreg__(168)
         const int b = kBarItem + read % kItems, ph = (read / kItems) & 1;
         if (block ? !wait(b, uint32_t(ph)) : !all(mbar_test(bar(b), uint32_t(ph)))) return -1;
         const Item& r = items[read % kItems];
-        const int live = r.live, tiles = r.je - r.jb;
+        const int live = r.live, tiles = r.je - r.jb, end = r.ke - (r.je - 1) * kTile;
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBarItemDone + read % kItems));
         __syncwarp();
         if (!all(live)) return 0;
         ++read;
+        rest = end;
         if (all(tiles > 0)) return tiles;
       }
     };
@@ -771,7 +787,10 @@ __global__ void __maxnreg__(168)
           for (uint32_t w = 0; w < 2 && ok; ++w) {
             if (!(ok = full(2 + w) && wait(kBarPFull + int(w), tt))) break;
             tc_fence_after();
-            issue_pv(int(w), stage(2 + w), s > 0);
+            // (an odd number of tiles: the second group's last one lies behind the item's keys)
+            const int keys = 2 * s + int(w) < tiles - 1 ? kTile : 2 * s + int(w) < tiles ? rest : 0;
+            clear_rest(stage(2 + w), keys);
+            issue_pv(int(w), stage(2 + w), s > 0, keys);
             commit(kBarEmpty + int(stage(2 + w)));
             if (all(s + 1 == steps)) {
               commit(kBarOFull + int(w));
@@ -798,6 +817,7 @@ __global__ void __maxnreg__(168)
     int qb = 0, qph = 0;  // Q buffer and phase of the current item
     while (ok && all(tiles > 0)) {
       int more = 0;  // key tiles of the next item
+      const int end = rest;
       const int qb_next = qb + 1 == kQBufs ? 0 : qb + 1, qph_next = qb + 1 == kQBufs ? qph ^ 1 : qph;
       for (int j = 0; ok && all(j < tiles); ++j, tt ^= 1) {
         // ring: key tile at 0, its values at 1, the next key tile at 2
@@ -807,12 +827,13 @@ __global__ void __maxnreg__(168)
         place(2, st_k, ph);
         // (the copies are waited for before P, which is what the products really wait for)
         ok = wait_full(1) && (last || wait_full(2));
+        if (last && ok) clear_rest(st_v, end);
         bool late = false;  // the next item was not there for S_0
 #pragma unroll 1
         for (int w = 0; w < 2 && ok; ++w) {
           if (!(ok = wait(kBarPFull + w, tt))) break;
           tc_fence_after();
-          issue_pv(w, st_v, j > 0);
+          issue_pv(w, st_v, j > 0, last ? end : kTile);
           int first = w;  // S products to issue: tiles first .. w
           if (last) {
             commit(kBarOFull + w);
