@@ -49,7 +49,7 @@ namespace {
 constexpr int kTile = 128;                  // rows of a query tile, keys of a key tile
 constexpr int kBoxBytes = kTile * 128;      // 128 rows of 64 values: one box of an operand tile
 constexpr int kThreads = 320;
-constexpr int kBarBytes = 768;              // barriers, TMEM address slot, abort flag, items
+constexpr int kBarBytes = 768;              // barriers, TMEM address slot, abort flag, progress count, items
 constexpr int kOutBytes = 32 * 64;          // 32 rows of 32 output columns
 constexpr int kItems = 4;                   // work items between the copy warp and the others
 constexpr uint32_t kTmemCols = 512;
@@ -99,7 +99,7 @@ struct Item {
   int slot, splits, split;  // partial result; splits 1: none
   int live;             // 0: no more items
 };
-constexpr int kOffItems = 8 * kNumBars + 8;  // in the barrier area
+constexpr int kOffItems = 8 * kNumBars + 16;  // in the barrier area
 static_assert(kOffItems + kItems * sizeof(Item) <= kBarBytes, "barrier area");
 
 // The items in order, worked out by the copy warp from the documents' lengths: a
@@ -112,8 +112,8 @@ static_assert(kOffItems + kItems * sizeof(Item) <= kBarBytes, "barrier area");
 class Schedule {
  public:
   // span: queries of an item; min_split: key tiles of a part at least.
-  __device__ __forceinline__ Schedule(const Params& p, int lane, int span, int min_split)
-      : p_(p), lane_(lane), docs_(p.docs), span_(span) {
+  __device__ __forceinline__ Schedule(const Params& p, int lane, int span, int min_split, unsigned* beat)
+      : p_(p), lane_(lane), docs_(p.docs), span_(span), beat_(beat) {
     chunk_ = 0x7fffffff;
     float work = 0.0f;
     bool bad = false;
@@ -210,6 +210,7 @@ class Schedule {
 
  private:
   __device__ __forceinline__ void load(int d0) {
+    if (lane_ == 0 && d0 % (1 << 20) == 0) atomicAdd(beat_, 1u);  // (2^20 documents are passed in a tenth of a second)
     bad_ = !document(p_, d0 + lane_, docs_, doc_);
     pairs_ = (doc_.lq + span_ - 1) / span_;
     tiles_ = (doc_.lk + kTile - 1) / kTile;  // of the last query
@@ -246,6 +247,7 @@ class Schedule {
   const Params& p_;
   int lane_, docs_, span_, chunk_;
   bool bad_;
+  unsigned* beat_;
   int items_ = 0;
   int d0_ = -32, base_ = 0, total_ = 0, slot_base_ = 0, slot_total_ = 0;
   Document doc_;  // this lane's
@@ -254,9 +256,26 @@ class Schedule {
 
 // A wait whose long form is one function for all of the kernel's waits: inlined, the waits alone
 // were a sixth of the code, and code that runs once an item then came from beyond the
-// instruction caches.
+// instruction caches. It gives up (as mbar_wait does) after the limit without a step of the work whose
+// length the inputs decide, which counts its steps behind the abort flag: rows that are computed
+// again, and documents that are passed on the way to an item.
 __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int* abort, int* err) {
-  return mbar_wait(bar, parity, abort, err);
+  unsigned long long t0 = globaltimer();
+  int seen = abort[1];
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (i & 255u) continue;
+    if (*abort) return false;
+    if (globaltimer() - t0 <= kWaitLimitNs) continue;
+    const int now = abort[1];
+    if (now == seen) {
+      *abort = 1;
+      atomicOr(err, kDevErrTimeout);
+      return false;
+    }
+    seen = now;
+    t0 = globaltimer();
+  }
 }
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort, int* err) {
   return mbar_try_wait(bar, parity) || wait_long(bar, parity, abort, err);
@@ -325,35 +344,69 @@ __device__ __noinline__ void join_parts(const Params& p, const Item& it, long lo
 // its item has no keys at all.
 enum { kNothing = 1, kPart = 2, kEmpty = 4 };
 
-// Row r of tile w whose O is not finite, again from the visible keys alone; of a part, its sums,
-// exponent and denominator.
-__device__ __noinline__ void write_again(const Params& p, const Item& it, long long out_to, int how, int w, int r) {
-  const int Dn = (p.D + 15) / 16 * 16;
+// The rows of tile w whose O is not finite (`bad`; r: this lane's), again from the visible keys alone where a key that
+// the row does not see has spoiled it; of a part, their sums, exponents and denominators. By a whole warp.
+__device__ __noinline__ void rows_again(const Params& p, const Item& it, long long out_to, int how, int w, int r, bool bad,
+                                        unsigned* beat) {
+  const int Dn = (p.D + 15) / 16 * 16, lane = r & 31;
+  const __half* k = p.k + it.k0 * p.ks + it.kvh * p.D;
+  const __half* v = p.v + it.k0 * p.vs + it.kvh * p.D;
   const int i = w * p.qt + r / p.group, head = it.kvh * p.group + r % p.group;
-  float* pb = p.partial + (size_t(it.slot) * 2 + w) * size_t(Dn + 2) * kTile + r;
-  float acc[128], m, l;
-  row_again(p, p.q + static_cast<long long>(it.q0 + i) * p.qs + head * p.D, p.k + it.k0 * p.ks + it.kvh * p.D,
-            p.v + it.k0 * p.vs + it.kvh * p.D, it.jb * kTile,
-            min(limit_of(p.causal, it.at + i, it.lk, it.prefix), it.je * kTile), it.at + i,
-            p.slopes ? __ldg(p.slopes + head) : 0.0f, acc, m, l);
-  for (int c = 0; c < p.D; c += 8) {
-    float y[8];
-    for (int e = 0; e < 8; ++e) y[e] = how & kPart ? acc[c + e] : acc[c + e] / l;
-    if (how & kPart)
-      for (int e = 0; e < 8; ++e) __stcg(pb + size_t(2 + c + e) * kTile, y[e]);
-    else
-      store8(p, size_t(out_to) + c, y);
-  }
-  if (how & kPart) {
-    __stcg(pb, m);
-    __stcg(pb + kTile, l);
+  const int kb = it.jb * kTile, ke = min(it.ke, it.je * kTile);  // the keys of the products
+  const int lim = out_to >= 0 && bad ? max(limit_of(p.causal, it.at + i, it.lk, it.prefix), kb) : ke;
+  const int low = __reduce_min_sync(0xffffffffu, lim);
+  const int last = low < ke ? last_spoiled(p, v, low, ke, lane) : -1;
+  const float slope = p.slopes && lim < ke ? __ldg(p.slopes + head) : 0.0f;
+  __syncwarp();  // (what the rows' own lanes have stored comes first)
+#pragma unroll 1
+  for (uint32_t todo = __ballot_sync(0xffffffffu, lim <= last); todo;) {
+    Row rows[4];
+    int src[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      src[x] = todo ? __ffs(int(todo)) - 1 : -1;
+      todo &= todo - 1;
+      auto of = [&](auto y) { return __shfl_sync(0xffffffffu, y, max(src[x], 0)); };
+      const int q_row = of(i);
+      rows[x].q = p.q + static_cast<long long>(it.q0 + q_row) * p.qs + of(head) * p.D;
+      rows[x].ke = src[x] < 0 ? kb : of(lim);
+      rows[x].at = it.at + q_row;
+      rows[x].slope = of(slope);
+    }
+    float4 acc[4];
+    float m, l;
+    rows_again4(p, rows, k, v, kb, lane, beat, acc, m, l);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const float row_m = __shfl_sync(0xffffffffu, m, 8 * x), row_l = __shfl_sync(0xffffffffu, l, 8 * x);
+      const long long to = __shfl_sync(0xffffffffu, out_to, max(src[x], 0));
+      const int row_how = __shfl_sync(0xffffffffu, how, max(src[x], 0));
+      if (src[x] < 0) continue;
+      if (row_how & kPart) {
+        float* pb = p.partial + (size_t(it.slot) * 2 + w) * size_t(Dn + 2) * kTile + (r - lane + src[x]);
+        if (lane == 0) {
+          __stcg(pb, row_m);
+          __stcg(pb + kTile, row_l);
+        }
+        if (lane < p.D / 4) {
+          pb += size_t(2 + 4 * lane) * kTile;
+          __stcg(pb, acc[x].x);
+          __stcg(pb + kTile, acc[x].y);
+          __stcg(pb + 2 * kTile, acc[x].z);
+          __stcg(pb + 3 * kTile, acc[x].w);
+        }
+      } else if (lane < p.D / 4) {
+        store4(p, size_t(to) + 4 * lane,
+               make_float4(acc[x].x / row_l, acc[x].y / row_l, acc[x].z / row_l, acc[x].w / row_l));
+      }
+    }
   }
 }
 
 // Row r of tile w where `how` is not 0 for its whole warp. Out of the way of the common case,
 // whose code must stay in the instruction caches.
 __device__ __noinline__ void write_special(const Params& p, const Item& it, uint32_t o_tm, float m, float l,
-                                           long long out_to, int how, int w, int r) {
+                                           long long out_to, int how, int w, int r, unsigned* beat) {
   const int Dn = (p.D + 15) / 16 * 16;
   const int i = w * p.qt + r / p.group;
   const int lim = out_to < 0 ? 0 : limit_of(p.causal, it.at + i, it.lk, it.prefix);
@@ -384,14 +437,13 @@ __device__ __noinline__ void write_special(const Params& p, const Item& it, uint
       store8(p, size_t(out_to) + c, y);
     }
   }
-  if (out_to >= 0 && bad != 0.0f) write_again(p, it, out_to, how, w, r);
-  __syncwarp();
+  if (__any_sync(0xffffffffu, out_to >= 0 && bad != 0.0f)) rows_again(p, it, out_to, how, w, r, bad != 0.0f, beat);
   if (how & kPart) join_parts(p, it, out_to, w, r);
 }
 
 // Row r of an item of one tile whose key tiles the two groups have shared out: exponent, denominator and O of both.
 __device__ __noinline__ void write_shared(const Params& p, const Item& it, uint32_t o_tm, float m0, float l0, float m1,
-                                          float l1, long long out_to, int how, int r) {
+                                          float l1, long long out_to, int how, int r, unsigned* beat) {
   const int Dn = (p.D + 15) / 16 * 16;
   const float mx = fmaxf(m0, m1), ref = mx == -INFINITY ? 0.0f : mx;
   const float f0 = ex2(m0 - ref), f1 = ex2(m1 - ref), l = fmaf(f1, l1, f0 * l0);
@@ -423,8 +475,7 @@ __device__ __noinline__ void write_shared(const Params& p, const Item& it, uint3
       store8(p, size_t(out_to) + c, y);
     }
   }
-  if (out_to >= 0 && bad != 0.0f) write_again(p, it, out_to, how, 0, r);
-  __syncwarp();
+  if (__any_sync(0xffffffffu, out_to >= 0 && bad != 0.0f)) rows_again(p, it, out_to, how, 0, r, bad != 0.0f, beat);
   if (how & kPart) join_parts(p, it, out_to, 0, r);
 }
 
@@ -439,9 +490,9 @@ __device__ __noinline__ void write_shared(const Params& p, const Item& it, uint3
 template <int NB, bool E4M3, typename F>
 __device__ __forceinline__ void write_rows(const Params& p, const Item& it, const CUtensorMap& to_map, uint8_t* stage,
                                            uint32_t o_tm, float m, float l, long long out_to, int how, int w, int r,
-                                           F loaded) {
+                                           unsigned* beat, F loaded) {
   if (__any_sync(0xffffffffu, how)) {
-    write_special(p, it, o_tm, m, l, out_to, how, w, r);
+    write_special(p, it, o_tm, m, l, out_to, how, w, r, beat);
     loaded();
     return;
   }
@@ -534,9 +585,8 @@ __device__ __forceinline__ void write_rows(const Params& p, const Item& it, cons
                 make_uint2(v[k][0], v[k][1]);
       }
     }
-    __syncwarp();  // (a row written again comes after the other lanes' stores to it)
   }
-  if (bad) write_again(p, it, out_to, how, w, r);
+  if (__any_sync(0xffffffffu, bad)) rows_again(p, it, out_to, how, w, r, bad, beat);
 }
 
 // SOLO: items of one tile, whose key tiles the two groups take in turn (for launches of few items: half the chain, and
@@ -556,6 +606,7 @@ __global__ void __maxnreg__(168)
   const uint32_t bar0 = sbase + L::kOffBar;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffBar + 8 * kNumBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  unsigned* beat = reinterpret_cast<unsigned*>(tmem_slot + 2);  // see wait_long
   auto bar = [&](int i) { return bar0 + 8u * uint32_t(i); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -581,6 +632,7 @@ __global__ void __maxnreg__(168)
     mbar_init(bar(kBarRead), 128);
     mbar_init(bar(kBarDrain), 1);
     *abort_flag = 0;
+    *beat = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -599,7 +651,7 @@ __global__ void __maxnreg__(168)
   };
 
   if (warp == 0) {
-    Schedule sched(p, lane, (SOLO ? 1 : 2) * p.qt, (SOLO ? 2 : 1) * kMinSplit);
+    Schedule sched(p, lane, (SOLO ? 1 : 2) * p.qt, (SOLO ? 2 : 1) * kMinSplit, beat);
     if (lane == 0) {
       prefetch_tmap(&tq);
       prefetch_tmap(&tk);
@@ -911,7 +963,7 @@ __global__ void __maxnreg__(168)
       if (lane == 0) mbar_arrive(bar(kBarItemDone + n % kItems));
     };
     // Rows are loaded 32 columns at a time. The columns that no product writes hold what an earlier kernel has left;
-    // a NaN among them would send every row the long way round (write_again).
+    // a NaN among them would send every row the long way round (rows_again).
     for (int c = Dn; c < (p.D + 31) / 32 * 32; c += 8) {
       const uint32_t zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
       tmem_st8(o_tm + uint32_t(c), zero);
@@ -933,7 +985,7 @@ __global__ void __maxnreg__(168)
         if (pending_keys && !__all_sync(0xffffffffu, wait_bar(bar(kBarOFull + w), (full - 1) & 1, abort_flag, p.err)))
           break;
         tc_fence_after();
-        write_rows<NB, E4M3>(p, items[pending % kItems], to, stage, o_tm, m, l, out_to, out_how, w, r, [] {});
+        write_rows<NB, E4M3>(p, items[pending % kItems], to, stage, o_tm, m, l, out_to, out_how, w, r, beat, [] {});
         done(pending);
         pending = -1;
       }
@@ -1108,7 +1160,8 @@ __global__ void __maxnreg__(168)
           // of this item, which overwrites O, waits for the arrival. Between the two O is only
           // loaded; its rows are written while the products run. (Written before the item's
           // first tile they took 4,000 to 6,000 cycles that nothing else ran in.)
-          write_rows<NB, E4M3>(p, items[pending % kItems], to, stage, o_tm, m_before, l_before, to_before, how_before, w, r, arrive);
+          write_rows<NB, E4M3>(p, items[pending % kItems], to, stage, o_tm, m_before, l_before, to_before, how_before, w, r,
+                               beat, arrive);
           done(pending);
           pending = -1;
         } else {
@@ -1130,13 +1183,13 @@ __global__ void __maxnreg__(168)
             if (!wait(kBarRead)) break;  // (the next item's P V writes O again)
           } else {
             if (!wait(kBarOFull) || !wait(kBarOFull + 1) || !wait(kBarJoin)) break;
-            write_shared(p, it, o_tm, m, l, ml->x, ml->y, out_to, out_how, r);
+            write_shared(p, it, o_tm, m, l, ml->x, ml->y, out_to, out_how, r, beat);
             tc_fence_before();
             mbar_arrive(bar(kBarRead));
           }
           ++full;
         } else if (w == 0) {
-          write_special(p, it, o_tm, m, l, out_to, out_how, 0, r);
+          write_special(p, it, o_tm, m, l, out_to, out_how, 0, r, beat);
         }
         done(n);
         continue;

@@ -126,35 +126,151 @@ __device__ __forceinline__ void store8(const Params& p, size_t at, const float* 
   put8(p.out_e4m3, static_cast<uint8_t*>(p.o) + (p.out_e4m3 ? at : 2 * at), y);
 }
 
+// Four values of an output row, on a multiple of four.
+__device__ __forceinline__ void store4(const Params& p, size_t at, const float4& y) {
+  if (p.out_e4m3) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(16.0f * y.x, 16.0f * y.y), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(16.0f * y.z, 16.0f * y.w), __NV_SATFINITE, __NV_E4M3);
+    *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.o) + at) = lo | hi << 16;
+  } else {
+    __half2 h[2] = {__floats2half2_rn(y.x, y.y), __floats2half2_rn(y.z, y.w)};
+    *reinterpret_cast<uint2*>(static_cast<__half*>(p.o) + at) = *reinterpret_cast<const uint2*>(h);
+  }
+}
+
 // One value of an output row.
 __device__ __forceinline__ void store1(const Params& p, size_t at, float y) {
   if (p.out_e4m3) static_cast<uint8_t*>(p.o)[at] = __nv_cvt_float_to_fp8(16.0f * y, __NV_SATFINITE, __NV_E4M3);
   else static_cast<__half*>(p.o)[at] = __float2half_rn(y);
 }
 
-// A row whose tensor-core result is not finite, again from the visible keys alone: a tile's
-// product multiplies the probability 0 of a hidden key with its value, which is NaN for an
-// infinite or NaN value. Keys kb .. ke - 1 of the document, query position `at`; unscaled
-// sums to acc[D], their exponent and denominator to m and l.
-static __device__ __noinline__ void row_again(const Params& p, const __half* q, const __half* k, const __half* v,
-                                              int kb, int ke, int at, float slope, float* acc, float& m_out,
-                                              float& l_out) {
-  float m = -INFINITY, l = 0.0f;
-  for (int c = 0; c < p.D; ++c) acc[c] = 0.0f;
-  for (int j = kb; j < ke; ++j) {
-    const __half *kr = k + j * p.ks, *vr = v + j * p.vs;
-    float s = 0.0f;
-    for (int c = 0; c < p.D; ++c) s = fmaf(__half2float(q[c]), __half2float(kr[c]), s);
-    s *= p.scale;
-    if (p.cap > 0.0f) s = p.cap * tanhf(s / p.cap);
-    s = (s - slope * fabsf(float(at - j))) * kLog2e;
-    const float mn = (s > m || s != s) ? s : m;  // NaN stays
-    const float ref = mn == -INFINITY ? 0.0f : mn;
-    const float f = m == mn ? 1.0f : exp2f(m - ref), e = exp2f(s - ref);
-    l = l * f + e;
-    for (int c = 0; c < p.D; ++c) acc[c] = fmaf(e, __half2float(vr[c]), acc[c] * f);
-    m = mn;
+// Rows whose result is not finite. A tile's product multiplies the probability 0 of a hidden key with its value,
+// which is NaN for an infinite or NaN value. Keys behind the last one that any row of an item sees never reach a
+// product, so only keys that some of its rows see and others do not can do this: a row is computed again where one
+// of those keys that it does not see holds such a value, and a row that sees one itself keeps the products' result,
+// which is not finite either.
+
+// The last of the keys from .. to - 1 whose value row (D values at v, a document's first) holds an infinity or NaN, -1:
+// none. By a whole warp.
+static __device__ __noinline__ int last_spoiled(const Params& p, const __half* v, int from, int to, int lane) {
+  const int chunks = p.D / 8;
+  int last = -1;
+  for (long long x = lane; x < static_cast<long long>(to - from) * chunks; x += 32) {
+    const int key = from + int(x / chunks);
+    const uint4 w = __ldg(reinterpret_cast<const uint4*>(v + key * p.vs) + int(x % chunks));
+    bool bad = false;
+    const uint32_t pairs[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      bad |= (pairs[e] & 0x7c00u) == 0x7c00u || (pairs[e] & 0x7c000000u) == 0x7c000000u;
+    if (bad) last = key;
   }
+  return __reduce_max_sync(0xffffffffu, last);
+}
+
+// A row to be computed again: its query, where its visible keys end, its position, its slope.
+struct Row {
+  const __half* q;
+  int ke, at;
+  float slope;
+};
+
+// Up to four rows of a key head from their visible keys alone, kb .. ke - 1 of the document (no keys: not a row), by a
+// whole warp: eight keys at a time, of which a lane holds the columns 4 lane .. 4 lane + 3 and then the score of row
+// lane / 8 and key lane % 8. Unscaled sums of the rows (the lane's columns) in acc, exponent and denominator of row
+// lane / 8 in m and l. 64 keys turn `beat` on (null: nobody waits for this). 31 rows over 20,000 keys of 128
+// dimensions, the warp alone on its SM: 30 ms (a row at a time 81, a thread a row 370).
+static __device__ __noinline__ void rows_again4(const Params& p, const Row (&rows)[4], const __half* k, const __half* v,
+                                                int kb, int lane, unsigned* beat, float4 (&acc)[4], float& m_out,
+                                                float& l_out) {
+  const bool mine = lane < p.D / 4;
+  auto four = [&](const __half* row) {
+    uint2 w = make_uint2(0u, 0u);
+    if (mine) w = __ldg(reinterpret_cast<const uint2*>(row) + lane);
+    return w;
+  };
+  auto wide = [](uint2 w) {
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&w.x));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
+    return make_float4(a.x, a.y, b.x, b.y);
+  };
+  float4 q[4], y[4];
+  int end = kb, ke = kb, at = 0;
+  float slope = 0.0f;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const bool real = rows[r].ke > kb;
+    q[r] = wide(real ? four(rows[r].q) : make_uint2(0u, 0u));
+    y[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    end = max(end, rows[r].ke);
+    if (lane / 8 == r && real) ke = rows[r].ke, at = rows[r].at, slope = rows[r].slope;
+  }
+  float m = -INFINITY, l = 0.0f;
+#pragma unroll 1
+  for (int j0 = kb; j0 < end; j0 += 8) {
+    uint2 kx[8], vx[8];
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+      kx[b] = vx[b] = make_uint2(0u, 0u);
+      if (j0 + b < end) {
+        kx[b] = four(k + (j0 + b) * p.ks);
+        vx[b] = four(v + (j0 + b) * p.vs);
+      }
+    }
+    float s[32];
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+      const float4 kf = wide(kx[b]);
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        s[8 * r + b] = fmaf(q[r].x, kf.x, fmaf(q[r].y, kf.y, fmaf(q[r].z, kf.z, q[r].w * kf.w)));
+    }
+    // summed over the lanes, each keeping one of the 32
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1)
+#pragma unroll
+      for (int b = 0; b < 16 / x; ++b) {
+        const bool odd = lane & x;
+        const float give = odd ? s[2 * b] : s[2 * b + 1];
+        s[b] = (odd ? s[2 * b + 1] : s[2 * b]) + __shfl_xor_sync(0xffffffffu, give, x);
+      }
+    const int key = j0 + (lane & 7);
+    float x = s[0] * p.scale;
+    if (p.cap > 0.0f) x = p.cap * tanhf(x / p.cap);
+    x = key < ke ? (x - slope * fabsf(float(at - key))) * kLog2e : -INFINITY;
+    float up = x;
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, o));
+    up = fmaxf(up, m);
+    const float ref = up == -INFINITY ? 0.0f : up, back = exp2f(m - ref), e = exp2f(x - ref);
+    m = up;
+    float sum = e;
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    l = fmaf(l, back, sum);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const float f = __shfl_sync(0xffffffffu, back, 8 * r);
+      y[r] = make_float4(y[r].x * f, y[r].y * f, y[r].z * f, y[r].w * f);
+    }
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+      const float4 vf = wide(vx[b]);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float eb = __shfl_sync(0xffffffffu, e, 8 * r + b);
+        if (j0 + b < rows[r].ke) {  // (a key that only a later row of the four sees stays out)
+          y[r].x = fmaf(eb, vf.x, y[r].x);
+          y[r].y = fmaf(eb, vf.y, y[r].y);
+          y[r].z = fmaf(eb, vf.z, y[r].z);
+          y[r].w = fmaf(eb, vf.w, y[r].w);
+        }
+      }
+    }
+    if (beat && lane == 0 && (j0 - kb) % 64 == 0) atomicAdd(beat, 1u);
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) acc[r] = y[r];
   m_out = m;
   l_out = l;
 }

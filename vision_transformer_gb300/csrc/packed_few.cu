@@ -426,6 +426,56 @@ __global__ void __launch_bounds__(kFewThreads, per_sm(NT, TAIL, HEADS)) few_kern
     const int c0 = share.cta_of(sg.base), c1 = share.cta_of(sg.base + sg.steps - 1);  // the item's parts
     const Parts parts{part(c0, 0), size_t(HEADS * kRows) * size_t(p.D + 2), c1 - c0 + 1, p.D, HEADS * kRows};
 
+    // Those of the rows `todo` (a bit a row) of head hw of the segment that a hidden key's value has spoiled, again
+    // from their visible keys alone, by one warp.
+    auto again = [&](int hw, unsigned todo) {
+      const __half* k = p.k + sg.doc.k0 * p.ks + (sg.kvh + hw) * p.D;
+      const __half* v = p.v + sg.doc.k0 * p.vs + (sg.kvh + hw) * p.D;
+      const int begin = sg.s0 * kStep, ln = int(threadIdx.x) & 31;
+      auto limit = [&](int r) {
+        return max(begin, limit_of(p.causal, (sg.row0 + r) / p.group + lk - sg.doc.lq, lk, sg.doc.prefix));
+      };
+      const int low = limit(__ffs(int(todo)) - 1);  // (later rows see no fewer keys)
+      const int spoiled = low < last ? last_spoiled(p, v, low, last, ln) : -1;
+      __syncwarp();  // (what other lanes have stored of the rows comes first)
+#pragma unroll 1
+      while (todo) {
+        Row of[4];
+        int at_r[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int r = at_r[x] = todo ? __ffs(int(todo)) - 1 : -1;
+          todo &= todo - 1;
+          const int i = (sg.row0 + max(r, 0)) / p.group;
+          const int head = (sg.kvh + hw) * p.group + (sg.row0 + max(r, 0) - i * p.group), lim = limit(max(r, 0));
+          if (lim > spoiled) at_r[x] = -1;  // (its result is the products')
+          of[x].q = p.q + static_cast<long long>(sg.doc.q0 + i) * p.qs + head * p.D;
+          of[x].ke = at_r[x] < 0 ? begin : min(last, lim);
+          of[x].at = i + lk - sg.doc.lq;
+          of[x].slope = p.slopes ? __ldg(p.slopes + head) : 0.0f;
+        }
+        float4 acc[4];
+        float mx, sum;
+        rows_again4(p, of, k, v, begin, ln, nullptr, acc, mx, sum);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int r = at_r[x];
+          const float row_m = __shfl_sync(0xffffffffu, mx, 8 * x), row_l = __shfl_sync(0xffffffffu, sum, 8 * x);
+          if (r < 0) continue;
+          const int i = (sg.row0 + r) / p.group, head = (sg.kvh + hw) * p.group + (sg.row0 + r - i * p.group);
+          const int row = hw * rows + r;
+          if (whole) {
+            if (ln < p.D / 4)
+              store4(p, size_t(sg.doc.q0 + i) * size_t(p.os) + size_t(head) * size_t(p.D) + size_t(4 * ln),
+                     make_float4(acc[x].x / row_l, acc[x].y / row_l, acc[x].z / row_l, acc[x].w / row_l));
+          } else {
+            if (ln < p.D / 4) __stcg(reinterpret_cast<float4*>(mine + row * p.D) + ln, acc[x]);
+            if (ln == 0) __stcg(reinterpret_cast<float2*>(mine_ml) + row, make_float2(row_m, row_l));
+          }
+        }
+      }
+    };
+
     // Row r of head hw of the item from all its parts, by one warp.
     auto join_row = [&](int hw, int r) {
       float mx, sum;
@@ -445,6 +495,7 @@ __global__ void __launch_bounds__(kFewThreads, per_sm(NT, TAIL, HEADS)) few_kern
     if constexpr (kSplit == 1) {
       // A warp has its head's rows to itself: they go out from its registers, and the warps of the
       // CTA need not wait for one another. A lane holds eight neighbouring columns of two rows.
+      unsigned redo = 0;  // rows that are not finite
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -483,24 +534,11 @@ __global__ void __launch_bounds__(kFewThreads, per_sm(NT, TAIL, HEADS)) few_kern
           }
           if (live && !whole && g == 0) __stcg(reinterpret_cast<float2*>(at_ml), make_float2(m[n][e], sum));
           const unsigned rows_bad = __ballot_sync(0xffffffffu, live && bad != 0.0f);
-          if (rows_bad) {  // again from the visible keys alone, a lane a row
-            __syncwarp();
-            if (g == 0 && (rows_bad & (0x11111111u << t))) {
-              const int pos = i + lk - sg.doc.lq;
-              float acc[128], mx;
-              row_again(p, p.q + static_cast<long long>(sg.doc.q0 + i) * p.qs + head * p.D, kb, vb, sg.s0 * kStep,
-                        min(last, lim[n][e]), pos, p.slopes ? __ldg(p.slopes + head) : 0.0f, acc, mx, sum);
-              for (int c = 0; c < p.D; c += 8) {
-                float y[8];
-                for (int j = 0; j < 8; ++j) y[j] = whole ? acc[c + j] / sum : acc[c + j];
-                if (whole) store8(p, to + c, y);
-                else put_part(at_p + c, y);
-              }
-              if (!whole) __stcg(reinterpret_cast<float2*>(at_ml), make_float2(mx, sum));
-            }
-            __syncwarp();
-          }
+#pragma unroll
+          for (int tt = 0; tt < 4; ++tt)  // (the columns of a row are in the lanes of one t)
+            if (rows_bad & (0x11111111u << tt)) redo |= 1u << (8 * n + 2 * tt + e);
         }
+      if (redo) again(my_head, redo);
       if (whole) continue;
       __threadfence();
       __syncwarp();
@@ -564,6 +602,7 @@ __global__ void __launch_bounds__(kFewThreads, per_sm(NT, TAIL, HEADS)) few_kern
         i = (sg.row0 + r) / p.group;
         head = (sg.kvh + hw) * p.group + (sg.row0 + r - i * p.group);
       };
+      int any_bad = 0;
       for (int x = int(threadIdx.x); x < HEADS * rows * chunks; x += kFewThreads) {
         const int row = x / chunks, c = 8 * (x - row * chunks);
         int hw, r, i, head;
@@ -585,7 +624,7 @@ __global__ void __launch_bounds__(kFewThreads, per_sm(NT, TAIL, HEADS)) few_kern
           y[e] = none ? 0.0f : y[e] * inv;
           bad = fmaf(y[e], 0.0f, bad);
         }
-        if (bad != 0.0f) row_bad[row] = 1;
+        if (bad != 0.0f) row_bad[row] = any_bad = 1;
         if (whole) {
           store8(p, size_t(sg.doc.q0 + i) * size_t(p.os) + size_t(head) * size_t(p.D) + size_t(c), y);
         } else {
@@ -593,24 +632,15 @@ __global__ void __launch_bounds__(kFewThreads, per_sm(NT, TAIL, HEADS)) few_kern
           if (c == 0) __stcg(reinterpret_cast<float2*>(mine_ml) + row, make_float2(mx, sum));
         }
       }
-      __syncthreads();
-      if (int(threadIdx.x) < HEADS * rows && row_bad[threadIdx.x]) {
-        const int row = int(threadIdx.x);
-        int hw, r, i, head;
-        row_of(row, hw, r, i, head);
-        const int pos = i + lk - sg.doc.lq;
-        float acc[128], mx, sum;
-        row_again(p, p.q + static_cast<long long>(sg.doc.q0 + i) * p.qs + head * p.D,
-                  p.k + sg.doc.k0 * p.ks + (sg.kvh + hw) * p.D, p.v + sg.doc.k0 * p.vs + (sg.kvh + hw) * p.D, sg.s0 * kStep,
-                  min(last, limit_of(p.causal, pos, lk, sg.doc.prefix)), pos, p.slopes ? __ldg(p.slopes + head) : 0.0f, acc,
-                  mx, sum);
-        for (int c = 0; c < p.D; c += 8) {
-          float y[8];
-          for (int e = 0; e < 8; ++e) y[e] = whole ? acc[c + e] / sum : acc[c + e];
-          if (whole) store8(p, size_t(sg.doc.q0 + i) * size_t(p.os) + size_t(head) * size_t(p.D) + size_t(c), y);
-          else put_part(mine + row * p.D + c, y);
+      if (__syncthreads_or(any_bad)) {
+        for (int x = warp; x < HEADS * ((rows + 3) / 4); x += 4) {  // four rows of a head a warp
+          const int hw = x % HEADS, r0 = x / HEADS * 4;
+          unsigned redo = 0;
+          for (int r = r0; r < min(r0 + 4, rows); ++r)
+            if (row_bad[hw * rows + r]) redo |= 1u << r;
+          if (redo) again(hw, redo);
         }
-        if (!whole) __stcg(reinterpret_cast<float2*>(mine_ml) + row, make_float2(mx, sum));
+        __syncthreads();  // row_bad is free again
       }
       if (whole) continue;
 
