@@ -7,7 +7,9 @@
 // the rotated part keep their values (they are the two halves of a run of 2 V values).
 // The norm comes first: RMS x / sqrt(mean x^2 + eps) gamma, or LayerNorm without a bias,
 // (x - mean) / sqrt(mean (x - mean)^2 + eps) gamma, statistics and arithmetic in F32, one
-// rounding to F16 at the end.
+// rounding to F16 at the end. Values behind the rotated part never meet their run's partners (cosine 1
+// and sine 0 would spoil them with a partner's infinity or NaN): without a norm they are not
+// touched at all, with one they are scaled alone.
 //
 // Angles: a position may be millions of radians away, where a F32 angle has lost its
 // fraction. The plan holds each frequency as a 64-bit fixed-point fraction of a turn per
@@ -158,7 +160,8 @@ __host__ __device__ constexpr size_t rope_smem(int head_dim, int parts) {
   return size_t(kRopeWarps) * kBufs * kBufBytes + size_t(kRopeWarps + parts) * (head_dim / 2) * sizeof(float2);
 }
 
-template <int V, int NORM>
+// PART: a norm, and pairs that are not rotated (a kernel of its own: looking for them costs the others 7%).
+template <int V, int NORM, bool PART>
 __global__ void __launch_bounds__(kRopeThreads, 2) rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kPer = Runs<V>::kPer, kRuns = Runs<V>::kRuns;
   extern __shared__ __align__(128) uint8_t rope_shared[];
@@ -191,9 +194,15 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_kernel(const __grid_cons
   // this lane's runs: run g = s lanes + l of the head
   int at_a[kRuns], at_b[kRuns], pair_of[kRuns];
   bool has[kRuns];
+  uint32_t behind = 0;  // pairs that are not rotated (without a norm they are neither loaded nor stored)
 #pragma unroll
   for (int s = 0; s < kRuns; ++s) {
-    has[s] = in && (s * p.lanes + l) * kPer < all;
+    has[s] = in && (s * p.lanes + l) * kPer < (NORM == kNormNone ? p.pairs : all);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int pair = (s * p.lanes + l) * kPer + i;
+      behind |= uint32_t(pair >= p.pairs && pair < all) << (s * kPer + i);
+    }
     pair_of[s] = min((s * p.lanes + l) * kPer, all - kPer);
     at_a[s] = first_of(pair_of[s]) + slot * p.head_dim;
     at_b[s] = V == 0 ? at_a[s] : second_of(pair_of[s]) + slot * p.head_dim;
@@ -336,16 +345,33 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_kernel(const __grid_cons
       for (int i = 0; i < 8; i += 2) {
         mul_x2(ya[i], ya[i + 1], a[i], a[i + 1], aa[i], aa[i + 1]);
         mul_x2(yb[i], yb[i + 1], b[i], b[i + 1], bb[i], bb[i + 1]);
-        fma_x2(ya[i], ya[i + 1], b[i], b[i + 1], ab[i], ab[i + 1], ya[i], ya[i + 1]);
-        fma_x2(yb[i], yb[i + 1], a[i], a[i + 1], ba[i], ba[i + 1], yb[i], yb[i + 1]);
+        if constexpr (!PART) {
+          fma_x2(ya[i], ya[i + 1], b[i], b[i + 1], ab[i], ab[i + 1], ya[i], ya[i + 1]);
+          fma_x2(yb[i], yb[i + 1], a[i], a[i + 1], ba[i], ba[i + 1], yb[i], yb[i + 1]);
+        } else {
+#pragma unroll
+          for (int k = i; k < i + 2; ++k)
+            if (!(behind >> k & 1)) {
+              ya[k] = fmaf(b[k], ab[k], ya[k]);
+              yb[k] = fmaf(a[k], ba[k], yb[k]);
+            }
+        }
         if constexpr (NORM != kNormNone) {
           mul_x2(ya[i], ya[i + 1], ya[i], ya[i + 1], rs, rs);
           mul_x2(yb[i], yb[i + 1], yb[i], yb[i + 1], rs, rs);
         }
       }
 #pragma unroll
-      for (int s = 0; s < kRuns; ++s)
-        if (live && has[s]) store_run<V>(xb, at_a[s], at_b[s], ya + s * kPer, yb + s * kPer);
+      for (int s = 0; s < kRuns; ++s) {
+        if (!live || !has[s]) continue;
+        if (NORM != kNormNone || V != 0 || !(behind >> (s * kPer) & 15)) {
+          store_run<V>(xb, at_a[s], at_b[s], ya + s * kPer, yb + s * kPer);
+        } else {
+          for (int i = 0; i < kPer; ++i)
+            if (!(behind >> (s * kPer + i) & 1))
+              *reinterpret_cast<__half2*>(xb + at_a[s] + 2 * i) = __floats2half2_rn(ya[s * kPer + i], yb[s * kPer + i]);
+        }
+      }
     }
     fence_proxy_async_smem();  // the lanes' writes, before the copy out reads them
     __syncwarp();
@@ -363,7 +389,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_kernel(const __grid_cons
   if (lane == 0) bulk_wait_all();
 }
 
-template <int V, int NORM>
+template <int V, int NORM, bool PART>
 cudaError_t rope_launch_as(const RopeParams& p, cudaStream_t s) {
   const size_t smem = rope_smem(p.head_dim, NORM == kNormNone ? 1 : 2);
   static unsigned long long attr_set = 0;  // the attribute is per device
@@ -372,20 +398,22 @@ cudaError_t rope_launch_as(const RopeParams& p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const unsigned long long bit = (dev >= 0 && dev < kMaxAttrDevices) ? 1ull << dev : 0ull;
   if (!(attr_set & bit) || !bit) {
-    e = cudaFuncSetAttribute(rope_kernel<V, NORM>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(rope_smem(256, 2)));
+    e = cudaFuncSetAttribute(rope_kernel<V, NORM, PART>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(rope_smem(256, 2)));
     if (e != cudaSuccess) return e;
     attr_set |= bit;
   }
   const long long jobs = static_cast<long long>(p.rows) * p.chunks, most = 2ll * num_sms();
   const long long blocks = (jobs + kRopeWarps - 1) / kRopeWarps;
-  return launch_pdl(rope_kernel<V, NORM>, dim3(unsigned(blocks < most ? blocks : most)), dim3(kRopeThreads), smem, s, p);
+  return launch_pdl(rope_kernel<V, NORM, PART>, dim3(unsigned(blocks < most ? blocks : most)), dim3(kRopeThreads), smem, s, p);
 }
 
 template <int V>
 cudaError_t rope_launch_v(const RopeParams& p, int norm, cudaStream_t s) {
-  if (norm == kNormRms) return rope_launch_as<V, kNormRms>(p, s);
-  if (norm == kNormLayer) return rope_launch_as<V, kNormLayer>(p, s);
-  return rope_launch_as<V, kNormNone>(p, s);
+  const bool part = 2 * p.pairs < p.head_dim;
+  if (norm == kNormRms) return part ? rope_launch_as<V, kNormRms, true>(p, s) : rope_launch_as<V, kNormRms, false>(p, s);
+  if (norm == kNormLayer)
+    return part ? rope_launch_as<V, kNormLayer, true>(p, s) : rope_launch_as<V, kNormLayer, false>(p, s);
+  return rope_launch_as<V, kNormNone, false>(p, s);
 }
 
 sv_status rope_launch(RopeParams& p, const sv_rope_plan* plan, int norm, cudaStream_t s) {
