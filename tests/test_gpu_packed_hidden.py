@@ -98,7 +98,7 @@ def test_a_spoiled_key_at_the_end_of_a_long_range(sv, poison, workspace, lq, hq,
 
 def test_rows_computed_again_for_longer_than_a_wait_may_last(sv):
     """The waits of the other warps count the progress of rows that are computed again."""
-    n = 2000000
+    n = 600000
     rest = [32] * 400
     c = Case([32] + rest, [n] + rest, 1, 1, 128, seed=1)
     c.v[n - 1] = math.nan

@@ -11,7 +11,7 @@
 // rows holds 128 / group queries with the `group` query heads of one key head (row r =
 // query r / group, head r % group), so shared key heads are read once for all of them, and
 // a single query of many heads fills rows. Persistent CTAs (one per SM) walk work items of
-// two such tiles against the document's key tiles of 128; 320 threads:
+// two such tiles against the document's key tiles of 128; 352 threads:
 //   warp 0      works out the items from the documents' lengths on the device (the lengths
 //               never visit the host) and copies: Q of an item, key and value tiles in turn
 //               into a ring, all by TMA from the caller's strided rows (values past a head's
@@ -20,7 +20,8 @@
 //               O_w += P_w V (P from tensor memory);
 //   warps 2..5  softmax of tile 0, warps 6..9 of tile 1: a thread per row turns its S row into
 //               P (F16, over S in tensor memory), keeps the exponent and the sum in F32, and
-//               rescales O in tensor memory when the exponent rises by more than 2^15.
+//               rescales O in tensor memory when the exponent rises by more than 2^15;
+//   warp 10     clears the value rows of an item's last tile that none of its rows sees.
 // An item's rows go out behind the next item's first tile: O is loaded between that tile's
 // softmax and the arrival of its P, and scaled, rounded and stored while the products run.
 // Items are handed out by tickets, the longest documents of every 32 first. In launches of few
@@ -48,8 +49,8 @@ namespace {
 
 constexpr int kTile = 128;                  // rows of a query tile, keys of a key tile
 constexpr int kBoxBytes = kTile * 128;      // 128 rows of 64 values: one box of an operand tile
-constexpr int kThreads = 320;
-constexpr int kBarBytes = 768;              // barriers, TMEM address slot, abort flag, progress count, items
+constexpr int kThreads = 352;
+constexpr int kBarBytes = 768;              // barriers, TMEM address slot, abort flag, items
 constexpr int kOutBytes = 32 * 64;          // 32 rows of 32 output columns
 constexpr int kItems = 4;                   // work items between the copy warp and the others
 constexpr uint32_t kTmemCols = 512;
@@ -81,11 +82,12 @@ enum {
   kBarPFull = 22,   // +group: the group has written P_w (and any O rescale) to TMEM
   kBarDrain = 24,
   kBarItem = 25,       // +item slot: the copy warp has written the item
-  kBarItemDone = 29,   // +item slot: the issuer and the eight softmax warps are through with it
+  kBarItemDone = 29,   // +item slot: the issuer, the eight softmax warps and warp 10 are through with it
   kBarOFull = 33,      // +group: the item's last P V product of the group has finished
   kBarJoin = 35,       // one tile an item: the second group's exponents and sums are in shared memory
   kBarRead = 36,       // and its O has been read
-  kNumBars = 37
+  kBarRest = 37,       // +stage: value rows that warp 10 has to clear have arrived
+  kNumBars = 45
 };
 
 // One work item: up to 2 qt queries of a document with the query heads of one key head
@@ -99,8 +101,14 @@ struct Item {
   int slot, splits, split;  // partial result; splits 1: none
   int live;             // 0: no more items
 };
-constexpr int kOffItems = 8 * kNumBars + 16;  // in the barrier area
-static_assert(kOffItems + kItems * sizeof(Item) <= kBarBytes, "barrier area");
+constexpr int kOffItems = 8 * kNumBars + 8;  // in the barrier area
+constexpr int kOffProgress = kBarBytes - 8;
+static_assert(kOffItems + kItems * sizeof(Item) <= kOffProgress && kBarBytes <= 1024, "barrier area");
+// Steps of work whose length the inputs decide (rows that are computed again), counted for those who wait; at: any
+// place in the barrier area, which starts on 1024 bytes.
+__device__ __forceinline__ unsigned* progress(const volatile void* at) {
+  return reinterpret_cast<unsigned*>((reinterpret_cast<uintptr_t>(at) & ~uintptr_t(1023)) + kOffProgress);
+}
 
 // The items in order, worked out by the copy warp from the documents' lengths: a
 // chunk of 32 documents at a time, one per lane, with their item counts summed by shuffles.
@@ -112,8 +120,8 @@ static_assert(kOffItems + kItems * sizeof(Item) <= kBarBytes, "barrier area");
 class Schedule {
  public:
   // span: queries of an item; min_split: key tiles of a part at least.
-  __device__ __forceinline__ Schedule(const Params& p, int lane, int span, int min_split, unsigned* beat)
-      : p_(p), lane_(lane), docs_(p.docs), span_(span), beat_(beat) {
+  __device__ __forceinline__ Schedule(const Params& p, int lane, int span, int min_split)
+      : p_(p), lane_(lane), docs_(p.docs), span_(span) {
     chunk_ = 0x7fffffff;
     float work = 0.0f;
     bool bad = false;
@@ -210,7 +218,6 @@ class Schedule {
 
  private:
   __device__ __forceinline__ void load(int d0) {
-    if (lane_ == 0 && d0 % (1 << 20) == 0) atomicAdd(beat_, 1u);  // (2^20 documents are passed in a tenth of a second)
     bad_ = !document(p_, d0 + lane_, docs_, doc_);
     pairs_ = (doc_.lq + span_ - 1) / span_;
     tiles_ = (doc_.lk + kTile - 1) / kTile;  // of the last query
@@ -247,7 +254,6 @@ class Schedule {
   const Params& p_;
   int lane_, docs_, span_, chunk_;
   bool bad_;
-  unsigned* beat_;
   int items_ = 0;
   int d0_ = -32, base_ = 0, total_ = 0, slot_base_ = 0, slot_total_ = 0;
   Document doc_;  // this lane's
@@ -256,18 +262,17 @@ class Schedule {
 
 // A wait whose long form is one function for all of the kernel's waits: inlined, the waits alone
 // were a sixth of the code, and code that runs once an item then came from beyond the
-// instruction caches. It gives up (as mbar_wait does) after the limit without a step of the work whose
-// length the inputs decide, which counts its steps behind the abort flag: rows that are computed
-// again, and documents that are passed on the way to an item.
+// instruction caches. It gives up (as mbar_wait does) after the limit without progress.
 __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int* abort, int* err) {
   unsigned long long t0 = globaltimer();
-  int seen = abort[1];
+  const volatile unsigned* steps = progress(abort);
+  unsigned seen = *steps;
   for (uint32_t i = 1;; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
     if (i & 255u) continue;
     if (*abort) return false;
     if (globaltimer() - t0 <= kWaitLimitNs) continue;
-    const int now = abort[1];
+    const unsigned now = *steps;
     if (now == seen) {
       *abort = 1;
       atomicOr(err, kDevErrTimeout);
@@ -344,61 +349,43 @@ __device__ __noinline__ void join_parts(const Params& p, const Item& it, long lo
 // its item has no keys at all.
 enum { kNothing = 1, kPart = 2, kEmpty = 4 };
 
-// The rows of tile w whose O is not finite (`bad`; r: this lane's), again from the visible keys alone where a key that
+// The rows of tile w whose O is not finite (r: this lane's; out_to -1: no such row), again from the visible keys alone where a key that
 // the row does not see has spoiled it; of a part, their sums, exponents and denominators. By a whole warp.
-__device__ __noinline__ void rows_again(const Params& p, const Item& it, long long out_to, int how, int w, int r, bool bad,
-                                        unsigned* beat) {
+__device__ __noinline__ void rows_again(const Params& p, const Item& it, long long out_to, int how, int w, int r) {
   const int Dn = (p.D + 15) / 16 * 16, lane = r & 31;
   const __half* k = p.k + it.k0 * p.ks + it.kvh * p.D;
   const __half* v = p.v + it.k0 * p.vs + it.kvh * p.D;
   const int i = w * p.qt + r / p.group, head = it.kvh * p.group + r % p.group;
   const int kb = it.jb * kTile, ke = min(it.ke, it.je * kTile);  // the keys of the products
-  const int lim = out_to >= 0 && bad ? max(limit_of(p.causal, it.at + i, it.lk, it.prefix), kb) : ke;
+  const int lim = out_to >= 0 ? max(limit_of(p.causal, it.at + i, it.lk, it.prefix), kb) : ke;
   const int low = __reduce_min_sync(0xffffffffu, lim);
   const int last = low < ke ? last_spoiled(p, v, low, ke, lane) : -1;
   const float slope = p.slopes && lim < ke ? __ldg(p.slopes + head) : 0.0f;
   __syncwarp();  // (what the rows' own lanes have stored comes first)
 #pragma unroll 1
-  for (uint32_t todo = __ballot_sync(0xffffffffu, lim <= last); todo;) {
-    Row rows[4];
-    int src[4];
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      src[x] = todo ? __ffs(int(todo)) - 1 : -1;
-      todo &= todo - 1;
-      auto of = [&](auto y) { return __shfl_sync(0xffffffffu, y, max(src[x], 0)); };
-      const int q_row = of(i);
-      rows[x].q = p.q + static_cast<long long>(it.q0 + q_row) * p.qs + of(head) * p.D;
-      rows[x].ke = src[x] < 0 ? kb : of(lim);
-      rows[x].at = it.at + q_row;
-      rows[x].slope = of(slope);
-    }
-    float4 acc[4];
+  for (uint32_t todo = __ballot_sync(0xffffffffu, lim <= last); todo; todo &= todo - 1) {
+    const int src = __ffs(int(todo)) - 1;
+    auto of = [&](auto x) { return __shfl_sync(0xffffffffu, x, src); };
+    const int row_i = of(i), row_head = of(head);
     float m, l;
-    rows_again4(p, rows, k, v, kb, lane, beat, acc, m, l);
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const float row_m = __shfl_sync(0xffffffffu, m, 8 * x), row_l = __shfl_sync(0xffffffffu, l, 8 * x);
-      const long long to = __shfl_sync(0xffffffffu, out_to, max(src[x], 0));
-      const int row_how = __shfl_sync(0xffffffffu, how, max(src[x], 0));
-      if (src[x] < 0) continue;
-      if (row_how & kPart) {
-        float* pb = p.partial + (size_t(it.slot) * 2 + w) * size_t(Dn + 2) * kTile + (r - lane + src[x]);
-        if (lane == 0) {
-          __stcg(pb, row_m);
-          __stcg(pb + kTile, row_l);
-        }
-        if (lane < p.D / 4) {
-          pb += size_t(2 + 4 * lane) * kTile;
-          __stcg(pb, acc[x].x);
-          __stcg(pb + kTile, acc[x].y);
-          __stcg(pb + 2 * kTile, acc[x].z);
-          __stcg(pb + 3 * kTile, acc[x].w);
-        }
-      } else if (lane < p.D / 4) {
-        store4(p, size_t(to) + 4 * lane,
-               make_float4(acc[x].x / row_l, acc[x].y / row_l, acc[x].z / row_l, acc[x].w / row_l));
+    const float4 y = row_again(p, p.q + static_cast<long long>(it.q0 + row_i) * p.qs + row_head * p.D, k, v, kb, of(lim),
+                               it.at + row_i, of(slope), lane, progress(&it), m, l);
+    const long long to = of(out_to);
+    if (of(how) & kPart) {
+      float* pb = p.partial + (size_t(it.slot) * 2 + w) * size_t(Dn + 2) * kTile + (r - lane + src);
+      if (lane == 0) {
+        __stcg(pb, m);
+        __stcg(pb + kTile, l);
       }
+      if (lane < p.D / 4) {
+        pb += size_t(2 + 4 * lane) * kTile;
+        __stcg(pb, y.x);
+        __stcg(pb + kTile, y.y);
+        __stcg(pb + 2 * kTile, y.z);
+        __stcg(pb + 3 * kTile, y.w);
+      }
+    } else if (lane < p.D / 4) {
+      store4(p, size_t(to) + 4 * lane, make_float4(y.x / l, y.y / l, y.z / l, y.w / l));
     }
   }
 }
@@ -406,7 +393,7 @@ __device__ __noinline__ void rows_again(const Params& p, const Item& it, long lo
 // Row r of tile w where `how` is not 0 for its whole warp. Out of the way of the common case,
 // whose code must stay in the instruction caches.
 __device__ __noinline__ void write_special(const Params& p, const Item& it, uint32_t o_tm, float m, float l,
-                                           long long out_to, int how, int w, int r, unsigned* beat) {
+                                           long long out_to, int how, int w, int r) {
   const int Dn = (p.D + 15) / 16 * 16;
   const int i = w * p.qt + r / p.group;
   const int lim = out_to < 0 ? 0 : limit_of(p.causal, it.at + i, it.lk, it.prefix);
@@ -437,13 +424,13 @@ __device__ __noinline__ void write_special(const Params& p, const Item& it, uint
       store8(p, size_t(out_to) + c, y);
     }
   }
-  if (__any_sync(0xffffffffu, out_to >= 0 && bad != 0.0f)) rows_again(p, it, out_to, how, w, r, bad != 0.0f, beat);
+  if (__any_sync(0xffffffffu, out_to >= 0 && bad != 0.0f)) rows_again(p, it, bad != 0.0f ? out_to : -1, how, w, r);
   if (how & kPart) join_parts(p, it, out_to, w, r);
 }
 
 // Row r of an item of one tile whose key tiles the two groups have shared out: exponent, denominator and O of both.
 __device__ __noinline__ void write_shared(const Params& p, const Item& it, uint32_t o_tm, float m0, float l0, float m1,
-                                          float l1, long long out_to, int how, int r, unsigned* beat) {
+                                          float l1, long long out_to, int how, int r) {
   const int Dn = (p.D + 15) / 16 * 16;
   const float mx = fmaxf(m0, m1), ref = mx == -INFINITY ? 0.0f : mx;
   const float f0 = ex2(m0 - ref), f1 = ex2(m1 - ref), l = fmaf(f1, l1, f0 * l0);
@@ -475,7 +462,7 @@ __device__ __noinline__ void write_shared(const Params& p, const Item& it, uint3
       store8(p, size_t(out_to) + c, y);
     }
   }
-  if (__any_sync(0xffffffffu, out_to >= 0 && bad != 0.0f)) rows_again(p, it, out_to, how, 0, r, bad != 0.0f, beat);
+  if (__any_sync(0xffffffffu, out_to >= 0 && bad != 0.0f)) rows_again(p, it, bad != 0.0f ? out_to : -1, how, 0, r);
   if (how & kPart) join_parts(p, it, out_to, 0, r);
 }
 
@@ -490,9 +477,9 @@ __device__ __noinline__ void write_shared(const Params& p, const Item& it, uint3
 template <int NB, bool E4M3, typename F>
 __device__ __forceinline__ void write_rows(const Params& p, const Item& it, const CUtensorMap& to_map, uint8_t* stage,
                                            uint32_t o_tm, float m, float l, long long out_to, int how, int w, int r,
-                                           unsigned* beat, F loaded) {
+                                           F loaded) {
   if (__any_sync(0xffffffffu, how)) {
-    write_special(p, it, o_tm, m, l, out_to, how, w, r, beat);
+    write_special(p, it, o_tm, m, l, out_to, how, w, r);
     loaded();
     return;
   }
@@ -526,6 +513,7 @@ __device__ __forceinline__ void write_rows(const Params& p, const Item& it, cons
     }
   }
   const bool bad = out_to >= 0 && bad0 + bad1 != 0.0f;
+  bool again = false;
   constexpr int kRow = E4M3 ? 32 : 64;  // bytes of a staged row, swizzled for a TMA store
   if (p.out_tma && __all_sync(0xffffffffu, out_to >= 0 && !bad)) {
     const int turn = E4M3 ? (lane >> 2) & 1 : (lane >> 1) & 3;  // swizzle
@@ -549,6 +537,7 @@ __device__ __forceinline__ void write_rows(const Params& p, const Item& it, cons
       }
     }
   } else if constexpr (!E4M3) {
+    again = __any_sync(0xffffffffu, bad);
     if (out_to >= 0)
 #pragma unroll
       for (int g = 0; g < NB * 8; ++g)
@@ -556,6 +545,7 @@ __device__ __forceinline__ void write_rows(const Params& p, const Item& it, cons
           *reinterpret_cast<uint4*>(static_cast<__half*>(p.o) + out_to + 8 * g) = make_uint4(
               o[g >> 2][4 * (g & 3)], o[g >> 2][4 * (g & 3) + 1], o[g >> 2][4 * (g & 3) + 2], o[g >> 2][4 * (g & 3) + 3]);
   } else if constexpr (E4M3) {
+    again = __any_sync(0xffffffffu, bad);
     const int quarter = lane & 3;
     long long to[4];  // the four rows' places
 #pragma unroll
@@ -586,7 +576,32 @@ __device__ __forceinline__ void write_rows(const Params& p, const Item& it, cons
       }
     }
   }
-  if (__any_sync(0xffffffffu, bad)) rows_again(p, it, out_to, how, w, r, bad, beat);
+  if (again) rows_again(p, it, bad ? out_to : -1, how, w, r);
+}
+
+// Four capped scores share a reciprocal (capped4), where a hidden one must have no part: those behind a row's `valid`
+// visible scores, up to the next multiple of eight, become -inf in tensor memory. The columns are the warp's, so the
+// rows take turns. (In registers, by a select for each of the 128 scores as after the cap, this costs 9% of such calls.)
+__device__ __forceinline__ void cut_scores(uint32_t s_tm, int valid) {
+  const bool cut = valid > 0 && valid < kTile && (valid & 3);
+  uint32_t todo = __ballot_sync(0xffffffffu, cut);
+  if (!todo) return;
+#pragma unroll 1
+  do {
+    const int at = __shfl_sync(0xffffffffu, valid, __ffs(int(todo)) - 1) & ~7;
+    const bool mine = cut && (valid & ~7) == at;
+    uint32_t s[8];
+    tmem_ld8(s_tm + uint32_t(at), s);
+    tmem_ld_wait();
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      asm volatile("" : "+r"(s[e]));  // no use before the wait
+      if (mine && at + e >= valid) s[e] = 0xff800000u;
+    }
+    tmem_st8(s_tm + uint32_t(at), s);
+    tmem_st_wait();
+    todo &= ~__ballot_sync(0xffffffffu, mine);
+  } while (todo);
 }
 
 // SOLO: items of one tile, whose key tiles the two groups take in turn (for launches of few items: half the chain, and
@@ -606,7 +621,6 @@ __global__ void __maxnreg__(168)
   const uint32_t bar0 = sbase + L::kOffBar;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffBar + 8 * kNumBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  unsigned* beat = reinterpret_cast<unsigned*>(tmem_slot + 2);  // see wait_long
   auto bar = [&](int i) { return bar0 + 8u * uint32_t(i); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -618,6 +632,7 @@ __global__ void __maxnreg__(168)
     for (int s = 0; s < kStages; ++s) {
       mbar_init(bar(kBarFull + s), 1);
       mbar_init(bar(kBarEmpty + s), 1);
+      mbar_init(bar(kBarRest + s), 1);
     }
     for (int w = 0; w < 2; ++w) {
       mbar_init(bar(kBarSFull + w), 1);
@@ -626,13 +641,13 @@ __global__ void __maxnreg__(168)
     }
     for (int s = 0; s < kItems; ++s) {
       mbar_init(bar(kBarItem + s), 1);
-      mbar_init(bar(kBarItemDone + s), 9);
+      mbar_init(bar(kBarItemDone + s), 10);
     }
     mbar_init(bar(kBarJoin), 128);
     mbar_init(bar(kBarRead), 128);
     mbar_init(bar(kBarDrain), 1);
     *abort_flag = 0;
-    *beat = 0;
+    *progress(abort_flag) = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -651,7 +666,7 @@ __global__ void __maxnreg__(168)
   };
 
   if (warp == 0) {
-    Schedule sched(p, lane, (SOLO ? 1 : 2) * p.qt, (SOLO ? 2 : 1) * kMinSplit, beat);
+    Schedule sched(p, lane, (SOLO ? 1 : 2) * p.qt, (SOLO ? 2 : 1) * kMinSplit);
     if (lane == 0) {
       prefetch_tmap(&tq);
       prefetch_tmap(&tk);
@@ -659,6 +674,7 @@ __global__ void __maxnreg__(168)
     }
     // copies in flight per full barrier (bit b: Q buffer b, 4 + stage) and their phase bits
     uint32_t issued = 0, issued_phase = 0;
+    uint32_t rest = 0, rest_phase = 0;  // stages whose last copy went to warp 10 first; the phase of the next that does
     auto note = [&](int bit, uint32_t ph) {
       issued |= 1u << bit;
       issued_phase = (issued_phase & ~(1u << bit)) | (ph << bit);
@@ -695,23 +711,28 @@ __global__ void __maxnreg__(168)
         // the last copies, whose room has to be waited for anyway (32 images: 124.5 -> 121.5 us; where it holds
         // four key tiles, earlier than behind the last copy costs 2%).
         const int copies = SOLO ? 4 * ((it.je - it.jb + 1) / 2) : 2 * (it.je - it.jb), draw_at = NB == 1 ? copies : copies - 2;
-        auto kv = [&](const CUtensorMap& map, int j) -> bool {
+        const int clean = min(it.ke, it.je * kTile) / kTile;  // tiles with values of the item's keys alone
+        auto kv = [&](bool values, int j) -> bool {
           const int st = t % kStages;
           const uint32_t ph = (t / kStages) & 1;
           if (!wait_bar(bar(kBarEmpty + st), ph ^ 1, abort_flag, p.err)) return false;
-          mbar_arrive_expect_tx(bar(kBarFull + st), kOp);
+          const bool clear = values && j >= clean;
+          const uint32_t full = bar((clear ? kBarRest : kBarFull) + st);
+          mbar_arrive_expect_tx(full, kOp);
           for (int b = 0; b < NB; ++b)
-            tma_load_3d(sbase + L::kOffKV + st * kOp + b * kBoxBytes, &map, bar(kBarFull + st), 64 * b, it.kvh,
+            tma_load_3d(sbase + L::kOffKV + st * kOp + b * kBoxBytes, values ? &tv : &tk, full, 64 * b, it.kvh,
                         it.k0 + j * kTile);
           note(4 + st, ph);
+          if (clear) rest |= 1u << st, rest_phase ^= 1u << st;
+          else rest &= ~(1u << st);
           ++t;
           return true;
         };
 #pragma unroll 1
         for (int x = 0; ok && x < copies; ++x) {  // a key tile, its values, the next key tile, ...
           if (x == draw_at) ticket = sched.draw();
-          if constexpr (SOLO) ok = kv(x & 2 ? tv : tk, it.jb + 2 * (x >> 2) + (x & 1));  // two keys, their values, ...
-          else ok = kv(x & 1 ? tv : tk, it.jb + (x >> 1));
+          if constexpr (SOLO) ok = kv(x & 2, it.jb + 2 * (x >> 2) + (x & 1));  // two keys, their values, ...
+          else ok = kv(x & 1, it.jb + (x >> 1));
           if (ok && x == 0) {
             const int qb = n % kQBufs;
             const uint32_t ph = (n / kQBufs) & 1;
@@ -733,8 +754,11 @@ __global__ void __maxnreg__(168)
     }
     if (lane == 0)  // every copy this thread issued lands before the CTA can exit
       for (int i = 0; i < 4 + kStages; ++i)
-        if (issued & (1u << i))
-          mbar_wait_bounded(bar(i < 4 ? kBarQFull + i : kBarFull + i - 4), (issued_phase >> i) & 1, p.err);
+        if (issued & (1u << i)) {
+          const int st = i - 4;
+          if (i >= 4 && (rest >> st & 1)) mbar_wait_bounded(bar(kBarRest + st), ~(rest_phase >> st) & 1, p.err);
+          else mbar_wait_bounded(bar(i < 4 ? kBarQFull + i : kBarFull + st), (issued_phase >> i) & 1, p.err);
+        }
   } else if (warp == 1) {
     // The MMA issuer: S_0(0), S_1(0), then per key tile t of all items: O_0 += P_0(t) V_t,
     // S_0(t+1), O_1 += P_1(t) V_t, S_1(t+1). MMAs run in issue order, so S_w(t+1)
@@ -775,27 +799,14 @@ __global__ void __maxnreg__(168)
       }
       commit(kBarSFull + w);
     };
-    // `keys` of the tile are an item's (kTile and more: all): the steps behind them are left out.
-    auto issue_pv = [&](int w, uint32_t st, uint32_t keep, int keys) {
+    auto issue_pv = [&](int w, uint32_t st, uint32_t keep) {
       const uint64_t vd = make_sdesc(sbase + L::kOffKV + st * kOp, kBoxBytes, 1024, 2);
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk)  // 16 keys a step: 8 TMEM columns of P, 16 rows of V
-        mma_f16_ts_if(kk == 0 || 16 * kk < keys ? lead : 0u, tmem + uint32_t(256 + 128 * w),
-                      tmem + uint32_t(128 * w + 8 * kk), vd + uint64_t(kk * (2048 >> 4)), idesc_o, kk > 0 ? 1u : keep);
-    };
-    // Value rows of a tile's last step that no row of the item sees (the next document's, say) become zeros: their
-    // probabilities are 0, but 0 times an infinity or NaN would spoil every row. The values must have arrived.
-    auto clear_rest = [&](uint32_t st, int keys) {
-      const int rows = keys > 0 ? -keys & 15 : 16;
-      if (keys >= kTile || !rows) return;
-      uint8_t* to = smem + L::kOffKV + st * kOp + max(keys, 0) * 128;
-      for (int b = 0; b < NB; ++b)
-        for (int x = lane; x < rows * 8; x += 32) *reinterpret_cast<uint4*>(to + b * kBoxBytes + 16 * x) = make_uint4(0, 0, 0, 0);
-      fence_proxy_async_smem();
-      __syncwarp();
+        mma_f16_ts_if(lead, tmem + uint32_t(256 + 128 * w), tmem + uint32_t(128 * w + 8 * kk), vd + uint64_t(kk * (2048 >> 4)),
+                      idesc_o, kk > 0 ? 1u : keep);
     };
     int read = 0;  // items so far
-    int rest = 0;  // keys of the last tile of the item that next() has returned
     // key tiles of the next item that has any (0: there is none); -1 after a time-out, or
     // where it is not there yet and `block` is false
     auto next = [&](bool block) -> int {
@@ -803,13 +814,12 @@ __global__ void __maxnreg__(168)
         const int b = kBarItem + read % kItems, ph = (read / kItems) & 1;
         if (block ? !wait(b, uint32_t(ph)) : !all(mbar_test(bar(b), uint32_t(ph)))) return -1;
         const Item& r = items[read % kItems];
-        const int live = r.live, tiles = r.je - r.jb, end = r.ke - (r.je - 1) * kTile;
+        const int live = r.live, tiles = r.je - r.jb;
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBarItemDone + read % kItems));
         __syncwarp();
         if (!all(live)) return 0;
         ++read;
-        rest = end;
         if (all(tiles > 0)) return tiles;
       }
     };
@@ -839,10 +849,7 @@ __global__ void __maxnreg__(168)
           for (uint32_t w = 0; w < 2 && ok; ++w) {
             if (!(ok = full(2 + w) && wait(kBarPFull + int(w), tt))) break;
             tc_fence_after();
-            // (an odd number of tiles: the second group's last one lies behind the item's keys)
-            const int keys = 2 * s + int(w) < tiles - 1 ? kTile : 2 * s + int(w) < tiles ? rest : 0;
-            clear_rest(stage(2 + w), keys);
-            issue_pv(int(w), stage(2 + w), s > 0, keys);
+            issue_pv(int(w), stage(2 + w), s > 0);
             commit(kBarEmpty + int(stage(2 + w)));
             if (all(s + 1 == steps)) {
               commit(kBarOFull + int(w));
@@ -869,7 +876,6 @@ __global__ void __maxnreg__(168)
     int qb = 0, qph = 0;  // Q buffer and phase of the current item
     while (ok && all(tiles > 0)) {
       int more = 0;  // key tiles of the next item
-      const int end = rest;
       const int qb_next = qb + 1 == kQBufs ? 0 : qb + 1, qph_next = qb + 1 == kQBufs ? qph ^ 1 : qph;
       for (int j = 0; ok && all(j < tiles); ++j, tt ^= 1) {
         // ring: key tile at 0, its values at 1, the next key tile at 2
@@ -879,13 +885,12 @@ __global__ void __maxnreg__(168)
         place(2, st_k, ph);
         // (the copies are waited for before P, which is what the products really wait for)
         ok = wait_full(1) && (last || wait_full(2));
-        if (last && ok) clear_rest(st_v, end);
         bool late = false;  // the next item was not there for S_0
 #pragma unroll 1
         for (int w = 0; w < 2 && ok; ++w) {
           if (!(ok = wait(kBarPFull + w, tt))) break;
           tc_fence_after();
-          issue_pv(w, st_v, j > 0, last ? end : kTile);
+          issue_pv(w, st_v, j > 0);
           int first = w;  // S products to issue: tiles first .. w
           if (last) {
             commit(kBarOFull + w);
@@ -925,6 +930,41 @@ __global__ void __maxnreg__(168)
     commit(kBarDrain);
     __syncwarp();
     mbar_wait_bounded(bar(kBarDrain), 0, p.err);
+  } else if (warp == 10) {
+    // Value rows of an item's last tile that none of its rows sees (the next document's, say) become zeros: their
+    // probabilities are 0, but 0 times an infinity or NaN would spoil every row. The values of such a tile arrive
+    // here, and go to the issuer from here. (A warp of its own: 1 to 2% of a call, in the issuer's or the softmax
+    // warps' loops 2 to 5%.)
+    uint32_t phase = 0;
+    int pairs = 0;  // pairs of key and value tiles so far
+    // (Its waits are long: it sleeps.)
+    auto wait = [&](int b, uint32_t parity) {
+      return __all_sync(0xffffffffu, mbar_try_wait<1000000>(bar(b), parity) || wait_bar(bar(b), parity, abort_flag, p.err));
+    };
+    for (int n = 0; wait(kBarItem + n % kItems, (n / kItems) & 1); ++n) {
+      const Item& it = items[n % kItems];
+      const int live = it.live, jb = it.jb, tiles = it.je - it.jb, end = min(it.ke, it.je * kTile);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarItemDone + n % kItems));
+      if (!live) break;
+      if (tiles <= 0) continue;
+      bool ok = true;
+      const int padded = SOLO ? (tiles + 1) / 2 * 2 : tiles;
+      for (int j = max(end / kTile - jb, 0); ok && j < padded; ++j) {
+        const int copy = 2 * pairs + (SOLO ? 4 * (j / 2) + 2 + j % 2 : 2 * j + 1), st = copy % kStages;
+        if (!(ok = wait(kBarRest + st, (phase >> st) & 1))) break;
+        phase ^= 1u << st;
+        uint8_t* values = smem + L::kOffKV + st * kOp;
+        for (int x = max(end - (jb + j) * kTile, 0) * 8 + lane; x < kTile * 8; x += 32)
+          for (int b = 0; b < NB; ++b)
+            *reinterpret_cast<uint4*>(values + b * kBoxBytes + 16 * x) = make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarFull + st));
+      }
+      if (!ok) break;
+      pairs += padded;
+    }
   } else {
     const int w = (warp - 2) >> 2;  // softmax group
     const int sub = warp & 3;       // TMEM lane quarter
@@ -985,7 +1025,7 @@ __global__ void __maxnreg__(168)
         if (pending_keys && !__all_sync(0xffffffffu, wait_bar(bar(kBarOFull + w), (full - 1) & 1, abort_flag, p.err)))
           break;
         tc_fence_after();
-        write_rows<NB, E4M3>(p, items[pending % kItems], to, stage, o_tm, m, l, out_to, out_how, w, r, beat, [] {});
+        write_rows<NB, E4M3>(p, items[pending % kItems], to, stage, o_tm, m, l, out_to, out_how, w, r, [] {});
         done(pending);
         pending = -1;
       }
@@ -1012,6 +1052,9 @@ __global__ void __maxnreg__(168)
           break;
         }
         tc_fence_after();
+        // visible keys of this tile (shared out, the second group's last may lie behind the item's)
+        const int valid = (SOLO ? min(lim, je * kTile) : lim) - j * kTile;
+        if constexpr (CAP) cut_scores(s_tm, valid);
         float sv[4][32];
         uint32_t(&su)[4][32] = reinterpret_cast<uint32_t(&)[4][32]>(sv);
         tmem_ld32(s_tm, su[0]);
@@ -1033,8 +1076,6 @@ __global__ void __maxnreg__(168)
         // (A row without a query has nothing to say.)
         const bool none_behind = BIAS && __all_sync(0xffffffffu, i < 0 || at >= min(lim, j * kTile + kTile) - 1);
         const bool line = BIAS && (none_behind || __all_sync(0xffffffffu, i < 0 || at <= j * kTile));
-        // visible keys of this tile (shared out, the second group's last may lie behind the item's)
-        const int valid = (SOLO ? min(lim, je * kTile) : lim) - j * kTile;
         float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
 #pragma unroll
         for (int h = 0; h < kSteps; ++h) {
@@ -1043,23 +1084,11 @@ __global__ void __maxnreg__(168)
             tmem_ld_wait(su[2]);
             reg_fence(su[3]);
           }
-          auto hide = [&]() {
-            if (valid < 32 * kC * (h + 1)) {
-#pragma unroll
-              for (int c = kC * h; c < kC * h + kC; ++c)
-                if (valid < 32 * c + 32)
-#pragma unroll
-                  for (int e = 0; e < 32; ++e)
-                    if (32 * c + e >= valid) sv[c][e] = -INFINITY;
-            }
-          };
-          if constexpr (CAP) {
-            hide();  // (a hidden score has no part in its neighbours' reciprocal)
+          if constexpr (CAP)
 #pragma unroll
             for (int c = kC * h; c < kC * h + kC; ++c)
 #pragma unroll
               for (int e = 0; e < 32; e += 4) capped4(&sv[c][e], sl2, cap2);
-          }
           if constexpr (BIAS) {
             const float on = CAP ? 1.0f : sl2;
             if (line) {
@@ -1078,7 +1107,14 @@ __global__ void __maxnreg__(168)
                   sv[c][e] = fmaf(-slope2, fabsf(d0 - float(32 * c + e)), CAP ? sv[c][e] : sv[c][e] * sl2);
             }
           }
-          hide();
+          if (valid < 32 * kC * (h + 1)) {
+#pragma unroll
+            for (int c = kC * h; c < kC * h + kC; ++c)
+              if (valid < 32 * c + 32)
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (32 * c + e >= valid) sv[c][e] = -INFINITY;
+          }
           float mq[2 * kC];
 #pragma unroll
           for (int k = 0; k < 2 * kC; ++k) {
@@ -1160,8 +1196,7 @@ __global__ void __maxnreg__(168)
           // of this item, which overwrites O, waits for the arrival. Between the two O is only
           // loaded; its rows are written while the products run. (Written before the item's
           // first tile they took 4,000 to 6,000 cycles that nothing else ran in.)
-          write_rows<NB, E4M3>(p, items[pending % kItems], to, stage, o_tm, m_before, l_before, to_before, how_before, w, r,
-                               beat, arrive);
+          write_rows<NB, E4M3>(p, items[pending % kItems], to, stage, o_tm, m_before, l_before, to_before, how_before, w, r, arrive);
           done(pending);
           pending = -1;
         } else {
@@ -1183,13 +1218,13 @@ __global__ void __maxnreg__(168)
             if (!wait(kBarRead)) break;  // (the next item's P V writes O again)
           } else {
             if (!wait(kBarOFull) || !wait(kBarOFull + 1) || !wait(kBarJoin)) break;
-            write_shared(p, it, o_tm, m, l, ml->x, ml->y, out_to, out_how, r, beat);
+            write_shared(p, it, o_tm, m, l, ml->x, ml->y, out_to, out_how, r);
             tc_fence_before();
             mbar_arrive(bar(kBarRead));
           }
           ++full;
         } else if (w == 0) {
-          write_special(p, it, o_tm, m, l, out_to, out_how, 0, r, beat);
+          write_special(p, it, o_tm, m, l, out_to, out_how, 0, r);
         }
         done(n);
         continue;

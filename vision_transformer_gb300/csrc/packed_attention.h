@@ -168,21 +168,15 @@ static __device__ __noinline__ int last_spoiled(const Params& p, const __half* v
   return __reduce_max_sync(0xffffffffu, last);
 }
 
-// A row to be computed again: its query, where its visible keys end, its position, its slope.
-struct Row {
-  const __half* q;
-  int ke, at;
-  float slope;
-};
-
-// Up to four rows of a key head from their visible keys alone, kb .. ke - 1 of the document (no keys: not a row), by a
-// whole warp: eight keys at a time, of which a lane holds the columns 4 lane .. 4 lane + 3 and then the score of row
-// lane / 8 and key lane % 8. Unscaled sums of the rows (the lane's columns) in acc, exponent and denominator of row
-// lane / 8 in m and l. 64 keys turn `beat` on (null: nobody waits for this). 31 rows over 20,000 keys of 128
-// dimensions, the warp alone on its SM: 30 ms (a row at a time 81, a thread a row 370).
-static __device__ __noinline__ void rows_again4(const Params& p, const Row (&rows)[4], const __half* k, const __half* v,
-                                                int kb, int lane, unsigned* beat, float4 (&acc)[4], float& m_out,
-                                                float& l_out) {
+// A row from its visible keys alone, by a whole warp: keys kb .. ke - 1 of the document, query position `at`. Four keys
+// at a time, of which a lane holds the columns 4 lane .. 4 lane + 3 and then the score of key lane % 4. Unscaled sums,
+// their exponent and denominator. 64 keys turn `beat` on (null: nobody waits for this). 31 rows over 20,000 keys of 128
+// dimensions, the warp alone on its SM: 110 ms; a thread a row 370. (Four rows and eight keys at a time 30, but so many
+// registers here make the callers' loops spill.)
+static __device__ __noinline__ float4 row_again(const Params& p, const __half* q, const __half* k, const __half* v,
+                                                int kb, int ke, int at, float slope, int lane, unsigned* beat,
+                                                float& m_out, float& l_out) {
+  constexpr int kKeys = 4;
   const bool mine = lane < p.D / 4;
   auto four = [&](const __half* row) {
     uint2 w = make_uint2(0u, 0u);
@@ -194,85 +188,66 @@ static __device__ __noinline__ void rows_again4(const Params& p, const Row (&row
     const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
     return make_float4(a.x, a.y, b.x, b.y);
   };
-  float4 q[4], y[4];
-  int end = kb, ke = kb, at = 0;
-  float slope = 0.0f;
-#pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const bool real = rows[r].ke > kb;
-    q[r] = wide(real ? four(rows[r].q) : make_uint2(0u, 0u));
-    y[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    end = max(end, rows[r].ke);
-    if (lane / 8 == r && real) ke = rows[r].ke, at = rows[r].at, slope = rows[r].slope;
-  }
+  const float4 qf = wide(four(q));
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   float m = -INFINITY, l = 0.0f;
 #pragma unroll 1
-  for (int j0 = kb; j0 < end; j0 += 8) {
-    uint2 kx[8], vx[8];
+  for (int j0 = kb; j0 < ke; j0 += kKeys) {
+    uint2 kx[kKeys], vx[kKeys];
 #pragma unroll
-    for (int b = 0; b < 8; ++b) {
+    for (int b = 0; b < kKeys; ++b) {
       kx[b] = vx[b] = make_uint2(0u, 0u);
-      if (j0 + b < end) {
+      if (j0 + b < ke) {
         kx[b] = four(k + (j0 + b) * p.ks);
         vx[b] = four(v + (j0 + b) * p.vs);
       }
     }
-    float s[32];
+    float s[kKeys];
 #pragma unroll
-    for (int b = 0; b < 8; ++b) {
+    for (int b = 0; b < kKeys; ++b) {
       const float4 kf = wide(kx[b]);
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        s[8 * r + b] = fmaf(q[r].x, kf.x, fmaf(q[r].y, kf.y, fmaf(q[r].z, kf.z, q[r].w * kf.w)));
+      s[b] = fmaf(qf.x, kf.x, fmaf(qf.y, kf.y, fmaf(qf.z, kf.z, qf.w * kf.w)));
     }
-    // summed over the lanes, each keeping one of the 32
+    // summed over the lanes, key j0 + lane % 4 left in each
 #pragma unroll
-    for (int x = 1; x < 32; x <<= 1)
+    for (int x = 1; x < kKeys; x <<= 1)
 #pragma unroll
-      for (int b = 0; b < 16 / x; ++b) {
+      for (int b = 0; b < kKeys / (2 * x); ++b) {
         const bool odd = lane & x;
         const float give = odd ? s[2 * b] : s[2 * b + 1];
         s[b] = (odd ? s[2 * b + 1] : s[2 * b]) + __shfl_xor_sync(0xffffffffu, give, x);
       }
-    const int key = j0 + (lane & 7);
+#pragma unroll
+    for (int x = kKeys; x < 32; x <<= 1) s[0] += __shfl_xor_sync(0xffffffffu, s[0], x);
+    const int key = j0 + lane % kKeys;
     float x = s[0] * p.scale;
     if (p.cap > 0.0f) x = p.cap * tanhf(x / p.cap);
     x = key < ke ? (x - slope * fabsf(float(at - key))) * kLog2e : -INFINITY;
     float up = x;
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, o));
+    for (int o = 1; o < kKeys; o <<= 1) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, o));
     up = fmaxf(up, m);
     const float ref = up == -INFINITY ? 0.0f : up, back = exp2f(m - ref), e = exp2f(x - ref);
     m = up;
     float sum = e;
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    for (int o = 1; o < kKeys; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     l = fmaf(l, back, sum);
+    acc = make_float4(acc.x * back, acc.y * back, acc.z * back, acc.w * back);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const float f = __shfl_sync(0xffffffffu, back, 8 * r);
-      y[r] = make_float4(y[r].x * f, y[r].y * f, y[r].z * f, y[r].w * f);
-    }
-#pragma unroll
-    for (int b = 0; b < 8; ++b) {
+    for (int b = 0; b < kKeys; ++b) {
+      const float eb = __shfl_sync(0xffffffffu, e, b);
       const float4 vf = wide(vx[b]);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float eb = __shfl_sync(0xffffffffu, e, 8 * r + b);
-        if (j0 + b < rows[r].ke) {  // (a key that only a later row of the four sees stays out)
-          y[r].x = fmaf(eb, vf.x, y[r].x);
-          y[r].y = fmaf(eb, vf.y, y[r].y);
-          y[r].z = fmaf(eb, vf.z, y[r].z);
-          y[r].w = fmaf(eb, vf.w, y[r].w);
-        }
-      }
+      acc.x = fmaf(eb, vf.x, acc.x);
+      acc.y = fmaf(eb, vf.y, acc.y);
+      acc.z = fmaf(eb, vf.z, acc.z);
+      acc.w = fmaf(eb, vf.w, acc.w);
     }
     if (beat && lane == 0 && (j0 - kb) % 64 == 0) atomicAdd(beat, 1u);
   }
-#pragma unroll
-  for (int r = 0; r < 4; ++r) acc[r] = y[r];
   m_out = m;
   l_out = l;
+  return acc;
 }
 
 }  // namespace packed

@@ -14,10 +14,10 @@
 //     accumulator's layout to the operand's by a transposing 8 x 8 move.
 // A warp takes 16 keys at a time (its registers of K are reloaded as soon as S^T is done, those
 // of V as soon as O^T is). The four warps of a CTA take four neighbouring key heads where their
-// number allows (or two heads and alternate keys, or one head): the rows of a key lie side by
-// side, a row of a narrow head is no whole number of DRAM's 64 bytes, and so the parts of a sector
+// number allows and a row is no whole number of 64 bytes (or two heads and alternate keys, or one
+// head): the rows of a key lie side by side, DRAM's sectors hold parts of two of them, and so these
 // are asked for at the same time (64 probes, 16 heads of 72: 252 MB read for 163 MB of keys and
-// values with a head per CTA). Two to four CTAs run per SM, by their registers: these hold what is in
+// values with a head per CTA). Two or three CTAs run per SM, by their registers: these hold what is in
 // flight.
 //
 // Work: the (document, group of key heads, block of rows) items are laid out one behind another
@@ -36,11 +36,11 @@ namespace {
 
 constexpr int kFewThreads = 128;
 constexpr int kMinShare = 64;       // keys of a CTA's share at least
-constexpr int kMostPerSm = 4;
+constexpr int kMostPerSm = 3;
 constexpr int kMaxFewGrid = kMaxSms * kMostPerSm;
-// CTAs an SM, by what the registers of a warp allow. (Four of heads of 72 side by side spill outside their loop
-// only; four of one such head, or of one of 64, inside it: 16 ranges of 8192 keys, 7 heads of 72, 115 against 47 us.)
-constexpr int per_sm(int nt, bool tail, int heads) { return nt > 1 ? 2 : (tail && heads == 4 ? 4 : 3); }
+// CTAs an SM, by what the registers of a warp allow: four of 8 rows spill inside their loop (64 probes, 16 heads of 72:
+// 65 against 40 us; 16 ranges of 8192 keys, 7 heads of 72: 115 against 47).
+constexpr int per_sm(int nt) { return nt > 1 ? 2 : 3; }
 
 __device__ __forceinline__ uint4 load16(const __half* p) {
   uint4 r;
@@ -233,13 +233,49 @@ __device__ __forceinline__ void put_part(float* to, const float* y) {
   __stcg(reinterpret_cast<float4*>(to) + 1, make_float4(y[4], y[5], y[6], y[7]));
 }
 
+// What rows of a segment need to be computed again: of its document the first query, the first key, queries, keys and
+// prefix; its key head, its first row, its keys; rows of a head, and their place in a part (null: they are results).
+struct Again {
+  int q0, k0, lq, lk, prefix, kvh, row0, begin, end, rows;
+  float *part, *part_ml;
+};
+// Those of the rows `todo` (a bit a row) of head hw that a hidden key's value has spoiled, again from their visible
+// keys alone, by one warp. (Not inlined: it took the registers of the loop.)
+__device__ __noinline__ void few_again(const Params& p, const Again sg, int hw, unsigned todo) {
+  const int lane = int(threadIdx.x) & 31;
+  const __half* k = p.k + sg.k0 * p.ks + (sg.kvh + hw) * p.D;
+  const __half* v = p.v + sg.k0 * p.vs + (sg.kvh + hw) * p.D;
+  auto limit = [&](int r) {
+    return max(sg.begin, limit_of(p.causal, (sg.row0 + r) / p.group + sg.lk - sg.lq, sg.lk, sg.prefix));
+  };
+  const int low = limit(__ffs(int(todo)) - 1);  // (later rows see no fewer keys)
+  const int last = low < sg.end ? last_spoiled(p, v, low, sg.end, lane) : -1;
+  __syncwarp();  // (what other lanes have stored of the rows comes first)
+#pragma unroll 1
+  for (; todo; todo &= todo - 1) {
+    const int r = __ffs(int(todo)) - 1, row = hw * sg.rows + r, lim = limit(r);
+    if (lim > last) break;  // (its result, and the later ones', are the products')
+    const int i = (sg.row0 + r) / p.group, head = (sg.kvh + hw) * p.group + (sg.row0 + r - i * p.group);
+    float m, l;
+    const float4 y = row_again(p, p.q + static_cast<long long>(sg.q0 + i) * p.qs + head * p.D, k, v, sg.begin,
+                               min(sg.end, lim), i + sg.lk - sg.lq, p.slopes ? __ldg(p.slopes + head) : 0.0f, lane,
+                               nullptr, m, l);
+    if (sg.part) {
+      if (lane < p.D / 4) __stcg(reinterpret_cast<float4*>(sg.part + row * p.D) + lane, y);
+      if (lane == 0) __stcg(reinterpret_cast<float2*>(sg.part_ml) + row, make_float2(m, l));
+    } else if (lane < p.D / 4) {
+      store4(p, size_t(sg.q0 + i) * size_t(p.os) + size_t(head) * size_t(p.D) + size_t(4 * lane),
+             make_float4(y.x / l, y.y / l, y.z / l, y.w / l));
+    }
+  }
+}
+
 // KI: 32-dimension groups of a key row, VI: 64-dimension groups of a value row, NT: 8-row
 // tiles of an item, HEADS: key heads of an item (4 / HEADS warps share a head's keys). TAIL: eight
 // more dimensions behind the groups (72), in instructions of their own: another group of each
-// would hold registers for 96 and 128 dimensions (64 probes, 16 heads of 72: 47.3 us with three CTAs
-// an SM; 42.4 so, and 41.2 with the four that then fit).
+// would hold registers for 96 and 128 dimensions (64 probes, 16 heads of 72: 47.3 us, 39.8 so).
 template <int KI, int VI, int NT, int HEADS, bool TAIL>
-__global__ void __launch_bounds__(kFewThreads, per_sm(NT, TAIL, HEADS)) few_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kFewThreads, per_sm(NT)) few_kernel(const __grid_constant__ Params p) {
   constexpr int kRows = 8 * NT, kSplit = 4 / HEADS, kStep = 16 * kSplit;
   constexpr int kOut = 64 * VI + (TAIL ? 12 : 4);  // row pitch of the merge buffer (floats)
   __shared__ __align__(16) float red[4][kRows][kOut];
@@ -426,56 +462,6 @@ __global__ void __launch_bounds__(kFewThreads, per_sm(NT, TAIL, HEADS)) few_kern
     const int c0 = share.cta_of(sg.base), c1 = share.cta_of(sg.base + sg.steps - 1);  // the item's parts
     const Parts parts{part(c0, 0), size_t(HEADS * kRows) * size_t(p.D + 2), c1 - c0 + 1, p.D, HEADS * kRows};
 
-    // Those of the rows `todo` (a bit a row) of head hw of the segment that a hidden key's value has spoiled, again
-    // from their visible keys alone, by one warp.
-    auto again = [&](int hw, unsigned todo) {
-      const __half* k = p.k + sg.doc.k0 * p.ks + (sg.kvh + hw) * p.D;
-      const __half* v = p.v + sg.doc.k0 * p.vs + (sg.kvh + hw) * p.D;
-      const int begin = sg.s0 * kStep, ln = int(threadIdx.x) & 31;
-      auto limit = [&](int r) {
-        return max(begin, limit_of(p.causal, (sg.row0 + r) / p.group + lk - sg.doc.lq, lk, sg.doc.prefix));
-      };
-      const int low = limit(__ffs(int(todo)) - 1);  // (later rows see no fewer keys)
-      const int spoiled = low < last ? last_spoiled(p, v, low, last, ln) : -1;
-      __syncwarp();  // (what other lanes have stored of the rows comes first)
-#pragma unroll 1
-      while (todo) {
-        Row of[4];
-        int at_r[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int r = at_r[x] = todo ? __ffs(int(todo)) - 1 : -1;
-          todo &= todo - 1;
-          const int i = (sg.row0 + max(r, 0)) / p.group;
-          const int head = (sg.kvh + hw) * p.group + (sg.row0 + max(r, 0) - i * p.group), lim = limit(max(r, 0));
-          if (lim > spoiled) at_r[x] = -1;  // (its result is the products')
-          of[x].q = p.q + static_cast<long long>(sg.doc.q0 + i) * p.qs + head * p.D;
-          of[x].ke = at_r[x] < 0 ? begin : min(last, lim);
-          of[x].at = i + lk - sg.doc.lq;
-          of[x].slope = p.slopes ? __ldg(p.slopes + head) : 0.0f;
-        }
-        float4 acc[4];
-        float mx, sum;
-        rows_again4(p, of, k, v, begin, ln, nullptr, acc, mx, sum);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int r = at_r[x];
-          const float row_m = __shfl_sync(0xffffffffu, mx, 8 * x), row_l = __shfl_sync(0xffffffffu, sum, 8 * x);
-          if (r < 0) continue;
-          const int i = (sg.row0 + r) / p.group, head = (sg.kvh + hw) * p.group + (sg.row0 + r - i * p.group);
-          const int row = hw * rows + r;
-          if (whole) {
-            if (ln < p.D / 4)
-              store4(p, size_t(sg.doc.q0 + i) * size_t(p.os) + size_t(head) * size_t(p.D) + size_t(4 * ln),
-                     make_float4(acc[x].x / row_l, acc[x].y / row_l, acc[x].z / row_l, acc[x].w / row_l));
-          } else {
-            if (ln < p.D / 4) __stcg(reinterpret_cast<float4*>(mine + row * p.D) + ln, acc[x]);
-            if (ln == 0) __stcg(reinterpret_cast<float2*>(mine_ml) + row, make_float2(row_m, row_l));
-          }
-        }
-      }
-    };
-
     // Row r of head hw of the item from all its parts, by one warp.
     auto join_row = [&](int hw, int r) {
       float mx, sum;
@@ -538,7 +524,9 @@ __global__ void __launch_bounds__(kFewThreads, per_sm(NT, TAIL, HEADS)) few_kern
           for (int tt = 0; tt < 4; ++tt)  // (the columns of a row are in the lanes of one t)
             if (rows_bad & (0x11111111u << tt)) redo |= 1u << (8 * n + 2 * tt + e);
         }
-      if (redo) again(my_head, redo);
+      if (redo)
+        few_again(p, {sg.doc.q0, sg.doc.k0, sg.doc.lq, lk, sg.doc.prefix, sg.kvh, sg.row0, sg.s0 * kStep, last, rows, mine,
+                      mine_ml}, my_head, redo);
       if (whole) continue;
       __threadfence();
       __syncwarp();
@@ -633,13 +621,14 @@ __global__ void __launch_bounds__(kFewThreads, per_sm(NT, TAIL, HEADS)) few_kern
         }
       }
       if (__syncthreads_or(any_bad)) {
-        for (int x = warp; x < HEADS * ((rows + 3) / 4); x += 4) {  // four rows of a head a warp
-          const int hw = x % HEADS, r0 = x / HEADS * 4;
-          unsigned redo = 0;
-          for (int r = r0; r < min(r0 + 4, rows); ++r)
-            if (row_bad[hw * rows + r]) redo |= 1u << r;
-          if (redo) again(hw, redo);
-        }
+        // (with one head every fourth row a warp, with two every second)
+        const int hw = warp % HEADS;
+        unsigned redo = 0;
+        for (int r = warp / HEADS; r < rows; r += kSplit)
+          if (row_bad[hw * rows + r]) redo |= 1u << r;
+        if (redo)
+          few_again(p, {sg.doc.q0, sg.doc.k0, sg.doc.lq, lk, sg.doc.prefix, sg.kvh, sg.row0, sg.s0 * kStep, last, rows, mine,
+                      mine_ml}, hw, redo);
         __syncthreads();  // row_bad is free again
       }
       if (whole) continue;
@@ -692,7 +681,7 @@ __global__ void __launch_bounds__(kFewThreads, per_sm(NT, TAIL, HEADS)) few_kern
 template <int KI, int VI, int NT, int HEADS, bool TAIL = false>
 cudaError_t few_launch_as(const Params& p, cudaStream_t s) {
   const int sms = num_sms() < kMaxSms ? num_sms() : kMaxSms;
-  return launch_pdl(few_kernel<KI, VI, NT, HEADS, TAIL>, dim3(unsigned(sms * per_sm(NT, TAIL, HEADS))), dim3(kFewThreads), 0, s,
+  return launch_pdl(few_kernel<KI, VI, NT, HEADS, TAIL>, dim3(unsigned(sms * per_sm(NT))), dim3(kFewThreads), 0, s,
                     p);
 }
 
@@ -707,11 +696,11 @@ cudaError_t few_launch_rows(const Params& p, cudaStream_t s) {
 template <int NT>
 cudaError_t few_launch_heads(const Params& p, cudaStream_t s) {
   // Neighbouring heads in a CTA where a head's row is no whole number of 64 bytes (64 probes over
-  // images, 16 heads of 72: 41 us against 58 with a head per CTA and 46 with two); else a head per CTA, whose
+  // images, 16 heads of 72: 40 us against 58 with a head per CTA and 46 with two); else a head per CTA, whose
   // warps then share its long run of keys (one token of 16 requests, 8 key heads of 128: 162 us
   // against 178). Also where there is so little to read that a head's keys had better be spread
   // over as many warps as there are.
-  const bool little = static_cast<long long>(p.total_k) * p.hk <= 64ll * 2 * kMaxFewGrid;
+  const bool little = static_cast<long long>(p.total_k) * p.hk <= 64ll * 8 * kMaxSms;
   if (p.D % 32 && !little && p.hk % 4 == 0) return few_launch_rows<NT, 4>(p, s);
   if (p.D % 32 && !little && p.hk % 2 == 0) return few_launch_rows<NT, 2>(p, s);
   return few_launch_rows<NT, 1>(p, s);
