@@ -302,7 +302,8 @@ __global__ void __launch_bounds__(kFewThreads, per_sm(NT)) few_kernel(const __gr
 
     // this lane's two rows of each tile as columns of S^T: visible keys, position, slope
     int lim[NT][2];
-    float at[NT][2], slope[NT][2];
+    int at[NT][2];
+    float slope[NT][2];
     uint32_t q[NT][KI][4], q_tail[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -311,7 +312,7 @@ __global__ void __launch_bounds__(kFewThreads, per_sm(NT)) few_kernel(const __gr
         const int r = sg.row0 + 8 * n + 2 * t + e;
         const int i = r / p.group, pos = i + lk - sg.doc.lq;
         lim[n][e] = r < rows_all ? limit_of(p.causal, pos, lk, sg.doc.prefix) : lk;
-        at[n][e] = float(pos);
+        at[n][e] = pos;
         slope[n][e] = p.slopes && r < rows_all ? __ldg(p.slopes + kvh * p.group + (r - i * p.group)) * kLog2e : 0.0f;
       }
       const int r = sg.row0 + 8 * n + g;  // Q^T: this lane's column
@@ -388,7 +389,7 @@ __global__ void __launch_bounds__(kFewThreads, per_sm(NT)) few_kernel(const __gr
           const int key = key0 + g + 8 * (e >> 1);
           float y = s[n][e] * sl2;
           if (p.cap > 0.0f) y = capped(y, p.cap * kLog2e);
-          if (p.slopes) y = fmaf(-slope[n][e & 1], fabsf(at[n][e & 1] - float(key)), y);
+          if (p.slopes) y = fmaf(-slope[n][e & 1], fabsf(float(at[n][e & 1] - key)), y);  // (positions pass 2^24)
           x[e] = key < min(lim[n][e & 1], last) ? y : -INFINITY;
         }
 #pragma unroll
