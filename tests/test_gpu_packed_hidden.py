@@ -131,3 +131,23 @@ def test_rows_beside_a_spoiled_key(sv, lq, lk, hq, hk, d, out):
         last = spoiled[-3:] if out == "f16" else spoiled[-3:].view(torch.float8_e4m3fn).float()
         assert torch.isnan(last).all()
     sv.sv_sync()
+
+
+@pytest.mark.parametrize("poison", [math.nan, math.inf])
+@pytest.mark.parametrize("hq,hk,d", [(2, 2, 72), (2, 1, 64), (4, 4, 72), (1, 1, 128)])
+def test_few_rows_read_no_key_behind_their_block(sv, poison, hq, hk, d):
+    """One document of more rows than a block among many single queries: blocks whose queries do not see a spoiled key
+    (8 rows each) have the bits that they have without it."""
+    lq, lk = [40] + [1] * 20, [30000] + [50] * 20
+    c = Case(lq, lk, hq, hk, d, seed=d + hq)
+    for workspace in (True, False):
+        want = c.run(sv, mask=1, workspace=workspace)
+        c.check(want, mask=1)
+        k, v = c.k.clone(), c.v.clone()
+        c.k[30000 - 5] = poison
+        c.v[30000 - 5] = poison
+        got = c.run(sv, mask=1, workspace=workspace)
+        c.k, c.v = k, v
+        assert torch.equal(got[:32], want[:32]) and torch.equal(got[40:], want[40:])
+        assert torch.isfinite(got[:35]).all() and not torch.isfinite(got[35:40]).any()
+    sv.sv_sync()

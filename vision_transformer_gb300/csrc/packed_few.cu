@@ -298,7 +298,9 @@ __global__ void __launch_bounds__(kFewThreads, per_sm(NT)) few_kernel(const __gr
     const int kvh = sg.kvh + my_head;
     const __half* kb = p.k + sg.doc.k0 * p.ks + kvh * p.D;
     const __half* vb = p.v + sg.doc.k0 * p.vs + kvh * p.D;
-    const int last = min(lk, sg.s1 * kStep);  // keys of this segment end here
+    // keys of this segment that one of its rows sees end here (the last row sees the most)
+    const int last = min(sg.s1 * kStep, limit_of(p.causal, (min(sg.row0 + kRows, rows_all) - 1) / p.group + lk - sg.doc.lq,
+                                                 lk, sg.doc.prefix));
 
     // this lane's two rows of each tile as columns of S^T: visible keys, position, slope
     int lim[NT][2];
