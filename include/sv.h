@@ -433,7 +433,8 @@ typedef enum {
 /* Options of sv_attention_packed (NULL there: every field 0). The pointers are device pointers, read during the call. */
 typedef struct {
   float scale;         /* factor on q . k; <= 0 selects 1 / sqrt(head_dim) */
-  float softcap;       /* > 0: scores become softcap * tanh(score / softcap); 0: they stay */
+  float softcap;       /* > 0: scores become softcap * tanh(score / softcap), off by at most 2^-21 of the cap (below 256)
+                          or 2^-18 of the score (from there on); 0: they stay */
   int mask;            /* sv_mask */
   const int* prefix;   /* int32 [docs]: visible prefix of each document (SV_MASK_PREFIX); NULL: none */
   const float* slopes; /* f32 [q_heads]: scores of head h lose slopes[h] * |p_i - j|, after the cap; NULL: none */
@@ -449,7 +450,8 @@ size_t sv_attention_packed_workspace(int docs, int total_q, int total_k, int q_h
  * Attention over documents packed one behind another: images of different sizes in one sequence, prompts, or one new
  * query for each of many long key sequences. o = softmax(scores) v over the keys that a query sees (sv_mask), scores
  * as in sv_attention_options; a query that sees no key gets zeros. Keys that a query does not see have no part in its
- * result, whatever their values (NaN and infinities too).
+ * result, whatever their values (NaN and infinities too); a query that sees a NaN or an infinity gets values that are
+ * not finite from it.
  * q: f16 [total_q, q_heads * head_dim], k, v: f16 [total_k, kv_heads * head_dim]; q_heads is a multiple of kv_heads,
  * and query head h reads key head h / (q_heads / kv_heads). Row strides in values, as in sv_rope (multiples of 8; 0:
  * contiguous): q, k and v may be columns of one projection's output.

@@ -606,7 +606,8 @@ __device__ __forceinline__ void cut_scores(uint32_t s_tm, int valid) {
 
 // SOLO: items of one tile, whose key tiles the two groups take in turn (for launches of few items: half the chain, and
 // an end at which the groups' sums are joined). The output's type is then read from the parameters.
-template <int NB, bool CAP, bool BIAS, bool E4M3, bool SOLO>
+// CAP: 0 none, 1 below kFarCap, 2 from there on (with BIAS, whose slopes may then be null, and without SOLO).
+template <int NB, int CAP, bool BIAS, bool E4M3, bool SOLO>
 // 10 warps: three share each of two SM sub-partitions, so a thread may hold at most
 // 16384 / (3 x 32) registers, rounded down to the allocation granule.
 __global__ void __maxnreg__(168)
@@ -974,7 +975,7 @@ __global__ void __maxnreg__(168)
     const uint32_t o_tm = tmem + uint32_t(256 + w * 128) + lane_off;
     const int qi = r / p.group, head = r - qi * p.group;  // this row's query in the tile, head in the group
     const int Dn = (p.D + 15) / 16 * 16;
-    const float sl2 = CAP ? 2.0f * kLog2e * p.scale / p.cap : kLog2e * p.scale;
+    const float sl2 = CAP ? cap_factor(p.scale, p.cap) : kLog2e * p.scale;
     const float cap2 = p.cap * kLog2e;
     // query of this row in an item: index, -1 if the row holds none
     auto query = [&](const Item& it) {
@@ -984,7 +985,7 @@ __global__ void __maxnreg__(168)
     auto out_at = [&](const Item& it, int i) {
       return size_t(it.q0 + i) * size_t(p.os) + size_t(it.kvh * p.group + head) * size_t(p.D);
     };
-    constexpr bool kUnits = CAP || BIAS;       // scores in units of log 2 before the exponentials
+    constexpr bool kUnits = CAP != 0 || BIAS;       // scores in units of log 2 before the exponentials
     // A tile of 128 keys in one step or in two of 64: then the second half of S is on its way while the first is
     // worked on, and only the first half's maximum stands before the first exponentials, but a row's exponent is
     // checked twice. 32 images of 729, 16 heads of 72, E4M3 out: 122 us in one step, 113 in two; 48 documents of up
@@ -1041,7 +1042,7 @@ __global__ void __maxnreg__(168)
       const int how_before = out_how;
       out_to = i < 0 ? -1 : static_cast<long long>(out_at(it, i));
       out_how = (lim == 0 ? kNothing : 0) | (it.splits > 1 ? kPart : 0) | (jb >= je ? kEmpty : 0);
-      const float slope2 = BIAS && i >= 0 ? __ldg(p.slopes + it.kvh * p.group + head) * kLog2e : 0.0f;
+      const float slope2 = BIAS && i >= 0 && (CAP != 2 || p.slopes) ? __ldg(p.slopes + it.kvh * p.group + head) * kLog2e : 0.0f;
       m = -INFINITY;
       l = 0.0f;
       const int j0 = SOLO ? jb + w : jb, j_end = SOLO ? jb + (je - jb + 1) / 2 * 2 : je;
@@ -1054,7 +1055,7 @@ __global__ void __maxnreg__(168)
         tc_fence_after();
         // visible keys of this tile (shared out, the second group's last may lie behind the item's)
         const int valid = (SOLO ? min(lim, je * kTile) : lim) - j * kTile;
-        if constexpr (CAP) cut_scores(s_tm, valid);
+        if constexpr (CAP != 0) cut_scores(s_tm, valid);
         float sv[4][32];
         uint32_t(&su)[4][32] = reinterpret_cast<uint32_t(&)[4][32]>(sv);
         tmem_ld32(s_tm, su[0]);
@@ -1084,11 +1085,21 @@ __global__ void __maxnreg__(168)
             tmem_ld_wait(su[2]);
             reg_fence(su[3]);
           }
-          if constexpr (CAP)
+          if constexpr (CAP != 0)
 #pragma unroll
             for (int c = kC * h; c < kC * h + kC; ++c)
 #pragma unroll
-              for (int e = 0; e < 32; e += 4) capped4(&sv[c][e], sl2, cap2);
+              for (int e = 0; e < 32; e += 4) {
+                float* s = &sv[c][e];
+                if constexpr (CAP == 1) {
+                  capped4(s, sl2, cap2);
+                } else {
+                  float big[4] = {s[0], s[1], s[2], s[3]};
+                  capped4(big, sl2, cap2);
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) s[k] = far_capped(s[k] * (kLog2e * p.scale), s[k] * sl2, big[k]);
+                }
+              }
           if constexpr (BIAS) {
             const float on = CAP ? 1.0f : sl2;
             if (line) {
@@ -1254,7 +1265,7 @@ sv_status packed_map(CUtensorMap* m, const void* ptr, int D, int heads, int rows
   return make_tmap(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, ptr, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <int NB, bool CAP, bool BIAS, bool E4M3, bool SOLO>
+template <int NB, int CAP, bool BIAS, bool E4M3, bool SOLO>
 sv_status packed_launch_as(const Params& p, int grid, cudaStream_t s) {
   auto kern = packed_tile_kernel<NB, CAP, BIAS, E4M3, SOLO>;
   static unsigned long long attr_set = 0;  // the attribute is per device
@@ -1290,11 +1301,13 @@ sv_status packed_launch_as(const Params& p, int grid, cudaStream_t s) {
 
 template <int NB, bool E4M3, bool SOLO>
 sv_status packed_launch(const Params& p, int grid, cudaStream_t s) {
+  if constexpr (!SOLO)
+    if (p.cap >= kFarCap) return packed_launch_as<NB, 2, true, E4M3, SOLO>(p, grid, s);
   if (p.cap > 0.0f)
-    return p.slopes ? packed_launch_as<NB, true, true, E4M3, SOLO>(p, grid, s)
-                    : packed_launch_as<NB, true, false, E4M3, SOLO>(p, grid, s);
-  return p.slopes ? packed_launch_as<NB, false, true, E4M3, SOLO>(p, grid, s)
-                  : packed_launch_as<NB, false, false, E4M3, SOLO>(p, grid, s);
+    return p.slopes ? packed_launch_as<NB, 1, true, E4M3, SOLO>(p, grid, s)
+                    : packed_launch_as<NB, 1, false, E4M3, SOLO>(p, grid, s);
+  return p.slopes ? packed_launch_as<NB, 0, true, E4M3, SOLO>(p, grid, s)
+                  : packed_launch_as<NB, 0, false, E4M3, SOLO>(p, grid, s);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -1309,7 +1322,7 @@ sv_status tile_launch(const Params& p, cudaStream_t s) {
   // Few items of 8 key tiles and more on average: a tile each, its keys shared out between the groups. (256 queries of
   // 8 heads of 128 over 2: 1,024 keys 19.2 us in items of two tiles and 18.0 so, 2,048 keys 34 and 25, 9,000 keys
   // 58 and 48; one image of 729 tokens, 16 heads of 72: 16.0 and 16.9, the end costs what the chain has saved.)
-  if (p.counters && 2 * items <= grid && p.total_k >= static_cast<long long>(kMinSplit) * kTile * p.docs)
+  if (p.counters && p.cap < kFarCap && 2 * items <= grid && p.total_k >= static_cast<long long>(kMinSplit) * kTile * p.docs)
     return p.D > 64 ? packed_launch<2, false, true>(p, grid, s) : packed_launch<1, false, true>(p, grid, s);
   if (p.out_e4m3) return p.D > 64 ? packed_launch<2, true, false>(p, grid, s) : packed_launch<1, true, false>(p, grid, s);
   return p.D > 64 ? packed_launch<2, false, false>(p, grid, s) : packed_launch<1, false, false>(p, grid, s);

@@ -73,7 +73,9 @@ __device__ __forceinline__ bool document(const Params& p, int d, int docs, Docum
 }
 
 // cap tanh(s / cap) = cap - 2 cap / (2^x + 1), x = 2 s log2 e / cap, c = cap in any unit; exact
-// limits for infinite s. The error, about 2^-22 cap, is that of the reciprocal of a number >= 1.
+// limits for infinite s. The error, about 2^-22 cap, is that of the reciprocal of a number >= 1; from caps of
+// kFarCap on, where that is more than 2^-14, scores that are small beside the cap are summed as a series.
+constexpr float kFarCap = 256.0f;
 __device__ __forceinline__ float capped(float x, float c) {
   const float u = ex2(x) + 1.0f;
   float r;
@@ -102,6 +104,21 @@ __device__ __forceinline__ void capped4(float* y, float x, float c) {
   const float ra = r * b, rb = r * a;
   fma_x2(y[0], y[1], ra, ra, u[1], u[0], c, c);
   fma_x2(y[2], y[3], rb, rb, u[3], u[2], c, c);
+}
+
+// Factor of the scores' products for x above: 1e30 stands for more (the smallest product that is not 0 is 2^-48), so
+// that a product of 0 stays 0 whatever the cap.
+__device__ __forceinline__ float cap_factor(float scale, float cap) { return fminf(2.0f * kLog2e * scale / cap, 1e30f); }
+
+// s: a score in units of log 2; x as above; big: what capped gives. Below |s / cap| = 1/4, where that cancels:
+// s (1 - z^2 / 3 + 2 z^4 / 15 - 17 z^6 / 315 + 62 z^8 / 2835), z = x ln 2 / 2 (the next term is below 2^-26).
+// The error is below 2^-18 of the score for any cap.
+__device__ __forceinline__ float far_capped(float s, float x, float big) {
+  const float z = x * 0.34657359f, y = z * z;
+  float t = fmaf(y, 62.0f / 2835.0f, -17.0f / 315.0f);
+  t = fmaf(y, t, 2.0f / 15.0f);
+  t = fmaf(y, t, -1.0f / 3.0f);
+  return fabsf(z) < 0.25f ? fmaf(s * y, t, s) : big;
 }
 
 // Eight values in the output's type at `to`.

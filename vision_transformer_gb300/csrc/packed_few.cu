@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kFewThreads, per_sm(NT)) few_kernel(const __gr
   const int my_head = warp % HEADS, my_keys = warp / HEADS;
   Share<kRows, HEADS> share(p, lane);
   const int chunks = p.D / 8;  // 16-byte chunks of a row
-  const float sl2 = p.cap > 0.0f ? 2.0f * kLog2e * p.scale / p.cap : kLog2e * p.scale;
+  const float sl2 = p.cap > 0.0f ? cap_factor(p.scale, p.cap) : kLog2e * p.scale;
 
   Segment sg;
   while (share.get(sg)) {
@@ -390,7 +390,10 @@ __global__ void __launch_bounds__(kFewThreads, per_sm(NT)) few_kernel(const __gr
         for (int e = 0; e < 4; ++e) {  // e & 1: the row, e >> 1: keys g, g + 8
           const int key = key0 + g + 8 * (e >> 1);
           float y = s[n][e] * sl2;
-          if (p.cap > 0.0f) y = capped(y, p.cap * kLog2e);
+          if (p.cap > 0.0f) {
+            const float big = capped(y, p.cap * kLog2e);
+            y = p.cap < kFarCap ? big : far_capped(s[n][e] * (kLog2e * p.scale), y, big);
+          }
           if (p.slopes) y = fmaf(-slope[n][e & 1], fabsf(float(at[n][e & 1] - key)), y);  // (positions pass 2^24)
           x[e] = key < min(lim[n][e & 1], last) ? y : -INFINITY;
         }
