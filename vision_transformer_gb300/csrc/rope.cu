@@ -324,7 +324,10 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_kernel(const __grid_cons
             add_x2(s0, s1, s0, s1, a[i], a[i + 1]);
             add_x2(s0, s1, s0, s1, b[i], b[i + 1]);
           }
-          const float mean = head_sum(s0 + s1) * p.inv_dim;
+          // (Rounded as a division. The product with 1 / D, which may also be fused into the differences, misses the
+          // value of a constant head where D is no power of two, and the norm divides what is left by next to nothing.)
+          const float sum = head_sum(s0 + s1), near = sum * p.inv_dim;
+          const float mean = fmaf(fmaf(-near, float(p.head_dim), sum), p.inv_dim, near);
 #pragma unroll
           for (int s = 0; s < kRuns; ++s)
 #pragma unroll
