@@ -38,3 +38,16 @@ def test_heads_far_from_zero(sv, d, base):
     ref = w / std
     tol = 2.0 ** -11 * abs(ref) + 2.0 ** -25 + 2.0 ** -18 * abs(ref).max() + 1.01 * 2.0 ** -24 * base / std
     assert (abs(y - ref) <= tol).all()
+
+
+@pytest.mark.parametrize("eps", [1e-45, 1e-40, 1e-30, 1e-6])
+@pytest.mark.parametrize("norm", [0, 1])
+def test_heads_of_zeros_with_any_eps(sv, eps, norm):
+    """0 / sqrt(eps) is 0 for the smallest eps; other heads do not notice one like that."""
+    x = torch.zeros(3, 72, dtype=torch.float16, device="cuda")
+    x[1] = torch.linspace(-2.0, 3.0, 72).half()
+    y = _norm(sv, x, norm, eps)
+    assert (y[0] == 0).all() and (y[2] == 0).all()
+    w = x[1].double() - (x[1].double().mean() if norm else 0.0)
+    ref = w / ((w * w).mean() + eps).sqrt()
+    assert ((y[1].double() - ref).abs() <= 2.0 ** -11 * ref.abs() + 2.0 ** -25 + 2.0 ** -18 * ref.abs().max()).all()

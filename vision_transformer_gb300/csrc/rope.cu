@@ -32,6 +32,7 @@
 // (72 values: 6 heads on 30 lanes), and neighbouring lanes hold neighbouring runs.
 // The cosines of a row are the same for all of its heads: a warp works them out once per row,
 // the norm's weights multiplied in.
+#include <cfloat>
 #include <cmath>
 
 #include "ptx.cuh"
@@ -598,7 +599,7 @@ sv_status sv_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out
   p.pos = positions;
   p.rows = rows;
   p.head_dim = head_dim;
-  p.eps = eps;
+  p.eps = eps > 0.0f && eps < FLT_MIN ? FLT_MIN : eps;  // (the reciprocal root takes subnormal numbers for 0)
   return rope_launch(p, plan, norm == SV_NORM_RMS ? kNormRms : kNormLayer, static_cast<cudaStream_t>(stream));
 }
 
