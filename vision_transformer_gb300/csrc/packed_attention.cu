@@ -1369,7 +1369,8 @@ sv_status sv_attention_packed(const void* q, const void* k, const void* v, void*
   }
   constexpr int kMostRows = 0x7fffffff - 4096;  // (key and row numbers run past the last by less than that)
   if (total_q > kMostRows || total_k > kMostRows || docs > (1 << 24) ||
-      (total_q / (2 * (kTile * kv_heads / q_heads)) + static_cast<long long>(docs)) * kv_heads >= (1ll << 30)) {
+      (total_q / (2 * kTile * kv_heads / q_heads) + static_cast<long long>(docs)) * kv_heads >= (1ll << 30)) {
+    // (items hold 2 (128 / group) queries, which may be a fifth fewer: their numbers stay below 2^31)
     set_error("%s: %d documents of %d queries with %d heads and %d keys are too many for one call", fn, docs, total_q,
               q_heads, total_k);
     return SV_ERR_UNSUPPORTED;
