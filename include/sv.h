@@ -363,7 +363,9 @@ typedef enum {
   SV_ROPE_SCALE_BASE = 2,    /* base * factor^(n / (n - 1)): the fastest pair stays, the slowest is divided by factor */
   SV_ROPE_SCALE_BY_PARTS = 3 /* by the turns r_i = original_len f_i / 2 pi that a pair makes over the trained length
                                 (YaRN, Peng et al. 2023): f_i (w + (1 - w) / factor) with w = (r_i - 1) / 31 held to
-                                [0, 1], cosines and sines multiplied by 0.1 ln(factor) + 1 */
+                                [0, 1], cosines and sines multiplied by 0.1 ln(factor) + 1. The weight runs over the
+                                turns, as in the paper; implementations whose weight runs over the pair's number
+                                have slightly other frequencies */
 } sv_rope_scaling;
 
 #define SV_ROPE_MAX_PAIRS 128

@@ -608,7 +608,7 @@ __device__ __forceinline__ void cut_scores(uint32_t s_tm, int valid) {
 // an end at which the groups' sums are joined). The output's type is then read from the parameters.
 // CAP: 0 none, 1 below kFarCap, 2 from there on (with BIAS, whose slopes may then be null, and without SOLO).
 template <int NB, int CAP, bool BIAS, bool E4M3, bool SOLO>
-// 10 warps: three share each of two SM sub-partitions, so a thread may hold at most
+// 11 warps: three share each of three SM sub-partitions, so a thread may hold at most
 // 16384 / (3 x 32) registers, rounded down to the allocation granule.
 __global__ void __maxnreg__(168)
     packed_tile_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap tq,
@@ -1157,6 +1157,7 @@ __global__ void __maxnreg__(168)
 #pragma unroll
               for (int e = 0; e < 32; ++e) {
                 const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&pk[e]));
+                // (f is a power of two: only what falls below 2^-14 loses bits, 2^-33 of the row's largest)
                 const __half2 y = __floats2half2_rn(x.x * f, x.y * f);
                 pk[e] = *reinterpret_cast<const uint32_t*>(&y);
               }
@@ -1190,6 +1191,8 @@ __global__ void __maxnreg__(168)
               x1 = ex2(x1);
               if (e & 1) add_x2(s2, s3, s2, s3, x0, x1);
               else add_x2(s0, s1, s0, s1, x0, x1);
+              // F16, what the products take at full rate: 2^-11 of each probability (with TF32 or in two F16 parts
+              // P V would take twice as long); their sum l is of the unrounded ones.
               const __half2 y = __floats2half2_rn(x0, x1);
               pk[e] = *reinterpret_cast<const uint32_t*>(&y);
             }

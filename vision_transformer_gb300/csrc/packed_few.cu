@@ -431,6 +431,7 @@ __global__ void __launch_bounds__(kFewThreads, per_sm(NT)) few_kernel(const __gr
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
+          // (F16, what the products take: 2^-11 of each probability; their sum l is of the unrounded ones)
           const __half2 w = __floats2half2_rn(x[2 * h], x[2 * h + 1]);
           b[n][h] = transpose8x8(*reinterpret_cast<const uint32_t*>(&w));
         }
@@ -694,7 +695,9 @@ cudaError_t few_launch_as(const Params& p, cudaStream_t s) {
 template <int NT, int HEADS>
 cudaError_t few_launch_rows(const Params& p, cudaStream_t s) {
   if (p.D <= 64) return few_launch_as<2, 1, NT, HEADS>(p, s);
-  if (p.D == 72) return few_launch_as<2, 1, NT, HEADS, true>(p, s);
+  // (eight behind whole groups of 32 of a key row and of 64 of a value row; of 40 and 104 the value row's groups are
+  // the same with a tail and without)
+  if (p.D == 64 + 8) return few_launch_as<2, 1, NT, HEADS, true>(p, s);
   if (p.D <= 96) return few_launch_as<3, 2, NT, HEADS>(p, s);
   return few_launch_as<4, 2, NT, HEADS>(p, s);
 }
