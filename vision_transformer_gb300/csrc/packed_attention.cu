@@ -37,8 +37,9 @@
 // in two halves, two warps for 32 rows, one arrival a warp, two issuers, warps of their own for
 // the output. The code of an item is as long as the instruction caches: what runs rarely is
 // out of line.
-// 32 images of 729 tokens, 16 heads of 72: 120 us (650 TFLOP/s of the products of visible keys);
-// one sequence of 8192 tokens behind the prefix mask, 32 heads of 128 over 8: 370 us, 1,490 TFLOP/s.
+// 32 images of 729 tokens, 16 heads of 72: 123 us (635 TFLOP/s of the products of visible keys);
+// one sequence of 8192 tokens behind the prefix mask, 32 heads of 128 over 8: 377 to 403 us by the GPU's
+// clock, 1,365 to 1,460 TFLOP/s.
 #include <cmath>
 
 #include "packed_attention.h"

@@ -188,8 +188,8 @@ static __device__ __noinline__ int last_spoiled(const Params& p, const __half* v
 // A row from its visible keys alone, by a whole warp: keys kb .. ke - 1 of the document, query position `at`. Four keys
 // at a time, of which a lane holds the columns 4 lane .. 4 lane + 3 and then the score of key lane % 4. Unscaled sums,
 // their exponent and denominator. 64 keys turn `beat` on (null: nobody waits for this). 31 rows over 20,000 keys of 128
-// dimensions, the warp alone on its SM: 110 ms; a thread a row 370. (Four rows and eight keys at a time 30, but so many
-// registers here make the callers' loops spill.)
+// dimensions, the warp alone on its SM: 110 ms; a thread a row 370. (Four rows and eight keys at a time 30, with three
+// times the registers, which the callers' loops need.)
 static __device__ __noinline__ float4 row_again(const Params& p, const __half* q, const __half* k, const __half* v,
                                                 int kb, int ke, int at, float slope, int lane, unsigned* beat,
                                                 float& m_out, float& l_out) {

@@ -23,8 +23,8 @@
 // ahead of the arithmetic, and works on them in place. (Loads and stores by the lanes, any
 // layout and prefetch tried: 64 us at best for 23,328 rows of 32 heads of 72, at 170
 // instructions per 216 values and 13 KB in flight per SM.)
-// 23,328 rows of 32 heads of 72 in pairs 18 values apart, RMS norm: 50 us, 4.3 TB/s (instructions: 2
-// values an access); 8,191 rows of 40 heads of 128, RMS norm: 31 us, 5.4 TB/s; 16,411 rows of 8 heads of
+// 23,328 rows of 32 heads of 72 in pairs 18 values apart, RMS norm: 50 us, 4.3 TB/s (2 values an
+// access: 56% of all cycles issue, from 16 warps an SM); 8,191 rows of 40 heads of 128, RMS norm: 31 us, 5.4 TB/s; 16,411 rows of 8 heads of
 // 128, half of each rotated, neighbouring pairs, no norm: 14.4 us, 4.7 TB/s (start and end of the launch).
 // A lane holds eight pairs: runs of V values and the runs n values on with their partners
 // (V = 4, 2 or 1 by what divides n, so that every run is one aligned access), or runs of eight
