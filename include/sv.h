@@ -452,8 +452,8 @@ size_t sv_attention_packed_workspace(int docs, int total_q, int total_k, int q_h
  * Attention over documents packed one behind another: images of different sizes in one sequence, prompts, or one new
  * query for each of many long key sequences. o = softmax(scores) v over the keys that a query sees (sv_mask), scores
  * as in sv_attention_options; a query that sees no key gets zeros. Keys that a query does not see have no part in its
- * result, whatever their values (NaN and infinities too); a query that sees a NaN or an infinity gets values that are
- * not finite from it.
+ * result, whatever their values (NaN and infinities too); those that it sees enter as IEEE arithmetic has it (an infinity
+ * times a probability that is 0 in F16 is NaN).
  * q: f16 [total_q, q_heads * head_dim], k, v: f16 [total_k, kv_heads * head_dim]; q_heads is a multiple of kv_heads,
  * and query head h reads key head h / (q_heads / kv_heads). Row strides in values, as in sv_rope (multiples of 8; 0:
  * contiguous): q, k and v may be columns of one projection's output.
