@@ -481,6 +481,103 @@ sv_status sv_attention_packed(const void* q, const void* k, const void* v, void*
                               long long o_stride, const sv_attention_options* options, int out_dtype, void* workspace,
                               size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------- paged key/value cache */
+
+/*
+ * A cache of keys and values in pages, described by the caller (host memory, read during the call).
+ * A page holds the tokens of one sequence at page_size consecutive positions (or of a prefix that sequences share):
+ *   keys   [kv_heads, page_size, head_dim], f16 or E4M3 codes (dtype), then
+ *   values [kv_heads, page_size, head_dim], then
+ *   a byte for every key [kv_heads, page_size], then for every value: b stands for the factor 2^(b - 16) on the
+ *   head's stored numbers, 255 for a head that held an infinity or NaN.
+ * E4M3: the stored number is the OCP E4M3 code (e4m3fn) of x / 2^e, rounded to nearest even, where e is the least
+ * exponent in -15 .. 8 with which the head's largest magnitude is at most 448 * 2^e (with e = 8 magnitudes end at
+ * 61440 = 240 * 2^8, since 256 * 2^8 is beyond F16); a factor for each token and head, as its keys and values
+ * differ in size. A power of two costs a floating-point code no accuracy, and code * 2^e is an F16 number, so that
+ * reading back rounds nothing. F16: the number itself, e = 0.
+ * A head that holds an infinity or NaN is kept as all NaN: its stored numbers are 0 and its byte is 255.
+ */
+typedef struct {
+  void* pages;   /* device memory: n_pages * sv_cache_page_bytes(), 16-byte aligned */
+  int n_pages;
+  int page_size; /* tokens: 16, 32, 64, 128 or 256 */
+  int kv_heads, head_dim;
+  int dtype;     /* sv_dtype */
+} sv_cache;
+
+/*
+ * The sequences of a call. Sequence s has lengths[s] tokens of its own, token t in page page_table[s * table_stride +
+ * t / page_size] at place t % page_size; before them stand the prefix_len tokens of a prefix that all of them share,
+ * in the pages prefix_pages. The pointers are device pointers, read by the call's kernels; entries behind the last
+ * page that a length needs are not read.
+ */
+typedef struct {
+  int count;
+  const int* page_table;   /* int32 [count, table_stride] */
+  int table_stride;
+  const int* lengths;      /* int32 [count], at most table_stride * page_size */
+  const int* prefix_pages; /* int32 [ceil(prefix_len / page_size)]; NULL: prefix_len is 0 */
+  int prefix_len;
+} sv_cache_batch;
+
+/* Bytes of a page (a multiple of 128). 0: sizes that no cache has. Host only. */
+size_t sv_cache_page_bytes(int page_size, int kv_heads, int head_dim, int dtype);
+
+/*
+ * Writes keys and values of the newest tokens of the sequences into their pages.
+ * k, v: f16 [total, kv_heads * head_dim] with row strides in values, as in sv_rope (multiples of 8; 0: contiguous).
+ * offsets: device int32 [count + 1], non-decreasing: sequence s has the rows offsets[s] .. offsets[s + 1] - 1, its
+ * last n = offsets[s + 1] - offsets[s] own tokens (lengths[s] counts them already: row i is token lengths[s] - n + i).
+ * NULL: total / count rows each. The prefix's pages are not written (to fill them, describe the prefix as a sequence).
+ * Rows of no sequence are skipped, and everything else in the pages is left as it was. No page may be written for two
+ * sequences of a call at the same place.
+ * Offsets that decrease or leave [0, total], lengths outside [n, table_stride * page_size] and page numbers outside
+ * the cache are reported by the next sv_sync as SV_ERR_INVALID_ARG; the rows that they concern are not written.
+ * Requirements: page_size 16, 32, 64, 128 or 256; head_dim a multiple of 8 in [8, 128]; kv_heads <= 65536; count,
+ * total below 2^31 - 4096, total * kv_heads below 2^33.
+ * Errors: SV_ERR_INVALID_ARG; SV_ERR_UNSUPPORTED (page_size, head_dim, sizes), SV_ERR_CUDA.
+ */
+sv_status sv_cache_write(const sv_cache* cache, const sv_cache_batch* batch, const void* k, const void* v,
+                         const int* offsets, int total, long long k_stride, long long v_stride, void* stream);
+
+/*
+ * Reads keys and values back as f16 rows, for instance to run a long prompt over them with sv_attention_packed: the
+ * last n = offsets[s + 1] - offsets[s] tokens of sequence s, of prefix and own ones together (n = prefix_len +
+ * lengths[s]: all). Arguments, requirements and errors as sv_cache_write; k and v are written, n is at most prefix_len
+ * + lengths[s]. Rows of no sequence are left as they were. A head whose byte is 255 comes back as NaN.
+ */
+sv_status sv_cache_read(const sv_cache* cache, const sv_cache_batch* batch, void* k, void* v, const int* offsets,
+                        int total, long long k_stride, long long v_stride, void* stream);
+
+/*
+ * Bytes of workspace that sv_attention_cached needs for these sizes, whatever the lengths: up to 40 MB, and with a
+ * prefix about 4 (head_dim + 2) more for each of the total_q * q_heads rows. Host only.
+ */
+size_t sv_attention_cached_workspace(const sv_cache* cache, const sv_cache_batch* batch, int total_q, int q_heads);
+
+/*
+ * Attention of new queries over a cache: o = softmax(scores) v as in sv_attention_packed, with the sequences as its
+ * documents, whose keys are the prefix followed by their own tokens. The prefix is read once for all sequences.
+ * q: f16 [total_q, q_heads * head_dim], o: [total_q, q_heads * head_dim] f16 or e4m3 (out_dtype), row strides and
+ * q_offsets (queries of each sequence) as there; q_heads is a multiple of kv_heads. o must not overlap q.
+ * options: as there, with mask SV_MASK_DOCUMENT, or SV_MASK_PREFIX: query i of n sees the whole prefix and its
+ * sequence's own tokens j <= lengths[s] - n + i (n may exceed lengths[s]: the first queries then see the prefix alone).
+ * Its fields prefix and slopes must be NULL (SV_ERR_UNSUPPORTED). A query that sees no key gets zeros; one that sees a
+ * key or value whose byte is 255 gets NaN.
+ * Scores, softmax and accumulation in F32; the probabilities are rounded to F16 for their product with the values.
+ * Rows of no sequence are left as they were. Bad offsets and lengths as in sv_cache_write: the call computes nothing,
+ * and the next sv_sync reports SV_ERR_INVALID_ARG; page numbers outside the cache are reported too, and the results of
+ * their sequences are undefined.
+ * workspace: sv_attention_cached_workspace() bytes of device memory (0: NULL will do), 16-byte aligned, zeroed before
+ * the first use by this function; rules as in sv_attention_packed. The same call gives the same bits every time.
+ * Requirements: as sv_cache_write; q_heads / kv_heads <= 64, q_heads <= 65536; 1 <= count <= 2^24.
+ * Errors: SV_ERR_INVALID_ARG; SV_ERR_UNSUPPORTED (head_dim, page_size, heads, options, sizes), SV_ERR_CUDA.
+ */
+sv_status sv_attention_cached(const sv_cache* cache, const sv_cache_batch* batch, const void* q, void* o,
+                              const int* q_offsets, int total_q, int q_heads, long long q_stride, long long o_stride,
+                              const sv_attention_options* options, int out_dtype, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
 /* ---------------------------------------------------------------- utilities */
 
 /* Pixels [batch, tokens, patch_dim] f16 uniform in [-1, 1] from `seed` (synth/synth.h), written to dev_dst. */
@@ -491,7 +588,7 @@ sv_status sv_make_pixels(uint64_t seed, int batch, void* dev_dst, void* stream);
  * library's device error word: SV_ERR_TIMEOUT if a kernel gave up a bounded
  * wait (the kernel then returned without finishing; its outputs are
  * undefined), SV_ERR_INVALID_ARG if sv_attention_packed was given bad document
- * offsets. Clears the error word.
+ * offsets, or a call on a cache bad offsets, lengths or page numbers. Clears the error word.
  */
 sv_status sv_sync(void* stream);
 

@@ -42,7 +42,21 @@ class SvAttentionOptions(ctypes.Structure):
                 ("prefix", ctypes.c_void_p), ("slopes", ctypes.c_void_p)]
 
 
+
+class SvCache(ctypes.Structure):
+    """sv_cache, see :func:`sv_cache`."""
+    _fields_ = [("pages", ctypes.c_void_p), ("n_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("dtype", ctypes.c_int)]
+
+
+class SvCacheBatch(ctypes.Structure):
+    """sv_cache_batch, see :func:`sv_cache_batch`."""
+    _fields_ = [("count", ctypes.c_int), ("page_table", ctypes.c_void_p), ("table_stride", ctypes.c_int),
+                ("lengths", ctypes.c_void_p), ("prefix_pages", ctypes.c_void_p), ("prefix_len", ctypes.c_int)]
+
+
 _PP, _OP = ctypes.POINTER(SvRopePlan), ctypes.POINTER(SvAttentionOptions)
+_CP, _BP = ctypes.POINTER(SvCache), ctypes.POINTER(SvCacheBatch)
 SIGNATURES = [
     ("sv_init_weights", _I, [_U64]),
     ("sv_init_weights_dims", _I, [_U64, _I, _I, _I, _I, _I, _I]),
@@ -70,6 +84,11 @@ SIGNATURES = [
     ("sv_attention_packed_workspace", _SZ, [_I, _I, _I, _I, _I, _I]),
     ("sv_attention_packed", _I, [_VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _I, _I, _LL, _LL, _LL, _LL, _OP, _I,
                                  _VP, _SZ, _VP]),
+    ("sv_cache_page_bytes", _SZ, [_I, _I, _I, _I]),
+    ("sv_cache_write", _I, [_CP, _BP, _VP, _VP, _VP, _I, _LL, _LL, _VP]),
+    ("sv_cache_read", _I, [_CP, _BP, _VP, _VP, _VP, _I, _LL, _LL, _VP]),
+    ("sv_attention_cached_workspace", _SZ, [_CP, _BP, _I, _I]),
+    ("sv_attention_cached", _I, [_CP, _BP, _VP, _VP, _VP, _I, _I, _LL, _LL, _OP, _I, _VP, _SZ, _VP]),
     ("sv_sync", _I, [_VP]),
     ("sv_last_error", ctypes.c_char_p, []),
     ("sv_launch_count", ctypes.c_longlong, []),
@@ -319,6 +338,52 @@ def sv_attention_packed(q, k, v, o, q_offsets, k_offsets, docs: int, total_q: in
         _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(q_offsets), _ptr(k_offsets), docs, total_q, total_k, q_heads,
         kv_heads, head_dim, q_stride, k_stride, v_stride, o_stride, options, out_dtype, _ptr(workspace),
         workspace_bytes, _stream(stream)))
+
+
+def sv_cache_page_bytes(page_size: int, kv_heads: int, head_dim: int, dtype: int = SV_DT_E4M3) -> int:
+    return int(load().sv_cache_page_bytes(page_size, kv_heads, head_dim, dtype))
+
+
+def sv_cache(pages, n_pages: int, page_size: int, kv_heads: int, head_dim: int, dtype: int = SV_DT_E4M3) -> SvCache:
+    """A cache's description; pages (a tensor or device pointer, n_pages * sv_cache_page_bytes()) is kept alive."""
+    cache = SvCache(_ptr(pages), n_pages, page_size, kv_heads, head_dim, dtype)
+    cache.tensors = (pages,)
+    return cache
+
+
+def sv_cache_batch(count: int, page_table, table_stride: int, lengths, prefix_pages=None,
+                   prefix_len: int = 0) -> SvCacheBatch:
+    """The sequences of a call on a cache; keeps the tensors (int32; or device pointers) alive."""
+    batch = SvCacheBatch(count, _ptr(page_table), table_stride, _ptr(lengths), _ptr(prefix_pages), prefix_len)
+    batch.tensors = (page_table, lengths, prefix_pages)
+    return batch
+
+
+def sv_cache_write(cache: SvCache, batch: SvCacheBatch, k, v, offsets, total: int, k_stride: int = 0,
+                   v_stride: int = 0, stream=None):
+    _check("sv_cache_write", load().sv_cache_write(cache, batch, _ptr(k), _ptr(v), _ptr(offsets), total, k_stride,
+                                                   v_stride, _stream(stream)))
+
+
+def sv_cache_read(cache: SvCache, batch: SvCacheBatch, k, v, offsets, total: int, k_stride: int = 0,
+                  v_stride: int = 0, stream=None):
+    _check("sv_cache_read", load().sv_cache_read(cache, batch, _ptr(k), _ptr(v), _ptr(offsets), total, k_stride,
+                                                 v_stride, _stream(stream)))
+
+
+def sv_attention_cached_workspace(cache: SvCache, batch: SvCacheBatch, total_q: int, q_heads: int) -> int:
+    return int(load().sv_attention_cached_workspace(cache, batch, total_q, q_heads))
+
+
+def sv_attention_cached(cache: SvCache, batch: SvCacheBatch, q, o, q_offsets, total_q: int, q_heads: int,
+                        q_stride: int = 0, o_stride: int = 0, options: SvAttentionOptions | None = None,
+                        out_dtype: int = SV_DT_F16, workspace=None, workspace_bytes: int | None = None, stream=None):
+    """workspace: a zeroed tensor of sv_attention_cached_workspace() bytes (or a device pointer and workspace_bytes)."""
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check("sv_attention_cached", load().sv_attention_cached(
+        cache, batch, _ptr(q), _ptr(o), _ptr(q_offsets), total_q, q_heads, q_stride, o_stride, options, out_dtype,
+        _ptr(workspace), workspace_bytes, _stream(stream)))
 
 
 def sv_sync(stream=None):

@@ -1,0 +1,317 @@
+// A key/value cache in pages (sv_cache_write, sv_cache_read): heads of tokens quantised into it and read back.
+//
+// A head x of a token (D values of F16) is stored as codes c = E4M3(x 2^-e) with the least e in -15 .. 8 for which
+// max |x| <= 448 2^e. With max |x| = m 2^p (1 <= m < 2) that is p - 8, or p - 7 where m > 1.75: both are read off the
+// bits of the largest magnitude, and no division or logarithm is needed. Two roundings do not meet: x 2^-e in F16 is
+// exact but below 2^-14, where the code is 0 either way (it rounds to multiples of 2^-9). Reading gives c 2^e, an
+// F16 number: c is 0 or a multiple of 2^-9 with four significant bits, and where c's own grid is finer than F16's
+// (x a multiple of 2^-24), x was on that grid already.
+//
+// Bound: DRAM, every value read once and written once in its other form (D = 128: 3 bytes and 1/128 a value).
+// A warp takes 16 consecutive tokens of one head of the keys (or values): 8 or 16 lanes a token, 16 bytes of F16 a
+// lane, all of its loads on their way at once (8 KB of F16 at 128 dimensions), the largest magnitude by shuffles among
+// the token's lanes. So the stored rows of a warp lie side by side in the page (as long as the tokens are of one
+// sequence), and the 16 scale bytes go out in one access. The tokens' sequences and pages are looked up a lane a token
+// (a binary search among the offsets), when writing behind the loads of the values, which do not depend on them.
+#include "cached.h"
+
+namespace sv {
+namespace cached {
+namespace {
+
+constexpr int kMoveThreads = 128;
+constexpr int kTokens = 16;  // of a warp
+
+struct MoveParams {
+  View c;
+  const __half *k, *v;  // written to when reading the cache
+  long long ks, vs;
+  const int* off;
+  int total;
+};
+
+// Where token t of the call is kept: the first byte of its page, and its place there; false: nowhere.
+template <bool READ>
+__device__ __forceinline__ bool place_of(const MoveParams& p, int t, long long& base, int& at) {
+  const View& c = p.c;
+  int s = 0;
+  if (p.off) {  // the number of offsets 1 .. count that are <= t
+    int hi = c.count;
+    while (s < hi) {
+      const int mid = s + (hi - s + 1) / 2;
+      if (__ldg(p.off + mid) <= t) s = mid;
+      else hi = mid - 1;
+    }
+  } else {
+    s = t / (p.total / c.count);
+  }
+  if (s >= c.count) return false;
+  const int q0 = row_offset(p.off, s, c.count, p.total), q1 = row_offset(p.off, s + 1, c.count, p.total);
+  if (t < q0 || t >= q1) return false;  // a row of no sequence
+  const int have = __ldg(c.lengths + s), first = READ ? c.prefix_len : 0;
+  const long long n = static_cast<long long>(q1) - q0;
+  if (q0 < 0 || q1 > p.total || have < 0 || have > (static_cast<long long>(c.stride) << c.shift) ||
+      n > static_cast<long long>(first) + have) {
+    atomicOr(c.err, kDevErrCache);
+    return false;
+  }
+  int pos = int(have - n + (t - q0));  // among its own tokens
+  const int* pages = c.table + static_cast<long long>(s) * c.stride;
+  if (READ && pos < 0) {
+    pages = c.prefix_pages;
+    pos += first;
+  }
+  const int page = __ldg(pages + (pos >> c.shift));
+  if (page < 0 || page >= c.n_pages) {
+    atomicOr(c.err, kDevErrCache);
+    return false;
+  }
+  base = page * c.page_bytes;
+  at = pos & ((1 << c.shift) - 1);
+  return true;
+}
+
+// LANES lanes hold a token's head, eight values each.
+template <bool READ, bool E4M3, int LANES>
+__global__ void __launch_bounds__(kMoveThreads) cache_kernel(const __grid_constant__ MoveParams p) {
+  constexpr int kPer = 32 / LANES, kSteps = kTokens / kPer;  // tokens of a step, steps
+  constexpr int kEs = E4M3 ? 1 : 2;
+  const View& c = p.c;
+  const int lane = threadIdx.x & 31;
+  pdl_launch_dependents();
+  pdl_wait();
+  const long long unit = static_cast<long long>(blockIdx.x) * (kMoveThreads / 32) + (threadIdx.x >> 5);
+  if (unit == 0 && p.off) {  // offsets that decrease or leave [0, total]
+    bool bad = false;
+    for (int s = lane; s < c.count; s += 32) {
+      const int a = __ldg(p.off + s), b = __ldg(p.off + s + 1);
+      bad |= a < 0 || b < a || b > p.total;
+    }
+    if (bad) atomicOr(c.err, kDevErrCache);
+  }
+  const long long t0 = unit / (2 * c.hk) * kTokens;
+  if (t0 >= p.total) return;
+  const int which = int(unit % (2 * c.hk));  // heads of the keys, then of the values
+  const bool values = which >= c.hk;
+  const int head = values ? which - c.hk : which;
+  const int chunk = lane % LANES;
+  const bool mine = 8 * chunk < c.D;
+  const __half* rows = (values ? p.v : p.k) + head * c.D + 8 * chunk;
+  const long long stride = values ? p.vs : p.ks;
+  const long long last = p.total - t0;  // tokens left
+
+  uint4 x[kSteps];
+  if constexpr (!READ)
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      const int r = i * kPer + lane / LANES;
+      x[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (mine && r < last) x[i] = __ldg(reinterpret_cast<const uint4*>(rows + (t0 + r) * stride));
+    }
+  long long base = -1;  // lane r < 16: token t0 + r
+  int at = 0;
+  if (lane < kTokens && lane < last && !place_of<READ>(p, int(t0) + lane, base, at)) base = -1;
+  // places in the page: of the head's codes of a token, of its scale byte
+  const int codes = (values ? value_bytes(c) : 0) + (head << c.shift) * c.D * kEs;
+  const int scale_at = scale_bytes(c) + ((which << c.shift) + at);
+  int scale = kNoScale;
+  if constexpr (READ) {
+    if (base >= 0) scale = __ldg(c.pages + base + scale_at);
+    __syncwarp();
+  }
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    const int r = i * kPer + lane / LANES;
+    const long long page = __shfl_sync(0xffffffffu, base, r);
+    uint8_t* to = c.pages + page + codes + (__shfl_sync(0xffffffffu, at, r) * c.D + 8 * chunk) * kEs;
+    const bool live = mine && page >= 0;
+    if constexpr (READ) {
+      x[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (live) {
+        if constexpr (E4M3) {
+          const uint2 w = __ldg(reinterpret_cast<const uint2*>(to));
+          x[i].x = w.x, x[i].y = w.y;
+        } else {
+          x[i] = __ldg(reinterpret_cast<const uint4*>(to));
+        }
+      }
+    } else {
+      // the largest magnitude's bits (an infinity or NaN is at least 0x7c00)
+      uint32_t m = __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
+                            __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu));
+#pragma unroll
+      for (int o = 1; o < LANES; o <<= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+      const int top = int(max(m & 0xffffu, m >> 16));
+      const bool bad = top >= 0x7c00;
+      if (bad) x[i] = make_uint4(0u, 0u, 0u, 0u);
+      int byte = bad ? kMarked : kNoScale;
+      if constexpr (E4M3) {
+        const int e = max(-15, (top >> 10) - 23 + ((top & 0x3ff) > 0x300));
+        if (!bad) byte = e + kNoScale;
+        const __half2 f = f16_power(bad ? 0 : -e);
+        __half2* h = reinterpret_cast<__half2*>(&x[i]);
+        // (at most 448 but for e = 8, where 256 is held to 240)
+        const __half2 most = __float2half2_rn(e == 8 ? 240.0f : 448.0f);
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const __half2 y = __hmax2(__hmin2(__hmul2(h[j], f), most), __hneg2(most));
+          w[j] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(y), __NV_SATFINITE, __NV_E4M3);
+        }
+        if (live) *reinterpret_cast<uint2*>(to) = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+      } else {
+        if (live) *reinterpret_cast<uint4*>(to) = x[i];
+      }
+      // the lane that holds the token's place keeps its byte
+      const int got = __shfl_sync(0xffffffffu, byte, (lane % kPer) * LANES);
+      if (lane / kPer == i) scale = got;
+    }
+  }
+  if constexpr (!READ) {
+    if (base >= 0) c.pages[base + scale_at] = uint8_t(scale);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      const int r = i * kPer + lane / LANES;
+      const int byte = __shfl_sync(0xffffffffu, scale, r);
+      const long long page = __shfl_sync(0xffffffffu, base, r);
+      uint4 y = x[i];
+      if constexpr (E4M3) {
+        y = e4m3_to_f16(make_uint2(x[i].x, x[i].y));
+        const __half2 f = f16_power(min(byte, 31) - kNoScale);
+        __half2* h = reinterpret_cast<__half2*>(&y);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[j] = __hmul2(h[j], f);
+      }
+      if (byte == kMarked) y = make_uint4(0x7e007e00u, 0x7e007e00u, 0x7e007e00u, 0x7e007e00u);
+      if (mine && page >= 0) *reinterpret_cast<uint4*>(const_cast<__half*>(rows) + (t0 + r) * stride) = y;
+    }
+  }
+}
+
+template <bool READ>
+sv_status move(const char* fn, const sv_cache* cache, const sv_cache_batch* batch, const void* k, const void* v,
+               const int* offsets, int total, long long k_stride, long long v_stride, cudaStream_t s) {
+  MoveParams p = {};
+  sv_status st = make_view(fn, cache, batch, offsets, total, &p.c);
+  if (st != SV_OK) return st;
+  const long long row = static_cast<long long>(p.c.hk) * p.c.D;
+  p.ks = k_stride ? k_stride : row;
+  p.vs = v_stride ? v_stride : row;
+  if (p.ks < row || p.vs < row || (p.ks | p.vs) % 8) {
+    set_error("%s: row strides must be multiples of 8 that cover a row (k %lld, v %lld)", fn, p.ks, p.vs);
+    return SV_ERR_INVALID_ARG;
+  }
+  if ((total && (!k || !v)) || ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 15)) {
+    set_error("%s: k and v must be 16-byte aligned pointers", fn);
+    return SV_ERR_INVALID_ARG;
+  }
+  if (total == 0) return SV_OK;
+  st = ensure_runtime();
+  if (st != SV_OK) return st;
+  p.c.err = dev_err();
+  p.k = static_cast<const __half*>(k);
+  p.v = static_cast<const __half*>(v);
+  p.off = offsets;
+  p.total = total;
+  const long long units = (static_cast<long long>(total) + kTokens - 1) / kTokens * (2 * p.c.hk);
+  const dim3 grid(unsigned((units + kMoveThreads / 32 - 1) / (kMoveThreads / 32)));
+  const double numbers = 2.0 * total * double(row);
+  LaunchScope L(kKindOther, 0.0, numbers * (2 + (p.c.e4m3 ? 1 : 2)), s);
+  void (*kern)(MoveParams);
+  if (p.c.D > 64) kern = p.c.e4m3 ? cache_kernel<READ, true, 16> : cache_kernel<READ, false, 16>;
+  else kern = p.c.e4m3 ? cache_kernel<READ, true, 8> : cache_kernel<READ, false, 8>;
+  const cudaError_t e = launch_pdl(kern, grid, dim3(kMoveThreads), 0, s, p);
+  return e == cudaSuccess ? SV_OK : cuda_fail(e, fn);
+}
+
+bool cache_sizes(int page_size, int kv_heads, int head_dim, int dtype) {
+  return page_size >= 16 && page_size <= 256 && (page_size & (page_size - 1)) == 0 && kv_heads >= 1 &&
+         kv_heads <= 65536 && head_dim >= 8 && head_dim <= 128 && head_dim % 8 == 0 &&
+         (dtype == SV_DT_F16 || dtype == SV_DT_E4M3) &&
+         // (places in a page are 32-bit numbers)
+         static_cast<long long>(page_size) * kv_heads * (2 * head_dim + 1) * 2 < (1ll << 31);
+}
+
+}  // namespace
+
+sv_status make_view(const char* fn, const sv_cache* cache, const sv_cache_batch* batch, const int* offsets, int total,
+                    View* v) {
+  if (!cache || !batch) {
+    set_error("%s: no cache or batch", fn);
+    return SV_ERR_INVALID_ARG;
+  }
+  if (cache->n_pages < 1 || cache->kv_heads < 1 || (cache->dtype != SV_DT_F16 && cache->dtype != SV_DT_E4M3) ||
+      batch->count < 1 || batch->table_stride < 0 || batch->prefix_len < 0 || total < 0) {
+    set_error("%s: bad arguments (n_pages %d, kv_heads %d, dtype %d, count %d, table_stride %d, prefix_len %d, total %d)",
+              fn, cache->n_pages, cache->kv_heads, cache->dtype, batch->count, batch->table_stride, batch->prefix_len,
+              total);
+    return SV_ERR_INVALID_ARG;
+  }
+  if (!cache_sizes(cache->page_size, cache->kv_heads, cache->head_dim, cache->dtype)) {
+    set_error("%s: page_size %d (16, 32, 64, 128 or 256), head_dim %d (a multiple of 8 in [8, 128]) or %d heads are not "
+              "supported", fn, cache->page_size, cache->head_dim, cache->kv_heads);
+    return SV_ERR_UNSUPPORTED;
+  }
+  constexpr int kMost = 0x7fffffff - 4096;  // (token and row numbers run past the last by less than that)
+  if (total > kMost || batch->count > kMost ||
+      static_cast<long long>(batch->prefix_len) +
+              static_cast<long long>(batch->table_stride) * cache->page_size > kMost ||
+      static_cast<long long>(total) * cache->kv_heads >= (1ll << 33)) {
+    set_error("%s: %d sequences of up to %d pages of %d behind %d tokens, %d rows, are too many for one call", fn,
+              batch->count, batch->table_stride, cache->page_size, batch->prefix_len, total);
+    return SV_ERR_UNSUPPORTED;
+  }
+  if (!offsets && total % batch->count) {
+    set_error("%s: without offsets, %d rows must divide by %d sequences", fn, total, batch->count);
+    return SV_ERR_INVALID_ARG;
+  }
+  if (!cache->pages || (reinterpret_cast<uintptr_t>(cache->pages) & 15) || !batch->lengths ||
+      (batch->table_stride && !batch->page_table) || (batch->prefix_len && !batch->prefix_pages) ||
+      ((reinterpret_cast<uintptr_t>(batch->page_table) | reinterpret_cast<uintptr_t>(batch->lengths) |
+        reinterpret_cast<uintptr_t>(batch->prefix_pages) | reinterpret_cast<uintptr_t>(offsets)) & 3)) {
+    set_error("%s: pages must be a 16-byte aligned pointer, page_table, lengths, prefix_pages and offsets 4-byte aligned "
+              "ones", fn);
+    return SV_ERR_INVALID_ARG;
+  }
+  v->pages = static_cast<uint8_t*>(cache->pages);
+  v->page_bytes = static_cast<long long>(
+      sv_cache_page_bytes(cache->page_size, cache->kv_heads, cache->head_dim, cache->dtype));
+  v->n_pages = cache->n_pages;
+  for (v->shift = 0; (1 << v->shift) < cache->page_size;) ++v->shift;
+  v->hk = cache->kv_heads;
+  v->D = cache->head_dim;
+  v->e4m3 = cache->dtype == SV_DT_E4M3;
+  v->count = batch->count;
+  v->stride = batch->table_stride;
+  v->prefix_len = batch->prefix_len;
+  v->table = batch->page_table;
+  v->lengths = batch->lengths;
+  v->prefix_pages = batch->prefix_pages;
+  return SV_OK;
+}
+
+}  // namespace cached
+}  // namespace sv
+
+extern "C" {
+
+size_t sv_cache_page_bytes(int page_size, int kv_heads, int head_dim, int dtype) {
+  if (!sv::cached::cache_sizes(page_size, kv_heads, head_dim, dtype)) return 0;
+  const size_t heads = size_t(page_size) * size_t(kv_heads);
+  return (heads * 2 * (size_t(head_dim) * (dtype == SV_DT_E4M3 ? 1 : 2) + 1) + 127) / 128 * 128;
+}
+
+sv_status sv_cache_write(const sv_cache* cache, const sv_cache_batch* batch, const void* k, const void* v,
+                         const int* offsets, int total, long long k_stride, long long v_stride, void* stream) {
+  return sv::cached::move<false>("sv_cache_write", cache, batch, k, v, offsets, total, k_stride, v_stride,
+                                 static_cast<cudaStream_t>(stream));
+}
+
+sv_status sv_cache_read(const sv_cache* cache, const sv_cache_batch* batch, void* k, void* v, const int* offsets,
+                        int total, long long k_stride, long long v_stride, void* stream) {
+  return sv::cached::move<true>("sv_cache_read", cache, batch, k, v, offsets, total, k_stride, v_stride,
+                                static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

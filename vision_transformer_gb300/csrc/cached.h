@@ -1,0 +1,67 @@
+// What the kernels on a paged key/value cache share (cache.cu: writing and reading it; cached_attention.cu,
+// cached_prefix.cu: attention over it).
+#pragma once
+#include <cuda_fp8.h>
+
+#include "ptx.cuh"
+#include "sv_internal.h"
+
+namespace sv {
+namespace cached {
+
+constexpr int kNoScale = 16;  // the byte of the factor 1
+constexpr int kMarked = 255;  // the byte of a head that held an infinity or NaN
+
+// A cache and the sequences of a call as the kernels read them.
+struct View {
+  uint8_t* pages;
+  long long page_bytes;
+  int n_pages, shift;  // page_size = 1 << shift
+  int hk, D;
+  int e4m3;
+  int count, stride, prefix_len;
+  const int *table, *lengths, *prefix_pages;
+  int* err;
+};
+
+// Bytes in a page before the values, and before the keys' scale bytes, of which there are hk << shift, then as many
+// of the values.
+__host__ __device__ __forceinline__ int value_bytes(const View& c) {
+  return (c.hk << c.shift) * c.D * (c.e4m3 ? 1 : 2);
+}
+__host__ __device__ __forceinline__ int scale_bytes(const View& c) { return 2 * value_bytes(c); }
+
+// Offset s of the rows of the call's sequences: the caller's, or equal parts.
+__device__ __forceinline__ int row_offset(const int* off, int s, int count, int total) {
+  return off ? __ldg(off + s) : (total / count) * s;
+}
+
+// The eight F16 numbers of eight E4M3 codes (without their factor).
+__device__ __forceinline__ uint4 e4m3_to_f16(uint2 w) {
+  uint4 r;
+  asm("{\n\t.reg .b16 a, b, c, d;\n\t"
+      "mov.b32 {a, b}, %4;\n\t"
+      "mov.b32 {c, d}, %5;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %3, d;\n\t}"
+      : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+      : "r"(w.x), "r"(w.y));
+  return r;
+}
+
+// 2^e as F16, twice, for e in -15 .. 15 (2^-15 is below the normal range).
+__device__ __forceinline__ __half2 f16_power(int e) {
+  const uint32_t h = e == -15 ? 0x0200u : uint32_t(e + 15) << 10;
+  const uint32_t w = h | h << 16;
+  return *reinterpret_cast<const __half2*>(&w);
+}
+
+// Host: checks a cache and a batch, of `total` rows with or without offsets, and fills the view (its device error
+// word once the runtime is there).
+sv_status make_view(const char* fn, const sv_cache* cache, const sv_cache_batch* batch, const int* offsets, int total,
+                    View* v);
+
+}  // namespace cached
+}  // namespace sv
