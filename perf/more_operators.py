@@ -238,6 +238,7 @@ def _prepare_own(s, c):
     s["batch"] = vt.sv_cache_batch(c["seqs"], s["table"], s["table"].stride(0), s["lengths"], s["prefix_pages"],
                                    c["prefix"])
     if c["op"] != "attention":
+        s["stored"] = _stored(s)  # the pages' contents, which a call changes in place
         return
     s["options"] = vt.sv_attention_options(softcap=c["softcap"], mask=0 if c["mask"] == "document" else 1)
     size = vt.sv_attention_cached_workspace(s["cache"], s["batch"], s["total"], c["heads"])
@@ -251,7 +252,7 @@ def _run_own(s):
     if c["op"] == "write":
         vt.sv_cache_write(s["cache"], s["batch"], s["k"], s["v"], s["offsets"], s["total"],
                           k_stride=s["k"].stride(0), v_stride=s["v"].stride(0))
-        return _stored(s)
+        return s["stored"]
     if c["op"] == "read":
         vt.sv_cache_read(s["cache"], s["batch"], s["k"], s["v"], s["offsets"], s["total"])
         return s["k"], s["v"]
