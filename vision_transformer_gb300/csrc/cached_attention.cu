@@ -103,27 +103,44 @@ __device__ __forceinline__ void two_pairs(uint32_t w, uint32_t& lo, uint32_t& hi
       : "r"(w));
 }
 
-// Eight stored numbers in the registers that they are loaded into.
+// Eight stored numbers in the registers that they are loaded into. ALONE: no other access needs the sectors that this one
+// touches (they are not kept in L1).
 template <bool E4M3>
 struct Eight;
 template <>
 struct Eight<true> {
   uint2 w;
+  template <bool ALONE>
   __device__ __forceinline__ void load(const uint8_t* p) {
-    asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(w.x), "=r"(w.y) : "l"(p));
+    if constexpr (ALONE) asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(w.x), "=r"(w.y) : "l"(p));
+    else asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(w.x), "=r"(w.y) : "l"(p));
   }
   __device__ __forceinline__ void clear() { w = make_uint2(0u, 0u); }
 };
 template <>
 struct Eight<false> {
   uint4 w;
+  template <bool ALONE>
   __device__ __forceinline__ void load(const uint8_t* p) {
-    asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
-                 : "l"(p));
+    if constexpr (ALONE)
+      asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                   : "l"(p));
+    else
+      asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                   : "l"(p));
   }
   __device__ __forceinline__ void clear() { w = make_uint4(0u, 0u, 0u, 0u); }
 };
+
+// Sixteen E4M3 codes in one access.
+__device__ __forceinline__ void load_two(Eight<true>& a, Eight<true>& b, const uint8_t* p) {
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(a.w.x), "=r"(a.w.y), "=r"(b.w.x), "=r"(b.w.y)
+               : "l"(p));
+}
+[[maybe_unused]] __device__ __forceinline__ void load_two(Eight<false>&, Eight<false>&, const uint8_t*) {}
 
 // 2^(byte - 16) and its reciprocal, for bytes of factors.
 __device__ __forceinline__ float power_of(int byte) { return __uint_as_float(uint32_t(byte + (127 - kNoScale)) << 23); }
@@ -166,113 +183,151 @@ struct Segment {
 };
 
 // The items of the sequences in order: sequences, key heads, blocks of rows. 32 sequences at a time, one per lane,
-// with their steps summed by shuffles; every warp works it out for itself.
+// with their steps summed by shuffles; every warp works it out for itself. What it knows lies in shared memory (`st`, the
+// warp's own): in registers it was in the way of the keys in flight.
+struct ShareState {
+  long long incl[32];  // steps of the sequences up to this one
+  Sequence seq[32];
+  int blocks[32], steps[32];
+  long long chunk, at, end, base, total;
+  int d0, count;
+};
 template <int ROWS, int STEP>
 class Share {
  public:
-  __device__ __forceinline__ Share(const Params& p, int lane) : p_(p), lane_(lane), count_(p.c.count) {
+  __device__ __forceinline__ Share(const Params& p, int lane, ShareState& st) : p_(p), lane_(lane), st_(st) {
+    int count = p.c.count;
     long long work = 0;
     bool bad = false;
     for (int d0 = 0; d0 < p.c.count; d0 += 32) {
-      bad |= !load(d0);
-      work += mine();
+      Sequence q;
+      int blocks, steps;
+      bad |= !load(d0, count, q, blocks, steps);
+      work += static_cast<long long>(blocks) * p.c.hk * steps;
     }
     for (int o = 16; o; o >>= 1) work += __shfl_xor_sync(0xffffffffu, work, o);
     // bad offsets or lengths: reported, and nothing is computed
     if (__any_sync(0xffffffffu, bad)) {
       if (lane == 0) atomicOr(p.c.err, kDevErrCache);
-      count_ = 0;
+      count = 0;
       work = 0;
     }
-    chunk_ = (work + gridDim.x - 1) / gridDim.x;
-    if (chunk_ < 1) chunk_ = 1;
-    at_ = chunk_ * blockIdx.x;
-    end_ = min(at_ + chunk_, work);  // (a share may begin behind the last step)
-    if (p.c.count > 32 || count_ == 0) load(0);
-    open();
+    const long long chunk = max(1ll, (work + gridDim.x - 1) / gridDim.x), at = chunk * blockIdx.x;
+    if (lane == 0) {
+      st_.chunk = chunk;
+      st_.at = at;
+      st_.end = min(at + chunk, work);  // (a share may begin behind the last step)
+      st_.base = 0;
+      st_.count = count;
+    }
+    __syncwarp();
+    open(0);
   }
   // The next segment of this CTA's share.
   __device__ __forceinline__ bool get(Segment& r) {
-    if (at_ >= end_) return false;
-    while (at_ >= base_ + total_) {
-      base_ += total_;
-      load(d0_ + 32);
-      open();
+    const long long at = st_.at;
+    if (at >= st_.end) return false;
+    while (at >= st_.base + st_.total) {
+      __syncwarp();
+      if (lane_ == 0) st_.base += st_.total;
+      __syncwarp();
+      open(st_.d0 + 32);
     }
-    const int src = __ffs(__ballot_sync(0xffffffffu, base_ + incl_ > at_)) - 1;
-    r.seq.q0 = of(seq_.q0, src);
-    r.seq.n = of(seq_.n, src);
-    r.seq.have = of(seq_.have, src);
-    r.pages = p_.c.table + static_cast<long long>(d0_ + src) * p_.c.stride;
-    r.steps = of(steps_, src);
-    const int blocks = of(blocks_, src);
-    const long long first = base_ + __shfl_sync(0xffffffffu, incl_ - mine(), src);
-    const long long item = (at_ - first) / r.steps;
-    r.base = first + item * r.steps;
-    r.kvh = int(item / blocks);
-    r.row0 = int(item - static_cast<long long>(r.kvh) * blocks) * ROWS;
-    r.s0 = int(at_ - r.base);
-    r.s1 = int(min(end_ - r.base, static_cast<long long>(r.steps)));
-    r.item = 0;
-    at_ = r.base + r.s1;
+    const long long base = st_.base;
+    const int src = __ffs(__ballot_sync(0xffffffffu, base + st_.incl[lane_] > at)) - 1;
+    const int steps = st_.steps[src], blocks = st_.blocks[src];
+    const long long first = base + st_.incl[src] - static_cast<long long>(blocks) * p_.c.hk * steps;
+    const long long item = (at - first) / steps;
+    Segment x;
+    x.seq = st_.seq[src];
+    x.pages = p_.c.table + static_cast<long long>(st_.d0 + src) * p_.c.stride;
+    x.steps = steps;
+    x.base = first + item * steps;
+    x.kvh = int(item / blocks);
+    x.row0 = int(item - static_cast<long long>(x.kvh) * blocks) * ROWS;
+    x.s0 = int(at - x.base);
+    x.s1 = int(min(st_.end - x.base, static_cast<long long>(steps)));
+    x.item = 0;
+    __syncwarp();
+    if (lane_ == 0) {
+      st_.at = x.base + x.s1;
+      r = x;
+    }
+    __syncwarp();
     return true;
   }
-  __device__ __forceinline__ int cta_of(long long step) const { return int(step / chunk_); }
+  __device__ __forceinline__ int cta_of(long long step) const { return int(step / st_.chunk); }
 
  private:
-  __device__ __forceinline__ static int of(int v, int src) { return __shfl_sync(0xffffffffu, v, src); }
-  __device__ __forceinline__ long long mine() const {
-    return static_cast<long long>(blocks_) * p_.c.hk * steps_;
-  }
-  __device__ __forceinline__ bool load(int d0) {
-    d0_ = d0;
-    const bool good = sequence(p_, d0 + lane_, count_, seq_);
-    blocks_ = int((static_cast<long long>(seq_.n) * p_.group + ROWS - 1) / ROWS);
-    steps_ = max(1, (seq_.have + STEP - 1) / STEP);  // (a step without keys writes the prefix's result, or zeros)
+  __device__ __forceinline__ bool load(int d0, int count, Sequence& q, int& blocks, int& steps) {
+    const bool good = sequence(p_, d0 + lane_, count, q);
+    blocks = int((static_cast<long long>(q.n) * p_.group + ROWS - 1) / ROWS);
+    steps = max(1, (q.have + STEP - 1) / STEP);  // (a step without keys writes the prefix's result, or zeros)
     return good;
   }
-  __device__ __forceinline__ void open() {
-    incl_ = mine();
+  __device__ __forceinline__ void open(int d0) {
+    Sequence q;
+    int blocks, steps;
+    load(d0, st_.count, q, blocks, steps);
+    long long incl = static_cast<long long>(blocks) * p_.c.hk * steps;
     for (int o = 1; o < 32; o <<= 1) {
-      const long long a = __shfl_up_sync(0xffffffffu, incl_, o);
-      if (lane_ >= o) incl_ += a;
+      const long long a = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane_ >= o) incl += a;
     }
-    total_ = __shfl_sync(0xffffffffu, incl_, 31);
+    st_.seq[lane_] = q;
+    st_.blocks[lane_] = blocks;
+    st_.steps[lane_] = steps;
+    st_.incl[lane_] = incl;
+    if (lane_ == 31) {
+      st_.total = incl;
+      st_.d0 = d0;
+    }
+    __syncwarp();
   }
   const Params& p_;
-  int lane_, count_, d0_ = 0, blocks_, steps_;
-  Sequence seq_;
-  long long chunk_, at_, end_, base_ = 0, total_ = 0, incl_;
+  const int lane_;
+  ShareState& st_;
 };
 
 // The same for the prefix pass: all rows of the batch over one run of keys.
 template <int ROWS>
 class PrefixShare {
  public:
-  __device__ __forceinline__ PrefixShare(const Params& p, int) : p_(p) {
+  __device__ __forceinline__ PrefixShare(const Params& p, int lane, ShareState& st) : p_(p), lane_(lane), st_(st) {
     const long long work = static_cast<long long>(p.pre.blocks) * p.c.hk * p.pre.steps;
-    at_ = p.pre.chunk * blockIdx.x;
-    end_ = min(at_ + p.pre.chunk, work);
+    if (lane == 0) {
+      st_.at = p.pre.chunk * blockIdx.x;
+      st_.end = min(st_.at + p.pre.chunk, work);
+    }
+    __syncwarp();
   }
   __device__ __forceinline__ bool get(Segment& r) {
-    if (at_ >= end_) return false;
-    const long long item = at_ / p_.pre.steps;
-    r.seq = {0, p_.total_q, p_.c.prefix_len};
-    r.pages = p_.c.prefix_pages;
-    r.kvh = int(item / p_.pre.blocks);
-    r.row0 = int(item - static_cast<long long>(r.kvh) * p_.pre.blocks) * ROWS;
-    r.steps = p_.pre.steps;
-    r.base = item * p_.pre.steps;
-    r.s0 = int(at_ - r.base);
-    r.s1 = int(min(end_ - r.base, static_cast<long long>(r.steps)));
-    r.item = int(item);
-    at_ = r.base + r.s1;
+    const long long at = st_.at, end = st_.end;
+    if (at >= end) return false;
+    const long long item = at / p_.pre.steps;
+    Segment x;
+    x.seq = {0, p_.total_q, p_.c.prefix_len};
+    x.pages = p_.c.prefix_pages;
+    x.kvh = int(item / p_.pre.blocks);
+    x.row0 = int(item - static_cast<long long>(x.kvh) * p_.pre.blocks) * ROWS;
+    x.steps = p_.pre.steps;
+    x.base = item * p_.pre.steps;
+    x.s0 = int(at - x.base);
+    x.s1 = int(min(end - x.base, static_cast<long long>(x.steps)));
+    x.item = int(item);
+    __syncwarp();
+    if (lane_ == 0) {
+      st_.at = x.base + x.s1;
+      r = x;
+    }
+    __syncwarp();
     return true;
   }
 
  private:
   const Params& p_;
-  long long at_, end_;
+  const int lane_;
+  ShareState& st_;
 };
 
 // Sums of a row with their exponent and denominator: four columns a lane.
@@ -353,33 +408,44 @@ __device__ __forceinline__ void finish_row(const Params& p, const Segment& sg, i
   }
 }
 
-// KI: 32-dimension groups of a key, VI: 64-dimension groups of a value, NT: 8-row tiles of an item.
-// PREFIX: all rows over the prefix, results left in parts; else the sequences' rows over their own tokens.
-template <int KI, int VI, int NT, bool E4M3, bool PREFIX>
+// KI: 32-dimension groups of a key, VI: 64-dimension groups of a value; FULL: heads of just so many dimensions.
+// NT: 8-row tiles of an item. PREFIX: all rows over the prefix, results left in parts; else the sequences' rows over their
+// own tokens.
+template <int KI, int VI, bool FULL, int NT, bool E4M3, bool PREFIX>
 __global__ void __launch_bounds__(kThreads, per_sm(NT)) cached_few_kernel(const __grid_constant__ Params p) {
   constexpr int kRows = 8 * NT, kStep = step_keys(E4M3), kSub = kStep / 64;  // kSub: 16-key groups of a warp's step
   constexpr int kEs = E4M3 ? 1 : 2;
   constexpr int kOut = 64 * VI + 4;  // row pitch of the merge buffer (floats)
+  static_assert(!FULL || 32 * KI == 64 * VI, "full heads");
+  // A lane's runs of dimensions: 16 of a key (value) where four (eight) lanes then hold a whole head, else 8.
+  constexpr bool kWideK = E4M3 && FULL, kWideV = kWideK && VI == 2;
+  auto key_run = [](int k, int t) { return kWideK ? 64 * (k >> 1) + 16 * t + 8 * (k & 1) : 32 * k + 8 * t; };
+  auto value_run = [](int k, int g) { return kWideV ? 16 * g + 8 * k : 64 * k + 8 * g; };
   __shared__ __align__(16) float red[4][kRows][kOut];
   __shared__ float red_m[4][kRows], red_l[4][kRows];
   __shared__ unsigned seen;
+  __shared__ ShareState state[4];
+  __shared__ Segment segment[4];  // of each warp, all the same
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   pdl_launch_dependents();
   pdl_wait();
   const View& c = p.c;
-  const int chunks = c.D / 8;
+  const int D = FULL ? 32 * KI : c.D;
+  const int chunks = D / 8;
   const float sl2 = p.cap > 0.0f ? cap_factor(p.scale, p.cap) : kLog2e * p.scale;
   const int to_values = value_bytes(c), to_scales = scale_bytes(c), page_mask = (1 << c.shift) - 1;
-  typename std::conditional<PREFIX, PrefixShare<kRows>, Share<kRows, kStep>>::type share(p, lane);
+  typename std::conditional<PREFIX, PrefixShare<kRows>, Share<kRows, kStep>>::type share(p, lane, state[warp]);
 
-  Segment sg;
+  Segment& sg = segment[warp];
   while (share.get(sg)) {
     const int rows_all = sg.seq.n * p.group;  // of the sequence (for this key head)
     // keys of this segment that one of its rows sees end here (the last row sees the most)
     int last = min(sg.s1 * kStep, sg.seq.have);
     if constexpr (!PREFIX)
       last = min(last, limit_of(p.causal, (min(sg.row0 + kRows, rows_all) - 1) / p.group, sg.seq.n, sg.seq.have));
+    // and the keys that all of them see end here
+    const int clear = PREFIX ? last : min(last, limit_of(p.causal, sg.row0 / p.group, sg.seq.n, sg.seq.have));
 
     // this lane's two rows of each tile as columns of S^T: visible keys
     int lim[NT][2];
@@ -393,63 +459,85 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT)) cached_few_kernel(const 
       }
       const int r = sg.row0 + 8 * n + g;  // Q^T: this lane's column
       const int i = r / p.group;
-      const __half* qr = p.q + static_cast<long long>(sg.seq.q0 + i) * p.qs + (sg.kvh * p.group + r - i * p.group) * c.D;
+      const __half* qr = p.q + static_cast<long long>(sg.seq.q0 + i) * p.qs + (sg.kvh * p.group + r - i * p.group) * D;
 #pragma unroll
       for (int k = 0; k < KI; ++k) {
         uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (r < rows_all && 4 * k + t < chunks) x = __ldg(reinterpret_cast<const uint4*>(qr) + 4 * k + t);
+        if (r < rows_all && (FULL || 4 * k + t < chunks)) x = __ldg(reinterpret_cast<const uint4*>(qr + key_run(k, t)));
         q[n][k][0] = x.x, q[n][k][1] = x.y, q[n][k][2] = x.z, q[n][k][3] = x.w;
       }
     }
 
-    // The page of 16 keys from `key` on (at key / 16 of the pages; behind the last key: any).
-    auto page_at = [&](int key) -> int {
-      if (key >= last) return 0;
-      const int page = __ldg(sg.pages + (key >> c.shift));
+    // Pages of the segment's keys, a lane each: 32 from number first_page on, and the 32 behind them. (Looked up key by
+    // key, a step's loads waited for L2 first: 107 us for one token of 16 requests over up to 32768 keys.)
+    auto page_of = [&](int number) -> int {
+      if (number >= (last + page_mask) >> c.shift) return 0;
+      const int page = __ldg(sg.pages + number);
       if (unsigned(page) < unsigned(c.n_pages)) return page;
-      if (lane == 0) atomicOr(c.err, kDevErrCache);
+      atomicOr(c.err, kDevErrCache);
       return 0;
     };
-    // The head's numbers of these keys, and the first of their scale bytes (the values' hk << shift on).
-    auto numbers_at = [&](int page, int key) {
-      return c.pages + page * c.page_bytes + ((sg.kvh << c.shift) + (key & page_mask)) * (c.D * kEs);
-    };
+    int first_page = (sg.s0 * kStep) >> c.shift;
+    int here = page_of(first_page + lane), there = page_of(first_page + 32 + lane);
+    const uint8_t* const head_at = c.pages + static_cast<long long>(sg.kvh << c.shift) * (D * kEs);
+    const uint8_t* const scales_at = c.pages + to_scales + ((sg.kvh + (lane >> 4) * c.hk) << c.shift) + (lane & 15);
     Eight<E4M3> kx[kSub][2][KI], vx[kSub][4][VI];
     int scale[kSub];  // lane < 16: the byte of key lane, else of value lane - 16
-    int page[kSub];   // of the next keys to be loaded
-    auto load_k = [&](int key0, const int (&pg)[kSub]) {
+    int page[kSub];   // of the keys that are loaded next
+    auto load_k = [&](int key0) {
 #pragma unroll
       for (int u = 0; u < kSub; ++u) {
-        const uint8_t* base = numbers_at(pg[u], key0 + 16 * u);
+        const int at = (key0 + 16 * u) & page_mask;
+        const long long base = page[u] * c.page_bytes;
+        const uint8_t* row = head_at + base + ((at + g) * D + key_run(0, t)) * kEs;
+        const uint8_t* byte = scales_at + base + at;
+        auto load = [&](auto live) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const bool live = key0 + 16 * u + g + 8 * h < last;
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int k = 0; k < KI; ++k) {
-            if (live && 4 * k + t < chunks) kx[u][h][k].load(base + ((g + 8 * h) * c.D + 8 * (4 * k + t)) * kEs);
-            else kx[u][h][k].clear();
-          }
-        }
-        scale[u] = kNoScale;
-        if (key0 + 16 * u + (lane & 15) < last)
-          scale[u] = __ldg(c.pages + pg[u] * c.page_bytes + to_scales + ((sg.kvh + (lane >> 4) * c.hk) << c.shift) +
-                           ((key0 + 16 * u) & page_mask) + (lane & 15));
+            for (int k = 0; k < KI; ++k) {
+              const uint8_t* from = row + (8 * h * D + key_run(k, 0)) * kEs;
+              if (kWideK && (k & 1)) continue;
+              if (live(g + 8 * h) && (FULL || 4 * k + t < chunks)) {
+                if constexpr (kWideK) load_two(kx[u][h][k], kx[u][h][k + 1 < KI ? k + 1 : 0], from);
+                else kx[u][h][k].template load<FULL>(from);
+              } else {
+                kx[u][h][k].clear();
+                if constexpr (kWideK) kx[u][h][k + 1 < KI ? k + 1 : 0].clear();
+              }
+            }
+          scale[u] = live(lane & 15) ? __ldg(byte) : kNoScale;
+        };
+        const int left = last - (key0 + 16 * u);
+        if (left >= 16) load([](int) { return true; });
+        else load([&](int key) { return key < left; });
       }
     };
-    auto load_v = [&](int key0, const int (&pg)[kSub]) {
+    auto load_v = [&](int key0) {
 #pragma unroll
       for (int u = 0; u < kSub; ++u) {
-        const uint8_t* base = numbers_at(pg[u], key0 + 16 * u) + to_values;
+        const uint8_t* row = head_at + page[u] * c.page_bytes + to_values +
+                             ((((key0 + 16 * u) & page_mask) + 2 * t) * D + value_run(0, g)) * kEs;
+        auto load = [&](auto live) {
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          const int at = 2 * t + (h & 1) + 8 * (h >> 1);
-          const bool live = key0 + 16 * u + at < last;
+          for (int h = 0; h < 4; ++h)
 #pragma unroll
-          for (int k = 0; k < VI; ++k) {
-            if (live && 8 * k + g < chunks) vx[u][h][k].load(base + (at * c.D + 8 * (8 * k + g)) * kEs);
-            else vx[u][h][k].clear();
-          }
-        }
+            for (int k = 0; k < VI; ++k) {
+              const int key = (h & 1) + 8 * (h >> 1);
+              const uint8_t* from = row + (key * D + value_run(k, 0)) * kEs;
+              if (kWideV && (k & 1)) continue;
+              if (live(2 * t + key) && (FULL || 8 * k + g < chunks)) {
+                if constexpr (kWideV) load_two(vx[u][h][k], vx[u][h][k + 1 < VI ? k + 1 : 0], from);
+                else vx[u][h][k].template load<FULL>(from);
+              } else {
+                vx[u][h][k].clear();
+                if constexpr (kWideV) vx[u][h][k + 1 < VI ? k + 1 : 0].clear();
+              }
+            }
+        };
+        const int left = last - (key0 + 16 * u);
+        if (left >= 16) load([](int) { return true; });
+        else load([&](int key) { return key < left; });
       }
     };
     float o[NT][4 * VI][4];
@@ -464,13 +552,20 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT)) cached_few_kernel(const 
 
     int key0 = sg.s0 * kStep + 16 * kSub * warp;
     auto look_up = [&](int key) {
+      if ((key >> c.shift) - first_page >= 32) {
+        first_page += 32;
+        here = there;
+        there = page_of(first_page + 32 + lane);
+      }
 #pragma unroll
-      for (int u = 0; u < kSub; ++u) page[u] = page_at(key + 16 * u);
+      for (int u = 0; u < kSub; ++u) {
+        const int n = ((key + 16 * u) >> c.shift) - first_page;
+        page[u] = __shfl_sync(0xffffffffu, n < 32 ? here : there, n & 31);
+      }
     };
     look_up(key0);
-    load_k(key0, page);
-    load_v(key0, page);
-    look_up(key0 + kStep);
+    load_k(key0);
+    load_v(key0);
     for (; key0 < last; key0 += kStep) {
       float s[kSub][NT][4];
       int byte[kSub];
@@ -496,43 +591,59 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT)) cached_few_kernel(const 
           }
         }
       }
-      load_k(key0 + kStep, page);
+      look_up(key0 + kStep);
+      load_k(key0 + kStep);
       uint32_t b[kSub][NT][2];
-      float x[kSub][NT][4];
-      float back[kSub][2];  // what a key's probability counts in the denominator: 2^-ev
+      float up[kSub][2], back[kSub][2];  // of keys g and g + 8: ev, and what a probability counts in the denominator, 2^-ev
 #pragma unroll
-      for (int u = 0; u < kSub; ++u) {
-        float unit[2], up[2];  // keys g and g + 8
+      for (int u = 0; u < kSub; ++u)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int kb = __shfl_sync(0xffffffffu, byte[u], g + 8 * h), vb = __shfl_sync(0xffffffffu, byte[u], 16 + g + 8 * h);
           // (a marked one counts NaN; 31 keeps the other bits a number)
-          unit[h] = max(kb, vb) == kMarked ? __uint_as_float(0x7fc00000u) : power_of(min(kb, 31));
-          up[h] = float(min(vb, 31) - kNoScale);
+          const float unit = max(kb, vb) == kMarked ? __uint_as_float(0x7fc00000u) : power_of(min(kb, 31));
+          up[u][h] = float(min(vb, 31) - kNoScale);
           back[u][h] = reciprocal_of(min(vb, 31));
-        }
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {  // e & 1: the row, e >> 1: keys g, g + 8
-            const int key = key0 + 16 * u + g + 8 * (e >> 1);
-            const float z = s[u][n][e] * unit[e >> 1];
-            float y = z * sl2;
-            if (p.cap > 0.0f) {
-              const float big = capped(y, p.cap * kLog2e);
-              y = p.cap < kFarCap ? big : far_capped(z * (kLog2e * p.scale), y, big);
-            }
-            x[u][n][e] = key < lim[n][e & 1] ? y + up[e >> 1] : -INFINITY;
+          for (int n = 0; n < NT; ++n) {
+            s[u][n][2 * h] *= unit;
+            s[u][n][2 * h + 1] *= unit;
           }
+        }
+      if (p.cap > 0.0f) {
+#pragma unroll
+        for (int u = 0; u < kSub; ++u)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float y = s[u][n][e] * sl2, big = capped(y, p.cap * kLog2e);
+              s[u][n][e] = (p.cap < kFarCap ? big : far_capped(s[u][n][e] * (kLog2e * p.scale), y, big)) + up[u][e >> 1];
+            }
+      } else {
+#pragma unroll
+        for (int u = 0; u < kSub; ++u)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[u][n][e] = fmaf(s[u][n][e], sl2, up[u][e >> 1]);
       }
+      if (key0 + 16 * kSub > clear)
+#pragma unroll
+        for (int u = 0; u < kSub; ++u)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)  // e & 1: the row, e >> 1: keys g, g + 8
+              if (key0 + 16 * u + g + 8 * (e >> 1) >= lim[n][e & 1]) s[u][n][e] = -INFINITY;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         float f[2];
         bool raise = false;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float mx = fmaxf(x[0][n][e], x[0][n][e + 2]);
-          if constexpr (kSub == 2) mx = fmaxf(mx, fmaxf(x[kSub - 1][n][e], x[kSub - 1][n][e + 2]));
+          float mx = fmaxf(s[0][n][e], s[0][n][e + 2]);
+          if constexpr (kSub == 2) mx = fmax3(mx, s[kSub - 1][n][e], s[kSub - 1][n][e + 2]);
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
@@ -558,14 +669,14 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT)) cached_few_kernel(const 
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const float ref = m[n][e] == -INFINITY ? 0.0f : m[n][e];
-            x[u][n][e] = ex2(x[u][n][e] - ref);
-            x[u][n][e + 2] = ex2(x[u][n][e + 2] - ref);
-            l[n][e] = fmaf(x[u][n][e], back[u][0], fmaf(x[u][n][e + 2], back[u][1], l[n][e]));
+            s[u][n][e] = ex2(s[u][n][e] - ref);
+            s[u][n][e + 2] = ex2(s[u][n][e + 2] - ref);
+            l[n][e] = fmaf(s[u][n][e], back[u][0], fmaf(s[u][n][e + 2], back[u][1], l[n][e]));
           }
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             // (F16, what the products take: 2^-11 of each probability; their sum l is of the unrounded ones)
-            const __half2 w = __floats2half2_rn(x[u][n][2 * h], x[u][n][2 * h + 1]);
+            const __half2 w = __floats2half2_rn(s[u][n][2 * h], s[u][n][2 * h + 1]);
             b[u][n][h] = transpose8x8(*reinterpret_cast<const uint32_t*>(&w));
           }
         }
@@ -601,8 +712,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT)) cached_few_kernel(const 
             for (int n = 0; n < NT; ++n)
               mma16816(o[n][4 * k + j], a[j][0], a[j][1], a[j][2], a[j][3], b[u][n][0], b[u][n][1]);
         }
-      load_v(key0 + kStep, page);
-      look_up(key0 + 2 * kStep);
+      load_v(key0 + kStep);
     }
 
     // the four warps' sums, brought to one exponent
@@ -625,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT)) cached_few_kernel(const 
       for (int j = 0; j < 4 * VI; j += 2)  // four neighbouring dimensions of a row
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-          *reinterpret_cast<float4*>(&red[warp][8 * n + 2 * t + e][64 * (j >> 2) + 8 * g + 2 * (j & 3)]) =
+          *reinterpret_cast<float4*>(&red[warp][8 * n + 2 * t + e][value_run(j >> 2, g) + 2 * (j & 3)]) =
               make_float4(o[n][j][e], o[n][j][e + 2], o[n][j + 1][e], o[n][j + 1][e + 2]);
     __syncthreads();
     const int rows = min(kRows, rows_all - sg.row0);
@@ -673,17 +783,20 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT)) cached_few_kernel(const 
   }
 }
 
-template <int KI, int VI, int NT, bool PREFIX>
+template <int KI, int VI, bool FULL, int NT, bool PREFIX>
 cudaError_t few_launch_as(const Params& p, int grid, cudaStream_t s) {
-  return launch_pdl(p.c.e4m3 ? cached_few_kernel<KI, VI, NT, true, PREFIX> : cached_few_kernel<KI, VI, NT, false, PREFIX>,
+  return launch_pdl(p.c.e4m3 ? cached_few_kernel<KI, VI, FULL, NT, true, PREFIX>
+                             : cached_few_kernel<KI, VI, FULL, NT, false, PREFIX>,
                     dim3(unsigned(grid)), dim3(kThreads), 0, s, p);
 }
 
 template <int NT, bool PREFIX>
 cudaError_t few_launch(const Params& p, int grid, cudaStream_t s) {
-  if (p.c.D <= 64) return few_launch_as<2, 1, NT, PREFIX>(p, grid, s);
-  if (p.c.D <= 96) return few_launch_as<3, 2, NT, PREFIX>(p, grid, s);
-  return few_launch_as<4, 2, NT, PREFIX>(p, grid, s);
+  if (p.c.D == 64) return few_launch_as<2, 1, true, NT, PREFIX>(p, grid, s);
+  if (p.c.D == 128) return few_launch_as<4, 2, true, NT, PREFIX>(p, grid, s);
+  if (p.c.D < 64) return few_launch_as<2, 1, false, NT, PREFIX>(p, grid, s);
+  if (p.c.D <= 96) return few_launch_as<3, 2, false, NT, PREFIX>(p, grid, s);
+  return few_launch_as<4, 2, false, NT, PREFIX>(p, grid, s);
 }
 
 // What the host alone decides of a call.
