@@ -101,13 +101,14 @@ __global__ void __launch_bounds__(kMoveThreads) cache_kernel(const __grid_consta
   const long long last = p.total - t0;  // tokens left
 
   uint4 x[kSteps];
-  if constexpr (!READ)
+  if constexpr (!READ) {
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       const int r = i * kPer + lane / LANES;
       x[i] = make_uint4(0u, 0u, 0u, 0u);
       if (mine && r < last) x[i] = __ldg(reinterpret_cast<const uint4*>(rows + (t0 + r) * stride));
     }
+  }
   long long base = -1;  // lane r < 16: token t0 + r
   int at = 0;
   if (lane < kTokens && lane < last && !place_of<READ>(p, int(t0) + lane, base, at)) base = -1;

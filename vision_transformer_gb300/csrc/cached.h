@@ -58,6 +58,52 @@ __device__ __forceinline__ __half2 f16_power(int e) {
   return *reinterpret_cast<const __half2*>(&w);
 }
 
+// Where the partial results of the prefix pass are: items (key head, block of rows) one behind another, each of `steps`
+// steps, `chunk` steps a CTA. Item i and CTA c meet in part i + c: `rows` rows of D sums, then exponent and denominator
+// of each.
+struct PrefixParts {
+  float* base;
+  int rows, blocks, steps, chunk;  // (all steps together: below 2^31)
+};
+
+struct Params {
+  View c;
+  const __half* q;
+  void* o;
+  const int* q_off;
+  int total_q, hq, group;
+  unsigned per_group;  // ceil(2^32 / group)
+  long long qs, os;
+  float scale, cap;
+  int causal, out_e4m3;
+  unsigned* counters;  // arrivals at cut items
+  float* partial;      // two parts a CTA: of the item cut at the start of its share, at its end
+  PrefixParts pre;
+};
+
+// Lets a kernel have that much dynamic shared memory (set: devices, by number, that have heard so already).
+template <typename K>
+cudaError_t allow_shared(K kern, int bytes, unsigned long long* set) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev >= 0 && dev < kMaxAttrDevices ? 1ull << dev : 0ull;
+  if ((*set & bit) && bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) *set |= bit;
+  return e;
+}
+
+// The query of row r of a key head (rows x group of a call are below 2^32).
+__device__ __forceinline__ int query_of(const Params& p, int r) {
+  return p.group == 1 ? r : int(__umulhi(unsigned(r), p.per_group));
+}
+
+// The prefix pass for many rows (cached_prefix.cu), in tiles of 128 rows and 128 keys: items of `rows` 256 or 128 rows,
+// steps of one key tile or two. grid: CTAs that have work.
+constexpr int kPrefixTile = 128;
+sv_status prefix_launch(const char* fn, const Params& p, int grid, cudaStream_t s);
+
 // Host: checks a cache and a batch, of `total` rows with or without offsets, and fills the view (its device error
 // word once the runtime is there).
 sv_status make_view(const char* fn, const sv_cache* cache, const sv_cache_batch* batch, const int* offsets, int total,

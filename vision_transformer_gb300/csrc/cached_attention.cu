@@ -22,14 +22,14 @@
 //   O^T += V^T P^T: 16 dimensions x 8 rows. Eight lanes read 64 neighbouring dimensions of a value, a lane has the same
 //     8 of the keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9; the bytes of two keys are interleaved before the conversion, which
 //     so gives pairs of keys. P^T goes from the accumulator's layout to the operand's by a transposing 8 x 8 move.
-// A warp takes 32 keys at a time (F16: 16), the registers of K loaded again as soon as S^T is done, those of V as soon as
-// O^T is: these hold what is in flight. The four warps of a CTA take neighbouring keys of one head; 16 keys lie in one
-// page.
+// A warp takes 16 to 64 keys at a time (by the bytes of a key), the registers of K loaded again as soon as S^T is done,
+// those of V as soon as O^T is: these hold what is in flight. 16 keys lie in one page.
 //
-// Work: the (sequence, key head, block of rows) items are laid out one behind another in steps of a CTA, and every CTA
-// takes an equal, contiguous share of the steps, so that any distribution of lengths fills the GPU. An item inside one
-// share is finished there; one that is cut goes in parts to the workspace, and the last CTA of its parts joins them in
-// order.
+// Work: the (sequence, key head, block of rows) items are laid out one behind another in steps of a warp, and every warp
+// takes an equal, contiguous share of the steps, so that any distribution of lengths fills the GPU and the items of
+// short sequences run side by side, a warp each. An item inside one share is finished there; the parts of others go to
+// shared memory, where the CTA's warps join them when all are through, and the parts of items that are cut between CTAs
+// to the workspace, where the last CTA of an item joins them in order.
 #include <cmath>
 #include <type_traits>
 
@@ -55,30 +55,9 @@ constexpr int kMaxGrid = kMaxSms * kMostPerSm;
 constexpr size_t kCounterBytes = (size_t(kMaxGrid) * sizeof(unsigned) + 127) / 128 * 128;
 // CTAs an SM, by what the registers of a warp allow
 constexpr int per_sm(int nt) { return nt > 1 ? 2 : 3; }
-constexpr int step_keys(bool e4m3) { return e4m3 ? 128 : 64; }  // of a CTA
-
-// Where the partial results of the prefix pass are: items (key head, block of rows) one behind another, each of `steps`
-// steps, `chunk` steps a CTA. Item i and CTA c meet in part i + c: `rows` rows of D sums, then exponent and denominator
-// of each.
-struct PrefixParts {
-  float* base;
-  int rows, blocks, steps;
-  long long chunk;
-};
-
-struct Params {
-  View c;
-  const __half* q;
-  void* o;
-  const int* q_off;
-  int total_q, hq, group;
-  long long qs, os;
-  float scale, cap;
-  int causal, out_e4m3;
-  unsigned* counters;  // arrivals at cut items
-  float* partial;      // two parts a CTA: of the item cut at the start of its share, at its end
-  PrefixParts pre;
-};
+constexpr int kWarps = kThreads / 32;
+// 16-key groups of a warp's step: what the registers of a key and a value in flight hold
+constexpr int groups_of(bool e4m3, int head_dim) { return (e4m3 ? 2 : 1) * (head_dim > 64 ? 1 : 2); }
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
@@ -103,17 +82,25 @@ __device__ __forceinline__ void two_pairs(uint32_t w, uint32_t& lo, uint32_t& hi
       : "r"(w));
 }
 
-// Eight stored numbers in the registers that they are loaded into. ALONE: no other access needs the sectors that this one
-// touches (they are not kept in L1).
+// Eight stored numbers in the registers that they are loaded into, and left as they were where `live` is false: what is
+// there then are other stored numbers, or zeros, which are finite. ALONE: no other access needs the sectors that this
+// one touches (they are not kept in L1).
 template <bool E4M3>
 struct Eight;
 template <>
 struct Eight<true> {
   uint2 w;
   template <bool ALONE>
-  __device__ __forceinline__ void load(const uint8_t* p) {
-    if constexpr (ALONE) asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(w.x), "=r"(w.y) : "l"(p));
-    else asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(w.x), "=r"(w.y) : "l"(p));
+  __device__ __forceinline__ void load(const uint8_t* p, bool live) {
+    if constexpr (ALONE) {
+      asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %3, 0;\n\t@p ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];\n\t}"
+                   : "+r"(w.x), "+r"(w.y)
+                   : "l"(p), "r"(uint32_t(live)));
+    } else {
+      asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %3, 0;\n\t@p ld.global.nc.v2.u32 {%0, %1}, [%2];\n\t}"
+                   : "+r"(w.x), "+r"(w.y)
+                   : "l"(p), "r"(uint32_t(live)));
+    }
   }
   __device__ __forceinline__ void clear() { w = make_uint2(0u, 0u); }
 };
@@ -121,28 +108,33 @@ template <>
 struct Eight<false> {
   uint4 w;
   template <bool ALONE>
-  __device__ __forceinline__ void load(const uint8_t* p) {
-    if constexpr (ALONE)
-      asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
-                   : "l"(p));
-    else
-      asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
-                   : "l"(p));
+  __device__ __forceinline__ void load(const uint8_t* p, bool live) {
+    if constexpr (ALONE) {
+      asm volatile(
+          "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t@p ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+          : "+r"(w.x), "+r"(w.y), "+r"(w.z), "+r"(w.w)
+          : "l"(p), "r"(uint32_t(live)));
+    } else {
+      asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t@p ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+                   : "+r"(w.x), "+r"(w.y), "+r"(w.z), "+r"(w.w)
+                   : "l"(p), "r"(uint32_t(live)));
+    }
   }
   __device__ __forceinline__ void clear() { w = make_uint4(0u, 0u, 0u, 0u); }
 };
 
 // Sixteen E4M3 codes in one access.
-__device__ __forceinline__ void load_two(Eight<true>& a, Eight<true>& b, const uint8_t* p) {
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(a.w.x), "=r"(a.w.y), "=r"(b.w.x), "=r"(b.w.y)
-               : "l"(p));
+__device__ __forceinline__ void load_two(Eight<true>& a, Eight<true>& b, const uint8_t* p, bool live) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t@p ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+               : "+r"(a.w.x), "+r"(a.w.y), "+r"(b.w.x), "+r"(b.w.y)
+               : "l"(p), "r"(uint32_t(live)));
 }
-[[maybe_unused]] __device__ __forceinline__ void load_two(Eight<false>&, Eight<false>&, const uint8_t*) {}
+[[maybe_unused]] __device__ __forceinline__ void load_two(Eight<false>&, Eight<false>&, const uint8_t*, bool) {}
 
-// 2^(byte - 16) and its reciprocal, for bytes of factors.
+// byte - 16 as a number, 2^(byte - 16) and its reciprocal, for bytes of factors.
+__device__ __forceinline__ float exponent_of(int byte) {  // (2^23 + byte, less 2^23 + 16)
+  return __uint_as_float(0x4b000000u | uint32_t(byte)) - float((1 << 23) + kNoScale);
+}
 __device__ __forceinline__ float power_of(int byte) { return __uint_as_float(uint32_t(byte + (127 - kNoScale)) << 23); }
 __device__ __forceinline__ float reciprocal_of(int byte) {
   return __uint_as_float(uint32_t(127 + kNoScale - byte) << 23);
@@ -172,81 +164,86 @@ __device__ __forceinline__ int limit_of(int causal, int i, int n, int have) {
   return causal ? max(0, min(have, have - n + i + 1)) : have;
 }
 
-// A run of steps of one item that falls into this CTA's share.
+// A run of steps of one item that falls into a warp's share. (Steps are counted in 32 bits: the host has seen to that.)
 struct Segment {
   Sequence seq;
-  const int* pages;       // of its keys
-  int kvh, row0;          // key head, first of the item's rows (query x group + head) in the sequence
-  int s0, s1, steps;      // steps of the item: this segment's, all
-  long long base;         // place of the item's first step among all steps
-  int item;               // (prefix pass)
+  const int* pages;   // of its keys
+  int kvh, row0;      // key head, first of the item's rows (query x group + head) in the sequence
+  int s0, s1, steps;  // steps of the item: this segment's, all
+  int base;           // place of the item's first step among all steps
+  int item;           // (prefix pass)
 };
 
-// The items of the sequences in order: sequences, key heads, blocks of rows. 32 sequences at a time, one per lane,
-// with their steps summed by shuffles; every warp works it out for itself. What it knows lies in shared memory (`st`, the
-// warp's own): in registers it was in the way of the keys in flight.
+// A warp's share of the steps. The items of the sequences in order: sequences, key heads, blocks of rows. 32 sequences at
+// a time, one per lane, with their steps summed by shuffles; every warp works it out for itself. What it knows lies in
+// shared memory (`st`, the warp's own): in registers it was in the way of the keys in flight.
 struct ShareState {
-  long long incl[32];  // steps of the sequences up to this one
+  int incl[32];  // steps of the sequences up to this one
   Sequence seq[32];
   int blocks[32], steps[32];
-  long long chunk, at, end, base, total;
+  int chunk, at, end, base, total;
   int d0, count;
 };
 template <int ROWS, int STEP>
 class Share {
  public:
-  __device__ __forceinline__ Share(const Params& p, int lane, ShareState& st) : p_(p), lane_(lane), st_(st) {
+  __device__ __forceinline__ Share(const Params& p, int warp, int lane, ShareState& st) : p_(p), lane_(lane), st_(st) {
     int count = p.c.count;
-    long long work = 0;
+    unsigned work = 0;
     bool bad = false;
+    Sequence q;
+    int blocks, steps;
     for (int d0 = 0; d0 < p.c.count; d0 += 32) {
-      Sequence q;
-      int blocks, steps;
       bad |= !load(d0, count, q, blocks, steps);
-      work += static_cast<long long>(blocks) * p.c.hk * steps;
+      work += unsigned(blocks * p.c.hk * steps);
     }
-    for (int o = 16; o; o >>= 1) work += __shfl_xor_sync(0xffffffffu, work, o);
+    work = __reduce_add_sync(0xffffffffu, work);
     // bad offsets or lengths: reported, and nothing is computed
     if (__any_sync(0xffffffffu, bad)) {
       if (lane == 0) atomicOr(p.c.err, kDevErrCache);
       count = 0;
       work = 0;
     }
-    const long long chunk = max(1ll, (work + gridDim.x - 1) / gridDim.x), at = chunk * blockIdx.x;
+    const unsigned warps = gridDim.x * kWarps, chunk = max(1u, (work + warps - 1) / warps);
     if (lane == 0) {
-      st_.chunk = chunk;
-      st_.at = at;
-      st_.end = min(at + chunk, work);  // (a share may begin behind the last step)
+      st_.chunk = int(chunk);
+      st_.at = int(min(chunk * (blockIdx.x * kWarps + warp), work));  // (a share may begin behind the last step)
+      st_.end = int(min(unsigned(st_.at) + chunk, work));
       st_.base = 0;
       st_.count = count;
     }
     __syncwarp();
-    open(0);
+    if (p.c.count > 32 || count == 0) load(0, count, q, blocks, steps);
+    open(0, q, blocks, steps);
   }
-  // The next segment of this CTA's share.
+  // The next segment of the share.
   __device__ __forceinline__ bool get(Segment& r) {
-    const long long at = st_.at;
+    const int at = st_.at;
     if (at >= st_.end) return false;
     while (at >= st_.base + st_.total) {
       __syncwarp();
       if (lane_ == 0) st_.base += st_.total;
       __syncwarp();
-      open(st_.d0 + 32);
+      Sequence q;
+      int blocks, steps;
+      const int d0 = st_.d0 + 32;
+      load(d0, st_.count, q, blocks, steps);
+      open(d0, q, blocks, steps);
     }
-    const long long base = st_.base;
+    const int base = st_.base;
     const int src = __ffs(__ballot_sync(0xffffffffu, base + st_.incl[lane_] > at)) - 1;
-    const int steps = st_.steps[src], blocks = st_.blocks[src];
-    const long long first = base + st_.incl[src] - static_cast<long long>(blocks) * p_.c.hk * steps;
-    const long long item = (at - first) / steps;
+    const unsigned steps = unsigned(st_.steps[src]), blocks = unsigned(st_.blocks[src]);
+    const int first = base + st_.incl[src] - int(blocks * unsigned(p_.c.hk) * steps);
+    const unsigned item = unsigned(at - first) / steps;
     Segment x;
     x.seq = st_.seq[src];
     x.pages = p_.c.table + static_cast<long long>(st_.d0 + src) * p_.c.stride;
-    x.steps = steps;
-    x.base = first + item * steps;
-    x.kvh = int(item / blocks);
-    x.row0 = int(item - static_cast<long long>(x.kvh) * blocks) * ROWS;
-    x.s0 = int(at - x.base);
-    x.s1 = int(min(st_.end - x.base, static_cast<long long>(steps)));
+    x.steps = int(steps);
+    x.base = first + int(item * steps);
+    x.kvh = blocks == 1 ? int(item) : int(item / blocks);
+    x.row0 = int(item - unsigned(x.kvh) * blocks) * ROWS;
+    x.s0 = at - x.base;
+    x.s1 = min(st_.end - x.base, x.steps);
     x.item = 0;
     __syncwarp();
     if (lane_ == 0) {
@@ -256,22 +253,19 @@ class Share {
     __syncwarp();
     return true;
   }
-  __device__ __forceinline__ int cta_of(long long step) const { return int(step / st_.chunk); }
 
  private:
   __device__ __forceinline__ bool load(int d0, int count, Sequence& q, int& blocks, int& steps) {
     const bool good = sequence(p_, d0 + lane_, count, q);
-    blocks = int((static_cast<long long>(q.n) * p_.group + ROWS - 1) / ROWS);
+    blocks = (q.n * p_.group + ROWS - 1) / ROWS;
     steps = max(1, (q.have + STEP - 1) / STEP);  // (a step without keys writes the prefix's result, or zeros)
     return good;
   }
-  __device__ __forceinline__ void open(int d0) {
-    Sequence q;
-    int blocks, steps;
-    load(d0, st_.count, q, blocks, steps);
-    long long incl = static_cast<long long>(blocks) * p_.c.hk * steps;
+  __device__ __forceinline__ void open(int d0, const Sequence& q, int blocks, int steps) {
+    __syncwarp();
+    int incl = blocks * p_.c.hk * steps;
     for (int o = 1; o < 32; o <<= 1) {
-      const long long a = __shfl_up_sync(0xffffffffu, incl, o);
+      const int a = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane_ >= o) incl += a;
     }
     st_.seq[lane_] = q;
@@ -293,28 +287,27 @@ class Share {
 template <int ROWS>
 class PrefixShare {
  public:
-  __device__ __forceinline__ PrefixShare(const Params& p, int lane, ShareState& st) : p_(p), lane_(lane), st_(st) {
-    const long long work = static_cast<long long>(p.pre.blocks) * p.c.hk * p.pre.steps;
+  __device__ __forceinline__ PrefixShare(const Params& p, int warp, int lane, ShareState& st) : p_(p), lane_(lane), st_(st) {
+    const int work = p.pre.blocks * p.c.hk * p.pre.steps, chunk = p.pre.chunk / kWarps;
     if (lane == 0) {
-      st_.at = p.pre.chunk * blockIdx.x;
-      st_.end = min(st_.at + p.pre.chunk, work);
+      st_.at = min(chunk * (int(blockIdx.x) * kWarps + warp), work);
+      st_.end = min(st_.at + chunk, work);
     }
     __syncwarp();
   }
   __device__ __forceinline__ bool get(Segment& r) {
-    const long long at = st_.at, end = st_.end;
+    const int at = st_.at, end = st_.end;
     if (at >= end) return false;
-    const long long item = at / p_.pre.steps;
     Segment x;
+    x.item = at / p_.pre.steps;
     x.seq = {0, p_.total_q, p_.c.prefix_len};
     x.pages = p_.c.prefix_pages;
-    x.kvh = int(item / p_.pre.blocks);
-    x.row0 = int(item - static_cast<long long>(x.kvh) * p_.pre.blocks) * ROWS;
+    x.kvh = x.item / p_.pre.blocks;
+    x.row0 = (x.item - x.kvh * p_.pre.blocks) * ROWS;
     x.steps = p_.pre.steps;
-    x.base = item * p_.pre.steps;
-    x.s0 = int(at - x.base);
-    x.s1 = int(min(end - x.base, static_cast<long long>(x.steps)));
-    x.item = int(item);
+    x.base = x.item * p_.pre.steps;
+    x.s0 = at - x.base;
+    x.s1 = min(end - x.base, x.steps);
     __syncwarp();
     if (lane_ == 0) {
       st_.at = x.base + x.s1;
@@ -330,102 +323,193 @@ class PrefixShare {
   ShareState& st_;
 };
 
-// Sums of a row with their exponent and denominator: four columns a lane.
-struct RowSums {
-  float4 y;
-  float m, l;
-  __device__ __forceinline__ void add(const float4& v, float mv, float lv) {
-    const float up = fmaxf(m, mv), ref = up == -INFINITY ? 0.0f : up;
-    const float a = ex2(m - ref), b = ex2(mv - ref);
-    m = up;
-    l = fmaf(a, l, b * lv);
-    y = make_float4(fmaf(a, y.x, b * v.x), fmaf(a, y.y, b * v.y), fmaf(a, y.z, b * v.z), fmaf(a, y.w, b * v.w));
-  }
-  // Adds `n` parts in order, sixteen on their way at a time (they come from L2, and nothing else hides its latency):
-  // at(w) is part w's place, [rows][D] sums and [rows] exponents and denominators.
-  template <typename F>
-  __device__ __forceinline__ void add_parts(int n, int row, int rows, int D, int lane, F at) {
-    for (int w0 = 0; w0 < n; w0 += 16) {
-      float4 v[16];
-      float2 ml[16];
+// Parts of a row's sums: part 0 at `first`, the others at `rest` and every `stride` floats on; a part has rows of `pitch`
+// floats, and behind `ml` floats exponent and denominator of each. In shared memory (few parts, joined one by one) or in
+// the workspace. (One form for both, by generic addresses, took 1,800 cycles for two parts in shared memory.)
+struct Source {
+  const float *first, *rest;
+  int stride, n, pitch, ml;
+  bool shared;
+};
+
+__device__ __forceinline__ float4 read_shared4(uint32_t at) {
+  float4 r;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(r.x), "=f"(r.y), "=f"(r.z), "=f"(r.w) : "r"(at) : "memory");
+  return r;
+}
+__device__ __forceinline__ float2 read_shared2(uint32_t at) {
+  float2 r;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(r.x), "=f"(r.y) : "r"(at) : "memory");
+  return r;
+}
+
+// Rows r, r + step, ... (up to four, `rows` of them) of an item, by one warp: the parts of their own keys' sums joined, and
+// with the prefix's parts written in the output's type, or (put) kept as one part of part_rows rows. Eight lanes a row, 16
+// columns each; with fewer rows the lanes share out the parts. Four parts are on their way at a time: they come from L2,
+// and nothing else hides its latency. One function for all of the kernel's ends: its code, run once an item, comes from
+// beyond the instruction caches.
+__device__ __noinline__ void settle(const Params& p, const Segment& sg, const Source own, int r, int step, int rows, float* put,
+                                    int part_rows) {
+  constexpr int kBatch = 4;
+  if (rows <= 0) return;
+  const int lane = int(threadIdx.x) & 31, D = p.c.D;
+  const int share = rows > 2 ? 4 : rows;  // rows at a time: 1, 2 or 4
+  const int k = (lane >> 3) & (share - 1), every = 4 / share, turn = (lane >> 3) / share;
+  const bool live = k < rows;
+  const int in_item = r + (live ? k : 0) * step, row = sg.row0 + in_item;  // of the item, of the sequence (for this key head)
+  float4 y[4];
+  float m = -INFINITY, l = 0.0f;
 #pragma unroll
-      for (int b = 0; b < 16; ++b) {
-        ml[b] = make_float2(-INFINITY, 0.0f);
-        v[b] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (w0 + b < n) {
-          const float* part = at(w0 + b);
-          ml[b] = __ldcg(reinterpret_cast<const float2*>(part + size_t(rows) * D) + row);
-          v[b] = __ldcg(reinterpret_cast<const float4*>(part + size_t(row) * D) + min(lane, D / 4 - 1));
+  for (int c = 0; c < 4; ++c) y[c] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  auto column = [&](int c) { return min((lane & 7) + 8 * c, D / 4 - 1) * 4; };
+
+  auto scale = [&](float f) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      mul_x2(y[c].x, y[c].y, y[c].x, y[c].y, f, f);
+      mul_x2(y[c].z, y[c].w, y[c].z, y[c].w, f, f);
+    }
+    l *= f;
+  };
+  auto add = [&](const float4 (&v)[4], float lv, float f) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      fma_x2(y[c].x, y[c].y, v[c].x, v[c].y, f, f, y[c].x, y[c].y);
+      fma_x2(y[c].z, y[c].w, v[c].z, v[c].w, f, f, y[c].z, y[c].w);
+    }
+    l = fmaf(f, lv, l);
+  };
+  Source from = own;
+  int at = in_item;
+  if (own.shared) {
+#pragma unroll 1
+    for (int w = turn; w < own.n; w += every) {
+      const uint32_t part = smem_u32(w == 0 ? own.first : own.rest + (w - 1) * own.stride);
+      const float2 e = read_shared2(part + 4u * uint32_t(own.ml + 2 * at));
+      float4 v[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[c] = read_shared4(part + 4u * uint32_t(at * own.pitch + column(c)));
+      const float up = fmaxf(m, e.x), ref = up == -INFINITY ? 0.0f : up;
+      scale(ex2(m - ref));
+      m = up;
+      add(v, e.y, ex2(e.x - ref));
+    }
+  }
+#pragma unroll 1
+  for (int pass = own.shared; pass < 2; ++pass) {
+    if (pass == 1) {
+      if (put || p.c.prefix_len == 0) break;
+      const PrefixParts& f = p.pre;
+      const unsigned all = unsigned(sg.seq.q0 * p.group + row), block = all / unsigned(f.rows);
+      const unsigned item = unsigned(sg.kvh * f.blocks) + block, begin = item * unsigned(f.steps), c0 = begin / unsigned(f.chunk);
+      from.stride = f.rows * (D + 2);
+      from.first = f.base + size_t(item + c0) * size_t(from.stride);
+      from.rest = from.first + from.stride;
+      from.n = int((begin + unsigned(f.steps) - 1) / unsigned(f.chunk) - c0) + 1;
+      from.pitch = D;
+      from.ml = f.rows * D;
+      at = int(all - block * unsigned(f.rows));
+    }
+#pragma unroll 1
+    for (int w0 = turn; w0 < from.n; w0 += kBatch * every) {
+      float4 v[kBatch][4];
+      float2 e[kBatch];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const int w = w0 + b * every;
+        e[b] = make_float2(-INFINITY, 0.0f);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[b][c] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (w < from.n) {
+          const float* part = w == 0 ? from.first : from.rest + (w - 1) * static_cast<long long>(from.stride);
+          e[b] = __ldcg(reinterpret_cast<const float2*>(part + from.ml + 2 * at));
+#pragma unroll
+          for (int c = 0; c < 4; ++c) v[b][c] = __ldcg(reinterpret_cast<const float4*>(part + at * from.pitch + column(c)));
         }
       }
       float up = m;
 #pragma unroll
-      for (int b = 0; b < 16; ++b) up = fmaxf(up, ml[b].x);
-      const float ref = up == -INFINITY ? 0.0f : up, back = ex2(m - ref);
+      for (int b = 0; b < kBatch; ++b) up = fmaxf(up, e[b].x);
+      const float ref = up == -INFINITY ? 0.0f : up;
+      scale(ex2(m - ref));
       m = up;
-      l *= back;
-      y = make_float4(y.x * back, y.y * back, y.z * back, y.w * back);
 #pragma unroll
-      for (int b = 0; b < 16; ++b) {
-        const float e = ex2(ml[b].x - ref);
-        l = fmaf(e, ml[b].y, l);
-        y.x = fmaf(e, v[b].x, y.x);
-        y.y = fmaf(e, v[b].y, y.y);
-        y.z = fmaf(e, v[b].z, y.z);
-        y.w = fmaf(e, v[b].w, y.w);
-      }
+      for (int b = 0; b < kBatch; ++b) add(v[b], e[b].y, ex2(e[b].x - ref));
     }
   }
-};
-
-// Row r of the item at row0 of a sequence (sums so far: its own keys'), by one warp: with the prefix's parts, in the
-// output's type.
-__device__ __forceinline__ void finish_row(const Params& p, const Segment& sg, int r, int lane, RowSums a) {
-  const int i = (sg.row0 + r) / p.group, head = sg.kvh * p.group + (sg.row0 + r - i * p.group);
-  if (p.c.prefix_len > 0) {
-    const PrefixParts& f = p.pre;
-    const long long row = static_cast<long long>(sg.seq.q0 + i) * p.group + (head - sg.kvh * p.group);  // of the key head
-    const int block = int(row / f.rows), at = int(row - static_cast<long long>(block) * f.rows);
-    const long long item = static_cast<long long>(sg.kvh) * f.blocks + block, first = item * f.steps;
-    const long long c0 = first / f.chunk, c1 = (first + f.steps - 1) / f.chunk;
-    const float* part = f.base + size_t(item + c0) * (size_t(f.rows) * size_t(p.c.D + 2));
-    a.add_parts(int(c1 - c0) + 1, at, f.rows, p.c.D, lane,
-                [&](int w) { return part + size_t(w) * (size_t(f.rows) * size_t(p.c.D + 2)); });
+  __syncwarp();
+#pragma unroll 1
+  for (int o = 8 * share; o < 32; o <<= 1) {  // the lanes that have shared out the parts of a row
+    const float mo = __shfl_xor_sync(0xffffffffu, m, o), lo = __shfl_xor_sync(0xffffffffu, l, o);
+    const float up = fmaxf(m, mo), ref = up == -INFINITY ? 0.0f : up, fa = ex2(m - ref), fb = ex2(mo - ref);
+    m = up;
+    l = fa * l + fb * lo;  // (both lanes: the same two products)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      float* x = reinterpret_cast<float*>(&y[c]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = fa * x[e] + fb * __shfl_xor_sync(0xffffffffu, x[e], o);
+    }
   }
+  if (!live || turn) return;
+  if (put) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if ((lane & 7) + 8 * c < D / 4) __stcg(reinterpret_cast<float4*>(put + size_t(in_item) * D + column(c)), y[c]);
+    if ((lane & 7) == 0) __stcg(reinterpret_cast<float2*>(put + size_t(part_rows) * D) + in_item, make_float2(m, l));
+    return;
+  }
+  const int i = query_of(p, row), head = sg.kvh * p.group + (row - i * p.group);
   const bool none = p.c.prefix_len == 0 && limit_of(p.causal, i, sg.seq.n, sg.seq.have) == 0;
-  const float inv = 1.0f / a.l;
-  if (lane >= p.c.D / 4) return;
-  const size_t to = size_t(sg.seq.q0 + i) * size_t(p.os) + size_t(head) * size_t(p.c.D) + size_t(4 * lane);
-  const float4 y = none ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
-                        : make_float4(a.y.x * inv, a.y.y * inv, a.y.z * inv, a.y.w * inv);
-  if (p.out_e4m3) {
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(16.0f * y.x, 16.0f * y.y), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(16.0f * y.z, 16.0f * y.w), __NV_SATFINITE, __NV_E4M3);
-    *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.o) + to) = lo | hi << 16;
-  } else {
-    __half2 h[2] = {__floats2half2_rn(y.x, y.y), __floats2half2_rn(y.z, y.w)};
-    *reinterpret_cast<uint2*>(static_cast<__half*>(p.o) + to) = *reinterpret_cast<const uint2*>(h);
+  const float inv = 1.0f / l;
+  const size_t to = size_t(sg.seq.q0 + i) * size_t(p.os) + size_t(head) * size_t(D);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    if ((lane & 7) + 8 * c >= D / 4) continue;
+    const float4 z = none ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
+                          : make_float4(y[c].x * inv, y[c].y * inv, y[c].z * inv, y[c].w * inv);
+    if (p.out_e4m3) {
+      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(16.0f * z.x, 16.0f * z.y), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(16.0f * z.z, 16.0f * z.w), __NV_SATFINITE, __NV_E4M3);
+      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.o) + to + column(c)) = lo | hi << 16;
+    } else {
+      __half2 h[2] = {__floats2half2_rn(z.x, z.y), __floats2half2_rn(z.z, z.w)};
+      *reinterpret_cast<uint2*>(static_cast<__half*>(p.o) + to + column(c)) = *reinterpret_cast<const uint2*>(h);
+    }
   }
 }
+
+// A warp's part of an item.
+template <int ROWS, int VI>
+struct Part {
+  float y[ROWS][64 * VI + 4];
+  float2 ml[ROWS];
+};
+template <int ROWS, int VI>
+struct FewShared {
+  Part<ROWS, VI> part[kWarps][2];  // of the item cut at the start of the warp's share, at its end (and whole items, in turn)
+  Segment cut[kWarps][2];          // these items; no steps: none
+  Segment segment[kWarps];         // the warp's present one
+  ShareState state[kWarps];
+  Params p;  // for settle(): the parameters' own place is far from a function that is not inlined
+  unsigned seen[2];
+};
 
 // KI: 32-dimension groups of a key, VI: 64-dimension groups of a value; FULL: heads of just so many dimensions.
 // NT: 8-row tiles of an item. PREFIX: all rows over the prefix, results left in parts; else the sequences' rows over their
 // own tokens.
 template <int KI, int VI, bool FULL, int NT, bool E4M3, bool PREFIX>
 __global__ void __launch_bounds__(kThreads, per_sm(NT)) cached_few_kernel(const __grid_constant__ Params p) {
-  constexpr int kRows = 8 * NT, kStep = step_keys(E4M3), kSub = kStep / 64;  // kSub: 16-key groups of a warp's step
+  constexpr int kRows = 8 * NT, kSub = groups_of(E4M3, 32 * KI), kStep = 16 * kSub;
   constexpr int kEs = E4M3 ? 1 : 2;
-  constexpr int kOut = 64 * VI + 4;  // row pitch of the merge buffer (floats)
+  using Mem = FewShared<kRows, VI>;
   static_assert(!FULL || 32 * KI == 64 * VI, "full heads");
   // A lane's runs of dimensions: 16 of a key (value) where four (eight) lanes then hold a whole head, else 8.
   constexpr bool kWideK = E4M3 && FULL, kWideV = kWideK && VI == 2;
   auto key_run = [](int k, int t) { return kWideK ? 64 * (k >> 1) + 16 * t + 8 * (k & 1) : 32 * k + 8 * t; };
   auto value_run = [](int k, int g) { return kWideV ? 16 * g + 8 * k : 64 * k + 8 * g; };
-  __shared__ __align__(16) float red[4][kRows][kOut];
-  __shared__ float red_m[4][kRows], red_l[4][kRows];
-  __shared__ unsigned seen;
-  __shared__ ShareState state[4];
-  __shared__ Segment segment[4];  // of each warp, all the same
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  Mem& mem = *reinterpret_cast<Mem*>(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   pdl_launch_dependents();
@@ -435,17 +519,29 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT)) cached_few_kernel(const 
   const int chunks = D / 8;
   const float sl2 = p.cap > 0.0f ? cap_factor(p.scale, p.cap) : kLog2e * p.scale;
   const int to_values = value_bytes(c), to_scales = scale_bytes(c), page_mask = (1 << c.shift) - 1;
-  typename std::conditional<PREFIX, PrefixShare<kRows>, Share<kRows, kStep>>::type share(p, lane, state[warp]);
+  typename std::conditional<PREFIX, PrefixShare<kRows>, Share<kRows, kStep>>::type share(p, warp, lane, mem.state[warp]);
+  if (lane < 2) mem.cut[warp][lane].steps = 0;  // (none)
+  if (threadIdx.x < sizeof(Params) / 4) reinterpret_cast<int*>(&mem.p)[threadIdx.x] = reinterpret_cast<const int*>(&p)[threadIdx.x];
+  static_assert(sizeof(Params) % 4 == 0 && sizeof(Params) / 4 <= kThreads, "a thread a word");
+  __syncthreads();
 
-  Segment& sg = segment[warp];
+  // parts in the workspace, and of the warps from `part` on
+  auto kept_at = [&](int part) { return (PREFIX ? p.pre.base : p.partial) + size_t(part) * (size_t(kRows) * size_t(D + 2)); };
+  auto shared_source = [](const Part<kRows, VI>* part, int n) -> Source {
+    constexpr int kPitch = 64 * VI + 4;
+    static_assert(sizeof(Part<kRows, VI>) % 16 == 0, "parts on 16 bytes");
+    return {part->y[0], part->y[0], int(2 * sizeof(Part<kRows, VI>) / sizeof(float)), n, kPitch, kRows * kPitch, true};
+  };
+
+  Segment& sg = mem.segment[warp];
   while (share.get(sg)) {
     const int rows_all = sg.seq.n * p.group;  // of the sequence (for this key head)
     // keys of this segment that one of its rows sees end here (the last row sees the most)
     int last = min(sg.s1 * kStep, sg.seq.have);
     if constexpr (!PREFIX)
-      last = min(last, limit_of(p.causal, (min(sg.row0 + kRows, rows_all) - 1) / p.group, sg.seq.n, sg.seq.have));
+      last = min(last, limit_of(p.causal, query_of(p, min(sg.row0 + kRows, rows_all) - 1), sg.seq.n, sg.seq.have));
     // and the keys that all of them see end here
-    const int clear = PREFIX ? last : min(last, limit_of(p.causal, sg.row0 / p.group, sg.seq.n, sg.seq.have));
+    const int clear = PREFIX ? last : min(last, limit_of(p.causal, query_of(p, sg.row0), sg.seq.n, sg.seq.have));
 
     // this lane's two rows of each tile as columns of S^T: visible keys
     int lim[NT][2];
@@ -455,10 +551,10 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT)) cached_few_kernel(const 
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int r = sg.row0 + 8 * n + 2 * t + e;
-        lim[n][e] = PREFIX || r >= rows_all ? last : min(last, limit_of(p.causal, r / p.group, sg.seq.n, sg.seq.have));
+        lim[n][e] = PREFIX || r >= rows_all ? last : min(last, limit_of(p.causal, query_of(p, r), sg.seq.n, sg.seq.have));
       }
       const int r = sg.row0 + 8 * n + g;  // Q^T: this lane's column
-      const int i = r / p.group;
+      const int i = query_of(p, r);
       const __half* qr = p.q + static_cast<long long>(sg.seq.q0 + i) * p.qs + (sg.kvh * p.group + r - i * p.group) * D;
 #pragma unroll
       for (int k = 0; k < KI; ++k) {
@@ -487,59 +583,53 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT)) cached_few_kernel(const 
     auto load_k = [&](int key0) {
 #pragma unroll
       for (int u = 0; u < kSub; ++u) {
-        const int at = (key0 + 16 * u) & page_mask;
+        const int at = (key0 + 16 * u) & page_mask, left = last - (key0 + 16 * u);  // (behind the last key nothing is live)
         const long long base = page[u] * c.page_bytes;
         const uint8_t* row = head_at + base + ((at + g) * D + key_run(0, t)) * kEs;
-        const uint8_t* byte = scales_at + base + at;
-        auto load = [&](auto live) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int k = 0; k < KI; ++k) {
-              const uint8_t* from = row + (8 * h * D + key_run(k, 0)) * kEs;
-              if (kWideK && (k & 1)) continue;
-              if (live(g + 8 * h) && (FULL || 4 * k + t < chunks)) {
-                if constexpr (kWideK) load_two(kx[u][h][k], kx[u][h][k + 1 < KI ? k + 1 : 0], from);
-                else kx[u][h][k].template load<FULL>(from);
-              } else {
-                kx[u][h][k].clear();
-                if constexpr (kWideK) kx[u][h][k + 1 < KI ? k + 1 : 0].clear();
-              }
+          for (int k = 0; k < KI; ++k) {
+            const uint8_t* from = row + (8 * h * D + key_run(k, 0)) * kEs;
+            const bool live = g + 8 * h < left && (FULL || 4 * k + t < chunks);
+            if constexpr (kWideK) {
+              if (!(k & 1)) load_two(kx[u][h][k], kx[u][h][k + 1 < KI ? k + 1 : 0], from, live);
+            } else {
+              kx[u][h][k].template load<FULL>(from, live);
             }
-          scale[u] = live(lane & 15) ? __ldg(byte) : kNoScale;
-        };
-        const int left = last - (key0 + 16 * u);
-        if (left >= 16) load([](int) { return true; });
-        else load([&](int key) { return key < left; });
+          }
+        scale[u] = kNoScale;
+        if ((lane & 15) < left) scale[u] = __ldg(scales_at + base + at);
       }
     };
     auto load_v = [&](int key0) {
 #pragma unroll
       for (int u = 0; u < kSub; ++u) {
+        const int left = last - (key0 + 16 * u);
         const uint8_t* row = head_at + page[u] * c.page_bytes + to_values +
                              ((((key0 + 16 * u) & page_mask) + 2 * t) * D + value_run(0, g)) * kEs;
-        auto load = [&](auto live) {
 #pragma unroll
-          for (int h = 0; h < 4; ++h)
+        for (int h = 0; h < 4; ++h)
 #pragma unroll
-            for (int k = 0; k < VI; ++k) {
-              const int key = (h & 1) + 8 * (h >> 1);
-              const uint8_t* from = row + (key * D + value_run(k, 0)) * kEs;
-              if (kWideV && (k & 1)) continue;
-              if (live(2 * t + key) && (FULL || 8 * k + g < chunks)) {
-                if constexpr (kWideV) load_two(vx[u][h][k], vx[u][h][k + 1 < VI ? k + 1 : 0], from);
-                else vx[u][h][k].template load<FULL>(from);
-              } else {
-                vx[u][h][k].clear();
-                if constexpr (kWideV) vx[u][h][k + 1 < VI ? k + 1 : 0].clear();
-              }
+          for (int k = 0; k < VI; ++k) {
+            const int key = (h & 1) + 8 * (h >> 1);
+            const uint8_t* from = row + (key * D + value_run(k, 0)) * kEs;
+            const bool live = 2 * t + key < left && (FULL || 8 * k + g < chunks);
+            if constexpr (kWideV) {
+              if (!(k & 1)) load_two(vx[u][h][k], vx[u][h][k + 1 < VI ? k + 1 : 0], from, live);
+            } else {
+              vx[u][h][k].template load<FULL>(from, live);
             }
-        };
-        const int left = last - (key0 + 16 * u);
-        if (left >= 16) load([](int) { return true; });
-        else load([&](int key) { return key < left; });
+          }
       }
     };
+#pragma unroll
+    for (int u = 0; u < kSub; ++u) {
+#pragma unroll
+      for (int k = 0; k < KI; ++k) kx[u][0][k].clear(), kx[u][1][k].clear();
+#pragma unroll
+      for (int k = 0; k < VI; ++k) vx[u][0][k].clear(), vx[u][1][k].clear(), vx[u][2][k].clear(), vx[u][3][k].clear();
+    }
     float o[NT][4 * VI][4];
     float m[NT][2], l[NT][2];
 #pragma unroll
@@ -550,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT)) cached_few_kernel(const 
       l[n][0] = l[n][1] = 0.0f;
     }
 
-    int key0 = sg.s0 * kStep + 16 * kSub * warp;
+    int key0 = sg.s0 * kStep;
     auto look_up = [&](int key) {
       if ((key >> c.shift) - first_page >= 32) {
         first_page += 32;
@@ -563,231 +653,258 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT)) cached_few_kernel(const 
         page[u] = __shfl_sync(0xffffffffu, n < 32 ? here : there, n & 31);
       }
     };
-    look_up(key0);
-    load_k(key0);
-    load_v(key0);
-    for (; key0 < last; key0 += kStep) {
+    // (the first step's loads and the others' are one piece of code: a short segment waits for its instructions)
+#pragma unroll 1
+    for (key0 -= kStep;; key0 += kStep) {
+      const bool some = key0 >= sg.s0 * kStep, more = key0 + kStep < last;
       float s[kSub][NT][4];
       int byte[kSub];
-#pragma unroll
-      for (int u = 0; u < kSub; ++u) {
-        byte[u] = scale[u];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) s[u][n][0] = s[u][n][1] = s[u][n][2] = s[u][n][3] = 0.0f;
-#pragma unroll
-        for (int k = 0; k < KI; ++k) {
-          uint4 a, b;  // eight dimensions of the keys g and g + 8
-          if constexpr (E4M3) {
-            a = e4m3_to_f16(kx[u][0][k].w);
-            b = e4m3_to_f16(kx[u][1][k].w);
-          } else {
-            a = kx[u][0][k].w;
-            b = kx[u][1][k].w;
-          }
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            mma16816(s[u][n], a.x, b.x, a.y, b.y, q[n][k][0], q[n][k][1]);
-            mma16816(s[u][n], a.z, b.z, a.w, b.w, q[n][k][2], q[n][k][3]);
-          }
-        }
-      }
-      look_up(key0 + kStep);
-      load_k(key0 + kStep);
-      uint32_t b[kSub][NT][2];
-      float up[kSub][2], back[kSub][2];  // of keys g and g + 8: ev, and what a probability counts in the denominator, 2^-ev
-#pragma unroll
-      for (int u = 0; u < kSub; ++u)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int kb = __shfl_sync(0xffffffffu, byte[u], g + 8 * h), vb = __shfl_sync(0xffffffffu, byte[u], 16 + g + 8 * h);
-          // (a marked one counts NaN; 31 keeps the other bits a number)
-          const float unit = max(kb, vb) == kMarked ? __uint_as_float(0x7fc00000u) : power_of(min(kb, 31));
-          up[u][h] = float(min(vb, 31) - kNoScale);
-          back[u][h] = reciprocal_of(min(vb, 31));
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            s[u][n][2 * h] *= unit;
-            s[u][n][2 * h + 1] *= unit;
-          }
-        }
-      if (p.cap > 0.0f) {
-#pragma unroll
-        for (int u = 0; u < kSub; ++u)
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float y = s[u][n][e] * sl2, big = capped(y, p.cap * kLog2e);
-              s[u][n][e] = (p.cap < kFarCap ? big : far_capped(s[u][n][e] * (kLog2e * p.scale), y, big)) + up[u][e >> 1];
-            }
-      } else {
-#pragma unroll
-        for (int u = 0; u < kSub; ++u)
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[u][n][e] = fmaf(s[u][n][e], sl2, up[u][e >> 1]);
-      }
-      if (key0 + 16 * kSub > clear)
-#pragma unroll
-        for (int u = 0; u < kSub; ++u)
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)  // e & 1: the row, e >> 1: keys g, g + 8
-              if (key0 + 16 * u + g + 8 * (e >> 1) >= lim[n][e & 1]) s[u][n][e] = -INFINITY;
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        float f[2];
-        bool raise = false;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float mx = fmaxf(s[0][n][e], s[0][n][e + 2]);
-          if constexpr (kSub == 2) mx = fmax3(mx, s[kSub - 1][n][e], s[kSub - 1][n][e + 2]);
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          const bool higher = mx > m[n][e] + kSlack;
-          const float mn = higher ? mx - kHead : m[n][e];
-          f[e] = higher ? ex2(m[n][e] - mn) : 1.0f;
-          m[n][e] = mn;
-          raise |= higher;
-        }
-        if (__any_sync(0xffffffffu, raise)) {
-#pragma unroll
-          for (int j = 0; j < 4 * VI; ++j) {
-            o[n][j][0] *= f[0];
-            o[n][j][1] *= f[1];
-            o[n][j][2] *= f[0];
-            o[n][j][3] *= f[1];
-          }
-          l[n][0] *= f[0];
-          l[n][1] *= f[1];
-        }
+      if (some) {
 #pragma unroll
         for (int u = 0; u < kSub; ++u) {
+          byte[u] = scale[u];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float ref = m[n][e] == -INFINITY ? 0.0f : m[n][e];
-            s[u][n][e] = ex2(s[u][n][e] - ref);
-            s[u][n][e + 2] = ex2(s[u][n][e + 2] - ref);
-            l[n][e] = fmaf(s[u][n][e], back[u][0], fmaf(s[u][n][e + 2], back[u][1], l[n][e]));
-          }
+          for (int n = 0; n < NT; ++n) s[u][n][0] = s[u][n][1] = s[u][n][2] = s[u][n][3] = 0.0f;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            // (F16, what the products take: 2^-11 of each probability; their sum l is of the unrounded ones)
-            const __half2 w = __floats2half2_rn(s[u][n][2 * h], s[u][n][2 * h + 1]);
-            b[u][n][h] = transpose8x8(*reinterpret_cast<const uint32_t*>(&w));
+          for (int k = 0; k < KI; ++k) {
+            uint4 a, b;  // eight dimensions of the keys g and g + 8
+            if constexpr (E4M3) {
+              a = e4m3_to_f16(kx[u][0][k].w);
+              b = e4m3_to_f16(kx[u][1][k].w);
+            } else {
+              a = kx[u][0][k].w;
+              b = kx[u][1][k].w;
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              mma16816(s[u][n], a.x, b.x, a.y, b.y, q[n][k][0], q[n][k][1]);
+              mma16816(s[u][n], a.z, b.z, a.w, b.w, q[n][k][2], q[n][k][3]);
+            }
           }
         }
       }
+      if (more) {
+        look_up(key0 + kStep);
+        load_k(key0 + kStep);
+      }
+      if (some) {
+        uint32_t b[kSub][NT][2];
+        int vbyte[kSub][2];  // the bytes of values g and g + 8 (31 at most)
 #pragma unroll
-      for (int u = 0; u < kSub; ++u)
+        for (int u = 0; u < kSub; ++u)
 #pragma unroll
-        for (int k = 0; k < VI; ++k) {
-          uint32_t a[4][4];  // [dimensions 2 j and 2 j + 1 of this lane's eight][operand register]
-          if constexpr (E4M3) {
+          for (int h = 0; h < 2; ++h) {
+            const int kb = __shfl_sync(0xffffffffu, byte[u], g + 8 * h), vb = __shfl_sync(0xffffffffu, byte[u], 16 + g + 8 * h);
+            // (a marked one counts NaN)
+            const float unit = max(kb, vb) == kMarked ? __uint_as_float(0x7fc00000u) : power_of(min(kb, 31));
+            vbyte[u][h] = min(vb, 31);
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {  // keys 2 t and 2 t + 1, then 2 t + 8 and 2 t + 9
-              const uint2 w0 = vx[u][2 * hh][k].w, w1 = vx[u][2 * hh + 1][k].w;
-              two_pairs(__byte_perm(w0.x, w1.x, 0x5140), a[0][2 * hh], a[0][2 * hh + 1]);
-              two_pairs(__byte_perm(w0.x, w1.x, 0x7362), a[1][2 * hh], a[1][2 * hh + 1]);
-              two_pairs(__byte_perm(w0.y, w1.y, 0x5140), a[2][2 * hh], a[2][2 * hh + 1]);
-              two_pairs(__byte_perm(w0.y, w1.y, 0x7362), a[3][2 * hh], a[3][2 * hh + 1]);
-            }
-          } else {
-            const uint32_t* v0 = reinterpret_cast<const uint32_t*>(&vx[u][0][k].w);
-            const uint32_t* v1 = reinterpret_cast<const uint32_t*>(&vx[u][1][k].w);
-            const uint32_t* v2 = reinterpret_cast<const uint32_t*>(&vx[u][2][k].w);
-            const uint32_t* v3 = reinterpret_cast<const uint32_t*>(&vx[u][3][k].w);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              a[j][0] = __byte_perm(v0[j], v1[j], 0x5410), a[j][1] = __byte_perm(v0[j], v1[j], 0x7632);
-              a[j][2] = __byte_perm(v2[j], v3[j], 0x5410), a[j][3] = __byte_perm(v2[j], v3[j], 0x7632);
+            for (int n = 0; n < NT; ++n) {
+              s[u][n][2 * h] *= unit;
+              s[u][n][2 * h + 1] *= unit;
             }
           }
+        if (p.cap > 0.0f) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+          for (int u = 0; u < kSub; ++u)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
-              mma16816(o[n][4 * k + j], a[j][0], a[j][1], a[j][2], a[j][3], b[u][n][0], b[u][n][1]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float y = s[u][n][e] * sl2, big = capped(y, p.cap * kLog2e);
+                s[u][n][e] = (p.cap < kFarCap ? big : far_capped(s[u][n][e] * (kLog2e * p.scale), y, big)) +
+                             exponent_of(vbyte[u][e >> 1]);
+              }
+        } else {
+#pragma unroll
+          for (int u = 0; u < kSub; ++u)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) s[u][n][e] = fmaf(s[u][n][e], sl2, exponent_of(vbyte[u][e >> 1]));
         }
+        if (key0 + 16 * kSub > clear)
+#pragma unroll
+          for (int u = 0; u < kSub; ++u)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)  // e & 1: the row, e >> 1: keys g, g + 8
+                if (key0 + 16 * u + g + 8 * (e >> 1) >= lim[n][e & 1]) s[u][n][e] = -INFINITY;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float f[2];
+          bool raise = false;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float mx = fmaxf(s[0][n][e], s[0][n][e + 2]);
+#pragma unroll
+            for (int u = 1; u < kSub; ++u) mx = fmax3(mx, s[u][n][e], s[u][n][e + 2]);
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            const bool higher = mx > m[n][e] + kSlack;
+            const float mn = higher ? mx - kHead : m[n][e];
+            f[e] = higher ? ex2(m[n][e] - mn) : 1.0f;
+            m[n][e] = mn;
+            raise |= higher;
+          }
+          if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+            for (int j = 0; j < 4 * VI; ++j) {
+              o[n][j][0] *= f[0];
+              o[n][j][1] *= f[1];
+              o[n][j][2] *= f[0];
+              o[n][j][3] *= f[1];
+            }
+            l[n][0] *= f[0];
+            l[n][1] *= f[1];
+          }
+#pragma unroll
+          for (int u = 0; u < kSub; ++u) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float ref = m[n][e] == -INFINITY ? 0.0f : m[n][e];
+              s[u][n][e] = ex2(s[u][n][e] - ref);
+              s[u][n][e + 2] = ex2(s[u][n][e + 2] - ref);
+              l[n][e] = fmaf(s[u][n][e], reciprocal_of(vbyte[u][0]), fmaf(s[u][n][e + 2], reciprocal_of(vbyte[u][1]), l[n][e]));
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              // (F16, what the products take: 2^-11 of each probability; their sum l is of the unrounded ones)
+              const __half2 w = __floats2half2_rn(s[u][n][2 * h], s[u][n][2 * h + 1]);
+              b[u][n][h] = transpose8x8(*reinterpret_cast<const uint32_t*>(&w));
+            }
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < kSub; ++u)
+#pragma unroll
+          for (int k = 0; k < VI; ++k) {
+            uint32_t a[4][4];  // [dimensions 2 j and 2 j + 1 of this lane's eight][operand register]
+            if constexpr (E4M3) {
+#pragma unroll
+              for (int hh = 0; hh < 2; ++hh) {  // keys 2 t and 2 t + 1, then 2 t + 8 and 2 t + 9
+                const uint2 w0 = vx[u][2 * hh][k].w, w1 = vx[u][2 * hh + 1][k].w;
+                two_pairs(__byte_perm(w0.x, w1.x, 0x5140), a[0][2 * hh], a[0][2 * hh + 1]);
+                two_pairs(__byte_perm(w0.x, w1.x, 0x7362), a[1][2 * hh], a[1][2 * hh + 1]);
+                two_pairs(__byte_perm(w0.y, w1.y, 0x5140), a[2][2 * hh], a[2][2 * hh + 1]);
+                two_pairs(__byte_perm(w0.y, w1.y, 0x7362), a[3][2 * hh], a[3][2 * hh + 1]);
+              }
+            } else {
+              const uint32_t* v0 = reinterpret_cast<const uint32_t*>(&vx[u][0][k].w);
+              const uint32_t* v1 = reinterpret_cast<const uint32_t*>(&vx[u][1][k].w);
+              const uint32_t* v2 = reinterpret_cast<const uint32_t*>(&vx[u][2][k].w);
+              const uint32_t* v3 = reinterpret_cast<const uint32_t*>(&vx[u][3][k].w);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                a[j][0] = __byte_perm(v0[j], v1[j], 0x5410), a[j][1] = __byte_perm(v0[j], v1[j], 0x7632);
+                a[j][2] = __byte_perm(v2[j], v3[j], 0x5410), a[j][3] = __byte_perm(v2[j], v3[j], 0x7632);
+              }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+                mma16816(o[n][4 * k + j], a[j][0], a[j][1], a[j][2], a[j][3], b[u][n][0], b[u][n][1]);
+          }
+      }
+      if (!more) break;
       load_v(key0 + kStep);
     }
 
-    // the four warps' sums, brought to one exponent
+    // the rows' sums, to shared memory
+    const bool whole = sg.s0 == 0 && sg.s1 == sg.steps;
+    const int rows = min(kRows, rows_all - sg.row0);
+    Part<kRows, VI>& mine = mem.part[warp][sg.s0 == 0 ? 1 : 0];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
+        const int r = 8 * n + 2 * t + e;
         float y = l[n][e];
         y += __shfl_xor_sync(0xffffffffu, y, 4);
         y += __shfl_xor_sync(0xffffffffu, y, 8);
         y += __shfl_xor_sync(0xffffffffu, y, 16);
-        if (g == 0) {
-          red_m[warp][8 * n + 2 * t + e] = m[n][e];
-          red_l[warp][8 * n + 2 * t + e] = y;
-        }
-      }
+        if (g == 0) mine.ml[r] = make_float2(m[n][e], y);
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int j = 0; j < 4 * VI; j += 2)  // four neighbouring dimensions of a row
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          *reinterpret_cast<float4*>(&red[warp][8 * n + 2 * t + e][value_run(j >> 2, g) + 2 * (j & 3)]) =
+        for (int j = 0; j < 4 * VI; j += 2)  // four neighbouring dimensions
+          *reinterpret_cast<float4*>(&mine.y[r][value_run(j >> 2, g) + 2 * (j & 3)]) =
               make_float4(o[n][j][e], o[n][j][e + 2], o[n][j + 1][e], o[n][j + 1][e + 2]);
-    __syncthreads();
-    const int rows = min(kRows, rows_all - sg.row0);
-    auto sums_of = [&](int r) {  // of row r, four columns a lane
-      RowSums a = {make_float4(0.0f, 0.0f, 0.0f, 0.0f), -INFINITY, 0.0f};
-#pragma unroll
-      for (int w = 0; w < 4; ++w)
-        a.add(*reinterpret_cast<const float4*>(&red[w][r][4 * min(lane, 16 * VI - 1)]), red_m[w][r], red_l[w][r]);
-      return a;
-    };
-    auto put_part = [&](float* part, int r, const RowSums& a) {
-      if (lane < c.D / 4) __stcg(reinterpret_cast<float4*>(part + size_t(r) * c.D) + lane, a.y);
-      if (lane == 0) __stcg(reinterpret_cast<float2*>(part + size_t(kRows) * c.D) + r, make_float2(a.m, a.l));
-    };
-    const size_t part_size = size_t(kRows) * size_t(c.D + 2);
-    if constexpr (PREFIX) {
-      float* part = p.pre.base + size_t(sg.item + blockIdx.x) * part_size;
-      for (int r = warp; r < rows; r += 4) put_part(part, r, sums_of(r));
-      __syncthreads();  // the merge buffers are free again
-    } else {
-      if (sg.s0 == 0 && sg.s1 == sg.steps) {
-        for (int r = warp; r < rows; r += 4) finish_row(p, sg, r, lane, sums_of(r));
-        __syncthreads();
-        continue;
       }
-      auto part_of = [&](int cta, int end) { return p.partial + (size_t(cta) * 2 + end) * part_size; };
-      float* mine = part_of(int(blockIdx.x), sg.s0 == 0 ? 1 : 0);
-      for (int r = warp; r < rows; r += 4) put_part(mine, r, sums_of(r));
-      // the last CTA of the item's parts joins them, in order
-      const int c0 = share.cta_of(sg.base), c1 = share.cta_of(sg.base + sg.steps - 1);
+    if (!whole && lane == 0) mem.cut[warp][sg.s0 == 0 ? 1 : 0] = sg;
+    __syncwarp();
+    if (whole) {
+#pragma unroll 1
+      for (int r = 0; r < rows; r += 4)
+        settle(mem.p, sg, shared_source(&mine, 1), r, 1, min(4, rows - r), PREFIX ? kept_at(sg.item + int(blockIdx.x)) : nullptr, kRows);
+      __syncwarp();
+    }
+  }
+
+  // Items that were cut between the warps: the one that the CTA before has begun, and those that go on behind each warp's
+  // share. Then, by the last CTA of an item's parts, those that were cut between CTAs. Every fourth row a warp.
+  static_assert(kRows <= 4 * kWarps, "rows of a warp");
+  __syncthreads();
+  auto cta_of = [&](int step) { return int(unsigned(step) / unsigned(mem.state[warp].chunk * kWarps)); };
+  int open[2] = {-1, -1};  // first warps of the items that are cut at the start and at the end of the CTA's share
+  int stage = 0;           // 0: the CTA's own parts, 1: items cut between CTAs
+#pragma unroll 1
+  for (int x = 0;; ++x) {
+    if (x > kWarps) {  // the CTA's parts are in place
+      if (PREFIX || stage == 1 || (open[0] < 0 && open[1] < 0)) break;
+      stage = 1;
+      x = 0;
       __threadfence();
       __syncthreads();
-      if (threadIdx.x == 0) seen = atomicInc(p.counters + c0, unsigned(c1 - c0));  // 0 .. c1 - c0, then 0 again
-      __syncthreads();
-      if (seen == unsigned(c1 - c0)) {
-        __threadfence();
-        for (int r = warp; r < rows; r += 4) {
-          RowSums a = {make_float4(0.0f, 0.0f, 0.0f, 0.0f), -INFINITY, 0.0f};
-          a.add_parts(c1 - c0 + 1, r, kRows, c.D, lane, [&](int w) { return part_of(c0 + w, w == 0 ? 1 : 0); });
-          finish_row(p, sg, r, lane, a);
-        }
+      if (threadIdx.x < 2 && open[threadIdx.x] >= 0) {
+        const Segment& cut = mem.cut[open[threadIdx.x]][threadIdx.x];
+        const int c0 = cta_of(cut.base), c1 = cta_of(cut.base + cut.steps - 1);
+        mem.seen[threadIdx.x] = atomicInc(p.counters + c0, unsigned(c1 - c0)) == unsigned(c1 - c0);  // then 0 again
       }
-      __syncthreads();  // `seen` and the merge buffers are free again
+      __syncthreads();
     }
+    if (stage == 1 && (x > 1 || open[x] < 0 || !mem.seen[x])) continue;
+    const int w0 = stage == 1 ? open[x] : max(x - 1, 0), slot = x > 0;
+    const Segment& first = mem.cut[w0][slot];
+    if (first.steps == 0) continue;
+    const int rows = min(kRows, first.seq.n * p.group - first.row0), some = (rows - warp + kWarps - 1) / kWarps;
+    Source from;
+    float* put = nullptr;
+    if (stage == 0) {
+      int n = 1, s1 = first.s1;
+      while (s1 < first.steps && w0 + n < kWarps) s1 = mem.cut[w0 + n++][0].s1;
+      from = shared_source(&mem.part[w0][slot], n);
+      if (w0 + 1 < kWarps) from.rest = mem.part[w0 + 1][0].y[0];
+      if (PREFIX) {
+        put = kept_at(first.item + int(blockIdx.x));
+      } else if (first.s0 > 0 || s1 < first.steps) {
+        const int end = first.s0 == 0;
+        open[end] = w0;
+        put = kept_at(2 * int(blockIdx.x) + end);
+      }
+    } else {
+      __threadfence();
+      const int c0 = cta_of(first.base), c1 = cta_of(first.base + first.steps - 1);
+      from = {kept_at(2 * c0 + 1), kept_at(2 * c0 + 2), 2 * kRows * (D + 2), c1 - c0 + 1, D, kRows * D, false};
+    }
+    settle(mem.p, first, from, warp, kWarps, some, put, kRows);
   }
 }
 
+template <int KI, int VI, bool FULL, int NT, bool E4M3, bool PREFIX>
+cudaError_t few_launch_type(const Params& p, int grid, cudaStream_t s) {
+  auto kern = cached_few_kernel<KI, VI, FULL, NT, E4M3, PREFIX>;
+  constexpr int kBytes = int(sizeof(FewShared<8 * NT, VI>));
+  static unsigned long long set = 0;
+  const cudaError_t e = allow_shared(kern, kBytes, &set);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3(unsigned(grid)), dim3(kThreads), size_t(kBytes), s, p);
+}
 template <int KI, int VI, bool FULL, int NT, bool PREFIX>
 cudaError_t few_launch_as(const Params& p, int grid, cudaStream_t s) {
-  return launch_pdl(p.c.e4m3 ? cached_few_kernel<KI, VI, FULL, NT, true, PREFIX>
-                             : cached_few_kernel<KI, VI, FULL, NT, false, PREFIX>,
-                    dim3(unsigned(grid)), dim3(kThreads), 0, s, p);
+  return p.c.e4m3 ? few_launch_type<KI, VI, FULL, NT, true, PREFIX>(p, grid, s)
+                  : few_launch_type<KI, VI, FULL, NT, false, PREFIX>(p, grid, s);
 }
 
 template <int NT, bool PREFIX>
@@ -802,9 +919,10 @@ cudaError_t few_launch(const Params& p, int grid, cudaStream_t s) {
 // What the host alone decides of a call.
 struct Plan {
   int nt, grid;          // the sequences' pass: 8-row tiles of an item, CTAs at most
-  int pre_nt, pre_grid;  // the prefix's
+  int pre_nt, pre_grid;  // the prefix's (pre_nt 0: tiles of 128 rows, cached_prefix.cu)
   PrefixParts pre;       // (its base is an offset in floats)
   size_t bytes;          // workspace
+  bool too_much;         // steps of the prefix pass
 };
 Plan plan_of(const View& c, int total_q, int group, int sms) {
   Plan r = {};
@@ -814,16 +932,24 @@ Plan plan_of(const View& c, int total_q, int group, int sms) {
   const size_t own = size_t(kMaxSms * per_sm(r.nt)) * 2 * size_t(8 * r.nt) * size_t(c.D + 2);
   r.bytes = kCounterBytes + own * sizeof(float);
   if (c.prefix_len > 0) {
-    r.pre_nt = rows <= 8 ? 1 : 2;
+    r.pre_nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 0;
+    int step = 16 * groups_of(c.e4m3, c.D), most = sms * per_sm(r.pre_nt), at_most = kMaxSms * per_sm(r.pre_nt);
+    int parts = kWarps;  // of a CTA's share: a whole number of steps each
     r.pre.rows = 8 * r.pre_nt;
+    if (r.pre_nt == 0) {
+      r.pre.rows = rows <= kPrefixTile ? kPrefixTile : 2 * kPrefixTile;
+      step = rows <= kPrefixTile ? 2 * kPrefixTile : kPrefixTile;
+      most = sms;
+      at_most = kMaxSms;
+      parts = 1;
+    }
     r.pre.blocks = int((rows + r.pre.rows - 1) / r.pre.rows);
-    const int step = step_keys(c.e4m3);
     r.pre.steps = (c.prefix_len + step - 1) / step;
     const long long items = static_cast<long long>(r.pre.blocks) * c.hk, work = items * r.pre.steps;
-    const int most = sms * per_sm(r.pre_nt);
-    r.pre.chunk = (work + most - 1) / most;
+    r.pre.chunk = int((work + static_cast<long long>(most) * parts - 1) / (static_cast<long long>(most) * parts) * parts);
+    r.too_much = work >= (1ll << 30);
     r.pre_grid = int((work + r.pre.chunk - 1) / r.pre.chunk);
-    r.bytes += size_t(items + kMaxSms * per_sm(r.pre_nt)) * size_t(r.pre.rows) * size_t(c.D + 2) * sizeof(float);
+    r.bytes += size_t(items + at_most) * size_t(r.pre.rows) * size_t(c.D + 2) * sizeof(float);
   }
   return r;
 }
@@ -841,6 +967,14 @@ sv_status check(const char* fn, const sv_cache* cache, const sv_cache_batch* bat
       static_cast<long long>(total_q) * q_heads > kMostRows) {
     set_error("%s: heads %d over %d, %d sequences or %d queries are too many for one call", fn, q_heads, c->hk, c->count,
               total_q);
+    return SV_ERR_UNSUPPORTED;
+  }
+  // (steps of 16 keys and blocks of 8 rows at least are counted in 32 bits)
+  const long long own = ((static_cast<long long>(total_q) * (q_heads / c->hk)) / 8 + c->count) * c->hk *
+                        ((static_cast<long long>(c->stride) << c->shift) / 16 + 1);
+  if (own >= (1ll << 31) - (1 << 20) || plan_of(*c, total_q, q_heads / c->hk, 1).too_much) {
+    set_error("%s: %d queries of %d heads over a prefix of %d and %d pages of %d are too many for one call", fn, total_q, q_heads,
+              c->prefix_len, c->stride, 1 << c->shift);
     return SV_ERR_UNSUPPORTED;
   }
   return SV_OK;
@@ -914,6 +1048,7 @@ sv_status sv_attention_cached(const sv_cache* cache, const sv_cache_batch* batch
   p.total_q = total_q;
   p.hq = q_heads;
   p.group = q_heads / p.c.hk;
+  p.per_group = unsigned((0xffffffffull + unsigned(p.group)) / unsigned(p.group));
   p.scale = opt.scale > 0.0f ? opt.scale : 1.0f / std::sqrt(float(p.c.D));
   p.cap = opt.softcap;
   p.causal = opt.mask == SV_MASK_PREFIX;
@@ -927,7 +1062,12 @@ sv_status sv_attention_cached(const sv_cache* cache, const sv_cache_batch* batch
   cudaError_t e = cudaSuccess;
   if (p.c.prefix_len > 0) {
     LaunchScope L(kKindAttn, 0.0, 0.0, s);
-    e = plan.pre_nt == 1 ? few_launch<1, true>(p, plan.pre_grid, s) : few_launch<2, true>(p, plan.pre_grid, s);
+    if (plan.pre_nt == 0) {
+      st = prefix_launch(fn, p, plan.pre_grid, s);
+      if (st != SV_OK) return st;
+    } else {
+      e = plan.pre_nt == 1 ? few_launch<1, true>(p, plan.pre_grid, s) : few_launch<2, true>(p, plan.pre_grid, s);
+    }
   }
   if (e == cudaSuccess) {
     LaunchScope L(kKindAttn, 0.0, 0.0, s);

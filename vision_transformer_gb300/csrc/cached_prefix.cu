@@ -1,0 +1,593 @@
+// The prefix pass of sv_attention_cached for many rows: all rows of the batch over the keys that its sequences share, on
+// the tensor cores, scores never leaving the SM.
+//
+// A row is a query and one of the query heads of a key head (row = query x group + head); every row sees every key of
+// the prefix, so that nothing but the last tile's end is masked. For each row, in F32,
+//   s_j = scale q . k_j, capped;  O = sum_j 2^(s_j log2 e - m) v_j,  l = sum_j 2^(s_j log2 e - m),
+// m following the running maximum, go to the workspace, a part for each CTA that has worked on the row's item
+// (PrefixParts); cached_attention.cu adds them to what the row's own tokens give.
+//
+// A CTA (one per SM) has two tiles of 128 rows, or, with at most 128 rows in the batch (SOLO), one whose key tiles two
+// groups take in turn. 14 warps:
+//   warps 0..3, 4..7   softmax of group 0 and 1: a thread per row turns its S row into P (F16, over S in tensor memory);
+//   warp 8             the MMA issuer: S_w = Q_w K^T (shared memory, 128-byte swizzle), O_w += P_w V (P from tensor memory);
+//   warp 9             copies keys and values in turn, with their scale bytes, page by page (a lane each): E4M3 codes as
+//                      they lie into a ring of their own, F16 numbers by TMA into the operands' ring;
+//   warps 10..13       Q, and the operands: codes in F16 with their factors applied (exactly, as sv_cache_read does); a
+//                      marked head becomes NaN, and with it every row; keys behind the prefix's end become zeros.
+// Tensor memory: S_0, S_1, O_0, O_1 of 128 columns each. A row's 128 scores do not fit the 128 registers that 14 warps
+// leave a thread: the upper half is read from tensor memory twice, for the maximum and for the exponentials.
+#include "cached.h"
+#include "packed_attention.h"
+
+namespace sv {
+namespace cached {
+namespace {
+
+using packed::capped4;
+using packed::cap_factor;
+using packed::far_capped;
+using packed::kFarCap;
+using packed::kHead;
+using packed::kLog2e;
+using packed::kSlack;
+
+constexpr int kTile = kPrefixTile;
+constexpr int kBoxBytes = kTile * 128;  // 128 rows of 64 values
+constexpr int kThreads = 448;
+constexpr int kLoaders = 128;           // threads of warps 10..13
+constexpr uint32_t kTmemCols = 512;
+
+template <int NB, bool E4M3>
+struct Smem {
+  static constexpr int kOp = NB * kBoxBytes;  // one operand tile
+  static constexpr int kStages = E4M3 ? (NB == 1 ? 6 : 3) : (NB == 1 ? 8 : 4);
+  static constexpr int kRaws = E4M3 ? 4 : kStages;              // tiles of codes; F16: of scale bytes alone
+  static constexpr int kRaw = E4M3 ? kTile * 64 * NB : 0;
+  static constexpr int kOffRing = 2 * kOp;                      // behind Q
+  static constexpr int kOffRaw = kOffRing + kStages * kOp;
+  static constexpr int kOffScales = kOffRaw + kRaws * kRaw;     // scale bytes of each tile
+  static constexpr int kOffBar = kOffScales + kRaws * kTile;
+  static constexpr int kOffJoin = kOp;  // SOLO: exponents and sums of both groups' rows, in place of a second tile of Q
+  static constexpr int kBytes = 1024 + kOffBar + 384;
+  static_assert(kBytes <= 232448, "shared memory budget");
+};
+
+enum {
+  kBarFull = 0,    // +stage: the operand tile is written
+  kBarEmpty = 8,   // +stage: products that read it have finished
+  kBarRaw = 16,    // +tile of the copies' ring: it has arrived
+  kBarRawFree = 24,
+  kBarQFull = 32,
+  kBarQEmpty = 33,
+  kBarSFull = 34,  // +group: S_w has finished (and with it the P V products before it)
+  kBarPFull = 36,  // +group: P_w (and any O rescale) is in tensor memory
+  kBarOFull = 38,  // +group: the segment's last P V product has finished
+  kBarJoin = 40,   // SOLO: both groups' exponents and sums are in shared memory
+  kBarRead = 41,   // SOLO: both have read O
+  kBarDrain = 42,
+  kNumBars = 43
+};
+
+// A run of steps of one item that falls into this CTA's share.
+struct Run {
+  int item, s0, s1, kvh, block;
+};
+struct Runs {
+  int at, end;
+  __device__ __forceinline__ Runs(const Params& p) {
+    const int work = p.pre.blocks * p.c.hk * p.pre.steps;
+    at = p.pre.chunk * int(blockIdx.x);
+    end = min(at + p.pre.chunk, work);
+  }
+  __device__ __forceinline__ bool get(const Params& p, Run& r) {
+    if (at >= end) return false;
+    r.item = at / p.pre.steps;
+    const int base = r.item * p.pre.steps;
+    r.s0 = at - base;
+    r.s1 = min(end - base, p.pre.steps);
+    r.kvh = r.item / p.pre.blocks;
+    r.block = r.item - r.kvh * p.pre.blocks;
+    at = base + r.s1;
+    return true;
+  }
+};
+
+// `bytes` (a multiple of 16, both addresses on 16) from global to shared memory, counted on an mbarrier.
+__device__ __forceinline__ void bulk_load(uint32_t to, const void* from, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to), "l"(from),
+               "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+// 16-byte chunk of row `row` of an operand tile (64 values a box, 128-byte swizzle).
+__device__ __forceinline__ uint32_t chunk_at(int row, int chunk) {
+  return uint32_t((chunk >> 3) * kBoxBytes + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
+}
+
+// pages: F16 pages as a tensor of [n_pages, 2 * kv_heads * page_size (keys, then values), head_dim].
+template <int NB, bool E4M3, bool SOLO, bool CAP>
+__global__ void __launch_bounds__(kThreads, 1)
+    cached_prefix_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap pages_map) {
+  using L = Smem<NB, E4M3>;
+  constexpr int kOp = L::kOp, kStages = L::kStages, kRaws = L::kRaws;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bar0 = sbase + L::kOffBar;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffBar + 8 * kNumBars);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  static_assert(8 * kNumBars + 8 <= 384, "barrier area");
+  auto bar = [&](int i) { return bar0 + 8u * uint32_t(i); };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const View& c = p.c;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(bar(kBarFull + s), kLoaders);
+      mbar_init(bar(kBarEmpty + s), 1);
+    }
+    for (int s = 0; s < kRaws; ++s) {
+      mbar_init(bar(kBarRaw + s), 1);
+      mbar_init(bar(kBarRawFree + s), kLoaders / 32);
+    }
+    mbar_init(bar(kBarQFull), kLoaders);
+    mbar_init(bar(kBarQEmpty), 1);
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(bar(kBarSFull + w), 1);
+      mbar_init(bar(kBarPFull + w), 128);
+      mbar_init(bar(kBarOFull + w), 1);
+    }
+    mbar_init(bar(kBarJoin), 256);
+    mbar_init(bar(kBarRead), 256);
+    mbar_init(bar(kBarDrain), 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish();
+  }
+  // Dimensions between D and the next multiple of 16 are read by the products and never written: zeros for good.
+  if (c.D % 16)
+    for (int x = int(threadIdx.x); x < (2 + kStages) * kTile; x += kThreads)
+      *reinterpret_cast<uint4*>(smem + x / kTile * kOp + chunk_at(x % kTile, c.D / 8)) = make_uint4(0u, 0u, 0u, 0u);
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int rows_all = p.total_q * p.group;  // (below 2^26)
+  auto wait = [&](int b, uint32_t parity) { return mbar_wait(bar(b), parity, abort_flag, p.c.err); };
+  auto wait_all = [&](int b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)) != 0; };
+
+  Runs runs(p);
+  Run run = {};
+  // Operand tile x of a run of `count` tiles from jb on: keys, values, keys, ... of one tile after another; SOLO: the keys
+  // of two tiles, their values, ...
+  auto is_values = [](int x) { return ((SOLO ? x >> 1 : x) & 1) != 0; };
+  auto tile_of = [](int x) { return SOLO ? (x >> 2) * 2 + (x & 1) : x >> 1; };
+  if (warp == 9) {
+    const int page_mask = (1 << c.shift) - 1, run_rows = min(kTile, page_mask + 1);
+    // The pages of a tile's keys, a lane each (8 at most; runs of run_rows keys).
+    auto pages_of = [&](int tile) -> int {
+      const int number = ((tile * kTile) >> c.shift) + lane;
+      if (lane >= kTile / run_rows || number >= (c.prefix_len + page_mask) >> c.shift) return -1;
+      const int page = __ldg(c.prefix_pages + number);
+      if (unsigned(page) < unsigned(c.n_pages)) return page;
+      atomicOr(c.err, kDevErrCache);
+      return 0;
+    };
+    if (!E4M3 && lane == 0) prefetch_tmap(&pages_map);
+    uint32_t issued = 0, issued_phase = 0;  // copies in flight per tile of the ring, and their phase bits
+    int use = 0;
+    bool ok = true;
+    while (ok && runs.get(p, run)) {
+      const int jb = SOLO ? 2 * run.s0 : run.s0, count = 2 * (run.s1 - run.s0) * (SOLO ? 2 : 1);
+      int page = pages_of(jb);
+      for (int x = 0; x < count; ++x, ++use) {
+        const int tile = jb + tile_of(x);
+        const int next = x + 1 < count ? pages_of(jb + tile_of(x + 1)) : -1;
+        const int slot = use % kRaws;
+        if (!(ok = wait_all((E4M3 ? kBarRawFree : kBarEmpty) + slot, ((use / kRaws) & 1) ^ 1))) break;
+        const int copies = __popc(__ballot_sync(0xffffffffu, page >= 0));
+        const uint32_t full = bar(kBarRaw + slot);
+        if (lane == 0) mbar_arrive_expect_tx(full, uint32_t(copies * run_rows * (1 + (E4M3 ? c.D : NB * 128))));
+        issued |= 1u << slot;
+        issued_phase = (issued_phase & ~(1u << slot)) | uint32_t((use / kRaws) & 1) << slot;
+        __syncwarp();
+        if (page >= 0) {
+          const int at = (tile * kTile) & page_mask, row = ((run.kvh + (is_values(x) ? c.hk : 0)) << c.shift) + at;
+          const uint8_t* from = c.pages + page * c.page_bytes;
+          bulk_load(sbase + L::kOffScales + slot * kTile + lane * run_rows, from + scale_bytes(c) + row, uint32_t(run_rows), full);
+          if constexpr (E4M3) {
+            bulk_load(sbase + L::kOffRaw + slot * L::kRaw + lane * run_rows * c.D, from + row * c.D, uint32_t(run_rows * c.D), full);
+          } else {
+            for (int b = 0; b < NB; ++b)
+              tma_load_3d(sbase + L::kOffRing + slot * kOp + b * kBoxBytes + lane * run_rows * 128, &pages_map, full, 64 * b, row, page);
+          }
+        }
+        page = next;
+      }
+    }
+    // (after a time-out: every copy issued lands before the CTA can exit)
+    for (int i = 0; i < kRaws; ++i)
+      if (issued & (1u << i)) mbar_wait_bounded(bar(kBarRaw + i), (issued_phase >> i) & 1, p.c.err);
+  } else if (warp >= 10) {
+    const int tid = int(threadIdx.x) - 10 * 32;
+    const int per_row = c.D / 8;  // 16-byte chunks of a row
+    const int row_step = kLoaders / per_row, chunk_step = kLoaders % per_row;
+    int use = 0;  // operand tiles so far
+    bool ok = true;
+    for (int n = 0; ok && runs.get(p, run); ++n) {
+      const int jb = SOLO ? 2 * run.s0 : run.s0, count = 2 * (run.s1 - run.s0) * (SOLO ? 2 : 1);
+      if (!(ok = wait_all(kBarQEmpty, (n & 1) ^ 1))) break;
+#pragma unroll 1
+      for (int w = 0; w < (SOLO ? 1 : 2); ++w) {
+        int row = tid / per_row, chunk = tid % per_row;
+#pragma unroll 8
+        for (int i = 0; i < per_row; ++i) {
+          const int r = run.block * p.pre.rows + w * kTile + row;
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (r < rows_all) {
+            const int q = query_of(p, r);
+            v = __ldg(reinterpret_cast<const uint4*>(p.q + q * p.qs + (run.kvh * p.group + (r - q * p.group)) * c.D) + chunk);
+          }
+          *reinterpret_cast<uint4*>(smem + w * kOp + chunk_at(row, chunk)) = v;
+          row += row_step;
+          chunk += chunk_step;
+          if (chunk >= per_row) chunk -= per_row, ++row;
+        }
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(bar(kBarQFull));
+#pragma unroll 1
+      for (int x = 0; x < count; ++x, ++use) {
+        const int slot = use % kRaws, st = use % kStages;
+        const int left = c.prefix_len - (jb + tile_of(x)) * kTile;  // keys of the tile
+        if (!(ok = wait_all(kBarRaw + slot, (use / kRaws) & 1))) break;
+        const uint8_t* scales = smem + L::kOffScales + slot * kTile;
+        uint8_t* to = smem + L::kOffRing + st * kOp;
+        if constexpr (E4M3) {
+          if (!(ok = wait_all(kBarEmpty + st, ((use / kStages) & 1) ^ 1))) break;
+          const uint2* raw = reinterpret_cast<const uint2*>(smem + L::kOffRaw + slot * L::kRaw) + tid;
+          int row = tid / per_row, chunk = tid % per_row;
+#pragma unroll 4
+          for (int i = 0; i < per_row; ++i) {
+            const int b = scales[row];
+            uint4 y = e4m3_to_f16(raw[i * kLoaders]);
+            const __half2 f = f16_power(min(b, 31) - kNoScale);
+            __half2* h = reinterpret_cast<__half2*>(&y);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) h[e] = __hmul2(h[e], f);
+            if (b == kMarked) y = make_uint4(0x7e007e00u, 0x7e007e00u, 0x7e007e00u, 0x7e007e00u);
+            if (row >= left) y = make_uint4(0u, 0u, 0u, 0u);
+            *reinterpret_cast<uint4*>(to + chunk_at(row, chunk)) = y;
+            row += row_step;
+            chunk += chunk_step;
+            if (chunk >= per_row) chunk -= per_row, ++row;
+          }
+        } else if (tid >= left || scales[tid] == kMarked) {
+          const uint32_t y = tid >= left ? 0u : 0x7e007e00u;
+          for (int i = 0; i < per_row; ++i) *reinterpret_cast<uint4*>(to + chunk_at(tid, i)) = make_uint4(y, y, y, y);
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(bar(kBarFull + st));
+        if constexpr (E4M3) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBarRawFree + slot));
+        }
+      }
+    }
+  } else if (warp == 8) {
+    constexpr uint32_t idesc_s = make_idesc(128, 128, 0, false);
+    const uint32_t idesc_o = make_idesc(128, (c.D + 15) / 16 * 16, 0, true);
+    const int steps = (c.D + 15) / 16;
+    const uint32_t lead = elect_one();
+    auto commit = [&](int b) { tc_commit_if(lead, bar(b)); };
+    int use = 0;  // operand tiles that earlier runs have used
+    auto full = [&](int ahead) {
+      const int u = use + ahead;
+      const bool got = wait_all(kBarFull + u % kStages, (u / kStages) & 1);
+      tc_fence_after();
+      return got;
+    };
+    auto issue_s = [&](int w, int ahead) {
+      const uint64_t qd = make_sdesc(sbase + uint32_t(SOLO ? 0 : w) * kOp, 16, 1024, 2);
+      const uint64_t kd = make_sdesc(sbase + L::kOffRing + uint32_t((use + ahead) % kStages) * kOp, 16, 1024, 2);
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)  // 32 bytes of each row a step
+          if (4 * b + kk < steps)
+            mma_f16_if(lead, tmem + uint32_t(128 * w), qd + uint64_t(b * (kBoxBytes >> 4) + 2 * kk),
+                       kd + uint64_t(b * (kBoxBytes >> 4) + 2 * kk), idesc_s, b + kk > 0);
+      commit(kBarSFull + w);
+    };
+    auto issue_pv = [&](int w, int ahead, uint32_t keep) {
+      const uint64_t vd = make_sdesc(sbase + L::kOffRing + uint32_t((use + ahead) % kStages) * kOp, kBoxBytes, 1024, 2);
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk)  // 16 keys a step: 8 columns of P, 16 rows of V
+        mma_f16_ts_if(lead, tmem + uint32_t(256 + 128 * w), tmem + uint32_t(128 * w + 8 * kk),
+                      vd + uint64_t(kk * (2048 >> 4)), idesc_o, kk > 0 ? 1u : keep);
+    };
+    auto empty = [&](int ahead) { commit(kBarEmpty + (use + ahead) % kStages); };
+    uint32_t tt = 0;  // parity of the groups' tiles
+    bool ok = true;
+    for (int n = 0; ok && runs.get(p, run); ++n) {
+      const int count = run.s1 - run.s0;
+      if (!(ok = wait_all(kBarQFull, n & 1))) break;
+      if constexpr (SOLO) {
+        for (int w = 0; w < 2 && ok; ++w) {
+          if (!(ok = full(w))) break;
+          issue_s(w, w);
+          empty(w);
+        }
+        if (count == 1) commit(kBarQEmpty);
+        for (int j = 0; ok && j < count; ++j, tt ^= 1, use += 4) {
+          const bool last = j + 1 == count;
+          for (int w = 0; w < 2 && ok; ++w) {
+            if (!(ok = full(2 + w) && wait_all(kBarPFull + w, tt))) break;
+            tc_fence_after();
+            issue_pv(w, 2 + w, j > 0);
+            empty(2 + w);
+            if (last) {
+              commit(kBarOFull + w);
+            } else {
+              if (!(ok = full(4 + w))) break;
+              issue_s(w, 4 + w);
+              empty(4 + w);
+              if (w == 1 && j + 2 == count) commit(kBarQEmpty);
+            }
+          }
+        }
+      } else {
+        if (!(ok = full(0))) break;
+        issue_s(0, 0);
+        issue_s(1, 0);
+        empty(0);
+        if (count == 1) commit(kBarQEmpty);
+        for (int j = 0; ok && j < count; ++j, tt ^= 1, use += 2) {
+          const bool last = j + 1 == count;
+          if (!(ok = full(1) && (last || full(2)))) break;
+          for (int w = 0; w < 2 && ok; ++w) {
+            if (!(ok = wait_all(kBarPFull + w, tt))) break;
+            tc_fence_after();
+            issue_pv(w, 1, j > 0);
+            if (last) commit(kBarOFull + w);
+            else issue_s(w, 2);
+          }
+          if (!ok) break;
+          empty(1);
+          if (!last) empty(2);
+          if (j + 2 == count) commit(kBarQEmpty);
+        }
+      }
+    }
+    commit(kBarDrain);
+    __syncwarp();
+    mbar_wait_bounded(bar(kBarDrain), 0, p.c.err);
+  } else {
+    const int w = warp >> 2;             // group
+    const int r = (warp & 3) * 32 + lane;  // row of the tile == lane of tensor memory
+    const uint32_t lane_off = uint32_t((warp & 3) * 32) << 16;
+    const uint32_t s_tm = tmem + uint32_t(w * 128) + lane_off;
+    const uint32_t o_tm = tmem + uint32_t(256) + lane_off;  // of group 0
+    const int Dn = (c.D + 15) / 16 * 16;
+    const float sl2 = CAP ? cap_factor(p.scale, p.cap) : kLog2e * p.scale;
+    const float on = CAP ? 1.0f : sl2;  // factor on the (capped) scores before the exponentials
+    const float cap2 = p.cap * kLog2e;
+    float2* join = reinterpret_cast<float2*>(smem + L::kOffJoin);
+    bool ok = true;
+    uint32_t t = 0;  // parity of the tiles so far
+    for (int n = 0; ok && runs.get(p, run); ++n) {
+      const int j0 = SOLO ? 2 * run.s0 + w : run.s0, je = SOLO ? 2 * run.s1 : run.s1;
+      float m = -INFINITY, l = 0.0f;
+      for (int j = j0; j < je; j += SOLO ? 2 : 1, t ^= 1) {
+        if (!(ok = wait_all(kBarSFull + w, t))) break;
+        tc_fence_after();
+        const int valid = c.prefix_len - j * kTile;  // keys of the tile
+        // (scores stay the words that tensor memory gives: the compiler may order accesses of two types as it likes)
+        auto prepare = [&](uint32_t* s, int first) {  // 32 scores from column `first` on: capped, hidden ones -inf
+          if constexpr (CAP) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              float big[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) big[k] = __uint_as_float(s[e + k]);
+              capped4(big, sl2, cap2);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float x = __uint_as_float(s[e + k]);
+                s[e + k] = __float_as_uint(p.cap < kFarCap ? big[k] : far_capped(x * (kLog2e * p.scale), x * sl2, big[k]));
+              }
+            }
+          }
+          if (valid < first + 32) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (first + e >= valid) s[e] = 0xff800000u;
+          }
+        };
+        auto top_of = [&](const uint32_t* s, float mx) {
+          auto f = [&](int e) { return __uint_as_float(s[e]); };
+          float a = fmax3(mx, f(0), f(1)), b = fmaxf(f(2), f(3));
+#pragma unroll
+          for (int e = 4; e < 32; e += 4) {
+            a = fmax3(a, f(e), f(e + 1));
+            b = fmax3(b, f(e + 2), f(e + 3));
+          }
+          return fmaxf(a, b);
+        };
+        uint32_t ua[2][32], ub[32];
+        float mx = -INFINITY;
+        tmem_ld32(s_tm + 64, ub);
+        tmem_ld32(s_tm, ua[0]);
+        tmem_ld_wait(ub);
+        reg_fence(ua[0]);
+        prepare(ub, 64);
+        mx = top_of(ub, mx);
+        tmem_ld32(s_tm + 96, ub);
+        tmem_ld32(s_tm + 32, ua[1]);
+        prepare(ua[0], 0);
+        mx = top_of(ua[0], mx);
+        tmem_ld_wait(ub);
+        reg_fence(ua[1]);
+        prepare(ub, 96);
+        mx = top_of(ub, mx);
+        prepare(ua[1], 32);
+        mx = top_of(ua[1], mx);
+        mx *= on;
+        const bool raise = mx > m + kSlack;
+        const float m_new = raise ? mx - kHead : m;
+        if (j > j0 && __any_sync(0xffffffffu, raise)) {
+          const float f = raise ? ex2(m - m_new) : 1.0f;
+          l *= f;
+#pragma unroll 1
+          for (int d = 0; d < Dn; d += 8) {
+            uint32_t e[8];
+            tmem_ld8(o_tm + uint32_t(128 * w + d), e);
+            tmem_ld_wait();
+            asm volatile("" : "+r"(e[0]), "+r"(e[1]), "+r"(e[2]), "+r"(e[3]), "+r"(e[4]), "+r"(e[5]), "+r"(e[6]), "+r"(e[7]));
+#pragma unroll
+            for (int k = 0; k < 8; ++k) e[k] = __float_as_uint(__uint_as_float(e[k]) * f);
+            tmem_st8(o_tm + uint32_t(128 * w + d), e);
+          }
+        }
+        m = m_new;
+        const float ref = m == -INFINITY ? 0.0f : m;
+        float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
+        auto exponentials = [&](const uint32_t* s, uint32_t* pk) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float x0, x1;
+            fma_x2(x0, x1, __uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]), on, on, -ref, -ref);
+            x0 = ex2(x0);
+            x1 = ex2(x1);
+            if (e & 1) add_x2(s2, s3, s2, s3, x0, x1);
+            else add_x2(s0, s1, s0, s1, x0, x1);
+            // F16, what the products take at full rate: 2^-11 of each probability; their sum l is of the unrounded ones
+            const __half2 y = __floats2half2_rn(x0, x1);
+            pk[e] = *reinterpret_cast<const uint32_t*>(&y);
+          }
+        };
+        uint32_t pk[32];
+        exponentials(ua[0], pk);
+        tmem_ld32(s_tm + 64, ub);
+        exponentials(ua[1], pk + 16);
+        tmem_st32(s_tm, pk);  // (over columns 0 .. 31: scores that are in registers)
+        tmem_ld32(s_tm + 96, ua[0]);
+        tmem_ld_wait(ub);
+        reg_fence(ua[0]);
+        prepare(ub, 64);
+        exponentials(ub, pk);
+        prepare(ua[0], 96);
+        exponentials(ua[0], pk + 16);
+        tmem_st32(s_tm + 32, pk);
+        l += (s0 + s1) + (s2 + s3);
+        tmem_st_wait();
+        if (SOLO && n > 0 && j == j0) {  // both groups have read what the next P V overwrites
+          if (!(ok = wait_all(kBarRead, (n - 1) & 1))) break;
+        }
+        tc_fence_before();
+        mbar_arrive(bar(kBarPFull + w));
+      }
+      if (!ok) break;
+      // the run's sums: a part of the row's result
+      const int row = run.block * p.pre.rows + (SOLO ? 0 : w * kTile) + r;  // among all rows
+      const int at = (SOLO ? 0 : w * kTile) + r;                             // in the part
+      float* part = p.pre.base + size_t(run.item + int(blockIdx.x)) * (size_t(p.pre.rows) * size_t(c.D + 2));
+      float f0 = 1.0f, f1 = 0.0f;
+      if constexpr (SOLO) {
+        join[w * kTile + r] = make_float2(m, l);
+        mbar_arrive(bar(kBarJoin));
+        if (!(ok = wait_all(kBarJoin, n & 1) && wait_all(kBarOFull, n & 1) && wait_all(kBarOFull + 1, n & 1))) break;
+        const float2 a = join[r], b = join[kTile + r];
+        m = fmaxf(a.x, b.x);
+        const float ref = m == -INFINITY ? 0.0f : m;
+        f0 = ex2(a.x - ref);
+        f1 = ex2(b.x - ref);
+        l = fmaf(f1, b.y, f0 * a.y);
+      } else {
+        if (!(ok = wait_all(kBarOFull + w, n & 1))) break;
+      }
+      tc_fence_after();
+      const bool live = row < rows_all;
+      if (live && (!SOLO || w == 0))
+        __stcg(reinterpret_cast<float2*>(part + size_t(p.pre.rows) * c.D) + at, make_float2(m, l));
+      // SOLO: each group writes every second run of 16 columns
+#pragma unroll 1
+      for (int d = SOLO ? 16 * w : 0; d < Dn; d += SOLO ? 32 : 16) {
+        uint32_t a[16], b[16];
+        tmem_ld16(o_tm + uint32_t((SOLO ? 0 : 128 * w) + d), a);
+        if constexpr (SOLO) tmem_ld16(o_tm + uint32_t(128 + d), b);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          asm volatile("" : "+r"(a[e]));  // no use before the wait
+          if constexpr (SOLO) {
+            asm volatile("" : "+r"(b[e]));
+            a[e] = __float_as_uint(fmaf(f1, __uint_as_float(b[e]), f0 * __uint_as_float(a[e])));
+          }
+        }
+        if (live)
+#pragma unroll
+          for (int e = 0; e < 16; e += 4)
+            if (d + e < c.D)
+              __stcg(reinterpret_cast<uint4*>(part + size_t(at) * c.D + d + e), make_uint4(a[e], a[e + 1], a[e + 2], a[e + 3]));
+      }
+      if constexpr (SOLO) {
+        tc_fence_before();
+        mbar_arrive(bar(kBarRead));
+      }
+    }
+    tmem_ld_wait();
+    tmem_st_wait();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int NB, bool E4M3, bool SOLO, bool CAP>
+cudaError_t launch_as(const Params& p, const CUtensorMap& pages, int grid, cudaStream_t s) {
+  auto kern = cached_prefix_kernel<NB, E4M3, SOLO, CAP>;
+  static unsigned long long set = 0;
+  const cudaError_t e = allow_shared(kern, Smem<NB, E4M3>::kBytes, &set);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3(unsigned(grid)), dim3(kThreads), size_t(Smem<NB, E4M3>::kBytes), s, p, pages);
+}
+
+template <int NB, bool E4M3>
+cudaError_t launch(const Params& p, const CUtensorMap& pages, int grid, cudaStream_t s) {
+  if (p.pre.rows == kTile)
+    return p.cap > 0.0f ? launch_as<NB, E4M3, true, true>(p, pages, grid, s) : launch_as<NB, E4M3, true, false>(p, pages, grid, s);
+  return p.cap > 0.0f ? launch_as<NB, E4M3, false, true>(p, pages, grid, s) : launch_as<NB, E4M3, false, false>(p, pages, grid, s);
+}
+
+}  // namespace
+
+sv_status prefix_launch(const char* fn, const Params& p, int grid, cudaStream_t s) {
+  CUtensorMap pages = {};
+  cudaError_t e;
+  if (p.c.e4m3) {
+    e = p.c.D > 64 ? launch<2, true>(p, pages, grid, s) : launch<1, true>(p, pages, grid, s);
+  } else {
+    const uint64_t dims[3] = {uint64_t(p.c.D), uint64_t(2 * p.c.hk) << p.c.shift, uint64_t(p.c.n_pages)};
+    const uint64_t strides[2] = {uint64_t(p.c.D) * 2u, uint64_t(p.c.page_bytes)};
+    const uint32_t box[3] = {64u, uint32_t(1 << p.c.shift < kTile ? 1 << p.c.shift : kTile), 1u};
+    const sv_status st =
+        make_tmap(&pages, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, p.c.pages, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (st != SV_OK) return st;
+    e = p.c.D > 64 ? launch<2, false>(p, pages, grid, s) : launch<1, false>(p, pages, grid, s);
+  }
+  return e == cudaSuccess ? SV_OK : cuda_fail(e, fn);
+}
+
+}  // namespace cached
+}  // namespace sv
