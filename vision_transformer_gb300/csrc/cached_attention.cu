@@ -177,12 +177,14 @@ struct Segment {
 // A warp's share of the steps. The items of the sequences in order: sequences, key heads, blocks of rows. 32 sequences at
 // a time, one per lane, with their steps summed by shuffles; every warp works it out for itself. What it knows lies in
 // shared memory (`st`, the warp's own): in registers it was in the way of the keys in flight.
+constexpr int kTotals = 32;
 struct ShareState {
   int incl[32];  // steps of the sequences up to this one
   Sequence seq[32];
   int blocks[32], steps[32];
   int chunk, at, end, base, total;
   int d0, count;
+  int totals[kTotals];  // steps of the first sequences, 32 and 32
 };
 template <int ROWS, int STEP>
 class Share {
@@ -193,11 +195,13 @@ class Share {
     bool bad = false;
     Sequence q;
     int blocks, steps;
+#pragma unroll 4
     for (int d0 = 0; d0 < p.c.count; d0 += 32) {
       bad |= !load(d0, count, q, blocks, steps);
-      work += unsigned(blocks * p.c.hk * steps);
+      const unsigned some = __reduce_add_sync(0xffffffffu, unsigned(blocks * p.c.hk * steps));
+      if (lane == 0 && d0 < 32 * kTotals) st_.totals[d0 / 32] = int(some);
+      work += some;
     }
-    work = __reduce_add_sync(0xffffffffu, work);
     // bad offsets or lengths: reported, and nothing is computed
     if (__any_sync(0xffffffffu, bad)) {
       if (lane == 0) atomicOr(p.c.err, kDevErrCache);
@@ -213,8 +217,17 @@ class Share {
       st_.count = count;
     }
     __syncwarp();
-    if (p.c.count > 32 || count == 0) load(0, count, q, blocks, steps);
-    open(0, q, blocks, steps);
+    // the first 32 sequences, or those that the share begins in
+    int d0 = 0;
+    while (d0 + 32 < count && d0 < 32 * kTotals && st_.base + st_.totals[d0 / 32] <= st_.at) {
+      const int total = st_.totals[d0 / 32];
+      __syncwarp();
+      if (lane == 0) st_.base += total;
+      __syncwarp();
+      d0 += 32;
+    }
+    if (p.c.count > 32 || count == 0) load(d0, count, q, blocks, steps);
+    open(d0, q, blocks, steps);
   }
   // The next segment of the share.
   __device__ __forceinline__ bool get(Segment& r) {
@@ -930,7 +943,7 @@ Plan plan_of(const View& c, int total_q, int group, int sms) {
   r.nt = rows <= 8ll * c.count ? 1 : 2;
   r.grid = sms * per_sm(r.nt);
   const size_t own = size_t(kMaxSms * per_sm(r.nt)) * 2 * size_t(8 * r.nt) * size_t(c.D + 2);
-  r.bytes = kCounterBytes + own * sizeof(float);
+  r.bytes = kCounterBytes + 128 + own * sizeof(float);  // (parts begin on 128 bytes)
   if (c.prefix_len > 0) {
     r.pre_nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 0;
     int step = 16 * groups_of(c.e4m3, c.D), most = sms * per_sm(r.pre_nt), at_most = kMaxSms * per_sm(r.pre_nt);
@@ -1055,7 +1068,7 @@ sv_status sv_attention_cached(const sv_cache* cache, const sv_cache_batch* batch
   p.out_e4m3 = out_dtype == SV_DT_E4M3;
   const Plan plan = plan_of(p.c, total_q, p.group, num_sms() < kMaxSms ? num_sms() : kMaxSms);
   p.counters = static_cast<unsigned*>(workspace);
-  p.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + kCounterBytes);
+  p.partial = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(workspace) + kCounterBytes + 127) & ~uintptr_t(127));
   p.pre = plan.pre;
   p.pre.base = p.partial + size_t(kMaxSms * per_sm(plan.nt)) * 2 * size_t(8 * plan.nt) * size_t(p.c.D + 2);
   cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -13,7 +13,7 @@
 //   warp 8             the MMA issuer: S_w = Q_w K^T (shared memory, 128-byte swizzle), O_w += P_w V (P from tensor memory);
 //   warp 9             copies keys and values in turn, with their scale bytes, page by page (a lane each): E4M3 codes as
 //                      they lie into a ring of their own, F16 numbers by TMA into the operands' ring;
-//   warps 10..13       Q, and the operands: codes in F16 with their factors applied (exactly, as sv_cache_read does); a
+//   warps 10..13       Q, and the operands, 32 rows of every tile a warp: codes in F16 with their factors applied (exactly, as sv_cache_read does); a
 //                      marked head becomes NaN, and with it every row; keys behind the prefix's end become zeros.
 // Tensor memory: S_0, S_1, O_0, O_1 of 128 columns each. A row's 128 scores do not fit the 128 registers that 14 warps
 // leave a thread: the upper half is read from tensor memory twice, for the maximum and for the exponentials.
@@ -36,13 +36,14 @@ constexpr int kTile = kPrefixTile;
 constexpr int kBoxBytes = kTile * 128;  // 128 rows of 64 values
 constexpr int kThreads = 448;
 constexpr int kLoaders = 128;           // threads of warps 10..13
+constexpr int kLoadWarps = kLoaders / 32;
 constexpr uint32_t kTmemCols = 512;
 
 template <int NB, bool E4M3>
 struct Smem {
   static constexpr int kOp = NB * kBoxBytes;  // one operand tile
-  static constexpr int kStages = E4M3 ? (NB == 1 ? 6 : 3) : (NB == 1 ? 8 : 4);
-  static constexpr int kRaws = E4M3 ? 4 : kStages;              // tiles of codes; F16: of scale bytes alone
+  static constexpr int kStages = NB == 1 ? 8 : 4;
+  static constexpr int kRaws = E4M3 ? 4 / NB : kStages;         // tiles of codes; F16: of scale bytes alone
   static constexpr int kRaw = E4M3 ? kTile * 64 * NB : 0;
   static constexpr int kOffRing = 2 * kOp;                      // behind Q
   static constexpr int kOffRaw = kOffRing + kStages * kOp;
@@ -100,13 +101,21 @@ __device__ __forceinline__ void bulk_load(uint32_t to, const void* from, uint32_
                : "memory");
 }
 
+// Eight words on 32 bytes: a whole sector a lane (by 16 bytes the sums of a CTA's rows took twice as long to leave).
+__device__ __forceinline__ void store8(float* to, const uint32_t* x) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]),
+               "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+               : "memory");
+}
+
 // 16-byte chunk of row `row` of an operand tile (64 values a box, 128-byte swizzle).
 __device__ __forceinline__ uint32_t chunk_at(int row, int chunk) {
   return uint32_t((chunk >> 3) * kBoxBytes + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
 }
 
 // pages: F16 pages as a tensor of [n_pages, 2 * kv_heads * page_size (keys, then values), head_dim].
-template <int NB, bool E4M3, bool SOLO, bool CAP>
+// FULL: heads of 64 NB dimensions.
+template <int NB, bool E4M3, bool SOLO, bool CAP, bool FULL>
 __global__ void __launch_bounds__(kThreads, 1)
     cached_prefix_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap pages_map) {
   using L = Smem<NB, E4M3>;
@@ -124,12 +133,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(bar(kBarFull + s), kLoaders);
+      mbar_init(bar(kBarFull + s), kLoadWarps);
       mbar_init(bar(kBarEmpty + s), 1);
     }
     for (int s = 0; s < kRaws; ++s) {
       mbar_init(bar(kBarRaw + s), 1);
-      mbar_init(bar(kBarRawFree + s), kLoaders / 32);
+      mbar_init(bar(kBarRawFree + s), kLoadWarps);
     }
     mbar_init(bar(kBarQFull), kLoaders);
     mbar_init(bar(kBarQEmpty), 1);
@@ -149,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   // Dimensions between D and the next multiple of 16 are read by the products and never written: zeros for good.
-  if (c.D % 16)
+  if (!FULL && c.D % 16)
     for (int x = int(threadIdx.x); x < (2 + kStages) * kTile; x += kThreads)
       *reinterpret_cast<uint4*>(smem + x / kTile * kOp + chunk_at(x % kTile, c.D / 8)) = make_uint4(0u, 0u, 0u, 0u);
   fence_proxy_async_smem();
@@ -217,25 +226,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (issued & (1u << i)) mbar_wait_bounded(bar(kBarRaw + i), (issued_phase >> i) & 1, p.c.err);
   } else if (warp >= 10) {
     const int tid = int(threadIdx.x) - 10 * 32;
-    const int per_row = c.D / 8;  // 16-byte chunks of a row
-    const int row_step = kLoaders / per_row, chunk_step = kLoaders % per_row;
-    int use = 0;  // operand tiles so far
+    const int per_row = FULL ? 8 * NB : c.D / 8;  // 16-byte chunks of a row
+    const int first = 32 * (warp - 10);  // row of the warp's piece of every tile
+    int use = 0;                         // operand tiles so far
     bool ok = true;
     for (int n = 0; ok && runs.get(p, run); ++n) {
       const int jb = SOLO ? 2 * run.s0 : run.s0, count = 2 * (run.s1 - run.s0) * (SOLO ? 2 : 1);
       if (!(ok = wait_all(kBarQEmpty, (n & 1) ^ 1))) break;
-#pragma unroll 1
-      for (int w = 0; w < (SOLO ? 1 : 2); ++w) {
-        int row = tid / per_row, chunk = tid % per_row;
+      {
+        const int row_step = kLoaders / per_row, chunk_step = kLoaders % per_row;
+        int row = tid / per_row, chunk = tid % per_row;  // (rows of both tiles)
 #pragma unroll 8
-        for (int i = 0; i < per_row; ++i) {
-          const int r = run.block * p.pre.rows + w * kTile + row;
+        for (; row < (SOLO ? 1 : 2) * kTile;) {
+          const int r = run.block * p.pre.rows + row;
           uint4 v = make_uint4(0u, 0u, 0u, 0u);
           if (r < rows_all) {
             const int q = query_of(p, r);
             v = __ldg(reinterpret_cast<const uint4*>(p.q + q * p.qs + (run.kvh * p.group + (r - q * p.group)) * c.D) + chunk);
           }
-          *reinterpret_cast<uint4*>(smem + w * kOp + chunk_at(row, chunk)) = v;
+          *reinterpret_cast<uint4*>(smem + (row >= kTile ? kOp : 0) + chunk_at(row & (kTile - 1), chunk)) = v;
           row += row_step;
           chunk += chunk_step;
           if (chunk >= per_row) chunk -= per_row, ++row;
@@ -243,48 +252,61 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       fence_proxy_async_smem();
       mbar_arrive(bar(kBarQFull));
+      constexpr int kMost = 8 * NB;  // chunks of a lane: of the rows `row`, `row` + row_step, ...
+      const int row0 = lane / per_row, chunk0 = lane % per_row, row_step = 32 / per_row, chunk_step = 32 % per_row;
 #pragma unroll 1
       for (int x = 0; x < count; ++x, ++use) {
         const int slot = use % kRaws, st = use % kStages;
-        const int left = c.prefix_len - (jb + tile_of(x)) * kTile;  // keys of the tile
+        const int left = c.prefix_len - (jb + tile_of(x)) * kTile - first;  // keys of the piece
         if (!(ok = wait_all(kBarRaw + slot, (use / kRaws) & 1))) break;
-        const uint8_t* scales = smem + L::kOffScales + slot * kTile;
-        uint8_t* to = smem + L::kOffRing + st * kOp;
+        const int byte = lane < left ? smem[L::kOffScales + slot * kTile + first + lane] : kNoScale;  // of row `lane`
+        uint8_t* to = smem + L::kOffRing + st * kOp + first * 128;
         if constexpr (E4M3) {
+          // The codes go to registers first: their ring is free for the next copy before this tile has its place.
+          const uint2* raw = reinterpret_cast<const uint2*>(smem + L::kOffRaw + slot * L::kRaw + first * c.D) + lane;
+          uint2 codes[kMost];
+#pragma unroll
+          for (int i = 0; i < kMost; ++i)
+            if (FULL || i < per_row) codes[i] = raw[i * 32];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBarRawFree + slot));
+          // (a marked head's codes are 0)
+          const uint32_t power = byte == 1 ? 0x0200u : uint32_t(byte - 1) << 10;
+          const uint32_t factor = byte == kMarked ? 0x7e007e00u : power << 16 | power;
           if (!(ok = wait_all(kBarEmpty + st, ((use / kStages) & 1) ^ 1))) break;
-          const uint2* raw = reinterpret_cast<const uint2*>(smem + L::kOffRaw + slot * L::kRaw) + tid;
-          int row = tid / per_row, chunk = tid % per_row;
-#pragma unroll 4
-          for (int i = 0; i < per_row; ++i) {
-            const int b = scales[row];
-            uint4 y = e4m3_to_f16(raw[i * kLoaders]);
-            const __half2 f = f16_power(min(b, 31) - kNoScale);
+          int row = row0, chunk = chunk0;
+#pragma unroll
+          for (int i = 0; i < kMost; ++i) {
+            if (!FULL && i >= per_row) continue;
+            if (left < 32 && row >= left) codes[i] = make_uint2(0u, 0u);
+            uint4 y = e4m3_to_f16(codes[i]);
+            const uint32_t w = __shfl_sync(0xffffffffu, factor, row);
+            const __half2 f = *reinterpret_cast<const __half2*>(&w);
             __half2* h = reinterpret_cast<__half2*>(&y);
 #pragma unroll
             for (int e = 0; e < 4; ++e) h[e] = __hmul2(h[e], f);
-            if (b == kMarked) y = make_uint4(0x7e007e00u, 0x7e007e00u, 0x7e007e00u, 0x7e007e00u);
-            if (row >= left) y = make_uint4(0u, 0u, 0u, 0u);
-            *reinterpret_cast<uint4*>(to + chunk_at(row, chunk)) = y;
+            // (whole heads: the steps change bits of the row that row0 leaves 0)
+            if constexpr (FULL)
+              *reinterpret_cast<uint4*>(to + (chunk_at(row0, chunk0) ^ uint32_t((i * (4 / NB) & 7) << 4)) + i * (4 / NB) * 128) = y;
+            else
+              *reinterpret_cast<uint4*>(to + chunk_at(row, chunk)) = y;
             row += row_step;
             chunk += chunk_step;
-            if (chunk >= per_row) chunk -= per_row, ++row;
+            if (!FULL && chunk >= per_row) chunk -= per_row, ++row;
           }
-        } else if (tid >= left || scales[tid] == kMarked) {
-          const uint32_t y = tid >= left ? 0u : 0x7e007e00u;
-          for (int i = 0; i < per_row; ++i) *reinterpret_cast<uint4*>(to + chunk_at(tid, i)) = make_uint4(y, y, y, y);
+        } else if (lane >= left || byte == kMarked) {
+          const uint32_t y = lane >= left ? 0u : 0x7e007e00u;
+          for (int i = 0; i < per_row; ++i) *reinterpret_cast<uint4*>(to + chunk_at(lane, i)) = make_uint4(y, y, y, y);
         }
         fence_proxy_async_smem();
-        mbar_arrive(bar(kBarFull + st));
-        if constexpr (E4M3) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(kBarRawFree + slot));
-        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarFull + st));
       }
     }
   } else if (warp == 8) {
     constexpr uint32_t idesc_s = make_idesc(128, 128, 0, false);
     const uint32_t idesc_o = make_idesc(128, (c.D + 15) / 16 * 16, 0, true);
-    const int steps = (c.D + 15) / 16;
+    const int steps = FULL ? 4 * NB : (c.D + 15) / 16;
     const uint32_t lead = elect_one();
     auto commit = [&](int b) { tc_commit_if(lead, bar(b)); };
     int use = 0;  // operand tiles that earlier runs have used
@@ -532,11 +554,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             a[e] = __float_as_uint(fmaf(f1, __uint_as_float(b[e]), f0 * __uint_as_float(a[e])));
           }
         }
-        if (live)
-#pragma unroll
-          for (int e = 0; e < 16; e += 4)
-            if (d + e < c.D)
-              __stcg(reinterpret_cast<uint4*>(part + size_t(at) * c.D + d + e), make_uint4(a[e], a[e + 1], a[e + 2], a[e + 3]));
+        if (live) {
+          store8(part + size_t(at) * c.D + d, a);
+          if (d + 8 < c.D) store8(part + size_t(at) * c.D + d + 8, a + 8);
+        }
       }
       if constexpr (SOLO) {
         tc_fence_before();
@@ -556,9 +577,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int NB, bool E4M3, bool SOLO, bool CAP>
 cudaError_t launch_as(const Params& p, const CUtensorMap& pages, int grid, cudaStream_t s) {
-  auto kern = cached_prefix_kernel<NB, E4M3, SOLO, CAP>;
-  static unsigned long long set = 0;
-  const cudaError_t e = allow_shared(kern, Smem<NB, E4M3>::kBytes, &set);
+  // (whole heads' chunks lie where a thread need not work them out; E4M3 alone is converted)
+  const bool full = E4M3 && p.c.D == 64 * NB;
+  auto kern = full ? cached_prefix_kernel<NB, E4M3, SOLO, CAP, E4M3> : cached_prefix_kernel<NB, E4M3, SOLO, CAP, false>;
+  static unsigned long long set[2] = {0, 0};
+  const cudaError_t e = allow_shared(kern, Smem<NB, E4M3>::kBytes, &set[full]);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3(unsigned(grid)), dim3(kThreads), size_t(Smem<NB, E4M3>::kBytes), s, p, pages);
 }
