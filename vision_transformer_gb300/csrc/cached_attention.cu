@@ -177,54 +177,81 @@ struct Segment {
 // A warp's share of the steps. The items of the sequences in order: sequences, key heads, blocks of rows. 32 sequences at
 // a time, one per lane, with their steps summed by shuffles; every warp works it out for itself. What it knows lies in
 // shared memory (`st`, the warp's own): in registers it was in the way of the keys in flight.
-constexpr int kTotals = 32;
 struct ShareState {
   int incl[32];  // steps of the sequences up to this one
   Sequence seq[32];
   int blocks[32], steps[32];
   int chunk, at, end, base, total;
   int d0, count;
-  int totals[kTotals];  // steps of the first sequences, 32 and 32
+};
+struct ShareTotals {  // of the CTA's warps together
+  int part[32];       // steps of the sequences, 32 and 32
+  unsigned work[kWarps];
+  int bad[kWarps];
 };
 template <int ROWS, int STEP>
 class Share {
  public:
-  __device__ __forceinline__ Share(const Params& p, int warp, int lane, ShareState& st) : p_(p), lane_(lane), st_(st) {
+  __device__ __forceinline__ Share(const Params& p, int warp, int lane, ShareState& st, ShareTotals& all)
+      : p_(p), lane_(lane), st_(st) {
     int count = p.c.count;
-    unsigned work = 0;
-    bool bad = false;
+    unsigned work;
+    bool bad;
     Sequence q;
     int blocks, steps;
-#pragma unroll 4
-    for (int d0 = 0; d0 < p.c.count; d0 += 32) {
-      bad |= !load(d0, count, q, blocks, steps);
-      const unsigned some = __reduce_add_sync(0xffffffffu, unsigned(blocks * p.c.hk * steps));
-      if (lane == 0 && d0 < 32 * kTotals) st_.totals[d0 / 32] = int(some);
-      work += some;
+    if (count <= 32) {
+      bad = !load(0, count, q, blocks, steps);
+      work = __reduce_add_sync(0xffffffffu, unsigned(blocks * p.c.hk * steps));
+      bad = __any_sync(0xffffffffu, bad);
+    } else {  // the CTA's warps share them out
+      work = 0;
+      bad = false;
+      for (int d0 = 32 * warp; d0 < count; d0 += 32 * kWarps) {
+        bad |= !load(d0, count, q, blocks, steps);
+        const unsigned some = __reduce_add_sync(0xffffffffu, unsigned(blocks * p.c.hk * steps));
+        if (lane == 0 && d0 < 32 * 32) all.part[d0 / 32] = int(some);
+        work += some;
+      }
+      bad = __any_sync(0xffffffffu, bad);
+      if (lane == 0) {
+        all.work[warp] = work;
+        all.bad[warp] = bad;
+      }
+      __syncthreads();
+      work = all.work[0] + all.work[1] + all.work[2] + all.work[3];
+      bad = all.bad[0] | all.bad[1] | all.bad[2] | all.bad[3];
+      static_assert(kWarps == 4, "sums of four");
     }
     // bad offsets or lengths: reported, and nothing is computed
-    if (__any_sync(0xffffffffu, bad)) {
+    if (bad) {
       if (lane == 0) atomicOr(p.c.err, kDevErrCache);
       count = 0;
       work = 0;
     }
     const unsigned warps = gridDim.x * kWarps, chunk = max(1u, (work + warps - 1) / warps);
+    const int at = int(min(chunk * (blockIdx.x * kWarps + warp), work));  // (a share may begin behind the last step)
+    // the 32 sequences that the share begins in; the first ones where there are more than 32 times 32
+    int d0 = 0, base = 0;
+    if (count > 32 && count <= 32 * 32) {
+      const int mine = 32 * lane < count ? all.part[lane] : 0;
+      int incl = mine;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int a = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += a;
+      }
+      const unsigned behind = __ballot_sync(0xffffffffu, incl > at);
+      if (behind) {
+        const int src = __ffs(int(behind)) - 1;
+        d0 = 32 * src;
+        base = __shfl_sync(0xffffffffu, incl - mine, src);
+      }
+    }
     if (lane == 0) {
       st_.chunk = int(chunk);
-      st_.at = int(min(chunk * (blockIdx.x * kWarps + warp), work));  // (a share may begin behind the last step)
-      st_.end = int(min(unsigned(st_.at) + chunk, work));
-      st_.base = 0;
+      st_.at = at;
+      st_.end = int(min(unsigned(at) + chunk, work));
+      st_.base = base;
       st_.count = count;
-    }
-    __syncwarp();
-    // the first 32 sequences, or those that the share begins in
-    int d0 = 0;
-    while (d0 + 32 < count && d0 < 32 * kTotals && st_.base + st_.totals[d0 / 32] <= st_.at) {
-      const int total = st_.totals[d0 / 32];
-      __syncwarp();
-      if (lane == 0) st_.base += total;
-      __syncwarp();
-      d0 += 32;
     }
     if (p.c.count > 32 || count == 0) load(d0, count, q, blocks, steps);
     open(d0, q, blocks, steps);
@@ -300,7 +327,7 @@ class Share {
 template <int ROWS>
 class PrefixShare {
  public:
-  __device__ __forceinline__ PrefixShare(const Params& p, int warp, int lane, ShareState& st) : p_(p), lane_(lane), st_(st) {
+  __device__ __forceinline__ PrefixShare(const Params& p, int warp, int lane, ShareState& st, ShareTotals&) : p_(p), lane_(lane), st_(st) {
     const int work = p.pre.blocks * p.c.hk * p.pre.steps, chunk = p.pre.chunk / kWarps;
     if (lane == 0) {
       st_.at = min(chunk * (int(blockIdx.x) * kWarps + warp), work);
@@ -504,6 +531,7 @@ struct FewShared {
   Segment cut[kWarps][2];          // these items; no steps: none
   Segment segment[kWarps];         // the warp's present one
   ShareState state[kWarps];
+  ShareTotals totals;
   Params p;  // for settle(): the parameters' own place is far from a function that is not inlined
   unsigned seen[2];
 };
@@ -532,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT)) cached_few_kernel(const 
   const int chunks = D / 8;
   const float sl2 = p.cap > 0.0f ? cap_factor(p.scale, p.cap) : kLog2e * p.scale;
   const int to_values = value_bytes(c), to_scales = scale_bytes(c), page_mask = (1 << c.shift) - 1;
-  typename std::conditional<PREFIX, PrefixShare<kRows>, Share<kRows, kStep>>::type share(p, warp, lane, mem.state[warp]);
+  typename std::conditional<PREFIX, PrefixShare<kRows>, Share<kRows, kStep>>::type share(p, warp, lane, mem.state[warp], mem.totals);
   if (lane < 2) mem.cut[warp][lane].steps = 0;  // (none)
   if (threadIdx.x < sizeof(Params) / 4) reinterpret_cast<int*>(&mem.p)[threadIdx.x] = reinterpret_cast<const int*>(&p)[threadIdx.x];
   static_assert(sizeof(Params) % 4 == 0 && sizeof(Params) / 4 <= kThreads, "a thread a word");
@@ -856,52 +884,53 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT)) cached_few_kernel(const 
   }
 
   // Items that were cut between the warps: the one that the CTA before has begun, and those that go on behind each warp's
-  // share. Then, by the last CTA of an item's parts, those that were cut between CTAs. Every fourth row a warp.
-  static_assert(kRows <= 4 * kWarps, "rows of a warp");
+  // share; four rows a warp in turn.
   __syncthreads();
   auto cta_of = [&](int step) { return int(unsigned(step) / unsigned(mem.state[warp].chunk * kWarps)); };
   int open[2] = {-1, -1};  // first warps of the items that are cut at the start and at the end of the CTA's share
-  int stage = 0;           // 0: the CTA's own parts, 1: items cut between CTAs
+  int task = 0;
 #pragma unroll 1
-  for (int x = 0;; ++x) {
-    if (x > kWarps) {  // the CTA's parts are in place
-      if (PREFIX || stage == 1 || (open[0] < 0 && open[1] < 0)) break;
-      stage = 1;
-      x = 0;
-      __threadfence();
-      __syncthreads();
-      if (threadIdx.x < 2 && open[threadIdx.x] >= 0) {
-        const Segment& cut = mem.cut[open[threadIdx.x]][threadIdx.x];
-        const int c0 = cta_of(cut.base), c1 = cta_of(cut.base + cut.steps - 1);
-        mem.seen[threadIdx.x] = atomicInc(p.counters + c0, unsigned(c1 - c0)) == unsigned(c1 - c0);  // then 0 again
-      }
-      __syncthreads();
-    }
-    if (stage == 1 && (x > 1 || open[x] < 0 || !mem.seen[x])) continue;
-    const int w0 = stage == 1 ? open[x] : max(x - 1, 0), slot = x > 0;
+  for (int x = 0; x <= kWarps; ++x) {
+    const int w0 = max(x - 1, 0), slot = x > 0;
     const Segment& first = mem.cut[w0][slot];
     if (first.steps == 0) continue;
-    const int rows = min(kRows, first.seq.n * p.group - first.row0), some = (rows - warp + kWarps - 1) / kWarps;
-    Source from;
+    int n = 1, s1 = first.s1;
+    while (s1 < first.steps && w0 + n < kWarps) s1 = mem.cut[w0 + n++][0].s1;
+    Source from = shared_source(&mem.part[w0][slot], n);
+    if (w0 + 1 < kWarps) from.rest = mem.part[w0 + 1][0].y[0];
     float* put = nullptr;
-    if (stage == 0) {
-      int n = 1, s1 = first.s1;
-      while (s1 < first.steps && w0 + n < kWarps) s1 = mem.cut[w0 + n++][0].s1;
-      from = shared_source(&mem.part[w0][slot], n);
-      if (w0 + 1 < kWarps) from.rest = mem.part[w0 + 1][0].y[0];
-      if (PREFIX) {
-        put = kept_at(first.item + int(blockIdx.x));
-      } else if (first.s0 > 0 || s1 < first.steps) {
-        const int end = first.s0 == 0;
-        open[end] = w0;
-        put = kept_at(2 * int(blockIdx.x) + end);
-      }
-    } else {
-      __threadfence();
-      const int c0 = cta_of(first.base), c1 = cta_of(first.base + first.steps - 1);
-      from = {kept_at(2 * c0 + 1), kept_at(2 * c0 + 2), 2 * kRows * (D + 2), c1 - c0 + 1, D, kRows * D, false};
+    if (PREFIX) {
+      put = kept_at(first.item + int(blockIdx.x));
+    } else if (first.s0 > 0 || s1 < first.steps) {
+      const int end = first.s0 == 0;
+      open[end] = w0;
+      put = kept_at(2 * int(blockIdx.x) + end);
     }
-    settle(mem.p, first, from, warp, kWarps, some, put, kRows);
+    const int rows = min(kRows, first.seq.n * p.group - first.row0);
+    for (int r = 0; r < rows; r += 4, ++task)
+      if (task % kWarps == warp) settle(mem.p, first, from, r, 1, min(4, rows - r), put, kRows);
+  }
+  if (PREFIX || (open[0] < 0 && open[1] < 0)) return;
+
+  // Items that were cut between CTAs: the last CTA of an item's parts joins them, every fourth row a warp.
+  static_assert(kRows <= 4 * kWarps, "rows of a warp");
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x < 2 && open[threadIdx.x] >= 0) {
+    const Segment& cut = mem.cut[open[threadIdx.x]][threadIdx.x];
+    const int c0 = cta_of(cut.base), c1 = cta_of(cut.base + cut.steps - 1);
+    mem.seen[threadIdx.x] = atomicInc(p.counters + c0, unsigned(c1 - c0)) == unsigned(c1 - c0);  // then 0 again
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int end = 0; end < 2; ++end) {
+    if (open[end] < 0 || !mem.seen[end]) continue;
+    __threadfence();
+    const Segment& cut = mem.cut[open[end]][end];
+    const int c0 = cta_of(cut.base), c1 = cta_of(cut.base + cut.steps - 1);
+    const int rows = min(kRows, cut.seq.n * p.group - cut.row0);
+    const Source from = {kept_at(2 * c0 + 1), kept_at(2 * c0 + 2), 2 * kRows * (D + 2), c1 - c0 + 1, D, kRows * D, false};
+    settle(mem.p, cut, from, warp, kWarps, (rows - warp + kWarps - 1) / kWarps, nullptr, kRows);
   }
 }
 

@@ -8,15 +8,15 @@
 // (PrefixParts); cached_attention.cu adds them to what the row's own tokens give.
 //
 // A CTA (one per SM) has two tiles of 128 rows, or, with at most 128 rows in the batch (SOLO), one whose key tiles two
-// groups take in turn. 14 warps:
+// groups take in turn. 16 warps:
 //   warps 0..3, 4..7   softmax of group 0 and 1: a thread per row turns its S row into P (F16, over S in tensor memory);
 //   warp 8             the MMA issuer: S_w = Q_w K^T (shared memory, 128-byte swizzle), O_w += P_w V (P from tensor memory);
 //   warp 9             copies keys and values in turn, with their scale bytes, page by page (a lane each): E4M3 codes as
 //                      they lie into a ring of their own, F16 numbers by TMA into the operands' ring;
 //   warps 10..13       Q, and the operands, 32 rows of every tile a warp: codes in F16 with their factors applied (exactly, as sv_cache_read does); a
 //                      marked head becomes NaN, and with it every row; keys behind the prefix's end become zeros.
-// Tensor memory: S_0, S_1, O_0, O_1 of 128 columns each. A row's 128 scores do not fit the 128 registers that 14 warps
-// leave a thread: the upper half is read from tensor memory twice, for the maximum and for the exponentials.
+//   warps 14, 15       nothing: registers are shared out by four warps.
+// Tensor memory: S_0, S_1, O_0, O_1 of 128 columns each.
 #include "cached.h"
 #include "packed_attention.h"
 
@@ -34,7 +34,9 @@ using packed::kSlack;
 
 constexpr int kTile = kPrefixTile;
 constexpr int kBoxBytes = kTile * 128;  // 128 rows of 64 values
-constexpr int kThreads = 448;
+// Four warpgroups, whose registers are shared out anew at the start: 2 x 128 x 176 + 2 x 128 x 80 = 512 x 128.
+constexpr int kThreads = 512;
+constexpr int kSoftmaxRegs = 176, kOtherRegs = 80;
 constexpr int kLoaders = 128;           // threads of warps 10..13
 constexpr int kLoadWarps = kLoaders / 32;
 constexpr uint32_t kTmemCols = 512;
@@ -178,220 +180,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // of two tiles, their values, ...
   auto is_values = [](int x) { return ((SOLO ? x >> 1 : x) & 1) != 0; };
   auto tile_of = [](int x) { return SOLO ? (x >> 2) * 2 + (x & 1) : x >> 1; };
-  if (warp == 9) {
-    const int page_mask = (1 << c.shift) - 1, run_rows = min(kTile, page_mask + 1);
-    // The pages of a tile's keys, a lane each (8 at most; runs of run_rows keys).
-    auto pages_of = [&](int tile) -> int {
-      const int number = ((tile * kTile) >> c.shift) + lane;
-      if (lane >= kTile / run_rows || number >= (c.prefix_len + page_mask) >> c.shift) return -1;
-      const int page = __ldg(c.prefix_pages + number);
-      if (unsigned(page) < unsigned(c.n_pages)) return page;
-      atomicOr(c.err, kDevErrCache);
-      return 0;
-    };
-    if (!E4M3 && lane == 0) prefetch_tmap(&pages_map);
-    uint32_t issued = 0, issued_phase = 0;  // copies in flight per tile of the ring, and their phase bits
-    int use = 0;
-    bool ok = true;
-    while (ok && runs.get(p, run)) {
-      const int jb = SOLO ? 2 * run.s0 : run.s0, count = 2 * (run.s1 - run.s0) * (SOLO ? 2 : 1);
-      int page = pages_of(jb);
-      for (int x = 0; x < count; ++x, ++use) {
-        const int tile = jb + tile_of(x);
-        const int next = x + 1 < count ? pages_of(jb + tile_of(x + 1)) : -1;
-        const int slot = use % kRaws;
-        if (!(ok = wait_all((E4M3 ? kBarRawFree : kBarEmpty) + slot, ((use / kRaws) & 1) ^ 1))) break;
-        const int copies = __popc(__ballot_sync(0xffffffffu, page >= 0));
-        const uint32_t full = bar(kBarRaw + slot);
-        if (lane == 0) mbar_arrive_expect_tx(full, uint32_t(copies * run_rows * (1 + (E4M3 ? c.D : NB * 128))));
-        issued |= 1u << slot;
-        issued_phase = (issued_phase & ~(1u << slot)) | uint32_t((use / kRaws) & 1) << slot;
-        __syncwarp();
-        if (page >= 0) {
-          const int at = (tile * kTile) & page_mask, row = ((run.kvh + (is_values(x) ? c.hk : 0)) << c.shift) + at;
-          const uint8_t* from = c.pages + page * c.page_bytes;
-          bulk_load(sbase + L::kOffScales + slot * kTile + lane * run_rows, from + scale_bytes(c) + row, uint32_t(run_rows), full);
-          if constexpr (E4M3) {
-            bulk_load(sbase + L::kOffRaw + slot * L::kRaw + lane * run_rows * c.D, from + row * c.D, uint32_t(run_rows * c.D), full);
-          } else {
-            for (int b = 0; b < NB; ++b)
-              tma_load_3d(sbase + L::kOffRing + slot * kOp + b * kBoxBytes + lane * run_rows * 128, &pages_map, full, 64 * b, row, page);
-          }
-        }
-        page = next;
-      }
-    }
-    // (after a time-out: every copy issued lands before the CTA can exit)
-    for (int i = 0; i < kRaws; ++i)
-      if (issued & (1u << i)) mbar_wait_bounded(bar(kBarRaw + i), (issued_phase >> i) & 1, p.c.err);
-  } else if (warp >= 10) {
-    const int tid = int(threadIdx.x) - 10 * 32;
-    const int per_row = FULL ? 8 * NB : c.D / 8;  // 16-byte chunks of a row
-    const int first = 32 * (warp - 10);  // row of the warp's piece of every tile
-    int use = 0;                         // operand tiles so far
-    bool ok = true;
-    for (int n = 0; ok && runs.get(p, run); ++n) {
-      const int jb = SOLO ? 2 * run.s0 : run.s0, count = 2 * (run.s1 - run.s0) * (SOLO ? 2 : 1);
-      if (!(ok = wait_all(kBarQEmpty, (n & 1) ^ 1))) break;
-      {
-        const int row_step = kLoaders / per_row, chunk_step = kLoaders % per_row;
-        int row = tid / per_row, chunk = tid % per_row;  // (rows of both tiles)
-#pragma unroll 8
-        for (; row < (SOLO ? 1 : 2) * kTile;) {
-          const int r = run.block * p.pre.rows + row;
-          uint4 v = make_uint4(0u, 0u, 0u, 0u);
-          if (r < rows_all) {
-            const int q = query_of(p, r);
-            v = __ldg(reinterpret_cast<const uint4*>(p.q + q * p.qs + (run.kvh * p.group + (r - q * p.group)) * c.D) + chunk);
-          }
-          *reinterpret_cast<uint4*>(smem + (row >= kTile ? kOp : 0) + chunk_at(row & (kTile - 1), chunk)) = v;
-          row += row_step;
-          chunk += chunk_step;
-          if (chunk >= per_row) chunk -= per_row, ++row;
-        }
-      }
-      fence_proxy_async_smem();
-      mbar_arrive(bar(kBarQFull));
-      constexpr int kMost = 8 * NB;  // chunks of a lane: of the rows `row`, `row` + row_step, ...
-      const int row0 = lane / per_row, chunk0 = lane % per_row, row_step = 32 / per_row, chunk_step = 32 % per_row;
-#pragma unroll 1
-      for (int x = 0; x < count; ++x, ++use) {
-        const int slot = use % kRaws, st = use % kStages;
-        const int left = c.prefix_len - (jb + tile_of(x)) * kTile - first;  // keys of the piece
-        if (!(ok = wait_all(kBarRaw + slot, (use / kRaws) & 1))) break;
-        const int byte = lane < left ? smem[L::kOffScales + slot * kTile + first + lane] : kNoScale;  // of row `lane`
-        uint8_t* to = smem + L::kOffRing + st * kOp + first * 128;
-        if constexpr (E4M3) {
-          // The codes go to registers first: their ring is free for the next copy before this tile has its place.
-          const uint2* raw = reinterpret_cast<const uint2*>(smem + L::kOffRaw + slot * L::kRaw + first * c.D) + lane;
-          uint2 codes[kMost];
-#pragma unroll
-          for (int i = 0; i < kMost; ++i)
-            if (FULL || i < per_row) codes[i] = raw[i * 32];
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(kBarRawFree + slot));
-          // (a marked head's codes are 0)
-          const uint32_t power = byte == 1 ? 0x0200u : uint32_t(byte - 1) << 10;
-          const uint32_t factor = byte == kMarked ? 0x7e007e00u : power << 16 | power;
-          if (!(ok = wait_all(kBarEmpty + st, ((use / kStages) & 1) ^ 1))) break;
-          int row = row0, chunk = chunk0;
-#pragma unroll
-          for (int i = 0; i < kMost; ++i) {
-            if (!FULL && i >= per_row) continue;
-            if (left < 32 && row >= left) codes[i] = make_uint2(0u, 0u);
-            uint4 y = e4m3_to_f16(codes[i]);
-            const uint32_t w = __shfl_sync(0xffffffffu, factor, row);
-            const __half2 f = *reinterpret_cast<const __half2*>(&w);
-            __half2* h = reinterpret_cast<__half2*>(&y);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) h[e] = __hmul2(h[e], f);
-            // (whole heads: the steps change bits of the row that row0 leaves 0)
-            if constexpr (FULL)
-              *reinterpret_cast<uint4*>(to + (chunk_at(row0, chunk0) ^ uint32_t((i * (4 / NB) & 7) << 4)) + i * (4 / NB) * 128) = y;
-            else
-              *reinterpret_cast<uint4*>(to + chunk_at(row, chunk)) = y;
-            row += row_step;
-            chunk += chunk_step;
-            if (!FULL && chunk >= per_row) chunk -= per_row, ++row;
-          }
-        } else if (lane >= left || byte == kMarked) {
-          const uint32_t y = lane >= left ? 0u : 0x7e007e00u;
-          for (int i = 0; i < per_row; ++i) *reinterpret_cast<uint4*>(to + chunk_at(lane, i)) = make_uint4(y, y, y, y);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarFull + st));
-      }
-    }
-  } else if (warp == 8) {
-    constexpr uint32_t idesc_s = make_idesc(128, 128, 0, false);
-    const uint32_t idesc_o = make_idesc(128, (c.D + 15) / 16 * 16, 0, true);
-    const int steps = FULL ? 4 * NB : (c.D + 15) / 16;
-    const uint32_t lead = elect_one();
-    auto commit = [&](int b) { tc_commit_if(lead, bar(b)); };
-    int use = 0;  // operand tiles that earlier runs have used
-    auto full = [&](int ahead) {
-      const int u = use + ahead;
-      const bool got = wait_all(kBarFull + u % kStages, (u / kStages) & 1);
-      tc_fence_after();
-      return got;
-    };
-    auto issue_s = [&](int w, int ahead) {
-      const uint64_t qd = make_sdesc(sbase + uint32_t(SOLO ? 0 : w) * kOp, 16, 1024, 2);
-      const uint64_t kd = make_sdesc(sbase + L::kOffRing + uint32_t((use + ahead) % kStages) * kOp, 16, 1024, 2);
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)  // 32 bytes of each row a step
-          if (4 * b + kk < steps)
-            mma_f16_if(lead, tmem + uint32_t(128 * w), qd + uint64_t(b * (kBoxBytes >> 4) + 2 * kk),
-                       kd + uint64_t(b * (kBoxBytes >> 4) + 2 * kk), idesc_s, b + kk > 0);
-      commit(kBarSFull + w);
-    };
-    auto issue_pv = [&](int w, int ahead, uint32_t keep) {
-      const uint64_t vd = make_sdesc(sbase + L::kOffRing + uint32_t((use + ahead) % kStages) * kOp, kBoxBytes, 1024, 2);
-#pragma unroll
-      for (int kk = 0; kk < 8; ++kk)  // 16 keys a step: 8 columns of P, 16 rows of V
-        mma_f16_ts_if(lead, tmem + uint32_t(256 + 128 * w), tmem + uint32_t(128 * w + 8 * kk),
-                      vd + uint64_t(kk * (2048 >> 4)), idesc_o, kk > 0 ? 1u : keep);
-    };
-    auto empty = [&](int ahead) { commit(kBarEmpty + (use + ahead) % kStages); };
-    uint32_t tt = 0;  // parity of the groups' tiles
-    bool ok = true;
-    for (int n = 0; ok && runs.get(p, run); ++n) {
-      const int count = run.s1 - run.s0;
-      if (!(ok = wait_all(kBarQFull, n & 1))) break;
-      if constexpr (SOLO) {
-        for (int w = 0; w < 2 && ok; ++w) {
-          if (!(ok = full(w))) break;
-          issue_s(w, w);
-          empty(w);
-        }
-        if (count == 1) commit(kBarQEmpty);
-        for (int j = 0; ok && j < count; ++j, tt ^= 1, use += 4) {
-          const bool last = j + 1 == count;
-          for (int w = 0; w < 2 && ok; ++w) {
-            if (!(ok = full(2 + w) && wait_all(kBarPFull + w, tt))) break;
-            tc_fence_after();
-            issue_pv(w, 2 + w, j > 0);
-            empty(2 + w);
-            if (last) {
-              commit(kBarOFull + w);
-            } else {
-              if (!(ok = full(4 + w))) break;
-              issue_s(w, 4 + w);
-              empty(4 + w);
-              if (w == 1 && j + 2 == count) commit(kBarQEmpty);
-            }
-          }
-        }
-      } else {
-        if (!(ok = full(0))) break;
-        issue_s(0, 0);
-        issue_s(1, 0);
-        empty(0);
-        if (count == 1) commit(kBarQEmpty);
-        for (int j = 0; ok && j < count; ++j, tt ^= 1, use += 2) {
-          const bool last = j + 1 == count;
-          if (!(ok = full(1) && (last || full(2)))) break;
-          for (int w = 0; w < 2 && ok; ++w) {
-            if (!(ok = wait_all(kBarPFull + w, tt))) break;
-            tc_fence_after();
-            issue_pv(w, 1, j > 0);
-            if (last) commit(kBarOFull + w);
-            else issue_s(w, 2);
-          }
-          if (!ok) break;
-          empty(1);
-          if (!last) empty(2);
-          if (j + 2 == count) commit(kBarQEmpty);
-        }
-      }
-    }
-    commit(kBarDrain);
-    __syncwarp();
-    mbar_wait_bounded(bar(kBarDrain), 0, p.c.err);
-  } else {
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int w = warp >> 2;             // group
     const int r = (warp & 3) * 32 + lane;  // row of the tile == lane of tensor memory
     const uint32_t lane_off = uint32_t((warp & 3) * 32) << 16;
@@ -443,24 +233,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           return fmaxf(a, b);
         };
-        uint32_t ua[2][32], ub[32];
+        uint32_t ua[4][32];
         float mx = -INFINITY;
-        tmem_ld32(s_tm + 64, ub);
-        tmem_ld32(s_tm, ua[0]);
-        tmem_ld_wait(ub);
-        reg_fence(ua[0]);
-        prepare(ub, 64);
-        mx = top_of(ub, mx);
-        tmem_ld32(s_tm + 96, ub);
-        tmem_ld32(s_tm + 32, ua[1]);
-        prepare(ua[0], 0);
-        mx = top_of(ua[0], mx);
-        tmem_ld_wait(ub);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tmem_ld32(s_tm + 32 * k, ua[k]);
+        tmem_ld_wait(ua[0]);
         reg_fence(ua[1]);
-        prepare(ub, 96);
-        mx = top_of(ub, mx);
-        prepare(ua[1], 32);
-        mx = top_of(ua[1], mx);
+        reg_fence(ua[2]);
+        reg_fence(ua[3]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          prepare(ua[k], 32 * k);
+          mx = top_of(ua[k], mx);
+        }
         mx *= on;
         const bool raise = mx > m + kSlack;
         const float m_new = raise ? mx - kHead : m;
@@ -495,19 +280,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             pk[e] = *reinterpret_cast<const uint32_t*>(&y);
           }
         };
-        uint32_t pk[32];
-        exponentials(ua[0], pk);
-        tmem_ld32(s_tm + 64, ub);
-        exponentials(ua[1], pk + 16);
-        tmem_st32(s_tm, pk);  // (over columns 0 .. 31: scores that are in registers)
-        tmem_ld32(s_tm + 96, ua[0]);
-        tmem_ld_wait(ub);
-        reg_fence(ua[0]);
-        prepare(ub, 64);
-        exponentials(ub, pk);
-        prepare(ua[0], 96);
-        exponentials(ua[0], pk + 16);
-        tmem_st32(s_tm + 32, pk);
+#pragma unroll
+        for (int k = 0; k < 4; k += 2) {
+          uint32_t pk[32];
+          exponentials(ua[k], pk);
+          exponentials(ua[k + 1], pk + 16);
+          tmem_st32(s_tm + 16 * k, pk);
+        }
         l += (s0 + s1) + (s2 + s3);
         tmem_st_wait();
         if (SOLO && n > 0 && j == j0) {  // both groups have read what the next P V overwrites
@@ -566,6 +345,222 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tmem_ld_wait();
     tmem_st_wait();
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == 9) {
+      const int page_mask = (1 << c.shift) - 1, run_rows = min(kTile, page_mask + 1);
+      // The pages of a tile's keys, a lane each (8 at most; runs of run_rows keys).
+      auto pages_of = [&](int tile) -> int {
+        const int number = ((tile * kTile) >> c.shift) + lane;
+        if (lane >= kTile / run_rows || number >= (c.prefix_len + page_mask) >> c.shift) return -1;
+        const int page = __ldg(c.prefix_pages + number);
+        if (unsigned(page) < unsigned(c.n_pages)) return page;
+        atomicOr(c.err, kDevErrCache);
+        return 0;
+      };
+      if (!E4M3 && lane == 0) prefetch_tmap(&pages_map);
+      uint32_t issued = 0, issued_phase = 0;  // copies in flight per tile of the ring, and their phase bits
+      int use = 0;
+      bool ok = true;
+      while (ok && runs.get(p, run)) {
+        const int jb = SOLO ? 2 * run.s0 : run.s0, count = 2 * (run.s1 - run.s0) * (SOLO ? 2 : 1);
+        int page = pages_of(jb);
+        for (int x = 0; x < count; ++x, ++use) {
+          const int tile = jb + tile_of(x);
+          const int next = x + 1 < count ? pages_of(jb + tile_of(x + 1)) : -1;
+          const int slot = use % kRaws;
+          if (!(ok = wait_all((E4M3 ? kBarRawFree : kBarEmpty) + slot, ((use / kRaws) & 1) ^ 1))) break;
+          const int copies = __popc(__ballot_sync(0xffffffffu, page >= 0));
+          const uint32_t full = bar(kBarRaw + slot);
+          if (lane == 0) mbar_arrive_expect_tx(full, uint32_t(copies * run_rows * (1 + (E4M3 ? c.D : NB * 128))));
+          issued |= 1u << slot;
+          issued_phase = (issued_phase & ~(1u << slot)) | uint32_t((use / kRaws) & 1) << slot;
+          __syncwarp();
+          if (page >= 0) {
+            const int at = (tile * kTile) & page_mask, row = ((run.kvh + (is_values(x) ? c.hk : 0)) << c.shift) + at;
+            const uint8_t* from = c.pages + page * c.page_bytes;
+            bulk_load(sbase + L::kOffScales + slot * kTile + lane * run_rows, from + scale_bytes(c) + row, uint32_t(run_rows), full);
+            if constexpr (E4M3) {
+              bulk_load(sbase + L::kOffRaw + slot * L::kRaw + lane * run_rows * c.D, from + row * c.D, uint32_t(run_rows * c.D), full);
+            } else {
+              for (int b = 0; b < NB; ++b)
+                tma_load_3d(sbase + L::kOffRing + slot * kOp + b * kBoxBytes + lane * run_rows * 128, &pages_map, full, 64 * b, row, page);
+            }
+          }
+          page = next;
+        }
+      }
+      // (after a time-out: every copy issued lands before the CTA can exit)
+      for (int i = 0; i < kRaws; ++i)
+        if (issued & (1u << i)) mbar_wait_bounded(bar(kBarRaw + i), (issued_phase >> i) & 1, p.c.err);
+    } else if (warp >= 10 && warp < 14) {
+      const int tid = int(threadIdx.x) - 10 * 32;
+      const int per_row = FULL ? 8 * NB : c.D / 8;  // 16-byte chunks of a row
+      const int first = 32 * (warp - 10);  // row of the warp's piece of every tile
+      int use = 0;                         // operand tiles so far
+      bool ok = true;
+      for (int n = 0; ok && runs.get(p, run); ++n) {
+        const int jb = SOLO ? 2 * run.s0 : run.s0, count = 2 * (run.s1 - run.s0) * (SOLO ? 2 : 1);
+        if (!(ok = wait_all(kBarQEmpty, (n & 1) ^ 1))) break;
+        {
+          const int row_step = kLoaders / per_row, chunk_step = kLoaders % per_row;
+          int row = tid / per_row, chunk = tid % per_row;  // (rows of both tiles)
+#pragma unroll 8
+          for (; row < (SOLO ? 1 : 2) * kTile;) {
+            const int r = run.block * p.pre.rows + row;
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (r < rows_all) {
+              const int q = query_of(p, r);
+              v = __ldg(reinterpret_cast<const uint4*>(p.q + q * p.qs + (run.kvh * p.group + (r - q * p.group)) * c.D) + chunk);
+            }
+            *reinterpret_cast<uint4*>(smem + (row >= kTile ? kOp : 0) + chunk_at(row & (kTile - 1), chunk)) = v;
+            row += row_step;
+            chunk += chunk_step;
+            if (chunk >= per_row) chunk -= per_row, ++row;
+          }
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(bar(kBarQFull));
+        constexpr int kMost = 8 * NB;  // chunks of a lane: of the rows `row`, `row` + row_step, ...
+        const int row0 = lane / per_row, chunk0 = lane % per_row, row_step = 32 / per_row, chunk_step = 32 % per_row;
+#pragma unroll 1
+        for (int x = 0; x < count; ++x, ++use) {
+          const int slot = use % kRaws, st = use % kStages;
+          const int left = c.prefix_len - (jb + tile_of(x)) * kTile - first;  // keys of the piece
+          if (!(ok = wait_all(kBarRaw + slot, (use / kRaws) & 1))) break;
+          const int byte = lane < left ? smem[L::kOffScales + slot * kTile + first + lane] : kNoScale;  // of row `lane`
+          uint8_t* to = smem + L::kOffRing + st * kOp + first * 128;
+          if constexpr (E4M3) {
+            // The codes go to registers first: their ring is free for the next copy before this tile has its place.
+            const uint2* raw = reinterpret_cast<const uint2*>(smem + L::kOffRaw + slot * L::kRaw + first * c.D) + lane;
+            uint2 codes[kMost];
+#pragma unroll
+            for (int i = 0; i < kMost; ++i)
+              if (FULL || i < per_row) codes[i] = raw[i * 32];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kBarRawFree + slot));
+            // (a marked head's codes are 0)
+            const uint32_t power = byte == 1 ? 0x0200u : uint32_t(byte - 1) << 10;
+            const uint32_t factor = byte == kMarked ? 0x7e007e00u : power << 16 | power;
+            if (!(ok = wait_all(kBarEmpty + st, ((use / kStages) & 1) ^ 1))) break;
+            int row = row0, chunk = chunk0;
+#pragma unroll
+            for (int i = 0; i < kMost; ++i) {
+              if (!FULL && i >= per_row) continue;
+              if (left < 32 && row >= left) codes[i] = make_uint2(0u, 0u);
+              uint4 y = e4m3_to_f16(codes[i]);
+              const uint32_t w = __shfl_sync(0xffffffffu, factor, row);
+              const __half2 f = *reinterpret_cast<const __half2*>(&w);
+              __half2* h = reinterpret_cast<__half2*>(&y);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) h[e] = __hmul2(h[e], f);
+              // (whole heads: the steps change bits of the row that row0 leaves 0)
+              if constexpr (FULL)
+                *reinterpret_cast<uint4*>(to + (chunk_at(row0, chunk0) ^ uint32_t((i * (4 / NB) & 7) << 4)) + i * (4 / NB) * 128) = y;
+              else
+                *reinterpret_cast<uint4*>(to + chunk_at(row, chunk)) = y;
+              row += row_step;
+              chunk += chunk_step;
+              if (!FULL && chunk >= per_row) chunk -= per_row, ++row;
+            }
+          } else if (lane >= left || byte == kMarked) {
+            const uint32_t y = lane >= left ? 0u : 0x7e007e00u;
+            for (int i = 0; i < per_row; ++i) *reinterpret_cast<uint4*>(to + chunk_at(lane, i)) = make_uint4(y, y, y, y);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBarFull + st));
+        }
+      }
+    } else if (warp == 8) {
+      constexpr uint32_t idesc_s = make_idesc(128, 128, 0, false);
+      const uint32_t idesc_o = make_idesc(128, (c.D + 15) / 16 * 16, 0, true);
+      const int steps = FULL ? 4 * NB : (c.D + 15) / 16;
+      const uint32_t lead = elect_one();
+      auto commit = [&](int b) { tc_commit_if(lead, bar(b)); };
+      int use = 0;  // operand tiles that earlier runs have used
+      auto full = [&](int ahead) {
+        const int u = use + ahead;
+        const bool got = wait_all(kBarFull + u % kStages, (u / kStages) & 1);
+        tc_fence_after();
+        return got;
+      };
+      auto issue_s = [&](int w, int ahead) {
+        const uint64_t qd = make_sdesc(sbase + uint32_t(SOLO ? 0 : w) * kOp, 16, 1024, 2);
+        const uint64_t kd = make_sdesc(sbase + L::kOffRing + uint32_t((use + ahead) % kStages) * kOp, 16, 1024, 2);
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)  // 32 bytes of each row a step
+            if (4 * b + kk < steps)
+              mma_f16_if(lead, tmem + uint32_t(128 * w), qd + uint64_t(b * (kBoxBytes >> 4) + 2 * kk),
+                         kd + uint64_t(b * (kBoxBytes >> 4) + 2 * kk), idesc_s, b + kk > 0);
+        commit(kBarSFull + w);
+      };
+      auto issue_pv = [&](int w, int ahead, uint32_t keep) {
+        const uint64_t vd = make_sdesc(sbase + L::kOffRing + uint32_t((use + ahead) % kStages) * kOp, kBoxBytes, 1024, 2);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)  // 16 keys a step: 8 columns of P, 16 rows of V
+          mma_f16_ts_if(lead, tmem + uint32_t(256 + 128 * w), tmem + uint32_t(128 * w + 8 * kk),
+                        vd + uint64_t(kk * (2048 >> 4)), idesc_o, kk > 0 ? 1u : keep);
+      };
+      auto empty = [&](int ahead) { commit(kBarEmpty + (use + ahead) % kStages); };
+      uint32_t tt = 0;  // parity of the groups' tiles
+      bool ok = true;
+      for (int n = 0; ok && runs.get(p, run); ++n) {
+        const int count = run.s1 - run.s0;
+        if (!(ok = wait_all(kBarQFull, n & 1))) break;
+        if constexpr (SOLO) {
+          for (int w = 0; w < 2 && ok; ++w) {
+            if (!(ok = full(w))) break;
+            issue_s(w, w);
+            empty(w);
+          }
+          if (count == 1) commit(kBarQEmpty);
+          for (int j = 0; ok && j < count; ++j, tt ^= 1, use += 4) {
+            const bool last = j + 1 == count;
+            for (int w = 0; w < 2 && ok; ++w) {
+              if (!(ok = full(2 + w) && wait_all(kBarPFull + w, tt))) break;
+              tc_fence_after();
+              issue_pv(w, 2 + w, j > 0);
+              empty(2 + w);
+              if (last) {
+                commit(kBarOFull + w);
+              } else {
+                if (!(ok = full(4 + w))) break;
+                issue_s(w, 4 + w);
+                empty(4 + w);
+                if (w == 1 && j + 2 == count) commit(kBarQEmpty);
+              }
+            }
+          }
+        } else {
+          if (!(ok = full(0))) break;
+          issue_s(0, 0);
+          issue_s(1, 0);
+          empty(0);
+          if (count == 1) commit(kBarQEmpty);
+          for (int j = 0; ok && j < count; ++j, tt ^= 1, use += 2) {
+            const bool last = j + 1 == count;
+            if (!(ok = full(1) && (last || full(2)))) break;
+            for (int w = 0; w < 2 && ok; ++w) {
+              if (!(ok = wait_all(kBarPFull + w, tt))) break;
+              tc_fence_after();
+              issue_pv(w, 1, j > 0);
+              if (last) commit(kBarOFull + w);
+              else issue_s(w, 2);
+            }
+            if (!ok) break;
+            empty(1);
+            if (!last) empty(2);
+            if (j + 2 == count) commit(kBarQEmpty);
+          }
+        }
+      }
+      commit(kBarDrain);
+      __syncwarp();
+      mbar_wait_bounded(bar(kBarDrain), 0, p.c.err);
+    }
   }
   tc_fence_before();
   __syncthreads();
