@@ -75,12 +75,13 @@ __device__ __forceinline__ bool place_of(const MoveParams& p, int t, long long& 
 template <bool READ, bool E4M3, int LANES>
 __global__ void __launch_bounds__(kMoveThreads) cache_kernel(const __grid_constant__ MoveParams p) {
   constexpr int kPer = 32 / LANES, kSteps = kTokens / kPer;  // tokens of a step, steps
+  static_assert(LANES == 2 * kSteps, "a token's lanes are two for each step");
   constexpr int kEs = E4M3 ? 1 : 2;
   const View& c = p.c;
   const int lane = threadIdx.x & 31;
   pdl_launch_dependents();
   pdl_wait();
-  const long long unit = static_cast<long long>(blockIdx.x) * (kMoveThreads / 32) + (threadIdx.x >> 5);
+  const unsigned unit = blockIdx.x * (kMoveThreads / 32) + (threadIdx.x >> 5);  // (below 2^31)
   if (unit == 0 && p.off) {  // offsets that decrease or leave [0, total]
     bool bad = false;
     for (int s = lane; s < c.count; s += 32) {
@@ -89,93 +90,64 @@ __global__ void __launch_bounds__(kMoveThreads) cache_kernel(const __grid_consta
     }
     if (bad) atomicOr(c.err, kDevErrCache);
   }
-  const long long t0 = unit / (2 * c.hk) * kTokens;
+  const unsigned block = unit / unsigned(2 * c.hk);
+  const int t0 = int(block) * kTokens;
   if (t0 >= p.total) return;
-  const int which = int(unit % (2 * c.hk));  // heads of the keys, then of the values
+  const int which = int(unit - block * unsigned(2 * c.hk));  // heads of the keys, then of the values
   const bool values = which >= c.hk;
   const int head = values ? which - c.hk : which;
-  const int chunk = lane % LANES;
+  const int group = lane / LANES, chunk = lane % LANES;
   const bool mine = 8 * chunk < c.D;
-  const __half* rows = (values ? p.v : p.k) + head * c.D + 8 * chunk;
   const long long stride = values ? p.vs : p.ks;
-  const long long last = p.total - t0;  // tokens left
+  const __half* rows = (values ? p.v : p.k) + (t0 + group) * stride + head * c.D + 8 * chunk;  // of step 0
+  const int last = p.total - t0 - group;  // this lane's tokens are steps i with i * kPer < last
 
   uint4 x[kSteps];
   if constexpr (!READ) {
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-      const int r = i * kPer + lane / LANES;
       x[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (mine && r < last) x[i] = __ldg(reinterpret_cast<const uint4*>(rows + (t0 + r) * stride));
+      if (mine && i * kPer < last) x[i] = __ldg(reinterpret_cast<const uint4*>(rows + i * kPer * stride));
     }
   }
-  long long base = -1;  // lane r < 16: token t0 + r
+  // Lane r < 16: where token t0 + r is kept, its codes' and its scale byte's place (-1: nowhere).
+  long long page = -1;
   int at = 0;
-  if (lane < kTokens && lane < last && !place_of<READ>(p, int(t0) + lane, base, at)) base = -1;
-  // places in the page: of the head's codes of a token, of its scale byte
+  if (lane < kTokens && t0 + lane < p.total && !place_of<READ>(p, t0 + lane, page, at)) page = -1;
+  __syncwarp();
   const int codes = (values ? value_bytes(c) : 0) + (head << c.shift) * c.D * kEs;
-  const int scale_at = scale_bytes(c) + ((which << c.shift) + at);
-  int scale = kNoScale;
+  const long long code_place = page < 0 ? -1 : page + codes + at * c.D * kEs;
+  const long long scale_place = page < 0 ? -1 : page + scale_bytes(c) + (which << c.shift) + at;
+  // Mostly the sixteen lie one behind another in a page: then nobody needs to be asked for a place.
+  const long long place0 = __shfl_sync(0xffffffffu, code_place, 0), scale0 = __shfl_sync(0xffffffffu, scale_place, 0);
+  const bool in_line = place0 >= 0 && __all_sync(0xffffffffu, lane >= kTokens || scale_place == scale0 + lane);
+  auto place_in = [&](int i) -> uint8_t* {  // of this lane's eight numbers of step i
+    const long long at_row = in_line ? place0 + (i * kPer + group) * c.D * kEs
+                                     : __shfl_sync(0xffffffffu, code_place, i * kPer + group);
+    return mine && at_row >= 0 ? c.pages + at_row + 8 * chunk * kEs : nullptr;
+  };
+
   if constexpr (READ) {
-    if (base >= 0) scale = __ldg(c.pages + base + scale_at);
+    int scale = kNoScale;
+    if (page >= 0) scale = __ldg(c.pages + scale_place);
     __syncwarp();
-  }
-#pragma unroll
-  for (int i = 0; i < kSteps; ++i) {
-    const int r = i * kPer + lane / LANES;
-    const long long page = __shfl_sync(0xffffffffu, base, r);
-    uint8_t* to = c.pages + page + codes + (__shfl_sync(0xffffffffu, at, r) * c.D + 8 * chunk) * kEs;
-    const bool live = mine && page >= 0;
-    if constexpr (READ) {
-      x[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (live) {
-        if constexpr (E4M3) {
-          const uint2 w = __ldg(reinterpret_cast<const uint2*>(to));
-          x[i].x = w.x, x[i].y = w.y;
-        } else {
-          x[i] = __ldg(reinterpret_cast<const uint4*>(to));
-        }
-      }
-    } else {
-      // the largest magnitude's bits (an infinity or NaN is at least 0x7c00)
-      uint32_t m = __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
-                            __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu));
-#pragma unroll
-      for (int o = 1; o < LANES; o <<= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const int top = int(max(m & 0xffffu, m >> 16));
-      const bool bad = top >= 0x7c00;
-      if (bad) x[i] = make_uint4(0u, 0u, 0u, 0u);
-      int byte = bad ? kMarked : kNoScale;
-      if constexpr (E4M3) {
-        const int e = max(-15, (top >> 10) - 23 + ((top & 0x3ff) > 0x300));
-        if (!bad) byte = e + kNoScale;
-        const __half2 f = f16_power(bad ? 0 : -e);
-        __half2* h = reinterpret_cast<__half2*>(&x[i]);
-        // (at most 448 but for e = 8, where 256 is held to 240)
-        const __half2 most = __float2half2_rn(e == 8 ? 240.0f : 448.0f);
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const __half2 y = __hmax2(__hmin2(__hmul2(h[j], f), most), __hneg2(most));
-          w[j] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(y), __NV_SATFINITE, __NV_E4M3);
-        }
-        if (live) *reinterpret_cast<uint2*>(to) = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
-      } else {
-        if (live) *reinterpret_cast<uint4*>(to) = x[i];
-      }
-      // the lane that holds the token's place keeps its byte
-      const int got = __shfl_sync(0xffffffffu, byte, (lane % kPer) * LANES);
-      if (lane / kPer == i) scale = got;
-    }
-  }
-  if constexpr (!READ) {
-    if (base >= 0) c.pages[base + scale_at] = uint8_t(scale);
-  } else {
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-      const int r = i * kPer + lane / LANES;
-      const int byte = __shfl_sync(0xffffffffu, scale, r);
-      const long long page = __shfl_sync(0xffffffffu, base, r);
+      const uint8_t* from = place_in(i);
+      x[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (from) {
+        if constexpr (E4M3) {
+          const uint2 w = __ldg(reinterpret_cast<const uint2*>(from));
+          x[i].x = w.x, x[i].y = w.y;
+        } else {
+          x[i] = __ldg(reinterpret_cast<const uint4*>(from));
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      const int byte = __shfl_sync(0xffffffffu, scale, i * kPer + group);
+      const bool live = in_line || __shfl_sync(0xffffffffu, code_place, i * kPer + group) >= 0;
       uint4 y = x[i];
       if constexpr (E4M3) {
         y = e4m3_to_f16(make_uint2(x[i].x, x[i].y));
@@ -185,7 +157,61 @@ __global__ void __launch_bounds__(kMoveThreads) cache_kernel(const __grid_consta
         for (int j = 0; j < 4; ++j) h[j] = __hmul2(h[j], f);
       }
       if (byte == kMarked) y = make_uint4(0x7e007e00u, 0x7e007e00u, 0x7e007e00u, 0x7e007e00u);
-      if (mine && page >= 0) *reinterpret_cast<uint4*>(const_cast<__half*>(rows) + (t0 + r) * stride) = y;
+      if (mine && live) *reinterpret_cast<uint4*>(const_cast<__half*>(rows) + i * kPer * stride) = y;
+    }
+  } else {
+    // The largest magnitude's bits of every token (an infinity or NaN is at least 0x7c00): each exchange halves the
+    // steps that a lane has a maximum of, until it has that of step lane % kSteps alone.
+    uint32_t m[kSteps];
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i)
+      m[i] = __vimax3_u16x2(__vimax3_u16x2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu, x[i].z & 0x7fff7fffu),
+                            x[i].w & 0x7fff7fffu, 0u);
+#pragma unroll
+    for (int o = 1; o < kSteps; o <<= 1) {
+      const bool high = lane & o;
+#pragma unroll
+      for (int i = 0; i < kSteps / (2 * o); ++i) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? m[2 * i] : m[2 * i + 1], o);
+        m[i] = __vimax3_u16x2(high ? m[2 * i + 1] : m[2 * i], got, 0u);
+      }
+    }
+    m[0] = __vimax3_u16x2(m[0], __shfl_xor_sync(0xffffffffu, m[0], kSteps), 0u);
+    const int top = int(max(m[0] & 0xffffu, m[0] >> 16));
+    const bool bad = top >= 0x7c00;
+    int e = 0;
+    if constexpr (E4M3) e = bad ? 0 : max(-15, (top >> 10) - 23 + ((top & 0x3ff) > 0x300));
+    // its scale byte
+    const int r = (lane % kSteps) * kPer + group;
+    const long long to = in_line ? scale0 + r : __shfl_sync(0xffffffffu, scale_place, r);
+    if (to >= 0 && !(lane & kSteps)) c.pages[to] = uint8_t(bad ? kMarked : e + kNoScale);
+    const bool some_bad = __any_sync(0xffffffffu, bad), some_large = __any_sync(0xffffffffu, e == 8);
+    const uint32_t power = uint32_t(15 - e) << 10;  // 2^-e in F16, twice
+    const uint32_t factor = power | power << 16;
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      const int holder = (lane & ~(LANES - 1)) + i;
+      if (some_bad && __shfl_sync(0xffffffffu, int(bad), holder)) x[i] = make_uint4(0u, 0u, 0u, 0u);
+      uint8_t* to_row = place_in(i);
+      if constexpr (E4M3) {
+        const uint32_t fw = __shfl_sync(0xffffffffu, factor, holder);
+        const __half2 f = *reinterpret_cast<const __half2*>(&fw);
+        __half2* h = reinterpret_cast<__half2*>(&x[i]);
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[j] = __hmul2(h[j], f);
+        if (some_large) {  // (at most 448 but for e = 8, where 256 is held to 240)
+          const __half2 most = __float2half2_rn(__shfl_sync(0xffffffffu, e, holder) == 8 ? 240.0f : 448.0f);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) h[j] = __hmax2(__hmin2(h[j], most), __hneg2(most));
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          w[j] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(h[j]), __NV_SATFINITE, __NV_E4M3);
+        if (to_row) *reinterpret_cast<uint2*>(to_row) = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+      } else {
+        if (to_row) *reinterpret_cast<uint4*>(to_row) = x[i];
+      }
     }
   }
 }

@@ -13,9 +13,9 @@
 //   warp 8             the MMA issuer: S_w = Q_w K^T (shared memory, 128-byte swizzle), O_w += P_w V (P from tensor memory);
 //   warp 9             copies keys and values in turn, with their scale bytes, page by page (a lane each): E4M3 codes as
 //                      they lie into a ring of their own, F16 numbers by TMA into the operands' ring;
-//   warps 10..13       Q, and the operands, 32 rows of every tile a warp: codes in F16 with their factors applied (exactly, as sv_cache_read does); a
+//   warps 10..13       the operands, 32 rows of every tile a warp: codes in F16 with their factors applied (exactly, as sv_cache_read does); a
 //                      marked head becomes NaN, and with it every row; keys behind the prefix's end become zeros.
-//   warps 14, 15       nothing: registers are shared out by four warps.
+//   warps 14, 15       bring Q.
 // Tensor memory: S_0, S_1, O_0, O_1 of 128 columns each.
 #include "cached.h"
 #include "packed_attention.h"
@@ -37,8 +37,8 @@ constexpr int kBoxBytes = kTile * 128;  // 128 rows of 64 values
 // Four warpgroups, whose registers are shared out anew at the start: 2 x 128 x 176 + 2 x 128 x 80 = 512 x 128.
 constexpr int kThreads = 512;
 constexpr int kSoftmaxRegs = 176, kOtherRegs = 80;
-constexpr int kLoaders = 128;           // threads of warps 10..13
-constexpr int kLoadWarps = kLoaders / 32;
+constexpr int kLoadWarps = 4;           // warps 10..13
+constexpr int kQueryThreads = 64;       // of warps 14, 15
 constexpr uint32_t kTmemCols = 512;
 
 template <int NB, bool E4M3>
@@ -50,8 +50,10 @@ struct Smem {
   static constexpr int kOffRing = 2 * kOp;                      // behind Q
   static constexpr int kOffRaw = kOffRing + kStages * kOp;
   static constexpr int kOffScales = kOffRaw + kRaws * kRaw;     // scale bytes of each tile
-  static constexpr int kOffBar = kOffScales + kRaws * kTile;
-  static constexpr int kOffJoin = kOp;  // SOLO: exponents and sums of both groups' rows, in place of a second tile of Q
+  // SOLO: exponents and sums of both groups' rows, then 4 KB a softmax warp; in place of a second tile of Q where that is
+  // large enough
+  static constexpr int kOffJoin = NB == 2 ? kOp : kOffScales + kRaws * kTile;
+  static constexpr int kOffBar = kOffScales + kRaws * kTile + (NB == 2 ? 0 : 8 * 4096);
   static constexpr int kBytes = 1024 + kOffBar + 384;
   static_assert(kBytes <= 232448, "shared memory budget");
 };
@@ -69,7 +71,8 @@ enum {
   kBarJoin = 40,   // SOLO: both groups' exponents and sums are in shared memory
   kBarRead = 41,   // SOLO: both have read O
   kBarDrain = 42,
-  kNumBars = 43
+  kBarJoined = 43, // SOLO: both groups have read the other's exponents and sums
+  kNumBars = 44
 };
 
 // A run of steps of one item that falls into this CTA's share.
@@ -142,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(kBarRaw + s), 1);
       mbar_init(bar(kBarRawFree + s), kLoadWarps);
     }
-    mbar_init(bar(kBarQFull), kLoaders);
+    mbar_init(bar(kBarQFull), kQueryThreads);
     mbar_init(bar(kBarQEmpty), 1);
     for (int w = 0; w < 2; ++w) {
       mbar_init(bar(kBarSFull + w), 1);
@@ -150,6 +153,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(kBarOFull + w), 1);
     }
     mbar_init(bar(kBarJoin), 256);
+    mbar_init(bar(kBarJoined), 256);
     mbar_init(bar(kBarRead), 256);
     mbar_init(bar(kBarDrain), 1);
     *abort_flag = 0;
@@ -318,29 +322,50 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool live = row < rows_all;
       if (live && (!SOLO || w == 0))
         __stcg(reinterpret_cast<float2*>(part + size_t(p.pre.rows) * c.D) + at, make_float2(m, l));
-      // SOLO: each group writes every second run of 16 columns
-#pragma unroll 1
-      for (int d = SOLO ? 16 * w : 0; d < Dn; d += SOLO ? 32 : 16) {
-        uint32_t a[16], b[16];
-        tmem_ld16(o_tm + uint32_t((SOLO ? 0 : 128 * w) + d), a);
-        if constexpr (SOLO) tmem_ld16(o_tm + uint32_t(128 + d), b);
-        tmem_ld_wait();
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          asm volatile("" : "+r"(a[e]));  // no use before the wait
-          if constexpr (SOLO) {
-            asm volatile("" : "+r"(b[e]));
-            a[e] = __float_as_uint(fmaf(f1, __uint_as_float(b[e]), f0 * __uint_as_float(a[e])));
-          }
-        }
-        if (live) {
-          store8(part + size_t(at) * c.D + d, a);
-          if (d + 8 < c.D) store8(part + size_t(at) * c.D + d + 8, a + 8);
-        }
-      }
       if constexpr (SOLO) {
+        // Both groups have read the other's exponents and sums: the place is the warps' to turn rows round in, so that
+        // eight lanes write 128 bytes of a row (a row a lane: 6,000 cycles, more than two tiles of keys take).
+        mbar_arrive(bar(kBarJoined));
+        if (!(ok = wait_all(kBarJoined, n & 1))) break;
+        uint8_t* stage = smem + L::kOffJoin + warp * 4096;
+#pragma unroll 1
+        for (int d = 32 * w; d < Dn; d += 64) {  // every second 32 columns
+          uint32_t a[32], b[32];
+          tmem_ld32(o_tm + uint32_t(d), a);
+          tmem_ld32(o_tm + uint32_t(128 + d), b);
+          tmem_ld_wait(a);
+          reg_fence(b);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) a[e] = __float_as_uint(fmaf(f1, __uint_as_float(b[e]), f0 * __uint_as_float(a[e])));
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            *reinterpret_cast<uint4*>(stage + lane * 128 + ((u ^ (lane & 7)) << 4)) =
+                make_uint4(a[4 * u], a[4 * u + 1], a[4 * u + 2], a[4 * u + 3]);
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int x = 4 * i + (lane >> 3), u = lane & 7;  // row of the warp, 16 bytes of it
+            const uint4 y = *reinterpret_cast<const uint4*>(stage + x * 128 + ((u ^ (x & 7)) << 4));
+            if (row - lane + x < rows_all && d + 4 * u < c.D)
+              __stcg(reinterpret_cast<uint4*>(part + size_t(at - lane + x) * c.D + d + 4 * u), y);
+          }
+          __syncwarp();
+        }
         tc_fence_before();
         mbar_arrive(bar(kBarRead));
+      } else {
+#pragma unroll 1
+        for (int d = 0; d < Dn; d += 16) {
+          uint32_t a[16];
+          tmem_ld16(o_tm + uint32_t(128 * w + d), a);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) asm volatile("" : "+r"(a[e]));  // no use before the wait
+          if (live) {
+            store8(part + size_t(at) * c.D + d, a);
+            if (d + 8 < c.D) store8(part + size_t(at) * c.D + d + 8, a + 8);
+          }
+        }
       }
     }
     tmem_ld_wait();
@@ -393,34 +418,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       // (after a time-out: every copy issued lands before the CTA can exit)
       for (int i = 0; i < kRaws; ++i)
         if (issued & (1u << i)) mbar_wait_bounded(bar(kBarRaw + i), (issued_phase >> i) & 1, p.c.err);
-    } else if (warp >= 10 && warp < 14) {
-      const int tid = int(threadIdx.x) - 10 * 32;
+    } else if (warp >= 14) {
+      const int tid = int(threadIdx.x) - 14 * 32;
       const int per_row = FULL ? 8 * NB : c.D / 8;  // 16-byte chunks of a row
-      const int first = 32 * (warp - 10);  // row of the warp's piece of every tile
-      int use = 0;                         // operand tiles so far
       bool ok = true;
       for (int n = 0; ok && runs.get(p, run); ++n) {
-        const int jb = SOLO ? 2 * run.s0 : run.s0, count = 2 * (run.s1 - run.s0) * (SOLO ? 2 : 1);
         if (!(ok = wait_all(kBarQEmpty, (n & 1) ^ 1))) break;
-        {
-          const int row_step = kLoaders / per_row, chunk_step = kLoaders % per_row;
-          int row = tid / per_row, chunk = tid % per_row;  // (rows of both tiles)
+        const int row_step = kQueryThreads / per_row, chunk_step = kQueryThreads % per_row;
+        int row = tid / per_row, chunk = tid % per_row;  // (rows of both tiles)
 #pragma unroll 8
-          for (; row < (SOLO ? 1 : 2) * kTile;) {
-            const int r = run.block * p.pre.rows + row;
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (r < rows_all) {
-              const int q = query_of(p, r);
-              v = __ldg(reinterpret_cast<const uint4*>(p.q + q * p.qs + (run.kvh * p.group + (r - q * p.group)) * c.D) + chunk);
-            }
-            *reinterpret_cast<uint4*>(smem + (row >= kTile ? kOp : 0) + chunk_at(row & (kTile - 1), chunk)) = v;
-            row += row_step;
-            chunk += chunk_step;
-            if (chunk >= per_row) chunk -= per_row, ++row;
+        for (; row < (SOLO ? 1 : 2) * kTile;) {
+          const int r = run.block * p.pre.rows + row;
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (r < rows_all) {
+            const int q = query_of(p, r);
+            v = __ldg(reinterpret_cast<const uint4*>(p.q + q * p.qs + (run.kvh * p.group + (r - q * p.group)) * c.D) + chunk);
           }
+          *reinterpret_cast<uint4*>(smem + (row >= kTile ? kOp : 0) + chunk_at(row & (kTile - 1), chunk)) = v;
+          row += row_step;
+          chunk += chunk_step;
+          if (chunk >= per_row) chunk -= per_row, ++row;
         }
         fence_proxy_async_smem();
         mbar_arrive(bar(kBarQFull));
+      }
+    } else if (warp >= 10) {
+      const int per_row = FULL ? 8 * NB : c.D / 8;
+      const int first = 32 * (warp - 10);  // row of the warp's piece of every tile
+      int use = 0;                         // operand tiles so far
+      bool ok = true;
+      while (ok && runs.get(p, run)) {
+        const int jb = SOLO ? 2 * run.s0 : run.s0, count = 2 * (run.s1 - run.s0) * (SOLO ? 2 : 1);
         constexpr int kMost = 8 * NB;  // chunks of a lane: of the rows `row`, `row` + row_step, ...
         const int row0 = lane / per_row, chunk0 = lane % per_row, row_step = 32 / per_row, chunk_step = 32 % per_row;
 #pragma unroll 1
