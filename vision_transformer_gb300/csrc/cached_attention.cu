@@ -553,8 +553,11 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT)) cached_few_kernel(const 
   Mem& mem = *reinterpret_cast<Mem*>(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
+  // Behind the prefix pass this kernel may begin before that one has ended, and needs nothing of it until its rows are
+  // joined; what the calls before have written (queries, cache, lengths) is in place, since the prefix pass lets others
+  // begin only after its own wait for them. Until the next wait nothing in global memory is written.
+  if (PREFIX || p.c.prefix_len == 0) pdl_wait();
   pdl_launch_dependents();
-  pdl_wait();
   const View& c = p.c;
   const int D = FULL ? 32 * KI : c.D;
   const int chunks = D / 8;
@@ -876,6 +879,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT)) cached_few_kernel(const 
     if (!whole && lane == 0) mem.cut[warp][sg.s0 == 0 ? 1 : 0] = sg;
     __syncwarp();
     if (whole) {
+      pdl_wait();
 #pragma unroll 1
       for (int r = 0; r < rows; r += 4)
         settle(mem.p, sg, shared_source(&mine, 1), r, 1, min(4, rows - r), PREFIX ? kept_at(sg.item + int(blockIdx.x)) : nullptr, kRows);
@@ -885,6 +889,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT)) cached_few_kernel(const 
 
   // Items that were cut between the warps: the one that the CTA before has begun, and those that go on behind each warp's
   // share; four rows a warp in turn.
+  pdl_wait();
   __syncthreads();
   auto cta_of = [&](int step) { return int(unsigned(step) / unsigned(mem.state[warp].chunk * kWarps)); };
   int open[2] = {-1, -1};  // first warps of the items that are cut at the start and at the end of the CTA's share

@@ -172,8 +172,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  pdl_launch_dependents();
   pdl_wait();
+  pdl_launch_dependents();  // (after the wait: the next kernel relies on what came before this one)
   const int rows_all = p.total_q * p.group;  // (below 2^26)
   auto wait = [&](int b, uint32_t parity) { return mbar_wait(bar(b), parity, abort_flag, p.c.err); };
   auto wait_all = [&](int b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)) != 0; };
