@@ -98,6 +98,9 @@ def test_workspace_does_not_depend_on_lengths(vt, p):
 
     assert 0 < size(16) <= 40 << 20 and size(16) == size(16, stride=10000)
     assert size(0) == 0
-    assert 0 < size(4096) <= 40 << 20
+    assert size(0, stride=10 ** 6) == 0
+    # 32 rows of a head and sequence on average and no more; else tiles of 128 rows
+    assert 0 < size(128) <= 40 << 20
+    assert 4096 * 32 * 130 * 4 < size(4096) <= 11 * 2 ** 20 + (4096 + 16 * 32) * 32 * 130 * 4
     for prefix in (1, 1000, 10 ** 6):
-        assert 0 < size(1024, prefix=prefix) <= (40 << 20) + 2 * 1024 * 32 * 130 * 4
+        assert 0 < size(1024, prefix=prefix) <= (32 << 20) + (2 * 1024 * 32 + 16 * 8 * 128 + 8 * 256) * 130 * 4

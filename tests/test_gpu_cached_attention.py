@@ -120,6 +120,27 @@ def test_batches_behind_a_long_prefix(sv, count, n, prefix, have, hq, hk, d):
     sv.sv_sync()
 
 
+@pytest.mark.parametrize("n,have", [([130, 1, 64], [130, 300, 1000]), ([9] * 50, [(61 * i) % 700 for i in range(50)]),
+                                    ([40], [9000]), ([300], [20]), ([0, 50, 0, 0, 33], [5, 50, 700, 0, 2049])])
+@pytest.mark.parametrize("hq,hk,d", [(8, 2, 128), (4, 1, 72), (6, 2, 64), (5, 1, 96)])
+@pytest.mark.parametrize("prefix,e4m3", [(0, True), (0, False), (300, True), (77, False)])
+def test_many_rows(sv, n, have, hq, hk, d, prefix, e4m3):
+    """Several queries of each sequence: rows in tiles of 128, those of a sequence among several, cut ranges."""
+    c = Case(n, have, hq, hk, d, page=16 if hk == 1 else 64, prefix=prefix, e4m3=e4m3, seed=sum(have) + d, lead=1, tail=3, wide=8)
+    c.check(c.run(sv, mask=1, wide=8), mask=1)
+    c.check(c.run(sv, softcap=20.0, out="e4m3"), softcap=20.0, out="e4m3")
+    sv.sv_sync()
+
+
+def test_many_sequences(sv):
+    """More than 32 times 32 sequences, empty ones among them, by either kernel."""
+    for n, hq in ((1, 2), (40, 1)):
+        count = 1100
+        c = Case([n if i % 3 else 0 for i in range(count)], [(7 * i) % 50 for i in range(count)], hq, 1, 64, page=16, prefix=20, seed=n)
+        c.check(c.run(sv, mask=1), mask=1)
+    sv.sv_sync()
+
+
 def test_uneven_long_caches(sv):
     """Ranges that are cut among CTAs, beside short ones and an empty one."""
     for hq, hk, d in ((8, 2, 128), (4, 4, 72), (16, 1, 64)):
@@ -133,6 +154,24 @@ def test_large_scores(sv):
     c = Case([1, 4], [700, 300], 4, 2, 64, prefix=200, seed=9, scale_q=30.0)
     c.check(c.run(sv, mask=1), mask=1)
     sv.sv_sync()
+
+
+@pytest.mark.parametrize("e4m3", [True, False])
+@pytest.mark.parametrize("which", [0, 1])
+@pytest.mark.parametrize("cap", [0.0, 30.0])
+def test_marked_heads_among_many_rows(sv, e4m3, which, cap):
+    """The same where a sequence's rows go through tiles: rows before a marked key have no part of it."""
+    c = Case([60], [90], 4, 2, 64, prefix=200, e4m3=e4m3, seed=2)
+    want = c.run(sv, mask=1, softcap=cap).view(60, 4, 64)
+    spoiled = torch.ones(1, 2, 64, device="cuda", dtype=torch.float16)
+    spoiled[0, 1, 7] = math.nan
+    c.b.pool.store(which, *c.b.places(0, 53, 54), spoiled)  # queries 23 on see it, query heads 2 and 3 read its head
+    got = c.run(sv, mask=1, softcap=cap).view(60, 4, 64)
+    sv.sv_sync()
+    bad = torch.zeros(60, 4, dtype=torch.bool, device="cuda")
+    bad[23:, 2:] = True
+    assert torch.equal(torch.isnan(got).all(-1), bad) and torch.equal(torch.isnan(got).any(-1), bad)
+    assert torch.equal(got[:23], want[:23])
 
 
 @pytest.mark.parametrize("e4m3", [True, False])

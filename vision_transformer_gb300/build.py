@@ -17,7 +17,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libsv.so")
 SOURCES = ["api.cu", "gemm_tc.cu", "attention.cu", "elementwise.cu", "map_static.cu", "rope.cu",
-           "packed_attention.cu", "packed_few.cu", "cache.cu", "cached_attention.cu", "cached_prefix.cu"]
+           "packed_attention.cu", "packed_few.cu", "cache.cu", "cached_attention.cu", "cached_tiles.cu"]
 HEADERS = ["ptx.cuh", "sv_internal.h", "packed_attention.h", "cached.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -1,5 +1,5 @@
 // What the kernels on a paged key/value cache share (cache.cu: writing and reading it; cached_attention.cu,
-// cached_prefix.cu: attention over it).
+// cached_tiles.cu: attention over it).
 #pragma once
 #include <cuda_fp8.h>
 
@@ -79,19 +79,52 @@ struct Params {
   unsigned* counters;  // arrivals at cut items
   float* partial;      // two parts a CTA: of the item cut at the start of its share, at its end
   PrefixParts pre;
+  // Where the sequences' rows go through tiles: parts of kTileRows rows, part i + c of item i and CTA c; number and first
+  // step of each sequence's first item, then (of one behind the last) the steps of a CTA.
+  float* tiles;
+  int2* firsts;
 };
 
-// Lets a kernel have that much dynamic shared memory (set: devices, by number, that have heard so already).
+// Lets a kernel have that much dynamic shared memory (set: devices, by number, that have heard so already). ctas: so many
+// an SM are to fit, and the rest of the SM's 228 KB is to be L1; 0: as it comes.
 template <typename K>
-cudaError_t allow_shared(K kern, int bytes, unsigned long long* set) {
+cudaError_t allow_shared(K kern, int bytes, unsigned long long* set, int ctas = 0) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const unsigned long long bit = dev >= 0 && dev < kMaxAttrDevices ? 1ull << dev : 0ull;
   if ((*set & bit) && bit) return cudaSuccess;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && ctas > 0) {
+    constexpr int kAll = 228 * 1024;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, (ctas * (bytes + 1024) * 100 + kAll - 1) / kAll);
+  }
   if (e == cudaSuccess) *set |= bit;
   return e;
+}
+
+// A sequence of the call: its first row of q, its queries, own tokens. False if the offsets or the length are bad.
+struct Sequence {
+  int q0, n, have;
+};
+__device__ __forceinline__ bool sequence(const Params& p, int s, int count, Sequence& r) {
+  r = {0, 0, 0};
+  if (s >= count) return true;
+  r.q0 = row_offset(p.q_off, s, p.c.count, p.total_q);
+  const int q1 = row_offset(p.q_off, s + 1, p.c.count, p.total_q);
+  r.have = __ldg(p.c.lengths + s);
+  if (r.q0 < 0 || q1 < r.q0 || q1 > p.total_q || r.have < 0 ||
+      r.have > (static_cast<long long>(p.c.stride) << p.c.shift)) {
+    r = {0, 0, 0};
+    return false;
+  }
+  r.n = q1 - r.q0;
+  return true;
+}
+
+// Own tokens that query i of n sees.
+__device__ __forceinline__ int limit_of(int causal, int i, int n, int have) {
+  return causal ? max(0, min(have, have - n + i + 1)) : have;
 }
 
 // The query of row r of a key head (rows x group of a call are below 2^32).
@@ -99,10 +132,12 @@ __device__ __forceinline__ int query_of(const Params& p, int r) {
   return p.group == 1 ? r : int(__umulhi(unsigned(r), p.per_group));
 }
 
-// The prefix pass for many rows (cached_prefix.cu), in tiles of 128 rows and 128 keys: items of `rows` 256 or 128 rows,
-// steps of one key tile or two. grid: CTAs that have work.
-constexpr int kPrefixTile = 128;
+// Many rows (cached_tiles.cu), in tiles of 128 rows and 128 keys, results left in parts. The prefix pass: items of `rows`
+// 256 or 128 rows, steps of one key tile or two; grid: CTAs that have work. The sequences' pass: items of 128 rows,
+// steps of two key tiles.
+constexpr int kTileRows = 128;
 sv_status prefix_launch(const char* fn, const Params& p, int grid, cudaStream_t s);
+sv_status own_tiles_launch(const char* fn, const Params& p, int grid, cudaStream_t s);
 
 // Host: checks a cache and a batch, of `total` rows with or without offsets, and fills the view (its device error
 // word once the runtime is there).

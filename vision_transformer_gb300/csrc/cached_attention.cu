@@ -10,9 +10,11 @@
 // result is small). A marked key or value (byte 255) makes s_j NaN for the rows that see it, and with it the whole row;
 // its codes are 0, and every stored number is finite, so that the probability 0 of a hidden key keeps it out.
 //
-// Two passes where there is a prefix: first all rows of the batch over its keys (here in blocks of 8 or 16 rows), sums,
-// exponents and denominators to the workspace; then every sequence's rows over its own tokens, which finish with
-// the prefix's parts. Without a prefix the second alone.
+// Two passes where there is a prefix: first all rows of the batch over its keys (blocks of 8 or 16 rows here, more in
+// cached_tiles.cu), sums, exponents and denominators to the workspace; then every sequence's rows over its own tokens,
+// which finish with the prefix's parts. Without a prefix the second alone. Sequences of more than 32 rows on average go
+// through cached_tiles.cu too, and cached_join_kernel puts their parts together. The second pass here needs the first
+// only where it finishes rows: it begins while the first still runs (256 samples behind 32768 keys: 189 us to 176).
 //
 // Bound: DRAM, every key and value read once for up to 8 or 16 rows. The arithmetic runs on warp-level matrix
 // instructions (mma.sync m16n8k16, F32 accumulation): few rows fill no tcgen05 tile, and codes go from global memory to
@@ -140,30 +142,6 @@ __device__ __forceinline__ float reciprocal_of(int byte) {
   return __uint_as_float(uint32_t(127 + kNoScale - byte) << 23);
 }
 
-// A sequence of the call: its first row of q, its queries, own tokens. False if the offsets or the length are bad.
-struct Sequence {
-  int q0, n, have;
-};
-__device__ __forceinline__ bool sequence(const Params& p, int s, int count, Sequence& r) {
-  r = {0, 0, 0};
-  if (s >= count) return true;
-  r.q0 = row_offset(p.q_off, s, p.c.count, p.total_q);
-  const int q1 = row_offset(p.q_off, s + 1, p.c.count, p.total_q);
-  r.have = __ldg(p.c.lengths + s);
-  if (r.q0 < 0 || q1 < r.q0 || q1 > p.total_q || r.have < 0 ||
-      r.have > (static_cast<long long>(p.c.stride) << p.c.shift)) {
-    r = {0, 0, 0};
-    return false;
-  }
-  r.n = q1 - r.q0;
-  return true;
-}
-
-// Own tokens that query i of n sees.
-__device__ __forceinline__ int limit_of(int causal, int i, int n, int have) {
-  return causal ? max(0, min(have, have - n + i + 1)) : have;
-}
-
 // A run of steps of one item that falls into a warp's share. (Steps are counted in 32 bits: the host has seen to that.)
 struct Segment {
   Sequence seq;
@@ -171,7 +149,7 @@ struct Segment {
   int kvh, row0;      // key head, first of the item's rows (query x group + head) in the sequence
   int s0, s1, steps;  // steps of the item: this segment's, all
   int base;           // place of the item's first step among all steps
-  int item;           // (prefix pass)
+  int item;           // prefix pass: its number; else that of the sequence
 };
 
 // A warp's share of the steps. The items of the sequences in order: sequences, key heads, blocks of rows. 32 sequences at
@@ -284,7 +262,7 @@ class Share {
     x.row0 = int(item - unsigned(x.kvh) * blocks) * ROWS;
     x.s0 = at - x.base;
     x.s1 = min(st_.end - x.base, x.steps);
-    x.item = 0;
+    x.item = st_.d0 + src;
     __syncwarp();
     if (lane_ == 0) {
       st_.at = x.base + x.s1;
@@ -298,7 +276,8 @@ class Share {
   __device__ __forceinline__ bool load(int d0, int count, Sequence& q, int& blocks, int& steps) {
     const bool good = sequence(p_, d0 + lane_, count, q);
     blocks = (q.n * p_.group + ROWS - 1) / ROWS;
-    steps = max(1, (q.have + STEP - 1) / STEP);  // (a step without keys writes the prefix's result, or zeros)
+    steps = 1;
+    if constexpr (STEP > 0) steps = max(1, (q.have + STEP - 1) / STEP);  // (one without keys writes the prefix's result, or zeros)
     return good;
   }
   __device__ __forceinline__ void open(int d0, const Sequence& q, int blocks, int steps) {
@@ -939,12 +918,51 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT)) cached_few_kernel(const 
   }
 }
 
+// Behind the sequences' pass through tiles: every row's parts joined, four rows a warp at a time.
+struct JoinShared {
+  Segment segment[kWarps];
+  ShareState state[kWarps];
+  ShareTotals totals;
+  Params p;
+};
+__global__ void __launch_bounds__(kThreads) cached_join_kernel(const __grid_constant__ Params p) {
+  __shared__ JoinShared mem;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_wait();
+  pdl_launch_dependents();
+  static_assert(sizeof(Params) / 4 <= kThreads, "a word a thread");
+  if (threadIdx.x < sizeof(Params) / 4)
+    reinterpret_cast<int*>(&mem.p)[threadIdx.x] = reinterpret_cast<const int*>(&p)[threadIdx.x];
+  __syncthreads();
+  Share<4, 0> share(p, warp, lane, mem.state[warp], mem.totals);  // (items of four rows, a step each)
+  Segment& sg = mem.segment[warp];
+  while (share.get(sg)) {
+    const int rows_all = sg.seq.n * p.group, row = sg.row0;
+    const int2 first = __ldcg(p.firsts + sg.item);
+    const int chunk = __ldcg(p.firsts + p.c.count).x;
+    const int blocks = (rows_all + kTileRows - 1) / kTileRows;
+    const int steps = max(1, (sg.seq.have + 2 * kTileRows - 1) / (2 * kTileRows));
+    const int k = sg.kvh * blocks + row / kTileRows, begin = first.y + k * steps;
+    const int c0 = begin / chunk, c1 = (begin + steps - 1) / chunk, D = p.c.D, size = kTileRows * (D + 2);
+    const float* part = p.tiles + size_t(first.x + k + c0) * size_t(size);
+    __syncwarp();
+    if (lane == 0) sg.row0 = row / kTileRows * kTileRows;
+    __syncwarp();
+    settle(mem.p, sg, {part, part + size, size, c1 - c0 + 1, D, kTileRows * D, false}, row % kTileRows, 1,
+           min(4, rows_all - row), nullptr, 0);
+    __syncwarp();
+  }
+}
+
 template <int KI, int VI, bool FULL, int NT, bool E4M3, bool PREFIX>
 cudaError_t few_launch_type(const Params& p, int grid, cudaStream_t s) {
   auto kern = cached_few_kernel<KI, VI, FULL, NT, E4M3, PREFIX>;
   constexpr int kBytes = int(sizeof(FewShared<8 * NT, VI>));
   static unsigned long long set = 0;
-  const cudaError_t e = allow_shared(kern, kBytes, &set);
+  // L1 brings the sectors of a key's line together that lanes ask for one after another. Behind a tile kernel an SM kept
+  // that one's 228 KB of shared memory where it was not told: 256 samples behind 32768 keys 177 us, now 170; 16 sequences
+  // of 900 to 32768 tokens (490 MB) take 118 us beside so little L1, and 86 like this.
+  const cudaError_t e = allow_shared(kern, kBytes, &set, per_sm(NT));
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3(unsigned(grid)), dim3(kThreads), size_t(kBytes), s, p);
 }
@@ -965,38 +983,51 @@ cudaError_t few_launch(const Params& p, int grid, cudaStream_t s) {
 
 // What the host alone decides of a call.
 struct Plan {
-  int nt, grid;          // the sequences' pass: 8-row tiles of an item, CTAs at most
-  int pre_nt, pre_grid;  // the prefix's (pre_nt 0: tiles of 128 rows, cached_prefix.cu)
+  int nt, grid;          // the sequences' pass: 8-row tiles of an item (0: tiles of 128 rows, cached_tiles.cu), CTAs at most
+  size_t own;            // bytes of its parts
+  int pre_nt, pre_grid;  // the prefix's (pre_nt 0: tiles of 128 rows, cached_tiles.cu)
   PrefixParts pre;       // (its base is an offset in floats)
   size_t bytes;          // workspace
-  bool too_much;         // steps of the prefix pass
+  bool too_much;         // steps (counted in 32 bits)
 };
 Plan plan_of(const View& c, int total_q, int group, int sms) {
   Plan r = {};
   const long long rows = static_cast<long long>(total_q) * group;  // of a key head
-  r.nt = rows <= 8ll * c.count ? 1 : 2;
-  r.grid = sms * per_sm(r.nt);
-  const size_t own = size_t(kMaxSms * per_sm(r.nt)) * 2 * size_t(8 * r.nt) * size_t(c.D + 2);
-  r.bytes = kCounterBytes + 128 + own * sizeof(float);  // (parts begin on 128 bytes)
+  // Blocks of 16 rows read a sequence's keys once each, tiles of 128 rows with a slower start. 64 sequences of 2250 tokens
+  // (32 heads over 8 of 128, E4M3), blocks and tiles: 24 rows each 135 and 130 us, 32 137 and 135, 40 194 and 133; the
+  // same with 225 tokens 32 and 46, 33 and 52, 40 and 50.
+  r.nt = rows <= 8ll * c.count ? 1 : rows <= 32ll * c.count ? 2 : 0;
+  r.grid = r.nt ? sms * per_sm(r.nt) : sms;
+  const long long tokens = static_cast<long long>(c.stride) << c.shift;
+  const int block = r.nt ? 8 * r.nt : kTileRows, keys = r.nt ? 16 * groups_of(c.e4m3, c.D) : 2 * kTileRows;
+  const long long items = (rows / block + (c.count < total_q ? c.count : total_q)) * c.hk;  // (every sequence rounds up)
+  r.too_much = items * (tokens / keys + 1) >= (1ll << 30);
+  if (r.nt) {
+    r.own = size_t(kMaxSms * per_sm(r.nt)) * 2 * size_t(8 * r.nt) * size_t(c.D + 2) * sizeof(float);
+  } else {
+    r.own = size_t(items + kMaxSms) * size_t(kTileRows) * size_t(c.D + 2) * sizeof(float) +
+            (size_t(c.count + 1) * sizeof(int2) + 127) / 128 * 128;
+  }
+  r.bytes = kCounterBytes + 128 + r.own;  // (parts begin on 128 bytes)
   if (c.prefix_len > 0) {
     r.pre_nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 0;
     int step = 16 * groups_of(c.e4m3, c.D), most = sms * per_sm(r.pre_nt), at_most = kMaxSms * per_sm(r.pre_nt);
     int parts = kWarps;  // of a CTA's share: a whole number of steps each
     r.pre.rows = 8 * r.pre_nt;
     if (r.pre_nt == 0) {
-      r.pre.rows = rows <= kPrefixTile ? kPrefixTile : 2 * kPrefixTile;
-      step = rows <= kPrefixTile ? 2 * kPrefixTile : kPrefixTile;
+      r.pre.rows = rows <= kTileRows ? kTileRows : 2 * kTileRows;
+      step = rows <= kTileRows ? 2 * kTileRows : kTileRows;
       most = sms;
       at_most = kMaxSms;
       parts = 1;
     }
     r.pre.blocks = int((rows + r.pre.rows - 1) / r.pre.rows);
     r.pre.steps = (c.prefix_len + step - 1) / step;
-    const long long items = static_cast<long long>(r.pre.blocks) * c.hk, work = items * r.pre.steps;
+    const long long pre_items = static_cast<long long>(r.pre.blocks) * c.hk, work = pre_items * r.pre.steps;
     r.pre.chunk = int((work + static_cast<long long>(most) * parts - 1) / (static_cast<long long>(most) * parts) * parts);
-    r.too_much = work >= (1ll << 30);
+    r.too_much |= work >= (1ll << 30);
     r.pre_grid = int((work + r.pre.chunk - 1) / r.pre.chunk);
-    r.bytes += size_t(items + at_most) * size_t(r.pre.rows) * size_t(c.D + 2) * sizeof(float);
+    r.bytes += size_t(pre_items + at_most) * size_t(r.pre.rows) * size_t(c.D + 2) * sizeof(float);
   }
   return r;
 }
@@ -1016,10 +1047,7 @@ sv_status check(const char* fn, const sv_cache* cache, const sv_cache_batch* bat
               total_q);
     return SV_ERR_UNSUPPORTED;
   }
-  // (steps of 16 keys and blocks of 8 rows at least are counted in 32 bits)
-  const long long own = ((static_cast<long long>(total_q) * (q_heads / c->hk)) / 8 + c->count) * c->hk *
-                        ((static_cast<long long>(c->stride) << c->shift) / 16 + 1);
-  if (own >= (1ll << 31) - (1 << 20) || plan_of(*c, total_q, q_heads / c->hk, 1).too_much) {
+  if (plan_of(*c, total_q, q_heads / c->hk, 1).too_much) {
     set_error("%s: %d queries of %d heads over a prefix of %d and %d pages of %d are too many for one call", fn, total_q, q_heads,
               c->prefix_len, c->stride, 1 << c->shift);
     return SV_ERR_UNSUPPORTED;
@@ -1104,7 +1132,9 @@ sv_status sv_attention_cached(const sv_cache* cache, const sv_cache_batch* batch
   p.counters = static_cast<unsigned*>(workspace);
   p.partial = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(workspace) + kCounterBytes + 127) & ~uintptr_t(127));
   p.pre = plan.pre;
-  p.pre.base = p.partial + size_t(kMaxSms * per_sm(plan.nt)) * 2 * size_t(8 * plan.nt) * size_t(p.c.D + 2);
+  p.firsts = reinterpret_cast<int2*>(p.partial);
+  p.tiles = p.partial + (size_t(p.c.count + 1) * sizeof(int2) + 127) / 128 * 128 / sizeof(float);
+  p.pre.base = p.partial + plan.own / sizeof(float);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
   if (p.c.prefix_len > 0) {
@@ -1116,9 +1146,18 @@ sv_status sv_attention_cached(const sv_cache* cache, const sv_cache_batch* batch
       e = plan.pre_nt == 1 ? few_launch<1, true>(p, plan.pre_grid, s) : few_launch<2, true>(p, plan.pre_grid, s);
     }
   }
-  if (e == cudaSuccess) {
+  if (e == cudaSuccess && plan.nt > 0) {
     LaunchScope L(kKindAttn, 0.0, 0.0, s);
     e = plan.nt == 1 ? few_launch<1, false>(p, plan.grid, s) : few_launch<2, false>(p, plan.grid, s);
+  } else if (e == cudaSuccess) {
+    {
+      LaunchScope L(kKindAttn, 0.0, 0.0, s);
+      st = own_tiles_launch(fn, p, plan.grid, s);
+      if (st != SV_OK) return st;
+    }
+    LaunchScope L(kKindAttn, 0.0, 0.0, s);
+    const int sms = num_sms() < kMaxSms ? num_sms() : kMaxSms;
+    e = launch_pdl(cached_join_kernel, dim3(unsigned(4 * sms)), dim3(kThreads), 0, s, p);
   }
   return e == cudaSuccess ? SV_OK : cuda_fail(e, fn);
 }

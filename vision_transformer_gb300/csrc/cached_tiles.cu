@@ -1,22 +1,33 @@
-// The prefix pass of sv_attention_cached for many rows: all rows of the batch over the keys that its sequences share, on
-// the tensor cores, scores never leaving the SM.
+// The passes of sv_attention_cached for many rows, on the tensor cores, scores never leaving the SM: all rows of the batch
+// over the keys that its sequences share (the prefix pass), and sequences of several queries each over their own tokens
+// (OWN).
 //
-// A row is a query and one of the query heads of a key head (row = query x group + head); every row sees every key of
-// the prefix, so that nothing but the last tile's end is masked. For each row, in F32,
+// A row is a query and one of the query heads of a key head (row = query x group + head). Of the prefix every row sees
+// every key, so that nothing but the last tile's end is masked; of its sequence's own tokens a row sees the first
+// limit_of(). For each row, in F32,
 //   s_j = scale q . k_j, capped;  O = sum_j 2^(s_j log2 e - m) v_j,  l = sum_j 2^(s_j log2 e - m),
-// m following the running maximum, go to the workspace, a part for each CTA that has worked on the row's item
-// (PrefixParts); cached_attention.cu adds them to what the row's own tokens give.
+// m following the running maximum, go to the workspace, a part for each CTA that has worked on the row's item;
+// cached_attention.cu joins them.
 //
-// A CTA (one per SM) has two tiles of 128 rows, or, with at most 128 rows in the batch (SOLO), one whose key tiles two
+// A CTA (one per SM) has two tiles of 128 rows, or (SOLO: at most 128 rows in the batch, and OWN) one whose key tiles two
 // groups take in turn. 16 warps:
 //   warps 0..3, 4..7   softmax of group 0 and 1: a thread per row turns its S row into P (F16, over S in tensor memory);
 //   warp 8             the MMA issuer: S_w = Q_w K^T (shared memory, 128-byte swizzle), O_w += P_w V (P from tensor memory);
 //   warp 9             copies keys and values in turn, with their scale bytes, page by page (a lane each): E4M3 codes as
-//                      they lie into a ring of their own, F16 numbers by TMA into the operands' ring;
-//   warps 10..13       the operands, 32 rows of every tile a warp: codes in F16 with their factors applied (exactly, as sv_cache_read does); a
-//                      marked head becomes NaN, and with it every row; keys behind the prefix's end become zeros.
+//                      they lie into a ring of their own, F16 numbers by TMA into the operands' ring. OWN: it also works
+//                      out the CTA's share of the sequences, run by run, and hands the runs to the others;
+//   warps 10..13       the operands, 32 rows of every tile a warp: codes in F16 with their factors applied (exactly, as
+//                      sv_cache_read does). Marked ones become NaN, and with them every row; OWN, where not every row sees
+//                      every key: the key of a marked value becomes NaN in its place (the value's numbers stay 0, so
+//                      that a probability of 0 keeps it out). Keys and values behind the last one become zeros.
 //   warps 14, 15       bring Q.
 // Tensor memory: S_0, S_1, O_0, O_1 of 128 columns each.
+//
+// Two tiles of rows and 128 keys of 128 dimensions take 3,860 cycles: the products 2,048, the exponentials 2,048, shared
+// memory's traffic 2,560, the softmax of a group with its products, one behind the other, 3,400 (256 samples of 32 heads
+// over 32768 shared keys: 116 us of 178, 1,190 TFLOP/s). One tile of rows takes 3,000: the copies of codes on their way
+// (four tiles of 16 KB instead of two: 3,360 before) and their conversion (8 sequences of 15000 keys, 128 rows of 8 key
+// heads each: 96 us, 2.6 TB/s, 660 TFLOP/s).
 #include "cached.h"
 #include "packed_attention.h"
 
@@ -32,7 +43,7 @@ using packed::kHead;
 using packed::kLog2e;
 using packed::kSlack;
 
-constexpr int kTile = kPrefixTile;
+constexpr int kTile = kTileRows;
 constexpr int kBoxBytes = kTile * 128;  // 128 rows of 64 values
 // Four warpgroups, whose registers are shared out anew at the start: 2 x 128 x 176 + 2 x 128 x 80 = 512 x 128.
 constexpr int kThreads = 512;
@@ -40,21 +51,27 @@ constexpr int kSoftmaxRegs = 176, kOtherRegs = 80;
 constexpr int kLoadWarps = 4;           // warps 10..13
 constexpr int kQueryThreads = 64;       // of warps 14, 15
 constexpr uint32_t kTmemCols = 512;
+constexpr int kRunSlots = 2;            // runs between warp 9 and the others
+constexpr int kOwnTotals = 32;
 
-template <int NB, bool E4M3>
+// Operand tiles and, of E4M3, tiles of codes on their way. One tile of rows (SOLO) asks less of the tensor cores, and what
+// it waits for is the copies: more of them, fewer operands.
+template <int NB, bool E4M3, bool SOLO>
 struct Smem {
   static constexpr int kOp = NB * kBoxBytes;  // one operand tile
-  static constexpr int kStages = NB == 1 ? 8 : 4;
-  static constexpr int kRaws = E4M3 ? 4 / NB : kStages;         // tiles of codes; F16: of scale bytes alone
+  static constexpr int kStages = E4M3 && SOLO ? (NB == 1 ? 5 : 3) : (NB == 1 ? 8 : 4);
+  static constexpr int kRaws = E4M3 ? (SOLO ? 8 : 4) / NB : kStages;  // tiles of codes; F16: of scale bytes alone
   static constexpr int kRaw = E4M3 ? kTile * 64 * NB : 0;
   static constexpr int kOffRing = 2 * kOp;                      // behind Q
   static constexpr int kOffRaw = kOffRing + kStages * kOp;
-  static constexpr int kOffScales = kOffRaw + kRaws * kRaw;     // scale bytes of each tile
+  static constexpr int kOffScales = kOffRaw + kRaws * kRaw;     // scale bytes of each tile; of keys, their values' behind
   // SOLO: exponents and sums of both groups' rows, then 4 KB a softmax warp; in place of a second tile of Q where that is
   // large enough
-  static constexpr int kOffJoin = NB == 2 ? kOp : kOffScales + kRaws * kTile;
-  static constexpr int kOffBar = kOffScales + kRaws * kTile + (NB == 2 ? 0 : 8 * 4096);
-  static constexpr int kBytes = 1024 + kOffBar + 384;
+  static constexpr int kOffJoin = NB == 2 ? kOp : kOffScales + 2 * kRaws * kTile;
+  static constexpr int kOffBar = kOffScales + 2 * kRaws * kTile + (NB == 2 ? 0 : 8 * 4096);
+  static constexpr int kOffRuns = kOffBar + 448;
+  static constexpr int kOffTotals = kOffRuns + kRunSlots * 64;
+  static constexpr int kBytes = 1024 + kOffTotals + kOwnTotals * 8;
   static_assert(kBytes <= 232448, "shared memory budget");
 };
 
@@ -71,14 +88,20 @@ enum {
   kBarJoin = 40,   // SOLO: both groups' exponents and sums are in shared memory
   kBarRead = 41,   // SOLO: both have read O
   kBarDrain = 42,
-  kBarJoined = 43, // SOLO: both groups have read the other's exponents and sums
-  kNumBars = 44
+  kBarJoined = 43,  // SOLO: both groups have read the other's exponents and sums
+  kBarRun = 44,     // OWN, +slot: warp 9 has written the run
+  kBarRunDone = 46, // OWN, +slot: the other warps have read it
+  kNumBars = 48
 };
 
 // A run of steps of one item that falls into this CTA's share.
 struct Run {
-  int item, s0, s1, kvh, block;
+  int item, s0, s1, kvh;  // (s1 0: there are no more)
+  int row0;               // first of the item's rows among those of the sequence, or of the batch
+  int q0, n, have;        // first row of q, queries, keys
+  const int* pages;
 };
+// The prefix pass: all rows of the batch over one run of keys.
 struct Runs {
   int at, end;
   __device__ __forceinline__ Runs(const Params& p) {
@@ -93,10 +116,101 @@ struct Runs {
     r.s0 = at - base;
     r.s1 = min(end - base, p.pre.steps);
     r.kvh = r.item / p.pre.blocks;
-    r.block = r.item - r.kvh * p.pre.blocks;
+    r.row0 = (r.item - r.kvh * p.pre.blocks) * p.pre.rows;
+    r.q0 = 0;
+    r.n = p.total_q;
+    r.have = p.c.prefix_len;
+    r.pages = p.c.prefix_pages;
     at = base + r.s1;
     return true;
   }
+};
+// The sequences' pass, worked out by one warp: sequences, key heads, blocks of rows in order, 32 sequences at a time, one
+// per lane; every CTA has an equal, contiguous share of the steps. totals: steps and items of the first sequences, 32
+// and 32 (shared memory).
+class OwnRuns {
+ public:
+  __device__ __forceinline__ OwnRuns(const Params& p, int lane, int2* totals) : p_(p), lane_(lane), count_(p.c.count) {
+    unsigned work = 0;
+    bool bad = false;
+#pragma unroll 4
+    for (int d0 = 0; d0 < count_; d0 += 32) {
+      bad |= !load(d0);
+      const unsigned steps = __reduce_add_sync(0xffffffffu, unsigned(blocks_ * p.c.hk * steps_));
+      const unsigned items = __reduce_add_sync(0xffffffffu, unsigned(blocks_ * p.c.hk));
+      if (lane == 0 && d0 < 32 * kOwnTotals) totals[d0 / 32] = make_int2(int(steps), int(items));
+      work += steps;
+    }
+    // bad offsets or lengths: reported, and nothing is computed
+    if (__any_sync(0xffffffffu, bad)) {
+      if (lane == 0) atomicOr(p.c.err, kDevErrCache);
+      count_ = 0;
+      work = 0;
+    }
+    const unsigned chunk = max(1u, (work + gridDim.x - 1) / gridDim.x);
+    if (blockIdx.x == 0 && lane == 0) p.firsts[p.c.count] = make_int2(int(chunk), 0);
+    at_ = int(min(chunk * blockIdx.x, work));
+    end_ = int(min(unsigned(at_) + chunk, work));
+    __syncwarp();
+    int d0 = 0;
+    while (d0 + 32 < count_ && d0 < 32 * kOwnTotals && base_ + totals[d0 / 32].x <= at_) {
+      base_ += totals[d0 / 32].x;
+      items_base_ += totals[d0 / 32].y;
+      d0 += 32;
+    }
+    load(d0);
+    open();
+  }
+  __device__ __forceinline__ void get(Run& r) {
+    r = {};
+    if (at_ >= end_) return;
+    while (at_ >= base_ + total_) {
+      base_ += total_;
+      items_base_ += items_total_;
+      load(d0_ + 32);
+      open();
+    }
+    const int src = __ffs(int(__ballot_sync(0xffffffffu, base_ + incl_ > at_))) - 1;
+    auto of = [&](int v) { return __shfl_sync(0xffffffffu, v, src); };
+    const int blocks = of(blocks_), steps = of(steps_), items = blocks * p_.c.hk;
+    const int first = base_ + of(incl_) - items * steps, item0 = items_base_ + of(items_) - items;
+    const int k = (at_ - first) / steps;  // among the sequence's items
+    r.item = item0 + k;
+    r.kvh = k / blocks;
+    r.row0 = (k - r.kvh * blocks) * kTileRows;
+    r.s0 = at_ - (first + k * steps);
+    r.s1 = min(end_ - (first + k * steps), steps);
+    r.q0 = of(seq_.q0);
+    r.n = of(seq_.n);
+    r.have = of(seq_.have);
+    r.pages = p_.c.table + static_cast<long long>(d0_ + src) * p_.c.stride;
+    if (at_ == first && lane_ == 0) p_.firsts[d0_ + src] = make_int2(item0, first);  // (one run of the launch is this one)
+    at_ = first + k * steps + r.s1;
+  }
+
+ private:
+  __device__ __forceinline__ bool load(int d0) {
+    d0_ = d0;
+    const bool good = sequence(p_, d0 + lane_, count_, seq_);
+    blocks_ = (seq_.n * p_.group + kTileRows - 1) / kTileRows;
+    steps_ = max(1, (seq_.have + 2 * kTileRows - 1) / (2 * kTileRows));  // (a step without keys leaves sums of 0)
+    return good;
+  }
+  __device__ __forceinline__ void open() {
+    items_ = blocks_ * p_.c.hk;
+    incl_ = items_ * steps_;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int a = __shfl_up_sync(0xffffffffu, incl_, o), b = __shfl_up_sync(0xffffffffu, items_, o);
+      if (lane_ >= o) incl_ += a, items_ += b;
+    }
+    total_ = __shfl_sync(0xffffffffu, incl_, 31);
+    items_total_ = __shfl_sync(0xffffffffu, items_, 31);
+  }
+  const Params& p_;
+  int lane_, count_, d0_, blocks_, steps_, incl_, items_, total_, items_total_;
+  int at_, end_, base_ = 0, items_base_ = 0;
+  Sequence seq_;
 };
 
 // `bytes` (a multiple of 16, both addresses on 16) from global to shared memory, counted on an mbarrier.
@@ -119,11 +233,11 @@ __device__ __forceinline__ uint32_t chunk_at(int row, int chunk) {
 }
 
 // pages: F16 pages as a tensor of [n_pages, 2 * kv_heads * page_size (keys, then values), head_dim].
-// FULL: heads of 64 NB dimensions.
-template <int NB, bool E4M3, bool SOLO, bool CAP, bool FULL>
+// OWN (with SOLO): the sequences' rows over their own tokens; else all rows over the prefix. FULL: heads of 64 NB dimensions.
+template <int NB, bool E4M3, bool SOLO, bool OWN, bool CAP, bool FULL>
 __global__ void __launch_bounds__(kThreads, 1)
-    cached_prefix_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap pages_map) {
-  using L = Smem<NB, E4M3>;
+    cached_tile_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap pages_map) {
+  using L = Smem<NB, E4M3, SOLO>;
   constexpr int kOp = L::kOp, kStages = L::kStages, kRaws = L::kRaws;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -131,7 +245,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t bar0 = sbase + L::kOffBar;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffBar + 8 * kNumBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert(8 * kNumBars + 8 <= 384, "barrier area");
+  static_assert(8 * kNumBars + 8 <= 448 && sizeof(Run) <= 64, "barrier area");
+  static_assert(!OWN || SOLO, "one tile of rows an item");
   auto bar = [&](int i) { return bar0 + 8u * uint32_t(i); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const View& c = p.c;
@@ -156,6 +271,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar(kBarJoined), 256);
     mbar_init(bar(kBarRead), 256);
     mbar_init(bar(kBarDrain), 1);
+    for (int s = 0; s < kRunSlots; ++s) {
+      mbar_init(bar(kBarRun + s), 1);
+      mbar_init(bar(kBarRunDone + s), kThreads / 32 - 1);
+    }
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -174,12 +293,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
   pdl_launch_dependents();  // (after the wait: the next kernel relies on what came before this one)
-  const int rows_all = p.total_q * p.group;  // (below 2^26)
   auto wait = [&](int b, uint32_t parity) { return mbar_wait(bar(b), parity, abort_flag, p.c.err); };
   auto wait_all = [&](int b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)) != 0; };
 
   Runs runs(p);
   Run run = {};
+  Run* ring = reinterpret_cast<Run*>(smem + L::kOffRuns);
+  auto next_run = [&](int n) -> bool {  // run n of the CTA; false: there is none (or a wait has run out)
+    if constexpr (!OWN) return runs.get(p, run);
+    const int slot = n % kRunSlots;
+    if (!wait_all(kBarRun + slot, (n / kRunSlots) & 1)) return false;
+    run = ring[slot];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(kBarRunDone + slot));
+    return run.s1 > 0;
+  };
   // Operand tile x of a run of `count` tiles from jb on: keys, values, keys, ... of one tile after another; SOLO: the keys
   // of two tiles, their values, ...
   auto is_values = [](int x) { return ((SOLO ? x >> 1 : x) & 1) != 0; };
@@ -198,16 +326,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     float2* join = reinterpret_cast<float2*>(smem + L::kOffJoin);
     bool ok = true;
     uint32_t t = 0;  // parity of the tiles so far
-    for (int n = 0; ok && runs.get(p, run); ++n) {
+    for (int n = 0; ok && next_run(n); ++n) {
       const int j0 = SOLO ? 2 * run.s0 + w : run.s0, je = SOLO ? 2 * run.s1 : run.s1;
+      const int rows_all = run.n * p.group, row = run.row0 + (SOLO ? 0 : w * kTile) + r;  // of the sequence, or of the batch
+      // keys that the row sees
+      const int seen = OWN && row < rows_all ? limit_of(p.causal, query_of(p, row), run.n, run.have) : run.have;
       float m = -INFINITY, l = 0.0f;
       for (int j = j0; j < je; j += SOLO ? 2 : 1, t ^= 1) {
         if (!(ok = wait_all(kBarSFull + w, t))) break;
         tc_fence_after();
-        const int valid = c.prefix_len - j * kTile;  // keys of the tile
+        const int valid = seen - j * kTile;  // keys of the tile
         // (scores stay the words that tensor memory gives: the compiler may order accesses of two types as it likes)
         auto prepare = [&](uint32_t* s, int first) {  // 32 scores from column `first` on: capped, hidden ones -inf
           if constexpr (CAP) {
+            if (OWN && valid < first + 32) {  // four scores share a reciprocal: a hidden NaN must not reach the others
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (first + e >= valid) s[e] = 0u;
+            }
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
               float big[4];
@@ -301,9 +437,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       // the run's sums: a part of the row's result
-      const int row = run.block * p.pre.rows + (SOLO ? 0 : w * kTile) + r;  // among all rows
-      const int at = (SOLO ? 0 : w * kTile) + r;                             // in the part
-      float* part = p.pre.base + size_t(run.item + int(blockIdx.x)) * (size_t(p.pre.rows) * size_t(c.D + 2));
+      const int at = (SOLO ? 0 : w * kTile) + r, part_rows = SOLO ? kTile : 2 * kTile;  // in the part
+      float* part = (OWN ? p.tiles : p.pre.base) + size_t(run.item + int(blockIdx.x)) * (size_t(part_rows) * size_t(c.D + 2));
       float f0 = 1.0f, f1 = 0.0f;
       if constexpr (SOLO) {
         join[w * kTile + r] = make_float2(m, l);
@@ -321,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const bool live = row < rows_all;
       if (live && (!SOLO || w == 0))
-        __stcg(reinterpret_cast<float2*>(part + size_t(p.pre.rows) * c.D) + at, make_float2(m, l));
+        __stcg(reinterpret_cast<float2*>(part + size_t(part_rows) * c.D) + at, make_float2(m, l));
       if constexpr (SOLO) {
         // Both groups have read the other's exponents and sums: the place is the warps' to turn rows round in, so that
         // eight lanes write 128 bytes of a row (a row a lane: 6,000 cycles, more than two tiles of keys take).
@@ -377,8 +512,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // The pages of a tile's keys, a lane each (8 at most; runs of run_rows keys).
       auto pages_of = [&](int tile) -> int {
         const int number = ((tile * kTile) >> c.shift) + lane;
-        if (lane >= kTile / run_rows || number >= (c.prefix_len + page_mask) >> c.shift) return -1;
-        const int page = __ldg(c.prefix_pages + number);
+        if (lane >= kTile / run_rows || number >= (run.have + page_mask) >> c.shift) return -1;
+        const int page = __ldg(run.pages + number);
         if (unsigned(page) < unsigned(c.n_pages)) return page;
         atomicOr(c.err, kDevErrCache);
         return 0;
@@ -387,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t issued = 0, issued_phase = 0;  // copies in flight per tile of the ring, and their phase bits
       int use = 0;
       bool ok = true;
-      while (ok && runs.get(p, run)) {
+      auto copies_of = [&]() {  // of the run
         const int jb = SOLO ? 2 * run.s0 : run.s0, count = 2 * (run.s1 - run.s0) * (SOLO ? 2 : 1);
         int page = pages_of(jb);
         for (int x = 0; x < count; ++x, ++use) {
@@ -397,14 +532,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!(ok = wait_all((E4M3 ? kBarRawFree : kBarEmpty) + slot, ((use / kRaws) & 1) ^ 1))) break;
           const int copies = __popc(__ballot_sync(0xffffffffu, page >= 0));
           const uint32_t full = bar(kBarRaw + slot);
-          if (lane == 0) mbar_arrive_expect_tx(full, uint32_t(copies * run_rows * (1 + (E4M3 ? c.D : NB * 128))));
+          const bool values = is_values(x);
+          if (lane == 0) mbar_arrive_expect_tx(full, uint32_t(copies * run_rows * ((OWN && !values ? 2 : 1) + (E4M3 ? c.D : NB * 128))));
           issued |= 1u << slot;
           issued_phase = (issued_phase & ~(1u << slot)) | uint32_t((use / kRaws) & 1) << slot;
           __syncwarp();
           if (page >= 0) {
-            const int at = (tile * kTile) & page_mask, row = ((run.kvh + (is_values(x) ? c.hk : 0)) << c.shift) + at;
+            const int at = (tile * kTile) & page_mask, row = ((run.kvh + (values ? c.hk : 0)) << c.shift) + at;
             const uint8_t* from = c.pages + page * c.page_bytes;
-            bulk_load(sbase + L::kOffScales + slot * kTile + lane * run_rows, from + scale_bytes(c) + row, uint32_t(run_rows), full);
+            const uint32_t to_scales = sbase + L::kOffScales + 2 * slot * kTile + lane * run_rows;
+            bulk_load(to_scales, from + scale_bytes(c) + row, uint32_t(run_rows), full);
+            if (OWN && !values)
+              bulk_load(to_scales + kTile, from + scale_bytes(c) + (c.hk << c.shift) + row, uint32_t(run_rows), full);
             if constexpr (E4M3) {
               bulk_load(sbase + L::kOffRaw + slot * L::kRaw + lane * run_rows * c.D, from + row * c.D, uint32_t(run_rows * c.D), full);
             } else {
@@ -414,6 +553,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           page = next;
         }
+      };
+      if constexpr (OWN) {
+        OwnRuns own(p, lane, reinterpret_cast<int2*>(smem + L::kOffTotals));
+        for (int n = 0; ok; ++n) {
+          own.get(run);
+          const int slot = n % kRunSlots;
+          if (!(ok = wait_all(kBarRunDone + slot, ((n / kRunSlots) & 1) ^ 1))) break;
+          if (lane == 0) {
+            ring[slot] = run;
+            mbar_arrive(bar(kBarRun + slot));
+          }
+          __syncwarp();
+          if (run.s1 == 0) break;
+          copies_of();
+        }
+      } else {
+        while (ok && runs.get(p, run)) copies_of();
       }
       // (after a time-out: every copy issued lands before the CTA can exit)
       for (int i = 0; i < kRaws; ++i)
@@ -422,17 +578,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tid = int(threadIdx.x) - 14 * 32;
       const int per_row = FULL ? 8 * NB : c.D / 8;  // 16-byte chunks of a row
       bool ok = true;
-      for (int n = 0; ok && runs.get(p, run); ++n) {
+      for (int n = 0; ok && next_run(n); ++n) {
         if (!(ok = wait_all(kBarQEmpty, (n & 1) ^ 1))) break;
+        const int rows_all = run.n * p.group;
         const int row_step = kQueryThreads / per_row, chunk_step = kQueryThreads % per_row;
         int row = tid / per_row, chunk = tid % per_row;  // (rows of both tiles)
 #pragma unroll 8
         for (; row < (SOLO ? 1 : 2) * kTile;) {
-          const int r = run.block * p.pre.rows + row;
+          const int r = run.row0 + row;
           uint4 v = make_uint4(0u, 0u, 0u, 0u);
           if (r < rows_all) {
             const int q = query_of(p, r);
-            v = __ldg(reinterpret_cast<const uint4*>(p.q + q * p.qs + (run.kvh * p.group + (r - q * p.group)) * c.D) + chunk);
+            v = __ldg(reinterpret_cast<const uint4*>(p.q + (run.q0 + q) * p.qs + (run.kvh * p.group + (r - q * p.group)) * c.D) + chunk);
           }
           *reinterpret_cast<uint4*>(smem + (row >= kTile ? kOp : 0) + chunk_at(row & (kTile - 1), chunk)) = v;
           row += row_step;
@@ -447,16 +604,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int first = 32 * (warp - 10);  // row of the warp's piece of every tile
       int use = 0;                         // operand tiles so far
       bool ok = true;
-      while (ok && runs.get(p, run)) {
+      for (int n = 0; ok && next_run(n); ++n) {
         const int jb = SOLO ? 2 * run.s0 : run.s0, count = 2 * (run.s1 - run.s0) * (SOLO ? 2 : 1);
         constexpr int kMost = 8 * NB;  // chunks of a lane: of the rows `row`, `row` + row_step, ...
         const int row0 = lane / per_row, chunk0 = lane % per_row, row_step = 32 / per_row, chunk_step = 32 % per_row;
 #pragma unroll 1
         for (int x = 0; x < count; ++x, ++use) {
           const int slot = use % kRaws, st = use % kStages;
-          const int left = c.prefix_len - (jb + tile_of(x)) * kTile - first;  // keys of the piece
+          const int left = run.have - (jb + tile_of(x)) * kTile - first;  // keys of the piece
           if (!(ok = wait_all(kBarRaw + slot, (use / kRaws) & 1))) break;
-          const int byte = lane < left ? smem[L::kOffScales + slot * kTile + first + lane] : kNoScale;  // of row `lane`
+          // The scale byte of row `lane`. OWN: a marked value makes its key NaN, for the rows that see it.
+          const uint8_t* scales = smem + L::kOffScales + 2 * slot * kTile + first + lane;
+          int byte = lane < left ? scales[0] : kNoScale;
+          if constexpr (OWN) {
+            if (is_values(x)) byte = byte == kMarked ? kNoScale : byte;
+            else if (lane < left && scales[kTile] == kMarked) byte = kMarked;
+          }
           uint8_t* to = smem + L::kOffRing + st * kOp + first * 128;
           if constexpr (E4M3) {
             // The codes go to registers first: their ring is free for the next copy before this tile has its place.
@@ -467,7 +630,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (FULL || i < per_row) codes[i] = raw[i * 32];
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kBarRawFree + slot));
-            // (a marked head's codes are 0)
             const uint32_t power = byte == 1 ? 0x0200u : uint32_t(byte - 1) << 10;
             const uint32_t factor = byte == kMarked ? 0x7e007e00u : power << 16 | power;
             if (!(ok = wait_all(kBarEmpty + st, ((use / kStages) & 1) ^ 1))) break;
@@ -535,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto empty = [&](int ahead) { commit(kBarEmpty + (use + ahead) % kStages); };
       uint32_t tt = 0;  // parity of the groups' tiles
       bool ok = true;
-      for (int n = 0; ok && runs.get(p, run); ++n) {
+      for (int n = 0; ok && next_run(n); ++n) {
         const int count = run.s1 - run.s0;
         if (!(ok = wait_all(kBarQFull, n & 1))) break;
         if constexpr (SOLO) {
@@ -598,31 +760,29 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int NB, bool E4M3, bool SOLO, bool CAP>
+template <int NB, bool E4M3, bool SOLO, bool OWN, bool CAP>
 cudaError_t launch_as(const Params& p, const CUtensorMap& pages, int grid, cudaStream_t s) {
   // (whole heads' chunks lie where a thread need not work them out; E4M3 alone is converted)
   const bool full = E4M3 && p.c.D == 64 * NB;
-  auto kern = full ? cached_prefix_kernel<NB, E4M3, SOLO, CAP, E4M3> : cached_prefix_kernel<NB, E4M3, SOLO, CAP, false>;
+  auto kern = full ? cached_tile_kernel<NB, E4M3, SOLO, OWN, CAP, E4M3> : cached_tile_kernel<NB, E4M3, SOLO, OWN, CAP, false>;
   static unsigned long long set[2] = {0, 0};
-  const cudaError_t e = allow_shared(kern, Smem<NB, E4M3>::kBytes, &set[full]);
+  const cudaError_t e = allow_shared(kern, Smem<NB, E4M3, SOLO>::kBytes, &set[full]);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(unsigned(grid)), dim3(kThreads), size_t(Smem<NB, E4M3>::kBytes), s, p, pages);
+  return launch_pdl(kern, dim3(unsigned(grid)), dim3(kThreads), size_t(Smem<NB, E4M3, SOLO>::kBytes), s, p, pages);
 }
 
-template <int NB, bool E4M3>
-cudaError_t launch(const Params& p, const CUtensorMap& pages, int grid, cudaStream_t s) {
-  if (p.pre.rows == kTile)
-    return p.cap > 0.0f ? launch_as<NB, E4M3, true, true>(p, pages, grid, s) : launch_as<NB, E4M3, true, false>(p, pages, grid, s);
-  return p.cap > 0.0f ? launch_as<NB, E4M3, false, true>(p, pages, grid, s) : launch_as<NB, E4M3, false, false>(p, pages, grid, s);
+template <int NB, bool E4M3, bool SOLO, bool OWN>
+cudaError_t launch_cap(const Params& p, const CUtensorMap& pages, int grid, cudaStream_t s) {
+  return p.cap > 0.0f ? launch_as<NB, E4M3, SOLO, OWN, true>(p, pages, grid, s)
+                      : launch_as<NB, E4M3, SOLO, OWN, false>(p, pages, grid, s);
 }
 
-}  // namespace
-
-sv_status prefix_launch(const char* fn, const Params& p, int grid, cudaStream_t s) {
+template <bool SOLO, bool OWN>
+sv_status launch(const char* fn, const Params& p, int grid, cudaStream_t s) {
   CUtensorMap pages = {};
   cudaError_t e;
   if (p.c.e4m3) {
-    e = p.c.D > 64 ? launch<2, true>(p, pages, grid, s) : launch<1, true>(p, pages, grid, s);
+    e = p.c.D > 64 ? launch_cap<2, true, SOLO, OWN>(p, pages, grid, s) : launch_cap<1, true, SOLO, OWN>(p, pages, grid, s);
   } else {
     const uint64_t dims[3] = {uint64_t(p.c.D), uint64_t(2 * p.c.hk) << p.c.shift, uint64_t(p.c.n_pages)};
     const uint64_t strides[2] = {uint64_t(p.c.D) * 2u, uint64_t(p.c.page_bytes)};
@@ -630,9 +790,18 @@ sv_status prefix_launch(const char* fn, const Params& p, int grid, cudaStream_t 
     const sv_status st =
         make_tmap(&pages, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, p.c.pages, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
     if (st != SV_OK) return st;
-    e = p.c.D > 64 ? launch<2, false>(p, pages, grid, s) : launch<1, false>(p, pages, grid, s);
+    e = p.c.D > 64 ? launch_cap<2, false, SOLO, OWN>(p, pages, grid, s) : launch_cap<1, false, SOLO, OWN>(p, pages, grid, s);
   }
   return e == cudaSuccess ? SV_OK : cuda_fail(e, fn);
+}
+
+}  // namespace
+
+sv_status prefix_launch(const char* fn, const Params& p, int grid, cudaStream_t s) {
+  return p.pre.rows == kTile ? launch<true, false>(fn, p, grid, s) : launch<false, false>(fn, p, grid, s);
+}
+sv_status own_tiles_launch(const char* fn, const Params& p, int grid, cudaStream_t s) {
+  return launch<true, true>(fn, p, grid, s);
 }
 
 }  // namespace cached
