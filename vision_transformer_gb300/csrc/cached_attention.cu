@@ -1157,7 +1157,7 @@ sv_status sv_attention_cached(const sv_cache* cache, const sv_cache_batch* batch
     }
     LaunchScope L(kKindAttn, 0.0, 0.0, s);
     const int sms = num_sms() < kMaxSms ? num_sms() : kMaxSms;
-    e = launch_pdl(cached_join_kernel, dim3(unsigned(4 * sms)), dim3(kThreads), 0, s, p);
+    e = launch_pdl(cached_join_kernel, dim3(unsigned(8 * sms)), dim3(kThreads), 0, s, p);
   }
   return e == cudaSuccess ? SV_OK : cuda_fail(e, fn);
 }

@@ -291,8 +291,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  pdl_wait();
-  pdl_launch_dependents();  // (after the wait: the next kernel relies on what came before this one)
+  // The sequences' pass behind a prefix pass begins as soon as SMs come free of that one, whose results it does not need: what
+  // came before the two is complete, since the prefix pass lets others begin only after its own wait. It waits before it
+  // ends, for the kernel that joins the parts of both. (24 requests of 35 rows behind 2047 keys: 55 us without, 51 so.)
+  const bool early = OWN && c.prefix_len > 0;
+  if (!early) pdl_wait();
+  pdl_launch_dependents();
   auto wait = [&](int b, uint32_t parity) { return mbar_wait(bar(b), parity, abort_flag, p.c.err); };
   auto wait_all = [&](int b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)) != 0; };
 
@@ -752,6 +756,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait_bounded(bar(kBarDrain), 0, p.c.err);
     }
   }
+  if (early) pdl_wait();
   tc_fence_before();
   __syncthreads();
   if (warp == 8) {
