@@ -200,23 +200,44 @@ def test_marked_heads(sv, e4m3, which):
     assert torch.isnan(got[:, 2:]).all() and not torch.isnan(got[:, :2]).any()
 
 
-def test_query_of_nan(sv):
+@pytest.mark.parametrize("n,have,hq", [([1] * 5, [90] * 5, 4), ([5], [90], 64), ([2, 1, 2], [700, 0, 1], 64)])
+@pytest.mark.parametrize("cap", [0.0, 30.0])
+def test_query_of_nan(sv, n, have, hq, cap):
     """A query that holds an infinity or NaN spoils its own row alone."""
-    c = Case([1] * 5, [90] * 5, 4, 2, 64, prefix=140, seed=3)
-    want = c.run(sv).view(5, 4, 64)
+    c = Case(n, have, hq, 2, 64, prefix=140, seed=3)
+    want = c.run(sv, softcap=cap).view(5, hq, 64)
     c.q[2, 64 + 5] = math.nan
-    c.q[3, 3 * 64 + 1] = math.inf
-    got = c.run(sv).view(5, 4, 64)
-    bad = torch.zeros(5, 4, dtype=torch.bool, device="cuda")
+    c.q[3, 3 * 64:4 * 64] = math.nan
+    if not cap:
+        c.q[3, 3 * 64:4 * 64] = math.inf  # (keys of both signs)
+    got = c.run(sv, softcap=cap).view(5, hq, 64)
+    bad = torch.zeros(5, hq, dtype=torch.bool, device="cuda")
     bad[2, 1] = bad[3, 3] = True
     assert torch.equal(torch.isnan(got).any(-1), bad)
     assert torch.equal(got[~bad], want[~bad])
 
 
+@pytest.mark.parametrize("n,hq", [([1], 2), ([40], 2)])
+def test_query_of_infinity(sv, n, hq):
+    """Scores of minus infinity alone leave 0 / 0, as the formula has it; with one of plus infinity the row is NaN too."""
+    c = Case(n, [1], hq, 1, 64, e4m3=False, seed=3)
+    key = torch.ones(1, 1, 64, device="cuda", dtype=torch.float16)
+    key[0, 0, 1] = -1.0
+    c.b.pool.store(0, *c.b.places(0, 0, 1), key)
+    c.q[0, :64] = 0.0
+    want = c.run(sv).view(-1, hq, 64)
+    c.q[0, 0] = -math.inf
+    c.q[0, 64 + 1] = -math.inf
+    got = c.run(sv).view(-1, hq, 64)
+    assert torch.isnan(got[0]).all() and torch.equal(got[1:], want[1:])
+    sv.sv_sync()
+
+
 def test_workspace_is_left_ready(sv):
     """One workspace for calls of several sizes in turn; the same call gives the same bits."""
     cases = [Case([1] * 7, [3000, 5, 0, 800, 90, 1, 4000], 8, 2, 128, prefix=900, seed=1),
-             Case([40, 1], [300, 6000], 4, 4, 72, seed=2), Case([2] * 30, [100] * 30, 8, 1, 64, prefix=5000, seed=3)]
+             Case([40, 1], [300, 6000], 4, 4, 72, seed=2), Case([40, 1], [300, 6000], 8, 2, 128, prefix=77, seed=4),
+             Case([300], [500], 4, 2, 64, seed=5), Case([2] * 30, [100] * 30, 8, 1, 64, prefix=5000, seed=3)]
     size = max(c.workspace(sv).numel() for c in cases)
     ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
     first = [c.run(sv, ws=ws, mask=1).clone() for c in cases]
@@ -229,8 +250,9 @@ def test_workspace_is_left_ready(sv):
 
 
 @pytest.mark.parametrize("what", ["offsets", "beyond", "length", "negative"])
-def test_bad_sequences_compute_nothing(sv, what):
-    c = Case([2, 1, 1], [40, 300, 20], 4, 2, 64, prefix=50, seed=1)
+@pytest.mark.parametrize("hq", [4, 80])
+def test_bad_sequences_compute_nothing(sv, what, hq):
+    c = Case([2, 1, 1], [40, 300, 20], hq, 2, 64, prefix=50, seed=1)
     if what == "offsets":
         c.off[1] = 4
     elif what == "beyond":
@@ -245,16 +267,17 @@ def test_bad_sequences_compute_nothing(sv, what):
         sv.sv_sync()
     assert e.value.status == sv.SV_ERR_INVALID_ARG and "cache" in str(e.value)
     assert torch.isnan(o).all()
-    c = Case([2, 1, 1], [40, 300, 20], 4, 2, 64, prefix=50, seed=1)
+    c = Case([2, 1, 1], [40, 300, 20], hq, 2, 64, prefix=50, seed=1)
     c.check(c.run(sv, ws=ws))
     sv.sv_sync()
 
 
 @pytest.mark.parametrize("where", ["own", "prefix"])
 @pytest.mark.parametrize("page", [-1, 10 ** 9])
-def test_bad_pages_are_reported(sv, where, page):
+@pytest.mark.parametrize("hq", [4, 80])
+def test_bad_pages_are_reported(sv, where, page, hq):
     """The other sequences' results stand."""
-    c = Case([1, 1, 1], [100, 300, 20], 4, 2, 64, prefix=50, seed=1)
+    c = Case([1, 1, 1], [100, 300, 20], hq, 2, 64, prefix=50, seed=1)
     want = c.run(sv)
     if where == "own":
         c.b.table[1, 3] = page
@@ -268,15 +291,16 @@ def test_bad_pages_are_reported(sv, where, page):
         assert torch.equal(o[0], want[0]) and torch.equal(o[2], want[2])
 
 
-def test_streams_and_graphs(sv):
+@pytest.mark.parametrize("n", [[1] * 4, [30, 1, 9, 40]])
+def test_streams_and_graphs(sv, n):
     """Two graphs with workspaces of their own replayed side by side, lengths that grow between replays."""
-    cases = [Case([1] * 4, [200, 900, 30, 4000], 8, 2, 128, prefix=600, seed=i) for i in range(2)]
+    cases = [Case(n, [200, 900, 30, 4000], 8, 2, 128, prefix=600, seed=i) for i in range(2)]
     streams, graphs, outs = [], [], []
     for c in cases:
         c.run(sv)
         s, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
         ws = c.workspace(sv)
-        o = torch.empty(4, 8 * 128, device="cuda", dtype=torch.float16)
+        o = torch.empty(sum(n), 8 * 128, device="cuda", dtype=torch.float16)
         s.wait_stream(torch.cuda.current_stream())
         with torch.cuda.graph(g, stream=s):
             c.run(sv, ws=ws, o=o)
