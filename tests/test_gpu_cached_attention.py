@@ -91,13 +91,16 @@ def test_head_widths(sv, d, e4m3):
     c = Case([1, 2, 4], [150, 33, 290], 4, 2, d, prefix=45, e4m3=e4m3, seed=d, wide=8)
     c.check(c.run(sv, wide=16))
     c.check(c.run(sv, out="e4m3", mask=1), out="e4m3", mask=1)
+    c = Case([70], [150], 4, 2, d, prefix=130, e4m3=e4m3, seed=d, wide=8)  # through tiles
+    c.check(c.run(sv, wide=16, mask=1), mask=1)
     sv.sv_sync()
 
 
 @pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
 @pytest.mark.parametrize("hq,hk", [(1, 1), (6, 2), (5, 1), (12, 4), (16, 1), (64, 1), (33, 1), (40, 8)])
-def test_shared_heads_and_pages(sv, page, hq, hk):
-    c = Case([1, 1, 3], [70, 1, 400], hq, hk, 64, page=page, prefix=page + 3, seed=hq)
+@pytest.mark.parametrize("more", [1, 12])
+def test_shared_heads_and_pages(sv, page, hq, hk, more):
+    c = Case([more, more, 3 * more], [70, 1, 400], hq, hk, 64, page=page, prefix=page + 3, seed=hq)
     c.check(c.run(sv, mask=1), mask=1)
     sv.sv_sync()
 

@@ -928,13 +928,15 @@ struct JoinShared {
 __global__ void __launch_bounds__(kThreads) cached_join_kernel(const __grid_constant__ Params p) {
   __shared__ JoinShared mem;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  pdl_wait();
-  pdl_launch_dependents();
   static_assert(sizeof(Params) / 4 <= kThreads, "a word a thread");
   if (threadIdx.x < sizeof(Params) / 4)
     reinterpret_cast<int*>(&mem.p)[threadIdx.x] = reinterpret_cast<const int*>(&p)[threadIdx.x];
   __syncthreads();
   Share<4, 0> share(p, warp, lane, mem.state[warp], mem.totals);  // (items of four rows, a step each)
+  // Offsets and lengths are in place, since the tiles let others begin only after a wait for them (their own, or the prefix
+  // pass's); the parts are not yet.
+  pdl_wait();
+  pdl_launch_dependents();
   Segment& sg = mem.segment[warp];
   while (share.get(sg)) {
     const int rows_all = sg.seq.n * p.group, row = sg.row0;
