@@ -21,7 +21,7 @@
 //                      every key: the key of a marked value becomes NaN in its place (the value's numbers stay 0, so
 //                      that a probability of 0 keeps it out). Keys and values behind the last one become zeros.
 //   warps 14, 15       bring Q, all of it on its way at once (eight 16-byte loads a thread at a time, by way of registers:
-//                      256 samples 170 us, now 162; 64 sequences of 16 rows behind 8192 keys 32, now 30).
+//                      256 samples 170 us, now 162; 32 requests of 4 rows behind 8192 keys 32, now 30).
 // Tensor memory: S_0, S_1, O_0, O_1 of 128 columns each.
 //
 // Two tiles of rows and 128 keys of 128 dimensions take 3,860 cycles: the products 2,048, the exponentials 2,048, shared
