@@ -99,8 +99,9 @@ def test_head_widths(sv, d, e4m3):
 @pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
 @pytest.mark.parametrize("hq,hk", [(1, 1), (6, 2), (5, 1), (12, 4), (16, 1), (64, 1), (33, 1), (40, 8)])
 @pytest.mark.parametrize("more", [1, 12])
-def test_shared_heads_and_pages(sv, page, hq, hk, more):
-    c = Case([more, more, 3 * more], [70, 1, 400], hq, hk, 64, page=page, prefix=page + 3, seed=hq)
+@pytest.mark.parametrize("e4m3", [True, False])
+def test_shared_heads_and_pages(sv, page, hq, hk, more, e4m3):
+    c = Case([more, more, 3 * more], [70, 1, 400], hq, hk, 64, page=page, prefix=page + 3, e4m3=e4m3, seed=hq)
     c.check(c.run(sv, mask=1), mask=1)
     sv.sv_sync()
 
@@ -132,6 +133,17 @@ def test_many_rows(sv, n, have, hq, hk, d, prefix, e4m3):
     c = Case(n, have, hq, hk, d, page=16 if hk == 1 else 64, prefix=prefix, e4m3=e4m3, seed=sum(have) + d, lead=1, tail=3, wide=8)
     c.check(c.run(sv, mask=1, wide=8), mask=1)
     c.check(c.run(sv, softcap=20.0, out="e4m3"), softcap=20.0, out="e4m3")
+    sv.sv_sync()
+
+
+@pytest.mark.parametrize("n", [[1, 2], [40, 0, 30]])
+def test_no_own_pages(sv, n):
+    """Sequences of the prefix alone: no page table at all."""
+    c = Case(n, [0] * len(n), 4, 2, 72, prefix=150, seed=1)
+    o, ws, cache, batch = torch.full((c.total, 288), math.nan, device="cuda", dtype=torch.float16), c.workspace(sv), c.b.cache(sv), c.b.batch(sv)
+    batch.page_table, batch.table_stride = None, 0
+    sv.sv_attention_cached(cache, batch, c.q, o, c.off, c.total, 4, options=sv.sv_attention_options(mask=1), workspace=ws)
+    c.check(o, mask=1)
     sv.sv_sync()
 
 
