@@ -32,6 +32,10 @@
 // short sequences run side by side, a warp each. An item inside one share is finished there; the parts of others go to
 // shared memory, where the CTA's warps join them when all are through, and the parts of items that are cut between CTAs
 // to the workspace, where the last CTA of an item joins them in order.
+//
+// One token of 16 sequences of 900 to 32768 tokens, 32 heads of 128 over 8, E4M3 (490 MB): 85 us, 86% of the copy
+// bandwidth. Short calls are a chain of latencies: shares 2,000 cycles, segment 2,000, a step 3,000, parts 1,500, fence and
+// counter 2,000, the join 3,000 (4 sequences of up to 700 tokens: 11.8 us).
 #include <cmath>
 #include <type_traits>
 
@@ -918,7 +922,9 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT)) cached_few_kernel(const 
   }
 }
 
-// Behind the sequences' pass through tiles: every row's parts joined, four rows a warp at a time.
+// Behind the sequences' pass through tiles: every row's parts joined, four rows a warp at a time. Latency: offsets, places
+// of the parts, parts, one after another (840 rows of 4 heads of 128, two parts of each pass: 9 us alone; 4 CTAs an SM
+// instead of 8: 1 us more, 16: as much more).
 struct JoinShared {
   Segment segment[kWarps];
   ShareState state[kWarps];
