@@ -568,6 +568,8 @@ size_t sv_attention_cached_workspace(const sv_cache* cache, const sv_cache_batch
  * Its fields prefix and slopes must be NULL (SV_ERR_UNSUPPORTED). A query that sees no key gets zeros; one that sees a
  * key or value whose byte is 255 gets NaN.
  * Scores, softmax and accumulation in F32; the probabilities are rounded to F16 for their product with the values.
+ * One kernel takes all sequences, by the rows that they have on average: a batch that mixes long prompts with single
+ * queries is faster in two calls.
  * Rows of no sequence are left as they were. Bad offsets and lengths as in sv_cache_write: the call computes nothing,
  * and the next sv_sync reports SV_ERR_INVALID_ARG; page numbers outside the cache are reported too, and the results of
  * their sequences are undefined.
