@@ -1032,8 +1032,11 @@ Plan plan_of(const View& c, int total_q, int group, int sms) {
     r.pre.blocks = int((rows + r.pre.rows - 1) / r.pre.rows);
     r.pre.steps = (c.prefix_len + step - 1) / step;
     const long long pre_items = static_cast<long long>(r.pre.blocks) * c.hk, work = pre_items * r.pre.steps;
+    if (work >= (1ll << 30)) {  // (behind it 32 bits would not hold the share)
+      r.too_much = true;
+      return r;
+    }
     r.pre.chunk = int((work + static_cast<long long>(most) * parts - 1) / (static_cast<long long>(most) * parts) * parts);
-    r.too_much |= work >= (1ll << 30);
     r.pre_grid = int((work + r.pre.chunk - 1) / r.pre.chunk);
     r.bytes += size_t(pre_items + at_most) * size_t(r.pre.rows) * size_t(c.D + 2) * sizeof(float);
   }
