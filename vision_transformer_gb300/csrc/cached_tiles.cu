@@ -636,10 +636,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < kMost; ++i)
               if (FULL || i < per_row) codes[i] = raw[i * 32];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kBarRawFree + slot));
             const uint32_t power = byte == 1 ? 0x0200u : uint32_t(byte - 1) << 10;
             const uint32_t factor = byte == kMarked ? 0x7e007e00u : power << 16 | power;
+            // The next copy writes by the async proxy, which an arrival alone does not hold back behind these reads: without
+            // the fence one call of 100 (256 samples behind 32768 keys) took 32 factors from the tile behind.
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kBarRawFree + slot));
             if (!(ok = wait_all(kBarEmpty + st, ((use / kStages) & 1) ^ 1))) break;
             int row = row0, chunk = chunk0;
 #pragma unroll
