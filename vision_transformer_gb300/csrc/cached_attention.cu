@@ -366,6 +366,14 @@ __device__ __forceinline__ float2 read_shared2(uint32_t at) {
   return r;
 }
 
+// A pair in F16, at most its largest number: a mean of stored numbers is within them, and what the probabilities' rounding
+// puts above 65504 (2^-11 of it) is not an infinity. NaN stays.
+__device__ __forceinline__ uint32_t f16_within(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 // Rows r, r + step, ... (up to four, `rows` of them) of an item, by one warp: the parts of their own keys' sums joined, and
 // with the prefix's parts written in the output's type, or (put) kept as one part of part_rows rows. Eight lanes a row, 16
 // columns each; with fewer rows the lanes share out the parts. Four parts are on their way at a time: they come from L2,
@@ -496,8 +504,8 @@ __device__ __noinline__ void settle(const Params& p, const Segment& sg, const So
       const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(16.0f * z.z, 16.0f * z.w), __NV_SATFINITE, __NV_E4M3);
       *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.o) + to + column(c)) = lo | hi << 16;
     } else {
-      __half2 h[2] = {__floats2half2_rn(z.x, z.y), __floats2half2_rn(z.z, z.w)};
-      *reinterpret_cast<uint2*>(static_cast<__half*>(p.o) + to + column(c)) = *reinterpret_cast<const uint2*>(h);
+      *reinterpret_cast<uint2*>(static_cast<__half*>(p.o) + to + column(c)) =
+          make_uint2(f16_within(z.x, z.y), f16_within(z.z, z.w));
     }
   }
 }
