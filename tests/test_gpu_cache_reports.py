@@ -1,0 +1,59 @@
+"""What sv_sync says of bad calls on a cache: sequences without rows, far offsets."""
+import pytest
+import torch
+
+import cache_ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("read", [False, True])
+@pytest.mark.parametrize("count,bad", [(3, 1), (100, 0), (100, 99), (2000, 1234)])
+@pytest.mark.parametrize("length", [-1, 33, 2 ** 31 - 1])
+def test_lengths_of_sequences_without_rows(sv, read, count, bad, length):
+    """Reported as sv_attention_cached reports them; the sequences with rows are served."""
+    have = [5 + i % 7 for i in range(count)]
+    b = cache_ref.Batch(have, 16, 2, 64, prefix=20, seed=1, fill=0)
+    b.stride = 2
+    b.table = torch.nn.functional.pad(b.table, (0, 2 - b.table.shape[1]), value=-7)
+    b.fill(1)
+    n = [i % 3 for i in range(count)]
+    n[bad] = 0
+    off = torch.tensor([0] + n).cumsum(0).to(torch.int32).cuda()
+    total = sum(n)
+    rows = torch.full((total, 128), 3.0, device="cuda", dtype=torch.float16)
+    k, v = rows.clone(), rows.clone()
+    call = sv.sv_cache_read if read else sv.sv_cache_write
+    for spoiled in (False, True):
+        if spoiled:
+            b.lengths[bad] = length
+        if read:
+            k.copy_(rows), v.copy_(rows)
+        call(b.cache(sv), b.batch(sv), k, v, off, total)
+        if spoiled:
+            with pytest.raises(sv.SvError) as e:
+                sv.sv_sync()
+            assert e.value.status == sv.SV_ERR_INVALID_ARG and "cache" in str(e.value)
+        sv.sv_sync()
+        row = 0
+        for i in range(0, count, 1 if count < 200 else 61):
+            row = int(off[i])
+            for which, x in enumerate((k, v)):
+                stored = b.pool.values(which, *b.places(i, have[i] - n[i], have[i]))
+                assert torch.equal(stored.reshape(n[i], 128), x[row:row + n[i]].double())
+
+
+@pytest.mark.parametrize("read", [False, True])
+def test_offsets_of_the_last_sequences(sv, read):
+    """Offsets that decrease far behind the rows of the call's first warp."""
+    count = 1000
+    b = cache_ref.Batch([9] * count, 16, 1, 64, seed=1, fill=0)
+    b.fill(1)
+    off = (torch.arange(count + 1) // 2).to(torch.int32).cuda()
+    off[991:994] = torch.tensor([495, 494, 496], dtype=torch.int32)
+    k, v = (torch.zeros(count // 2, 64, device="cuda", dtype=torch.float16) for _ in range(2))
+    (sv.sv_cache_read if read else sv.sv_cache_write)(b.cache(sv), b.batch(sv), k, v, off, count // 2)
+    with pytest.raises(sv.SvError) as e:
+        sv.sv_sync()
+    assert e.value.status == sv.SV_ERR_INVALID_ARG and "cache" in str(e.value)
+    sv.sv_sync()

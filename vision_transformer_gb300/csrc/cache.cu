@@ -33,6 +33,11 @@ struct MoveParams {
   int total;
 };
 
+// Whether a sequence with n rows in the call, behind `first` tokens that count as its own, cannot have `have` tokens.
+__device__ __forceinline__ bool bad_length(const View& c, int have, long long n, int first) {
+  return have < 0 || have > (static_cast<long long>(c.stride) << c.shift) || n > static_cast<long long>(first) + have;
+}
+
 // Where token t of the call is kept: the first byte of its page, and its place there; false: nowhere.
 template <bool READ>
 __device__ __forceinline__ bool place_of(const MoveParams& p, int t, long long& base, int& at) {
@@ -53,8 +58,7 @@ __device__ __forceinline__ bool place_of(const MoveParams& p, int t, long long& 
   if (t < q0 || t >= q1) return false;  // a row of no sequence
   const int have = __ldg(c.lengths + s), first = READ ? c.prefix_len : 0;
   const long long n = static_cast<long long>(q1) - q0;
-  if (q0 < 0 || q1 > p.total || have < 0 || have > (static_cast<long long>(c.stride) << c.shift) ||
-      n > static_cast<long long>(first) + have) {
+  if (q0 < 0 || q1 > p.total || bad_length(c, have, n, first)) {
     atomicOr(c.err, kDevErrCache);
     return false;
   }
@@ -85,11 +89,13 @@ __global__ void __launch_bounds__(kMoveThreads) cache_kernel(const __grid_consta
   pdl_launch_dependents();
   pdl_wait();
   const unsigned unit = blockIdx.x * (kMoveThreads / 32) + (threadIdx.x >> 5);  // (below 2^31)
-  if (unit == 0 && p.off) {  // offsets that decrease or leave [0, total]
+  // Sequences, 32 a warp: offsets that decrease or leave [0, total], and lengths, of those without rows too. (Without
+  // offsets every sequence has rows.)
+  if (p.off) {
     bool bad = false;
-    for (int s = lane; s < c.count; s += 32) {
-      const int a = __ldg(p.off + s), b = __ldg(p.off + s + 1);
-      bad |= a < 0 || b < a || b > p.total;
+    for (long long s = 32ll * unit + lane; s < c.count; s += 32ll * (kMoveThreads / 32) * gridDim.x) {
+      const int a = __ldg(p.off + s), b = __ldg(p.off + s + 1), have = __ldg(c.lengths + s);
+      bad |= a < 0 || b < a || b > p.total || bad_length(c, have, static_cast<long long>(b) - a, READ ? c.prefix_len : 0);
     }
     if (bad) atomicOr(c.err, kDevErrCache);
   }
