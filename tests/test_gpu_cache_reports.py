@@ -1,4 +1,4 @@
-"""What sv_sync says of bad calls on a cache: sequences without rows, far offsets."""
+"""What sv_sync says of bad calls on a cache: sequences without rows, far offsets, errors of two kinds at once."""
 import pytest
 import torch
 
@@ -57,3 +57,23 @@ def test_offsets_of_the_last_sequences(sv, read):
         sv.sv_sync()
     assert e.value.status == sv.SV_ERR_INVALID_ARG and "cache" in str(e.value)
     sv.sv_sync()
+
+
+def test_errors_of_two_kinds(sv):
+    """Bad documents and a bad cache before one sv_sync: it names both."""
+    q = torch.zeros(4, 64, device="cuda", dtype=torch.float16)
+    o = torch.empty_like(q)
+    bad = torch.tensor([0, 3, 2, 4], dtype=torch.int32, device="cuda")
+    b = cache_ref.Batch([4, 4, 4], 16, 1, 64, seed=1, fill=0)
+    packed = lambda: sv.sv_attention_packed(q, q, q, o, bad, bad, 3, 4, 4, 1, 1, 64)
+    write = lambda: sv.sv_cache_write(b.cache(sv), b.batch(sv), q, q, bad, 4)
+    for calls, names in (((packed,), ("sv_attention_packed",)), ((write,), ("cache",)),
+                         ((packed, write), ("sv_attention_packed", "cache"))):
+        for call in calls:
+            call()
+        with pytest.raises(sv.SvError) as e:
+            sv.sv_sync()
+        assert e.value.status == sv.SV_ERR_INVALID_ARG
+        for name in ("sv_attention_packed", "cache"):
+            assert (name in str(e.value)) == (name in names)
+        sv.sv_sync()

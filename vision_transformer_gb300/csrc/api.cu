@@ -1283,9 +1283,11 @@ sv_status sv_sync(void* stream) {
   if (flag) {
     cudaMemset(g_rt.dev_err, 0, sizeof(int));
     if (!(flag & kDevErrTimeout)) {
-      set_error("%s", flag & kDevErrCache
-                          ? "a call on a cache was given bad offsets, lengths or page numbers; what they concern was not computed"
-                          : "sv_attention_packed: document offsets decrease or leave [0, total]; nothing was computed");
+      set_error("%s%s%s",
+                flag & kDevErrOffsets ? "sv_attention_packed: document offsets decrease or leave [0, total]; nothing was computed" : "",
+                (flag & kDevErrOffsets) && (flag & kDevErrCache) ? "; " : "",
+                flag & kDevErrCache
+                    ? "a call on a cache was given bad offsets, lengths or page numbers; what they concern was not computed" : "");
       return SV_ERR_INVALID_ARG;
     }
     set_error("a kernel gave up a bounded wait (device error word 0x%x); its outputs are undefined", flag);
