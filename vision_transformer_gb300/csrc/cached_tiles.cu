@@ -54,6 +54,9 @@ constexpr int kQueryThreads = 64;       // of warps 14, 15
 constexpr uint32_t kTmemCols = 512;
 constexpr int kRunSlots = 2;            // runs between warp 9 and the others
 constexpr int kOwnTotals = 32;
+// Steps of a run at most. The tensor cores add to O by truncation: up to 16384 keys an accumulator its sums lose 1e-4 (with
+// 2^20 they lost 6.6e-3, and with 2^28 equal ones stopped growing). What an item's runs leave behind is added up in F32.
+constexpr int kMostSteps = 128;
 
 // Operand tiles and, of E4M3, tiles of codes on their way. One tile of rows (SOLO) asks less of the tensor cores, and what
 // it waits for is the copies: more of them, fewer operands.
@@ -100,14 +103,15 @@ struct Run {
   int item, s0, s1, kvh;  // (s1 0: there are no more)
   int row0;               // first of the item's rows among those of the sequence, or of the batch
   int q0, n, have;        // first row of q, queries, keys
+  int again;              // the CTA's run before was of the same item: its sums are in the part
   const int* pages;
 };
 // The prefix pass: all rows of the batch over one run of keys.
 struct Runs {
-  int at, end;
+  int at, end, begin;
   __device__ __forceinline__ Runs(const Params& p) {
     const int work = p.pre.blocks * p.c.hk * p.pre.steps;
-    at = p.pre.chunk * int(blockIdx.x);
+    begin = at = p.pre.chunk * int(blockIdx.x);
     end = min(at + p.pre.chunk, work);
   }
   __device__ __forceinline__ bool get(const Params& p, Run& r) {
@@ -115,7 +119,8 @@ struct Runs {
     r.item = at / p.pre.steps;
     const int base = r.item * p.pre.steps;
     r.s0 = at - base;
-    r.s1 = min(end - base, p.pre.steps);
+    r.s1 = min(min(end - base, p.pre.steps), r.s0 + kMostSteps);
+    r.again = r.s0 > 0 && at > begin;
     r.kvh = r.item / p.pre.blocks;
     r.row0 = (r.item - r.kvh * p.pre.blocks) * p.pre.rows;
     r.q0 = 0;
@@ -150,7 +155,7 @@ class OwnRuns {
     }
     const unsigned chunk = max(1u, (work + gridDim.x - 1) / gridDim.x);
     if (blockIdx.x == 0 && lane == 0) p.firsts[p.c.count] = make_int2(int(chunk), 0);
-    at_ = int(min(chunk * blockIdx.x, work));
+    begin_ = at_ = int(min(chunk * blockIdx.x, work));
     end_ = int(min(unsigned(at_) + chunk, work));
     __syncwarp();
     int d0 = 0;
@@ -180,7 +185,8 @@ class OwnRuns {
     r.kvh = k / blocks;
     r.row0 = (k - r.kvh * blocks) * kTileRows;
     r.s0 = at_ - (first + k * steps);
-    r.s1 = min(end_ - (first + k * steps), steps);
+    r.s1 = min(min(end_ - (first + k * steps), steps), r.s0 + kMostSteps);
+    r.again = r.s0 > 0 && at_ > begin_;
     r.q0 = of(seq_.q0);
     r.n = of(seq_.n);
     r.have = of(seq_.have);
@@ -210,7 +216,7 @@ class OwnRuns {
   }
   const Params& p_;
   int lane_, count_, d0_, blocks_, steps_, incl_, items_, total_, items_total_;
-  int at_, end_, base_ = 0, items_base_ = 0;
+  int at_, end_, begin_, base_ = 0, items_base_ = 0;
   Sequence seq_;
 };
 
@@ -465,29 +471,42 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the run's sums: a part of the row's result
       const int at = (SOLO ? 0 : w * kTile) + r, part_rows = SOLO ? kTile : 2 * kTile;  // in the part
       float* part = (OWN ? p.tiles : p.pre.base) + size_t(run.item + int(blockIdx.x)) * (size_t(part_rows) * size_t(c.D + 2));
-      float f0 = 1.0f, f1 = 0.0f;
+      float2* exponents = reinterpret_cast<float2*>(part + size_t(part_rows) * c.D) + at;
+      const bool live = row < rows_all;
+      // factors on the groups' O (SOLO; else on the group's own) and on what the item's run before has left
+      float f0 = 1.0f, f1 = 0.0f, keep = 0.0f;
+      float2 before = make_float2(-INFINITY, 0.0f);
+      if (run.again && live) before = __ldcg(exponents);
       if constexpr (SOLO) {
         join[w * kTile + r] = make_float2(m, l);
         mbar_arrive(bar(kBarJoin));
         if (!(ok = wait_all(kBarJoin, n & 1) && wait_all(kBarOFull, n & 1) && wait_all(kBarOFull + 1, n & 1))) break;
         const float2 a = join[r], b = join[kTile + r];
-        m = fmaxf(a.x, b.x);
+        m = fmax3(a.x, b.x, before.x);
         const float ref = m == -INFINITY ? 0.0f : m;
         f0 = ex2(a.x - ref);
         f1 = ex2(b.x - ref);
-        l = fmaf(f1, b.y, f0 * a.y);
+        keep = ex2(before.x - ref);
+        l = fmaf(keep, before.y, fmaf(f1, b.y, f0 * a.y));
       } else {
         if (!(ok = wait_all(kBarOFull + w, n & 1))) break;
+        if (run.again) {
+          const float up = fmaxf(m, before.x), ref = up == -INFINITY ? 0.0f : up;
+          f0 = ex2(m - ref);
+          keep = ex2(before.x - ref);
+          l = fmaf(keep, before.y, f0 * l);
+          m = up;
+        }
+        if (live) __stcg(exponents, make_float2(m, l));
       }
       tc_fence_after();
-      const bool live = row < rows_all;
-      if (live && (!SOLO || w == 0))
-        __stcg(reinterpret_cast<float2*>(part + size_t(part_rows) * c.D) + at, make_float2(m, l));
       if constexpr (SOLO) {
-        // Both groups have read the other's exponents and sums: the place is the warps' to turn rows round in, so that
-        // eight lanes write 128 bytes of a row (a row a lane: 6,000 cycles, more than two tiles of keys take).
+        // Both groups have read the other's exponents and sums, and those of the run before: the place is the warps' to turn
+        // rows round in, so that eight lanes write 128 bytes of a row (a row a lane: 6,000 cycles, more than two tiles of
+        // keys take).
         mbar_arrive(bar(kBarJoined));
         if (!(ok = wait_all(kBarJoined, n & 1))) break;
+        if (live && w == 0) __stcg(exponents, make_float2(m, l));
         uint8_t* stage = smem + L::kOffJoin + warp * 4096;
 #pragma unroll 1
         for (int d = 32 * w; d < Dn; d += 64) {  // every second 32 columns
@@ -503,6 +522,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             *reinterpret_cast<uint4*>(stage + lane * 128 + ((u ^ (lane & 7)) << 4)) =
                 make_uint4(a[4 * u], a[4 * u + 1], a[4 * u + 2], a[4 * u + 3]);
           __syncwarp();
+          if (run.again)  // what this lane has written there, added in the place where it reads next
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) {
+              const int x = 4 * i + (lane >> 3), u = lane & 7;
+              const float k = __shfl_sync(0xffffffffu, keep, x);
+              if (row - lane + x >= rows_all || d + 4 * u >= c.D) continue;
+              const float4 z = __ldcg(reinterpret_cast<const float4*>(part + size_t(at - lane + x) * c.D + d + 4 * u));
+              float4& y = *reinterpret_cast<float4*>(stage + x * 128 + ((u ^ (x & 7)) << 4));
+              y = make_float4(fmaf(k, z.x, y.x), fmaf(k, z.y, y.y), fmaf(k, z.z, y.z), fmaf(k, z.w, y.w));
+            }
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int x = 4 * i + (lane >> 3), u = lane & 7;  // row of the warp, 16 bytes of it
@@ -522,6 +551,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld_wait();
 #pragma unroll
           for (int e = 0; e < 16; ++e) asm volatile("" : "+r"(a[e]));  // no use before the wait
+          if (run.again && live) {
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+              if (e == 8 && d + 8 >= c.D) break;
+              const float4 z = __ldcg(reinterpret_cast<const float4*>(part + size_t(at) * c.D + d + e));
+              a[e] = __float_as_uint(fmaf(keep, z.x, f0 * __uint_as_float(a[e])));
+              a[e + 1] = __float_as_uint(fmaf(keep, z.y, f0 * __uint_as_float(a[e + 1])));
+              a[e + 2] = __float_as_uint(fmaf(keep, z.z, f0 * __uint_as_float(a[e + 2])));
+              a[e + 3] = __float_as_uint(fmaf(keep, z.w, f0 * __uint_as_float(a[e + 3])));
+            }
+          }
           if (live) {
             store8(part + size_t(at) * c.D + d, a);
             if (d + 8 < c.D) store8(part + size_t(at) * c.D + d + 8, a + 8);
