@@ -1,4 +1,6 @@
 """sv_attention_cached at the ends of its range: results at the end of F16's, keys by the hundred million."""
+import math
+
 import pytest
 import torch
 
@@ -54,33 +56,46 @@ def test_hundreds_of_millions_of_keys(sv, own):
     assert torch.equal(o, v[:1].expand(rows, d))
 
 
-@pytest.mark.parametrize("kind", ["prefix", "prefix of one tile", "own"])
+@pytest.mark.parametrize("kind", ["prefix", "prefix of one tile", "own", "few", "few cut", "few over the prefix"])
 @pytest.mark.parametrize("lg", [15, 17, 20])
 @pytest.mark.parametrize("d,e4m3", [(64, False), (72, True), (128, True)])
 def test_sums_over_many_keys(sv, kind, lg, d, e4m3):
-    """Sums of the tensor cores, which truncate, are short: 2^lg keys of one CTA by way of one page, listed again and again.
+    """Sums of the tensor cores, which truncate, are short: 2^lg keys of one CTA or warp (of several: cut) by way of one page,
+    listed again and again.
 
     A product of 16 keys is added in two parts at most, each addition losing less than 2^-23 of the sum; over 16384 keys
     2^-12, beside the errors of bound()."""
-    page, hk = 256, 152 if kind == "prefix of one tile" else 1
-    rows = {"prefix": 152 * 256, "prefix of one tile": 100, "own": 152 * 128}[kind]
+    page, count, n = 256, 1, 1
+    hk = {"prefix of one tile": 152, "few over the prefix": 1824}.get(kind, 1)
+    if kind in ("few", "few cut"):
+        count, n = (1824, 1) if kind == "few" else (100, 2)
+    rows = {"prefix": 152 * 256, "prefix of one tile": 100, "own": 152 * 128, "few over the prefix": 1}.get(kind, count * n)
     c = Case([1], [page], hk, hk, d, page=page, e4m3=e4m3, seed=lg)
-    places = c.b.places(0, 0, page)
     g = torch.Generator("cuda").manual_seed(2)
+    places = c.b.places(0, 0, page)
     c.b.pool.store(1, *places, (1 + torch.rand(page, hk, d, generator=g, device="cuda")).half())  # all of one sign
     n_keys = 2 ** lg
-    pages = torch.full((n_keys // page,), int(c.b.table[0, 0]), dtype=torch.int32, device="cuda")
-    own = kind == "own"
-    lengths = torch.full((1,), n_keys if own else 0, dtype=torch.int32, device="cuda")
-    batch = sv.sv_cache_batch(1, pages, len(pages) if own else 0, lengths, None if own else pages, 0 if own else n_keys)
+    pages = torch.full((count, n_keys // page), int(c.b.table[0, 0]), dtype=torch.int32, device="cuda")
+    own = "prefix" not in kind
+    lengths = torch.full((count,), n_keys if own else 0, dtype=torch.int32, device="cuda")
+    batch = sv.sv_cache_batch(count, pages, n_keys // page if own else 0, lengths, None if own else pages, 0 if own else n_keys)
     cache = c.b.cache(sv)
     q = torch.randn(rows, hk * d, generator=g, device="cuda").half()
     o = torch.empty_like(q)
     ws = torch.zeros(sv.sv_attention_cached_workspace(cache, batch, rows, hk), dtype=torch.uint8, device="cuda")
-    sv.sv_attention_cached(cache, batch, q, o, None, rows, hk, workspace=ws)
+    mask = 1 if kind == "few cut" else 0
+    sv.sv_attention_cached(cache, batch, q, o, None, rows, hk, options=sv.sv_attention_options(mask=mask), workspace=ws)
     sv.sv_sync()
     k, v = c.b.sequence(0, 0), c.b.sequence(0, 1)
     some = torch.arange(0, rows, max(1, rows // 500), device="cuda")
-    ref, a, terms = cache_ref.attention(q[some].view(-1, hk, d), k, v, page, False)
-    tol = cache_ref.bound(ref, a, terms, page, float(v.abs().max()), d) + 2.0 ** -12 * a
+    x = q[some].view(-1, hk, d)
+    times = torch.full((len(some), 1, page), n_keys / page, dtype=torch.float64, device="cuda")  # a key's in the sequence
+    if mask:  # the first query of two does not see the last key
+        times[some % 2 == 0, :, -1] -= 1
+    s = torch.einsum("rhd,khd->rhk", x.double(), k) / math.sqrt(d)
+    terms = (torch.einsum("rhd,khd->rhk", x.double().abs(), k.abs()) / math.sqrt(d)).amax(-1, keepdim=True)
+    p = times * torch.exp(s - s.amax(-1, keepdim=True))
+    ref = torch.einsum("rhk,khd->rhd", p / p.sum(-1, keepdim=True), v)
+    # (values of one sign: sum p |v| is the result)
+    tol = cache_ref.bound(ref, ref, terms, page, float(v.abs().max()), d) + 2.0 ** -12 * ref
     assert ((o[some].double().view(ref.shape) - ref).abs() <= tol).all()

@@ -62,6 +62,9 @@ constexpr size_t kCounterBytes = (size_t(kMaxGrid) * sizeof(unsigned) + 127) / 1
 // CTAs an SM, by what the registers of a warp allow
 constexpr int per_sm(int nt) { return nt > 1 ? 2 : 3; }
 constexpr int kWarps = kThreads / 32;
+// Keys that an accumulator sums up at most. The tensor cores add by truncation: the sums of 16384 keys lose 1e-4 (those of a
+// million lost 6.6e-3); a warp's part in shared memory takes them in F32.
+constexpr int kMostKeys = 16384;
 // 16-key groups of a warp's step: what the registers of a key and a value in flight hold
 constexpr int groups_of(bool e4m3, int head_dim) { return (e4m3 ? 2 : 1) * (head_dim > 64 ? 1 : 2); }
 
@@ -152,6 +155,7 @@ struct Segment {
   const int* pages;   // of its keys
   int kvh, row0;      // key head, first of the item's rows (query x group + head) in the sequence
   int s0, s1, steps;  // steps of the item: this segment's, all
+  int at;             // first of the present piece's, kMostKeys keys of the segment
   int base;           // place of the item's first step among all steps
   int item;           // prefix pass: its number; else that of the sequence
 };
@@ -266,6 +270,7 @@ class Share {
     x.row0 = int(item - unsigned(x.kvh) * blocks) * ROWS;
     x.s0 = at - x.base;
     x.s1 = min(st_.end - x.base, x.steps);
+    x.at = x.s0;
     x.item = st_.d0 + src;
     __syncwarp();
     if (lane_ == 0) {
@@ -331,6 +336,7 @@ class PrefixShare {
     x.base = x.item * p_.pre.steps;
     x.s0 = at - x.base;
     x.s1 = min(end - x.base, x.steps);
+    x.at = x.s0;
     __syncwarp();
     if (lane_ == 0) {
       st_.at = x.base + x.s1;
@@ -569,10 +575,20 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT)) cached_few_kernel(const 
   };
 
   Segment& sg = mem.segment[warp];
-  while (share.get(sg)) {
+  constexpr int kMostSteps = kMostKeys / kStep;
+  bool more_pieces = false;
+  auto next = [&]() -> bool {  // the segment's next piece, or the next segment
+    if (!more_pieces) return share.get(sg);
+    __syncwarp();
+    if (lane == 0) sg.at += kMostSteps;
+    __syncwarp();
+    return true;
+  };
+  while (next()) {
+    more_pieces = sg.at + kMostSteps < sg.s1;
     const int rows_all = sg.seq.n * p.group;  // of the sequence (for this key head)
-    // keys of this segment that one of its rows sees end here (the last row sees the most)
-    int last = min(sg.s1 * kStep, sg.seq.have);
+    // keys of this piece that one of its rows sees end here (the last row sees the most)
+    int last = min(min(sg.s1, sg.at + kMostSteps) * kStep, sg.seq.have);
     if constexpr (!PREFIX)
       last = min(last, limit_of(p.causal, query_of(p, min(sg.row0 + kRows, rows_all) - 1), sg.seq.n, sg.seq.have));
     // and the keys that all of them see end here
@@ -599,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT)) cached_few_kernel(const 
       }
     }
 
-    // Pages of the segment's keys, a lane each: 32 from number first_page on, and the 32 behind them. (Looked up key by
+    // Pages of the piece's keys, a lane each: 32 from number first_page on, and the 32 behind them. (Looked up key by
     // key, a step's loads waited for L2 first: 107 us for one token of 16 requests over up to 32768 keys.)
     auto page_of = [&](int number) -> int {
       if (number >= (last + page_mask) >> c.shift) return 0;
@@ -608,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT)) cached_few_kernel(const 
       atomicOr(c.err, kDevErrCache);
       return 0;
     };
-    int first_page = (sg.s0 * kStep) >> c.shift;
+    int first_page = (sg.at * kStep) >> c.shift;
     int here = page_of(first_page + lane), there = page_of(first_page + 32 + lane);
     const uint8_t* const head_at = c.pages + static_cast<long long>(sg.kvh << c.shift) * (D * kEs);
     const uint8_t* const scales_at = c.pages + to_scales + ((sg.kvh + (lane >> 4) * c.hk) << c.shift) + (lane & 15);
@@ -675,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT)) cached_few_kernel(const 
       l[n][0] = l[n][1] = 0.0f;
     }
 
-    int key0 = sg.s0 * kStep;
+    int key0 = sg.at * kStep;
     auto look_up = [&](int key) {
       if ((key >> c.shift) - first_page >= 32) {
         first_page += 32;
@@ -691,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT)) cached_few_kernel(const 
     // (the first step's loads and the others' are one piece of code: a short segment waits for its instructions)
 #pragma unroll 1
     for (key0 -= kStep;; key0 += kStep) {
-      const bool some = key0 >= sg.s0 * kStep, more = key0 + kStep < last;
+      const bool some = key0 >= sg.at * kStep, more = key0 + kStep < last;
       float s[kSub][NT][4];
       int byte[kSub];
       if (some) {
@@ -852,6 +868,28 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT)) cached_few_kernel(const 
     const bool whole = sg.s0 == 0 && sg.s1 == sg.steps;
     const int rows = min(kRows, rows_all - sg.row0);
     Part<kRows, VI>& mine = mem.part[warp][sg.s0 == 0 ? 1 : 0];
+    if (sg.at > sg.s0) {  // to those of the pieces before, which this lane has written (m and l: the lanes of a row)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = 8 * n + 2 * t + e;
+          const float2 before = mine.ml[r];
+          const float up = fmaxf(m[n][e], before.x), ref = up == -INFINITY ? 0.0f : up;
+          const float f = ex2(m[n][e] - ref), keep = ex2(before.x - ref);
+          m[n][e] = up;
+          l[n][e] = f * l[n][e] + (g == 0 ? keep * before.y : 0.0f);
+#pragma unroll
+          for (int j = 0; j < 4 * VI; j += 2) {
+            const float4 z = *reinterpret_cast<const float4*>(&mine.y[r][value_run(j >> 2, g) + 2 * (j & 3)]);
+            o[n][j][e] = fmaf(keep, z.x, f * o[n][j][e]);
+            o[n][j][e + 2] = fmaf(keep, z.y, f * o[n][j][e + 2]);
+            o[n][j + 1][e] = fmaf(keep, z.z, f * o[n][j + 1][e]);
+            o[n][j + 1][e + 2] = fmaf(keep, z.w, f * o[n][j + 1][e + 2]);
+          }
+        }
+      __syncwarp();
+    }
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -869,7 +907,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT)) cached_few_kernel(const 
       }
     if (!whole && lane == 0) mem.cut[warp][sg.s0 == 0 ? 1 : 0] = sg;
     __syncwarp();
-    if (whole) {
+    if (whole && !more_pieces) {
       pdl_wait();
 #pragma unroll 1
       for (int r = 0; r < rows; r += 4)
