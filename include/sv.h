@@ -551,10 +551,10 @@ sv_status sv_cache_read(const sv_cache* cache, const sv_cache_batch* batch, void
 
 /*
  * Bytes of workspace that sv_attention_cached needs for these sizes, whatever the lengths and the GPU: with at most 32
- * rows (queries times q_heads / kv_heads) a sequence on average up to 40 MB; with more about 4 (head_dim + 2) for each
- * of the total_q * q_heads rows, rounded up to 128 for every sequence and key head, and up to 11 MB; with a prefix up to
- * 21 MB more and 4 (head_dim + 2) for each of the rows, rounded up to 256 for every key head. 0: refused, or nothing to
- * do. Host only.
+ * rows (queries times q_heads / kv_heads) a sequence on average up to 5.1 MB; with more about 4 (head_dim + 2) for each
+ * of the total_q * q_heads rows, rounded up to 128 for every sequence and key head, 8 for each sequence, and up to 11 MB;
+ * with a prefix up to 21 MB more and 4 (head_dim + 2) for each of the rows, rounded up to 256 for every key head. 0:
+ * refused, or nothing to do. Host only.
  */
 size_t sv_attention_cached_workspace(const sv_cache* cache, const sv_cache_batch* batch, int total_q, int q_heads);
 
@@ -573,8 +573,9 @@ size_t sv_attention_cached_workspace(const sv_cache* cache, const sv_cache_batch
  * Rows of no sequence are left as they were. Bad offsets and lengths as in sv_cache_write: the call computes nothing,
  * and the next sv_sync reports SV_ERR_INVALID_ARG; page numbers outside the cache are reported too, and the results of
  * their sequences are undefined.
- * workspace: sv_attention_cached_workspace() bytes of device memory (0: NULL will do), 16-byte aligned, zeroed before
- * the first use by this function; rules as in sv_attention_packed. The same call gives the same bits every time.
+ * workspace: sv_attention_cached_workspace() bytes of device memory (0: NULL will do), 16-byte aligned, the first 4096 of
+ * them zeroed before the first use by this function; rules as in sv_attention_packed. The same call gives the same bits
+ * every time.
  * Requirements: as sv_cache_write; q_heads / kv_heads <= 64, q_heads <= 65536; 1 <= count <= 2^24; total_q * q_heads
  * at most 2^26; the keys that the prefix and table_stride allow, in steps of 16 or more, times blocks of rows, below
  * 2^30 (a decoding step of 256 sequences and 8 key heads: over a million own tokens each).

@@ -39,3 +39,15 @@ def test_prefix_steps_beyond_the_limit(vt, p, total, prefix, heads):
 def test_prefix_steps_within_the_limit(vt, p, total, prefix):
     cache = vt.sv_cache(p, 4, 16, 1, 8)
     assert vt.sv_attention_cached_workspace(cache, vt.sv_cache_batch(1, p, 1, p, p, prefix), total, 1) > 0
+
+
+@pytest.mark.parametrize("count,total,heads,kv_heads,dim", [(16, 16, 32, 8, 128), (16, 128, 32, 8, 128), (1, 1, 1, 1, 8), (256, 2048, 8, 8, 128),
+                                                            (7, 33, 28, 4, 72), (2, 1, 64, 1, 128)])
+@pytest.mark.parametrize("prefix", [0, 1, 5000])
+def test_workspace_of_few_rows(vt, p, count, total, heads, kv_heads, dim, prefix):
+    """At most 32 rows a sequence on average: 5.1 MB and what a prefix adds; never less than the counters' 4096 bytes."""
+    rows = total * heads // kv_heads
+    assert rows <= 32 * count
+    size = vt.sv_attention_cached_workspace(vt.sv_cache(p, 4, 16, kv_heads, dim), vt.sv_cache_batch(count, p, 3, p, p, prefix), total, heads)
+    blocks = -(-rows // 256) * 256 * kv_heads
+    assert 4096 <= size <= 5.1e6 + (21e6 + blocks * 4 * (dim + 2) if prefix else 0)

@@ -83,3 +83,16 @@ def test_pages_behind_32_bits(sv, n, e4m3):
     c = Case(n, [600, 30], 16, 8, 128, page=256, prefix=300, e4m3=e4m3, seed=1, first_page=(5 << 30) // size)
     c.check(c.run(sv, mask=1), mask=1)
     sv.sv_sync()
+
+
+@pytest.mark.parametrize("n,have", [FEW, ONE, TWO])
+def test_workspace_behind_its_counters(sv, n, have):
+    """Only the first 4096 bytes have to be zero before the first use."""
+    c = Case(n, have, 8, 2, 128, prefix=700, seed=3)
+    ws = c.workspace(sv)
+    want = c.run(sv, ws=ws, mask=1)
+    other = torch.full_like(ws, 0xFF)
+    other[:4096] = 0
+    assert torch.equal(c.run(sv, ws=other, mask=1), want)
+    assert torch.equal(c.run(sv, ws=other, mask=1), want)
+    sv.sv_sync()
