@@ -42,7 +42,7 @@ def test_prefix_steps_within_the_limit(vt, p, total, prefix):
 
 
 @pytest.mark.parametrize("count,total,heads,kv_heads,dim", [(16, 16, 32, 8, 128), (16, 128, 32, 8, 128), (1, 1, 1, 1, 8), (256, 2048, 8, 8, 128),
-                                                            (7, 33, 28, 4, 72), (2, 1, 64, 1, 128)])
+                                                            (7, 32, 28, 4, 72), (2, 1, 64, 1, 128)])
 @pytest.mark.parametrize("prefix", [0, 1, 5000])
 def test_workspace_of_few_rows(vt, p, count, total, heads, kv_heads, dim, prefix):
     """At most 32 rows a sequence on average: 5.1 MB and what a prefix adds; never less than the counters' 4096 bytes."""
