@@ -489,7 +489,8 @@ sv_status sv_attention_packed(const void* q, const void* k, const void* v, void*
  *   keys   [kv_heads, page_size, head_dim], f16 or E4M3 codes (dtype), then
  *   values [kv_heads, page_size, head_dim], then
  *   a byte for every key [kv_heads, page_size], then for every value: b stands for the factor 2^(b - 16) on the
- *   head's stored numbers, 255 for a head that held an infinity or NaN.
+ *   head's stored numbers, 255 for a head that held an infinity or NaN. E4M3 heads have 1 .. 24 or 255, F16 heads 16 or
+ *   255; what other bytes, which no call writes, do to the results of queries that see them is not defined.
  * E4M3: the stored number is the OCP E4M3 code (e4m3fn) of x / 2^e, rounded to nearest even, where e is the least
  * exponent in -15 .. 8 with which the head's largest magnitude is at most 448 * 2^e (with e = 8 magnitudes end at
  * 61440 = 240 * 2^8, since 256 * 2^8 is beyond F16); a factor for each token and head, as its keys and values
@@ -567,7 +568,8 @@ size_t sv_attention_cached_workspace(const sv_cache* cache, const sv_cache_batch
  * sequence's own tokens j <= lengths[s] - n + i (n may exceed lengths[s]: the first queries then see the prefix alone).
  * Its fields prefix and slopes must be NULL (SV_ERR_UNSUPPORTED). A query that sees no key gets zeros; one that sees a
  * key or value whose byte is 255 gets NaN.
- * Scores, softmax and accumulation in F32; the probabilities are rounded to F16 for their product with the values.
+ * Scores, softmax and accumulation in F32; the probabilities (few rows: times the value's factor) are rounded to F16 for
+ * their product with the values, and below 2^-22 of the row's largest they keep fewer bits.
  * One kernel takes all sequences, by the rows that they have on average: a batch that mixes long prompts with single
  * queries is faster in two calls.
  * Rows of no sequence are left as they were. Bad offsets and lengths as in sv_cache_write: the call computes nothing,
@@ -612,6 +614,8 @@ long long sv_launch_count(void);
  * kernel class (0 GEMM, 1 attention, 2 LayerNorm, 3 MAP attention, 4 other),
  * the summed device milliseconds, the algorithmic FLOPs and bytes of those
  * launches and their count, then resets that class. It synchronises the device.
+ * sv_attention_packed and sv_attention_cached count no FLOPs and bytes: how long
+ * their sequences are is known on the device alone.
  */
 sv_status sv_profile_enable(int on);
 sv_status sv_profile_read(int kind, double* ms, double* flops, double* bytes, long long* launches);

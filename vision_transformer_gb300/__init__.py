@@ -42,7 +42,6 @@ class SvAttentionOptions(ctypes.Structure):
                 ("prefix", ctypes.c_void_p), ("slopes", ctypes.c_void_p)]
 
 
-
 class SvCache(ctypes.Structure):
     """sv_cache, see :func:`sv_cache`."""
     _fields_ = [("pages", ctypes.c_void_p), ("n_pages", ctypes.c_int), ("page_size", ctypes.c_int),

@@ -71,7 +71,7 @@ struct Params {
   const __half* q;
   void* o;
   const int* q_off;
-  int total_q, hq, group;
+  int total_q, group;
   unsigned per_group;  // ceil(2^32 / group)
   long long qs, os;
   float scale, cap;

@@ -1178,7 +1178,6 @@ sv_status sv_attention_cached(const sv_cache* cache, const sv_cache_batch* batch
   p.o = o;
   p.q_off = q_offsets;
   p.total_q = total_q;
-  p.hq = q_heads;
   p.group = q_heads / p.c.hk;
   p.per_group = unsigned((0xffffffffull + unsigned(p.group)) / unsigned(p.group));
   p.scale = opt.scale > 0.0f ? opt.scale : 1.0f / std::sqrt(float(p.c.D));
