@@ -13,8 +13,8 @@
 // the token's lanes. So the stored rows of a warp lie side by side in the page (as long as the tokens are of one
 // sequence), and the 16 scale bytes go out in one access. The tokens' sequences and pages are looked up a lane a token
 // (a binary search among the offsets), when writing behind the loads of the values, which do not depend on them.
-// 14,174 tokens of 8 heads of 128 are written in 18.4 us (4.7 TB/s; 56% of all cycles issue), 23,328 of 16 heads of 72
-// as F16 in 40.6 (79% of the copy bandwidth), 24,742 of 8 heads of 128 read back in 29.2 (90%). 64 or 512 threads a
+// 14,174 tokens of 8 heads of 128 are written in 18.2 us (4.8 TB/s; 56% of all cycles issue), 23,328 of 16 heads of 72
+// as F16 in 40.4 (80% of the copy bandwidth), 24,742 of 8 heads of 128 read back in 29.0 (90%). 64 or 512 threads a
 // CTA, or registers for 8 or 10 of them an SM, change nothing or lose.
 #include "cached.h"
 

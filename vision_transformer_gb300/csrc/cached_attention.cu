@@ -33,9 +33,9 @@
 // shared memory, where the CTA's warps join them when all are through, and the parts of items that are cut between CTAs
 // to the workspace, where the last CTA of an item joins them in order.
 //
-// One token of 16 sequences of 900 to 32768 tokens, 32 heads of 128 over 8, E4M3 (490 MB): 85 us, 86% of the copy
+// One token of 16 sequences of 900 to 32768 tokens, 32 heads of 128 over 8, E4M3 (490 MB): 87 us, 85% of the copy
 // bandwidth. Short calls are a chain of latencies: shares 2,000 cycles, segment 2,000, a step 3,000, parts 1,500, fence and
-// counter 2,000, the join 3,000 (4 sequences of up to 700 tokens: 11.8 us).
+// counter 2,000, the join 3,000 (4 sequences of up to 700 tokens: 11.9 us).
 #include <cmath>
 #include <type_traits>
 

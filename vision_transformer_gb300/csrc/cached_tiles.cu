@@ -26,9 +26,9 @@
 //
 // Two tiles of rows and 128 keys of 128 dimensions take 3,700 cycles: the products 2,048, the exponentials 2,048, shared
 // memory's traffic 2,560, and what bounds it: the softmax of a group, its products and the next scores, one behind the
-// other, 3,400 (256 samples of 32 heads over 32768 shared keys: 107 us of 162, 1,280 TFLOP/s). One tile of rows takes
+// other, 3,400 (256 samples of 32 heads over 32768 shared keys: 107 us of 160, 1,280 TFLOP/s). One tile of rows takes
 // 3,000: the copies of codes on their way (four tiles of 16 KB instead of two: 3,360 before) and the same chain (8
-// sequences of 15000 keys, 128 rows of 8 key heads each: 96 us, 2.6 TB/s, 660 TFLOP/s).
+// sequences of 15000 keys, 128 rows of 8 key heads each: 97 us, 2.6 TB/s, 650 TFLOP/s).
 #include "cached.h"
 #include "packed_attention.h"
 
